@@ -13,6 +13,8 @@ import numpy as np
 from ._lib import (PACE_BUF_FP32, PACE_BUF_INT8, PACE_BUF_MIXED, PACE_ERR_STATE, PACE_ERR_TIMEOUT, PACE_IO_BF16,
                    PACE_IO_F32, PACE_MAX_DP, PACE_MAX_HEADS, PACE_STATE_BF16, PACE_STATE_BF16_BUF, PACE_STATE_FP32,
                    PACE_STATE_QUANT, PACE_GUARD_BYTES, PACE_VALIDATE_N, PaceError, check, lib, pace_config, pace_layout)
+from . import kv as _kv
+from .kv import *  # noqa: F401,F403
 
 __all__ = [
     "pace_config", "make_config", "pace_state_bytes", "pace_state_alloc", "pace_state_free",
@@ -25,7 +27,7 @@ __all__ = [
     "PACE_STATE_QUANT", "PACE_STATE_FP32", "PACE_STATE_BF16", "PACE_STATE_BF16_BUF", "PACE_BUF_INT8", "PACE_BUF_MIXED",
     "PACE_BUF_FP32", "PACE_IO_BF16", "PACE_IO_F32", "PACE_MAX_HEADS", "PACE_MAX_DP", "PACE_GUARD_BYTES",
     "PACE_VALIDATE_N",
-]
+] + _kv.__all__
 
 
 def make_config(n_heads: int, d: int, max_batch: int, dP: int = 8, group: int = 64, zero_point: int = 0,

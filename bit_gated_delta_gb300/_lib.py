@@ -35,6 +35,26 @@ class pace_layout(C.Structure):
                 ("head_slot", C.c_int * PACE_MAX_HEADS), ("head_is_int8", C.c_uint8 * PACE_MAX_HEADS)]
 
 
+class pace_rope_config(C.Structure):
+    _fields_ = [("rot", C.c_int), ("max_pos", C.c_int), ("layout", C.c_int), ("scaling", C.c_int), ("base", C.c_double),
+                ("factor", C.c_double), ("orig_pos", C.c_int), ("beta_fast", C.c_double), ("beta_slow", C.c_double),
+                ("mscale", C.c_double)]
+
+
+class pace_tensor(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("stride_b", C.c_int64), ("stride_t", C.c_int64), ("stride_h", C.c_int64)]
+
+
+class pace_kv_config(C.Structure):
+    _fields_ = [("q_heads", C.c_int), ("kv_heads", C.c_int), ("d", C.c_int), ("bits", C.c_int), ("page_tokens", C.c_int),
+                ("n_pages", C.c_int), ("max_batch", C.c_int), ("max_new", C.c_int), ("io_dtype", C.c_int)]
+
+
+class pace_kv_step(C.Structure):
+    _fields_ = [("batch", C.c_int), ("n_tokens", C.c_int), ("lens", C.c_void_p), ("n_new", C.c_void_p), ("table", C.c_void_p),
+                ("table_cols", C.c_int)]
+
+
 class PaceError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{_STATUS_NAMES.get(status, status)}: {msg}")
@@ -69,6 +89,22 @@ _SIGS = {
     "pace_validate_state": (_I, [_VP, C.POINTER(C.c_int64), _VP]),
 }
 
+_PT, _PS, _PR = C.POINTER(pace_tensor), C.POINTER(pace_kv_step), C.POINTER(pace_rope_config)
+_KV_SIGS = {   # include/pace_kv.h
+    "pace_rope_bytes": (_I, [_PR, C.POINTER(_SZ)]),
+    "pace_rope_table": (_I, [_PR, _VP, _SZ, _VP]),
+    "pace_rope_apply": (_I, [_PR, _VP, _I, _I, _I, _I, _PT, _VP, _PT, _I, _VP]),
+    "pace_kv_tile_bytes": (_SZ, [C.POINTER(pace_kv_config)]),
+    "pace_kv_bytes": (_I, [C.POINTER(pace_kv_config), C.POINTER(_SZ)]),
+    "pace_kv_alloc": (_I, [C.POINTER(pace_kv_config), _VP, _SZ, _VP, C.POINTER(_VP)]),
+    "pace_kv_free": (None, [_VP]),
+    "pace_kv_append": (_I, [_VP, _PS, _PT, _PT, _PT, _PT, _PR, _VP, _VP, _VP]),
+    "pace_kv_read": (_I, [_VP, _PS, _VP, _VP, _PT, _PT, _VP]),
+    "pace_kv_attend": (_I, [_VP, _PS, _PT, _VP, _F, _PT, _VP]),
+    "pace_kv_keep": (_I, [_VP, _PS, _VP, _VP, _VP]),
+    "pace_kv_get_status": (_I, [_VP, _I, C.POINTER(C.c_int), _VP]),
+}
+
 
 def lib() -> C.CDLL:
     """The loaded library. Raises if libpace.so has not been built (no fallback exists)."""
@@ -78,7 +114,7 @@ def lib() -> C.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m bit_gated_delta_gb300.build` "
                                "or __graft_entry__.build(); there is no fallback implementation")
         L = C.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in {**_SIGS, **_KV_SIGS}.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -87,7 +123,13 @@ def lib() -> C.CDLL:
 
 
 def exported_symbols() -> list[str]:
+    """Names declared in include/pace.h."""
     return list(_SIGS)
+
+
+def exported_kv_symbols() -> list[str]:
+    """Names declared in include/pace_kv.h."""
+    return list(_KV_SIGS)
 
 
 def check(status: int) -> None:

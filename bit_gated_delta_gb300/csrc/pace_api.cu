@@ -12,9 +12,9 @@
 
 #include "pace_internal.h"
 
-namespace {
+static thread_local std::string g_last_error;
 
-thread_local std::string g_last_error;
+namespace pace {
 
 pace_status fail(pace_status st, const char *fmt, ...) {
   char buf[512];
@@ -30,6 +30,13 @@ pace_status ok() {
   g_last_error.clear();
   return PACE_OK;
 }
+
+}  // namespace pace
+
+namespace {
+
+using pace::fail;
+using pace::ok;
 
 pace_status cuda_fail(cudaError_t e, const char *what) {
   return fail(PACE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));

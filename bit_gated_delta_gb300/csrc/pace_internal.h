@@ -7,6 +7,12 @@
 
 #include "pace.h"
 
+// Status of an entry point: fail() keeps the message pace_last_error() returns to this thread, ok() clears it.
+namespace pace {
+pace_status fail(pace_status st, const char *fmt, ...);
+pace_status ok();
+}  // namespace pace
+
 // Device view of one state, passed by value to every kernel (fits in the kernel parameter space).
 struct PaceDev {
   int B, H, D, G, NG, dP;
