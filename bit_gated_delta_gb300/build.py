@@ -17,7 +17,8 @@ SOURCES = ["pace_api.cu", "decode.cu", "decode_mma_s8.cu", "decode_mma_sm.cu", "
            "decode_fold_s8.cu", "decode_fold_sm.cu", "decode_fold_z8.cu", "decode_fold_zm.cu", "decode_fold_bf.cu",
            "decode_fold_t32.cu",
            "decode_bf16.cu", "prefill.cu", "prefill_tc.cu", "state_ops.cu",
-           "kv_api.cu", "kv_cache.cu", "kv_attend.cu", "kv_attend_4.cu", "kv_attend_8.cu"]
+           "kv_api.cu", "kv_cache.cu", "kv_attend.cu", "kv_attend_4.cu", "kv_attend_8.cu",
+           "kv_attend_tc_4.cu", "kv_attend_tc_8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

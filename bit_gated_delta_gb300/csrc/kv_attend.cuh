@@ -156,7 +156,9 @@ struct AttendShape {
   static constexpr size_t SCRATCH = (size_t)NW * ROWS * OROW * 4;
   static constexpr size_t ML = (size_t)NW * ROWS * 2 * 4;
   static constexpr size_t FIXED = RING + BARS + SCRATCH + ML + 64 * 8 + 16;
-  static size_t smem(int batch) { return FIXED + (size_t)(batch + 1) * 8; }
+  // prefix sums of up to this many sequences: few capacities, so that the occupancy of each is asked for once
+  static constexpr int capacity(int batch) { return batch <= 128 ? 128 : PACE_KV_MAX_BATCH; }
+  static constexpr size_t smem(int batch) { return FIXED + (size_t)(capacity(batch) + 1) * 8; }
 };
 
 template <int D, int BITS, int NT, int PARTS, int NW, int STAGES, int MINB>
@@ -678,6 +680,19 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   }
 }
 
+// resident_blocks of the capacity for large batches (its own cache entry)
+template <auto K>
+int resident_blocks_large(int threads, size_t smem) {
+  static std::atomic<int> cache[PACE_MAX_DEVICES];
+  const int dev = current_device();
+  int v = cache[dev].load(std::memory_order_relaxed);
+  if (v <= 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, K, threads, smem) != cudaSuccess || v <= 0) v = 1;
+    cache[dev].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
 template <int D, int BITS, int NT, int PARTS, int NW, int STAGES, int MINB>
 cudaError_t launch_attend(AttendArgs a, cudaStream_t s) {
   using S = AttendShape<D, BITS, NT, PARTS, NW, STAGES>;
@@ -688,10 +703,8 @@ cudaError_t launch_attend(AttendArgs a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   a.row_blocks = (a.c.n_tokens * a.c.group + S::ROWS - 1) / S::ROWS;
   a.min_share = NW;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, K, S::THREADS, smem);
-  if (e != cudaSuccess) return e;
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  static int (*const resident[2])(int, size_t) = {resident_blocks<K>, resident_blocks_large<K>};
+  const int per_sm = resident[S::capacity(a.c.batch) > 128](S::THREADS, smem);
   // no more blocks than the longest possible line of tiles has shares
   const long line = (long)a.c.batch * a.c.Hkv * a.row_blocks * (((long)a.c.table_cols * a.c.page + TILE - 1) / TILE);
   long grid = (long)per_sm * device_sm_count();

@@ -1,0 +1,715 @@
+// Attention of many query rows over the quantized KV cache on the 5th-generation tensor cores (bf16 I/O).
+//
+// A work item is 128 query rows of one KV head (row r = token r/G, head r%G), or two such blocks that share the keys and values.
+// Per 64 cached tokens:  S = Q K^T  and  O += P V,  both tcgen05 with the left operand in TMEM (Q and P, a row per lane) and the
+// dequantized keys and values in shared memory as fp16; S and O accumulate in TMEM in fp32.
+//
+// fp16 carries 11 bits, against 8 of bf16, so that held values, queries and weights are rounded to 2^-12; its range is kept by
+// exact powers of two: a row of Q is scaled by its largest element, K and V of a tile by its largest group scale (E_k, E_v; in
+// tiles with new tokens, where rows may see different tokens, each token by its own), weights are taken relative to 2^10 of the
+// running maximum. The powers return with the scores, and in O as a running exponent per row raised like the maximum.
+//
+// Roles (warps): softmax (four a group; thread = row = TMEM lane), four that dequantize, one that copies tiles in, one that issues
+// the products. Two softmax groups take turns, so that the tensor cores work on one group's products while the other group forms
+// its weights: the groups are two row blocks (SHARE), or even and odd tiles of one block (ALT, joined at the end through TMEM).
+//   bound: per 64 tokens and row block of 128 at D = 128, 512 cycles of tensor work; 64 scores a thread (4.5 instructions each, two
+//   groups a scheduler) and a quarter of 16,384 codes a scheduler (about two instructions each) come to about the same.
+// Every wait is bounded; one that gives up sets the status word, and the block leaves after its copies and products have ended.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kv_attend.cuh"
+
+namespace pace {
+namespace kv {
+
+enum { TC_SHARE = 0, TC_ALT = 1, TC_ONE = 2 };
+constexpr int KVT = 64;               // cached tokens a tile
+constexpr int TC_BLOCKS = 160;        // most blocks of a launch (one an SM)
+
+template <int D, int BITS, int MODE>
+struct TcShape {
+  using L = Tile<D, BITS>;
+  static constexpr int NWG = MODE == TC_ONE ? 1 : 2;
+  static constexpr int NRB = MODE == TC_SHARE ? 2 : 1;                  // row blocks an item
+  static constexpr int ROWS = 128 * NRB;
+  static constexpr int KS = 2, VS = 2;                                  // dequantized stages
+  static constexpr int RS = D == 256 ? (BITS == 4 ? 3 : 2) : 4;         // raw stages
+  static constexpr int WARPS = 4 * NWG + 6, THREADS = WARPS * 32;
+  static constexpr int W_DEQ = 4 * NWG, W_LOAD = W_DEQ + 4, W_MMA = W_DEQ + 5;
+  // TMEM columns
+  static constexpr int CQ = 0, CO = NRB * D / 2, CS = CO + NWG * D;
+  static_assert(CS + NWG * KVT <= 512, "TMEM");
+  // shared memory
+  static constexpr int KB = KVT * D * 2;                                // one dequantized tile
+  static constexpr int RAW = 2 * L::BYTES;
+  static constexpr int OK = 0, OV = OK + KS * KB, ORAW = OV + VS * KB, OPAR = ORAW + RS * RAW;
+  static constexpr int PAR = 2 * L::NG * KVT * 16;                      // scales and zero points, twice
+  static constexpr int OEXP = OPAR + 2 * PAR;                           // exponents [8 tiles][k, v][64] int8
+  static constexpr int OML = OEXP + 8 * 2 * KVT;                        // m, l, exponent of group 1 (ALT)
+  static constexpr int OBAR = OML + 128 * 12;
+  static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 4 * NWG + 1;
+  static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flag, red[4]
+  static constexpr int OCUM = (OMISC + 64 + 15) / 16 * 16;
+  static constexpr size_t smem(int batch) { return OCUM + 64 * 8 + (size_t)(batch + 1) * 8; }
+};
+constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 128 + 2 (128 of 256 + 2 are fewer)
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
+  return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
+                            *reinterpret_cast<const __half2 *>(&c));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t h2pack(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void bar_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
+
+// Eight 4-bit codes (one word) times their scale: p.x = scale pair, p.y = -(1024 + z), p.z = -(64 + z). The nibble at bit 0 of a half
+// under the exponent of 1024 reads 1024 + u, the one at bit 4 reads 1024 + 16 u = 16 (64 + u): both give u - z exactly.
+__device__ __forceinline__ uint4 dequant4(uint32_t w, const uint4 &p) {
+  uint32_t r[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t x = w >> (8 * h);
+    r[2 * h] = h2mul(h2add((x & 0x000F000Fu) | 0x64006400u, p.y), p.x);
+    r[2 * h + 1] = h2mul(h2fma((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u /* 1/16 */, p.z), p.x);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// Eight 8-bit codes (two words): a byte under the exponent of 1024 reads 1024 + u, u = c + 128.
+__device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, uint32_t s) {
+  const uint32_t off = 0xE480E480u;   // -1152
+  return make_uint4(h2mul(h2add(__byte_perm(w0, 0x64646464u, 0x4240), off), s), h2mul(h2add(__byte_perm(w0, 0x64646464u, 0x4341), off), s),
+                    h2mul(h2add(__byte_perm(w1, 0x64646464u, 0x4240), off), s), h2mul(h2add(__byte_perm(w1, 0x64646464u, 0x4341), off), s));
+}
+
+// 64 visibility bits of the columns of a tile for row t: columns jd0 + c of the new tokens (negative: context).
+__device__ __forceinline__ uint64_t visible(const AttendArgs &p, int b, int t, int jd0, int nn) {
+  const int T = p.c.n_tokens;
+  if (t >= nn) return 0;
+  const int c0 = jd0 < 0 ? min(-jd0, 64) : 0;
+  const uint64_t ctx = c0 >= 64 ? ~0ull : (1ull << c0) - 1;
+  if (c0 >= 64) return ctx;
+  const int j0 = jd0 + c0;                             // first new token of the tile
+  const int n = min(64 - c0, nn - j0);                 // columns that hold one
+  if (n <= 0) return ctx;
+  uint64_t bits;
+  if (!p.mask) {
+    const int k = t - j0 + 1;
+    bits = k <= 0 ? 0 : k >= 64 ? ~0ull : (1ull << k) - 1;
+  } else {
+    const int words = (T + 31) >> 5, w0 = j0 >> 5, sh = j0 & 31;
+    const uint32_t *row = p.mask + ((long)b * T + t) * words;
+    const uint32_t a = row[w0], m = w0 + 1 < words ? row[w0 + 1] : 0, z = w0 + 2 < words ? row[w0 + 2] : 0;
+    bits = (uint64_t)__funnelshift_r(a, m, sh) | ((uint64_t)__funnelshift_r(m, z, sh) << 32);
+  }
+  if (n < 64) bits &= (1ull << n) - 1;
+  return ctx | (bits << c0);
+}
+
+__device__ __forceinline__ void tc_line(const KvDev &c, long per_seq, long *cum, long *warp_sums) {
+  // as tile_line, in tiles of KVT
+  const int n = c.batch, nt = blockDim.x, per = (n + nt - 1) / nt, b0 = threadIdx.x * per;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  long s = 0;
+  for (int i = 0; i < per && b0 + i < n; ++i) {
+    bool over;
+    const int tok = seq_tokens(c, b0 + i, over);
+    if (over) atomicOr(c.status, PACE_KV_BAD_PAGE);
+    s += max((tok + KVT - 1) / KVT, 1) * per_seq;
+    cum[b0 + i + 1] = s;
+  }
+  long x = s;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[w] = x;
+  __syncthreads();
+  long base = x - s;
+  for (int i = 0; i < w; ++i) base += warp_sums[i];
+  for (int i = 0; i < per && b0 + i < n; ++i) cum[b0 + i + 1] += base;
+  if (threadIdx.x == 0) cum[0] = 0;
+  __syncthreads();
+}
+
+template <int D, int BITS, int MODE>
+__global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_kernel(AttendArgs p) {
+  using S = TcShape<D, BITS, MODE>;
+  using L = Tile<D, BITS>;
+  using namespace umma;
+  constexpr int NG = L::NG, NWG = S::NWG, KS = S::KS, VS = S::VS, RS = S::RS;
+  constexpr uint64_t LIMIT = WAIT_LIMIT_NS;
+  extern __shared__ __align__(128) char smem[];
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::OBAR);
+  uint64_t *raw_full = bar, *raw_free = raw_full + RS, *k_full = raw_free + RS, *k_free = k_full + KS, *v_full = k_free + KS,
+           *v_free = v_full + VS, *s_full = v_free + VS, *p_ready = s_full + NWG, *o_full = p_ready + NWG,
+           *q_ready = o_full + NWG, *drain = q_ready + NWG;
+  int *raw_flags = reinterpret_cast<int *>(smem + S::OMISC);            // [RS]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_flags + 4);
+  int *join_flag = raw_flags + 5;
+  float *red = reinterpret_cast<float *>(raw_flags + 8);                // [4]
+  long *wsum = reinterpret_cast<long *>(smem + S::OCUM);
+  long *cum = wsum + 64;
+  int8_t *exps = reinterpret_cast<int8_t *>(smem + S::OEXP);
+  const KvDev &c = p.c;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = c.group, T = c.n_tokens;
+
+  if (tid == 0) {
+    for (int i = 0; i < RS; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], 4);
+    for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], 4), mbar_init(&k_free[i], 1);
+    for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 4), mbar_init(&v_free[i], 1);
+    for (int i = 0; i < NWG; ++i) {
+      mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128), mbar_init(&o_full[i], 1);
+      mbar_init(&q_ready[i], 128);
+    }
+    mbar_init(drain, 1);
+    mbar_fence_init();
+  }
+  if (warp == S::W_MMA) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  pdl_enter();
+  fence_before_sync();
+  tc_line(c, (long)p.row_blocks * c.Hkv, cum, wsum);      // (its barriers also publish the set-up above)
+  fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  const long total = cum[c.batch];
+  long share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < p.min_share) share = p.min_share;
+  const long lo = min((long)blockIdx.x * share, total), hi = min(total, lo + share);
+  auto at = [&](long pos) { return segment_at(cum, c.batch, p.row_blocks, c.Hkv, pos, hi); };
+  // A role whose wait gives up goes on without waiting or touching the tensor cores, but keeps the barriers it shares, so that no
+  // other warp is left at one; the others' waits then run out too.
+  auto gave_up = [&]() { atomicOr(c.status, PACE_KV_TIMEOUT); };
+
+  if (warp == S::W_LOAD) {
+    // ---------------------------------------------------------------- copies: raw tiles of 2 x 32 tokens
+    int stage = 0, n = 0;
+    bool good = true;
+    for (long pos = lo; pos < hi && good;) {
+      const Segment sg = at(pos);
+      pos += sg.end - sg.tile;
+      bool over;
+      const int tokens = seq_tokens(c, sg.b, over);
+      const int last = 2 * sg.end;
+      for (int s0 = 2 * sg.tile; s0 < last && good; s0 += 32) {         // pages of 32 storage tiles, one a lane
+        const long tok = (long)(s0 + lane) * TILE;
+        int page = tok < tokens && s0 + lane < last ? page_of(c, sg.b, tok) : -2;
+        if (page == -1) atomicOr(c.status, PACE_KV_BAD_PAGE);
+        const int kn = min(32, last - s0);
+        for (int k = 0; k < kn; k += 2) {
+          const int pa = __shfl_sync(0xffffffffu, page, k), pb = __shfl_sync(0xffffffffu, page, k + 1);
+          if (n >= RS && !mbar_wait(&raw_free[stage], (n / RS - 1) & 1, LIMIT)) good = false;
+          good = __all_sync(0xffffffffu, good);
+          if (!good) break;
+          if (lane == 0) {
+            raw_flags[stage] = (pa >= 0 ? 1 : 0) | (pb >= 0 ? 2 : 0);
+            const uint32_t bytes = ((pa >= 0) + (pb >= 0)) * L::BYTES;
+            if (bytes) mbar_arrive_expect_tx(&raw_full[stage], bytes);
+            else mbar_arrive(&raw_full[stage]);
+            char *dst = smem + S::ORAW + stage * S::RAW;
+            if (pa >= 0) bulk_g2s(dst, tile_at<L::BYTES>(c, pa, sg.h, (long)(s0 + k) * TILE), L::BYTES, &raw_full[stage]);
+            if (pb >= 0) bulk_g2s(dst + L::BYTES, tile_at<L::BYTES>(c, pb, sg.h, (long)(s0 + k + 1) * TILE), L::BYTES, &raw_full[stage]);
+          }
+          ++n;
+          stage = stage + 1 == RS ? 0 : stage + 1;
+        }
+      }
+    }
+    if (!good && lane == 0) gave_up();
+    // copies still in flight land before the block leaves (at most RS of them)
+    for (int i = max(0, n - RS); i < n; ++i) mbar_wait(&raw_full[i % RS], (i / RS) & 1, LIMIT);
+  } else if (warp >= S::W_DEQ && warp < S::W_LOAD) {
+    // ---------------------------------------------------------------- dequantize
+    const int dt = tid - S::W_DEQ * 32, dw = warp - S::W_DEQ;
+    int n = 0;
+    bool good = true;
+    for (long pos = lo; pos < hi;) {
+      const Segment sg = at(pos);
+      pos += sg.end - sg.tile;
+      bool over;
+      const int tokens = seq_tokens(c, sg.b, over), len = max(c.lens[sg.b], 0);
+      for (int tile = sg.tile; tile < sg.end; ++tile, ++n) {
+        const int rs = n % RS;
+        good = good && mbar_wait(&raw_full[rs], (n / RS) & 1, LIMIT);
+        good = __all_sync(0xffffffffu, good);
+        const char *raw = smem + S::ORAW + rs * S::RAW;
+        char *par = smem + S::OPAR + (n & 1) * S::PAR;
+        // parameters: thread = token of K (0..63) or V (64..127)
+        {
+          const int part = dt >> 6, t = dt & 63, sub = t >> 5, tt = t & 31;
+          const char *st = raw + sub * L::BYTES;
+          const bool live = tile * KVT + t < tokens && ((raw_flags[rs] >> sub) & 1);
+          const int ps = L::pos(tt);
+          float s[NG], top = 0.0f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            s[g] = live ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(st + (part ? L::VS : L::KS))[g * TILE + ps]) : 0.0f;
+            top = fmaxf(top, s[g]);
+          }
+          const bool own = (tile + 1) * KVT > len;                      // new tokens in the tile: an exponent a token
+          float all = warp_max(top);
+          if (lane == 0) red[dw] = all;
+          bar_sync(1, 128);
+          all = fmaxf(red[part * 2], red[part * 2 + 1]);
+          const float ref = own ? top : all;
+          const int e = ref > 0.0f ? (int)(__float_as_uint(ref) >> 23) - 127 : 0;
+          exps[((n & 7) * 2 + part) * KVT + t] = (int8_t)e;
+          const float down = exp2i(-e < 127 ? -e : 127);                // (e >= -126)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float sc = s[g] * down;
+            uint4 v = make_uint4(h2pack(sc, sc), 0, 0, 0);
+            if (BITS == 4) {
+              const int z = reinterpret_cast<const uint8_t *>(st + (part ? L::VZ : L::KZ))[g * TILE + ps];
+              v.y = h2pack(-(1024.0f + z), -(1024.0f + z));
+              v.z = h2pack(-(64.0f + z), -(64.0f + z));
+            }
+            *reinterpret_cast<uint4 *>(par + ((part * NG + g) * KVT + t) * 16) = v;
+          }
+          bar_sync(1, 128);
+        }
+        // codes: warp = 16 tokens; eight lanes write eight tokens' pieces of one 128-byte core
+        auto param = [&](int part, int g, int t) { return *reinterpret_cast<const uint4 *>(par + ((part * NG + g) * KVT + t) * 16); };
+        auto put = [&](char *dst, int t, int a, const uint4 &v) {
+          *reinterpret_cast<uint4 *>(dst + ((t >> 3) * (D / 8) + a) * 128 + (t & 7) * 16) = v;
+        };
+        {
+          const int ks = n % KS;
+          if (n >= KS) good = good && mbar_wait(&k_free[ks], (n / KS - 1) & 1, LIMIT);
+          good = __all_sync(0xffffffffu, good);
+          if (!good) continue;
+          char *dst = smem + S::OK + ks * S::KB;
+          constexpr int CHUNKS = BITS == 8 ? D / 16 : D == 64 ? 4 : D / 32;
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int q = 0; q < CHUNKS; q += 4) {
+              const int t = dw * 16 + o * 8 + (lane & 7), ch = q + (lane >> 3), tt = t & 31;
+              const char *src = raw + (t >> 5) * L::BYTES + L::kchunk(tt, ch);
+              if (BITS == 8) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(src);
+                const int g = ch >> 2, a = 8 * g + 2 * (ch & 3);
+                const uint32_t s = param(0, g, t).x;
+                put(dst, t, a, dequant8(w.x, w.y, s));
+                put(dst, t, a + 1, dequant8(w.z, w.w, s));
+              } else if (D == 64) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                const uint4 pr = param(0, 0, t);
+                put(dst, t, 2 * ch, dequant4(w.x, pr));
+                put(dst, t, 2 * ch + 1, dequant4(w.y, pr));
+              } else {
+                const uint4 w = *reinterpret_cast<const uint4 *>(src);
+                const int g = 2 * (ch >> 2), a = 8 * g + 2 * (ch & 3);
+                const uint4 p0 = param(0, g, t), p1 = param(0, NG > 1 ? g + 1 : g, t);
+                put(dst, t, a, dequant4(w.x, p0));
+                put(dst, t, a + 1, dequant4(w.y, p0));
+                put(dst, t, a + 8, dequant4(w.z, p1));
+                put(dst, t, a + 9, dequant4(w.w, p1));
+              }
+            }
+          fence_smem_to_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_full[ks]);
+        }
+        {
+          const int vs = n % VS;
+          if (n >= VS) good = good && mbar_wait(&v_free[vs], (n / VS - 1) & 1, LIMIT);
+          good = __all_sync(0xffffffffu, good);
+          if (!good) continue;
+          char *dst = smem + S::OV + vs * S::KB;
+          constexpr int UNITS = BITS == 8 ? D / 8 : D == 64 ? 8 : D / 16;
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int q = 0; q < UNITS; q += 4) {
+              const int t = dw * 16 + o * 8 + (lane & 7), u = q + (lane >> 3), tt = t & 31;
+              const char *src = raw + (t >> 5) * L::BYTES + L::vunit(tt, u);
+              if (BITS == 8) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                put(dst, t, u, dequant8(w.x, w.y, param(1, u >> 3, t).x));
+              } else if (D == 64) {
+                put(dst, t, u, dequant4(*reinterpret_cast<const uint32_t *>(src), param(1, 0, t)));
+              } else {
+                const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                const int g = 2 * (u >> 3), a = 8 * g + (u & 7);
+                put(dst, t, a, dequant4(w.x, param(1, g, t)));
+                put(dst, t, a + 8, dequant4(w.y, param(1, NG > 1 ? g + 1 : g, t)));
+              }
+            }
+          fence_smem_to_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&v_full[vs]);
+            mbar_arrive(&raw_free[rs]);
+          }
+        }
+      }
+    }
+    if (!good && lane == 0) gave_up();
+  } else if (warp == S::W_MMA) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      bool good = true;
+      const uint32_t sb = smem_u32(smem);
+      int ntile = 0;                                      // tiles of the segments before
+      int nq = 0;
+      int np[2] = {0, 0};                                 // tasks done per group
+      constexpr uint32_t ID_S = idesc_f16(128, KVT, 0), ID_O = idesc_f16(128, D, 1);
+      for (long pos = lo; pos < hi && good;) {
+        const Segment sg = at(pos);
+        pos += sg.end - sg.tile;
+        const int tiles = sg.end - sg.tile;
+        const int tasks = MODE == TC_SHARE ? 2 * tiles : tiles;
+        auto wg_of = [&](int k) { return MODE == TC_ONE ? 0 : k & 1; };
+        auto tile_of = [&](int k) { return ntile + (MODE == TC_SHARE ? k >> 1 : k); };
+        auto qk = [&](int k) {
+          const int w = wg_of(k), tl = tile_of(k), ks = tl % KS;
+          if (!mbar_wait(&k_full[ks], (tl / KS) & 1, LIMIT)) return false;
+          fence_after_sync();
+          const uint32_t kb = sb + S::OK + ks * S::KB;
+          const uint32_t qa = tmem + S::CQ + (MODE == TC_SHARE ? w * (D / 2) : 0);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+            mma_ts(tmem + S::CS + w * KVT, qa + 8 * i, smem_desc(kb + i * 256, 128, (D / 8) * 128), ID_S, i ? 1u : 0u);
+          commit(&s_full[w]);
+          if (MODE != TC_SHARE || w == 1) commit(&k_free[ks]);
+          return true;
+        };
+        auto pv = [&](int k) {
+          const int w = wg_of(k), tl = tile_of(k), vs = tl % VS;
+          if (!mbar_wait(&v_full[vs], (tl / VS) & 1, LIMIT)) return false;
+          if (!mbar_wait(&p_ready[w], np[w] & 1, LIMIT)) return false;
+          ++np[w];
+          fence_after_sync();
+          const uint32_t vb = sb + S::OV + vs * S::KB;
+          const bool first = k < (MODE == TC_ONE ? 1 : 2);
+#pragma unroll
+          for (int i = 0; i < KVT / 16; ++i)
+            mma_ts(tmem + S::CO + w * D, tmem + S::CS + w * KVT + 8 * i, smem_desc(vb + i * 2 * (D / 8) * 128, (D / 8) * 128, 128),
+                   ID_O, first && i == 0 ? 0u : 1u);
+          if (MODE != TC_SHARE || w == 1) commit(&v_free[vs]);
+          if (k + NWG >= tasks) commit(&o_full[w]);
+          return true;
+        };
+        for (int w = 0; w < (MODE == TC_SHARE ? 2 : 1); ++w) good = good && mbar_wait(&q_ready[w], nq & 1, LIMIT);
+        if (MODE == TC_ALT) good = good && mbar_wait(&q_ready[1], nq & 1, LIMIT);
+        ++nq;
+        fence_after_sync();
+        for (int k = 0; k < NWG && k < tasks && good; ++k) good = qk(k);
+        for (int k = 0; k < tasks && good; ++k) {
+          good = pv(k);
+          if (good && k + NWG < tasks) good = qk(k + NWG);
+        }
+        ntile += tiles;
+      }
+      if (!good) gave_up();
+      commit(drain);                                      // every product has ended before the block frees its TMEM
+      mbar_wait(drain, 0, LIMIT);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax: thread = row
+    const int w = warp >> 2, row_lane = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + S::CS + w * KVT, tO = tmem + lanes + S::CO + w * D;
+    const float sl2 = fabsf(p.scale_log2);
+    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
+    int ntile = 0, ns = 0, no = 0;
+    bool good = true;
+    for (long pos = lo; pos < hi;) {
+      const Segment sg = at(pos);
+      pos += sg.end - sg.tile;
+      const int tiles = sg.end - sg.tile;
+      const int len = max(c.lens[sg.b], 0), nn = new_tokens(c, sg.b);
+      const int row = sg.rb * S::ROWS + (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
+      const int t = row / G, hh = sg.h * G + row - t * G;
+      const bool in = row < T * G;
+      // ---- the row's query as fp16 over a power of two, into TMEM (ALT: group 0 writes, group 1 only needs the power)
+      float crow = 0.0f;
+      if (good) {
+        const char *src = p.q.p + (sg.b * p.q.sb + (long)t * p.q.st + (long)hh * p.q.sh) * 2;
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = in ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max((v[e] << 16) & 0x7FFF0000u, v[e] & 0x7FFF0000u));
+        }
+        int e = (int)(top >> 23) - 127;
+        e = max(min(e, 126), -126);
+        crow = sl2 * exp2i(e);
+        const float down = exp2i(-e);
+        if (MODE != TC_ALT || w == 0) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t r[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 x = in ? reinterpret_cast<const uint4 *>(src)[4 * i + k] : make_uint4(0, 0, 0, 0);
+              const uint32_t v[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+#pragma unroll
+              for (int d = 0; d < 4; ++d)
+                r[4 * k + d] = h2pack(__uint_as_float(v[d] << 16) * down, __uint_as_float(v[d] & 0xFFFF0000u) * down);
+            }
+            tmem_st16(tmem + lanes + S::CQ + (MODE == TC_SHARE ? w * (D / 2) : 0) + 16 * i, r);
+          }
+          tmem_wait_st();
+        }
+        fence_before_sync();
+        mbar_arrive(&q_ready[w]);
+      }
+      float m = -INFINITY, l = 0.0f;
+      int E = 0;
+      bool first = true;
+      for (int i = MODE == TC_ALT ? w : 0; i < tiles && good; i += MODE == TC_ALT ? 2 : 1) {
+        const int tl = ntile + i, tok0 = (sg.tile + i) * KVT;
+        good = mbar_wait(&s_full[w], ns & 1, LIMIT);
+        good = __all_sync(0xffffffffu, good);
+        if (!good) break;
+        ++ns;
+        fence_after_sync();
+        float s[64];
+        {
+          uint32_t r[4][16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld16(tS + 16 * k, r[k]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[16 * k + e] = __uint_as_float(r[k][e]);
+        }
+        const int8_t *ek = exps + ((tl & 7) * 2) * KVT, *ev = ek + KVT;
+        const bool edge = tok0 + KVT > len;
+        float mx = -INFINITY, cs = crow;
+        int Et = -126;
+        if (!edge) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) mx = fmaxf(mx, s[k]);
+          cs = crow * exp2i(ek[0]);
+          mx *= cs;
+          Et = ev[0];
+        } else {
+          const uint64_t vis = in ? visible(p, sg.b, t, tok0 - len, nn) : 0ull;
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            const bool see = (vis >> k) & 1;
+            s[k] = see ? s[k] * (crow * exp2i(ek[k])) : -INFINITY;
+            mx = fmaxf(mx, s[k]);
+            if (see) Et = max(Et, (int)ev[k]);
+          }
+        }
+        // ---- raise the row's references when a score passes the maximum by 2^4 or the values' exponent grows
+        const bool grow = mx > m + 4.0f || Et > E || first;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float m2 = fmaxf(m, mx);
+          const int E2 = first ? Et : max(E, Et);
+          const float al = m == -INFINITY ? 0.0f : exp2_approx(m - m2);
+          l *= al;
+          if (!first) {
+            const float f = m == -INFINITY ? 0.0f : exp2_approx(m - m2 + (float)(E - E2));
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t r[16];
+              tmem_ld16(tO + 16 * k, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+              tmem_st16(tO + 16 * k, r);
+            }
+          }
+          m = m2;
+          E = E2;
+          first = false;
+        }
+        const float mu = m == -INFINITY ? 0.0f : m;
+        float sum = 0.0f;
+        if (!edge) {
+          const int dE = max(Et - E, -60);
+          const float add = 10.0f + (float)dE - mu;
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            s[k] = exp2_approx(fmaf(s[k], cs, add));
+            sum += s[k];
+          }
+          l = fmaf(sum, exp2i(-dE), l);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            const float pr = exp2_approx(s[k] - mu + 10.0f);
+            sum += pr;
+            s[k] = pr * exp2i(min(max((int)ev[k] - E, -60), 0));
+          }
+          l += sum;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t r[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[e] = h2pack(s[32 * k + 2 * e], s[32 * k + 2 * e + 1]);
+          tmem_st16(tS + 16 * k, r);
+        }
+        tmem_wait_st();
+        fence_before_sync();
+        mbar_arrive(&p_ready[w]);
+      }
+      // ---- the segment's result
+      const bool has = MODE != TC_ALT || w < tiles;
+      if (has && good) {
+        good = mbar_wait(&o_full[w], no & 1, LIMIT);
+        good = __all_sync(0xffffffffu, good);
+        ++no;
+        fence_after_sync();
+      }
+      const bool whole = sg.tile == 0 && sg.end == sg.tiles;
+      const long item_lo = pos - tiles - sg.tile;
+      const int fb = (int)(item_lo / share), lb = (int)((item_lo + sg.tiles - 1) / share);
+      float *part = c.part + (long)(2 * blockIdx.x + (blockIdx.x == fb ? 1 : 0)) * TC_PART_FLOATS;
+      const int prow = (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
+      float f0 = 1.0f, f1 = 0.0f, M = m, Ls = l;
+      int E0 = E, E1 = 0;
+      bool two = false;
+      if (MODE == TC_ALT) {
+        float *mlp = reinterpret_cast<float *>(smem + S::OML) + row_lane * 3;
+        if (w == 1) mlp[0] = m, mlp[1] = l, mlp[2] = (float)E;
+        fence_before_sync();
+        bar_sync(2, 256);
+        fence_after_sync();
+        if (w == 0) {
+          const float m1 = mlp[0];
+          two = tiles > 1;
+          M = fmaxf(m, m1);
+          f0 = m == -INFINITY ? 0.0f : exp2_approx(m - M);
+          f1 = m1 == -INFINITY ? 0.0f : exp2_approx(m1 - M);
+          Ls = f0 * l + f1 * mlp[1];
+          E1 = (int)mlp[2];
+        }
+      }
+      if ((MODE != TC_ALT || w == 0) && good) {
+        const float inv = t < nn && Ls > 0.0f ? 1.0f / Ls : 0.0f;
+        const float g0 = f0 * exp2i(E0), g1 = f1 * exp2i(E1);
+        char *dst = p.o.p + (sg.b * p.o.sb + (long)t * p.o.st + (long)hh * p.o.sh) * 2;
+#pragma unroll 1
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t r[16], r1[16];
+          tmem_ld16(tO + 16 * k, r);
+          if (MODE == TC_ALT && two) tmem_ld16(tO + D + 16 * k, r1);
+          tmem_wait_ld();
+          float y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            y[e] = __uint_as_float(r[e]) * g0;
+            if (MODE == TC_ALT && two) y[e] = fmaf(__uint_as_float(r1[e]), g1, y[e]);
+          }
+          if (whole) {
+            if (in) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                reinterpret_cast<uint4 *>(dst)[2 * k + h] =
+                    make_uint4(pack_bf16x2(y[8 * h] * inv, y[8 * h + 1] * inv), pack_bf16x2(y[8 * h + 2] * inv, y[8 * h + 3] * inv),
+                               pack_bf16x2(y[8 * h + 4] * inv, y[8 * h + 5] * inv), pack_bf16x2(y[8 * h + 6] * inv, y[8 * h + 7] * inv));
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              *reinterpret_cast<float4 *>(part + prow * D + 16 * k + 4 * h) = make_float4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]);
+          }
+        }
+        if (!whole) {
+          part[S::ROWS * D + 2 * prow] = M;
+          part[S::ROWS * D + 2 * prow + 1] = Ls;
+        }
+      }
+      if (!whole) {
+        __threadfence();
+        bar_sync(2, NWG * 128);
+        if (tid == 0) {
+          const int before = atomicAdd(&c.count[fb], 1);
+          *join_flag = before == lb - fb;
+          if (before == lb - fb) c.count[fb] = 0;
+        }
+        bar_sync(2, NWG * 128);
+        if (*join_flag) {
+          __threadfence();
+          constexpr int CH = D / 8;
+          for (int x = tid; x < S::ROWS * CH; x += NWG * 128) {
+            const int r = x / CH, e8 = (x % CH) * 8, rr = sg.rb * S::ROWS + r, tt = rr / G;
+            if (rr >= T * G) continue;
+            float MM = -INFINITY;
+            for (int i = fb; i <= lb; ++i)
+              MM = fmaxf(MM, __ldcg(c.part + (long)(2 * i + (i == fb ? 1 : 0)) * TC_PART_FLOATS + S::ROWS * D + 2 * r));
+            float y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, LL = 0.0f;
+#pragma unroll 2
+            for (int i = fb; i <= lb; ++i) {
+              const float *src = c.part + (long)(2 * i + (i == fb ? 1 : 0)) * TC_PART_FLOATS;
+              const float2 e = __ldcg(reinterpret_cast<const float2 *>(src + S::ROWS * D + 2 * r));
+              const float f = e.x == -INFINITY ? 0.0f : exp2_approx(e.x - MM);
+              const float4 u = __ldcg(reinterpret_cast<const float4 *>(src + r * D + e8));
+              const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + r * D + e8 + 4));
+              LL += f * e.y;
+              y[0] += f * u.x, y[1] += f * u.y, y[2] += f * u.z, y[3] += f * u.w;
+              y[4] += f * v.x, y[5] += f * v.y, y[6] += f * v.z, y[7] += f * v.w;
+            }
+            const float inv = tt < nn && LL > 0.0f ? 1.0f / LL : 0.0f;
+            char *dst = p.o.p + (sg.b * p.o.sb + (long)tt * p.o.st + (long)(sg.h * G + rr - tt * G) * p.o.sh + e8) * 2;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv),
+                                                         pack_bf16x2(y[4] * inv, y[5] * inv), pack_bf16x2(y[6] * inv, y[7] * inv));
+          }
+        }
+      }
+      fence_before_sync();
+      if (NWG == 2) bar_sync(2, 256);                     // both groups have read what the next segment overwrites
+      ntile += tiles;
+    }
+    if (!good && lane == 0) gave_up();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == S::W_MMA) tmem_dealloc(tmem, 512);
+}
+
+template <int D, int BITS, int MODE>
+cudaError_t launch_attend_tc(AttendArgs a, cudaStream_t s) {
+  using S = TcShape<D, BITS, MODE>;
+  constexpr auto K = attend_tc_kernel<D, BITS, MODE>;
+  static_assert(S::ROWS * (D + 2) <= TC_PART_FLOATS, "the work area holds every shape's partial results");
+  const size_t smem = S::smem(a.c.batch);
+  cudaError_t e = smem_opt_in<K>(227 * 1024);
+  if (e != cudaSuccess) return e;
+  a.row_blocks = (a.c.n_tokens * a.c.group + S::ROWS - 1) / S::ROWS;
+  a.min_share = 4;
+  long grid = device_sm_count();
+  if (grid > TC_BLOCKS) grid = TC_BLOCKS;
+  const long line = (long)a.c.batch * a.c.Hkv * a.row_blocks * (((long)a.c.table_cols * a.c.page + KVT - 1) / KVT);
+  const long shares = (line + a.min_share - 1) / a.min_share;
+  if (grid > shares) grid = shares;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)grid), dim3(S::THREADS), smem, s, attr);
+  return cudaLaunchKernelEx(&cfg, K, a);
+}
+
+}  // namespace kv
+}  // namespace pace

@@ -7,13 +7,16 @@ with d contiguous; lengths, page tables, masks and paths are contiguous int32 te
 from __future__ import annotations
 
 import ctypes as C
-import math
+import functools
+
+import torch
 
 from ._lib import (PACE_ERR_STATE, PACE_ERR_TIMEOUT, PACE_IO_BF16, PACE_IO_F32, check, lib, pace_kv_config, pace_kv_step,
                    pace_rope_config, pace_tensor)
 
 PACE_KV_BAD_PAGE, PACE_KV_BAD_POSITION, PACE_KV_BAD_KEEP, PACE_KV_TIMEOUT = 1, 2, 4, 8
 PACE_KV_MAX_BATCH, PACE_KV_MAX_NEW = 1024, 4096
+_INTS = (torch.int32, torch.uint32)
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 
@@ -24,15 +27,21 @@ __all__ = ["make_rope_config", "pace_rope_bytes", "pace_rope_table", "pace_rope_
            "PACE_KV_MAX_NEW"]
 
 
+# The calls below are made for every layer and token, so their marshalling is kept short: raw stream handles, one stride() per
+# tensor, library functions looked up once.
 def _stream(s):
-    import torch
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return s if isinstance(s, int) else s.cuda_stream
 
 
+@functools.lru_cache(maxsize=None)
+def _fn(name):
+    return getattr(lib(), name)
+
+
+@functools.lru_cache(maxsize=None)
 def _dtype(io):
-    import torch
     return torch.float32 if io == PACE_IO_F32 else torch.bfloat16
 
 
@@ -40,32 +49,24 @@ def _tensor(t, io, shape, name):
     """pace_tensor of a [.., tokens, heads, d] view, or a ValueError that says what is wrong with it."""
     if t is None:
         return None
-    if t.dtype != _dtype(io):
-        raise ValueError(f"{name}: expected {_dtype(io)}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    st = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim())]
-    sb = st[0] if t.dim() == 4 else 0
-    return C.byref(pace_tensor(t.data_ptr(), sb, st[-3], st[-2]))
+    st = t.stride()
+    if t.dtype is not _dtype(io) or not t.is_cuda or t.shape != shape or (st[-1] != 1 and shape[-1] > 1 and t.numel()):
+        raise ValueError(f"{name}: expected a {_dtype(io)} CUDA tensor of shape {tuple(shape)} with its last dimension contiguous, "
+                         f"got {t.dtype} on {t.device}, shape {tuple(t.shape)}, strides {st}")
+    if 1 in shape:                       # the stride of a single element is anything
+        st = [0 if n == 1 else x for n, x in zip(shape, st)]
+    return pace_tensor(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
 
 
 def _ints(t, shape, name, optional=False):
     """Pointer of a contiguous int32 (masks: also uint32) CUDA tensor of the given shape."""
-    import torch
     if t is None:
-        if not optional:
-            raise ValueError(f"{name} is missing")
-        return None
-    if t.dtype not in (torch.int32, torch.uint32):
-        raise ValueError(f"{name}: expected int32, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if t.dtype not in _INTS or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor of shape {tuple(shape)}, got {t.dtype} on {t.device}, "
+                         f"shape {tuple(t.shape)}, strides {t.stride()}")
     return t.data_ptr()
 
 
@@ -93,23 +94,21 @@ class PaceRope:
     """A cos/sin table: `rot` elements of a head, positions 0..max_pos-1, built once."""
 
     def __init__(self, rot: int, max_pos: int, device="cuda", stream=None, **kw):
-        import torch
         self.cfg = make_rope_config(rot, max_pos, **kw)
         self.nbytes = pace_rope_bytes(self.cfg)
         self.table = torch.empty(max_pos, rot // 2, 2, dtype=torch.float32, device=device)
-        pace_rope_table(self.cfg, self.table, self.nbytes, stream)
+        self.ptr = self.table.data_ptr()
+        pace_rope_table(self.cfg, self.ptr, self.nbytes, stream)
 
 
 def pace_rope_apply(rope: PaceRope, x, positions, out, inverse: bool = False, stream=None) -> None:
     """Rotates x [n, heads, d] (bf16 or fp32) at positions [n] into out (x itself is allowed). inverse: the gradient."""
-    import torch
     if x.dim() != 3:
         raise ValueError("x: expected [n, heads, d]")
-    io = PACE_IO_F32 if x.dtype == torch.float32 else PACE_IO_BF16
-    n, h, d = x.shape
-    check(lib().pace_rope_apply(C.byref(rope.cfg), rope.table.data_ptr(), n, h, d, io, _tensor(x, io, (n, h, d), "x"),
-                                _ints(positions, (n,), "positions"), _tensor(out, io, (n, h, d), "out"), int(inverse),
-                                _stream(stream)))
+    io = PACE_IO_F32 if x.dtype is torch.float32 else PACE_IO_BF16
+    shape = n, h, d = x.shape
+    check(_fn("pace_rope_apply")(rope.cfg, rope.ptr, n, h, d, io, _tensor(x, io, shape, "x"), _ints(positions, (n,), "positions"),
+                                 _tensor(out, io, shape, "out"), inverse, _stream(stream)))
 
 
 # ---- the cache ----------------------------------------------------------------------------------------------------------------
@@ -142,44 +141,41 @@ def pace_kv_free(handle) -> None:
 def _step(B, T, lens, table, n_new):
     if table is None or table.dim() != 2:
         raise ValueError("table: expected [batch, columns]")
+    cols = table.shape[1]
     return pace_kv_step(B, T, None if lens is None else _ints(lens, (B,), "lens"), _ints(n_new, (B,), "n_new", True),
-                        _ints(table, (B, table.shape[1]), "table"), table.shape[1])
+                        _ints(table, (B, cols), "table"), cols)
 
 
 def pace_kv_append(handle, cfg, q, k, v, lens, table, rope=None, positions=None, n_new=None, q_out=None, stream=None) -> None:
     B, T = k.shape[0], k.shape[1]
     io = cfg.io_dtype
     kv, qs = (B, T, cfg.kv_heads, cfg.d), (B, T, cfg.q_heads, cfg.d)
-    st = _step(B, T, lens, table, n_new)
-    check(lib().pace_kv_append(handle, C.byref(st), _tensor(q, io, qs, "q"), _tensor(k, io, kv, "k"), _tensor(v, io, kv, "v"),
-                               _tensor(q_out, io, qs, "q_out"), C.byref(rope.cfg) if rope else None,
-                               rope.table.data_ptr() if rope else None, _ints(positions, (B, T), "positions", True),
-                               _stream(stream)))
+    check(_fn("pace_kv_append")(handle, _step(B, T, lens, table, n_new), _tensor(q, io, qs, "q"), _tensor(k, io, kv, "k"),
+                                _tensor(v, io, kv, "v"), _tensor(q_out, io, qs, "q_out"), rope.cfg if rope else None,
+                                rope.ptr if rope else None, _ints(positions, (B, T), "positions", True), _stream(stream)))
 
 
 def pace_kv_read(handle, cfg, k_out, v_out, table, first=None, end=None, stream=None) -> None:
     B, n = k_out.shape[0], k_out.shape[1]
     shape = (B, n, cfg.kv_heads, cfg.d)
-    st = _step(B, n, None, table, None)
-    check(lib().pace_kv_read(handle, C.byref(st), _ints(first, (B,), "first", True), _ints(end, (B,), "end", True),
-                             _tensor(k_out, cfg.io_dtype, shape, "k_out"), _tensor(v_out, cfg.io_dtype, shape, "v_out"),
-                             _stream(stream)))
+    check(_fn("pace_kv_read")(handle, _step(B, n, None, table, None), _ints(first, (B,), "first", True),
+                              _ints(end, (B,), "end", True), _tensor(k_out, cfg.io_dtype, shape, "k_out"),
+                              _tensor(v_out, cfg.io_dtype, shape, "v_out"), _stream(stream)))
 
 
 def pace_kv_attend(handle, cfg, q, o, lens, table, mask=None, n_new=None, scale=None, stream=None) -> None:
     B, T = q.shape[0], q.shape[1]
-    shape = (B, T, cfg.q_heads, cfg.d)
-    st = _step(B, T, lens, table, n_new)
-    check(lib().pace_kv_attend(handle, C.byref(st), _tensor(q, cfg.io_dtype, shape, "q"),
-                               _ints(mask, (B, T, (T + 31) // 32), "mask", True),
-                               1.0 / math.sqrt(cfg.d) if scale is None else scale, _tensor(o, cfg.io_dtype, shape, "o"),
-                               _stream(stream)))
+    d = cfg.d
+    shape = (B, T, cfg.q_heads, d)
+    check(_fn("pace_kv_attend")(handle, _step(B, T, lens, table, n_new), _tensor(q, cfg.io_dtype, shape, "q"),
+                                _ints(mask, (B, T, (T + 31) // 32), "mask", True), d ** -0.5 if scale is None else scale,
+                                _tensor(o, cfg.io_dtype, shape, "o"), _stream(stream)))
 
 
 def pace_kv_keep(handle, lens, table, idx, n_keep, stream=None) -> None:
     B, K = idx.shape
-    st = _step(B, K, lens, table, None)
-    check(lib().pace_kv_keep(handle, C.byref(st), _ints(idx, (B, K), "idx"), _ints(n_keep, (B,), "n_keep"), _stream(stream)))
+    check(_fn("pace_kv_keep")(handle, _step(B, K, lens, table, None), _ints(idx, (B, K), "idx"), _ints(n_keep, (B,), "n_keep"),
+                              _stream(stream)))
 
 
 def pace_kv_get_status(handle, clear: bool = False, stream=None) -> int:
@@ -199,7 +195,6 @@ class PaceKV:
     """
 
     def __init__(self, cfg: pace_kv_config, device="cuda", stream=None):
-        import torch
         self.cfg = cfg
         self.nbytes = pace_kv_bytes(cfg)
         self.mem = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
