@@ -12,11 +12,6 @@ namespace kv {
 constexpr int THREADS = 128;
 
 template <int IO32>
-struct Vec8 {
-  float x[8];
-};
-
-template <int IO32>
 __device__ __forceinline__ void load8(const char *p, float (&x)[8]) {
   if (IO32) {
     const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
@@ -47,7 +42,89 @@ __device__ __forceinline__ void store8(char *p, const float (&x)[8]) {
   }
 }
 
-// cos and sin of the lane's eight elements (interleaved: of its four pairs) at one position.
+// A rotated vector is cut into rot/8 pieces of four pairs and (d - rot)/8 pieces of eight elements that pass through, one a lane,
+// so that no lane needs another's elements and each angle is read once: the two 4-element parts of piece a start at `lo` and `hi`.
+struct Piece {
+  int lo, hi;
+  bool turn;
+};
+__device__ __forceinline__ Piece piece_of(const KvRope &r, int a) {
+  const bool turn = 8 * a < r.rot, split = turn && !r.interleaved;
+  return Piece{split ? 4 * a : 8 * a, split ? (r.rot >> 1) + 4 * a : 8 * a + 4, turn};
+}
+template <int IO32>
+struct Four {
+  using type = uint2;
+};
+template <>
+struct Four<1> {
+  using type = float4;
+};
+__device__ __forceinline__ float4 widen(const uint2 &w) {
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ float4 widen(const float4 &w) { return w; }
+__device__ __forceinline__ void narrow(const float4 &x, uint2 &w) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+__device__ __forceinline__ void narrow(const float4 &x, float4 &w) { w = x; }
+
+// (a, b) -> (a c - b s, b c + a s). Products and sums are rounded apart (no contraction), so that a rotated value is the same
+// wherever it is formed.
+__device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
+  const float u = a, v = b;
+  a = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
+  b = __fadd_rn(__fmul_rn(v, c), __fmul_rn(u, s));
+}
+
+// HC heads of one token, from head h0: the angles of the lane's four pairs are read once for all of them.
+template <int IO32, int HC>
+__device__ __forceinline__ void rotate_heads(const KvRope &r, const char *src, int64_t src_h, char *dst, int64_t dst_h, int n, int a,
+                                             int pos, float sign) {
+  using V = typename Four<IO32>::type;
+  constexpr int ES = IO32 ? 4 : 2;
+  const Piece pc = piece_of(r, a);
+  V lo[HC], hi[HC];
+#pragma unroll
+  for (int i = 0; i < HC; ++i)
+    if (i < n) {
+      lo[i] = *reinterpret_cast<const V *>(src + (i * src_h + pc.lo) * ES);
+      hi[i] = *reinterpret_cast<const V *>(src + (i * src_h + pc.hi) * ES);
+    }
+  float4 t0 = make_float4(1, 0, 1, 0), t1 = t0;
+  if (pc.turn) {
+    const float4 *row = reinterpret_cast<const float4 *>(r.table + (long)pos * (r.rot >> 1) + 4 * a);
+    t0 = row[0];
+    t1 = row[1];
+  }
+#pragma unroll
+  for (int i = 0; i < HC; ++i)
+    if (i < n) {
+      if (pc.turn) {
+        float4 x = widen(lo[i]), y = widen(hi[i]);
+        if (r.interleaved) {
+          turn(x.x, x.y, t0.x, sign * t0.y);
+          turn(x.z, x.w, t0.z, sign * t0.w);
+          turn(y.x, y.y, t1.x, sign * t1.y);
+          turn(y.z, y.w, t1.z, sign * t1.w);
+        } else {
+          turn(x.x, y.x, t0.x, sign * t0.y);
+          turn(x.y, y.y, t0.z, sign * t0.w);
+          turn(x.z, y.z, t1.x, sign * t1.y);
+          turn(x.w, y.w, t1.z, sign * t1.w);
+        }
+        narrow(x, lo[i]);
+        narrow(y, hi[i]);
+      }
+      *reinterpret_cast<V *>(dst + (i * dst_h + pc.lo) * ES) = lo[i];
+      *reinterpret_cast<V *>(dst + (i * dst_h + pc.hi) * ES) = hi[i];
+    }
+}
+
+// The same for eight consecutive elements a lane, as the quantizer holds them: the partner half comes by shuffle, and every lane of
+// the warp takes part.
 struct Angles {
   float2 cs[8];
 };
@@ -64,29 +141,24 @@ __device__ __forceinline__ void load_angles(const KvRope &r, int pos, int a, Ang
     g.cs[2 * i + 1] = make_float2(t.z, t.w);
   }
 }
-// Rotate the lane's eight elements in place; every lane of the warp takes part (the partner half comes by shuffle). Products
-// and sums are rounded apart (no contraction), so that the rotated value is the same wherever it is formed.
-__device__ __forceinline__ void rotate8(const KvRope &r, const Angles &g, int a, bool on, float sign, float (&x)[8]) {
+__device__ __forceinline__ void rotate8(const KvRope &r, const Angles &g, int a, bool on, float (&x)[8]) {
   const int half = r.rot >> 1, e0 = 8 * a, lane = threadIdx.x & 31;
   const bool in = on && e0 < r.rot;
   if (r.interleaved) {
     if (!in) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float c = g.cs[i].x, s = sign * g.cs[i].y, u = x[2 * i], v = x[2 * i + 1];
-      x[2 * i] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
-      x[2 * i + 1] = __fadd_rn(__fmul_rn(v, c), __fmul_rn(u, s));
-    }
+    for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], g.cs[i].x, g.cs[i].y);
     return;
   }
   const bool lo = e0 < half;
   const int src = e0 < r.rot ? (lo ? lane + (half >> 3) : lane - (half >> 3)) : lane;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float p = __shfl_sync(0xffffffffu, x[i], src & 31);
+    float p = __shfl_sync(0xffffffffu, x[i], src & 31), y = x[i];
     if (in) {
-      const float c = g.cs[i].x, s = sign * g.cs[i].y;
-      x[i] = lo ? __fsub_rn(__fmul_rn(x[i], c), __fmul_rn(p, s)) : __fadd_rn(__fmul_rn(x[i], c), __fmul_rn(p, s));
+      if (lo) turn(y, p, g.cs[i].x, g.cs[i].y);
+      else turn(p, y, g.cs[i].x, g.cs[i].y);
+      x[i] = y;
     }
   }
 }
@@ -114,29 +186,22 @@ __global__ void rope_table_kernel(pace_rope_config r, float2 *table) {
   }
 }
 
-// x [n][heads][d] -> out. A lane keeps its position's angles for HC heads, so the table is read once per HC vectors.
+// x [n][heads][d] -> out, HC heads a lane.
 template <int IO32, int HC>
 __global__ void __launch_bounds__(THREADS) rope_kernel(KvRope r, int n, int heads, int d, KvTensor x,
                                                        const int32_t *__restrict__ positions, KvTensor out, float sign) {
   constexpr int ES = IO32 ? 4 : 2;
+  pdl_enter();
   // vectors are packed d/8 lanes each from lane 0 of a warp; lanes past the last whole vector idle
   const int lpv = d >> 3, vpw = 32 / lpv, lane = threadIdx.x & 31;
   const int sub = lane / lpv, a = lane - sub * lpv;
-  const int chunks = (heads + HC - 1) / HC;
-  const long item = ((long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5)) * vpw + sub;
-  const bool live = sub < vpw && item < (long)n * chunks;
-  const int t = live ? (int)(item / chunks) : 0, h0 = live ? (int)(item - (long)t * chunks) * HC : 0;
-  float v[HC][8];
-#pragma unroll
-  for (int i = 0; i < HC; ++i)
-    if (live && h0 + i < heads) load8<IO32>(x.p + ((long)t * x.st + (long)(h0 + i) * x.sh + 8 * a) * ES, v[i]);
-  Angles g;
-  if (live) load_angles(r, min(max(positions[t], 0), r.max_pos - 1), a, g);
-#pragma unroll
-  for (int i = 0; i < HC; ++i) {
-    rotate8(r, g, a, live, sign, v[i]);
-    if (live && h0 + i < heads) store8<IO32>(out.p + ((long)t * out.st + (long)(h0 + i) * out.sh + 8 * a) * ES, v[i]);
-  }
+  const unsigned chunks = (heads + HC - 1) / HC;
+  const unsigned item = (blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5)) * vpw + sub;
+  if (sub >= vpw || item >= n * chunks) return;
+  const unsigned t = item / chunks, h0 = (item - t * chunks) * HC;
+  const int pos = min(max(positions[t], 0), r.max_pos - 1);
+  rotate_heads<IO32, HC>(r, x.p + ((long)t * x.st + (long)h0 * x.sh) * ES, x.sh, out.p + ((long)t * out.st + (long)h0 * out.sh) * ES,
+                         out.sh, min(HC, (int)(heads - h0)), a, pos, sign);
 }
 
 // Quantize the lane's eight elements within their group of 64 (eight lanes): codes, scale, zero point. quant_group's
@@ -179,29 +244,44 @@ __device__ __forceinline__ void quant8(const float (&xin)[8], uint32_t (&u)[8], 
   }
 }
 
-// The new tokens of a call: query vectors rotated, key vectors rotated and quantized, value vectors quantized. A warp holds
-// 256/D vectors of one token (HC steps of them over the vectors q.., k.., v.. of that token).
-template <int D, int BITS, int IO32, int HC>
+// The new tokens of a call. The first q_blocks blocks rotate queries (HC heads a lane); the others take key and value vectors, 256/D
+// a warp and KC steps of them: keys are rotated, both quantized and written to their tile.
+template <int D, int BITS, int IO32, int HC, int KC>
 __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, KvTensor k, KvTensor v, KvTensor qo, KvRope r,
-                                                         const int32_t *__restrict__ positions) {
+                                                         const int32_t *__restrict__ positions, int q_blocks) {
   using L = Tile<D, BITS>;
   constexpr int LPV = D / 8, VPW = 32 / LPV, ES = IO32 ? 4 : 2;
   const int lane = threadIdx.x & 31, sub = lane / LPV, a = lane % LPV;
-  const int nq = q.p ? c.Hq : 0, nvec = nq + 2 * c.Hkv;
-  const int chunks = (nvec + HC * VPW - 1) / (HC * VPW);
-  const long item = (long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
-  if (item >= (long)c.batch * c.n_tokens * chunks) return;   // whole warps
-  const int tok = (int)(item / chunks), v0 = (int)(item - (long)tok * chunks) * HC * VPW;
+  pdl_enter();
+  const unsigned tokens = (unsigned)c.batch * c.n_tokens;
+  auto position = [&](unsigned tok, int b, int t, bool report) {
+    const long pos = positions ? positions[tok] : (long)c.lens[b] + t;
+    if (pos >= 0 && pos < r.max_pos) return (int)pos;
+    if (report && t < new_tokens(c, b)) atomicOr(c.status, PACE_KV_BAD_POSITION);
+    return pos < 0 ? 0 : r.max_pos - 1;
+  };
+  if ((int)blockIdx.x < q_blocks) {
+    const unsigned chunks = (c.Hq + HC - 1) / HC;
+    const unsigned item = (blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5)) * VPW + sub;
+    if (item >= tokens * chunks) return;
+    const unsigned tok = item / chunks, h0 = (item - tok * chunks) * HC;
+    const int b = tok / c.n_tokens, t = tok - b * c.n_tokens;
+    rotate_heads<IO32, HC>(r, q.p + (b * q.sb + t * q.st + h0 * q.sh) * ES, q.sh, qo.p + (b * qo.sb + t * qo.st + h0 * qo.sh) * ES,
+                           qo.sh, min(HC, (int)(c.Hq - h0)), a, position(tok, b, t, a == 0), 1.0f);
+    return;
+  }
+  const unsigned nvec = 2 * c.Hkv, chunks = (nvec + KC * VPW - 1) / (KC * VPW);
+  const unsigned item = (blockIdx.x - q_blocks) * (THREADS / 32) + (threadIdx.x >> 5);
+  if (item >= tokens * chunks) return;                 // whole warps
+  const unsigned tok = item / chunks;
+  const int v0 = (item - tok * chunks) * KC * VPW;
   const int b = tok / c.n_tokens, t = tok - b * c.n_tokens;
-  float x[HC][8];
-  int kind[HC], head[HC];       // 0 query, 1 key, 2 value, -1 none
+  float x[KC][8];
 #pragma unroll
-  for (int i = 0; i < HC; ++i) {
+  for (int i = 0; i < KC; ++i) {
     const int vec = v0 + i * VPW + sub;
-    kind[i] = vec < nq ? 0 : vec < nq + c.Hkv ? 1 : vec < nvec ? 2 : -1;
-    head[i] = kind[i] == 0 ? vec : kind[i] == 1 ? vec - nq : vec - nq - c.Hkv;
-    const KvTensor &s = kind[i] == 0 ? q : kind[i] == 1 ? k : v;
-    if (kind[i] >= 0) load8<IO32>(s.p + (b * s.sb + t * s.st + head[i] * s.sh + 8 * a) * ES, x[i]);
+    const KvTensor &s = vec < c.Hkv ? k : v;
+    if (vec < (int)nvec) load8<IO32>(s.p + (b * s.sb + t * s.st + (vec < c.Hkv ? vec : vec - c.Hkv) * s.sh + 8 * a) * ES, x[i]);
     else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
@@ -211,27 +291,21 @@ __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, Kv
   const long slot = (long)len + t;
   const bool fresh = t < new_tokens(c, b);
   const int page = fresh ? page_of(c, b, len < 0 ? -1 : slot) : -1;
-  Angles g;
-  if (r.table) {
-    const long pos = positions ? positions[tok] : slot;
-    const bool bad = pos < 0 || pos >= r.max_pos;
-    if (bad && fresh && lane == 0 && v0 < nq + c.Hkv) atomicOr(c.status, PACE_KV_BAD_POSITION);
-    load_angles(r, bad ? (pos < 0 ? 0 : r.max_pos - 1) : (int)pos, a, g);
-  }
   if (fresh && page < 0 && lane == 0) atomicOr(c.status, PACE_KV_BAD_PAGE);
+  Angles g;
+  if (r.table && v0 < c.Hkv) load_angles(r, position(tok, b, t, lane == 0), a, g);
 #pragma unroll
-  for (int i = 0; i < HC; ++i) {
-    if (r.table) rotate8(r, g, a, kind[i] == 0 || kind[i] == 1, 1.0f, x[i]);
-    if (kind[i] == 0) store8<IO32>(qo.p + (b * qo.sb + t * qo.st + head[i] * qo.sh + 8 * a) * ES, x[i]);
-    if (__all_sync(0xffffffffu, kind[i] <= 0)) continue;
+  for (int i = 0; i < KC; ++i) {
+    const int vec = v0 + i * VPW + sub;
+    const bool key = vec < c.Hkv;
+    if (r.table && v0 < c.Hkv) rotate8(r, g, a, key, x[i]);
     uint32_t u[8];
     float s;
     int z;
     quant8<BITS>(x[i], u, s, z);
-    if (kind[i] <= 0 || page < 0) continue;
-    char *tile = tile_at<L::BYTES>(c, page, head[i], slot);
+    if (vec >= (int)nvec || page < 0) continue;
+    char *tile = tile_at<L::BYTES>(c, page, key ? vec : vec - c.Hkv, slot);
     const int tt = (int)(slot % TILE);
-    const bool key = kind[i] == 1;
     const uint2 w = pack8<BITS>(u);
     char *at = tile + (key ? L::k8(tt, a) : L::v8(tt, a));
     if (BITS == 4) *reinterpret_cast<uint32_t *>(at) = w.x;
@@ -252,6 +326,7 @@ __global__ void __launch_bounds__(THREADS) read_kernel(KvDev c, const int32_t *_
   using L = Tile<D, BITS>;
   constexpr int LPV = D / 8, ROWS = THREADS / LPV, ES = IO32 ? 4 : 2;
   const int a = threadIdx.x % LPV, row = threadIdx.x / LPV;
+  pdl_enter();
   const long item = blockIdx.x;
   const int head = (int)(item % c.Hkv), ti = (int)((item / c.Hkv) % tiles), b = (int)(item / ((long)c.Hkv * tiles));
   const long f = first ? first[b] : 0;
@@ -263,33 +338,42 @@ __global__ void __launch_bounds__(THREADS) read_kernel(KvDev c, const int32_t *_
   const int page = any ? page_of(c, b, base) : -1;
   if (any && page < 0 && threadIdx.x == 0) atomicOr(c.status, PACE_KV_BAD_PAGE);
   const char *tile = page >= 0 ? tile_at<L::BYTES>(c, page, head, base) : nullptr;
+  // all of the lane's codes and parameters are loaded before the first store: the stores could alias them
+  constexpr int N = TILE / ROWS;
+  uint2 w[2][N];
+  __nv_bfloat16 sc[2][N];
+  uint8_t z[2][N];
 #pragma unroll
-  for (int part = 0; part < 2; ++part) {
+  for (int i = 0; i < 2 * N; ++i) {
+    const int part = i / N, t = (i % N) * ROWS + row;
+    const long slot = base + t;
+    if (!tile || slot < f || slot >= live_end) continue;
+    const char *at = tile + (part ? L::v8(t, a) : L::k8(t, a));
+    if (BITS == 4) w[part][i % N] = make_uint2(*reinterpret_cast<const uint32_t *>(at), 0);
+    else w[part][i % N] = *reinterpret_cast<const uint2 *>(at);
+    const int p = (a >> 3) * TILE + L::pos(t);
+    sc[part][i % N] = reinterpret_cast<const __nv_bfloat16 *>(tile + (part ? L::VS : L::KS))[p];
+    if (BITS == 4) z[part][i % N] = reinterpret_cast<const uint8_t *>(tile + (part ? L::VZ : L::KZ))[p];
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * N; ++i) {
+    const int part = i / N, t = (i % N) * ROWS + row;
+    const long slot = base + t;
+    if (slot < f || slot >= f + c.n_tokens) continue;
     const KvTensor &o = part ? v : k;
+    float y[8];
+    if (tile && slot < e) {
+      int u[8];
+      unpack8<BITS>(w[part][i % N], u);
+      const float s = __bfloat162float(sc[part][i % N]);
+      const int zero = BITS == 4 ? z[part][i % N] : 128;
 #pragma unroll
-    for (int t0 = 0; t0 < TILE; t0 += ROWS) {
-      const int t = t0 + row;
-      const long slot = base + t;
-      if (slot < f || slot >= f + c.n_tokens) continue;
-      float y[8];
-      if (slot < e && tile) {
-        const char *at = tile + (part ? L::v8(t, a) : L::k8(t, a));
-        uint2 w;
-        if (BITS == 4) w = make_uint2(*reinterpret_cast<const uint32_t *>(at), 0);
-        else w = *reinterpret_cast<const uint2 *>(at);
-        const int p = (a >> 3) * TILE + L::pos(t);
-        const float s = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(tile + (part ? L::VS : L::KS))[p]);
-        const int z = BITS == 4 ? reinterpret_cast<const uint8_t *>(tile + (part ? L::VZ : L::KZ))[p] : 128;
-        int u[8];
-        unpack8<BITS>(w, u);
+      for (int j = 0; j < 8; ++j) y[j] = s * (float)(u[j] - zero);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = s * (float)(u[i] - z);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-      }
-      store8<IO32>(o.p + (b * o.sb + (slot - f) * o.st + head * o.sh + 8 * a) * ES, y);
+      for (int j = 0; j < 8; ++j) y[j] = 0.0f;
     }
+    store8<IO32>(o.p + (b * o.sb + (slot - f) * o.st + head * o.sh + 8 * a) * ES, y);
   }
 }
 
@@ -305,6 +389,7 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(KvDev c, int max_new, con
   __shared__ uint16_t scale[TILE][2][L::NG];
   __shared__ uint8_t zero[TILE][2][L::NG];
   const int b = blockIdx.x / c.Hkv, head = blockIdx.x % c.Hkv;
+  pdl_enter();
   const int n = min(max(n_keep[b], 0), c.n_tokens);
   const long len = c.lens[b];
   const int32_t *row = idx + (long)b * c.n_tokens;
@@ -360,14 +445,22 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(KvDev c, int max_new, con
   }
 }
 
-template <int D, int BITS, int IO32, int HC>
+// Launch with the programmatic-serialization attribute: the kernels wait for the one before at their first instruction.
+template <typename... P, typename... A>
+cudaError_t pdl_launch(void (*kernel)(P...), long blocks, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)blocks), dim3(THREADS), 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, int BITS, int IO32, int HC, int KC>
 cudaError_t launch_append(const KvDev &c, const KvTensor &q, const KvTensor &k, const KvTensor &v, const KvTensor &qo,
                           const KvRope &r, const int32_t *pos, cudaStream_t s) {
-  constexpr int VPW = 32 / (D / 8);
-  const int nvec = (q.p ? c.Hq : 0) + 2 * c.Hkv, chunks = (nvec + HC * VPW - 1) / (HC * VPW);
-  const long warps = (long)c.batch * c.n_tokens * chunks;
-  append_kernel<D, BITS, IO32, HC><<<(unsigned)((warps + THREADS / 32 - 1) / (THREADS / 32)), THREADS, 0, s>>>(c, q, k, v, qo, r, pos);
-  return cudaGetLastError();
+  constexpr int VPW = 32 / (D / 8), W = THREADS / 32;
+  const long tokens = (long)c.batch * c.n_tokens;
+  const long q_items = q.p ? tokens * ((c.Hq + HC - 1) / HC) : 0, q_blocks = (q_items + W * VPW - 1) / (W * VPW);
+  const long kv_warps = tokens * ((2 * c.Hkv + KC * VPW - 1) / (KC * VPW));
+  return pdl_launch(append_kernel<D, BITS, IO32, HC, KC>, q_blocks + (kv_warps + W - 1) / W, s, c, q, k, v, qo, r, pos, (int)q_blocks);
 }
 
 }  // namespace kv
@@ -403,30 +496,26 @@ cudaError_t rope_go(const KvRope &r, int n, int heads, int d, const KvTensor &x,
                     int inverse, cudaStream_t s) {
   const int per_block = (THREADS / 32) * (32 / (d / 8));
   const long items = (long)n * ((heads + HC - 1) / HC);
-  rope_kernel<IO32, HC><<<(unsigned)((items + per_block - 1) / per_block), THREADS, 0, s>>>(r, n, heads, d, x, pos, out,
-                                                                                          inverse ? -1.0f : 1.0f);
-  return cudaGetLastError();
+  return pdl_launch(rope_kernel<IO32, HC>, (items + per_block - 1) / per_block, s, r, n, heads, d, x, pos, out, inverse ? -1.0f : 1.0f);
 }
 template <int D, int BITS, int IO32>
 cudaError_t append_go(const KvDev &c, const KvTensor &q, const KvTensor &k, const KvTensor &v, const KvTensor &qo,
                       const KvRope &r, const int32_t *pos, cudaStream_t s) {
   const long vecs = (long)c.batch * c.n_tokens * ((q.p ? c.Hq : 0) + 2 * c.Hkv);
   if (vecs * (D / 8) > 4L * 2048 * device_sm_count())
-    return launch_append<D, BITS, IO32, 4>(c, q, k, v, qo, r, pos, s);
-  return launch_append<D, BITS, IO32, 1>(c, q, k, v, qo, r, pos, s);
+    return launch_append<D, BITS, IO32, 4, 2>(c, q, k, v, qo, r, pos, s);
+  return launch_append<D, BITS, IO32, 1, 1>(c, q, k, v, qo, r, pos, s);
 }
 template <int D, int BITS, int IO32>
 cudaError_t read_go(const KvDev &c, const int32_t *first, const int32_t *end, const KvTensor &k, const KvTensor &v,
                     cudaStream_t s) {
   const int tiles = (c.n_tokens + TILE - 1) / TILE + (first ? 1 : 0);
   const long blocks = (long)c.batch * c.Hkv * tiles;
-  read_kernel<D, BITS, IO32><<<(unsigned)blocks, THREADS, 0, s>>>(c, first, end, k, v, tiles);
-  return cudaGetLastError();
+  return pdl_launch(read_kernel<D, BITS, IO32>, blocks, s, c, first, end, k, v, tiles);
 }
 template <int D, int BITS, int IO32>
 cudaError_t keep_go(const KvDev &c, int max_new, const int32_t *idx, const int32_t *n_keep, cudaStream_t s) {
-  keep_kernel<D, BITS><<<(unsigned)(c.batch * c.Hkv), THREADS, 0, s>>>(c, max_new, idx, n_keep);
-  return cudaGetLastError();
+  return pdl_launch(keep_kernel<D, BITS>, (long)c.batch * c.Hkv, s, c, max_new, idx, n_keep);
 }
 }  // namespace
 
