@@ -34,6 +34,8 @@ pace_status check_config(const pace_kv_config *c) {
     return fail(PACE_ERR_INVALID_ARG, "page_tokens %d is not a multiple of %d in %d..4096", c->page_tokens, PACE_KV_TILE,
                 PACE_KV_TILE);
   if (c->n_pages < 1) return fail(PACE_ERR_INVALID_ARG, "n_pages %d < 1", c->n_pages);
+  if ((int64_t)c->n_pages * c->kv_heads * (c->page_tokens / PACE_KV_TILE) > (int64_t)INT32_MAX)
+    return fail(PACE_ERR_UNSUPPORTED, "the pool has more than 2^31 - 1 tiles of %d tokens", PACE_KV_TILE);
   if (c->max_batch < 1 || c->max_batch > PACE_KV_MAX_BATCH)
     return fail(PACE_ERR_INVALID_ARG, "max_batch %d outside 1..%d", c->max_batch, PACE_KV_MAX_BATCH);
   if (c->max_new < 1 || c->max_new > PACE_KV_MAX_NEW)
@@ -106,7 +108,8 @@ pace_status check_step(const pace_kv *kv, const pace_kv_step *s, const char *cal
   if ((lens && !s->lens) || !s->table) return fail(PACE_ERR_INVALID_ARG, "%s: lens or table is NULL", call);
   if (!aligned(s->lens, 4) || !aligned(s->n_new, 4) || !aligned(s->table, 4))
     return fail(PACE_ERR_INVALID_ARG, "%s: lens, n_new and table must be 4-byte aligned", call);
-  if (s->table_cols < 1) return fail(PACE_ERR_INVALID_ARG, "%s: table_cols %d < 1", call, s->table_cols);
+  if (s->table_cols < 1 || (int64_t)s->table_cols * kv->cfg.page_tokens > (int64_t)1 << 30)
+    return fail(PACE_ERR_INVALID_ARG, "%s: table_cols %d outside 1..2^30 tokens' pages", call, s->table_cols);
   *d = kv->dev;
   d->batch = s->batch;
   d->n_tokens = s->n_tokens;

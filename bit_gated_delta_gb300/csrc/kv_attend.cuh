@@ -8,16 +8,17 @@
 // rows on that side would take, and the softmax handles no empty rows.
 //
 // The cache is bound by bytes only if its codes reach the tensor cores in about three instructions each (46 4-bit elements a
-// clock and SM at the measured 6.8 TB/s against 128 lanes), so codes become bf16 by bit operations and enter the products as
-// exact integers: 4 bits: (w & 0x000F000F) | 0x43004300 is the pair 128 + u; values subtract 128 + z exactly, keys leave it to
-// the scores (acc - (128 + z) * sum(q), per group). 8 bits: 128 + (u & 127) minus 128 or 256 by the top bit. The scales of
-// a key group multiply the fp32 accumulators, those of a value group the weights before they are rounded to bf16 (fp32 I/O: three
-// bf16 parts of queries and weights, and keys subtracted too, so nothing is rounded below 2^-24).
+// clock and SM at the measured 6.8 TB/s against 128 lanes, half of that for bit operations), so codes become fp16 under the
+// exponent of 1024 by one bit operation a pair and one exact subtraction on the other pipe, and enter the products as integers.
+// The scales of a key group multiply the fp32 accumulators, those of a value group enter the exponent of the weights. Queries and
+// weights are fp16 relative to a power of two (11 bits); with fp32 I/O both are three bf16 parts, so nothing is rounded below 2^-24.
 //
 // Work: the tiles of all (sequence, KV head, row block) items form one line, cut into equal shares, one a block; a block's warps
 // take its tiles in turn, each through its own ring of tiles filled by bulk copies (one copy a tile). Items cut by a share
 // boundary leave partial results; the last block to finish an item joins them, in block order, so results do not depend on timing.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "kv_common.cuh"
 #include "umma.cuh"
@@ -61,6 +62,56 @@ __device__ __forceinline__ uint32_t pair4(uint32_t w, int p) { return ((w >> (4 
 // bytes 0 and 2 of w (codes c + 128) as the exact bf16 pair of c
 __device__ __forceinline__ uint32_t pair8(uint32_t w) {
   return sub_bf16x2((w & 0x007F007Fu) | 0x43004300u, (~w & 0x00800080u) | 0x43004300u);
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t h2sub(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
+                            *reinterpret_cast<const __half2 *>(&c));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t h2pack(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+// The four pairs of a word of 4-bit codes as fp16 u - z, exactly: the nibble at bit 0 of a half under the exponent of 1024 reads
+// 1024 + u, the one at bit 4 reads 1024 + 16 u = 16 (64 + u). z1024 and z64 are the pairs 1024 + z and 64 + z.
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t z1024, uint32_t z64, uint32_t (&r)[4]) {
+  constexpr uint32_t SIXTEENTH = 0x2C002C00u;
+  const uint32_t x = w >> 8, nz = z64 ^ 0x80008000u;
+  r[0] = h2sub((w & 0x000F000Fu) | 0x64006400u, z1024);
+  r[1] = h2fma((w & 0x00F000F0u) | 0x64006400u, SIXTEENTH, nz);
+  r[2] = h2sub((x & 0x000F000Fu) | 0x64006400u, z1024);
+  r[3] = h2fma((x & 0x00F000F0u) | 0x64006400u, SIXTEENTH, nz);
+}
+// Bytes (0, 2) and (1, 3) of a word of 8-bit codes c + 128 as fp16 c.
+__device__ __forceinline__ void codes8(uint32_t w, uint32_t &even, uint32_t &odd) {
+  constexpr uint32_t M1152 = 0xE480E480u;
+  even = h2add(__byte_perm(w, 0x64646464u, 0x4240), M1152);
+  odd = h2add(__byte_perm(w, 0x64646464u, 0x4341), M1152);
 }
 
 // x ~= sum of PARTS bf16 parts, for a pair.
@@ -166,7 +217,6 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   using S = AttendShape<D, BITS, NT, PARTS, NW, STAGES>;
   using L = Tile<D, BITS>;
   constexpr int NG = L::NG, ROWS = S::ROWS;
-  constexpr bool SUBK = BITS == 4 && PARTS > 1;       // keys subtracted exactly; else the scores take it
   extern __shared__ __align__(128) char smem[];
   char *ring_all = smem;
   uint64_t *bars_all = reinterpret_cast<uint64_t *>(smem + S::RING);
@@ -195,7 +245,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   // ---- the warp's fetch side: its tiles of all segments of the block, STAGES ahead
   long fpos = lo;                                     // line position of the fetch segment's end
   Segment f{0, 0, 0, 0, 0, 0};
-  int ftile = 0, fbatch = 0, fstage = 0, mypage = -1;
+  const int tpp = c.page / TILE;                      // tiles a page
+  int ftile = 0, fbatch = 0, fstage = 0, mytile = -1;
   uint32_t bad = 0;                                   // stages whose page was bad (their tile is masked)
   bool dead = false;
   uint32_t phase = 0;                                 // parity per stage
@@ -212,21 +263,21 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       fbatch = 32;
     }
     if (fdone || dead) return;
-    if (fbatch == 32) {                               // pages of the warp's next 32 tiles of this segment, one a lane
+    if (fbatch == 32) {                               // the warp's next 32 tiles of this segment, one a lane
       const int t = ftile + NW * lane;
-      mypage = t < f.end ? page_of(c, f.b, (long)t * TILE) : 0;
-      if (mypage < 0) atomicOr(c.status, PACE_KV_BAD_PAGE);
+      mytile = t < f.end ? tile_index(c, f.b, f.h, t, tpp) : 0;
+      if (mytile < 0) atomicOr(c.status, PACE_KV_BAD_PAGE);
       fbatch = 0;
     }
-    const int page = __shfl_sync(0xffffffffu, mypage, fbatch);
-    if (page < 0) {
+    const int at = __shfl_sync(0xffffffffu, mytile, fbatch);
+    if (at < 0) {
       bad |= 1u << fstage;
       if (lane == 0) umma::mbar_arrive(&bars[fstage]);
     } else {
       bad &= ~(1u << fstage);
       if (lane == 0) {
         umma::mbar_arrive_expect_tx(&bars[fstage], L::BYTES);
-        umma::bulk_g2s(ring + fstage * L::BYTES, tile_at<L::BYTES>(c, page, f.h, (long)ftile * TILE), L::BYTES, &bars[fstage]);
+        umma::bulk_g2s(ring + fstage * L::BYTES, c.pool + (long)at * L::BYTES, L::BYTES, &bars[fstage]);
       }
     }
     ftile += NW;
@@ -254,7 +305,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 
     // ---- queries as B fragments: lane (j, cc) holds dims 64g + 16cc .. + 15 of row j of each block of eight
     uint32_t qf[NT][NG][PARTS][8];
-    float qs[NT][NG][2];                              // sum of the group's queries of rows 2cc, 2cc+1 (4-bit keys)
+    float crow[NT][2];                                // what a score of rows 2cc, 2cc+1 is multiplied by
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int row = row0 + 8 * n + j, t = row / G, hh = sg.h * G + row - t * G;
@@ -284,15 +335,26 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
             for (int e = 0; e < PARTS; ++e) qf[n][g][e][2 * i] = a[e], qf[n][g][e][2 * i + 1] = b[e];
           }
         }
-        if (BITS == 4 && !SUBK) {
-          float s = 0.0f;
+      }
+      crow[n][0] = crow[n][1] = p.scale_log2;
+      if (PARTS == 1) {
+        // bf16 -> fp16 over a power of two that puts the row's largest element in [1, 2): exact but below 2^-14 of it
+        uint32_t top = 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s += __uint_as_float(qf[n][g][0][i] << 16) + __uint_as_float(qf[n][g][0][i] & 0xFFFF0000u);
-          s += __shfl_xor_sync(0xffffffffu, s, 1);
-          s += __shfl_xor_sync(0xffffffffu, s, 2);
-          qs[n][g][0] = __shfl_sync(0xffffffffu, s, 8 * cc);
-          qs[n][g][1] = __shfl_sync(0xffffffffu, s, 8 * cc + 4);
-        }
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = max(top, max((qf[n][g][0][i] << 16) & 0x7FFF0000u, qf[n][g][0][i] & 0x7FFF0000u));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max(min((int)(top >> 23) - 127, 126), -126);
+        const float down = exp2i(-e);
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            qf[n][g][0][i] = h2pack(__uint_as_float(qf[n][g][0][i] << 16) * down, __uint_as_float(qf[n][g][0][i] & 0xFFFF0000u) * down);
+        crow[n][0] = p.scale_log2 * exp2i(__shfl_sync(0xffffffffu, e, 8 * cc));
+        crow[n][1] = p.scale_log2 * exp2i(__shfl_sync(0xffffffffu, e, 8 * cc + 4));
       }
     }
 
@@ -368,43 +430,55 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
-            uint32_t zka = 0, zkb = 0;
-            if (SUBK) {
-              zka = __byte_perm(kzw[g], 0, 0x4040 | (2 * blk) | ((2 * blk) << 8)) | 0x43004300u;
-              zkb = __byte_perm(kzw[g], 0, 0x4040 | (2 * blk + 1) | ((2 * blk + 1) << 8)) | 0x43004300u;
+            uint32_t zka = 0, zkb = 0, z64a = 0, z64b = 0;
+            if (BITS == 4) {
+              const uint32_t hi = PARTS == 1 ? 0x64646464u : 0x43434343u;                     // 1024 + z or 128 + z
+              zka = __byte_perm(kzw[g], hi, 0x4040 | (2 * blk) | ((2 * blk) << 8));
+              zkb = __byte_perm(kzw[g], hi, 0x4040 | (2 * blk + 1) | ((2 * blk + 1) << 8));
+              if (PARTS == 1) z64a = h2add(zka, 0xE380E380u /* -960 */), z64b = h2add(zkb, 0xE380E380u);
+            }
+            uint32_t fa[8], fb[8];                      // the group's pairs of the two tokens
+            if (PARTS == 1) {
+              if (BITS == 4) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t r[4];
+                  codes4(wa[g][h], zka, z64a, r);
+                  fa[4 * h] = r[0], fa[4 * h + 1] = r[1], fa[4 * h + 2] = r[2], fa[4 * h + 3] = r[3];
+                  codes4(wb[g][h], zkb, z64b, r);
+                  fb[4 * h] = r[0], fb[4 * h + 1] = r[1], fb[4 * h + 2] = r[2], fb[4 * h + 3] = r[3];
+                }
+              } else {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  codes8(wa[g][h % (BITS == 4 ? 2 : 4)], fa[2 * h], fa[2 * h + 1]);
+                  codes8(wb[g][h % (BITS == 4 ? 2 : 4)], fb[2 * h], fb[2 * h + 1]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (BITS == 4) {
+                  const uint32_t x = wa[g][k >> 1], y = wb[g][k >> 1];
+                  fa[2 * k] = sub_bf16x2(pair4(x, 2 * (k & 1)), zka), fb[2 * k] = sub_bf16x2(pair4(y, 2 * (k & 1)), zkb);
+                  fa[2 * k + 1] = sub_bf16x2(pair4(x, 2 * (k & 1) + 1), zka), fb[2 * k + 1] = sub_bf16x2(pair4(y, 2 * (k & 1) + 1), zkb);
+                } else {
+                  const uint32_t x = wa[g][k % (BITS == 4 ? 2 : 4)], y = wb[g][k % (BITS == 4 ? 2 : 4)];
+                  fa[2 * k] = pair8(x), fb[2 * k] = pair8(y), fa[2 * k + 1] = pair8(x >> 8), fb[2 * k + 1] = pair8(y >> 8);
+                }
+              }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t a0, a1, a2, a3;
-              if (BITS == 4) {
-                const uint32_t x = wa[g][k >> 1], y = wb[g][k >> 1];
-                a0 = pair4(x, 2 * (k & 1)), a1 = pair4(y, 2 * (k & 1));
-                a2 = pair4(x, 2 * (k & 1) + 1), a3 = pair4(y, 2 * (k & 1) + 1);
-                if (SUBK) a0 = sub_bf16x2(a0, zka), a1 = sub_bf16x2(a1, zkb), a2 = sub_bf16x2(a2, zka), a3 = sub_bf16x2(a3, zkb);
-              } else {
-                const uint32_t x = wa[g][k % (BITS == 4 ? 2 : 4)], y = wb[g][k % (BITS == 4 ? 2 : 4)];
-                a0 = pair8(x), a1 = pair8(y), a2 = pair8(x >> 8), a3 = pair8(y >> 8);
-              }
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < PARTS; ++e)
-                  mma_bf16(d[n], a0, a1, a2, a3, qf[n][g][e][2 * k], qf[n][g][e][2 * k + 1]);
-            }
+                for (int e = 0; e < PARTS; ++e) {
+                  if (PARTS == 1) mma_f16(d[n], fa[2 * k], fb[2 * k], fa[2 * k + 1], fb[2 * k + 1], qf[n][g][e][2 * k], qf[n][g][e][2 * k + 1]);
+                  else mma_bf16(d[n], fa[2 * k], fb[2 * k], fa[2 * k + 1], fb[2 * k + 1], qf[n][g][e][2 * k], qf[n][g][e][2 * k + 1]);
+                }
             const uint32_t sw = blk ? ksw[g].y : ksw[g].x;
-            const float s0 = __uint_as_float(sw << 16) * p.scale_log2, s1 = __uint_as_float(sw & 0xFFFF0000u) * p.scale_log2;
-            if (BITS == 4 && !SUBK) {
-              // 2^23 + z from the byte, then 128 + z
-              const float z0 = __uint_as_float(__byte_perm(kzw[g], 0x4B000000u, 0x7440 | (2 * blk))) - (8388608.0f - 128.0f);
-              const float z1 = __uint_as_float(__byte_perm(kzw[g], 0x4B000000u, 0x7440 | (2 * blk + 1))) - (8388608.0f - 128.0f);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                d[n][0] = fmaf(-z0, qs[n][g][0], d[n][0]);
-                d[n][1] = fmaf(-z0, qs[n][g][1], d[n][1]);
-                d[n][2] = fmaf(-z1, qs[n][g][0], d[n][2]);
-                d[n][3] = fmaf(-z1, qs[n][g][1], d[n][3]);
-              }
-            }
+            const float s0 = __uint_as_float(sw << 16), s1 = __uint_as_float(sw & 0xFFFF0000u);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               s[blk][n][0] = fmaf(s0, d[n][0], s[blk][n][0]);
@@ -413,6 +487,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
               s[blk][n][3] = fmaf(s1, d[n][3], s[blk][n][3]);
             }
           }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[blk][n][e] *= crow[n][e & 1];
         }
       }
       // ---- masks: only tiles that reach past the context (or were lost)
@@ -437,14 +515,36 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
               }
           }
       }
-      // ---- running maximum: raised only when a score passes it by 2^8 (weights up to 256, the sum is fp32)
+      // ---- weights. bf16 I/O: the scale of a value group enters the exponent, w = 2^(s + log2 s_v - m + 6) with m the running
+      // maximum of s + log2 s_v, so that fp16 weights keep 11 bits whatever the scales; the sum takes 2^(s - m). fp32 I/O: the
+      // scale multiplies the weight. m is raised only when a score passes it by 2^8 (fp16 weights up to 2^14, sums in fp32).
+      float lv[NG][2][2], lm[2][2];                      // log2 of the value scales of the lane's tokens, their largest
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) lm[blk][half] = PARTS == 1 ? -60.0f : 0.0f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint2 vsw = *reinterpret_cast<const uint2 *>(st + L::VS + g * 64 + j * 8);
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          const uint32_t sw = blk ? vsw.y : vsw.x;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float x = __uint_as_float(half ? sw & 0xFFFF0000u : sw << 16);
+            if (edge && (tok0 + 16 * blk + 8 * half + tau(j) >= tokens || lost)) x = 0.0f;   // never written: may hold anything
+            lv[g][blk][half] = PARTS == 1 ? log2_approx(x) : x;
+            if (PARTS == 1) lm[blk][half] = fmaxf(lm[blk][half], lv[g][blk][half]);
+          }
+        }
+      }
       float mx[NT][2];
       bool grow = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          mx[n][r] = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r]));
+          mx[n][r] = fmaxf(fmaxf(s[0][n][r] + lm[0][0], s[0][n][2 + r] + lm[0][1]), fmaxf(s[1][n][r] + lm[1][0], s[1][n][2 + r] + lm[1][1]));
           grow |= mx[n][r] > m[n][r] + 8.0f;
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -474,9 +574,11 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
           for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const float pr = exp2_approx(s[blk][n][2 * half + r] - mu);
-              s[blk][n][2 * half + r] = pr;
+              float &x = s[blk][n][2 * half + r];
+              x -= mu;
+              const float pr = exp2_approx(x);
               l[n][r] += pr;
+              x = PARTS == 1 ? x + 6.0f : pr;
             }
         }
       // ---- output
@@ -503,56 +605,74 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 #pragma unroll
           for (int gi = 0; gi < GP; ++gi) {
             const int g = g0 + gi;
-            const uint32_t sw = *reinterpret_cast<const uint32_t *>(st + L::VS + g * 64 + j * 8 + blk * 4);
-            float s0 = __uint_as_float(sw << 16), s1 = __uint_as_float(sw & 0xFFFF0000u);
-            if (edge) {                                 // slots never written may hold anything
-              const int tk = tok0 + 16 * blk + tau(j);
-              if (tk >= tokens || lost) s0 = 0.0f;
-              if (tk + 8 >= tokens || lost) s1 = 0.0f;
-            }
             uint32_t bf[NT][PARTS][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               uint32_t x[PARTS], y[PARTS];
-              split_pair<PARTS>(s[blk][n][0] * s0, s[blk][n][1] * s0, x);
-              split_pair<PARTS>(s[blk][n][2] * s1, s[blk][n][3] * s1, y);
+              const float v0s = lv[g][blk][0], v1s = lv[g][blk][1];
+              if (PARTS == 1) {
+                x[0] = h2pack(exp2_approx(s[blk][n][0] + v0s), exp2_approx(s[blk][n][1] + v0s));
+                y[0] = h2pack(exp2_approx(s[blk][n][2] + v1s), exp2_approx(s[blk][n][3] + v1s));
+              } else {
+                split_pair<PARTS>(s[blk][n][0] * v0s, s[blk][n][1] * v0s, x);
+                split_pair<PARTS>(s[blk][n][2] * v1s, s[blk][n][3] * v1s, y);
+              }
 #pragma unroll
               for (int e = 0; e < PARTS; ++e) bf[n][e][0] = movmatrix(x[e]), bf[n][e][1] = movmatrix(y[e]);
             }
+            uint32_t a01[8], a23[8];                     // dims 8j + 0..7 (even: A row j, odd: row j + 8) of the two token pairs
             if (BITS == 4) {
               const uint32_t x0 = gi ? v0.y : v0.x, x1 = gi ? v1.y : v1.x, x2 = gi ? v2.y : v2.x, x3 = gi ? v3.y : v3.x;
-              const uint32_t lo01 = __byte_perm(x0, x1, 0x5410), hi01 = __byte_perm(x0, x1, 0x7632);
-              const uint32_t lo23 = __byte_perm(x2, x3, 0x5410), hi23 = __byte_perm(x2, x3, 0x7632);
+              const uint32_t w[4] = {__byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632), __byte_perm(x2, x3, 0x5410),
+                                     __byte_perm(x2, x3, 0x7632)};
               const uint2 vzw = *reinterpret_cast<const uint2 *>(st + L::VZ + g * 32 + cc * 8);
               const int q0 = 2 * blk, q1 = 2 * blk + 1;
-              const uint32_t z01 = (__byte_perm(vzw.x, vzw.y, q0 * 0x0011 + (4 + q0) * 0x1100) & 0x00FF00FFu) | 0x43004300u;
-              const uint32_t z23 = (__byte_perm(vzw.x, vzw.y, q1 * 0x0011 + (4 + q1) * 0x1100) & 0x00FF00FFu) | 0x43004300u;
+              const uint32_t hi = PARTS == 1 ? 0x64006400u : 0x43004300u;                       // 1024 + z or 128 + z
+              const uint32_t z01 = (__byte_perm(vzw.x, vzw.y, q0 * 0x0011 + (4 + q0) * 0x1100) & 0x00FF00FFu) | hi;
+              const uint32_t z23 = (__byte_perm(vzw.x, vzw.y, q1 * 0x0011 + (4 + q1) * 0x1100) & 0x00FF00FFu) | hi;
+              if (PARTS == 1) {
+                const uint32_t y01 = h2add(z01, 0xE380E380u), y23 = h2add(z23, 0xE380E380u);    // 64 + z
+                uint32_t r[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t a0 = sub_bf16x2(pair4(lo01, i), z01), a1 = sub_bf16x2(pair4(hi01, i), z01);
-                const uint32_t a2 = sub_bf16x2(pair4(lo23, i), z23), a3 = sub_bf16x2(pair4(hi23, i), z23);
+                for (int o = 0; o < 2; ++o) {
+                  codes4(w[o], z01, y01, r);
+                  a01[o] = r[0], a01[2 + o] = r[1], a01[4 + o] = r[2], a01[6 + o] = r[3];
+                  codes4(w[2 + o], z23, y23, r);
+                  a23[o] = r[0], a23[2 + o] = r[1], a23[4 + o] = r[2], a23[6 + o] = r[3];
+                }
+              } else {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                  for (int e = 0; e < PARTS; ++e) mma_bf16(acc[g][i][n], a0, a1, a2, a3, bf[n][e][0], bf[n][e][1]);
+                  for (int o = 0; o < 2; ++o) a01[2 * i + o] = sub_bf16x2(pair4(w[o], i), z01), a23[2 * i + o] = sub_bf16x2(pair4(w[2 + o], i), z23);
               }
             } else {
 #pragma unroll
               for (int h2 = 0; h2 < 2; ++h2) {
                 const uint32_t x0 = h2 ? v0.y : v0.x, x1 = h2 ? v1.y : v1.x, x2 = h2 ? v2.y : v2.x, x3 = h2 ? v3.y : v3.x;
-                const uint32_t lo01 = __byte_perm(x0, x1, 0x5410), hi01 = __byte_perm(x0, x1, 0x7632);
-                const uint32_t lo23 = __byte_perm(x2, x3, 0x5410), hi23 = __byte_perm(x2, x3, 0x7632);
+                const uint32_t w[4] = {__byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632), __byte_perm(x2, x3, 0x5410),
+                                       __byte_perm(x2, x3, 0x7632)};
 #pragma unroll
-                for (int ii = 0; ii < 2; ++ii) {
-                  const uint32_t a0 = pair8(lo01 >> (8 * ii)), a1 = pair8(hi01 >> (8 * ii));
-                  const uint32_t a2 = pair8(lo23 >> (8 * ii)), a3 = pair8(hi23 >> (8 * ii));
-#pragma unroll
-                  for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < PARTS; ++e) mma_bf16(acc[g][2 * h2 + ii][n], a0, a1, a2, a3, bf[n][e][0], bf[n][e][1]);
+                for (int o = 0; o < 2; ++o) {
+                  if (PARTS == 1) {
+                    codes8(w[o], a01[4 * h2 + o], a01[4 * h2 + 2 + o]);
+                    codes8(w[2 + o], a23[4 * h2 + o], a23[4 * h2 + 2 + o]);
+                  } else {
+                    a01[4 * h2 + o] = pair8(w[o]), a01[4 * h2 + 2 + o] = pair8(w[o] >> 8);
+                    a23[4 * h2 + o] = pair8(w[2 + o]), a23[4 * h2 + 2 + o] = pair8(w[2 + o] >> 8);
+                  }
                 }
               }
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < PARTS; ++e) {
+                  if (PARTS == 1) mma_f16(acc[g][i][n], a01[2 * i], a01[2 * i + 1], a23[2 * i], a23[2 * i + 1], bf[n][e][0], bf[n][e][1]);
+                  else mma_bf16(acc[g][i][n], a01[2 * i], a01[2 * i + 1], a23[2 * i], a23[2 * i + 1], bf[n][e][0], bf[n][e][1]);
+                }
           }
         }
       }
@@ -596,8 +716,9 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
         const float mi = ml[(i * ROWS + row) * 2];
-        const float f2 = mi == -INFINITY ? 0.0f : exp2_approx(mi - M);
+        float f2 = mi == -INFINITY ? 0.0f : exp2_approx(mi - M);
         Ls += f2 * ml[(i * ROWS + row) * 2 + 1];
+        if (PARTS == 1) f2 *= 0x1p-6f;
         const float4 u = *reinterpret_cast<const float4 *>(scratch + (i * ROWS + row) * S::OROW + e8);
         const float4 v = *reinterpret_cast<const float4 *>(scratch + (i * ROWS + row) * S::OROW + e8 + 4);
         y[0] += f2 * u.x, y[1] += f2 * u.y, y[2] += f2 * u.z, y[3] += f2 * u.w;

@@ -17,8 +17,6 @@
 // Every wait is bounded; one that gives up sets the status word, and the block leaves after its copies and products have ended.
 #pragma once
 
-#include <cuda_fp16.h>
-
 #include "kv_attend.cuh"
 
 namespace pace {
@@ -58,24 +56,6 @@ constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 1
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
   return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
-__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
-  const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
-                            *reinterpret_cast<const __half2 *>(&c));
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t h2pack(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
 }
 __device__ __forceinline__ void bar_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
 
@@ -204,6 +184,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
 
   if (warp == S::W_LOAD) {
     // ---------------------------------------------------------------- copies: raw tiles of 2 x 32 tokens
+    const int tpp = c.page / TILE;
     int stage = 0, n = 0;
     bool good = true;
     for (long pos = lo; pos < hi && good;) {
@@ -212,13 +193,12 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       bool over;
       const int tokens = seq_tokens(c, sg.b, over);
       const int last = 2 * sg.end;
-      for (int s0 = 2 * sg.tile; s0 < last && good; s0 += 32) {         // pages of 32 storage tiles, one a lane
-        const long tok = (long)(s0 + lane) * TILE;
-        int page = tok < tokens && s0 + lane < last ? page_of(c, sg.b, tok) : -2;
-        if (page == -1) atomicOr(c.status, PACE_KV_BAD_PAGE);
+      for (int s0 = 2 * sg.tile; s0 < last && good; s0 += 32) {         // 32 storage tiles, one a lane
+        const int mytile = (s0 + lane) < last && (s0 + lane) * TILE < tokens ? tile_index(c, sg.b, sg.h, s0 + lane, tpp) : -2;
+        if (mytile == -1) atomicOr(c.status, PACE_KV_BAD_PAGE);
         const int kn = min(32, last - s0);
         for (int k = 0; k < kn; k += 2) {
-          const int pa = __shfl_sync(0xffffffffu, page, k), pb = __shfl_sync(0xffffffffu, page, k + 1);
+          const int pa = __shfl_sync(0xffffffffu, mytile, k), pb = __shfl_sync(0xffffffffu, mytile, k + 1);
           if (n >= RS && !mbar_wait(&raw_free[stage], (n / RS - 1) & 1, LIMIT)) good = false;
           good = __all_sync(0xffffffffu, good);
           if (!good) break;
@@ -228,8 +208,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             if (bytes) mbar_arrive_expect_tx(&raw_full[stage], bytes);
             else mbar_arrive(&raw_full[stage]);
             char *dst = smem + S::ORAW + stage * S::RAW;
-            if (pa >= 0) bulk_g2s(dst, tile_at<L::BYTES>(c, pa, sg.h, (long)(s0 + k) * TILE), L::BYTES, &raw_full[stage]);
-            if (pb >= 0) bulk_g2s(dst + L::BYTES, tile_at<L::BYTES>(c, pb, sg.h, (long)(s0 + k + 1) * TILE), L::BYTES, &raw_full[stage]);
+            if (pa >= 0) bulk_g2s(dst, c.pool + (long)pa * L::BYTES, L::BYTES, &raw_full[stage]);
+            if (pb >= 0) bulk_g2s(dst + L::BYTES, c.pool + (long)pb * L::BYTES, L::BYTES, &raw_full[stage]);
           }
           ++n;
           stage = stage + 1 == RS ? 0 : stage + 1;

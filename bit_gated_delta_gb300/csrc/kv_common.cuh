@@ -133,6 +133,13 @@ __device__ __forceinline__ char *tile_at(const KvDev &c, int page, int head, lon
   const long tiles = c.page / TILE;
   return c.pool + (((long)page * c.Hkv + head) * tiles + (slot % c.page) / TILE) * (long)TB;
 }
+// Index in the pool of tile t (tokens 32t ..) of sequence b and KV head h, or -1; tpp = tiles a page.
+__device__ __forceinline__ int tile_index(const KvDev &c, int b, int h, int t, int tpp) {
+  const int col = t / tpp;
+  if (col >= c.table_cols) return -1;
+  const int pg = c.table[(long)b * c.table_cols + col];
+  return pg >= 0 && pg < c.n_pages ? (pg * c.Hkv + h) * tpp + (t - col * tpp) : -1;
+}
 __device__ __forceinline__ int new_tokens(const KvDev &c, int b) {
   return c.n_new ? min(max(c.n_new[b], 0), c.n_tokens) : c.n_tokens;
 }
