@@ -93,19 +93,35 @@ __device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
                             *reinterpret_cast<const __half2 *>(&c));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
+__device__ __forceinline__ uint32_t h2fms(uint32_t a, uint32_t b, uint32_t c) {   // a b - c
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
+                            __hneg2(*reinterpret_cast<const __half2 *>(&c)));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
 __device__ __forceinline__ uint32_t h2pack(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 // The four pairs of a word of 4-bit codes as fp16 u - z, exactly: the nibble at bit 0 of a half under the exponent of 1024 reads
 // 1024 + u, the one at bit 4 reads 1024 + 16 u = 16 (64 + u). z1024 and z64 are the pairs 1024 + z and 64 + z.
-__device__ __forceinline__ void codes4(uint32_t w, uint32_t z1024, uint32_t z64, uint32_t (&r)[4]) {
+// `magic` is 0x64006400, kept in a register (opaque) so that mask and exponent are one three-input operation.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  uint32_t y;
+  asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(w), "r"(mask), "r"(magic));
+  return y;
+}
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t z1024, uint32_t z64, uint32_t magic, uint32_t (&r)[4]) {
   constexpr uint32_t SIXTEENTH = 0x2C002C00u;
-  const uint32_t x = w >> 8, nz = z64 ^ 0x80008000u;
-  r[0] = h2sub((w & 0x000F000Fu) | 0x64006400u, z1024);
-  r[1] = h2fma((w & 0x00F000F0u) | 0x64006400u, SIXTEENTH, nz);
-  r[2] = h2sub((x & 0x000F000Fu) | 0x64006400u, z1024);
-  r[3] = h2fma((x & 0x00F000F0u) | 0x64006400u, SIXTEENTH, nz);
+  const uint32_t x = w >> 8;
+  r[0] = h2sub(mask_or(w, 0x000F000Fu, magic), z1024);
+  r[1] = h2fms(mask_or(w, 0x00F000F0u, magic), SIXTEENTH, z64);
+  r[2] = h2sub(mask_or(x, 0x000F000Fu, magic), z1024);
+  r[3] = h2fms(mask_or(x, 0x00F000F0u, magic), SIXTEENTH, z64);
 }
 // Bytes (0, 2) and (1, 3) of a word of 8-bit codes c + 128 as fp16 c.
 __device__ __forceinline__ void codes8(uint32_t w, uint32_t &even, uint32_t &odd) {
@@ -134,32 +150,42 @@ struct AttendArgs {
   int min_share;        // fewest tiles a block takes
 };
 
-// One position on the line of tiles.
+// One stretch of an item on the line of tiles.
 struct Segment {
   int b, h, rb;         // item
   int tile, end;        // tiles [tile, end) of it
   int tiles;            // of the whole item
 };
+// One sequence of the call: cached tokens, new tokens, both together (no more than the page table holds).
+struct Seq {
+  int len, fresh, tokens;
+};
 
-// Exclusive prefix sums over the sequences of their items' tiles, in shared memory: cum[0..batch].
-__device__ __forceinline__ int seq_tokens(const KvDev &c, int b, bool &over) {
-  const long cap = (long)c.table_cols * c.page;
-  const long n = (long)max(c.lens[b], 0) + new_tokens(c, b);
-  over = n > cap || c.lens[b] < 0;
-  return (int)(n < cap ? n : cap);
+__device__ __forceinline__ Seq sequence(const KvDev &c, int b, bool report) {
+  const int cap = c.table_cols * c.page, len = c.lens[b];
+  const int fresh = new_tokens(c, b);
+  Seq q{max(len, 0), fresh, 0};
+  const long n = (long)q.len + fresh;
+  q.tokens = (int)min(n, (long)cap);
+  if (report && (n > cap || len < 0)) atomicOr(c.status, PACE_KV_BAD_PAGE);
+  return q;
 }
-__device__ __forceinline__ int seq_tiles(int tokens) { return max((tokens + TILE - 1) / TILE, 1); }
+// 64-bit quotient of non-negative numbers, by the short division where both fit 32 bits.
+__device__ __forceinline__ long quotient(long a, long b) {
+  return ((a | b) >> 32) == 0 ? (long)((unsigned)a / (unsigned)b) : a / b;
+}
 
-__device__ __forceinline__ void tile_line(const KvDev &c, long per_seq, long *cum, long *warp_sums) {
+// The sequences, and the exclusive prefix sums of their items' tiles of TOK tokens (at least one each), in shared memory:
+// seq[0..batch), cum[0..batch].
+template <int TOK>
+__device__ __forceinline__ void tile_line(const KvDev &c, long per_seq, Seq *seq, long *cum, long *warp_sums) {
   const int n = c.batch, nt = blockDim.x, per = (n + nt - 1) / nt, b0 = threadIdx.x * per;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = nt >> 5;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   long s = 0;
-  for (int i = 0; i < per; ++i) {
-    if (b0 + i >= n) break;
-    bool over;
-    const int tok = seq_tokens(c, b0 + i, over);
-    if (over) atomicOr(c.status, PACE_KV_BAD_PAGE);
-    s += seq_tiles(tok) * per_seq;
+  for (int i = 0; i < per && b0 + i < n; ++i) {
+    const Seq q = sequence(c, b0 + i, blockIdx.x == 0);
+    seq[b0 + i] = q;
+    s += max((q.tokens + TOK - 1) / TOK, 1) * per_seq;
     cum[b0 + i + 1] = s;
   }
   long x = s;
@@ -171,14 +197,14 @@ __device__ __forceinline__ void tile_line(const KvDev &c, long per_seq, long *cu
   if (lane == 31) warp_sums[w] = x;
   __syncthreads();
   long base = x - s;
-  for (int i = 0; i < w && i < nw; ++i) base += warp_sums[i];
-  for (int i = 0; i < per; ++i)
-    if (b0 + i < n) cum[b0 + i + 1] += base;
+  for (int i = 0; i < w; ++i) base += warp_sums[i];
+  for (int i = 0; i < per && b0 + i < n; ++i) cum[b0 + i + 1] += base;
   if (threadIdx.x == 0) cum[0] = 0;
   __syncthreads();
 }
 
-__device__ __forceinline__ Segment segment_at(const long *cum, int batch, int row_blocks, int kv_heads, long p, long hi) {
+template <int TOK>
+__device__ __forceinline__ Segment segment_at(const Seq *seq, const long *cum, int batch, int row_blocks, long p, long hi) {
   int lo = 0, up = batch;                  // last b with cum[b] <= p
   while (up - lo > 1) {
     const int mid = (lo + up) >> 1;
@@ -187,9 +213,9 @@ __device__ __forceinline__ Segment segment_at(const long *cum, int batch, int ro
   }
   Segment s;
   s.b = lo;
-  s.tiles = (int)((cum[lo + 1] - cum[lo]) / ((long)row_blocks * kv_heads));
+  s.tiles = max((seq[lo].tokens + TOK - 1) / TOK, 1);
   const long r = p - cum[lo];
-  const int item = (int)(r / s.tiles);
+  const int item = (int)quotient(r, s.tiles);
   s.tile = (int)(r - (long)item * s.tiles);
   s.h = item / row_blocks;
   s.rb = item - s.h * row_blocks;
@@ -197,72 +223,143 @@ __device__ __forceinline__ Segment segment_at(const long *cum, int batch, int ro
   return s;
 }
 
+// Eight outputs of a row, bf16 or fp32.
+template <bool F32>
+__device__ __forceinline__ void store_out(char *dst, const float (&y)[8], float f) {
+  if (F32) {
+    reinterpret_cast<float4 *>(dst)[0] = make_float4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+    reinterpret_cast<float4 *>(dst)[1] = make_float4(y[4] * f, y[5] * f, y[6] * f, y[7] * f);
+  } else {
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f),
+                                                 pack_bf16x2(y[4] * f, y[5] * f), pack_bf16x2(y[6] * f, y[7] * f));
+  }
+}
+
+// Join the partial results of one item (rows of D values, then maximum and sum of each row) that blocks first..last left, in that
+// order, and write its outputs. All of `threads` threads take part.
+template <int D, int ROWS, bool F32>
+__device__ void join_parts(const AttendArgs &p, const float *parts, long stride, int first, int last, int b, int h, int row0, int fresh,
+                           int thread, int threads) {
+  constexpr int CH = D / 8;
+  const int G = p.c.group, rows = p.c.n_tokens * G;
+  for (int x = thread; x < ROWS * CH; x += threads) {
+    const int row = x / CH, e8 = (x % CH) * 8, rr = row0 + row, t = rr / G;
+    if (rr >= rows) continue;
+    float M = -INFINITY;
+    for (int i = first; i <= last; ++i) M = fmaxf(M, __ldcg(parts + (2 * i + (i == first)) * stride + ROWS * D + 2 * row));
+    float y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, L = 0.0f;
+#pragma unroll 4
+    for (int i = first; i <= last; ++i) {
+      const float *src = parts + (2 * i + (i == first)) * stride;
+      const float2 e = __ldcg(reinterpret_cast<const float2 *>(src + ROWS * D + 2 * row));
+      const float f = e.x == -INFINITY ? 0.0f : exp2_approx(e.x - M);
+      const float4 u = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8));
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8 + 4));
+      L += f * e.y;
+      y[0] += f * u.x, y[1] += f * u.y, y[2] += f * u.z, y[3] += f * u.w;
+      y[4] += f * v.x, y[5] += f * v.y, y[6] += f * v.z, y[7] += f * v.w;
+    }
+    char *dst = p.o.p + (b * p.o.sb + (long)t * p.o.st + (long)(h * G + rr - t * G) * p.o.sh + e8) * (F32 ? 4 : 2);
+    store_out<F32>(dst, y, t < fresh && L > 0.0f ? 1.0f / L : 0.0f);
+  }
+}
+
 template <int D, int BITS, int NT, int PARTS, int NW, int STAGES>
 struct AttendShape {
   using L = Tile<D, BITS>;
   static constexpr int ROWS = 8 * NT, THREADS = NW * 32;
   static constexpr int OROW = D + 4;                                    // padded scratch row
+  static constexpr int QROW = D * (PARTS > 1 ? 4 : 2);                  // bytes of a query row
   static constexpr size_t RING = (size_t)NW * STAGES * L::BYTES;
-  static constexpr size_t BARS = NW * STAGES * 8;
+  static constexpr size_t QRAW = (size_t)2 * ROWS * QROW;               // queries of this and the next segment
+  static constexpr size_t QF = (size_t)NT * L::NG * PARTS * 1024;       // queries as fragments
   static constexpr size_t SCRATCH = (size_t)NW * ROWS * OROW * 4;
   static constexpr size_t ML = (size_t)NW * ROWS * 2 * 4;
-  static constexpr size_t FIXED = RING + BARS + SCRATCH + ML + 64 * 8 + 16;
+  static constexpr size_t OQRAW = RING, OQF = OQRAW + QRAW, OSCR = OQF + QF, OML = OSCR + SCRATCH, OROWS = OML + ML,
+                          OBAR = OROWS + ROWS * 4, OSUM = OBAR + (NW * STAGES * 8 + 15) / 16 * 16, OCUM = OSUM + 64 * 8 + 16;
   // prefix sums of up to this many sequences: few capacities, so that the occupancy of each is asked for once
-  static constexpr int capacity(int batch) { return batch <= 128 ? 128 : PACE_KV_MAX_BATCH; }
-  static constexpr size_t smem(int batch) { return FIXED + (size_t)(capacity(batch) + 1) * 8; }
+  __host__ __device__ static constexpr int capacity(int batch) { return batch <= 128 ? 128 : PACE_KV_MAX_BATCH; }
+  static constexpr size_t smem(int batch) { return OCUM + (size_t)(capacity(batch) + 1) * 8 + (size_t)capacity(batch) * sizeof(Seq); }
 };
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(umma::smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
 
 template <int D, int BITS, int NT, int PARTS, int NW, int STAGES, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   using S = AttendShape<D, BITS, NT, PARTS, NW, STAGES>;
   using L = Tile<D, BITS>;
-  constexpr int NG = L::NG, ROWS = S::ROWS;
+  constexpr int NG = L::NG, ROWS = S::ROWS, ES = PARTS > 1 ? 4 : 2;
+  constexpr bool F32 = PARTS > 1;
   extern __shared__ __align__(128) char smem[];
-  char *ring_all = smem;
-  uint64_t *bars_all = reinterpret_cast<uint64_t *>(smem + S::RING);
-  float *scratch = reinterpret_cast<float *>(smem + S::RING + S::BARS);
-  float *ml = scratch + S::SCRATCH / 4;
-  long *wsum = reinterpret_cast<long *>(reinterpret_cast<char *>(ml) + S::ML);
-  long *cum = wsum + 64;
-  int *flag = reinterpret_cast<int *>(cum + p.c.batch + 1);
+  char *qraw = smem + S::OQRAW;
+  uint32_t *qf = reinterpret_cast<uint32_t *>(smem + S::OQF);
+  float *scratch = reinterpret_cast<float *>(smem + S::OSCR);
+  float *ml = reinterpret_cast<float *>(smem + S::OML);
+  float *rowmul = reinterpret_cast<float *>(smem + S::OROWS);     // what a row's scores are multiplied by
+  long *wsum = reinterpret_cast<long *>(smem + S::OSUM);
+  int *flag = reinterpret_cast<int *>(wsum + 64);
+  long *cum = reinterpret_cast<long *>(smem + S::OCUM);
+  Seq *seq = reinterpret_cast<Seq *>(cum + S::capacity(p.c.batch) + 1);
 
   const KvDev &c = p.c;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, j = lane >> 2, cc = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, j = lane >> 2, cc = lane & 3;
   const int G = c.group, T = c.n_tokens, words = (T + 31) >> 5;
-  char *ring = ring_all + (size_t)w * STAGES * L::BYTES;
-  uint64_t *bars = bars_all + w * STAGES;
+  char *ring = smem + (size_t)w * STAGES * L::BYTES;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::OBAR) + w * STAGES;
   if (lane < STAGES) umma::mbar_init(&bars[lane], 1);
   umma::mbar_fence_init();
   pdl_enter();
-  tile_line(c, (long)p.row_blocks * c.Hkv, cum, wsum);
+  tile_line<TILE>(c, (long)p.row_blocks * c.Hkv, seq, cum, wsum);
 
+  // equal shares, but no cut finer than a tile for every warp or a whole average item
   const long total = cum[c.batch];
-  const long even = (total + gridDim.x - 1) / gridDim.x;
-  const long share = even > p.min_share ? even : p.min_share;
+  long share = quotient(total + gridDim.x - 1, gridDim.x);
+  {
+    const long mean = quotient(total, (long)c.batch * c.Hkv * p.row_blocks), least = mean < NW ? mean : NW;
+    if (share < least) share = least;
+  }
   const long lo = (long)blockIdx.x * share, hi = min(total, lo + share);
   if (lo >= total) return;
+  auto segment = [&](long at) { return segment_at<TILE>(seq, cum, c.batch, p.row_blocks, at, hi); };
+
+  // ---- queries of a segment, copied one segment ahead
+  auto copy_queries = [&](const Segment &s, int buf) {
+    constexpr int CH = S::QROW / 16;
+    for (int x = tid; x < ROWS * CH; x += S::THREADS) {
+      const int row = x / CH, ch = x % CH, rr = s.rb * ROWS + row, t = rr / G;
+      const bool in = rr < T * G;
+      const char *src = in ? p.q.p + (s.b * p.q.sb + (long)t * p.q.st + (long)(s.h * G + rr - t * G) * p.q.sh) * ES + ch * 16 : p.q.p;
+      cp_async16(qraw + buf * ROWS * S::QROW + row * S::QROW + ch * 16, src, in);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  Segment sg = segment(lo);
+  copy_queries(sg, 0);
 
   // ---- the warp's fetch side: its tiles of all segments of the block, STAGES ahead
-  long fpos = lo;                                     // line position of the fetch segment's end
-  Segment f{0, 0, 0, 0, 0, 0};
+  Segment f = sg;
+  long fpos = lo + (sg.end - sg.tile);                // line position of the fetch segment's end
   const int tpp = c.page / TILE;                      // tiles a page
-  int ftile = 0, fbatch = 0, fstage = 0, mytile = -1;
+  int ftile = sg.tile + w, fbatch = 32, fstage = 0, mytile = -1;
   uint32_t bad = 0;                                   // stages whose page was bad (their tile is masked)
   bool dead = false;
   uint32_t phase = 0;                                 // parity per stage
   bool fdone = false;
+  int issued = 0, used = 0;
   auto fetch = [&]() {
-    while (!fdone && ftile >= f.end) {
+    while (ftile >= f.end) {
       if (fpos >= hi) {
         fdone = true;
-        break;
+        return;
       }
-      f = segment_at(cum, c.batch, p.row_blocks, c.Hkv, fpos, hi);
+      f = segment(fpos);
       fpos += f.end - f.tile;
       ftile = f.tile + w;
       fbatch = 32;
     }
-    if (fdone || dead) return;
+    if (dead) return;
     if (fbatch == 32) {                               // the warp's next 32 tiles of this segment, one a lane
       const int t = ftile + NW * lane;
       mytile = t < f.end ? tile_index(c, f.b, f.h, t, tpp) : 0;
@@ -270,93 +367,80 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       fbatch = 0;
     }
     const int at = __shfl_sync(0xffffffffu, mytile, fbatch);
-    if (at < 0) {
-      bad |= 1u << fstage;
-      if (lane == 0) umma::mbar_arrive(&bars[fstage]);
-    } else {
-      bad &= ~(1u << fstage);
-      if (lane == 0) {
+    bad = at < 0 ? bad | (1u << fstage) : bad & ~(1u << fstage);
+    if (lane == 0) {
+      if (at < 0) {
+        umma::mbar_arrive(&bars[fstage]);
+      } else {
         umma::mbar_arrive_expect_tx(&bars[fstage], L::BYTES);
         umma::bulk_g2s(ring + fstage * L::BYTES, c.pool + (long)at * L::BYTES, L::BYTES, &bars[fstage]);
       }
     }
+    ++issued;
     ftile += NW;
     ++fbatch;
     fstage = fstage + 1 == STAGES ? 0 : fstage + 1;
   };
-  int issued = 0, used = 0;
-  auto fetch_one = [&]() {
-    fetch();
-    if (!fdone && !dead) ++issued;
-  };
   __syncwarp();
 #pragma unroll 1
-  for (int i = 0; i < STAGES - 1; ++i) fetch_one();
+  for (int i = 0; i < STAGES - 1; ++i) fetch();
 
-  int stage = 0;
+  const uint32_t magic = opaque(0x64006400u);
+  int stage = 0, qbuf = 0;
+  // items this block shares with others: the one it began with and the one it ends with
+  int pseg = 0;
 #pragma unroll 1
-  for (long pos = lo; pos < hi;) {
-    const Segment sg = segment_at(cum, c.batch, p.row_blocks, c.Hkv, pos, hi);
+  for (long pos = lo; pos < hi; qbuf ^= 1) {
     pos += sg.end - sg.tile;
-    const int len = max(c.lens[sg.b], 0), nn = new_tokens(c, sg.b);
-    bool over_;
-    const int tokens = seq_tokens(c, sg.b, over_);
+    const Seq sq = seq[sg.b];
+    const int len = sq.len, nn = sq.fresh, tokens = sq.tokens;
     const int row0 = sg.rb * ROWS;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();                                  // this segment's queries are here; the last one's areas are free
+    if (pos < hi) copy_queries(segment(pos), qbuf ^ 1);
 
-    // ---- queries as B fragments: lane (j, cc) holds dims 64g + 16cc .. + 15 of row j of each block of eight
-    uint32_t qf[NT][NG][PARTS][8];
-    float crow[NT][2];                                // what a score of rows 2cc, 2cc+1 is multiplied by
+    // ---- queries as B fragments: lane (j, cc) takes dims 64g + 16cc .. + 15 of row j of each block of eight. bf16: as fp16 over a
+    // power of two that puts the row's largest element in [1, 2), exact but below 2^-14 of it. fp32: as three bf16 parts.
+    {
+      constexpr int TPR = S::THREADS / ROWS, PAIRS = D / TPR / 2;
+      const int row = tid / TPR, e0 = (tid % TPR) * 2 * PAIRS;
+      const char *src = qraw + qbuf * ROWS * S::QROW + row * S::QROW + e0 * ES;
+      const bool neg = p.scale_log2 < 0.0f;
+      float mul = fabsf(p.scale_log2);
+      auto put = [&](int i, int part, uint32_t v) {
+        const int e = e0 + 2 * i, g = e >> 6, k = (e & 15) >> 1, ln = (row & 7) * 4 + ((e & 63) >> 4);
+        qf[((((row >> 3) * NG + g) * PARTS + part) * 2 + (k >> 2)) * 128 + ln * 4 + (k & 3)] = v;
+      };
+      if (!F32) {
+        uint32_t x[PAIRS], top = 0;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int row = row0 + 8 * n + j, t = row / G, hh = sg.h * G + row - t * G;
-      const bool in = row < T * G;
-      const long at = sg.b * p.q.sb + (long)t * p.q.st + (long)hh * p.q.sh + 16 * cc;
+        for (int i = 0; i < PAIRS; ++i) {
+          x[i] = reinterpret_cast<const uint32_t *>(src)[i];
+          top = max(top, max((x[i] << 16) & 0x7FFF0000u, x[i] & 0x7FFF0000u));
+        }
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        if (PARTS == 1) {
-          uint4 x = make_uint4(0, 0, 0, 0), y = x;
-          if (in) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.q.p + (at + 64 * g) * 2);
-            x = src[0];
-            y = src[1];
-          }
-          const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        for (int o = 1; o < TPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int e = max(min((int)(top >> 23) - 127, 126), -126);
+        const float down = neg ? -exp2i(-e) : exp2i(-e);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) qf[n][g][0][i] = v[i];
-        } else {
+        for (int i = 0; i < PAIRS; ++i) put(i, 0, h2pack(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xFFFF0000u) * down));
+        mul *= exp2i(e);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float4 x = make_float4(0, 0, 0, 0);
-            if (in) x = reinterpret_cast<const float4 *>(p.q.p + (at + 64 * g) * 4)[i];
-            uint32_t a[PARTS], b[PARTS];
-            split_pair<PARTS>(x.x, x.y, a);
-            split_pair<PARTS>(x.z, x.w, b);
+        for (int i = 0; i < PAIRS; ++i) {
+          const float2 x = reinterpret_cast<const float2 *>(src)[i];
+          uint32_t a[PARTS];
+          split_pair<PARTS>(neg ? -x.x : x.x, neg ? -x.y : x.y, a);
 #pragma unroll
-            for (int e = 0; e < PARTS; ++e) qf[n][g][e][2 * i] = a[e], qf[n][g][e][2 * i + 1] = b[e];
-          }
+          for (int e = 0; e < PARTS; ++e) put(i, e, a[e]);
         }
       }
-      crow[n][0] = crow[n][1] = p.scale_log2;
-      if (PARTS == 1) {
-        // bf16 -> fp16 over a power of two that puts the row's largest element in [1, 2): exact but below 2^-14 of it
-        uint32_t top = 0;
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) top = max(top, max((qf[n][g][0][i] << 16) & 0x7FFF0000u, qf[n][g][0][i] & 0x7FFF0000u));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max(min((int)(top >> 23) - 127, 126), -126);
-        const float down = exp2i(-e);
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            qf[n][g][0][i] = h2pack(__uint_as_float(qf[n][g][0][i] << 16) * down, __uint_as_float(qf[n][g][0][i] & 0xFFFF0000u) * down);
-        crow[n][0] = p.scale_log2 * exp2i(__shfl_sync(0xffffffffu, e, 8 * cc));
-        crow[n][1] = p.scale_log2 * exp2i(__shfl_sync(0xffffffffu, e, 8 * cc + 4));
-      }
+      if (tid % TPR == 0) rowmul[row] = fmaxf(mul, FLT_MIN);          // (not 0: a masked score is -inf)
     }
+    __syncthreads();
+    float crow[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) crow[n][0] = rowmul[8 * n + 2 * cc], crow[n][1] = rowmul[8 * n + 2 * cc + 1];
 
     float acc[NG][4][NT][4];
 #pragma unroll
@@ -373,7 +457,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 
 #pragma unroll 1
     for (int tile = sg.tile + w; tile < sg.end; tile += NW) {
-      fetch_one();
+      if (!fdone) fetch();
       if (!dead && !umma::mbar_wait(&bars[stage], (phase >> stage) & 1u, WAIT_LIMIT_NS)) {
         dead = true;
         if (lane == 0) atomicOr(c.status, PACE_KV_TIMEOUT);
@@ -383,101 +467,92 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       const char *st = ring + stage * L::BYTES;
       const bool lost = dead || ((bad >> stage) & 1u);
 
-      // ---- scores
+      // ---- scores, without the rows' factors
+      constexpr int GP = BITS == 4 && D > 64 ? 2 : 1;   // groups whose words share a chunk
+      constexpr int KW = BITS == 4 ? 2 : 4;             // words of a token's 16 dims
       float s[2][NT][4];
-      {
-        uint2 ksw[NG];
-        uint32_t kzw[NG];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          ksw[g] = *reinterpret_cast<const uint2 *>(st + L::KS + g * 64 + j * 8);
-          if (BITS == 4) kzw[g] = *reinterpret_cast<const uint32_t *>(st + L::KZ + g * 32 + j * 4);
-        }
+      for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
-          const int ta = 16 * blk + tau(j), tb = ta + 8;
-          uint32_t wa[NG][BITS == 4 ? 2 : 4], wb[NG][BITS == 4 ? 2 : 4];
-          if (BITS == 8) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(st + L::kchunk(ta, g * 4 + cc));
-              const uint4 y = *reinterpret_cast<const uint4 *>(st + L::kchunk(tb, g * 4 + cc));
-              wa[g][0] = x.x, wa[g][1] = x.y, wa[g][2 % (BITS == 4 ? 2 : 4)] = x.z, wa[g][3 % (BITS == 4 ? 2 : 4)] = x.w;
-              wb[g][0] = y.x, wb[g][1] = y.y, wb[g][2 % (BITS == 4 ? 2 : 4)] = y.z, wb[g][3 % (BITS == 4 ? 2 : 4)] = y.w;
-            }
-          } else if (D == 64) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(st + L::kchunk(ta, cc));
-            const uint2 y = *reinterpret_cast<const uint2 *>(st + L::kchunk(tb, cc));
-            wa[0][0] = x.x, wa[0][1] = x.y, wb[0][0] = y.x, wb[0][1] = y.y;
-          } else {
+          for (int e = 0; e < 4; ++e) s[blk][n][e] = 0.0f;
 #pragma unroll
-            for (int g = 0; g < NG; g += 2) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(st + L::kchunk(ta, (g >> 1) * 4 + cc));
-              const uint4 y = *reinterpret_cast<const uint4 *>(st + L::kchunk(tb, (g >> 1) * 4 + cc));
-              constexpr int g1 = NG > 1 ? 1 : 0;
-              wa[g][0] = x.x, wa[g][1] = x.y, wa[g + g1][0] = x.z, wa[g + g1][1] = x.w;
-              wb[g][0] = y.x, wb[g][1] = y.y, wb[g + g1][0] = y.z, wb[g + g1][1] = y.w;
+      for (int g0 = 0; g0 < NG; g0 += GP) {
+        uint32_t kw[2][2][GP * KW];
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const char *at = st + L::kchunk(16 * blk + 8 * half + tau(j), (g0 / GP) * 4 + cc);
+            if (GP * KW == 2) {
+              const uint2 x = *reinterpret_cast<const uint2 *>(at);
+              kw[blk][half][0] = x.x, kw[blk][half][1] = x.y;
+            } else {
+              const uint4 x = *reinterpret_cast<const uint4 *>(at);
+              kw[blk][half][0] = x.x, kw[blk][half][1] = x.y, kw[blk][half][2 % (GP * KW)] = x.z, kw[blk][half][3 % (GP * KW)] = x.w;
             }
           }
 #pragma unroll
+        for (int gi = 0; gi < GP; ++gi) {
+          const int g = g0 + gi;
+          uint32_t q[NT][PARTS][8];
+#pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[blk][n][e] = 0.0f;
+            for (int e = 0; e < PARTS; ++e) {
+              const uint4 *src = reinterpret_cast<const uint4 *>(qf + ((n * NG + g) * PARTS + e) * 256) + lane;
+              const uint4 x = src[0], y = src[32];
+              q[n][e][0] = x.x, q[n][e][1] = x.y, q[n][e][2] = x.z, q[n][e][3] = x.w;
+              q[n][e][4] = y.x, q[n][e][5] = y.y, q[n][e][6] = y.z, q[n][e][7] = y.w;
+            }
+          const uint2 ksw = *reinterpret_cast<const uint2 *>(st + L::KS + g * 64 + j * 8);
+          uint32_t kz = 0;
+          if (BITS == 4) kz = *reinterpret_cast<const uint32_t *>(st + L::KZ + g * 32 + j * 4);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
+          for (int blk = 0; blk < 2; ++blk) {
+            uint32_t fr[2][8];                           // the group's pairs of the two tokens
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t *x = kw[blk][half] + gi * KW;
+              uint32_t z = 0;                            // the pair 1024 + z or 128 + z
+              if (BITS == 4) z = __byte_perm(kz, F32 ? 0x43434343u : 0x64646464u, 0x4040 | (2 * blk + half) * 0x0101);
+              if (!F32) {
+                if (BITS == 4) {
+                  const uint32_t z64 = h2add(z, 0xE380E380u /* -960 */);
+                  uint32_t r[4];
+#pragma unroll
+                  for (int h = 0; h < KW; ++h) {
+                    codes4(x[h], z, z64, magic, r);
+                    fr[half][4 * (h % 2)] = r[0], fr[half][4 * (h % 2) + 1] = r[1], fr[half][4 * (h % 2) + 2] = r[2], fr[half][4 * (h % 2) + 3] = r[3];
+                  }
+                } else {
+#pragma unroll
+                  for (int h = 0; h < KW; ++h) codes8(x[h], fr[half][2 * h], fr[half][2 * h + 1]);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  if (BITS == 4) fr[half][k] = sub_bf16x2(pair4(x[(k >> 2) % KW], k & 3), z);
+                  else fr[half][k] = pair8((k & 1) ? x[(k >> 1) % KW] >> 8 : x[(k >> 1) % KW]);
+                }
+              }
+            }
             float d[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
-            uint32_t zka = 0, zkb = 0, z64a = 0, z64b = 0;
-            if (BITS == 4) {
-              const uint32_t hi = PARTS == 1 ? 0x64646464u : 0x43434343u;                     // 1024 + z or 128 + z
-              zka = __byte_perm(kzw[g], hi, 0x4040 | (2 * blk) | ((2 * blk) << 8));
-              zkb = __byte_perm(kzw[g], hi, 0x4040 | (2 * blk + 1) | ((2 * blk + 1) << 8));
-              if (PARTS == 1) z64a = h2add(zka, 0xE380E380u /* -960 */), z64b = h2add(zkb, 0xE380E380u);
-            }
-            uint32_t fa[8], fb[8];                      // the group's pairs of the two tokens
-            if (PARTS == 1) {
-              if (BITS == 4) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  uint32_t r[4];
-                  codes4(wa[g][h], zka, z64a, r);
-                  fa[4 * h] = r[0], fa[4 * h + 1] = r[1], fa[4 * h + 2] = r[2], fa[4 * h + 3] = r[3];
-                  codes4(wb[g][h], zkb, z64b, r);
-                  fb[4 * h] = r[0], fb[4 * h + 1] = r[1], fb[4 * h + 2] = r[2], fb[4 * h + 3] = r[3];
-                }
-              } else {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                  codes8(wa[g][h % (BITS == 4 ? 2 : 4)], fa[2 * h], fa[2 * h + 1]);
-                  codes8(wb[g][h % (BITS == 4 ? 2 : 4)], fb[2 * h], fb[2 * h + 1]);
-                }
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (BITS == 4) {
-                  const uint32_t x = wa[g][k >> 1], y = wb[g][k >> 1];
-                  fa[2 * k] = sub_bf16x2(pair4(x, 2 * (k & 1)), zka), fb[2 * k] = sub_bf16x2(pair4(y, 2 * (k & 1)), zkb);
-                  fa[2 * k + 1] = sub_bf16x2(pair4(x, 2 * (k & 1) + 1), zka), fb[2 * k + 1] = sub_bf16x2(pair4(y, 2 * (k & 1) + 1), zkb);
-                } else {
-                  const uint32_t x = wa[g][k % (BITS == 4 ? 2 : 4)], y = wb[g][k % (BITS == 4 ? 2 : 4)];
-                  fa[2 * k] = pair8(x), fb[2 * k] = pair8(y), fa[2 * k + 1] = pair8(x >> 8), fb[2 * k + 1] = pair8(y >> 8);
-                }
-              }
-            }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < PARTS; ++e) {
-                  if (PARTS == 1) mma_f16(d[n], fa[2 * k], fb[2 * k], fa[2 * k + 1], fb[2 * k + 1], qf[n][g][e][2 * k], qf[n][g][e][2 * k + 1]);
-                  else mma_bf16(d[n], fa[2 * k], fb[2 * k], fa[2 * k + 1], fb[2 * k + 1], qf[n][g][e][2 * k], qf[n][g][e][2 * k + 1]);
+                  if (!F32) mma_f16(d[n], fr[0][2 * k], fr[1][2 * k], fr[0][2 * k + 1], fr[1][2 * k + 1], q[n][e][2 * k], q[n][e][2 * k + 1]);
+                  else mma_bf16(d[n], fr[0][2 * k], fr[1][2 * k], fr[0][2 * k + 1], fr[1][2 * k + 1], q[n][e][2 * k], q[n][e][2 * k + 1]);
                 }
-            const uint32_t sw = blk ? ksw[g].y : ksw[g].x;
+            const uint32_t sw = blk ? ksw.y : ksw.x;
             const float s0 = __uint_as_float(sw << 16), s1 = __uint_as_float(sw & 0xFFFF0000u);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -487,10 +562,6 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
               s[blk][n][3] = fmaf(s1, d[n][3], s[blk][n][3]);
             }
           }
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[blk][n][e] *= crow[n][e & 1];
         }
       }
       // ---- masks: only tiles that reach past the context (or were lost)
@@ -516,13 +587,13 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
           }
       }
       // ---- weights. bf16 I/O: the scale of a value group enters the exponent, w = 2^(s + log2 s_v - m + 6) with m the running
-      // maximum of s + log2 s_v, so that fp16 weights keep 11 bits whatever the scales; the sum takes 2^(s - m). fp32 I/O: the
+      // maximum of s + log2 s_v, so that fp16 weights keep 11 bits whatever the scales; the sum takes 2^(s - m + 6). fp32 I/O: the
       // scale multiplies the weight. m is raised only when a score passes it by 2^8 (fp16 weights up to 2^14, sums in fp32).
       float lv[NG][2][2], lm[2][2];                      // log2 of the value scales of the lane's tokens, their largest
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) lm[blk][half] = PARTS == 1 ? -60.0f : 0.0f;
+        for (int half = 0; half < 2; ++half) lm[blk][half] = !F32 ? -60.0f : 0.0f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const uint2 vsw = *reinterpret_cast<const uint2 *>(st + L::VS + g * 64 + j * 8);
@@ -533,8 +604,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
           for (int half = 0; half < 2; ++half) {
             float x = __uint_as_float(half ? sw & 0xFFFF0000u : sw << 16);
             if (edge && (tok0 + 16 * blk + 8 * half + tau(j) >= tokens || lost)) x = 0.0f;   // never written: may hold anything
-            lv[g][blk][half] = PARTS == 1 ? log2_approx(x) : x;
-            if (PARTS == 1) lm[blk][half] = fmaxf(lm[blk][half], lv[g][blk][half]);
+            lv[g][blk][half] = !F32 ? log2_approx(x) : x;
+            if (!F32) lm[blk][half] = fmaxf(lm[blk][half], lv[g][blk][half]);
           }
         }
       }
@@ -544,7 +615,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          mx[n][r] = fmaxf(fmaxf(s[0][n][r] + lm[0][0], s[0][n][2 + r] + lm[0][1]), fmaxf(s[1][n][r] + lm[1][0], s[1][n][2 + r] + lm[1][1]));
+          mx[n][r] = fmaxf(fmaxf(fmaf(s[0][n][r], crow[n][r], lm[0][0]), fmaf(s[0][n][2 + r], crow[n][r], lm[0][1])),
+                           fmaxf(fmaf(s[1][n][r], crow[n][r], lm[1][0]), fmaf(s[1][n][2 + r], crow[n][r], lm[1][1])));
           grow |= mx[n][r] > m[n][r] + 8.0f;
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -569,20 +641,19 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float mu = m[n][r] == -INFINITY ? 0.0f : m[n][r];
+          const float add = m[n][r] == -INFINITY ? 0.0f : 6.0f - m[n][r];
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               float &x = s[blk][n][2 * half + r];
-              x -= mu;
+              x = fmaf(x, crow[n][r], add);
               const float pr = exp2_approx(x);
               l[n][r] += pr;
-              x = PARTS == 1 ? x + 6.0f : pr;
+              if (F32) x = pr;
             }
         }
       // ---- output
-      constexpr int GP = BITS == 4 && D > 64 ? 2 : 1;   // groups whose words share a unit
 #pragma unroll
       for (int g0 = 0; g0 < NG; g0 += GP) {
 #pragma unroll
@@ -610,7 +681,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
             for (int n = 0; n < NT; ++n) {
               uint32_t x[PARTS], y[PARTS];
               const float v0s = lv[g][blk][0], v1s = lv[g][blk][1];
-              if (PARTS == 1) {
+              if (!F32) {
                 x[0] = h2pack(exp2_approx(s[blk][n][0] + v0s), exp2_approx(s[blk][n][1] + v0s));
                 y[0] = h2pack(exp2_approx(s[blk][n][2] + v1s), exp2_approx(s[blk][n][3] + v1s));
               } else {
@@ -625,19 +696,17 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
               const uint32_t x0 = gi ? v0.y : v0.x, x1 = gi ? v1.y : v1.x, x2 = gi ? v2.y : v2.x, x3 = gi ? v3.y : v3.x;
               const uint32_t w[4] = {__byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632), __byte_perm(x2, x3, 0x5410),
                                      __byte_perm(x2, x3, 0x7632)};
-              const uint2 vzw = *reinterpret_cast<const uint2 *>(st + L::VZ + g * 32 + cc * 8);
-              const int q0 = 2 * blk, q1 = 2 * blk + 1;
-              const uint32_t hi = PARTS == 1 ? 0x64006400u : 0x43004300u;                       // 1024 + z or 128 + z
-              const uint32_t z01 = (__byte_perm(vzw.x, vzw.y, q0 * 0x0011 + (4 + q0) * 0x1100) & 0x00FF00FFu) | hi;
-              const uint32_t z23 = (__byte_perm(vzw.x, vzw.y, q1 * 0x0011 + (4 + q1) * 0x1100) & 0x00FF00FFu) | hi;
-              if (PARTS == 1) {
+              const uint32_t vz = *reinterpret_cast<const uint32_t *>(st + L::VZ + g * 32 + cc * 8 + blk * 4);
+              const uint32_t hi = F32 ? 0x43434343u : 0x64646464u;                              // 1024 + z or 128 + z
+              const uint32_t z01 = __byte_perm(vz, hi, 0x4140), z23 = __byte_perm(vz, hi, 0x4342);
+              if (!F32) {
                 const uint32_t y01 = h2add(z01, 0xE380E380u), y23 = h2add(z23, 0xE380E380u);    // 64 + z
                 uint32_t r[4];
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {
-                  codes4(w[o], z01, y01, r);
+                  codes4(w[o], z01, y01, magic, r);
                   a01[o] = r[0], a01[2 + o] = r[1], a01[4 + o] = r[2], a01[6 + o] = r[3];
-                  codes4(w[2 + o], z23, y23, r);
+                  codes4(w[2 + o], z23, y23, magic, r);
                   a23[o] = r[0], a23[2 + o] = r[1], a23[4 + o] = r[2], a23[6 + o] = r[3];
                 }
               } else {
@@ -654,7 +723,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
                                        __byte_perm(x2, x3, 0x7632)};
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {
-                  if (PARTS == 1) {
+                  if (!F32) {
                     codes8(w[o], a01[4 * h2 + o], a01[4 * h2 + 2 + o]);
                     codes8(w[2 + o], a23[4 * h2 + o], a23[4 * h2 + 2 + o]);
                   } else {
@@ -670,7 +739,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < PARTS; ++e) {
-                  if (PARTS == 1) mma_f16(acc[g][i][n], a01[2 * i], a01[2 * i + 1], a23[2 * i], a23[2 * i + 1], bf[n][e][0], bf[n][e][1]);
+                  if (!F32) mma_f16(acc[g][i][n], a01[2 * i], a01[2 * i + 1], a23[2 * i], a23[2 * i + 1], bf[n][e][0], bf[n][e][1]);
                   else mma_bf16(acc[g][i][n], a01[2 * i], a01[2 * i + 1], a23[2 * i], a23[2 * i + 1], bf[n][e][0], bf[n][e][1]);
                 }
           }
@@ -680,7 +749,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       __syncwarp();                                   // every lane is done with the stage before it is filled again
     }
 
-    // ---- join the warps
+    // ---- join the warps (their areas were free from the segment's first barrier on)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -701,12 +770,12 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       }
     __syncthreads();
     const bool whole = sg.tile == 0 && sg.end == sg.tiles;
-    const long item_lo = pos - (sg.end - sg.tile) - sg.tile;          // line position of the item's first tile
-    const int first = (int)(item_lo / share), last = (int)((item_lo + sg.tiles - 1) / share);
-    const int PF = part_floats(D, NT);
+    const long item_lo = pos - sg.end;                                 // line position of the item's first tile
+    const int first = whole ? blockIdx.x : (int)quotient(item_lo, share);
+    constexpr int PF = part_floats(D, NT);
     float *mine = c.part + (long)(2 * blockIdx.x + (blockIdx.x == first ? 1 : 0)) * PF;
     constexpr int CH = D / 8;                                          // 8-element pieces of a row
-    for (int x = threadIdx.x; x < ROWS * CH; x += S::THREADS) {
+    for (int x = tid; x < ROWS * CH; x += S::THREADS) {
       const int row = x / CH, e8 = (x % CH) * 8;
       const int rr = row0 + row, t = rr / G;
       float M = -INFINITY;
@@ -716,9 +785,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
         const float mi = ml[(i * ROWS + row) * 2];
-        float f2 = mi == -INFINITY ? 0.0f : exp2_approx(mi - M);
+        const float f2 = mi == -INFINITY ? 0.0f : exp2_approx(mi - M);
         Ls += f2 * ml[(i * ROWS + row) * 2 + 1];
-        if (PARTS == 1) f2 *= 0x1p-6f;
         const float4 u = *reinterpret_cast<const float4 *>(scratch + (i * ROWS + row) * S::OROW + e8);
         const float4 v = *reinterpret_cast<const float4 *>(scratch + (i * ROWS + row) * S::OROW + e8 + 4);
         y[0] += f2 * u.x, y[1] += f2 * u.y, y[2] += f2 * u.z, y[3] += f2 * u.w;
@@ -726,71 +794,50 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       }
       if (whole) {
         if (rr >= T * G) continue;
-        const float inv = t < nn && Ls > 0.0f ? 1.0f / Ls : 0.0f;
-        char *dst = p.o.p + (sg.b * p.o.sb + (long)t * p.o.st + (long)(sg.h * G + rr - t * G) * p.o.sh + e8) * (PARTS > 1 ? 4 : 2);
-        if (PARTS > 1) {
-          reinterpret_cast<float4 *>(dst)[0] = make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-          reinterpret_cast<float4 *>(dst)[1] = make_float4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
-        } else {
-          *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv),
-                                                       pack_bf16x2(y[4] * inv, y[5] * inv), pack_bf16x2(y[6] * inv, y[7] * inv));
-        }
+        store_out<F32>(p.o.p + (sg.b * p.o.sb + (long)t * p.o.st + (long)(sg.h * G + rr - t * G) * p.o.sh + e8) * ES, y,
+                       t < nn && Ls > 0.0f ? 1.0f / Ls : 0.0f);
       } else {
         float *dst = mine + row * D + e8;
         *reinterpret_cast<float4 *>(dst) = make_float4(y[0], y[1], y[2], y[3]);
         *reinterpret_cast<float4 *>(dst + 4) = make_float4(y[4], y[5], y[6], y[7]);
-        if (e8 == 0) {
-          mine[ROWS * D + 2 * row] = M;
-          mine[ROWS * D + 2 * row + 1] = Ls;
-        }
+        if (e8 == 0) *reinterpret_cast<float2 *>(mine + ROWS * D + 2 * row) = make_float2(M, Ls);
       }
     }
-    // ---- an item that several blocks share: the last to arrive joins the parts in block order
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        const int before = atomicAdd(&c.count[first], 1);
-        *flag = before == last - first;
-        if (*flag) c.count[first] = 0;
+    if (!whole) pseg |= sg.tile ? 1 : 2;              // began in an earlier block, or goes on in a later one
+    if (pos < hi) sg = segment(pos);
+  }
+  // ---- items that several blocks share: the last to arrive joins the parts in block order
+  if (pseg) {
+    __threadfence();
+    __syncthreads();
+    // (of the two, the first holds the block's first tile, the second its last)
+    auto shared = [&](int k, Segment &it, int &first, int &last) {
+      const long at = k ? hi - 1 : lo;
+      it = segment(at);
+      first = (int)quotient(at - it.tile, share);
+      last = (int)quotient(at - it.tile + it.tiles - 1, share);
+    };
+    if (tid < 2) {
+      int joins = 0;
+      if ((pseg >> tid) & 1) {
+        Segment it;
+        int first, last;
+        shared(tid, it, first, last);
+        joins = atomicAdd(&c.count[first], 1) == last - first;
+        if (joins) c.count[first] = 0;
       }
-      __syncthreads();
-      if (*flag) {
+      flag[tid] = joins;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k)
+      if (flag[k]) {
         __threadfence();
-        for (int x = threadIdx.x; x < ROWS * CH; x += S::THREADS) {
-          const int row = x / CH, e8 = (x % CH) * 8;
-          const int rr = row0 + row, t = rr / G;
-          if (rr >= T * G) continue;
-          float M = -INFINITY;
-          for (int i = first; i <= last; ++i) {
-            const float *src = c.part + (long)(2 * i + (i == first ? 1 : 0)) * PF;
-            M = fmaxf(M, __ldcg(src + ROWS * D + 2 * row));
-          }
-          float y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, Ls = 0.0f;
-#pragma unroll 4
-          for (int i = first; i <= last; ++i) {
-            const float *src = c.part + (long)(2 * i + (i == first ? 1 : 0)) * PF;
-            const float2 e = __ldcg(reinterpret_cast<const float2 *>(src + ROWS * D + 2 * row));
-            const float f2 = e.x == -INFINITY ? 0.0f : exp2_approx(e.x - M);
-            Ls += f2 * e.y;
-            const float4 u = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8));
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8 + 4));
-            y[0] += f2 * u.x, y[1] += f2 * u.y, y[2] += f2 * u.z, y[3] += f2 * u.w;
-            y[4] += f2 * v.x, y[5] += f2 * v.y, y[6] += f2 * v.z, y[7] += f2 * v.w;
-          }
-          const float inv = t < nn && Ls > 0.0f ? 1.0f / Ls : 0.0f;
-          char *dst = p.o.p + (sg.b * p.o.sb + (long)t * p.o.st + (long)(sg.h * G + rr - t * G) * p.o.sh + e8) * (PARTS > 1 ? 4 : 2);
-          if (PARTS > 1) {
-            reinterpret_cast<float4 *>(dst)[0] = make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-            reinterpret_cast<float4 *>(dst)[1] = make_float4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
-          } else {
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv),
-                                                         pack_bf16x2(y[4] * inv, y[5] * inv), pack_bf16x2(y[6] * inv, y[7] * inv));
-          }
-        }
+        Segment it;
+        int first, last;
+        shared(k, it, first, last);
+        join_parts<D, ROWS, F32>(p, c.part, part_floats(D, NT), first, last, it.b, it.h, it.rb * ROWS, seq[it.b].fresh, tid, S::THREADS);
       }
-    }
-    __syncthreads();                                  // scratch is free for the next segment
   }
   if (dead) {                                         // a wait gave up: let the copies in flight land (bounded) before leaving
     for (; used < issued; ++used) {

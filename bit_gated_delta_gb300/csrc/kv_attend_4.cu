@@ -13,7 +13,7 @@ cudaError_t attend_4(const AttendArgs &a, int rows, cudaStream_t s) {
   }
   if (a.c.d == 128) {
     if (f32) return launch_attend<128, 4, 1, 3, 4, 3, 2>(a, s);
-    if (rows <= 8) return launch_attend<128, 4, 1, 1, 4, 3, 3>(a, s);
+    if (rows <= 8) return launch_attend<128, 4, 1, 1, 4, 2, 4>(a, s);
     return launch_attend<128, 4, 2, 1, 4, 3, 2>(a, s);
   }
   if (f32) return launch_attend<256, 4, 1, 3, 4, 2, 1>(a, s);

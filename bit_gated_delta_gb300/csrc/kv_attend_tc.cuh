@@ -50,7 +50,7 @@ struct TcShape {
   static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 4 * NWG + 1;
   static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flag, red[4]
   static constexpr int OCUM = (OMISC + 64 + 15) / 16 * 16;
-  static constexpr size_t smem(int batch) { return OCUM + 64 * 8 + (size_t)(batch + 1) * 8; }
+  static constexpr size_t smem(int batch) { return OCUM + 64 * 8 + (size_t)(batch + 1) * 8 + (size_t)batch * sizeof(Seq); }
 };
 constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 128 + 2 (128 of 256 + 2 are fewer)
 
@@ -102,33 +102,6 @@ __device__ __forceinline__ uint64_t visible(const AttendArgs &p, int b, int t, i
   return ctx | (bits << c0);
 }
 
-__device__ __forceinline__ void tc_line(const KvDev &c, long per_seq, long *cum, long *warp_sums) {
-  // as tile_line, in tiles of KVT
-  const int n = c.batch, nt = blockDim.x, per = (n + nt - 1) / nt, b0 = threadIdx.x * per;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  long s = 0;
-  for (int i = 0; i < per && b0 + i < n; ++i) {
-    bool over;
-    const int tok = seq_tokens(c, b0 + i, over);
-    if (over) atomicOr(c.status, PACE_KV_BAD_PAGE);
-    s += max((tok + KVT - 1) / KVT, 1) * per_seq;
-    cum[b0 + i + 1] = s;
-  }
-  long x = s;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sums[w] = x;
-  __syncthreads();
-  long base = x - s;
-  for (int i = 0; i < w; ++i) base += warp_sums[i];
-  for (int i = 0; i < per && b0 + i < n; ++i) cum[b0 + i + 1] += base;
-  if (threadIdx.x == 0) cum[0] = 0;
-  __syncthreads();
-}
-
 template <int D, int BITS, int MODE>
 __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_kernel(AttendArgs p) {
   using S = TcShape<D, BITS, MODE>;
@@ -137,6 +110,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   constexpr int NG = L::NG, NWG = S::NWG, KS = S::KS, VS = S::VS, RS = S::RS;
   constexpr uint64_t LIMIT = WAIT_LIMIT_NS;
   extern __shared__ __align__(128) char smem[];
+  const KvDev &c = p.c;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::OBAR);
   uint64_t *raw_full = bar, *raw_free = raw_full + RS, *k_full = raw_free + RS, *k_free = k_full + KS, *v_full = k_free + KS,
            *v_free = v_full + VS, *s_full = v_free + VS, *p_ready = s_full + NWG, *o_full = p_ready + NWG,
@@ -147,8 +121,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   float *red = reinterpret_cast<float *>(raw_flags + 8);                // [4]
   long *wsum = reinterpret_cast<long *>(smem + S::OCUM);
   long *cum = wsum + 64;
+  Seq *seq = reinterpret_cast<Seq *>(cum + c.batch + 1);
   int8_t *exps = reinterpret_cast<int8_t *>(smem + S::OEXP);
-  const KvDev &c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = c.group, T = c.n_tokens;
 
@@ -169,15 +143,15 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   }
   pdl_enter();
   fence_before_sync();
-  tc_line(c, (long)p.row_blocks * c.Hkv, cum, wsum);      // (its barriers also publish the set-up above)
+  tile_line<KVT>(c, (long)p.row_blocks * c.Hkv, seq, cum, wsum);      // (its barriers also publish the set-up above)
   fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
   const long total = cum[c.batch];
-  long share = (total + gridDim.x - 1) / gridDim.x;
+  long share = quotient(total + gridDim.x - 1, gridDim.x);
   if (share < p.min_share) share = p.min_share;
   const long lo = min((long)blockIdx.x * share, total), hi = min(total, lo + share);
-  auto at = [&](long pos) { return segment_at(cum, c.batch, p.row_blocks, c.Hkv, pos, hi); };
+  auto at = [&](long pos) { return segment_at<KVT>(seq, cum, c.batch, p.row_blocks, pos, hi); };
   // A role whose wait gives up goes on without waiting or touching the tensor cores, but keeps the barriers it shares, so that no
   // other warp is left at one; the others' waits then run out too.
   auto gave_up = [&]() { atomicOr(c.status, PACE_KV_TIMEOUT); };
@@ -190,8 +164,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     for (long pos = lo; pos < hi && good;) {
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
-      bool over;
-      const int tokens = seq_tokens(c, sg.b, over);
+      const int tokens = seq[sg.b].tokens;
       const int last = 2 * sg.end;
       for (int s0 = 2 * sg.tile; s0 < last && good; s0 += 32) {         // 32 storage tiles, one a lane
         const int mytile = (s0 + lane) < last && (s0 + lane) * TILE < tokens ? tile_index(c, sg.b, sg.h, s0 + lane, tpp) : -2;
@@ -227,8 +200,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     for (long pos = lo; pos < hi;) {
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
-      bool over;
-      const int tokens = seq_tokens(c, sg.b, over), len = max(c.lens[sg.b], 0);
+      const int tokens = seq[sg.b].tokens, len = seq[sg.b].len;
       for (int tile = sg.tile; tile < sg.end; ++tile, ++n) {
         const int rs = n % RS;
         good = good && mbar_wait(&raw_full[rs], (n / RS) & 1, LIMIT);
@@ -261,7 +233,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             const float sc = s[g] * down;
             uint4 v = make_uint4(h2pack(sc, sc), 0, 0, 0);
             if (BITS == 4) {
-              const int z = reinterpret_cast<const uint8_t *>(st + (part ? L::VZ : L::KZ))[g * TILE + ps];
+              const int z = reinterpret_cast<const uint8_t *>(st + (part ? L::VZ : L::KZ))[g * TILE + (part ? L::vpos(tt) : ps)];
               v.y = h2pack(-(1024.0f + z), -(1024.0f + z));
               v.z = h2pack(-(64.0f + z), -(64.0f + z));
             }
@@ -421,7 +393,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
       const int tiles = sg.end - sg.tile;
-      const int len = max(c.lens[sg.b], 0), nn = new_tokens(c, sg.b);
+      const int len = seq[sg.b].len, nn = seq[sg.b].fresh;
       const int row = sg.rb * S::ROWS + (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
       const int t = row / G, hh = sg.h * G + row - t * G;
       const bool in = row < T * G;
@@ -565,7 +537,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       }
       const bool whole = sg.tile == 0 && sg.end == sg.tiles;
       const long item_lo = pos - tiles - sg.tile;
-      const int fb = (int)(item_lo / share), lb = (int)((item_lo + sg.tiles - 1) / share);
+      const int fb = (int)quotient(item_lo, share), lb = (int)quotient(item_lo + sg.tiles - 1, share);
       float *part = c.part + (long)(2 * blockIdx.x + (blockIdx.x == fb ? 1 : 0)) * TC_PART_FLOATS;
       const int prow = (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
       float f0 = 1.0f, f1 = 0.0f, M = m, Ls = l;
@@ -633,30 +605,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         bar_sync(2, NWG * 128);
         if (*join_flag) {
           __threadfence();
-          constexpr int CH = D / 8;
-          for (int x = tid; x < S::ROWS * CH; x += NWG * 128) {
-            const int r = x / CH, e8 = (x % CH) * 8, rr = sg.rb * S::ROWS + r, tt = rr / G;
-            if (rr >= T * G) continue;
-            float MM = -INFINITY;
-            for (int i = fb; i <= lb; ++i)
-              MM = fmaxf(MM, __ldcg(c.part + (long)(2 * i + (i == fb ? 1 : 0)) * TC_PART_FLOATS + S::ROWS * D + 2 * r));
-            float y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, LL = 0.0f;
-#pragma unroll 2
-            for (int i = fb; i <= lb; ++i) {
-              const float *src = c.part + (long)(2 * i + (i == fb ? 1 : 0)) * TC_PART_FLOATS;
-              const float2 e = __ldcg(reinterpret_cast<const float2 *>(src + S::ROWS * D + 2 * r));
-              const float f = e.x == -INFINITY ? 0.0f : exp2_approx(e.x - MM);
-              const float4 u = __ldcg(reinterpret_cast<const float4 *>(src + r * D + e8));
-              const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + r * D + e8 + 4));
-              LL += f * e.y;
-              y[0] += f * u.x, y[1] += f * u.y, y[2] += f * u.z, y[3] += f * u.w;
-              y[4] += f * v.x, y[5] += f * v.y, y[6] += f * v.z, y[7] += f * v.w;
-            }
-            const float inv = tt < nn && LL > 0.0f ? 1.0f / LL : 0.0f;
-            char *dst = p.o.p + (sg.b * p.o.sb + (long)tt * p.o.st + (long)(sg.h * G + rr - tt * G) * p.o.sh + e8) * 2;
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv),
-                                                         pack_bf16x2(y[4] * inv, y[5] * inv), pack_bf16x2(y[6] * inv, y[7] * inv));
-          }
+          join_parts<D, S::ROWS, false>(p, c.part, TC_PART_FLOATS, fb, lb, sg.b, sg.h, sg.rb * S::ROWS, nn, tid, NWG * 128);
         }
       }
       fence_before_sync();

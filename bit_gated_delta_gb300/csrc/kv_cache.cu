@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, Kv
     if ((a & 7) == 0) {
       const int o = (a >> 3) * TILE + L::pos(tt);
       reinterpret_cast<__nv_bfloat16 *>(tile + (key ? L::KS : L::VS))[o] = __float2bfloat16_rn(s);
-      if (BITS == 4) reinterpret_cast<uint8_t *>(tile + (key ? L::KZ : L::VZ))[o] = (uint8_t)z;
+      if (BITS == 4) tile[key ? L::KZ + o : L::VZ + (a >> 3) * TILE + L::vpos(tt)] = (char)z;
     }
   }
 }
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(THREADS) read_kernel(KvDev c, const int32_t *_
     else w[part][i % N] = *reinterpret_cast<const uint2 *>(at);
     const int p = (a >> 3) * TILE + L::pos(t);
     sc[part][i % N] = reinterpret_cast<const __nv_bfloat16 *>(tile + (part ? L::VS : L::KS))[p];
-    if (BITS == 4) z[part][i % N] = reinterpret_cast<const uint8_t *>(tile + (part ? L::VZ : L::KZ))[p];
+    if (BITS == 4) z[part][i % N] = (uint8_t)tile[part ? L::VZ + (a >> 3) * TILE + L::vpos(t) : L::KZ + p];
   }
 #pragma unroll
   for (int i = 0; i < 2 * N; ++i) {
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(KvDev c, int max_new, con
       if ((a & 7) == 0) {
         const int o = (a >> 3) * TILE + L::pos(t);
         scale[i][part][a >> 3] = reinterpret_cast<const uint16_t *>(tile + (part ? L::VS : L::KS))[o];
-        if (BITS == 4) zero[i][part][a >> 3] = reinterpret_cast<const uint8_t *>(tile + (part ? L::VZ : L::KZ))[o];
+        if (BITS == 4) zero[i][part][a >> 3] = (uint8_t)tile[part ? L::VZ + (a >> 3) * TILE + L::vpos(t) : L::KZ + o];
       }
     }
     __syncthreads();
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(KvDev c, int max_new, con
       if ((a & 7) == 0) {
         const int o = (a >> 3) * TILE + L::pos(t);
         reinterpret_cast<uint16_t *>(tile + (part ? L::VS : L::KS))[o] = scale[i][part][a >> 3];
-        if (BITS == 4) reinterpret_cast<uint8_t *>(tile + (part ? L::VZ : L::KZ))[o] = zero[i][part][a >> 3];
+        if (BITS == 4) tile[part ? L::VZ + (a >> 3) * TILE + L::vpos(t) : L::KZ + o] = (char)zero[i][part][a >> 3];
       }
     }
     __syncthreads();

@@ -38,7 +38,7 @@ constexpr int TILE = PACE_KV_TILE;
 constexpr int GROUP = PACE_KV_GROUP;
 
 // One 32-token tile of one head. Rows of D*BITS/8 bytes per token for K, then for V; scales bf16 [NG][32] and zero points
-// u8 [NG][32] in row order `pos` below. The orders inside a row are those of the attention kernel's fragments: every
+// u8 [NG][32] in row order (`pos`, `vpos`). The orders inside a row are those of the attention kernel's fragments: every
 // shared-memory read of a warp then covers all 32 banks once, straight from the bytes a bulk copy brought.
 //  * mma row r of a 16-token block holds token tau(r): tau(2m) = m, tau(2m+1) = 4 + (m^3) in each half of 8, so that the
 //    two rows of a value pair and neighbouring key rows differ in the token bits that pick the banks;
@@ -80,6 +80,8 @@ struct Tile {
     const int u = t & 7, r = u < 4 ? 2 * u : 2 * ((u - 4) ^ 3) + 1;
     return r * 4 + (t >> 4) * 2 + ((t >> 3) & 1);
   }
+  // place of a value's zero point: rows 2c and 2c+1, which share a register, side by side
+  __host__ __device__ static constexpr int vpos(int t) { return (pos(t) >> 3) * 8 + (pos(t) & 3) * 2 + ((pos(t) >> 2) & 1); }
 };
 
 // mma row r (0..7) of each half of a 16-token block -> token in that half
