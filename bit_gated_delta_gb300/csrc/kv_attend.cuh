@@ -20,6 +20,8 @@
 
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "kv_common.cuh"
 #include "umma.cuh"
 
@@ -147,7 +149,7 @@ struct AttendArgs {
   const uint32_t *mask;
   float scale_log2;     // softmax scale * log2(e)
   int row_blocks;       // items of one (sequence, KV head)
-  int min_share;        // fewest tiles a block takes
+  int min_share;        // fewest tiles a block takes (tensor-memory kernel)
 };
 
 // One stretch of an item on the line of tiles.
@@ -170,41 +172,49 @@ __device__ __forceinline__ Seq sequence(const KvDev &c, int b, bool report) {
   if (report && (n > cap || len < 0)) atomicOr(c.status, PACE_KV_BAD_PAGE);
   return q;
 }
-// 64-bit quotient of non-negative numbers, by the short division where both fit 32 bits.
-__device__ __forceinline__ long quotient(long a, long b) {
-  return ((a | b) >> 32) == 0 ? (long)((unsigned)a / (unsigned)b) : a / b;
-}
-
 // The sequences, and the exclusive prefix sums of their items' tiles of TOK tokens (at least one each), in shared memory:
-// seq[0..batch), cum[0..batch].
+// seq[0..batch), cum[0..batch]. (32 bits: the host keeps the line of one launch below 2^31 tiles.)
 template <int TOK>
-__device__ __forceinline__ void tile_line(const KvDev &c, long per_seq, Seq *seq, long *cum, long *warp_sums) {
+__device__ __forceinline__ void tile_line(const KvDev &c, unsigned per_seq, Seq *seq, unsigned *cum, unsigned *warp_sums) {
   const int n = c.batch, nt = blockDim.x, per = (n + nt - 1) / nt, b0 = threadIdx.x * per;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  long s = 0;
+  unsigned s = 0;
   for (int i = 0; i < per && b0 + i < n; ++i) {
     const Seq q = sequence(c, b0 + i, blockIdx.x == 0);
     seq[b0 + i] = q;
     s += max((q.tokens + TOK - 1) / TOK, 1) * per_seq;
     cum[b0 + i + 1] = s;
   }
-  long x = s;
+  if (threadIdx.x == 0) cum[0] = 0;
+  if (n <= 32 && per == 1) {                           // one warp holds them all
+    if (w == 0) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+      }
+      if (lane < n) cum[lane + 1] = s;
+    }
+    __syncthreads();
+    return;
+  }
+  unsigned x = s;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long y = __shfl_up_sync(0xffffffffu, x, o);
+    const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) warp_sums[w] = x;
   __syncthreads();
-  long base = x - s;
+  unsigned base = x - s;
   for (int i = 0; i < w; ++i) base += warp_sums[i];
   for (int i = 0; i < per && b0 + i < n; ++i) cum[b0 + i + 1] += base;
-  if (threadIdx.x == 0) cum[0] = 0;
   __syncthreads();
 }
 
+// The item that holds line position p, and its stretch from there up to hi.
 template <int TOK>
-__device__ __forceinline__ Segment segment_at(const Seq *seq, const long *cum, int batch, int row_blocks, long p, long hi) {
+__device__ __forceinline__ Segment segment_at(const Seq *seq, const unsigned *cum, int batch, int row_blocks, unsigned p, unsigned hi) {
   int lo = 0, up = batch;                  // last b with cum[b] <= p
   while (up - lo > 1) {
     const int mid = (lo + up) >> 1;
@@ -214,13 +224,41 @@ __device__ __forceinline__ Segment segment_at(const Seq *seq, const long *cum, i
   Segment s;
   s.b = lo;
   s.tiles = max((seq[lo].tokens + TOK - 1) / TOK, 1);
-  const long r = p - cum[lo];
-  const int item = (int)quotient(r, s.tiles);
-  s.tile = (int)(r - (long)item * s.tiles);
+  const unsigned r = p - cum[lo], item = r / (unsigned)s.tiles;
+  s.tile = (int)(r - item * s.tiles);
   s.h = item / row_blocks;
   s.rb = item - s.h * row_blocks;
-  s.end = (int)min((long)s.tiles, s.tile + (hi - p));
+  s.end = (int)min((unsigned)s.tiles, s.tile + (hi - p));
   return s;
+}
+// The stretches of a block from line position lo on, SEGS at most, into shared memory by one warp (a lane each): the one at lo, then
+// whole items until hi. Returns how many; segs[n].tile of the one after them is the line position where they end.
+constexpr int SEGS = 32;
+template <int TOK>
+__device__ __forceinline__ int list_segments(const Seq *seq, const unsigned *cum, int batch, int row_blocks, int kv_heads, unsigned lo,
+                                             unsigned hi, Segment *segs) {
+  const int lane = threadIdx.x & 31;
+  const Segment a = segment_at<TOK>(seq, cum, batch, row_blocks, lo, hi);
+  const unsigned per_b = (unsigned)row_blocks * kv_heads;
+  const unsigned item = (unsigned)a.h * row_blocks + a.rb + lane, db = item / per_b;
+  Segment s = a;
+  unsigned at = lo;
+  bool in = lane == 0;
+  if (lane > 0 && a.b + (int)db < batch) {
+    s.b = a.b + db;
+    s.tiles = max((seq[s.b].tokens + TOK - 1) / TOK, 1);
+    const unsigned k = item - db * per_b;
+    s.h = k / row_blocks;
+    s.rb = k - s.h * row_blocks;
+    s.tile = 0;
+    at = cum[s.b] + k * s.tiles;
+    in = at < hi;
+    s.end = in ? (int)min((unsigned)s.tiles, hi - at) : 0;
+  }
+  const int n = __popc(__ballot_sync(0xffffffffu, in));
+  if (in) segs[lane] = s;
+  if (lane == n - 1) segs[SEGS].tile = (int)(at + (s.end - s.tile));
+  return n;
 }
 
 // Eight outputs of a row, bf16 or fp32.
@@ -235,6 +273,16 @@ __device__ __forceinline__ void store_out(char *dst, const float (&y)[8], float 
   }
 }
 
+// One more block has left its part of an item: whether it was the last of n. The caller's barrier before and after make the parts of
+// all blocks visible to the block that joins them.
+__device__ __forceinline__ bool last_part(int32_t *count, int n) {
+  int before;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
+  if (before != n - 1) return false;
+  *count = 0;
+  return true;
+}
+
 // Join the partial results of one item (rows of D values, then maximum and sum of each row) that blocks first..last left, in that
 // order, and write its outputs. All of `threads` threads take part.
 template <int D, int ROWS, bool F32>
@@ -245,19 +293,34 @@ __device__ void join_parts(const AttendArgs &p, const float *parts, long stride,
   for (int x = thread; x < ROWS * CH; x += threads) {
     const int row = x / CH, e8 = (x % CH) * 8, rr = row0 + row, t = rr / G;
     if (rr >= rows) continue;
-    float M = -INFINITY;
-    for (int i = first; i <= last; ++i) M = fmaxf(M, __ldcg(parts + (2 * i + (i == first)) * stride + ROWS * D + 2 * row));
-    float y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, L = 0.0f;
-#pragma unroll 4
-    for (int i = first; i <= last; ++i) {
-      const float *src = parts + (2 * i + (i == first)) * stride;
-      const float2 e = __ldcg(reinterpret_cast<const float2 *>(src + ROWS * D + 2 * row));
-      const float f = e.x == -INFINITY ? 0.0f : exp2_approx(e.x - M);
-      const float4 u = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8));
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8 + 4));
-      L += f * e.y;
-      y[0] += f * u.x, y[1] += f * u.y, y[2] += f * u.z, y[3] += f * u.w;
-      y[4] += f * v.x, y[5] += f * v.y, y[6] += f * v.z, y[7] += f * v.w;
+    float M = -INFINITY, y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, L = 0.0f;
+    for (int i0 = first; i0 <= last; i0 += 4) {        // four parts at a time: their loads go out together
+      float2 e[4];
+      float4 u[4], v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = min(i0 + k, last);
+        const float *src = parts + (2 * i + (i == first)) * stride;
+        e[k] = __ldcg(reinterpret_cast<const float2 *>(src + ROWS * D + 2 * row));
+        u[k] = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8));
+        v[k] = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8 + 4));
+      }
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k <= last) top = fmaxf(top, e[k].x);
+      const float keep = M == -INFINITY ? 0.0f : exp2_approx(M - top);
+      M = top;
+      L *= keep;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] *= keep;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = i0 + k <= last && e[k].x != -INFINITY ? exp2_approx(e[k].x - M) : 0.0f;
+        L += f * e[k].y;
+        y[0] += f * u[k].x, y[1] += f * u[k].y, y[2] += f * u[k].z, y[3] += f * u[k].w;
+        y[4] += f * v[k].x, y[5] += f * v[k].y, y[6] += f * v[k].z, y[7] += f * v[k].w;
+      }
     }
     char *dst = p.o.p + (b * p.o.sb + (long)t * p.o.st + (long)(h * G + rr - t * G) * p.o.sh + e8) * (F32 ? 4 : 2);
     store_out<F32>(dst, y, t < fresh && L > 0.0f ? 1.0f / L : 0.0f);
@@ -276,10 +339,11 @@ struct AttendShape {
   static constexpr size_t SCRATCH = (size_t)NW * ROWS * OROW * 4;
   static constexpr size_t ML = (size_t)NW * ROWS * 2 * 4;
   static constexpr size_t OQRAW = RING, OQF = OQRAW + QRAW, OSCR = OQF + QF, OML = OSCR + SCRATCH, OROWS = OML + ML,
-                          OBAR = OROWS + ROWS * 4, OSUM = OBAR + (NW * STAGES * 8 + 15) / 16 * 16, OCUM = OSUM + 64 * 8 + 16;
+                          OBAR = OROWS + ROWS * 4, OSEG = OBAR + (NW * STAGES * 8 + 15) / 16 * 16,
+                          OSUM = OSEG + (SEGS + 1) * sizeof(Segment), OCUM = OSUM + 32 * 4 + 16;
   // prefix sums of up to this many sequences: few capacities, so that the occupancy of each is asked for once
   __host__ __device__ static constexpr int capacity(int batch) { return batch <= 128 ? 128 : PACE_KV_MAX_BATCH; }
-  static constexpr size_t smem(int batch) { return OCUM + (size_t)(capacity(batch) + 1) * 8 + (size_t)capacity(batch) * sizeof(Seq); }
+  static constexpr size_t smem(int batch) { return OCUM + (size_t)(capacity(batch) + 1) * 4 + (size_t)capacity(batch) * sizeof(Seq); }
 };
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in) {
@@ -298,9 +362,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   float *scratch = reinterpret_cast<float *>(smem + S::OSCR);
   float *ml = reinterpret_cast<float *>(smem + S::OML);
   float *rowmul = reinterpret_cast<float *>(smem + S::OROWS);     // what a row's scores are multiplied by
-  long *wsum = reinterpret_cast<long *>(smem + S::OSUM);
-  int *flag = reinterpret_cast<int *>(wsum + 64);
-  long *cum = reinterpret_cast<long *>(smem + S::OCUM);
+  Segment *segs = reinterpret_cast<Segment *>(smem + S::OSEG);
+  unsigned *wsum = reinterpret_cast<unsigned *>(smem + S::OSUM);
+  int *flag = reinterpret_cast<int *>(wsum + 32);
+  unsigned *cum = reinterpret_cast<unsigned *>(smem + S::OCUM);
   Seq *seq = reinterpret_cast<Seq *>(cum + S::capacity(p.c.batch) + 1);
 
   const KvDev &c = p.c;
@@ -311,18 +376,18 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   if (lane < STAGES) umma::mbar_init(&bars[lane], 1);
   umma::mbar_fence_init();
   pdl_enter();
-  tile_line<TILE>(c, (long)p.row_blocks * c.Hkv, seq, cum, wsum);
+  tile_line<TILE>(c, (unsigned)p.row_blocks * c.Hkv, seq, cum, wsum);
 
   // equal shares, but no cut finer than a tile for every warp or a whole average item
-  const long total = cum[c.batch];
-  long share = quotient(total + gridDim.x - 1, gridDim.x);
+  const unsigned total = cum[c.batch];
+  unsigned share = (total + gridDim.x - 1) / gridDim.x;
   {
-    const long mean = quotient(total, (long)c.batch * c.Hkv * p.row_blocks), least = mean < NW ? mean : NW;
-    if (share < least) share = least;
+    const unsigned mean = total / ((unsigned)c.batch * c.Hkv * p.row_blocks);
+    share = max(share, min(mean, (unsigned)NW));
   }
-  const long lo = (long)blockIdx.x * share, hi = min(total, lo + share);
-  if (lo >= total) return;
-  auto segment = [&](long at) { return segment_at<TILE>(seq, cum, c.batch, p.row_blocks, at, hi); };
+  const unsigned lo = blockIdx.x * share, hi = min(total, lo + share);
+  if (blockIdx.x > total / share || lo >= total) return;
+  auto segment = [&](unsigned at) { return segment_at<TILE>(seq, cum, c.batch, p.row_blocks, at, hi); };
 
   // ---- queries of a segment, copied one segment ahead
   auto copy_queries = [&](const Segment &s, int buf) {
@@ -335,38 +400,41 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  Segment sg = segment(lo);
-  copy_queries(sg, 0);
 
-  // ---- the warp's fetch side: its tiles of all segments of the block, STAGES ahead
-  Segment f = sg;
-  long fpos = lo + (sg.end - sg.tile);                // line position of the fetch segment's end
+  // ---- the warp's fetch side: its tiles of all segments of the round, STAGES ahead; the pages of its next 32 tiles (one a lane) are
+  // looked up one batch ahead
   const int tpp = c.page / TILE;                      // tiles a page
-  int ftile = sg.tile + w, fbatch = 32, fstage = 0, mytile = -1;
+  int nseg = 0;
+  int fleft = 0, fnext = 0, fstage = 0, mytile = -1;               // batch in use: tiles left, next one's lane
+  int nxseg = 0, nxtile = 0, nxpage = -1;                          // batch ahead: segment, first tile, the lane's page
   uint32_t bad = 0;                                   // stages whose page was bad (their tile is masked)
   bool dead = false;
   uint32_t phase = 0;                                 // parity per stage
-  bool fdone = false;
   int issued = 0, used = 0;
+  auto look_ahead = [&](int k, int t) {               // the batch at or after tile t of segment k
+    while (k < nseg && t >= segs[k].end) {
+      if (++k < nseg) t = segs[k].tile + w;
+    }
+    nxseg = k;
+    nxtile = t;
+    if (k < nseg) {
+      const int mine = t + NW * lane, col = mine / tpp, b = segs[k].b;
+      nxpage = mine < segs[k].end && mine * TILE < seq[b].tokens ? c.table[(long)b * c.table_cols + col] : -2;   // -2: no tokens
+    }
+  };
   auto fetch = [&]() {
-    while (ftile >= f.end) {
-      if (fpos >= hi) {
-        fdone = true;
-        return;
-      }
-      f = segment(fpos);
-      fpos += f.end - f.tile;
-      ftile = f.tile + w;
-      fbatch = 32;
-    }
     if (dead) return;
-    if (fbatch == 32) {                               // the warp's next 32 tiles of this segment, one a lane
-      const int t = ftile + NW * lane;
-      mytile = t < f.end ? tile_index(c, f.b, f.h, t, tpp) : 0;
-      if (mytile < 0) atomicOr(c.status, PACE_KV_BAD_PAGE);
-      fbatch = 0;
+    if (fleft == 0) {
+      if (nxseg >= nseg) return;
+      const int fseg = nxseg, ftile = nxtile, t = ftile + NW * lane;
+      fnext = 0;
+      fleft = min(32, (segs[fseg].end - ftile + NW - 1) / NW);
+      const bool ok = nxpage >= 0 && nxpage < c.n_pages;
+      if (!ok && nxpage != -2) atomicOr(c.status, PACE_KV_BAD_PAGE);
+      mytile = ok ? (nxpage * c.Hkv + segs[fseg].h) * tpp + t % tpp : -1;
+      look_ahead(fseg, ftile + 32 * NW);
     }
-    const int at = __shfl_sync(0xffffffffu, mytile, fbatch);
+    const int at = __shfl_sync(0xffffffffu, mytile, fnext);
     bad = at < 0 ? bad | (1u << fstage) : bad & ~(1u << fstage);
     if (lane == 0) {
       if (at < 0) {
@@ -377,27 +445,35 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       }
     }
     ++issued;
-    ftile += NW;
-    ++fbatch;
+    ++fnext;
+    --fleft;
     fstage = fstage + 1 == STAGES ? 0 : fstage + 1;
   };
-  __syncwarp();
-#pragma unroll 1
-  for (int i = 0; i < STAGES - 1; ++i) fetch();
-
   const uint32_t magic = opaque(0x64006400u);
   int stage = 0, qbuf = 0;
-  // items this block shares with others: the one it began with and the one it ends with
-  int pseg = 0;
+  int pseg = 0;                                       // items shared with other blocks: 1 the one it began with, 2 the one it ends with
 #pragma unroll 1
-  for (long pos = lo; pos < hi; qbuf ^= 1) {
-    pos += sg.end - sg.tile;
+  for (unsigned round = lo; round < hi;) {            // SEGS segments a round
+   if (w == 0) {
+     const int n = list_segments<TILE>(seq, cum, c.batch, p.row_blocks, c.Hkv, round, hi, segs);
+     if (lane == 0) segs[SEGS].end = n;
+   }
+   __syncthreads();
+   nseg = segs[SEGS].end;
+   round = (unsigned)segs[SEGS].tile;
+   look_ahead(0, segs[0].tile + w);
+   copy_queries(segs[0], qbuf);
+#pragma unroll 1
+   for (int i = 0; i < STAGES - 1; ++i) fetch();
+#pragma unroll 1
+   for (int k = 0; k < nseg; ++k, qbuf ^= 1) {
+    const Segment sg = segs[k];
     const Seq sq = seq[sg.b];
     const int len = sq.len, nn = sq.fresh, tokens = sq.tokens;
     const int row0 = sg.rb * ROWS;
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();                                  // this segment's queries are here; the last one's areas are free
-    if (pos < hi) copy_queries(segment(pos), qbuf ^ 1);
+    if (k + 1 < nseg) copy_queries(segs[k + 1], qbuf ^ 1);
 
     // ---- queries as B fragments: lane (j, cc) takes dims 64g + 16cc .. + 15 of row j of each block of eight. bf16: as fp16 over a
     // power of two that puts the row's largest element in [1, 2), exact but below 2^-14 of it. fp32: as three bf16 parts.
@@ -457,7 +533,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 
 #pragma unroll 1
     for (int tile = sg.tile + w; tile < sg.end; tile += NW) {
-      if (!fdone) fetch();
+      fetch();
       if (!dead && !umma::mbar_wait(&bars[stage], (phase >> stage) & 1u, WAIT_LIMIT_NS)) {
         dead = true;
         if (lane == 0) atomicOr(c.status, PACE_KV_TIMEOUT);
@@ -770,10 +846,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       }
     __syncthreads();
     const bool whole = sg.tile == 0 && sg.end == sg.tiles;
-    const long item_lo = pos - sg.end;                                 // line position of the item's first tile
-    const int first = whole ? blockIdx.x : (int)quotient(item_lo, share);
-    constexpr int PF = part_floats(D, NT);
-    float *mine = c.part + (long)(2 * blockIdx.x + (blockIdx.x == first ? 1 : 0)) * PF;
+    // (an item that is shared and starts in this block is the block's last)
+    float *mine = c.part + (long)(2 * blockIdx.x + (sg.tile == 0 ? 1 : 0)) * part_floats(D, NT);
     constexpr int CH = D / 8;                                          // 8-element pieces of a row
     for (int x = tid; x < ROWS * CH; x += S::THREADS) {
       const int row = x / CH, e8 = (x % CH) * 8;
@@ -803,28 +877,26 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
         if (e8 == 0) *reinterpret_cast<float2 *>(mine + ROWS * D + 2 * row) = make_float2(M, Ls);
       }
     }
-    if (!whole) pseg |= sg.tile ? 1 : 2;              // began in an earlier block, or goes on in a later one
-    if (pos < hi) sg = segment(pos);
+    if (!whole) pseg |= sg.tile ? 1 : 2;
+   }
+   __syncthreads();                                   // the list of segments and the areas are free
   }
   // ---- items that several blocks share: the last to arrive joins the parts in block order
   if (pseg) {
-    __threadfence();
-    __syncthreads();
-    // (of the two, the first holds the block's first tile, the second its last)
+    // (the first holds the block's first tile, the second its last)
     auto shared = [&](int k, Segment &it, int &first, int &last) {
-      const long at = k ? hi - 1 : lo;
+      const unsigned at = k ? hi - 1 : lo;
       it = segment(at);
-      first = (int)quotient(at - it.tile, share);
-      last = (int)quotient(at - it.tile + it.tiles - 1, share);
+      first = (int)((at - it.tile) / share);
+      last = (int)((at - it.tile + it.tiles - 1) / share);
     };
     if (tid < 2) {
-      int joins = 0;
+      bool joins = false;
       if ((pseg >> tid) & 1) {
         Segment it;
         int first, last;
         shared(tid, it, first, last);
-        joins = atomicAdd(&c.count[first], 1) == last - first;
-        if (joins) c.count[first] = 0;
+        joins = last_part(&c.count[first], last - first + 1);
       }
       flag[tid] = joins;
     }
@@ -832,7 +904,6 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 #pragma unroll 1
     for (int k = 0; k < 2; ++k)
       if (flag[k]) {
-        __threadfence();
         Segment it;
         int first, last;
         shared(k, it, first, last);
@@ -846,6 +917,28 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
   }
+}
+
+// Calls launch(args, tiles) for as many sequences at a time as keep the line of tiles of `tok` tokens, which is counted in 32 bits,
+// below 2^31 whatever their lengths (all of them, but for the largest products of batch, heads, new tokens and table).
+template <typename F>
+cudaError_t by_batches(const AttendArgs &a, int tok, F launch) {
+  const long per_seq = (long)a.c.Hkv * a.row_blocks * (((long)a.c.table_cols * a.c.page + tok - 1) / tok);
+  const long most = std::max(1L, ((1L << 31) - 1) / per_seq);
+  const int words = (a.c.n_tokens + 31) / 32, es = a.c.io == PACE_IO_F32 ? 4 : 2;
+  for (int b = 0; b < a.c.batch; b += (int)most) {
+    AttendArgs part = a;
+    part.c.batch = (int)std::min(most, (long)a.c.batch - b);
+    part.c.lens += b;
+    if (part.c.n_new) part.c.n_new += b;
+    part.c.table += (long)b * a.c.table_cols;
+    if (part.mask) part.mask += (long)b * a.c.n_tokens * words;
+    part.q.p += b * a.q.sb * es;
+    part.o.p += b * a.o.sb * es;
+    const cudaError_t e = launch(part, per_seq * part.c.batch);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 // resident_blocks of the capacity for large batches (its own cache entry)
@@ -870,18 +963,17 @@ cudaError_t launch_attend(AttendArgs a, cudaStream_t s) {
   cudaError_t e = smem_opt_in<K>(227 * 1024);
   if (e != cudaSuccess) return e;
   a.row_blocks = (a.c.n_tokens * a.c.group + S::ROWS - 1) / S::ROWS;
-  a.min_share = NW;
   static int (*const resident[2])(int, size_t) = {resident_blocks<K>, resident_blocks_large<K>};
   const int per_sm = resident[S::capacity(a.c.batch) > 128](S::THREADS, smem);
-  // no more blocks than the longest possible line of tiles has shares
-  const long line = (long)a.c.batch * a.c.Hkv * a.row_blocks * (((long)a.c.table_cols * a.c.page + TILE - 1) / TILE);
-  long grid = (long)per_sm * device_sm_count();
-  if (grid > MAX_BLOCKS) grid = MAX_BLOCKS;
-  const long shares = (line + a.min_share - 1) / a.min_share;
-  if (grid > shares) grid = shares;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)grid), dim3(S::THREADS), smem, s, attr);
-  return cudaLaunchKernelEx(&cfg, K, a);
+  return by_batches(a, TILE, [&](const AttendArgs &part, long line) {
+    // no more blocks than the longest possible line of tiles
+    long grid = (long)per_sm * device_sm_count();
+    if (grid > MAX_BLOCKS) grid = MAX_BLOCKS;
+    if (grid > line) grid = line;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)grid), dim3(S::THREADS), smem, s, attr);
+    return cudaLaunchKernelEx(&cfg, K, part);
+  });
 }
 
 }  // namespace kv

@@ -50,7 +50,7 @@ struct TcShape {
   static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 4 * NWG + 1;
   static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flag, red[4]
   static constexpr int OCUM = (OMISC + 64 + 15) / 16 * 16;
-  static constexpr size_t smem(int batch) { return OCUM + 64 * 8 + (size_t)(batch + 1) * 8 + (size_t)batch * sizeof(Seq); }
+  static constexpr size_t smem(int batch) { return OCUM + 32 * 4 + (size_t)(batch + 1) * 4 + (size_t)batch * sizeof(Seq); }
 };
 constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 128 + 2 (128 of 256 + 2 are fewer)
 
@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_flags + 4);
   int *join_flag = raw_flags + 5;
   float *red = reinterpret_cast<float *>(raw_flags + 8);                // [4]
-  long *wsum = reinterpret_cast<long *>(smem + S::OCUM);
-  long *cum = wsum + 64;
+  unsigned *wsum = reinterpret_cast<unsigned *>(smem + S::OCUM);
+  unsigned *cum = wsum + 32;
   Seq *seq = reinterpret_cast<Seq *>(cum + c.batch + 1);
   int8_t *exps = reinterpret_cast<int8_t *>(smem + S::OEXP);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -143,15 +143,14 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   }
   pdl_enter();
   fence_before_sync();
-  tile_line<KVT>(c, (long)p.row_blocks * c.Hkv, seq, cum, wsum);      // (its barriers also publish the set-up above)
+  tile_line<KVT>(c, (unsigned)p.row_blocks * c.Hkv, seq, cum, wsum);      // (its barriers also publish the set-up above)
   fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  const long total = cum[c.batch];
-  long share = quotient(total + gridDim.x - 1, gridDim.x);
-  if (share < p.min_share) share = p.min_share;
-  const long lo = min((long)blockIdx.x * share, total), hi = min(total, lo + share);
-  auto at = [&](long pos) { return segment_at<KVT>(seq, cum, c.batch, p.row_blocks, pos, hi); };
+  const unsigned total = cum[c.batch];
+  const unsigned share = max((total + gridDim.x - 1) / gridDim.x, (unsigned)p.min_share);
+  const unsigned lo = blockIdx.x <= total / share ? blockIdx.x * share : total, hi = min(total, lo + share);
+  auto at = [&](unsigned pos) { return segment_at<KVT>(seq, cum, c.batch, p.row_blocks, pos, hi); };
   // A role whose wait gives up goes on without waiting or touching the tensor cores, but keeps the barriers it shares, so that no
   // other warp is left at one; the others' waits then run out too.
   auto gave_up = [&]() { atomicOr(c.status, PACE_KV_TIMEOUT); };
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     const int tpp = c.page / TILE;
     int stage = 0, n = 0;
     bool good = true;
-    for (long pos = lo; pos < hi && good;) {
+    for (unsigned pos = lo; pos < hi && good;) {
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
       const int tokens = seq[sg.b].tokens;
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     const int dt = tid - S::W_DEQ * 32, dw = warp - S::W_DEQ;
     int n = 0;
     bool good = true;
-    for (long pos = lo; pos < hi;) {
+    for (unsigned pos = lo; pos < hi;) {
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
       const int tokens = seq[sg.b].tokens, len = seq[sg.b].len;
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       int nq = 0;
       int np[2] = {0, 0};                                 // tasks done per group
       constexpr uint32_t ID_S = idesc_f16(128, KVT, 0), ID_O = idesc_f16(128, D, 1);
-      for (long pos = lo; pos < hi && good;) {
+      for (unsigned pos = lo; pos < hi && good;) {
         const Segment sg = at(pos);
         pos += sg.end - sg.tile;
         const int tiles = sg.end - sg.tile;
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
     int ntile = 0, ns = 0, no = 0;
     bool good = true;
-    for (long pos = lo; pos < hi;) {
+    for (unsigned pos = lo; pos < hi;) {
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
       const int tiles = sg.end - sg.tile;
@@ -536,8 +535,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         fence_after_sync();
       }
       const bool whole = sg.tile == 0 && sg.end == sg.tiles;
-      const long item_lo = pos - tiles - sg.tile;
-      const int fb = (int)quotient(item_lo, share), lb = (int)quotient(item_lo + sg.tiles - 1, share);
+      const unsigned item_lo = pos - sg.end;
+      const int fb = (int)(item_lo / share), lb = (int)((item_lo + sg.tiles - 1) / share);
       float *part = c.part + (long)(2 * blockIdx.x + (blockIdx.x == fb ? 1 : 0)) * TC_PART_FLOATS;
       const int prow = (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
       float f0 = 1.0f, f1 = 0.0f, M = m, Ls = l;
@@ -595,16 +594,10 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         }
       }
       if (!whole) {
-        __threadfence();
         bar_sync(2, NWG * 128);
-        if (tid == 0) {
-          const int before = atomicAdd(&c.count[fb], 1);
-          *join_flag = before == lb - fb;
-          if (before == lb - fb) c.count[fb] = 0;
-        }
+        if (tid == 0) *join_flag = last_part(&c.count[fb], lb - fb + 1);
         bar_sync(2, NWG * 128);
         if (*join_flag) {
-          __threadfence();
           join_parts<D, S::ROWS, false>(p, c.part, TC_PART_FLOATS, fb, lb, sg.b, sg.h, sg.rb * S::ROWS, nn, tid, NWG * 128);
         }
       }
@@ -630,14 +623,13 @@ cudaError_t launch_attend_tc(AttendArgs a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   a.row_blocks = (a.c.n_tokens * a.c.group + S::ROWS - 1) / S::ROWS;
   a.min_share = 4;
-  long grid = device_sm_count();
-  if (grid > TC_BLOCKS) grid = TC_BLOCKS;
-  const long line = (long)a.c.batch * a.c.Hkv * a.row_blocks * (((long)a.c.table_cols * a.c.page + KVT - 1) / KVT);
-  const long shares = (line + a.min_share - 1) / a.min_share;
-  if (grid > shares) grid = shares;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)grid), dim3(S::THREADS), smem, s, attr);
-  return cudaLaunchKernelEx(&cfg, K, a);
+  return by_batches(a, KVT, [&](const AttendArgs &part, long line) {
+    long grid = std::min((long)device_sm_count(), (long)TC_BLOCKS);
+    grid = std::min(grid, (line + a.min_share - 1) / a.min_share);
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)grid), dim3(S::THREADS), smem, s, attr);
+    return cudaLaunchKernelEx(&cfg, K, part);
+  });
 }
 
 }  // namespace kv
