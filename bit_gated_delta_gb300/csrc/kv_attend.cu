@@ -5,8 +5,8 @@
 
 namespace pace {
 namespace kv {
-cudaError_t attend_4(const AttendArgs &a, int rows, cudaStream_t s);
-cudaError_t attend_8(const AttendArgs &a, int rows, cudaStream_t s);
+cudaError_t attend_4(const AttendArgs &a, int rows, bool few, cudaStream_t s);
+cudaError_t attend_8(const AttendArgs &a, int rows, bool few, cudaStream_t s);
 cudaError_t attend_tc_4(const AttendArgs &a, int rows, cudaStream_t s);
 cudaError_t attend_tc_8(const AttendArgs &a, int rows, cudaStream_t s);
 }  // namespace kv
@@ -17,6 +17,7 @@ using namespace pace::kv;
 namespace {
 // Rows of one KV head from which the tensor-memory kernel takes over (bf16 I/O).
 constexpr int TC_ROWS = 33;
+constexpr int FEW_ITEMS = 64;
 bool use_tc(int io, int rows) { return io == PACE_IO_BF16 && rows >= TC_ROWS; }
 }  // namespace
 
@@ -32,5 +33,6 @@ cudaError_t pace_launch_kv_attend(const KvDev &c, const KvTensor &q, const uint3
   AttendArgs a{c, q, o, mask, scale * 1.44269504088896340736f, 0, 0};
   const int rows = c.n_tokens * c.group;
   if (use_tc(c.io, rows)) return c.bits == 4 ? attend_tc_4(a, rows, s) : attend_tc_8(a, rows, s);
-  return c.bits == 4 ? attend_4(a, rows, s) : attend_8(a, rows, s);
+  const bool few = (long)c.batch * c.Hkv <= FEW_ITEMS;
+  return c.bits == 4 ? attend_4(a, rows, few, s) : attend_8(a, rows, few, s);
 }

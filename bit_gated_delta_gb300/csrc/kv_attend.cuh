@@ -41,6 +41,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {   // d = A B
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -283,23 +290,53 @@ __device__ __forceinline__ bool last_part(int32_t *count, int n) {
   return true;
 }
 
-// Join the partial results of one item (rows of D values, then maximum and sum of each row) that blocks first..last left, in that
-// order, and write its outputs. All of `threads` threads take part.
-template <int D, int ROWS, bool F32>
+// Join the partial results of one item (rows of D values, then maximum and sum of each row) that blocks first..last left, and write
+// its outputs. Threads 0..THREADS-1 take part: ROWS * D/8 of them (or all) a group, a group every GROUPS-th part; the groups' results
+// meet in `area` (GROUPS - 1 times ROWS * D/8 * 10 floats; `sync` is the threads' barrier).
+template <int D, int ROWS, int THREADS>
+struct JoinShape {
+  static constexpr int PIECES = ROWS * D / 8;
+  static constexpr int GROUPS = THREADS > PIECES ? THREADS / PIECES : 1;
+  static constexpr size_t AREA = (size_t)(GROUPS - 1) * PIECES * 10 * 4;
+};
+template <int D, int ROWS, int THREADS, bool F32, typename Sync>
 __device__ void join_parts(const AttendArgs &p, const float *parts, long stride, int first, int last, int b, int h, int row0, int fresh,
-                           int thread, int threads) {
+                           int thread, float *area, Sync sync) {
+  using J = JoinShape<D, ROWS, THREADS>;
   constexpr int CH = D / 8;
-  const int G = p.c.group, rows = p.c.n_tokens * G;
-  for (int x = thread; x < ROWS * CH; x += threads) {
-    const int row = x / CH, e8 = (x % CH) * 8, rr = row0 + row, t = rr / G;
-    if (rr >= rows) continue;
-    float M = -INFINITY, y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, L = 0.0f;
-    for (int i0 = first; i0 <= last; i0 += 4) {        // four parts at a time: their loads go out together
+  const int G = p.c.group, rows = p.c.n_tokens * G, grp = thread / J::PIECES;
+  float M = -INFINITY, y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, L = 0.0f;
+  auto add = [&](float m, float l, const float4 &u, const float4 &v) {
+    const float f = m == -INFINITY ? 0.0f : exp2_approx(m - M);
+    L += f * l;
+    y[0] += f * u.x, y[1] += f * u.y, y[2] += f * u.z, y[3] += f * u.w;
+    y[4] += f * v.x, y[5] += f * v.y, y[6] += f * v.z, y[7] += f * v.w;
+  };
+  auto raise = [&](float top) {
+    const float keep = M == -INFINITY ? 0.0f : exp2_approx(M - top);
+    M = top;
+    L *= keep;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] *= keep;
+  };
+  auto write = [&](int row, int e8) {
+    const int rr = row0 + row, t = rr / G;
+    if (rr >= rows) return;
+    char *dst = p.o.p + (b * p.o.sb + (long)t * p.o.st + (long)(h * G + rr - t * G) * p.o.sh + e8) * (F32 ? 4 : 2);
+    store_out<F32>(dst, y, t < fresh && L > 0.0f ? 1.0f / L : 0.0f);
+  };
+  for (int x = J::GROUPS > 1 ? thread % J::PIECES : thread; x < J::PIECES; x += J::GROUPS > 1 ? J::PIECES : THREADS) {
+    const int row = x / CH, e8 = (x % CH) * 8;
+    M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = 0.0f;
+    const bool live = grp < J::GROUPS && row0 + row < rows;
+    for (int i0 = first + (J::GROUPS > 1 ? grp : 0); live && i0 <= last; i0 += 4 * J::GROUPS) {   // four at a time: their loads go out together
       float2 e[4];
       float4 u[4], v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int i = min(i0 + k, last);
+        const int i = min(i0 + k * J::GROUPS, last);
         const float *src = parts + (2 * i + (i == first)) * stride;
         e[k] = __ldcg(reinterpret_cast<const float2 *>(src + ROWS * D + 2 * row));
         u[k] = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8));
@@ -308,22 +345,35 @@ __device__ void join_parts(const AttendArgs &p, const float *parts, long stride,
       float top = M;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (i0 + k <= last) top = fmaxf(top, e[k].x);
-      const float keep = M == -INFINITY ? 0.0f : exp2_approx(M - top);
-      M = top;
-      L *= keep;
+        if (i0 + k * J::GROUPS <= last) top = fmaxf(top, e[k].x);
+      raise(top);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] *= keep;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f = i0 + k <= last && e[k].x != -INFINITY ? exp2_approx(e[k].x - M) : 0.0f;
-        L += f * e[k].y;
-        y[0] += f * u[k].x, y[1] += f * u[k].y, y[2] += f * u[k].z, y[3] += f * u[k].w;
-        y[4] += f * v[k].x, y[5] += f * v[k].y, y[6] += f * v[k].z, y[7] += f * v[k].w;
-      }
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k * J::GROUPS <= last) add(e[k].x, e[k].y, u[k], v[k]);
     }
-    char *dst = p.o.p + (b * p.o.sb + (long)t * p.o.st + (long)(h * G + rr - t * G) * p.o.sh + e8) * (F32 ? 4 : 2);
-    store_out<F32>(dst, y, t < fresh && L > 0.0f ? 1.0f / L : 0.0f);
+    if (J::GROUPS == 1) write(row, e8);
+  }
+  if (J::GROUPS > 1) {
+    const int x = thread % J::PIECES, row = x / CH, e8 = (x % CH) * 8;
+    if (grp > 0 && grp < J::GROUPS) {
+      float *dst = area + ((grp - 1) * J::PIECES + x) * 2;
+      dst[0] = M;
+      dst[1] = L;
+      float4 *o = reinterpret_cast<float4 *>(area + (J::GROUPS - 1) * J::PIECES * 2) + ((grp - 1) * J::PIECES + x) * 2;
+      o[0] = make_float4(y[0], y[1], y[2], y[3]);
+      o[1] = make_float4(y[4], y[5], y[6], y[7]);
+    }
+    sync();
+    if (grp == 0) {
+      for (int q = 0; q < J::GROUPS - 1; ++q) {
+        const float *src = area + (q * J::PIECES + x) * 2;
+        const float4 *o = reinterpret_cast<const float4 *>(area + (J::GROUPS - 1) * J::PIECES * 2) + (q * J::PIECES + x) * 2;
+        raise(fmaxf(M, src[0]));
+        add(src[0], src[1], o[0], o[1]);
+      }
+      write(row, e8);
+    }
+    sync();
   }
 }
 
@@ -331,18 +381,18 @@ template <int D, int BITS, int NT, int PARTS, int NW, int STAGES>
 struct AttendShape {
   using L = Tile<D, BITS>;
   static constexpr int ROWS = 8 * NT, THREADS = NW * 32;
-  static constexpr int OROW = D + 4;                                    // padded scratch row
   static constexpr int QROW = D * (PARTS > 1 ? 4 : 2);                  // bytes of a query row
   static constexpr size_t RING = (size_t)NW * STAGES * L::BYTES;
-  static constexpr size_t QRAW = (size_t)2 * ROWS * QROW;               // queries of this and the next segment
+  static constexpr size_t QRAW = (size_t)ROWS * QROW;                   // queries of the next segment
   static constexpr size_t QF = (size_t)NT * L::NG * PARTS * 1024;       // queries as fragments
-  static constexpr size_t SCRATCH = (size_t)NW * ROWS * OROW * 4;
+  static constexpr size_t SCRATCH = (size_t)(NW - 1) * ROWS * D * 4;    // the warps' results, but the first one's
+  static_assert(JoinShape<D, ROWS, THREADS>::AREA <= SCRATCH, "the groups of a join meet in the warps' areas");
   static constexpr size_t ML = (size_t)NW * ROWS * 2 * 4;
   static constexpr size_t OQRAW = RING, OQF = OQRAW + QRAW, OSCR = OQF + QF, OML = OSCR + SCRATCH, OROWS = OML + ML,
                           OBAR = OROWS + ROWS * 4, OSEG = OBAR + (NW * STAGES * 8 + 15) / 16 * 16,
                           OSUM = OSEG + (SEGS + 1) * sizeof(Segment), OCUM = OSUM + 32 * 4 + 16;
   // prefix sums of up to this many sequences: few capacities, so that the occupancy of each is asked for once
-  __host__ __device__ static constexpr int capacity(int batch) { return batch <= 128 ? 128 : PACE_KV_MAX_BATCH; }
+  __host__ __device__ static constexpr int capacity(int batch) { return batch <= 64 ? 64 : batch <= 256 ? 256 : PACE_KV_MAX_BATCH; }
   static constexpr size_t smem(int batch) { return OCUM + (size_t)(capacity(batch) + 1) * 4 + (size_t)capacity(batch) * sizeof(Seq); }
 };
 
@@ -378,25 +428,26 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   pdl_enter();
   tile_line<TILE>(c, (unsigned)p.row_blocks * c.Hkv, seq, cum, wsum);
 
-  // equal shares, but no cut finer than a tile for every warp or a whole average item
+  // equal shares, but none finer than a tile for every warp, or than a whole average item of up to three: joining one costs about as
+  // much as three rounds of tiles
   const unsigned total = cum[c.batch];
   unsigned share = (total + gridDim.x - 1) / gridDim.x;
   {
     const unsigned mean = total / ((unsigned)c.batch * c.Hkv * p.row_blocks);
-    share = max(share, min(mean, (unsigned)NW));
+    share = max(share, mean <= 3u * NW ? mean : NW);
   }
   const unsigned lo = blockIdx.x * share, hi = min(total, lo + share);
   if (blockIdx.x > total / share || lo >= total) return;
   auto segment = [&](unsigned at) { return segment_at<TILE>(seq, cum, c.batch, p.row_blocks, at, hi); };
 
   // ---- queries of a segment, copied one segment ahead
-  auto copy_queries = [&](const Segment &s, int buf) {
+  auto copy_queries = [&](const Segment &s) {
     constexpr int CH = S::QROW / 16;
     for (int x = tid; x < ROWS * CH; x += S::THREADS) {
       const int row = x / CH, ch = x % CH, rr = s.rb * ROWS + row, t = rr / G;
       const bool in = rr < T * G;
       const char *src = in ? p.q.p + (s.b * p.q.sb + (long)t * p.q.st + (long)(s.h * G + rr - t * G) * p.q.sh) * ES + ch * 16 : p.q.p;
-      cp_async16(qraw + buf * ROWS * S::QROW + row * S::QROW + ch * 16, src, in);
+      cp_async16(qraw + row * S::QROW + ch * 16, src, in);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -450,7 +501,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
     fstage = fstage + 1 == STAGES ? 0 : fstage + 1;
   };
   const uint32_t magic = opaque(0x64006400u);
-  int stage = 0, qbuf = 0;
+  int stage = 0;
   int pseg = 0;                                       // items shared with other blocks: 1 the one it began with, 2 the one it ends with
 #pragma unroll 1
   for (unsigned round = lo; round < hi;) {            // SEGS segments a round
@@ -462,32 +513,31 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
    nseg = segs[SEGS].end;
    round = (unsigned)segs[SEGS].tile;
    look_ahead(0, segs[0].tile + w);
-   copy_queries(segs[0], qbuf);
+   copy_queries(segs[0]);
 #pragma unroll 1
    for (int i = 0; i < STAGES - 1; ++i) fetch();
 #pragma unroll 1
-   for (int k = 0; k < nseg; ++k, qbuf ^= 1) {
+   for (int k = 0; k < nseg; ++k) {
     const Segment sg = segs[k];
     const Seq sq = seq[sg.b];
     const int len = sq.len, nn = sq.fresh, tokens = sq.tokens;
     const int row0 = sg.rb * ROWS;
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();                                  // this segment's queries are here; the last one's areas are free
-    if (k + 1 < nseg) copy_queries(segs[k + 1], qbuf ^ 1);
-
     // ---- queries as B fragments: lane (j, cc) takes dims 64g + 16cc .. + 15 of row j of each block of eight. bf16: as fp16 over a
     // power of two that puts the row's largest element in [1, 2), exact but below 2^-14 of it. fp32: as three bf16 parts.
     {
-      constexpr int TPR = S::THREADS / ROWS, PAIRS = D / TPR / 2;
+      constexpr int TPR = S::THREADS / ROWS < 32 ? S::THREADS / ROWS : 32, PAIRS = D / TPR / 2;      // threads a row
       const int row = tid / TPR, e0 = (tid % TPR) * 2 * PAIRS;
-      const char *src = qraw + qbuf * ROWS * S::QROW + row * S::QROW + e0 * ES;
+      const char *src = qraw + row * S::QROW + e0 * ES;
       const bool neg = p.scale_log2 < 0.0f;
       float mul = fabsf(p.scale_log2);
       auto put = [&](int i, int part, uint32_t v) {
         const int e = e0 + 2 * i, g = e >> 6, k = (e & 15) >> 1, ln = (row & 7) * 4 + ((e & 63) >> 4);
         qf[((((row >> 3) * NG + g) * PARTS + part) * 2 + (k >> 2)) * 128 + ln * 4 + (k & 3)] = v;
       };
-      if (!F32) {
+      if (row >= ROWS) {
+      } else if (!F32) {
         uint32_t x[PAIRS], top = 0;
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
@@ -511,9 +561,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
           for (int e = 0; e < PARTS; ++e) put(i, e, a[e]);
         }
       }
-      if (tid % TPR == 0) rowmul[row] = fmaxf(mul, FLT_MIN);          // (not 0: a masked score is -inf)
+      if (tid % TPR == 0 && row < ROWS) rowmul[row] = fmaxf(mul, FLT_MIN);          // (not 0: a masked score is -inf)
     }
     __syncthreads();
+    if (k + 1 < nseg) copy_queries(segs[k + 1]);
     float crow[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) crow[n][0] = rowmul[8 * n + 2 * cc], crow[n][1] = rowmul[8 * n + 2 * cc + 1];
@@ -547,12 +598,6 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       constexpr int GP = BITS == 4 && D > 64 ? 2 : 1;   // groups whose words share a chunk
       constexpr int KW = BITS == 4 ? 2 : 4;             // words of a token's 16 dims
       float s[2][NT][4];
-#pragma unroll
-      for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[blk][n][e] = 0.0f;
 #pragma unroll
       for (int g0 = 0; g0 < NG; g0 += GP) {
         uint32_t kw[2][2][GP * KW];
@@ -615,28 +660,31 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
               }
             }
             float d[NT][4];
+            if (F32) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+              for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < PARTS; ++e) {
-                  if (!F32) mma_f16(d[n], fr[0][2 * k], fr[1][2 * k], fr[0][2 * k + 1], fr[1][2 * k + 1], q[n][e][2 * k], q[n][e][2 * k + 1]);
+                  if (!F32 && k == 0) mma_f16_first(d[n], fr[0][0], fr[1][0], fr[0][1], fr[1][1], q[n][e][0], q[n][e][1]);
+                  else if (!F32) mma_f16(d[n], fr[0][2 * k], fr[1][2 * k], fr[0][2 * k + 1], fr[1][2 * k + 1], q[n][e][2 * k], q[n][e][2 * k + 1]);
                   else mma_bf16(d[n], fr[0][2 * k], fr[1][2 * k], fr[0][2 * k + 1], fr[1][2 * k + 1], q[n][e][2 * k], q[n][e][2 * k + 1]);
                 }
             const uint32_t sw = blk ? ksw.y : ksw.x;
             const float s0 = __uint_as_float(sw << 16), s1 = __uint_as_float(sw & 0xFFFF0000u);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              s[blk][n][0] = fmaf(s0, d[n][0], s[blk][n][0]);
-              s[blk][n][1] = fmaf(s0, d[n][1], s[blk][n][1]);
-              s[blk][n][2] = fmaf(s1, d[n][2], s[blk][n][2]);
-              s[blk][n][3] = fmaf(s1, d[n][3], s[blk][n][3]);
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float sk = e < 2 ? s0 : s1;
+                s[blk][n][e] = g == 0 ? sk * d[n][e] : fmaf(sk, d[n][e], s[blk][n][e]);
+              }
           }
         }
       }
@@ -825,57 +873,88 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       __syncwarp();                                   // every lane is done with the stage before it is filled again
     }
 
-    // ---- join the warps (their areas were free from the segment's first barrier on)
+    // ---- join the warps: the others leave their accumulators, as they lie in the fragments, for the first one
+    const bool whole = sg.tile == 0 && sg.end == sg.tiles;
+    constexpr int FR = NG * 4 * NT * 32;               // float4s a warp
+    float4 *left = reinterpret_cast<float4 *>(scratch);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], o);
-        const int row = 8 * n + 2 * cc + r;
-        if (j == 0) {
-          ml[(w * ROWS + row) * 2] = m[n][r];
-          ml[(w * ROWS + row) * 2 + 1] = l[n][r];
-        }
-        float *dst = scratch + (w * ROWS + row) * S::OROW + 8 * j;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          *reinterpret_cast<float4 *>(dst + 64 * g) = make_float4(acc[g][0][n][r], acc[g][0][n][2 + r], acc[g][1][n][r], acc[g][1][n][2 + r]);
-          *reinterpret_cast<float4 *>(dst + 64 * g + 4) = make_float4(acc[g][2][n][r], acc[g][2][n][2 + r], acc[g][3][n][r], acc[g][3][n][2 + r]);
-        }
+        if (w > 0 && j == 0) *reinterpret_cast<float2 *>(ml + (w * ROWS + 8 * n + 2 * cc + r) * 2) = make_float2(m[n][r], l[n][r]);
       }
+    if (w > 0) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            left[(w - 1) * FR + ((g * 4 + i) * NT + n) * 32 + lane] = make_float4(acc[g][i][n][0], acc[g][i][n][1], acc[g][i][n][2], acc[g][i][n][3]);
+    }
     __syncthreads();
-    const bool whole = sg.tile == 0 && sg.end == sg.tiles;
-    // (an item that is shared and starts in this block is the block's last)
-    float *mine = c.part + (long)(2 * blockIdx.x + (sg.tile == 0 ? 1 : 0)) * part_floats(D, NT);
-    constexpr int CH = D / 8;                                          // 8-element pieces of a row
-    for (int x = tid; x < ROWS * CH; x += S::THREADS) {
-      const int row = x / CH, e8 = (x % CH) * 8;
-      const int rr = row0 + row, t = rr / G;
-      float M = -INFINITY;
+    if (w == 0) {
+      float M[NT][2], f0[NT][2];
 #pragma unroll
-      for (int i = 0; i < NW; ++i) M = fmaxf(M, ml[(i * ROWS + row) * 2]);
-      float y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, Ls = 0.0f;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        const float mi = ml[(i * ROWS + row) * 2];
-        const float f2 = mi == -INFINITY ? 0.0f : exp2_approx(mi - M);
-        Ls += f2 * ml[(i * ROWS + row) * 2 + 1];
-        const float4 u = *reinterpret_cast<const float4 *>(scratch + (i * ROWS + row) * S::OROW + e8);
-        const float4 v = *reinterpret_cast<const float4 *>(scratch + (i * ROWS + row) * S::OROW + e8 + 4);
-        y[0] += f2 * u.x, y[1] += f2 * u.y, y[2] += f2 * u.z, y[3] += f2 * u.w;
-        y[4] += f2 * v.x, y[5] += f2 * v.y, y[6] += f2 * v.z, y[7] += f2 * v.w;
+        for (int r = 0; r < 2; ++r) {
+          M[n][r] = m[n][r];
+          for (int i = 1; i < NW; ++i) M[n][r] = fmaxf(M[n][r], ml[(i * ROWS + 8 * n + 2 * cc + r) * 2]);
+          f0[n][r] = m[n][r] == -INFINITY ? 0.0f : exp2_approx(m[n][r] - M[n][r]);
+          l[n][r] *= f0[n][r];
+        }
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[g][i][n][e] *= f0[n][e & 1];
+#pragma unroll 2
+      for (int i = 1; i < NW; ++i) {
+        float f[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 e = *reinterpret_cast<const float2 *>(ml + (i * ROWS + 8 * n + 2 * cc + r) * 2);
+            f[n][r] = e.x == -INFINITY ? 0.0f : exp2_approx(e.x - M[n][r]);
+            l[n][r] = fmaf(f[n][r], e.y, l[n][r]);
+          }
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const float4 x = left[(i - 1) * FR + ((g * 4 + t) * NT + n) * 32 + lane];
+              acc[g][t][n][0] = fmaf(f[n][0], x.x, acc[g][t][n][0]), acc[g][t][n][1] = fmaf(f[n][1], x.y, acc[g][t][n][1]);
+              acc[g][t][n][2] = fmaf(f[n][0], x.z, acc[g][t][n][2]), acc[g][t][n][3] = fmaf(f[n][1], x.w, acc[g][t][n][3]);
+            }
       }
-      if (whole) {
-        if (rr >= T * G) continue;
-        store_out<F32>(p.o.p + (sg.b * p.o.sb + (long)t * p.o.st + (long)(sg.h * G + rr - t * G) * p.o.sh + e8) * ES, y,
-                       t < nn && Ls > 0.0f ? 1.0f / Ls : 0.0f);
-      } else {
-        float *dst = mine + row * D + e8;
-        *reinterpret_cast<float4 *>(dst) = make_float4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<float4 *>(dst + 4) = make_float4(y[4], y[5], y[6], y[7]);
-        if (e8 == 0) *reinterpret_cast<float2 *>(mine + ROWS * D + 2 * row) = make_float2(M, Ls);
-      }
+      // (an item that is shared and starts in this block is the block's last)
+      float *mine = c.part + (long)(2 * blockIdx.x + (sg.tile == 0 ? 1 : 0)) * part_floats(D, NT);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = 8 * n + 2 * cc + r, rr = row0 + row, t = rr / G;
+          if (rr >= T * G) continue;
+          const float inv = !whole ? 1.0f : t < nn && l[n][r] > 0.0f ? 1.0f / l[n][r] : 0.0f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float y[8] = {acc[g][0][n][r], acc[g][0][n][2 + r], acc[g][1][n][r], acc[g][1][n][2 + r],
+                                acc[g][2][n][r], acc[g][2][n][2 + r], acc[g][3][n][r], acc[g][3][n][2 + r]};
+            const int e8 = 64 * g + 8 * j;
+            if (whole) store_out<F32>(p.o.p + (sg.b * p.o.sb + (long)t * p.o.st + (long)(sg.h * G + rr - t * G) * p.o.sh + e8) * ES, y, inv);
+            else store_out<true>(reinterpret_cast<char *>(mine + row * D + e8), y, 1.0f);
+          }
+          if (!whole && j == 0) *reinterpret_cast<float2 *>(mine + ROWS * D + 2 * row) = make_float2(M[n][r], l[n][r]);
+        }
     }
     if (!whole) pseg |= sg.tile ? 1 : 2;
    }
@@ -907,7 +986,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
         Segment it;
         int first, last;
         shared(k, it, first, last);
-        join_parts<D, ROWS, F32>(p, c.part, part_floats(D, NT), first, last, it.b, it.h, it.rb * ROWS, seq[it.b].fresh, tid, S::THREADS);
+        join_parts<D, ROWS, S::THREADS, F32>(p, c.part, part_floats(D, NT), first, last, it.b, it.h, it.rb * ROWS, seq[it.b].fresh, tid,
+                                             scratch, [] { __syncthreads(); });
       }
   }
   if (dead) {                                         // a wait gave up: let the copies in flight land (bounded) before leaving

@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         if (tid == 0) *join_flag = last_part(&c.count[fb], lb - fb + 1);
         bar_sync(2, NWG * 128);
         if (*join_flag) {
-          join_parts<D, S::ROWS, false>(p, c.part, TC_PART_FLOATS, fb, lb, sg.b, sg.h, sg.rb * S::ROWS, nn, tid, NWG * 128);
+          join_parts<D, S::ROWS, NWG * 128, false>(p, c.part, TC_PART_FLOATS, fb, lb, sg.b, sg.h, sg.rb * S::ROWS, nn, tid, nullptr,
+                                                   [] { bar_sync(2, NWG * 128); });
         }
       }
       fence_before_sync();
