@@ -9,8 +9,8 @@
 // tiles with new tokens, where rows may see different tokens, each token by its own), weights are taken relative to 2^10 of the
 // running maximum. The powers return with the scores, and in O as a running exponent per row raised like the maximum.
 //
-// Roles (warps): softmax (four a group; thread = row = TMEM lane), four that dequantize, one that copies tiles in, one that issues
-// the products. Two softmax groups take turns, so that the tensor cores work on one group's products while the other group forms
+// Roles (warps): softmax (four a group; thread = row = TMEM lane), four that dequantize, two that prepare a tile's scales for them, one
+// that copies tiles in, one that issues the products. Two softmax groups take turns, so that the tensor cores work on one group's products while the other group forms
 // its weights: the groups are two row blocks (SHARE), or even and odd tiles of one block (ALT, joined at the end through TMEM).
 //   bound: per 64 tokens and row block of 128 at D = 128, 512 cycles of tensor work; 64 scores a thread (4.5 instructions each, two
 //   groups a scheduler) and a quarter of 16,384 codes a scheduler (about two instructions each) come to about the same.
@@ -34,8 +34,8 @@ struct TcShape {
   static constexpr int ROWS = 128 * NRB;
   static constexpr int KS = 2, VS = 2;                                  // dequantized stages
   static constexpr int RS = D == 256 ? (BITS == 4 ? 3 : 2) : 4;         // raw stages
-  static constexpr int WARPS = 4 * NWG + 6, THREADS = WARPS * 32;
-  static constexpr int W_DEQ = 4 * NWG, W_LOAD = W_DEQ + 4, W_MMA = W_DEQ + 5;
+  static constexpr int WARPS = 4 * NWG + 8, THREADS = WARPS * 32;
+  static constexpr int W_DEQ = 4 * NWG, W_PAR = W_DEQ + 4, W_LOAD = W_PAR + 2, W_MMA = W_LOAD + 1;
   // TMEM columns
   static constexpr int CQ = 0, CO = NRB * D / 2, CS = CO + NWG * D;
   static_assert(CS + NWG * KVT <= 512, "TMEM");
@@ -47,8 +47,8 @@ struct TcShape {
   static constexpr int OEXP = OPAR + 2 * PAR;                           // exponents [8 tiles][k, v][64] int8
   static constexpr int OML = OEXP + 8 * 2 * KVT;                        // m, l, exponent of group 1 (ALT)
   static constexpr int OBAR = OML + 128 * 12;
-  static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 4 * NWG + 1;
-  static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flag, red[4]
+  static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 4 * NWG + 5;
+  static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flag, red[8]
   static constexpr int OCUM = (OMISC + 64 + 15) / 16 * 16;
   static constexpr size_t smem(int batch) { return OCUM + 32 * 4 + (size_t)(batch + 1) * 4 + (size_t)batch * sizeof(Seq); }
 };
@@ -56,6 +56,11 @@ constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 1
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
   return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void bar_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
 
@@ -114,7 +119,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::OBAR);
   uint64_t *raw_full = bar, *raw_free = raw_full + RS, *k_full = raw_free + RS, *k_free = k_full + KS, *v_full = k_free + KS,
            *v_free = v_full + VS, *s_full = v_free + VS, *p_ready = s_full + NWG, *o_full = p_ready + NWG,
-           *q_ready = o_full + NWG, *drain = q_ready + NWG;
+           *q_ready = o_full + NWG, *par_full = q_ready + NWG, *par_free = par_full + 2, *drain = par_free + 2;
   int *raw_flags = reinterpret_cast<int *>(smem + S::OMISC);            // [RS]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_flags + 4);
   int *join_flag = raw_flags + 5;
@@ -134,6 +139,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128), mbar_init(&o_full[i], 1);
       mbar_init(&q_ready[i], 128);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&par_full[i], 2), mbar_init(&par_free[i], 4);
     mbar_init(drain, 1);
     mbar_fence_init();
   }
@@ -145,7 +151,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   fence_before_sync();
   tile_line<KVT>(c, (unsigned)p.row_blocks * c.Hkv, seq, cum, wsum);      // (its barriers also publish the set-up above)
   fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;          // the whole of TMEM is this block's: its first column (a constant keeps addresses uniform)
 
   const unsigned total = cum[c.batch];
   const unsigned share = max((total + gridDim.x - 1) / gridDim.x, (unsigned)p.min_share);
@@ -171,8 +177,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         const int kn = min(32, last - s0);
         for (int k = 0; k < kn; k += 2) {
           const int pa = __shfl_sync(0xffffffffu, mytile, k), pb = __shfl_sync(0xffffffffu, mytile, k + 1);
-          if (n >= RS && !mbar_wait(&raw_free[stage], (n / RS - 1) & 1, LIMIT)) good = false;
-          good = __all_sync(0xffffffffu, good);
+          if (n >= RS) good = __all_sync(0xffffffffu, mbar_wait(&raw_free[stage], (n / RS - 1) & 1, LIMIT));
           if (!good) break;
           if (lane == 0) {
             raw_flags[stage] = (pa >= 0 ? 1 : 0) | (pb >= 0 ? 2 : 0);
@@ -191,55 +196,23 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     if (!good && lane == 0) gave_up();
     // copies still in flight land before the block leaves (at most RS of them)
     for (int i = max(0, n - RS); i < n; ++i) mbar_wait(&raw_full[i % RS], (i / RS) & 1, LIMIT);
-  } else if (warp >= S::W_DEQ && warp < S::W_LOAD) {
+  } else if (warp >= S::W_DEQ && warp < S::W_PAR) {
     // ---------------------------------------------------------------- dequantize
-    const int dt = tid - S::W_DEQ * 32, dw = warp - S::W_DEQ;
+    const int dw = warp - S::W_DEQ;
     int n = 0;
     bool good = true;
     for (unsigned pos = lo; pos < hi;) {
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
-      const int tokens = seq[sg.b].tokens, len = seq[sg.b].len;
       for (int tile = sg.tile; tile < sg.end; ++tile, ++n) {
         const int rs = n % RS;
         good = good && mbar_wait(&raw_full[rs], (n / RS) & 1, LIMIT);
         good = __all_sync(0xffffffffu, good);
         const char *raw = smem + S::ORAW + rs * S::RAW;
         char *par = smem + S::OPAR + (n & 1) * S::PAR;
-        // parameters: thread = token of K (0..63) or V (64..127)
-        {
-          const int part = dt >> 6, t = dt & 63, sub = t >> 5, tt = t & 31;
-          const char *st = raw + sub * L::BYTES;
-          const bool live = tile * KVT + t < tokens && ((raw_flags[rs] >> sub) & 1);
-          const int ps = L::pos(tt);
-          float s[NG], top = 0.0f;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            s[g] = live ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(st + (part ? L::VS : L::KS))[g * TILE + ps]) : 0.0f;
-            top = fmaxf(top, s[g]);
-          }
-          const bool own = (tile + 1) * KVT > len;                      // new tokens in the tile: an exponent a token
-          float all = warp_max(top);
-          if (lane == 0) red[dw] = all;
-          bar_sync(1, 128);
-          all = fmaxf(red[part * 2], red[part * 2 + 1]);
-          const float ref = own ? top : all;
-          const int e = ref > 0.0f ? (int)(__float_as_uint(ref) >> 23) - 127 : 0;
-          exps[((n & 7) * 2 + part) * KVT + t] = (int8_t)e;
-          const float down = exp2i(-e < 127 ? -e : 127);                // (e >= -126)
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float sc = s[g] * down;
-            uint4 v = make_uint4(h2pack(sc, sc), 0, 0, 0);
-            if (BITS == 4) {
-              const int z = reinterpret_cast<const uint8_t *>(st + (part ? L::VZ : L::KZ))[g * TILE + (part ? L::vpos(tt) : ps)];
-              v.y = h2pack(-(1024.0f + z), -(1024.0f + z));
-              v.z = h2pack(-(64.0f + z), -(64.0f + z));
-            }
-            *reinterpret_cast<uint4 *>(par + ((part * NG + g) * KVT + t) * 16) = v;
-          }
-          bar_sync(1, 128);
-        }
+        good = good && mbar_wait(&par_full[n & 1], (n >> 1) & 1, LIMIT);
+        good = __all_sync(0xffffffffu, good);
+        if (!good) continue;
         // codes: warp = 16 tokens; eight lanes write eight tokens' pieces of one 128-byte core
         auto param = [&](int part, int g, int t) { return *reinterpret_cast<const uint4 *>(par + ((part * NG + g) * KVT + t) * 16); };
         auto put = [&](char *dst, int t, int a, const uint4 &v) {
@@ -313,71 +286,152 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           if (lane == 0) {
             mbar_arrive(&v_full[vs]);
             mbar_arrive(&raw_free[rs]);
+            mbar_arrive(&par_free[n & 1]);
           }
         }
       }
     }
     if (!good && lane == 0) gave_up();
+  } else if (warp >= S::W_PAR && warp < S::W_LOAD) {
+    // ---------------------------------------------------------------- a tile's scales and exponents: lane = token
+    const int pw = warp - S::W_PAR, t = pw * 32 + lane, ps = L::pos(lane), vp = L::vpos(lane);
+    int n = 0;
+    bool good = true;
+    for (unsigned pos = lo; pos < hi;) {
+      const Segment sg = at(pos);
+      pos += sg.end - sg.tile;
+      const int tokens = seq[sg.b].tokens, len = seq[sg.b].len;
+      for (int tile = sg.tile; tile < sg.end; ++tile, ++n) {
+        const int rs = n % RS;
+        good = good && mbar_wait(&raw_full[rs], (n / RS) & 1, LIMIT);
+        if (n >= 2) good = good && mbar_wait(&par_free[n & 1], ((n >> 1) - 1) & 1, LIMIT);
+        good = __all_sync(0xffffffffu, good);
+        const char *st = smem + S::ORAW + rs * S::RAW + pw * L::BYTES;
+        char *par = smem + S::OPAR + (n & 1) * S::PAR;
+        const bool live = tile * KVT + t < tokens && ((raw_flags[rs] >> pw) & 1);
+        const bool own = (tile + 1) * KVT > len;                        // new tokens in the tile: an exponent a token
+        float s[2][NG], top[2];
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          top[part] = 0.0f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            s[part][g] = live ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(st + (part ? L::VS : L::KS))[g * TILE + ps]) : 0.0f;
+            top[part] = fmaxf(top[part], s[part][g]);
+          }
+          const float all = warp_max(top[part]);
+          if (lane == 0) red[(n & 1) * 4 + part * 2 + pw] = all;
+        }
+        bar_sync(1, 64);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const float *r = red + (n & 1) * 4 + part * 2;
+          const float ref = own ? top[part] : fmaxf(r[0], r[1]);
+          const int e = ref > 0.0f ? (int)(__float_as_uint(ref) >> 23) - 127 : 0;
+          exps[((n & 7) * 2 + part) * KVT + t] = (int8_t)e;
+          const float down = exp2i(-e < 127 ? -e : 127);                // (e >= -126)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float sc = s[part][g] * down;
+            uint4 v = make_uint4(h2pack(sc, sc), 0, 0, 0);
+            if (BITS == 4) {
+              const int z = reinterpret_cast<const uint8_t *>(st + (part ? L::VZ : L::KZ))[g * TILE + (part ? vp : ps)];
+              v.y = h2pack(-(1024.0f + z), -(1024.0f + z));
+              v.z = h2pack(-(64.0f + z), -(64.0f + z));
+            }
+            *reinterpret_cast<uint4 *>(par + ((part * NG + g) * KVT + t) * 16) = v;
+          }
+        }
+        __syncwarp();
+        if (lane == 0 && good) mbar_arrive(&par_full[n & 1]);
+      }
+    }
+    if (!good && lane == 0) gave_up();
   } else if (warp == S::W_MMA) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
-      bool good = true;
-      const uint32_t sb = smem_u32(smem);
-      int ntile = 0;                                      // tiles of the segments before
-      int nq = 0;
-      int np[2] = {0, 0};                                 // tasks done per group
-      constexpr uint32_t ID_S = idesc_f16(128, KVT, 0), ID_O = idesc_f16(128, D, 1);
-      for (unsigned pos = lo; pos < hi && good;) {
-        const Segment sg = at(pos);
-        pos += sg.end - sg.tile;
-        const int tiles = sg.end - sg.tile;
-        const int tasks = MODE == TC_SHARE ? 2 * tiles : tiles;
-        auto wg_of = [&](int k) { return MODE == TC_ONE ? 0 : k & 1; };
-        auto tile_of = [&](int k) { return ntile + (MODE == TC_SHARE ? k >> 1 : k); };
-        auto qk = [&](int k) {
-          const int w = wg_of(k), tl = tile_of(k), ks = tl % KS;
-          if (!mbar_wait(&k_full[ks], (tl / KS) & 1, LIMIT)) return false;
-          fence_after_sync();
-          const uint32_t kb = sb + S::OK + ks * S::KB;
-          const uint32_t qa = tmem + S::CQ + (MODE == TC_SHARE ? w * (D / 2) : 0);
+    // The warp runs as one, so that descriptors and addresses stay in uniform registers; one lane issues.
+    bool good = true;
+    const bool leader = elect_one();
+    const uint32_t sb = smem_u32(smem);
+    int ntile = 0;                                        // tiles of the segments before
+    int nq = 0;
+    int np0 = 0, np1 = 0;                                 // tasks done per group
+    constexpr uint32_t ID_S = idesc_f16(128, KVT, 0), ID_O = idesc_f16(128, D, 1);
+    const uint64_t kdesc = smem_desc(sb + S::OK, 128, (D / 8) * 128), vdesc = smem_desc(sb + S::OV, (D / 8) * 128, 128);
+    auto ready = [&](uint64_t *b, int phase) {
+      // (all lanes together: a lane left behind could miss the phase it waits for)
+      good = __all_sync(0xffffffffu, good && mbar_wait(b, phase & 1, LIMIT));
+      return good;
+    };
+    auto qk = [&](int w, int tl, bool last_use) {         // S of group w for tile tl
+      const int ks = tl % KS;
+      if (!ready(&k_full[ks], tl / KS)) return;
+      fence_after_sync();
+      if (leader) {
+        const uint64_t kd = kdesc + (uint64_t)(ks * (S::KB >> 4));
+        const uint32_t qa = tmem + S::CQ + (MODE == TC_SHARE ? w * (D / 2) : 0);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            mma_ts(tmem + S::CS + w * KVT, qa + 8 * i, smem_desc(kb + i * 256, 128, (D / 8) * 128), ID_S, i ? 1u : 0u);
-          commit(&s_full[w]);
-          if (MODE != TC_SHARE || w == 1) commit(&k_free[ks]);
-          return true;
-        };
-        auto pv = [&](int k) {
-          const int w = wg_of(k), tl = tile_of(k), vs = tl % VS;
-          if (!mbar_wait(&v_full[vs], (tl / VS) & 1, LIMIT)) return false;
-          if (!mbar_wait(&p_ready[w], np[w] & 1, LIMIT)) return false;
-          ++np[w];
-          fence_after_sync();
-          const uint32_t vb = sb + S::OV + vs * S::KB;
-          const bool first = k < (MODE == TC_ONE ? 1 : 2);
-#pragma unroll
-          for (int i = 0; i < KVT / 16; ++i)
-            mma_ts(tmem + S::CO + w * D, tmem + S::CS + w * KVT + 8 * i, smem_desc(vb + i * 2 * (D / 8) * 128, (D / 8) * 128, 128),
-                   ID_O, first && i == 0 ? 0u : 1u);
-          if (MODE != TC_SHARE || w == 1) commit(&v_free[vs]);
-          if (k + NWG >= tasks) commit(&o_full[w]);
-          return true;
-        };
-        for (int w = 0; w < (MODE == TC_SHARE ? 2 : 1); ++w) good = good && mbar_wait(&q_ready[w], nq & 1, LIMIT);
-        if (MODE == TC_ALT) good = good && mbar_wait(&q_ready[1], nq & 1, LIMIT);
-        ++nq;
-        fence_after_sync();
-        for (int k = 0; k < NWG && k < tasks && good; ++k) good = qk(k);
-        for (int k = 0; k < tasks && good; ++k) {
-          good = pv(k);
-          if (good && k + NWG < tasks) good = qk(k + NWG);
-        }
-        ntile += tiles;
+        for (int i = 0; i < D / 16; ++i) mma_ts(tmem + S::CS + w * KVT, qa + 8 * i, kd + i * (256 >> 4), ID_S, i ? 1u : 0u);
+        commit(&s_full[w]);
+        if (last_use) commit(&k_free[ks]);
       }
-      if (!good) gave_up();
-      commit(drain);                                      // every product has ended before the block frees its TMEM
-      mbar_wait(drain, 0, LIMIT);
+    };
+    auto pv = [&](int w, int tl, bool first, bool last_use, bool last) {
+      const int vs = tl % VS;
+      if (!ready(&v_full[vs], tl / VS) || !ready(&p_ready[w], w ? np1 : np0)) return;
+      if (w) ++np1;
+      else ++np0;
+      fence_after_sync();
+      if (leader) {
+        const uint64_t vd = vdesc + (uint64_t)(vs * (S::KB >> 4));
+#pragma unroll
+        for (int i = 0; i < KVT / 16; ++i)
+          mma_ts(tmem + S::CO + w * D, tmem + S::CS + w * KVT + 8 * i, vd + i * ((2 * (D / 8) * 128) >> 4), ID_O, first && i == 0 ? 0u : 1u);
+        if (last_use) commit(&v_free[vs]);
+        if (last) commit(&o_full[w]);
+      }
+    };
+    for (unsigned pos = lo; pos < hi && good;) {
+      const Segment sg = at(pos);
+      pos += sg.end - sg.tile;
+      const int tiles = sg.end - sg.tile;
+      for (int w = 0; w < NWG; ++w) ready(&q_ready[w], nq);
+      ++nq;
+      fence_after_sync();
+      if (MODE == TC_SHARE) {
+        qk(0, ntile, false);
+        if (good) qk(1, ntile, true);
+        for (int i = 0; i < tiles && good; ++i) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (good) pv(w, ntile + i, i == 0, w == 1, i + 1 == tiles);
+            if (good && i + 1 < tiles) qk(w, ntile + i + 1, w == 1);
+          }
+        }
+      } else if (MODE == TC_ALT) {
+        qk(0, ntile, true);
+        if (good && tiles > 1) qk(1, ntile + 1, true);
+        for (int i = 0; i < tiles && good; i += 2) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (i + w < tiles) {
+              if (good) pv(w, ntile + i + w, i == 0, true, i + w + 2 >= tiles);
+              if (good && i + w + 2 < tiles) qk(w, ntile + i + w + 2, true);
+            }
+          }
+        }
+      } else {
+        qk(0, ntile, true);
+        for (int i = 0; i < tiles && good; ++i) {
+          pv(0, ntile + i, i == 0, true, i + 1 == tiles);
+          if (good && i + 1 < tiles) qk(0, ntile + i + 1, true);
+        }
+      }
+      ntile += tiles;
     }
+    if (!good && lane == 0) gave_up();
+    if (leader) commit(drain);                            // every product has ended before the block frees its TMEM
+    mbar_wait(drain, 0, LIMIT);
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax: thread = row
@@ -457,8 +511,10 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         float mx = -INFINITY, cs = crow;
         int Et = -126;
         if (!edge) {
+          float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int k = 0; k < 64; ++k) mx = fmaxf(mx, s[k]);
+          for (int k = 4; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           cs = crow * exp2i(ek[0]);
           mx *= cs;
           Et = ev[0];
@@ -496,24 +552,24 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           first = false;
         }
         const float mu = m == -INFINITY ? 0.0f : m;
-        float sum = 0.0f;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (!edge) {
           const int dE = max(Et - E, -60);
           const float add = 10.0f + (float)dE - mu;
 #pragma unroll
           for (int k = 0; k < 64; ++k) {
             s[k] = exp2_approx(fmaf(s[k], cs, add));
-            sum += s[k];
+            sum[k & 3] += s[k];
           }
-          l = fmaf(sum, exp2i(-dE), l);
+          l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), exp2i(-dE), l);
         } else {
 #pragma unroll
           for (int k = 0; k < 64; ++k) {
             const float pr = exp2_approx(s[k] - mu + 10.0f);
-            sum += pr;
+            sum[k & 3] += pr;
             s[k] = pr * exp2i(min(max((int)ev[k] - E, -60), 0));
           }
-          l += sum;
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -611,7 +667,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  if (warp == S::W_MMA) tmem_dealloc(tmem, 512);
+  if (warp == S::W_MMA) tmem_dealloc(*tmem_slot, 512);
 }
 
 template <int D, int BITS, int MODE>
