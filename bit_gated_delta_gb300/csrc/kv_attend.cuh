@@ -156,7 +156,6 @@ struct AttendArgs {
   const uint32_t *mask;
   float scale_log2;     // softmax scale * log2(e)
   int row_blocks;       // items of one (sequence, KV head)
-  int min_share;        // fewest tiles a block takes (tensor-memory kernel)
 };
 
 // One stretch of an item on the line of tiles.
@@ -291,89 +290,112 @@ __device__ __forceinline__ bool last_part(int32_t *count, int n) {
 }
 
 // Join the partial results of one item (rows of D values, then maximum and sum of each row) that blocks first..last left, and write
-// its outputs. Threads 0..THREADS-1 take part: ROWS * D/8 of them (or all) a group, a group every GROUPS-th part; the groups' results
-// meet in `area` (GROUPS - 1 times ROWS * D/8 * 10 floats; `sync` is the threads' barrier).
+// its outputs. All THREADS threads of the block take part. A thread takes pieces of eight values, two at a time and four parts of
+// each, so that their loads go out together; where there are fewer pieces than threads, groups of threads share the parts and
+// meet in `area` (JoinShape::AREA bytes).
 template <int D, int ROWS, int THREADS>
 struct JoinShape {
   static constexpr int PIECES = ROWS * D / 8;
   static constexpr int GROUPS = THREADS > PIECES ? THREADS / PIECES : 1;
   static constexpr size_t AREA = (size_t)(GROUPS - 1) * PIECES * 10 * 4;
 };
-template <int D, int ROWS, int THREADS, bool F32, typename Sync>
-__device__ void join_parts(const AttendArgs &p, const float *parts, long stride, int first, int last, int b, int h, int row0, int fresh,
-                           int thread, float *area, Sync sync) {
-  using J = JoinShape<D, ROWS, THREADS>;
-  constexpr int CH = D / 8;
-  const int G = p.c.group, rows = p.c.n_tokens * G, grp = thread / J::PIECES;
-  float M = -INFINITY, y[8] = {0, 0, 0, 0, 0, 0, 0, 0}, L = 0.0f;
-  auto add = [&](float m, float l, const float4 &u, const float4 &v) {
-    const float f = m == -INFINITY ? 0.0f : exp2_approx(m - M);
-    L += f * l;
-    y[0] += f * u.x, y[1] += f * u.y, y[2] += f * u.z, y[3] += f * u.w;
-    y[4] += f * v.x, y[5] += f * v.y, y[6] += f * v.z, y[7] += f * v.w;
-  };
-  auto raise = [&](float top) {
+struct JoinSum {
+  float M, L, y[8];
+  __device__ __forceinline__ void clear() {
+    M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = 0.0f;
+  }
+  __device__ __forceinline__ void raise(float top) {
     const float keep = M == -INFINITY ? 0.0f : exp2_approx(M - top);
     M = top;
     L *= keep;
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] *= keep;
-  };
-  auto write = [&](int row, int e8) {
-    const int rr = row0 + row, t = rr / G;
-    if (rr >= rows) return;
-    char *dst = p.o.p + (b * p.o.sb + (long)t * p.o.st + (long)(h * G + rr - t * G) * p.o.sh + e8) * (F32 ? 4 : 2);
-    store_out<F32>(dst, y, t < fresh && L > 0.0f ? 1.0f / L : 0.0f);
-  };
-  for (int x = J::GROUPS > 1 ? thread % J::PIECES : thread; x < J::PIECES; x += J::GROUPS > 1 ? J::PIECES : THREADS) {
-    const int row = x / CH, e8 = (x % CH) * 8;
-    M = -INFINITY, L = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = 0.0f;
-    const bool live = grp < J::GROUPS && row0 + row < rows;
-    for (int i0 = first + (J::GROUPS > 1 ? grp : 0); live && i0 <= last; i0 += 4 * J::GROUPS) {   // four at a time: their loads go out together
-      float2 e[4];
-      float4 u[4], v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = min(i0 + k * J::GROUPS, last);
-        const float *src = parts + (2 * i + (i == first)) * stride;
-        e[k] = __ldcg(reinterpret_cast<const float2 *>(src + ROWS * D + 2 * row));
-        u[k] = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8));
-        v[k] = __ldcg(reinterpret_cast<const float4 *>(src + row * D + e8 + 4));
-      }
-      float top = M;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i0 + k * J::GROUPS <= last) top = fmaxf(top, e[k].x);
-      raise(top);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i0 + k * J::GROUPS <= last) add(e[k].x, e[k].y, u[k], v[k]);
-    }
-    if (J::GROUPS == 1) write(row, e8);
   }
-  if (J::GROUPS > 1) {
-    const int x = thread % J::PIECES, row = x / CH, e8 = (x % CH) * 8;
-    if (grp > 0 && grp < J::GROUPS) {
-      float *dst = area + ((grp - 1) * J::PIECES + x) * 2;
-      dst[0] = M;
-      dst[1] = L;
-      float4 *o = reinterpret_cast<float4 *>(area + (J::GROUPS - 1) * J::PIECES * 2) + ((grp - 1) * J::PIECES + x) * 2;
-      o[0] = make_float4(y[0], y[1], y[2], y[3]);
-      o[1] = make_float4(y[4], y[5], y[6], y[7]);
+  __device__ __forceinline__ void add(float m, float l, const float4 &u, const float4 &v) {
+    const float f = m == -INFINITY ? 0.0f : exp2_approx(m - M);
+    L += f * l;
+    y[0] += f * u.x, y[1] += f * u.y, y[2] += f * u.z, y[3] += f * u.w;
+    y[4] += f * v.x, y[5] += f * v.y, y[6] += f * v.z, y[7] += f * v.w;
+  }
+};
+template <int D, int ROWS, int THREADS, bool F32>
+__device__ void join_parts(const AttendArgs &p, const float *parts, long stride, int first, int last, int b, int h, int row0, int fresh,
+                           float *area) {
+  using J = JoinShape<D, ROWS, THREADS>;
+  constexpr int CH = D / 8, U = J::GROUPS > 1 ? 1 : 2, P = 4;
+  const int G = p.c.group, rows = p.c.n_tokens * G, grp = J::GROUPS > 1 ? threadIdx.x / J::PIECES : 0;
+  JoinSum sum[U];
+  auto gather = [&](int x0, int step) {               // pieces x0, x0 + step: this group's parts
+    bool live[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      sum[q].clear();
+      live[q] = x0 + q * step < J::PIECES && row0 + (x0 + q * step) / CH < rows;
     }
-    sync();
+    for (int i0 = first + grp; i0 <= last; i0 += P * J::GROUPS) {
+      float2 e[U][P];
+      float4 u[U][P], v[U][P];
+#pragma unroll
+      for (int q = 0; q < U; ++q)
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const int i = i0 + k * J::GROUPS, x = x0 + q * step, row = x / CH;
+          const float *src = parts + (2 * i + (i == first)) * stride;
+          e[q][k] = make_float2(-INFINITY, 0.0f);
+          u[q][k] = v[q][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (i <= last && live[q]) {
+            e[q][k] = __ldcg(reinterpret_cast<const float2 *>(src + ROWS * D + 2 * row));
+            u[q][k] = __ldcg(reinterpret_cast<const float4 *>(src + x * 8));
+            v[q][k] = __ldcg(reinterpret_cast<const float4 *>(src + x * 8 + 4));
+          }
+        }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        float top = sum[q].M;
+#pragma unroll
+        for (int k = 0; k < P; ++k) top = fmaxf(top, e[q][k].x);
+        sum[q].raise(top);
+#pragma unroll
+        for (int k = 0; k < P; ++k) sum[q].add(e[q][k].x, e[q][k].y, u[q][k], v[q][k]);
+      }
+    }
+  };
+  auto write = [&](int x, JoinSum &s) {
+    const int rr = row0 + x / CH, t = rr / G;
+    if (x >= J::PIECES || rr >= rows) return;
+    char *dst = p.o.p + (b * p.o.sb + (long)t * p.o.st + (long)(h * G + rr - t * G) * p.o.sh + (x % CH) * 8) * (F32 ? 4 : 2);
+    store_out<F32>(dst, s.y, t < fresh && s.L > 0.0f ? 1.0f / s.L : 0.0f);
+  };
+  if (J::GROUPS == 1) {
+    for (int x = threadIdx.x; x < J::PIECES; x += U * THREADS) {
+      gather(x, THREADS);
+#pragma unroll
+      for (int q = 0; q < U; ++q) write(x + q * THREADS, sum[q]);
+    }
+  } else {
+    const int x = threadIdx.x % J::PIECES;
+    float2 *ml = reinterpret_cast<float2 *>(area);
+    float4 *ys = reinterpret_cast<float4 *>(area + (J::GROUPS - 1) * J::PIECES * 2);
+    if (grp < J::GROUPS) gather(x, 0);
+    if (grp > 0 && grp < J::GROUPS) {
+      const int at = (grp - 1) * J::PIECES + x;
+      ml[at] = make_float2(sum[0].M, sum[0].L);
+      ys[2 * at] = make_float4(sum[0].y[0], sum[0].y[1], sum[0].y[2], sum[0].y[3]);
+      ys[2 * at + 1] = make_float4(sum[0].y[4], sum[0].y[5], sum[0].y[6], sum[0].y[7]);
+    }
+    __syncthreads();
     if (grp == 0) {
       for (int q = 0; q < J::GROUPS - 1; ++q) {
-        const float *src = area + (q * J::PIECES + x) * 2;
-        const float4 *o = reinterpret_cast<const float4 *>(area + (J::GROUPS - 1) * J::PIECES * 2) + (q * J::PIECES + x) * 2;
-        raise(fmaxf(M, src[0]));
-        add(src[0], src[1], o[0], o[1]);
+        const int at = q * J::PIECES + x;
+        const float2 e = ml[at];
+        sum[0].raise(fmaxf(sum[0].M, e.x));
+        sum[0].add(e.x, e.y, ys[2 * at], ys[2 * at + 1]);
       }
-      write(row, e8);
+      write(x, sum[0]);
     }
-    sync();
+    __syncthreads();
   }
 }
 
@@ -986,8 +1008,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
         Segment it;
         int first, last;
         shared(k, it, first, last);
-        join_parts<D, ROWS, S::THREADS, F32>(p, c.part, part_floats(D, NT), first, last, it.b, it.h, it.rb * ROWS, seq[it.b].fresh, tid,
-                                             scratch, [] { __syncthreads(); });
+        join_parts<D, ROWS, S::THREADS, F32>(p, c.part, part_floats(D, NT), first, last, it.b, it.h, it.rb * ROWS, seq[it.b].fresh, scratch);
       }
   }
   if (dead) {                                         // a wait gave up: let the copies in flight land (bounded) before leaving

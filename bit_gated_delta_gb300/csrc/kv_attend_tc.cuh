@@ -25,6 +25,7 @@ namespace kv {
 enum { TC_SHARE = 0, TC_ALT = 1, TC_ONE = 2 };
 constexpr int KVT = 64;               // cached tokens a tile
 constexpr int TC_BLOCKS = 160;        // most blocks of a launch (one an SM)
+constexpr int TC_LEAST = 4, TC_WHOLE = 12;   // fewest tiles a block takes; items of up to so many on average are not cut
 
 template <int D, int BITS, int MODE>
 struct TcShape {
@@ -45,11 +46,12 @@ struct TcShape {
   static constexpr int OK = 0, OV = OK + KS * KB, ORAW = OV + VS * KB, OPAR = ORAW + RS * RAW;
   static constexpr int PAR = 2 * L::NG * KVT * 16;                      // scales and zero points, twice
   static constexpr int OEXP = OPAR + 2 * PAR;                           // exponents [8 tiles][k, v][64] int8
-  static constexpr int OML = OEXP + 8 * 2 * KVT;                        // m, l, exponent of group 1 (ALT)
+  static constexpr int OOWN = OEXP + 8 * 2 * KVT;                       // whether a tile's tokens have their own [8]
+  static constexpr int OML = OOWN + 16;                                 // m, l, exponent of group 1 (ALT)
   static constexpr int OBAR = OML + 128 * 12;
   static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 4 * NWG + 5;
-  static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flag, red[8]
-  static constexpr int OCUM = (OMISC + 64 + 15) / 16 * 16;
+  static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flags, red[16]
+  static constexpr int OCUM = (OMISC + 96 + 15) / 16 * 16;
   static constexpr size_t smem(int batch) { return OCUM + 32 * 4 + (size_t)(batch + 1) * 4 + (size_t)batch * sizeof(Seq); }
 };
 constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 128 + 2 (128 of 256 + 2 are fewer)
@@ -123,11 +125,12 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   int *raw_flags = reinterpret_cast<int *>(smem + S::OMISC);            // [RS]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_flags + 4);
   int *join_flag = raw_flags + 5;
-  float *red = reinterpret_cast<float *>(raw_flags + 8);                // [4]
+  float *red = reinterpret_cast<float *>(raw_flags + 8);                // [16]
   unsigned *wsum = reinterpret_cast<unsigned *>(smem + S::OCUM);
   unsigned *cum = wsum + 32;
   Seq *seq = reinterpret_cast<Seq *>(cum + c.batch + 1);
   int8_t *exps = reinterpret_cast<int8_t *>(smem + S::OEXP);
+  volatile uint8_t *own_exps = reinterpret_cast<uint8_t *>(smem + S::OOWN);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = c.group, T = c.n_tokens;
 
@@ -139,6 +142,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128), mbar_init(&o_full[i], 1);
       mbar_init(&q_ready[i], 128);
     }
+    join_flag[0] = 0;
     for (int i = 0; i < 2; ++i) mbar_init(&par_full[i], 2), mbar_init(&par_free[i], 4);
     mbar_init(drain, 1);
     mbar_fence_init();
@@ -154,7 +158,11 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   constexpr uint32_t tmem = 0;          // the whole of TMEM is this block's: its first column (a constant keeps addresses uniform)
 
   const unsigned total = cum[c.batch];
-  const unsigned share = max((total + gridDim.x - 1) / gridDim.x, (unsigned)p.min_share);
+  unsigned share = (total + gridDim.x - 1) / gridDim.x;
+  {
+    const unsigned mean = total / ((unsigned)c.batch * c.Hkv * p.row_blocks);
+    share = max(share, mean <= TC_WHOLE ? mean : (unsigned)TC_LEAST);
+  }
   const unsigned lo = blockIdx.x <= total / share ? blockIdx.x * share : total, hi = min(total, lo + share);
   auto at = [&](unsigned pos) { return segment_at<KVT>(seq, cum, c.batch, p.row_blocks, pos, hi); };
   // A role whose wait gives up goes on without waiting or touching the tensor cores, but keeps the barriers it shares, so that no
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         const char *st = smem + S::ORAW + rs * S::RAW + pw * L::BYTES;
         char *par = smem + S::OPAR + (n & 1) * S::PAR;
         const bool live = tile * KVT + t < tokens && ((raw_flags[rs] >> pw) & 1);
-        const bool own = (tile + 1) * KVT > len;                        // new tokens in the tile: an exponent a token
+        const bool edge = (tile + 1) * KVT > len;                       // new tokens in the tile, which not every row sees
         float s[2][NG], top[2];
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -319,14 +327,21 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             s[part][g] = live ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(st + (part ? L::VS : L::KS))[g * TILE + ps]) : 0.0f;
             top[part] = fmaxf(top[part], s[part][g]);
           }
-          const float all = warp_max(top[part]);
-          if (lane == 0) red[(n & 1) * 4 + part * 2 + pw] = all;
+          const float all = warp_max(top[part]), least = -warp_max(top[part] > 0.0f ? -top[part] : -FLT_MAX);
+          if (lane == 0) {
+            red[(n & 1) * 8 + part * 2 + pw] = all;
+            red[(n & 1) * 8 + 4 + part * 2 + pw] = least;
+          }
         }
         bar_sync(1, 64);
+        // one exponent for the tile keeps ten bits of every token whose scale is within 2^12 of the largest; where a new token (that some
+        // rows may not see) makes them spread further, each token gets its own
+        const float *rr = red + (n & 1) * 8;
+        const bool own = edge && (fmaxf(rr[0], rr[1]) > 4096.0f * fminf(rr[4], rr[5]) || fmaxf(rr[2], rr[3]) > 4096.0f * fminf(rr[6], rr[7]));
+        if (pw == 0 && lane == 0) own_exps[n & 7] = own;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
-          const float *r = red + (n & 1) * 4 + part * 2;
-          const float ref = own ? top[part] : fmaxf(r[0], r[1]);
+          const float ref = own ? top[part] : fmaxf(rr[part * 2], rr[part * 2 + 1]);
           const int e = ref > 0.0f ? (int)(__float_as_uint(ref) >> 23) - 127 : 0;
           exps[((n & 7) * 2 + part) * KVT + t] = (int8_t)e;
           const float down = exp2i(-e < 127 ? -e : 127);                // (e >= -126)
@@ -455,30 +470,42 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       if (good) {
         const char *src = p.q.p + (sg.b * p.q.sb + (long)t * p.q.st + (long)hh * p.q.sh) * 2;
         uint32_t top = 0;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = in ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
-          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+        constexpr int HALF = D > 128 ? 2 : 1;             // (at D = 256 in two passes over the row: registers)
+        uint4 x[D / 8 / HALF];
+        auto load = [&](int h) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max((v[e] << 16) & 0x7FFF0000u, v[e] & 0x7FFF0000u));
+          for (int i = 0; i < D / 8 / HALF; ++i)
+            x[i] = in ? reinterpret_cast<const uint4 *>(src)[h * (D / 8 / HALF) + i] : make_uint4(0, 0, 0, 0);
+        };
+        for (int h = 0; h < HALF; ++h) {
+          load(h);
+#pragma unroll
+          for (int i = 0; i < D / 8 / HALF; ++i) {
+            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max((v[e] << 16) & 0x7FFF0000u, v[e] & 0x7FFF0000u));
+          }
         }
         int e = (int)(top >> 23) - 127;
         e = max(min(e, 126), -126);
         crow = sl2 * exp2i(e);
         const float down = exp2i(-e);
         if (MODE != TC_ALT || w == 0) {
+          for (int h = 0; h < HALF; ++h) {
+            if (HALF > 1) load(h);
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t r[16];
+            for (int i = 0; i < D / 32 / HALF; ++i) {
+              uint32_t r[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 x = in ? reinterpret_cast<const uint4 *>(src)[4 * i + k] : make_uint4(0, 0, 0, 0);
-              const uint32_t v[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+              for (int k = 0; k < 4; ++k) {
+                const uint4 y = x[4 * i + k];
+                const uint32_t v[4] = {y.x ^ flip, y.y ^ flip, y.z ^ flip, y.w ^ flip};
 #pragma unroll
-              for (int d = 0; d < 4; ++d)
-                r[4 * k + d] = h2pack(__uint_as_float(v[d] << 16) * down, __uint_as_float(v[d] & 0xFFFF0000u) * down);
+                for (int d = 0; d < 4; ++d)
+                  r[4 * k + d] = h2pack(__uint_as_float(v[d] << 16) * down, __uint_as_float(v[d] & 0xFFFF0000u) * down);
+              }
+              tmem_st16(tmem + lanes + S::CQ + (MODE == TC_SHARE ? w * (D / 2) : 0) + 16 * (h * (D / 32 / HALF) + i), r);
             }
-            tmem_st16(tmem + lanes + S::CQ + (MODE == TC_SHARE ? w * (D / 2) : 0) + 16 * i, r);
           }
           tmem_wait_st();
         }
@@ -490,6 +517,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       bool first = true;
       for (int i = MODE == TC_ALT ? w : 0; i < tiles && good; i += MODE == TC_ALT ? 2 : 1) {
         const int tl = ntile + i, tok0 = (sg.tile + i) * KVT;
+        const bool edge = tok0 + KVT > len;               // new tokens or the end in the tile
+        const uint64_t vis = edge && in ? visible(p, sg.b, t, tok0 - len, nn) : 0ull;
         good = mbar_wait(&s_full[w], ns & 1, LIMIT);
         good = __all_sync(0xffffffffu, good);
         if (!good) break;
@@ -507,24 +536,29 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             for (int e = 0; e < 16; ++e) s[16 * k + e] = __uint_as_float(r[k][e]);
         }
         const int8_t *ek = exps + ((tl & 7) * 2) * KVT, *ev = ek + KVT;
-        const bool edge = tok0 + KVT > len;
-        float mx = -INFINITY, cs = crow;
+        const bool apart = edge && own_exps[tl & 7];      // each token by its own exponent
+        float mx, cs = crow;
         int Et = -126;
-        if (!edge) {
+        if (!apart) {
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k) s[k] = (uint32_t)(k < 32 ? vis : vis >> 32) & (1u << (k & 31)) ? s[k] : -INFINITY;
+          }
           float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int k = 4; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
           mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          cs = crow * exp2i(ek[0]);
+          cs = fmaxf(crow * exp2i(ek[0]), FLT_MIN);       // (not 0: a masked score is -inf)
           mx *= cs;
           Et = ev[0];
         } else {
-          const uint64_t vis = in ? visible(p, sg.b, t, tok0 - len, nn) : 0ull;
+          mx = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 64; ++k) {
             const bool see = (vis >> k) & 1;
-            s[k] = see ? s[k] * (crow * exp2i(ek[k])) : -INFINITY;
-            mx = fmaxf(mx, s[k]);
+            const float x = see ? s[k] * (crow * exp2i(ek[k])) : -INFINITY;
+            s[k] = x;
+            mx = fmaxf(mx, x);
             if (see) Et = max(Et, (int)ev[k]);
           }
         }
@@ -553,7 +587,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         }
         const float mu = m == -INFINITY ? 0.0f : m;
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (!edge) {
+        if (!apart) {
           const int dE = max(Et - E, -60);
           const float add = 10.0f + (float)dE - mu;
 #pragma unroll
@@ -591,9 +625,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         fence_after_sync();
       }
       const bool whole = sg.tile == 0 && sg.end == sg.tiles;
-      const unsigned item_lo = pos - sg.end;
-      const int fb = (int)(item_lo / share), lb = (int)((item_lo + sg.tiles - 1) / share);
-      float *part = c.part + (long)(2 * blockIdx.x + (blockIdx.x == fb ? 1 : 0)) * TC_PART_FLOATS;
+      float *part = c.part + (long)(2 * blockIdx.x + (sg.tile == 0 ? 1 : 0)) * TC_PART_FLOATS;   // (a shared item that starts here is the last)
       const int prow = (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
       float f0 = 1.0f, f1 = 0.0f, M = m, Ls = l;
       int E0 = E, E1 = 0;
@@ -649,15 +681,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           part[S::ROWS * D + 2 * prow + 1] = Ls;
         }
       }
-      if (!whole) {
-        bar_sync(2, NWG * 128);
-        if (tid == 0) *join_flag = last_part(&c.count[fb], lb - fb + 1);
-        bar_sync(2, NWG * 128);
-        if (*join_flag) {
-          join_parts<D, S::ROWS, NWG * 128, false>(p, c.part, TC_PART_FLOATS, fb, lb, sg.b, sg.h, sg.rb * S::ROWS, nn, tid, nullptr,
-                                                   [] { bar_sync(2, NWG * 128); });
-        }
-      }
+      if (!whole && tid == 0) join_flag[0] |= sg.tile ? 1 : 2;          // began in an earlier block, or goes on in a later one
       fence_before_sync();
       if (NWG == 2) bar_sync(2, 256);                     // both groups have read what the next segment overwrites
       ntile += tiles;
@@ -668,6 +692,35 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   __syncthreads();
   fence_after_sync();
   if (warp == S::W_MMA) tmem_dealloc(*tmem_slot, 512);
+  // ---- items that several blocks share: the last to arrive joins the parts in block order
+  const int pseg = join_flag[0];
+  if (pseg) {
+    auto shared = [&](int k, Segment &it, int &first, int &last) {        // the item of the block's first tile, or of its last
+      const unsigned pos = k ? hi - 1 : lo;
+      it = at(pos);
+      first = (int)((pos - it.tile) / share);
+      last = (int)((pos - it.tile + it.tiles - 1) / share);
+    };
+    if (tid < 2) {
+      bool joins = false;
+      if ((pseg >> tid) & 1) {
+        Segment it;
+        int first, last;
+        shared(tid, it, first, last);
+        joins = last_part(&c.count[first], last - first + 1);
+      }
+      join_flag[1 + tid] = joins;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k)
+      if (join_flag[1 + k]) {
+        Segment it;
+        int first, last;
+        shared(k, it, first, last);
+        join_parts<D, S::ROWS, S::THREADS, false>(p, c.part, TC_PART_FLOATS, first, last, it.b, it.h, it.rb * S::ROWS, seq[it.b].fresh, nullptr);
+      }
+  }
 }
 
 template <int D, int BITS, int MODE>
@@ -679,10 +732,9 @@ cudaError_t launch_attend_tc(AttendArgs a, cudaStream_t s) {
   cudaError_t e = smem_opt_in<K>(227 * 1024);
   if (e != cudaSuccess) return e;
   a.row_blocks = (a.c.n_tokens * a.c.group + S::ROWS - 1) / S::ROWS;
-  a.min_share = 4;
   return by_batches(a, KVT, [&](const AttendArgs &part, long line) {
     long grid = std::min((long)device_sm_count(), (long)TC_BLOCKS);
-    grid = std::min(grid, (line + a.min_share - 1) / a.min_share);
+    grid = std::min(grid, line);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)grid), dim3(S::THREADS), smem, s, attr);
     return cudaLaunchKernelEx(&cfg, K, part);
