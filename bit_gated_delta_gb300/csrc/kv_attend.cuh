@@ -237,6 +237,52 @@ __device__ __forceinline__ Segment segment_at(const Seq *seq, const unsigned *cu
   s.end = (int)min((unsigned)s.tiles, s.tile + (hi - p));
   return s;
 }
+// Where the line is cut: at every `share` tiles, moved to the next item boundary where one lies within `slack` tiles, since an item
+// that two blocks share costs each of them the writing of a part and one of them the joining.
+struct Cuts {
+  unsigned share, slack, total;
+};
+template <int TOK>
+__device__ __forceinline__ unsigned cut_at(const Seq *seq, const unsigned *cum, int batch, const Cuts &c, unsigned i) {
+  const unsigned p = i * c.share;
+  if (p >= c.total) return c.total;
+  if (c.slack == 0) return p;
+  int lo = 0, up = batch;
+  while (up - lo > 1) {
+    const int mid = (lo + up) >> 1;
+    if (cum[mid] <= p) lo = mid;
+    else up = mid;
+  }
+  const unsigned tiles = max((seq[lo].tokens + TOK - 1) / TOK, 1), off = (p - cum[lo]) % tiles, rest = tiles - off;
+  if (off <= rest) return off <= c.slack ? p - off : p;
+  return rest <= c.slack ? p + rest : p;
+}
+// The block whose stretch holds line position pos.
+template <int TOK>
+__device__ __forceinline__ unsigned block_of(const Seq *seq, const unsigned *cum, int batch, const Cuts &c, unsigned pos) {
+  unsigned i = pos / c.share;
+  const unsigned off = pos - i * c.share;
+  if (off >= c.slack && c.share - off > c.slack) return i;             // no cut this near
+  while (cut_at<TOK>(seq, cum, batch, c, i + 1) <= pos) ++i;
+  while (cut_at<TOK>(seq, cum, batch, c, i) > pos) --i;
+  return i;
+}
+// The cuts of a launch and this block's two, by one warp's first lanes; every warp may call it.
+template <int TOK>
+__device__ __forceinline__ Cuts make_cuts(const Seq *seq, const unsigned *cum, int batch, unsigned items, unsigned least, unsigned whole,
+                                          unsigned slack, unsigned &lo, unsigned &hi) {
+  Cuts c;
+  c.total = cum[batch];
+  c.slack = slack;
+  const unsigned mean = c.total / items;
+  c.share = max((c.total + gridDim.x - 1) / gridDim.x, mean <= whole ? mean : least);
+  const unsigned i = blockIdx.x + (threadIdx.x & 31 ? 1 : 0);
+  const unsigned at = i > c.total / c.share ? c.total : cut_at<TOK>(seq, cum, batch, c, i);
+  lo = __shfl_sync(0xffffffffu, at, 0);
+  hi = __shfl_sync(0xffffffffu, at, 1);
+  return c;
+}
+
 // The stretches of a block from line position lo on, SEGS at most, into shared memory by one warp (a lane each): the one at lo, then
 // whole items until hi. Returns how many; segs[n].tile of the one after them is the line position where they end.
 constexpr int SEGS = 32;
@@ -452,14 +498,9 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 
   // equal shares, but none finer than a tile for every warp, or than a whole average item of up to three: joining one costs about as
   // much as three rounds of tiles
-  const unsigned total = cum[c.batch];
-  unsigned share = (total + gridDim.x - 1) / gridDim.x;
-  {
-    const unsigned mean = total / ((unsigned)c.batch * c.Hkv * p.row_blocks);
-    share = max(share, mean <= 3u * NW ? mean : NW);
-  }
-  const unsigned lo = blockIdx.x * share, hi = min(total, lo + share);
-  if (blockIdx.x > total / share || lo >= total) return;
+  unsigned lo, hi;
+  const Cuts cuts = make_cuts<TILE>(seq, cum, c.batch, (unsigned)c.batch * c.Hkv * p.row_blocks, NW, 3 * NW, 0, lo, hi);
+  if (lo >= hi) return;
   auto segment = [&](unsigned at) { return segment_at<TILE>(seq, cum, c.batch, p.row_blocks, at, hi); };
 
   // ---- queries of a segment, copied one segment ahead
@@ -988,8 +1029,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
     auto shared = [&](int k, Segment &it, int &first, int &last) {
       const unsigned at = k ? hi - 1 : lo;
       it = segment(at);
-      first = (int)((at - it.tile) / share);
-      last = (int)((at - it.tile + it.tiles - 1) / share);
+      first = (int)block_of<TILE>(seq, cum, c.batch, cuts, at - it.tile);
+      last = (int)block_of<TILE>(seq, cum, c.batch, cuts, at - it.tile + it.tiles - 1);
     };
     if (tid < 2) {
       bool joins = false;

@@ -6,11 +6,11 @@
 //
 // fp16 carries 11 bits, against 8 of bf16, so that held values, queries and weights are rounded to 2^-12; its range is kept by
 // exact powers of two: a row of Q is scaled by its largest element, K and V of a tile by its largest group scale (E_k, E_v; in
-// tiles with new tokens, where rows may see different tokens, each token by its own), weights are taken relative to 2^10 of the
+// tiles with new tokens, where rows may see different tokens, each token by its own), weights are 2^8 at the row's
 // running maximum. The powers return with the scores, and in O as a running exponent per row raised like the maximum.
 //
-// Roles (warps): softmax (four a group; thread = row = TMEM lane), four that dequantize, two that prepare a tile's scales for them, one
-// that copies tiles in, one that issues the products. Two softmax groups take turns, so that the tensor cores work on one group's products while the other group forms
+// Roles (warps): softmax (four a group; thread = row = TMEM lane), four that dequantize, two that copy tiles in and prepare their scales,
+// one a softmax group that issues its products (issued by the softmax warps themselves, a prompt chunk took 206 us, not 172). Two softmax groups take turns, so that the tensor cores work on one group's products while the other group forms
 // its weights: the groups are two row blocks (SHARE), or even and odd tiles of one block (ALT, joined at the end through TMEM).
 //   bound: per 64 tokens and row block of 128 at D = 128, 512 cycles of tensor work; 64 scores a thread (4.5 instructions each, two
 //   groups a scheduler) and a quarter of 16,384 codes a scheduler (about two instructions each) come to about the same.
@@ -25,7 +25,9 @@ namespace kv {
 enum { TC_SHARE = 0, TC_ALT = 1, TC_ONE = 2 };
 constexpr int KVT = 64;               // cached tokens a tile
 constexpr int TC_BLOCKS = 160;        // most blocks of a launch (one an SM)
-constexpr int TC_LEAST = 4, TC_WHOLE = 12;   // fewest tiles a block takes; items of up to so many on average are not cut
+// Tiles: the fewest a block takes; items of up to so many on average are not cut; cuts move to an item boundary this near. (A shared
+// item costs about 20 us, its parts written and joined; a tile 0.7 to 1.3 us.)
+constexpr int TC_LEAST = 4, TC_WHOLE = 12, TC_SLACK = 8;
 
 template <int D, int BITS, int MODE>
 struct TcShape {
@@ -36,7 +38,7 @@ struct TcShape {
   static constexpr int KS = 2, VS = 2;                                  // dequantized stages
   static constexpr int RS = D == 256 ? (BITS == 4 ? 3 : 2) : 4;         // raw stages
   static constexpr int WARPS = 4 * NWG + 8, THREADS = WARPS * 32;
-  static constexpr int W_DEQ = 4 * NWG, W_PAR = W_DEQ + 4, W_LOAD = W_PAR + 2, W_MMA = W_LOAD + 1;
+  static constexpr int W_DEQ = 4 * NWG, W_PAR = W_DEQ + 4, W_MMA = W_PAR + 2;
   // TMEM columns
   static constexpr int CQ = 0, CO = NRB * D / 2, CS = CO + NWG * D;
   static_assert(CS + NWG * KVT <= 512, "TMEM");
@@ -58,6 +60,23 @@ constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 1
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
   return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// two fp32 operations at once
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -116,6 +135,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   using namespace umma;
   constexpr int NG = L::NG, NWG = S::NWG, KS = S::KS, VS = S::VS, RS = S::RS;
   constexpr uint64_t LIMIT = WAIT_LIMIT_NS;
+  constexpr float OFFSET = 8.0f;        // weights are 2^OFFSET at the row's reference: fp16 then reaches 2^-32 below it
   extern __shared__ __align__(128) char smem[];
   const KvDev &c = p.c;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::OBAR);
@@ -131,20 +151,17 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   Seq *seq = reinterpret_cast<Seq *>(cum + c.batch + 1);
   int8_t *exps = reinterpret_cast<int8_t *>(smem + S::OEXP);
   volatile uint8_t *own_exps = reinterpret_cast<uint8_t *>(smem + S::OOWN);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be uniform)
   const int G = c.group, T = c.n_tokens;
 
   if (tid == 0) {
     for (int i = 0; i < RS; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], 4);
-    for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], 4), mbar_init(&k_free[i], 1);
-    for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 4), mbar_init(&v_free[i], 1);
-    for (int i = 0; i < NWG; ++i) {
-      mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128), mbar_init(&o_full[i], 1);
-      mbar_init(&q_ready[i], 128);
-    }
+    for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], 4), mbar_init(&k_free[i], S::NRB);
+    for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 4), mbar_init(&v_free[i], S::NRB);
+    for (int i = 0; i < NWG; ++i) mbar_init(&s_full[i], 1), mbar_init(&o_full[i], 1), mbar_init(&p_ready[i], 4), mbar_init(&q_ready[i], 4);
     join_flag[0] = 0;
     for (int i = 0; i < 2; ++i) mbar_init(&par_full[i], 2), mbar_init(&par_free[i], 4);
-    mbar_init(drain, 1);
+    mbar_init(drain, NWG);
     mbar_fence_init();
   }
   if (warp == S::W_MMA) {
@@ -157,54 +174,14 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   fence_after_sync();
   constexpr uint32_t tmem = 0;          // the whole of TMEM is this block's: its first column (a constant keeps addresses uniform)
 
-  const unsigned total = cum[c.batch];
-  unsigned share = (total + gridDim.x - 1) / gridDim.x;
-  {
-    const unsigned mean = total / ((unsigned)c.batch * c.Hkv * p.row_blocks);
-    share = max(share, mean <= TC_WHOLE ? mean : (unsigned)TC_LEAST);
-  }
-  const unsigned lo = blockIdx.x <= total / share ? blockIdx.x * share : total, hi = min(total, lo + share);
+  unsigned lo, hi;
+  const Cuts cuts = make_cuts<KVT>(seq, cum, c.batch, (unsigned)c.batch * c.Hkv * p.row_blocks, TC_LEAST, TC_WHOLE, TC_SLACK, lo, hi);
   auto at = [&](unsigned pos) { return segment_at<KVT>(seq, cum, c.batch, p.row_blocks, pos, hi); };
   // A role whose wait gives up goes on without waiting or touching the tensor cores, but keeps the barriers it shares, so that no
   // other warp is left at one; the others' waits then run out too.
   auto gave_up = [&]() { atomicOr(c.status, PACE_KV_TIMEOUT); };
 
-  if (warp == S::W_LOAD) {
-    // ---------------------------------------------------------------- copies: raw tiles of 2 x 32 tokens
-    const int tpp = c.page / TILE;
-    int stage = 0, n = 0;
-    bool good = true;
-    for (unsigned pos = lo; pos < hi && good;) {
-      const Segment sg = at(pos);
-      pos += sg.end - sg.tile;
-      const int tokens = seq[sg.b].tokens;
-      const int last = 2 * sg.end;
-      for (int s0 = 2 * sg.tile; s0 < last && good; s0 += 32) {         // 32 storage tiles, one a lane
-        const int mytile = (s0 + lane) < last && (s0 + lane) * TILE < tokens ? tile_index(c, sg.b, sg.h, s0 + lane, tpp) : -2;
-        if (mytile == -1) atomicOr(c.status, PACE_KV_BAD_PAGE);
-        const int kn = min(32, last - s0);
-        for (int k = 0; k < kn; k += 2) {
-          const int pa = __shfl_sync(0xffffffffu, mytile, k), pb = __shfl_sync(0xffffffffu, mytile, k + 1);
-          if (n >= RS) good = __all_sync(0xffffffffu, mbar_wait(&raw_free[stage], (n / RS - 1) & 1, LIMIT));
-          if (!good) break;
-          if (lane == 0) {
-            raw_flags[stage] = (pa >= 0 ? 1 : 0) | (pb >= 0 ? 2 : 0);
-            const uint32_t bytes = ((pa >= 0) + (pb >= 0)) * L::BYTES;
-            if (bytes) mbar_arrive_expect_tx(&raw_full[stage], bytes);
-            else mbar_arrive(&raw_full[stage]);
-            char *dst = smem + S::ORAW + stage * S::RAW;
-            if (pa >= 0) bulk_g2s(dst, c.pool + (long)pa * L::BYTES, L::BYTES, &raw_full[stage]);
-            if (pb >= 0) bulk_g2s(dst + L::BYTES, c.pool + (long)pb * L::BYTES, L::BYTES, &raw_full[stage]);
-          }
-          ++n;
-          stage = stage + 1 == RS ? 0 : stage + 1;
-        }
-      }
-    }
-    if (!good && lane == 0) gave_up();
-    // copies still in flight land before the block leaves (at most RS of them)
-    for (int i = max(0, n - RS); i < n; ++i) mbar_wait(&raw_full[i % RS], (i / RS) & 1, LIMIT);
-  } else if (warp >= S::W_DEQ && warp < S::W_PAR) {
+  if (warp >= S::W_DEQ && warp < S::W_PAR) {
     // ---------------------------------------------------------------- dequantize
     const int dw = warp - S::W_DEQ;
     int n = 0;
@@ -214,11 +191,9 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       pos += sg.end - sg.tile;
       for (int tile = sg.tile; tile < sg.end; ++tile, ++n) {
         const int rs = n % RS;
-        good = good && mbar_wait(&raw_full[rs], (n / RS) & 1, LIMIT);
-        good = __all_sync(0xffffffffu, good);
         const char *raw = smem + S::ORAW + rs * S::RAW;
         char *par = smem + S::OPAR + (n & 1) * S::PAR;
-        good = good && mbar_wait(&par_full[n & 1], (n >> 1) & 1, LIMIT);
+        good = good && mbar_wait(&raw_full[rs], (n / RS) & 1, LIMIT) && mbar_wait(&par_full[n & 1], (n >> 1) & 1, LIMIT);
         good = __all_sync(0xffffffffu, good);
         if (!good) continue;
         // codes: warp = 16 tokens; eight lanes write eight tokens' pieces of one 128-byte core
@@ -228,30 +203,41 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         };
         {
           const int ks = n % KS;
-          if (n >= KS) good = good && mbar_wait(&k_free[ks], (n / KS - 1) & 1, LIMIT);
-          good = __all_sync(0xffffffffu, good);
-          if (!good) continue;
           char *dst = smem + S::OK + ks * S::KB;
           constexpr int CHUNKS = BITS == 8 ? D / 16 : D == 64 ? 4 : D / 32;
+          uint4 word[2][CHUNKS / 4];                        // (read before the wait)
 #pragma unroll
           for (int o = 0; o < 2; ++o)
 #pragma unroll
             for (int q = 0; q < CHUNKS; q += 4) {
-              const int t = dw * 16 + o * 8 + (lane & 7), ch = q + (lane >> 3), tt = t & 31;
-              const char *src = raw + (t >> 5) * L::BYTES + L::kchunk(tt, ch);
+              const int t = dw * 16 + o * 8 + (lane & 7), ch = q + (lane >> 3);
+              const char *src = raw + (t >> 5) * L::BYTES + L::kchunk(t & 31, ch);
+              if (BITS == 4 && D == 64) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                word[o][q / 4] = make_uint4(x.x, x.y, 0, 0);
+              } else {
+                word[o][q / 4] = *reinterpret_cast<const uint4 *>(src);
+              }
+            }
+          if (n >= KS) good = good && mbar_wait(&k_free[ks], (n / KS - 1) & 1, LIMIT);
+          good = __all_sync(0xffffffffu, good);
+          if (!good) continue;
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int q = 0; q < CHUNKS; q += 4) {
+              const int t = dw * 16 + o * 8 + (lane & 7), ch = q + (lane >> 3);
+              const uint4 w = word[o][q / 4];
               if (BITS == 8) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(src);
                 const int g = ch >> 2, a = 8 * g + 2 * (ch & 3);
                 const uint32_t s = param(0, g, t).x;
                 put(dst, t, a, dequant8(w.x, w.y, s));
                 put(dst, t, a + 1, dequant8(w.z, w.w, s));
               } else if (D == 64) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(src);
                 const uint4 pr = param(0, 0, t);
                 put(dst, t, 2 * ch, dequant4(w.x, pr));
                 put(dst, t, 2 * ch + 1, dequant4(w.y, pr));
               } else {
-                const uint4 w = *reinterpret_cast<const uint4 *>(src);
                 const int g = 2 * (ch >> 2), a = 8 * g + 2 * (ch & 3);
                 const uint4 p0 = param(0, g, t), p1 = param(0, NG > 1 ? g + 1 : g, t);
                 put(dst, t, a, dequant4(w.x, p0));
@@ -266,24 +252,32 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         }
         {
           const int vs = n % VS;
-          if (n >= VS) good = good && mbar_wait(&v_free[vs], (n / VS - 1) & 1, LIMIT);
-          good = __all_sync(0xffffffffu, good);
-          if (!good) continue;
           char *dst = smem + S::OV + vs * S::KB;
           constexpr int UNITS = BITS == 8 ? D / 8 : D == 64 ? 8 : D / 16;
+          uint2 word[2][UNITS / 4];
 #pragma unroll
           for (int o = 0; o < 2; ++o)
 #pragma unroll
             for (int q = 0; q < UNITS; q += 4) {
-              const int t = dw * 16 + o * 8 + (lane & 7), u = q + (lane >> 3), tt = t & 31;
-              const char *src = raw + (t >> 5) * L::BYTES + L::vunit(tt, u);
+              const int t = dw * 16 + o * 8 + (lane & 7), u = q + (lane >> 3);
+              const char *src = raw + (t >> 5) * L::BYTES + L::vunit(t & 31, u);
+              if (BITS == 4 && D == 64) word[o][q / 4] = make_uint2(*reinterpret_cast<const uint32_t *>(src), 0);
+              else word[o][q / 4] = *reinterpret_cast<const uint2 *>(src);
+            }
+          if (n >= VS) good = good && mbar_wait(&v_free[vs], (n / VS - 1) & 1, LIMIT);
+          good = __all_sync(0xffffffffu, good);
+          if (!good) continue;
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int q = 0; q < UNITS; q += 4) {
+              const int t = dw * 16 + o * 8 + (lane & 7), u = q + (lane >> 3);
+              const uint2 w = word[o][q / 4];
               if (BITS == 8) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(src);
                 put(dst, t, u, dequant8(w.x, w.y, param(1, u >> 3, t).x));
               } else if (D == 64) {
-                put(dst, t, u, dequant4(*reinterpret_cast<const uint32_t *>(src), param(1, 0, t)));
+                put(dst, t, u, dequant4(w.x, param(1, 0, t)));
               } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(src);
                 const int g = 2 * (u >> 3), a = 8 * g + (u & 7);
                 put(dst, t, a, dequant4(w.x, param(1, g, t)));
                 put(dst, t, a + 8, dequant4(w.y, param(1, NG > 1 ? g + 1 : g, t)));
@@ -300,11 +294,49 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       }
     }
     if (!good && lane == 0) gave_up();
-  } else if (warp >= S::W_PAR && warp < S::W_LOAD) {
-    // ---------------------------------------------------------------- a tile's scales and exponents: lane = token
+  } else if (warp >= S::W_PAR && warp < S::W_MMA) {
+    // ---------------------------------------------------------------- copies of tiles; their scales and exponents: lane = token
     const int pw = warp - S::W_PAR, t = pw * 32 + lane, ps = L::pos(lane), vp = L::vpos(lane);
     int n = 0;
     bool good = true;
+    // the copying side, RS - 1 tiles ahead (first of the two warps): segment, storage tiles [at, end) of it, and the pool index of the
+    // 32 from `base` on, one a lane
+    const int tpp = c.page / TILE;
+    unsigned lpos = lo;
+    Segment ls{0, 0, 0, 0, 0, 0};
+    int lat = 0, lend = 0, lbase = 0, mytile = -2, copied = 0;
+    auto copy_next = [&]() {
+      if (lat >= lend) {
+        if (lpos >= hi) return;
+        ls = at(lpos);
+        lpos += ls.end - ls.tile;
+        lat = 2 * ls.tile;
+        lend = 2 * ls.end;
+        lbase = lat - 32;
+      }
+      if (lat - lbase >= 32) {
+        lbase = lat;
+        mytile = lat + lane < lend && (lat + lane) * TILE < seq[ls.b].tokens ? tile_index(c, ls.b, ls.h, lat + lane, tpp) : -2;
+        if (mytile == -1) atomicOr(c.status, PACE_KV_BAD_PAGE);
+      }
+      const int pa = __shfl_sync(0xffffffffu, mytile, lat - lbase), pb = __shfl_sync(0xffffffffu, mytile, lat - lbase + 1);
+      const int stage = copied % RS;
+      if (copied >= RS) good = __all_sync(0xffffffffu, good && mbar_wait(&raw_free[stage], (copied / RS - 1) & 1, LIMIT));
+      if (!good) return;
+      if (lane == 0) {
+        raw_flags[stage] = (pa >= 0 ? 1 : 0) | (pb >= 0 ? 2 : 0);
+        const uint32_t bytes = ((pa >= 0) + (pb >= 0)) * L::BYTES;
+        if (bytes) mbar_arrive_expect_tx(&raw_full[stage], bytes);
+        else mbar_arrive(&raw_full[stage]);
+        char *dst = smem + S::ORAW + stage * S::RAW;
+        if (pa >= 0) bulk_g2s(dst, c.pool + (long)pa * L::BYTES, L::BYTES, &raw_full[stage]);
+        if (pb >= 0) bulk_g2s(dst + L::BYTES, c.pool + (long)pb * L::BYTES, L::BYTES, &raw_full[stage]);
+      }
+      ++copied;
+      lat += 2;
+    };
+    if (pw == 0)
+      for (int i = 0; i < RS - 1; ++i) copy_next();
     for (unsigned pos = lo; pos < hi;) {
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
@@ -359,87 +391,62 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         }
         __syncwarp();
         if (lane == 0 && good) mbar_arrive(&par_full[n & 1]);
+        if (pw == 0) copy_next();
       }
     }
     if (!good && lane == 0) gave_up();
-  } else if (warp == S::W_MMA) {
-    // ---------------------------------------------------------------- products
-    // The warp runs as one, so that descriptors and addresses stay in uniform registers; one lane issues.
+    if (pw == 0)                                          // copies still in flight land before the block leaves
+      for (int i = max(0, copied - RS); i < copied; ++i) mbar_wait(&raw_full[i % RS], (i / RS) & 1, LIMIT);
+  } else if (warp >= S::W_MMA && warp < S::W_MMA + NWG) {
+    // ---------------------------------------------------------------- a group's products. The warp runs as one, so that descriptors and
+    // addresses stay in uniform registers; one lane issues. Products run in the order of issue: a score tile may overwrite weights
+    // whose product was issued before.
+    const int w = warp - S::W_MMA;
+    constexpr int STEP = MODE == TC_ALT ? 2 : 1;
+    const int i0 = MODE == TC_ALT ? w : 0;
     bool good = true;
     const bool leader = elect_one();
-    const uint32_t sb = smem_u32(smem);
-    int ntile = 0;                                        // tiles of the segments before
-    int nq = 0;
-    int np0 = 0, np1 = 0;                                 // tasks done per group
+    int ntile = 0, nq = 0, np = 0;                        // tiles of the segments before; segments and tiles of this group
     constexpr uint32_t ID_S = idesc_f16(128, KVT, 0), ID_O = idesc_f16(128, D, 1);
-    const uint64_t kdesc = smem_desc(sb + S::OK, 128, (D / 8) * 128), vdesc = smem_desc(sb + S::OV, (D / 8) * 128, 128);
-    auto ready = [&](uint64_t *b, int phase) {
-      // (all lanes together: a lane left behind could miss the phase it waits for)
+    const uint64_t kdesc = smem_desc(smem_u32(smem) + S::OK, 128, (D / 8) * 128);
+    const uint64_t vdesc = smem_desc(smem_u32(smem) + S::OV, (D / 8) * 128, 128);
+    const uint32_t cS = tmem + S::CS + w * KVT, cO = tmem + S::CO + w * D, cQ = tmem + S::CQ + (MODE == TC_SHARE ? w * (D / 2) : 0);
+    auto ready = [&](uint64_t *b, int phase) {            // (all lanes together: one left behind could miss the phase it waits for)
       good = __all_sync(0xffffffffu, good && mbar_wait(b, phase & 1, LIMIT));
       return good;
     };
-    auto qk = [&](int w, int tl, bool last_use) {         // S of group w for tile tl
+    auto scores = [&](int tl) {
       const int ks = tl % KS;
       if (!ready(&k_full[ks], tl / KS)) return;
       fence_after_sync();
       if (leader) {
         const uint64_t kd = kdesc + (uint64_t)(ks * (S::KB >> 4));
-        const uint32_t qa = tmem + S::CQ + (MODE == TC_SHARE ? w * (D / 2) : 0);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) mma_ts(tmem + S::CS + w * KVT, qa + 8 * i, kd + i * (256 >> 4), ID_S, i ? 1u : 0u);
+        for (int i = 0; i < D / 16; ++i) mma_ts(cS, cQ + 8 * i, kd + i * (256 >> 4), ID_S, i ? 1u : 0u);
         commit(&s_full[w]);
-        if (last_use) commit(&k_free[ks]);
-      }
-    };
-    auto pv = [&](int w, int tl, bool first, bool last_use, bool last) {
-      const int vs = tl % VS;
-      if (!ready(&v_full[vs], tl / VS) || !ready(&p_ready[w], w ? np1 : np0)) return;
-      if (w) ++np1;
-      else ++np0;
-      fence_after_sync();
-      if (leader) {
-        const uint64_t vd = vdesc + (uint64_t)(vs * (S::KB >> 4));
-#pragma unroll
-        for (int i = 0; i < KVT / 16; ++i)
-          mma_ts(tmem + S::CO + w * D, tmem + S::CS + w * KVT + 8 * i, vd + i * ((2 * (D / 8) * 128) >> 4), ID_O, first && i == 0 ? 0u : 1u);
-        if (last_use) commit(&v_free[vs]);
-        if (last) commit(&o_full[w]);
+        commit(&k_free[ks]);
       }
     };
     for (unsigned pos = lo; pos < hi && good;) {
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
       const int tiles = sg.end - sg.tile;
-      for (int w = 0; w < NWG; ++w) ready(&q_ready[w], nq);
-      ++nq;
-      fence_after_sync();
-      if (MODE == TC_SHARE) {
-        qk(0, ntile, false);
-        if (good) qk(1, ntile, true);
-        for (int i = 0; i < tiles && good; ++i) {
+      if (i0 < tiles) {
+        ready(&q_ready[w], nq++);
+        if (good) scores(ntile + i0);
+        for (int i = i0; i < tiles && good; i += STEP) {
+          const int tl = ntile + i, vs = tl % VS;
+          ready(&v_full[vs], tl / VS);
+          if (!ready(&p_ready[w], np++)) break;
+          fence_after_sync();
+          if (leader) {
+            const uint64_t vd = vdesc + (uint64_t)(vs * (S::KB >> 4));
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (good) pv(w, ntile + i, i == 0, w == 1, i + 1 == tiles);
-            if (good && i + 1 < tiles) qk(w, ntile + i + 1, w == 1);
+            for (int k = 0; k < KVT / 16; ++k) mma_ts(cO, cS + 8 * k, vd + k * ((2 * (D / 8) * 128) >> 4), ID_O, i == i0 && k == 0 ? 0u : 1u);
+            commit(&v_free[vs]);
+            if (i + STEP >= tiles) commit(&o_full[w]);
           }
-        }
-      } else if (MODE == TC_ALT) {
-        qk(0, ntile, true);
-        if (good && tiles > 1) qk(1, ntile + 1, true);
-        for (int i = 0; i < tiles && good; i += 2) {
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (i + w < tiles) {
-              if (good) pv(w, ntile + i + w, i == 0, true, i + w + 2 >= tiles);
-              if (good && i + w + 2 < tiles) qk(w, ntile + i + w + 2, true);
-            }
-          }
-        }
-      } else {
-        qk(0, ntile, true);
-        for (int i = 0; i < tiles && good; ++i) {
-          pv(0, ntile + i, i == 0, true, i + 1 == tiles);
-          if (good && i + 1 < tiles) qk(0, ntile + i + 1, true);
+          if (i + STEP < tiles) scores(tl + STEP);
         }
       }
       ntile += tiles;
@@ -448,7 +455,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     if (leader) commit(drain);                            // every product has ended before the block frees its TMEM
     mbar_wait(drain, 0, LIMIT);
     __syncwarp();
-  } else {
+  } else if (warp < S::W_DEQ) {
     // ---------------------------------------------------------------- softmax: thread = row
     const int w = warp >> 2, row_lane = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -509,21 +516,66 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           }
           tmem_wait_st();
         }
-        fence_before_sync();
-        mbar_arrive(&q_ready[w]);
       }
+      constexpr int STEP = MODE == TC_ALT ? 2 : 1;
+      const int i0 = MODE == TC_ALT ? w : 0;
+      fence_before_sync();
+      if (MODE == TC_ALT) bar_sync(2, 256);               // (group 1 uses what group 0 wrote)
+      __syncwarp();
+      if (lane == 0 && good && i0 < tiles) mbar_arrive(&q_ready[w]);
       float m = -INFINITY, l = 0.0f;
       int E = 0;
       bool first = true;
-      for (int i = MODE == TC_ALT ? w : 0; i < tiles && good; i += MODE == TC_ALT ? 2 : 1) {
+      for (int i = i0; i < tiles; i += STEP) {
         const int tl = ntile + i, tok0 = (sg.tile + i) * KVT;
         const bool edge = tok0 + KVT > len;               // new tokens or the end in the tile
         const uint64_t vis = edge && in ? visible(p, sg.b, t, tok0 - len, nn) : 0ull;
-        good = mbar_wait(&s_full[w], ns & 1, LIMIT);
-        good = __all_sync(0xffffffffu, good);
-        if (!good) break;
+        good = __all_sync(0xffffffffu, good && mbar_wait(&s_full[w], ns & 1, LIMIT));
         ++ns;
         fence_after_sync();
+        const int8_t *ek = exps + ((tl & 7) * 2) * KVT, *ev = ek + KVT;
+        const bool apart = edge && own_exps[tl & 7];      // each token by its own exponent
+        bool done = !good;
+        // ---- weights by the references at hand: if their sum fits fp16 each of them does, and no maximum is needed
+        if (good && !__any_sync(0xffffffffu, first || apart || ev[0] > E)) {
+          const int dE = max((int)ev[0] - E, -60);
+          const float cs = crow * exp2i(ek[0]), add = OFFSET + (float)dE - (m == -INFINITY ? 0.0f : m);
+          const uint64_t cs2 = pack2(cs, cs), ad2 = pack2(add, add);
+          uint32_t r[4][16], h[32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld16(tS + 16 * k, r[k]);
+          tmem_wait_ld();
+          uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(r[k >> 3][(2 * k) & 15]), __uint_as_float(r[k >> 3][(2 * k + 1) & 15])), cs2, ad2), x, y);
+            x = exp2_approx(x);
+            y = exp2_approx(y);
+            if (edge) {
+              const uint32_t v = (uint32_t)(k < 16 ? vis : vis >> 32);
+              x = v & (1u << ((2 * k) & 31)) ? x : 0.0f;
+              y = v & (1u << ((2 * k + 1) & 31)) ? y : 0.0f;
+            }
+            h[k] = h2pack(x, y);
+            sum2[k & 1] = add2(sum2[k & 1], pack2(x, y));
+          }
+          float a, b;
+          unpack2(add2(sum2[0], sum2[1]), a, b);
+          if (__all_sync(0xffffffffu, a + b <= 60000.0f)) {
+            l = fmaf(a + b, exp2i(-dE), l);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t o[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = h[16 * k + e];
+              tmem_st16(tS + 16 * k, o);
+            }
+            tmem_wait_st();
+            done = true;
+          }
+        }
+        if (!done) {
         float s[64];
         {
           uint32_t r[4][16];
@@ -535,8 +587,6 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[16 * k + e] = __uint_as_float(r[k][e]);
         }
-        const int8_t *ek = exps + ((tl & 7) * 2) * KVT, *ev = ek + KVT;
-        const bool apart = edge && own_exps[tl & 7];      // each token by its own exponent
         float mx, cs = crow;
         int Et = -126;
         if (!apart) {
@@ -562,9 +612,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             if (see) Et = max(Et, (int)ev[k]);
           }
         }
-        // ---- raise the row's references when a score passes the maximum by 2^4 or the values' exponent grows
-        const bool grow = mx > m + 4.0f || Et > E || first;
-        if (__any_sync(0xffffffffu, grow)) {
+        // ---- raise the row's references: the maximum and the values' exponent
+        {
           const float m2 = fmaxf(m, mx);
           const int E2 = first ? Et : max(E, Et);
           const float al = m == -INFINITY ? 0.0f : exp2_approx(m - m2);
@@ -589,7 +638,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (!apart) {
           const int dE = max(Et - E, -60);
-          const float add = 10.0f + (float)dE - mu;
+          const float add = OFFSET + (float)dE - mu;
 #pragma unroll
           for (int k = 0; k < 64; ++k) {
             s[k] = exp2_approx(fmaf(s[k], cs, add));
@@ -599,7 +648,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         } else {
 #pragma unroll
           for (int k = 0; k < 64; ++k) {
-            const float pr = exp2_approx(s[k] - mu + 10.0f);
+            const float pr = exp2_approx(s[k] - mu + OFFSET);
             sum[k & 3] += pr;
             s[k] = pr * exp2i(min(max((int)ev[k] - E, -60), 0));
           }
@@ -613,14 +662,15 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           tmem_st16(tS + 16 * k, r);
         }
         tmem_wait_st();
+        }
         fence_before_sync();
-        mbar_arrive(&p_ready[w]);
+        __syncwarp();
+        if (lane == 0 && good) mbar_arrive(&p_ready[w]);
       }
       // ---- the segment's result
-      const bool has = MODE != TC_ALT || w < tiles;
-      if (has && good) {
-        good = mbar_wait(&o_full[w], no & 1, LIMIT);
-        good = __all_sync(0xffffffffu, good);
+      const bool has = i0 < tiles;
+      if (has) {
+        good = __all_sync(0xffffffffu, good && mbar_wait(&o_full[w], no & 1, LIMIT));
         ++no;
         fence_after_sync();
       }
@@ -698,8 +748,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     auto shared = [&](int k, Segment &it, int &first, int &last) {        // the item of the block's first tile, or of its last
       const unsigned pos = k ? hi - 1 : lo;
       it = at(pos);
-      first = (int)((pos - it.tile) / share);
-      last = (int)((pos - it.tile + it.tiles - 1) / share);
+      first = (int)block_of<KVT>(seq, cum, c.batch, cuts, pos - it.tile);
+      last = (int)block_of<KVT>(seq, cum, c.batch, cuts, pos - it.tile + it.tiles - 1);
     };
     if (tid < 2) {
       bool joins = false;
