@@ -28,7 +28,20 @@
 namespace pace {
 namespace kv {
 
-constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
+// Wait for a barrier's phase, suspended by the hardware for up to a millisecond at a time so that waiting warps leave the issue slots
+// to the others; gives up after about a second.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+  for (int i = 0; i < 1000; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(umma::smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
 constexpr int MAX_BLOCKS = 1024;       // blocks of a launch (sizes the work area)
 constexpr int MAX_ROWS_FLOATS = 8 * 258;   // floats of one partial result: 8*NT rows of D + 2 with NT * D <= 256 (rounded up)
 
@@ -648,7 +661,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 #pragma unroll 1
     for (int tile = sg.tile + w; tile < sg.end; tile += NW) {
       fetch();
-      if (!dead && !umma::mbar_wait(&bars[stage], (phase >> stage) & 1u, WAIT_LIMIT_NS)) {
+      if (!dead && !bar_wait(&bars[stage], (phase >> stage) & 1u)) {
         dead = true;
         if (lane == 0) atomicOr(c.status, PACE_KV_TIMEOUT);
       }
@@ -1054,7 +1067,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   }
   if (dead) {                                         // a wait gave up: let the copies in flight land (bounded) before leaving
     for (; used < issued; ++used) {
-      umma::mbar_wait(&bars[stage], (phase >> stage) & 1u, WAIT_LIMIT_NS);
+      bar_wait(&bars[stage], (phase >> stage) & 1u);
       phase ^= 1u << stage;
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }

@@ -17,6 +17,8 @@
 // Every wait is bounded; one that gives up sets the status word, and the block leaves after its copies and products have ended.
 #pragma once
 
+#include <type_traits>
+
 #include "kv_attend.cuh"
 
 namespace pace {
@@ -35,48 +37,37 @@ struct TcShape {
   static constexpr int NWG = MODE == TC_ONE ? 1 : 2;
   static constexpr int NRB = MODE == TC_SHARE ? 2 : 1;                  // row blocks an item
   static constexpr int ROWS = 128 * NRB;
-  static constexpr int KS = 2, VS = 2;                                  // dequantized stages
-  static constexpr int RS = D == 256 ? (BITS == 4 ? 3 : 2) : 4;         // raw stages
-  static constexpr int WARPS = 4 * NWG + 8, THREADS = WARPS * 32;
-  static constexpr int W_DEQ = 4 * NWG, W_PAR = W_DEQ + 4, W_MMA = W_PAR + 2;
-  // TMEM columns
-  static constexpr int CQ = 0, CO = NRB * D / 2, CS = CO + NWG * D;
-  static_assert(CS + NWG * KVT <= 512, "TMEM");
+  // dequantized stages (ALT: score tiles are formed four tiles ahead, two a group) and raw ones
+  static constexpr int KS = MODE == TC_ALT ? 4 : 2, VS = KS;
+  static constexpr int RS = BITS == 4 ? (D == 256 ? 3 : 4) : (D == 256 || (MODE == TC_ALT && D == 128) ? 2 : 4);
+  static constexpr int NDEQ = 8;                                        // dequantizing warps
+  static constexpr int W_DEQ = 4 * NWG, W_PAR = W_DEQ + NDEQ, W_MMA = W_PAR + 2;
+  static constexpr int WARPS = (W_MMA + NWG + 3) / 4 * 4, THREADS = WARPS * 32;
+  // TMEM columns: O, two score tiles a group (each later its weights), and Q where it fits beside them; else Q is in shared memory
+  static constexpr bool QSMEM = D == 128;
+  static constexpr int CO = 0, CS = NWG * D, CQ = CS + NWG * 2 * KVT;
+  static_assert(CQ + (QSMEM ? 0 : NRB * D / 2) <= 512, "TMEM");
   // shared memory
   static constexpr int KB = KVT * D * 2;                                // one dequantized tile
+  static constexpr int QB = QSMEM ? 128 * D * 2 : 0;                    // one block of queries
   static constexpr int RAW = 2 * L::BYTES;
-  static constexpr int OK = 0, OV = OK + KS * KB, ORAW = OV + VS * KB, OPAR = ORAW + RS * RAW;
-  static constexpr int PAR = 2 * L::NG * KVT * 16;                      // scales and zero points, twice
+  static constexpr int OK = 0, OV = OK + KS * KB, OQ = OV + VS * KB, ORAW = OQ + NRB * QB, OPAR = ORAW + RS * RAW;
+  static constexpr int PB = BITS == 4 ? 16 : 4;                         // scale (and zero points) of one token and group
+  static constexpr int PAR = 2 * L::NG * KVT * PB;                      // of a tile
   static constexpr int OEXP = OPAR + 2 * PAR;                           // exponents [8 tiles][k, v][64] int8
   static constexpr int OOWN = OEXP + 8 * 2 * KVT;                       // whether a tile's tokens have their own [8]
   static constexpr int OML = OOWN + 16;                                 // m, l, exponent of group 1 (ALT)
   static constexpr int OBAR = OML + 128 * 12;
-  static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 4 * NWG + 5;
+  static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 7 * NWG + 5;
   static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flags, red[16]
   static constexpr int OCUM = (OMISC + 96 + 15) / 16 * 16;
   static constexpr size_t smem(int batch) { return OCUM + 32 * 4 + (size_t)(batch + 1) * 4 + (size_t)batch * sizeof(Seq); }
+  static_assert(OCUM + 128 + 4 + 1024 * 16 <= 227 * 1024, "shared memory");
 };
 constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 128 + 2 (128 of 256 + 2 are fewer)
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
   return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-// two fp32 operations at once
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -87,15 +78,10 @@ __device__ __forceinline__ void bar_sync(int id, int count) { asm volatile("bar.
 
 // Eight 4-bit codes (one word) times their scale: p.x = scale pair, p.y = -(1024 + z), p.z = -(64 + z). The nibble at bit 0 of a half
 // under the exponent of 1024 reads 1024 + u, the one at bit 4 reads 1024 + 16 u = 16 (64 + u): both give u - z exactly.
-__device__ __forceinline__ uint4 dequant4(uint32_t w, const uint4 &p) {
-  uint32_t r[4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t x = w >> (8 * h);
-    r[2 * h] = h2mul(h2add((x & 0x000F000Fu) | 0x64006400u, p.y), p.x);
-    r[2 * h + 1] = h2mul(h2fma((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u /* 1/16 */, p.z), p.x);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+__device__ __forceinline__ uint4 dequant4(uint32_t w, const uint4 &p, uint32_t magic) {
+  const uint32_t x = w >> 8;
+  return make_uint4(h2mul(h2add(mask_or(w, 0x000F000Fu, magic), p.y), p.x), h2mul(h2fma(mask_or(w, 0x00F000F0u, magic), 0x2C002C00u /* 1/16 */, p.z), p.x),
+                    h2mul(h2add(mask_or(x, 0x000F000Fu, magic), p.y), p.x), h2mul(h2fma(mask_or(x, 0x00F000F0u, magic), 0x2C002C00u, p.z), p.x));
 }
 // Eight 8-bit codes (two words): a byte under the exponent of 1024 reads 1024 + u, u = c + 128.
 __device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, uint32_t s) {
@@ -134,14 +120,14 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   using L = Tile<D, BITS>;
   using namespace umma;
   constexpr int NG = L::NG, NWG = S::NWG, KS = S::KS, VS = S::VS, RS = S::RS;
-  constexpr uint64_t LIMIT = WAIT_LIMIT_NS;
   constexpr float OFFSET = 8.0f;        // weights are 2^OFFSET at the row's reference: fp16 then reaches 2^-32 below it
   extern __shared__ __align__(128) char smem[];
   const KvDev &c = p.c;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::OBAR);
+  // (s_full, p_ready and pv_done: two a group, taken in turn by its tiles)
   uint64_t *raw_full = bar, *raw_free = raw_full + RS, *k_full = raw_free + RS, *k_free = k_full + KS, *v_full = k_free + KS,
-           *v_free = v_full + VS, *s_full = v_free + VS, *p_ready = s_full + NWG, *o_full = p_ready + NWG,
-           *q_ready = o_full + NWG, *par_full = q_ready + NWG, *par_free = par_full + 2, *drain = par_free + 2;
+           *v_free = v_full + VS, *s_full = v_free + VS, *p_ready = s_full + 2 * NWG, *pv_done = p_ready + 2 * NWG,
+           *q_ready = pv_done + 2 * NWG, *par_full = q_ready + NWG, *par_free = par_full + 2, *drain = par_free + 2;
   int *raw_flags = reinterpret_cast<int *>(smem + S::OMISC);            // [RS]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_flags + 4);
   int *join_flag = raw_flags + 5;
@@ -155,12 +141,13 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   const int G = c.group, T = c.n_tokens;
 
   if (tid == 0) {
-    for (int i = 0; i < RS; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], 4);
-    for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], 4), mbar_init(&k_free[i], S::NRB);
-    for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 4), mbar_init(&v_free[i], S::NRB);
-    for (int i = 0; i < NWG; ++i) mbar_init(&s_full[i], 1), mbar_init(&o_full[i], 1), mbar_init(&p_ready[i], 4), mbar_init(&q_ready[i], 4);
+    for (int i = 0; i < RS; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_free[i], S::NDEQ);
+    for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], S::NDEQ), mbar_init(&k_free[i], S::NRB);
+    for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], S::NDEQ), mbar_init(&v_free[i], S::NRB);
+    for (int i = 0; i < 2 * NWG; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 4), mbar_init(&pv_done[i], 1);
+    for (int i = 0; i < NWG; ++i) mbar_init(&q_ready[i], 4);
     join_flag[0] = 0;
-    for (int i = 0; i < 2; ++i) mbar_init(&par_full[i], 2), mbar_init(&par_free[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&par_full[i], 2), mbar_init(&par_free[i], S::NDEQ);
     mbar_init(drain, NWG);
     mbar_fence_init();
   }
@@ -184,6 +171,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   if (warp >= S::W_DEQ && warp < S::W_PAR) {
     // ---------------------------------------------------------------- dequantize
     const int dw = warp - S::W_DEQ;
+    const uint32_t magic = opaque(0x64006400u);
     int n = 0;
     bool good = true;
     for (unsigned pos = lo; pos < hi;) {
@@ -193,11 +181,14 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         const int rs = n % RS;
         const char *raw = smem + S::ORAW + rs * S::RAW;
         char *par = smem + S::OPAR + (n & 1) * S::PAR;
-        good = good && mbar_wait(&raw_full[rs], (n / RS) & 1, LIMIT) && mbar_wait(&par_full[n & 1], (n >> 1) & 1, LIMIT);
+        good = good && bar_wait(&raw_full[rs], (n / RS) & 1) && bar_wait(&par_full[n & 1], (n >> 1) & 1);
         good = __all_sync(0xffffffffu, good);
         if (!good) continue;
-        // codes: warp = 16 tokens; eight lanes write eight tokens' pieces of one 128-byte core
-        auto param = [&](int part, int g, int t) { return *reinterpret_cast<const uint4 *>(par + ((part * NG + g) * KVT + t) * 16); };
+        // codes: warp = 8 tokens; eight lanes write eight tokens' pieces of one 128-byte core
+        auto param = [&](int part, int g, int t) {
+          const char *at = par + ((part * NG + g) * KVT + t) * S::PB;
+          return BITS == 4 ? *reinterpret_cast<const uint4 *>(at) : make_uint4(*reinterpret_cast<const uint32_t *>(at), 0, 0, 0);
+        };
         auto put = [&](char *dst, int t, int a, const uint4 &v) {
           *reinterpret_cast<uint4 *>(dst + ((t >> 3) * (D / 8) + a) * 128 + (t & 7) * 16) = v;
         };
@@ -205,29 +196,25 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           const int ks = n % KS;
           char *dst = smem + S::OK + ks * S::KB;
           constexpr int CHUNKS = BITS == 8 ? D / 16 : D == 64 ? 4 : D / 32;
-          uint4 word[2][CHUNKS / 4];                        // (read before the wait)
-#pragma unroll
-          for (int o = 0; o < 2; ++o)
+          uint4 word[CHUNKS / 4];                        // (read before the wait)
 #pragma unroll
             for (int q = 0; q < CHUNKS; q += 4) {
-              const int t = dw * 16 + o * 8 + (lane & 7), ch = q + (lane >> 3);
+              const int t = dw * 8 + (lane & 7), ch = q + (lane >> 3);
               const char *src = raw + (t >> 5) * L::BYTES + L::kchunk(t & 31, ch);
               if (BITS == 4 && D == 64) {
                 const uint2 x = *reinterpret_cast<const uint2 *>(src);
-                word[o][q / 4] = make_uint4(x.x, x.y, 0, 0);
+                word[q / 4] = make_uint4(x.x, x.y, 0, 0);
               } else {
-                word[o][q / 4] = *reinterpret_cast<const uint4 *>(src);
+                word[q / 4] = *reinterpret_cast<const uint4 *>(src);
               }
             }
-          if (n >= KS) good = good && mbar_wait(&k_free[ks], (n / KS - 1) & 1, LIMIT);
+          if (n >= KS) good = good && bar_wait(&k_free[ks], (n / KS - 1) & 1);
           good = __all_sync(0xffffffffu, good);
           if (!good) continue;
 #pragma unroll
-          for (int o = 0; o < 2; ++o)
-#pragma unroll
             for (int q = 0; q < CHUNKS; q += 4) {
-              const int t = dw * 16 + o * 8 + (lane & 7), ch = q + (lane >> 3);
-              const uint4 w = word[o][q / 4];
+              const int t = dw * 8 + (lane & 7), ch = q + (lane >> 3);
+              const uint4 w = word[q / 4];
               if (BITS == 8) {
                 const int g = ch >> 2, a = 8 * g + 2 * (ch & 3);
                 const uint32_t s = param(0, g, t).x;
@@ -235,15 +222,15 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
                 put(dst, t, a + 1, dequant8(w.z, w.w, s));
               } else if (D == 64) {
                 const uint4 pr = param(0, 0, t);
-                put(dst, t, 2 * ch, dequant4(w.x, pr));
-                put(dst, t, 2 * ch + 1, dequant4(w.y, pr));
+                put(dst, t, 2 * ch, dequant4(w.x, pr, magic));
+                put(dst, t, 2 * ch + 1, dequant4(w.y, pr, magic));
               } else {
                 const int g = 2 * (ch >> 2), a = 8 * g + 2 * (ch & 3);
                 const uint4 p0 = param(0, g, t), p1 = param(0, NG > 1 ? g + 1 : g, t);
-                put(dst, t, a, dequant4(w.x, p0));
-                put(dst, t, a + 1, dequant4(w.y, p0));
-                put(dst, t, a + 8, dequant4(w.z, p1));
-                put(dst, t, a + 9, dequant4(w.w, p1));
+                put(dst, t, a, dequant4(w.x, p0, magic));
+                put(dst, t, a + 1, dequant4(w.y, p0, magic));
+                put(dst, t, a + 8, dequant4(w.z, p1, magic));
+                put(dst, t, a + 9, dequant4(w.w, p1, magic));
               }
             }
           fence_smem_to_async();
@@ -254,33 +241,29 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           const int vs = n % VS;
           char *dst = smem + S::OV + vs * S::KB;
           constexpr int UNITS = BITS == 8 ? D / 8 : D == 64 ? 8 : D / 16;
-          uint2 word[2][UNITS / 4];
-#pragma unroll
-          for (int o = 0; o < 2; ++o)
+          uint2 word[UNITS / 4];
 #pragma unroll
             for (int q = 0; q < UNITS; q += 4) {
-              const int t = dw * 16 + o * 8 + (lane & 7), u = q + (lane >> 3);
+              const int t = dw * 8 + (lane & 7), u = q + (lane >> 3);
               const char *src = raw + (t >> 5) * L::BYTES + L::vunit(t & 31, u);
-              if (BITS == 4 && D == 64) word[o][q / 4] = make_uint2(*reinterpret_cast<const uint32_t *>(src), 0);
-              else word[o][q / 4] = *reinterpret_cast<const uint2 *>(src);
+              if (BITS == 4 && D == 64) word[q / 4] = make_uint2(*reinterpret_cast<const uint32_t *>(src), 0);
+              else word[q / 4] = *reinterpret_cast<const uint2 *>(src);
             }
-          if (n >= VS) good = good && mbar_wait(&v_free[vs], (n / VS - 1) & 1, LIMIT);
+          if (n >= VS) good = good && bar_wait(&v_free[vs], (n / VS - 1) & 1);
           good = __all_sync(0xffffffffu, good);
           if (!good) continue;
 #pragma unroll
-          for (int o = 0; o < 2; ++o)
-#pragma unroll
             for (int q = 0; q < UNITS; q += 4) {
-              const int t = dw * 16 + o * 8 + (lane & 7), u = q + (lane >> 3);
-              const uint2 w = word[o][q / 4];
+              const int t = dw * 8 + (lane & 7), u = q + (lane >> 3);
+              const uint2 w = word[q / 4];
               if (BITS == 8) {
                 put(dst, t, u, dequant8(w.x, w.y, param(1, u >> 3, t).x));
               } else if (D == 64) {
-                put(dst, t, u, dequant4(w.x, param(1, 0, t)));
+                put(dst, t, u, dequant4(w.x, param(1, 0, t), magic));
               } else {
                 const int g = 2 * (u >> 3), a = 8 * g + (u & 7);
-                put(dst, t, a, dequant4(w.x, param(1, g, t)));
-                put(dst, t, a + 8, dequant4(w.y, param(1, NG > 1 ? g + 1 : g, t)));
+                put(dst, t, a, dequant4(w.x, param(1, g, t), magic));
+                put(dst, t, a + 8, dequant4(w.y, param(1, NG > 1 ? g + 1 : g, t), magic));
               }
             }
           fence_smem_to_async();
@@ -321,7 +304,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       }
       const int pa = __shfl_sync(0xffffffffu, mytile, lat - lbase), pb = __shfl_sync(0xffffffffu, mytile, lat - lbase + 1);
       const int stage = copied % RS;
-      if (copied >= RS) good = __all_sync(0xffffffffu, good && mbar_wait(&raw_free[stage], (copied / RS - 1) & 1, LIMIT));
+      if (copied >= RS) good = __all_sync(0xffffffffu, good && bar_wait(&raw_free[stage], (copied / RS - 1) & 1));
       if (!good) return;
       if (lane == 0) {
         raw_flags[stage] = (pa >= 0 ? 1 : 0) | (pb >= 0 ? 2 : 0);
@@ -343,26 +326,30 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       const int tokens = seq[sg.b].tokens, len = seq[sg.b].len;
       for (int tile = sg.tile; tile < sg.end; ++tile, ++n) {
         const int rs = n % RS;
-        good = good && mbar_wait(&raw_full[rs], (n / RS) & 1, LIMIT);
-        if (n >= 2) good = good && mbar_wait(&par_free[n & 1], ((n >> 1) - 1) & 1, LIMIT);
+        good = good && bar_wait(&raw_full[rs], (n / RS) & 1);
+        if (n >= 2) good = good && bar_wait(&par_free[n & 1], ((n >> 1) - 1) & 1);
         good = __all_sync(0xffffffffu, good);
         const char *st = smem + S::ORAW + rs * S::RAW + pw * L::BYTES;
         char *par = smem + S::OPAR + (n & 1) * S::PAR;
         const bool live = tile * KVT + t < tokens && ((raw_flags[rs] >> pw) & 1);
         const bool edge = (tile + 1) * KVT > len;                       // new tokens in the tile, which not every row sees
         float s[2][NG], top[2];
+        uint32_t z[2][NG];
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           top[part] = 0.0f;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             s[part][g] = live ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(st + (part ? L::VS : L::KS))[g * TILE + ps]) : 0.0f;
+            if (BITS == 4) z[part][g] = reinterpret_cast<const uint8_t *>(st + (part ? L::VZ : L::KZ))[g * TILE + (part ? vp : ps)];
             top[part] = fmaxf(top[part], s[part][g]);
           }
-          const float all = warp_max(top[part]), least = -warp_max(top[part] > 0.0f ? -top[part] : -FLT_MAX);
+          // (scales are not negative: their bits order as integers)
+          const uint32_t bits = __float_as_uint(top[part]);
+          const uint32_t all = __reduce_max_sync(0xffffffffu, bits), least = __reduce_min_sync(0xffffffffu, bits ? bits : 0x7F7FFFFFu);
           if (lane == 0) {
-            red[(n & 1) * 8 + part * 2 + pw] = all;
-            red[(n & 1) * 8 + 4 + part * 2 + pw] = least;
+            red[(n & 1) * 8 + part * 2 + pw] = __uint_as_float(all);
+            red[(n & 1) * 8 + 4 + part * 2 + pw] = __uint_as_float(least);
           }
         }
         bar_sync(1, 64);
@@ -380,13 +367,11 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             const float sc = s[part][g] * down;
-            uint4 v = make_uint4(h2pack(sc, sc), 0, 0, 0);
-            if (BITS == 4) {
-              const int z = reinterpret_cast<const uint8_t *>(st + (part ? L::VZ : L::KZ))[g * TILE + (part ? vp : ps)];
-              v.y = h2pack(-(1024.0f + z), -(1024.0f + z));
-              v.z = h2pack(-(64.0f + z), -(64.0f + z));
-            }
-            *reinterpret_cast<uint4 *>(par + ((part * NG + g) * KVT + t) * 16) = v;
+            char *dst = par + ((part * NG + g) * KVT + t) * S::PB;
+            if (BITS == 4)                                // with -(1024 + z) and -(64 + z) as fp16 pairs
+              *reinterpret_cast<uint4 *>(dst) = make_uint4(h2pack(sc, sc), (0xE400u | z[part][g]) * 0x10001u, (0xD400u | (z[part][g] << 4)) * 0x10001u, 0);
+            else
+              *reinterpret_cast<uint32_t *>(dst) = h2pack(sc, sc);
           }
         }
         __syncwarp();
@@ -396,7 +381,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     }
     if (!good && lane == 0) gave_up();
     if (pw == 0)                                          // copies still in flight land before the block leaves
-      for (int i = max(0, copied - RS); i < copied; ++i) mbar_wait(&raw_full[i % RS], (i / RS) & 1, LIMIT);
+      for (int i = max(0, copied - RS); i < copied; ++i) bar_wait(&raw_full[i % RS], (i / RS) & 1);
   } else if (warp >= S::W_MMA && warp < S::W_MMA + NWG) {
     // ---------------------------------------------------------------- a group's products. The warp runs as one, so that descriptors and
     // addresses stay in uniform registers; one lane issues. Products run in the order of issue: a score tile may overwrite weights
@@ -410,20 +395,26 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     constexpr uint32_t ID_S = idesc_f16(128, KVT, 0), ID_O = idesc_f16(128, D, 1);
     const uint64_t kdesc = smem_desc(smem_u32(smem) + S::OK, 128, (D / 8) * 128);
     const uint64_t vdesc = smem_desc(smem_u32(smem) + S::OV, (D / 8) * 128, 128);
-    const uint32_t cS = tmem + S::CS + w * KVT, cO = tmem + S::CO + w * D, cQ = tmem + S::CQ + (MODE == TC_SHARE ? w * (D / 2) : 0);
+    const int blk = MODE == TC_SHARE ? w : 0;             // its block of queries
+    const uint64_t qdesc = smem_desc(smem_u32(smem) + S::OQ + blk * S::QB, 128, (D / 8) * 128);
+    const uint32_t cS = tmem + S::CS + w * 2 * KVT, cO = tmem + S::CO + w * D, cQ = tmem + S::CQ + blk * (D / 2);
     auto ready = [&](uint64_t *b, int phase) {            // (all lanes together: one left behind could miss the phase it waits for)
-      good = __all_sync(0xffffffffu, good && mbar_wait(b, phase & 1, LIMIT));
+      good = __all_sync(0xffffffffu, good && bar_wait(b, phase & 1));
       return good;
     };
-    auto scores = [&](int tl) {
+    auto scores = [&](int tl, int task) {                 // two tiles ahead of the weights
       const int ks = tl % KS;
       if (!ready(&k_full[ks], tl / KS)) return;
       fence_after_sync();
       if (leader) {
         const uint64_t kd = kdesc + (uint64_t)(ks * (S::KB >> 4));
+        const uint32_t to = cS + (task & 1) * KVT;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) mma_ts(cS, cQ + 8 * i, kd + i * (256 >> 4), ID_S, i ? 1u : 0u);
-        commit(&s_full[w]);
+        for (int i = 0; i < D / 16; ++i) {
+          if (S::QSMEM) mma_ss(to, qdesc + i * (256 >> 4), kd + i * (256 >> 4), ID_S, i ? 1u : 0u);
+          else mma_ts(to, cQ + 8 * i, kd + i * (256 >> 4), ID_S, i ? 1u : 0u);
+        }
+        commit(&s_full[2 * w + (task & 1)]);
         commit(&k_free[ks]);
       }
     };
@@ -433,36 +424,38 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       const int tiles = sg.end - sg.tile;
       if (i0 < tiles) {
         ready(&q_ready[w], nq++);
-        if (good) scores(ntile + i0);
-        for (int i = i0; i < tiles && good; i += STEP) {
+        if (good) scores(ntile + i0, np);
+        if (good && i0 + STEP < tiles) scores(ntile + i0 + STEP, np + 1);
+        for (int i = i0; i < tiles && good; i += STEP, ++np) {
           const int tl = ntile + i, vs = tl % VS;
           ready(&v_full[vs], tl / VS);
-          if (!ready(&p_ready[w], np++)) break;
+          if (!ready(&p_ready[2 * w + (np & 1)], np >> 1)) break;
           fence_after_sync();
           if (leader) {
             const uint64_t vd = vdesc + (uint64_t)(vs * (S::KB >> 4));
+            const uint32_t from = cS + (np & 1) * KVT;
 #pragma unroll
-            for (int k = 0; k < KVT / 16; ++k) mma_ts(cO, cS + 8 * k, vd + k * ((2 * (D / 8) * 128) >> 4), ID_O, i == i0 && k == 0 ? 0u : 1u);
+            for (int k = 0; k < KVT / 16; ++k) mma_ts(cO, from + 8 * k, vd + k * ((2 * (D / 8) * 128) >> 4), ID_O, i == i0 && k == 0 ? 0u : 1u);
             commit(&v_free[vs]);
-            if (i + STEP >= tiles) commit(&o_full[w]);
+            commit(&pv_done[2 * w + (np & 1)]);
           }
-          if (i + STEP < tiles) scores(tl + STEP);
+          if (i + 2 * STEP < tiles) scores(tl + 2 * STEP, np + 2);
         }
       }
       ntile += tiles;
     }
     if (!good && lane == 0) gave_up();
     if (leader) commit(drain);                            // every product has ended before the block frees its TMEM
-    mbar_wait(drain, 0, LIMIT);
+    bar_wait(drain, 0);
     __syncwarp();
   } else if (warp < S::W_DEQ) {
     // ---------------------------------------------------------------- softmax: thread = row
     const int w = warp >> 2, row_lane = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + S::CS + w * KVT, tO = tmem + lanes + S::CO + w * D;
+    const uint32_t tO = tmem + lanes + S::CO + w * D;
     const float sl2 = fabsf(p.scale_log2);
     const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
-    int ntile = 0, ns = 0, no = 0;
+    int ntile = 0, task = 0;                              // tiles of the segments before; tiles of this group
     bool good = true;
     for (unsigned pos = lo; pos < hi;) {
       const Segment sg = at(pos);
@@ -498,23 +491,30 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         crow = sl2 * exp2i(e);
         const float down = exp2i(-e);
         if (MODE != TC_ALT || w == 0) {
+          const int blk = MODE == TC_SHARE ? w : 0;
+          auto conv = [&](uint32_t v) { return h2pack(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down); };
           for (int h = 0; h < HALF; ++h) {
             if (HALF > 1) load(h);
+            if (S::QSMEM) {
+              char *dst = smem + S::OQ + blk * S::QB + (row_lane >> 3) * (D / 8) * 128 + (row_lane & 7) * 16;
 #pragma unroll
-            for (int i = 0; i < D / 32 / HALF; ++i) {
-              uint32_t r[16];
+              for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<uint4 *>(dst + i * 128) = make_uint4(conv(x[i].x ^ flip), conv(x[i].y ^ flip), conv(x[i].z ^ flip), conv(x[i].w ^ flip));
+            } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint4 y = x[4 * i + k];
-                const uint32_t v[4] = {y.x ^ flip, y.y ^ flip, y.z ^ flip, y.w ^ flip};
+              for (int i = 0; i < D / 32 / HALF; ++i) {
+                uint32_t r[16];
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
-                  r[4 * k + d] = h2pack(__uint_as_float(v[d] << 16) * down, __uint_as_float(v[d] & 0xFFFF0000u) * down);
+                for (int k = 0; k < 4; ++k) {
+                  const uint4 y = x[4 * i + k];
+                  r[4 * k] = conv(y.x ^ flip), r[4 * k + 1] = conv(y.y ^ flip), r[4 * k + 2] = conv(y.z ^ flip), r[4 * k + 3] = conv(y.w ^ flip);
+                }
+                tmem_st16(tmem + lanes + S::CQ + blk * (D / 2) + 16 * (h * (D / 32 / HALF) + i), r);
               }
-              tmem_st16(tmem + lanes + S::CQ + (MODE == TC_SHARE ? w * (D / 2) : 0) + 16 * (h * (D / 32 / HALF) + i), r);
             }
           }
-          tmem_wait_st();
+          if (S::QSMEM) fence_smem_to_async();
+          else tmem_wait_st();
         }
       }
       constexpr int STEP = MODE == TC_ALT ? 2 : 1;
@@ -526,12 +526,12 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       float m = -INFINITY, l = 0.0f;
       int E = 0;
       bool first = true;
-      for (int i = i0; i < tiles; i += STEP) {
-        const int tl = ntile + i, tok0 = (sg.tile + i) * KVT;
+      for (int i = i0; i < tiles; i += STEP, ++task) {
+        const int tl = ntile + i, tok0 = (sg.tile + i) * KVT, buf = 2 * w + (task & 1);
+        const uint32_t tS = tmem + lanes + S::CS + buf * KVT;
         const bool edge = tok0 + KVT > len;               // new tokens or the end in the tile
         const uint64_t vis = edge && in ? visible(p, sg.b, t, tok0 - len, nn) : 0ull;
-        good = __all_sync(0xffffffffu, good && mbar_wait(&s_full[w], ns & 1, LIMIT));
-        ++ns;
+        good = __all_sync(0xffffffffu, good && bar_wait(&s_full[buf], (task >> 1) & 1));
         fence_after_sync();
         const int8_t *ek = exps + ((tl & 7) * 2) * KVT, *ev = ek + KVT;
         const bool apart = edge && own_exps[tl & 7];      // each token by its own exponent
@@ -540,138 +540,117 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         if (good && !__any_sync(0xffffffffu, first || apart || ev[0] > E)) {
           const int dE = max((int)ev[0] - E, -60);
           const float cs = crow * exp2i(ek[0]), add = OFFSET + (float)dE - (m == -INFINITY ? 0.0f : m);
-          const uint64_t cs2 = pack2(cs, cs), ad2 = pack2(add, add);
-          uint32_t r[4][16], h[32];
+          uint32_t h[2][16];
+          float sum4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          auto form = [&](auto masked) {                  // (two copies, so that whole tiles pay nothing for masks)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld16(tS + 16 * k, r[k]);
-          tmem_wait_ld();
-          uint64_t sum2[2] = {0ull, 0ull};
+            for (int half = 0; half < 2; ++half) {
+              uint32_t r[2][16];
+              tmem_ld16(tS + 32 * half, r[0]);
+              tmem_ld16(tS + 32 * half + 16, r[1]);
+              tmem_wait_ld();
+              const uint32_t v = (uint32_t)(vis >> (32 * half));
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float x, y;
-            unpack2(fma2(pack2(__uint_as_float(r[k >> 3][(2 * k) & 15]), __uint_as_float(r[k >> 3][(2 * k + 1) & 15])), cs2, ad2), x, y);
-            x = exp2_approx(x);
-            y = exp2_approx(y);
-            if (edge) {
-              const uint32_t v = (uint32_t)(k < 16 ? vis : vis >> 32);
-              x = v & (1u << ((2 * k) & 31)) ? x : 0.0f;
-              y = v & (1u << ((2 * k + 1) & 31)) ? y : 0.0f;
+              for (int k = 0; k < 16; ++k) {
+                float x = exp2_approx(fmaf(__uint_as_float(r[k >> 3][(2 * k) & 15]), cs, add));
+                float y = exp2_approx(fmaf(__uint_as_float(r[k >> 3][(2 * k + 1) & 15]), cs, add));
+                if (decltype(masked)::value) {
+                  x = v & (1u << (2 * k)) ? x : 0.0f;
+                  y = v & (1u << (2 * k + 1)) ? y : 0.0f;
+                }
+                h[half][k] = h2pack(x, y);
+                sum4[2 * (k & 1)] += x;
+                sum4[2 * (k & 1) + 1] += y;
+              }
             }
-            h[k] = h2pack(x, y);
-            sum2[k & 1] = add2(sum2[k & 1], pack2(x, y));
-          }
-          float a, b;
-          unpack2(add2(sum2[0], sum2[1]), a, b);
-          if (__all_sync(0xffffffffu, a + b <= 60000.0f)) {
-            l = fmaf(a + b, exp2i(-dE), l);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t o[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = h[16 * k + e];
-              tmem_st16(tS + 16 * k, o);
-            }
+          };
+          if (edge) form(std::true_type{});
+          else form(std::false_type{});
+          const float sum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+          if (__all_sync(0xffffffffu, sum <= 60000.0f)) {
+            l = fmaf(sum, exp2i(-dE), l);
+            tmem_st16(tS, h[0]);
+            tmem_st16(tS + 16, h[1]);
             tmem_wait_st();
             done = true;
           }
         }
         if (!done) {
-        float s[64];
-        {
-          uint32_t r[4][16];
+          // ---- the long way, sixteen columns at a time: the largest visible score (and value exponent) first
+          const float cs = fmaxf(crow * exp2i(ek[0]), FLT_MIN);           // (not 0: a masked score is -inf)
+          float mx = -INFINITY;
+          int Et = apart ? -126 : (int)ev[0];
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t r[16];
+            tmem_ld16(tS + 16 * k, r);
+            tmem_wait_ld();
+            const uint32_t v = edge ? (uint32_t)(vis >> (16 * k)) : 0xFFFFu;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld16(tS + 16 * k, r[k]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[16 * k + e] = __uint_as_float(r[k][e]);
-        }
-        float mx, cs = crow;
-        int Et = -126;
-        if (!apart) {
-          if (edge) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k) s[k] = (uint32_t)(k < 32 ? vis : vis >> 32) & (1u << (k & 31)) ? s[k] : -INFINITY;
+            for (int e = 0; e < 16; ++e) {
+              const bool see = (v >> e) & 1;
+              const float x = __uint_as_float(r[e]) * (apart ? crow * exp2i(ek[16 * k + e]) : cs);
+              mx = fmaxf(mx, see ? x : -INFINITY);
+              if (apart && see) Et = max(Et, (int)ev[16 * k + e]);
+            }
           }
-          float m4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int k = 4; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          cs = fmaxf(crow * exp2i(ek[0]), FLT_MIN);       // (not 0: a masked score is -inf)
-          mx *= cs;
-          Et = ev[0];
-        } else {
-          mx = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            const bool see = (vis >> k) & 1;
-            const float x = see ? s[k] * (crow * exp2i(ek[k])) : -INFINITY;
-            s[k] = x;
-            mx = fmaxf(mx, x);
-            if (see) Et = max(Et, (int)ev[k]);
-          }
-        }
-        // ---- raise the row's references: the maximum and the values' exponent
-        {
+          // ---- raise the row's references, and with them what is in O (once the product before has ended)
           const float m2 = fmaxf(m, mx);
           const int E2 = first ? Et : max(E, Et);
-          const float al = m == -INFINITY ? 0.0f : exp2_approx(m - m2);
-          l *= al;
+          l *= m == -INFINITY ? 0.0f : exp2_approx(m - m2);
           if (!first) {
             const float f = m == -INFINITY ? 0.0f : exp2_approx(m - m2 + (float)(E - E2));
+            const int before = task - 1;
+            good = __all_sync(0xffffffffu, bar_wait(&pv_done[2 * w + (before & 1)], (before >> 1) & 1));
+            fence_after_sync();
+            if (__any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t r[16];
-              tmem_ld16(tO + 16 * k, r);
-              tmem_wait_ld();
+              for (int k = 0; k < D / 16; ++k) {
+                uint32_t r[16];
+                tmem_ld16(tO + 16 * k, r);
+                tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-              tmem_st16(tO + 16 * k, r);
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                tmem_st16(tO + 16 * k, r);
+              }
             }
           }
           m = m2;
           E = E2;
           first = false;
-        }
-        const float mu = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (!apart) {
           const int dE = max(Et - E, -60);
-          const float add = OFFSET + (float)dE - mu;
+          const float mu = m == -INFINITY ? 0.0f : m, off = OFFSET - mu;
+          float sum = 0.0f;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t r[16], h[8];
+            tmem_ld16(tS + 16 * k, r);
+            tmem_wait_ld();
+            const uint32_t v = edge ? (uint32_t)(vis >> (16 * k)) : 0xFFFFu;
+            float x[16];
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            s[k] = exp2_approx(fmaf(s[k], cs, add));
-            sum[k & 3] += s[k];
+            for (int e = 0; e < 16; ++e) {
+              const bool see = (v >> e) & 1;
+              x[e] = exp2_approx(fmaf(__uint_as_float(r[e]), apart ? crow * exp2i(ek[16 * k + e]) : cs, off));
+              x[e] = see ? x[e] : 0.0f;
+              sum += x[e];
+              if (see) x[e] *= exp2i(apart ? min(max((int)ev[16 * k + e] - E, -60), 0) : dE);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = h2pack(x[2 * e], x[2 * e + 1]);
+            tmem_st8(tS + 8 * k, h);                      // (columns that were read)
           }
-          l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), exp2i(-dE), l);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            const float pr = exp2_approx(s[k] - mu + OFFSET);
-            sum[k & 3] += pr;
-            s[k] = pr * exp2i(min(max((int)ev[k] - E, -60), 0));
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t r[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) r[e] = h2pack(s[32 * k + 2 * e], s[32 * k + 2 * e + 1]);
-          tmem_st16(tS + 16 * k, r);
-        }
-        tmem_wait_st();
+          l += sum;
+          tmem_wait_st();
         }
         fence_before_sync();
         __syncwarp();
-        if (lane == 0 && good) mbar_arrive(&p_ready[w]);
+        if (lane == 0 && good) mbar_arrive(&p_ready[buf]);
       }
       // ---- the segment's result
-      const bool has = i0 < tiles;
-      if (has) {
-        good = __all_sync(0xffffffffu, good && mbar_wait(&o_full[w], no & 1, LIMIT));
-        ++no;
+      if (i0 < tiles) {
+        const int before = task - 1;
+        good = __all_sync(0xffffffffu, good && bar_wait(&pv_done[2 * w + (before & 1)], (before >> 1) & 1));
         fence_after_sync();
       }
       const bool whole = sg.tile == 0 && sg.end == sg.tiles;
