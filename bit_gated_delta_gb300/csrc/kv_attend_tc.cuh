@@ -40,7 +40,7 @@ struct TcShape {
   // dequantized stages (ALT: score tiles are formed four tiles ahead, two a group) and raw ones
   static constexpr int KS = MODE == TC_ALT ? 4 : 2, VS = KS;
   static constexpr int RS = BITS == 4 ? (D == 256 ? 3 : 4) : (D == 256 || (MODE == TC_ALT && D == 128) ? 2 : 4);
-  static constexpr int NDEQ = 8;                                        // dequantizing warps
+  static constexpr int NDEQ = MODE == TC_SHARE ? 4 : 8;                 // dequantizing warps (SHARE: a tile serves two row blocks)
   static constexpr int W_DEQ = 4 * NWG, W_PAR = W_DEQ + NDEQ, W_MMA = W_PAR + 2;
   static constexpr int WARPS = (W_MMA + NWG + 3) / 4 * 4, THREADS = WARPS * 32;
   // TMEM columns: O, two score tiles a group (each later its weights), and Q where it fits beside them; else Q is in shared memory
@@ -68,6 +68,23 @@ constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 1
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
   return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// two fp32 operations at once
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -184,7 +201,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         good = good && bar_wait(&raw_full[rs], (n / RS) & 1) && bar_wait(&par_full[n & 1], (n >> 1) & 1);
         good = __all_sync(0xffffffffu, good);
         if (!good) continue;
-        // codes: warp = 8 tokens; eight lanes write eight tokens' pieces of one 128-byte core
+        // codes: warp = 8 or 16 tokens; eight lanes write eight tokens' pieces of one 128-byte core
+        constexpr int OCT = 8 / S::NDEQ;
         auto param = [&](int part, int g, int t) {
           const char *at = par + ((part * NG + g) * KVT + t) * S::PB;
           return BITS == 4 ? *reinterpret_cast<const uint4 *>(at) : make_uint4(*reinterpret_cast<const uint32_t *>(at), 0, 0, 0);
@@ -196,25 +214,29 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           const int ks = n % KS;
           char *dst = smem + S::OK + ks * S::KB;
           constexpr int CHUNKS = BITS == 8 ? D / 16 : D == 64 ? 4 : D / 32;
-          uint4 word[CHUNKS / 4];                        // (read before the wait)
+          uint4 word[OCT][CHUNKS / 4];                        // (read before the wait)
+#pragma unroll
+          for (int o = 0; o < OCT; ++o)
 #pragma unroll
             for (int q = 0; q < CHUNKS; q += 4) {
-              const int t = dw * 8 + (lane & 7), ch = q + (lane >> 3);
+              const int t = (dw * OCT + o) * 8 + (lane & 7), ch = q + (lane >> 3);
               const char *src = raw + (t >> 5) * L::BYTES + L::kchunk(t & 31, ch);
               if (BITS == 4 && D == 64) {
                 const uint2 x = *reinterpret_cast<const uint2 *>(src);
-                word[q / 4] = make_uint4(x.x, x.y, 0, 0);
+                word[o][q / 4] = make_uint4(x.x, x.y, 0, 0);
               } else {
-                word[q / 4] = *reinterpret_cast<const uint4 *>(src);
+                word[o][q / 4] = *reinterpret_cast<const uint4 *>(src);
               }
             }
           if (n >= KS) good = good && bar_wait(&k_free[ks], (n / KS - 1) & 1);
           good = __all_sync(0xffffffffu, good);
           if (!good) continue;
 #pragma unroll
+          for (int o = 0; o < OCT; ++o)
+#pragma unroll
             for (int q = 0; q < CHUNKS; q += 4) {
-              const int t = dw * 8 + (lane & 7), ch = q + (lane >> 3);
-              const uint4 w = word[q / 4];
+              const int t = (dw * OCT + o) * 8 + (lane & 7), ch = q + (lane >> 3);
+              const uint4 w = word[o][q / 4];
               if (BITS == 8) {
                 const int g = ch >> 2, a = 8 * g + 2 * (ch & 3);
                 const uint32_t s = param(0, g, t).x;
@@ -241,21 +263,25 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           const int vs = n % VS;
           char *dst = smem + S::OV + vs * S::KB;
           constexpr int UNITS = BITS == 8 ? D / 8 : D == 64 ? 8 : D / 16;
-          uint2 word[UNITS / 4];
+          uint2 word[OCT][UNITS / 4];
+#pragma unroll
+          for (int o = 0; o < OCT; ++o)
 #pragma unroll
             for (int q = 0; q < UNITS; q += 4) {
-              const int t = dw * 8 + (lane & 7), u = q + (lane >> 3);
+              const int t = (dw * OCT + o) * 8 + (lane & 7), u = q + (lane >> 3);
               const char *src = raw + (t >> 5) * L::BYTES + L::vunit(t & 31, u);
-              if (BITS == 4 && D == 64) word[q / 4] = make_uint2(*reinterpret_cast<const uint32_t *>(src), 0);
-              else word[q / 4] = *reinterpret_cast<const uint2 *>(src);
+              if (BITS == 4 && D == 64) word[o][q / 4] = make_uint2(*reinterpret_cast<const uint32_t *>(src), 0);
+              else word[o][q / 4] = *reinterpret_cast<const uint2 *>(src);
             }
           if (n >= VS) good = good && bar_wait(&v_free[vs], (n / VS - 1) & 1);
           good = __all_sync(0xffffffffu, good);
           if (!good) continue;
 #pragma unroll
+          for (int o = 0; o < OCT; ++o)
+#pragma unroll
             for (int q = 0; q < UNITS; q += 4) {
-              const int t = dw * 8 + (lane & 7), u = q + (lane >> 3);
-              const uint2 w = word[q / 4];
+              const int t = (dw * OCT + o) * 8 + (lane & 7), u = q + (lane >> 3);
+              const uint2 w = word[o][q / 4];
               if (BITS == 8) {
                 put(dst, t, u, dequant8(w.x, w.y, param(1, u >> 3, t).x));
               } else if (D == 64) {
@@ -541,7 +567,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           const int dE = max((int)ev[0] - E, -60);
           const float cs = crow * exp2i(ek[0]), add = OFFSET + (float)dE - (m == -INFINITY ? 0.0f : m);
           uint32_t h[2][16];
-          float sum4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const uint64_t cs2 = pack2(cs, cs), ad2 = pack2(add, add);
+          uint64_t sum2[2] = {0ull, 0ull};
           auto form = [&](auto masked) {                  // (two copies, so that whole tiles pay nothing for masks)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -552,21 +579,24 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
               const uint32_t v = (uint32_t)(vis >> (32 * half));
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
-                float x = exp2_approx(fmaf(__uint_as_float(r[k >> 3][(2 * k) & 15]), cs, add));
-                float y = exp2_approx(fmaf(__uint_as_float(r[k >> 3][(2 * k + 1) & 15]), cs, add));
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(r[k >> 3][(2 * k) & 15]), __uint_as_float(r[k >> 3][(2 * k + 1) & 15])), cs2, ad2), x, y);
+                x = exp2_approx(x);
+                y = exp2_approx(y);
                 if (decltype(masked)::value) {
                   x = v & (1u << (2 * k)) ? x : 0.0f;
                   y = v & (1u << (2 * k + 1)) ? y : 0.0f;
                 }
                 h[half][k] = h2pack(x, y);
-                sum4[2 * (k & 1)] += x;
-                sum4[2 * (k & 1) + 1] += y;
+                sum2[k & 1] = add2(sum2[k & 1], pack2(x, y));
               }
             }
           };
           if (edge) form(std::true_type{});
           else form(std::false_type{});
-          const float sum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+          float sum, odd;
+          unpack2(add2(sum2[0], sum2[1]), sum, odd);
+          sum += odd;
           if (__all_sync(0xffffffffu, sum <= 60000.0f)) {
             l = fmaf(sum, exp2i(-dE), l);
             tmem_st16(tS, h[0]);
