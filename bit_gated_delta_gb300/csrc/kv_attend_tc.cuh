@@ -131,13 +131,84 @@ __device__ __forceinline__ uint64_t visible(const AttendArgs &p, int b, int t, i
   return ctx | (bits << c0);
 }
 
+// Join the parts of an item, as join_parts, for many rows: the rows' factors go to shared memory first, then each thread takes eight
+// 16-byte pieces of two parts at a time.
+template <int D, int ROWS, int THREADS>
+__device__ void tc_join(const AttendArgs &p, int first, int last, int b, int h, int row0, int fresh, float *factor) {
+  const int G = p.c.group, rows = min(ROWS, p.c.n_tokens * G - row0);
+  const float *parts = p.c.part;
+  auto part = [&](int i) { return parts + (2 * i + (i == first)) * (long)TC_PART_FLOATS; };
+  constexpr int BATCH = 16;                            // parts whose factors are held at a time
+  float *top = factor + ROWS * BATCH, *inv = top + ROWS;
+  for (int r = threadIdx.x; r < rows; r += THREADS) {
+    float M = -INFINITY, L = 0.0f;
+    for (int i = first; i <= last; ++i) {
+      const float2 e = __ldcg(reinterpret_cast<const float2 *>(part(i) + ROWS * D + 2 * r));
+      const float m = fmaxf(M, e.x);
+      L = (M == -INFINITY ? 0.0f : L * exp2_approx(M - m)) + (e.x == -INFINITY ? 0.0f : e.y * exp2_approx(e.x - m));
+      M = m;
+    }
+    top[r] = M;
+    inv[r] = (row0 + r) / G < fresh && L > 0.0f ? 1.0f / L : 0.0f;
+  }
+  constexpr int CH = D / 4, U = 8;                     // 16-byte pieces of a row; pieces a thread has under way
+  static_assert(ROWS * CH % (THREADS * U) == 0 || (ROWS * CH >= THREADS && ROWS * CH <= THREADS * U), "every thread takes the same rounds");
+  __syncthreads();
+  for (int x0 = threadIdx.x; x0 < ROWS * CH; x0 += THREADS * U) {
+    float4 y[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) y[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = first; i0 <= last; i0 += BATCH) {
+      const int n = min(BATCH, last - i0 + 1);
+      __syncthreads();
+      for (int x = threadIdx.x; x < rows * n; x += THREADS) {
+        const int r = x % rows, i = x / rows;
+        const float m = __ldcg(part(i0 + i) + ROWS * D + 2 * r);
+        factor[i * ROWS + r] = m == -INFINITY ? 0.0f : exp2_approx(m - top[r]);
+      }
+      __syncthreads();
+      for (int i = 0; i < n; i += 2) {
+        float4 v[2][U];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int q = 0; q < U; ++q) {
+            const int x = x0 + q * THREADS;
+            v[k][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i + k < n && x < rows * CH) v[k][q] = __ldcg(reinterpret_cast<const float4 *>(part(i0 + i + k)) + x);
+          }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int q = 0; q < U; ++q) {
+            const int r = (x0 + q * THREADS) / CH;
+            const float f = i + k < n && r < rows ? factor[(i + k) * ROWS + r] : 0.0f;
+            y[q].x = fmaf(f, v[k][q].x, y[q].x), y[q].y = fmaf(f, v[k][q].y, y[q].y);
+            y[q].z = fmaf(f, v[k][q].z, y[q].z), y[q].w = fmaf(f, v[k][q].w, y[q].w);
+          }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const int x = x0 + q * THREADS, r = x / CH, rr = row0 + r, t = rr / G;
+      if (r >= rows) continue;
+      const float f = inv[r];
+      *reinterpret_cast<uint2 *>(p.o.p + (b * p.o.sb + (long)t * p.o.st + (long)(h * G + rr - t * G) * p.o.sh + (x % CH) * 4) * 2) =
+          make_uint2(pack_bf16x2(y[q].x * f, y[q].y * f), pack_bf16x2(y[q].z * f, y[q].w * f));
+    }
+  }
+  __syncthreads();
+}
+
 template <int D, int BITS, int MODE>
 __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_kernel(AttendArgs p) {
   using S = TcShape<D, BITS, MODE>;
   using L = Tile<D, BITS>;
   using namespace umma;
   constexpr int NG = L::NG, NWG = S::NWG, KS = S::KS, VS = S::VS, RS = S::RS;
-  constexpr float OFFSET = 8.0f;        // weights are 2^OFFSET at the row's reference: fp16 then reaches 2^-32 below it
+  // Weights are 2^(OFFSET - ROOM) at the row's reference and the largest value exponent met so far: fp16 reaches 2^-32 below that.
+  constexpr int ROOM = 3;
+  constexpr float OFFSET = 10.0f;
   extern __shared__ __align__(128) char smem[];
   const KvDev &c = p.c;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::OBAR);
@@ -491,42 +562,70 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       const int row = sg.rb * S::ROWS + (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
       const int t = row / G, hh = sg.h * G + row - t * G;
       const bool in = row < T * G;
-      // ---- the row's query as fp16 over a power of two, into TMEM (ALT: group 0 writes, group 1 only needs the power)
+      // ---- the row's query as fp16 over a power of two, for the products (ALT: group 0 writes, group 1 only needs the power)
       float crow = 0.0f;
       if (good) {
-        const char *src = p.q.p + (sg.b * p.q.sb + (long)t * p.q.st + (long)hh * p.q.sh) * 2;
+        const int blk = MODE == TC_SHARE ? w : 0;
         uint32_t top = 0;
-        constexpr int HALF = D > 128 ? 2 : 1;             // (at D = 256 in two passes over the row: registers)
-        uint4 x[D / 8 / HALF];
-        auto load = [&](int h) {
+        auto widen = [&](const uint4 &x) {
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int i = 0; i < D / 8 / HALF; ++i)
-            x[i] = in ? reinterpret_cast<const uint4 *>(src)[h * (D / 8 / HALF) + i] : make_uint4(0, 0, 0, 0);
+          for (int e = 0; e < 4; ++e) top = max(top, max((v[e] << 16) & 0x7FFF0000u, v[e] & 0x7FFF0000u));
         };
-        for (int h = 0; h < HALF; ++h) {
-          load(h);
-#pragma unroll
-          for (int i = 0; i < D / 8 / HALF; ++i) {
-            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max((v[e] << 16) & 0x7FFF0000u, v[e] & 0x7FFF0000u));
+        float down = 0.0f;
+        auto power = [&]() {
+          const int e = max(min((int)(top >> 23) - 127, 126), -126);
+          crow = sl2 * exp2i(e);
+          down = exp2i(-e);
+        };
+        auto conv = [&](uint32_t v) { return h2pack(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down); };
+        if (S::QSMEM) {
+          // the block's rows by coalesced asynchronous copies to where the converted ones will lie; then each thread its row in place
+          char *block = smem + S::OQ + blk * S::QB;
+          constexpr int CH = D / 8, STRIDE = MODE == TC_ALT ? 256 : 128;
+          const int r0 = sg.rb * S::ROWS + blk * 128;
+          for (int x = MODE == TC_ALT ? tid : row_lane; x < 128 * CH; x += STRIDE) {
+            const int r = x / CH, ch = x % CH, rr = r0 + r, tt = rr / G;
+            const bool ok = rr < T * G;
+            const char *src = ok ? p.q.p + (sg.b * p.q.sb + (long)tt * p.q.st + (long)(sg.h * G + rr - tt * G) * p.q.sh + ch * 8) * 2 : p.q.p;
+            cp_async16(block + (r >> 3) * CH * 128 + ch * 128 + (r & 7) * 16, src, ok);
           }
-        }
-        int e = (int)(top >> 23) - 127;
-        e = max(min(e, 126), -126);
-        crow = sl2 * exp2i(e);
-        const float down = exp2i(-e);
-        if (MODE != TC_ALT || w == 0) {
-          const int blk = MODE == TC_SHARE ? w : 0;
-          auto conv = [&](uint32_t v) { return h2pack(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down); };
-          for (int h = 0; h < HALF; ++h) {
-            if (HALF > 1) load(h);
-            if (S::QSMEM) {
-              char *dst = smem + S::OQ + blk * S::QB + (row_lane >> 3) * (D / 8) * 128 + (row_lane & 7) * 16;
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          if (MODE == TC_ALT) bar_sync(2, 256);
+          else bar_sync(3 + w, 128);
+          char *mine = block + (row_lane >> 3) * CH * 128 + (row_lane & 7) * 16;
+          uint4 x[CH];
 #pragma unroll
-              for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<uint4 *>(dst + i * 128) = make_uint4(conv(x[i].x ^ flip), conv(x[i].y ^ flip), conv(x[i].z ^ flip), conv(x[i].w ^ flip));
-            } else {
+          for (int i = 0; i < CH; ++i) {
+            x[i] = *reinterpret_cast<const uint4 *>(mine + i * 128);
+            widen(x[i]);
+          }
+          power();
+          if (MODE == TC_ALT) bar_sync(2, 256);           // (both groups have read)
+          if (MODE != TC_ALT || w == 0) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              *reinterpret_cast<uint4 *>(mine + i * 128) = make_uint4(conv(x[i].x ^ flip), conv(x[i].y ^ flip), conv(x[i].z ^ flip), conv(x[i].w ^ flip));
+            fence_smem_to_async();
+          }
+        } else {
+          const char *src = p.q.p + (sg.b * p.q.sb + (long)t * p.q.st + (long)hh * p.q.sh) * 2;
+          constexpr int HALF = D > 128 ? 2 : 1;           // (at D = 256 in two passes over the row: registers)
+          uint4 x[D / 8 / HALF];
+          auto load = [&](int h) {
+#pragma unroll
+            for (int i = 0; i < D / 8 / HALF; ++i)
+              x[i] = in ? reinterpret_cast<const uint4 *>(src)[h * (D / 8 / HALF) + i] : make_uint4(0, 0, 0, 0);
+          };
+          for (int h = 0; h < HALF; ++h) {
+            load(h);
+#pragma unroll
+            for (int i = 0; i < D / 8 / HALF; ++i) widen(x[i]);
+          }
+          power();
+          if (MODE != TC_ALT || w == 0) {
+            for (int h = 0; h < HALF; ++h) {
+              if (HALF > 1) load(h);
 #pragma unroll
               for (int i = 0; i < D / 32 / HALF; ++i) {
                 uint32_t r[16];
@@ -538,10 +637,12 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
                 tmem_st16(tmem + lanes + S::CQ + blk * (D / 2) + 16 * (h * (D / 32 / HALF) + i), r);
               }
             }
+            tmem_wait_st();
           }
-          if (S::QSMEM) fence_smem_to_async();
-          else tmem_wait_st();
         }
+      } else if (S::QSMEM) {                              // (the barriers of the other side)
+        if (MODE == TC_ALT) bar_sync(2, 256), bar_sync(2, 256);
+        else bar_sync(3 + w, 128);
       }
       constexpr int STEP = MODE == TC_ALT ? 2 : 1;
       const int i0 = MODE == TC_ALT ? w : 0;
@@ -565,7 +666,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         // ---- weights by the references at hand: if their sum fits fp16 each of them does, and no maximum is needed
         if (good && !__any_sync(0xffffffffu, first || apart || ev[0] > E)) {
           const int dE = max((int)ev[0] - E, -60);
-          const float cs = crow * exp2i(ek[0]), add = OFFSET + (float)dE - (m == -INFINITY ? 0.0f : m);
+          const float cs = crow * exp2i(ek[0]), add = in ? OFFSET + (float)dE - (m == -INFINITY ? 0.0f : m) : -126.0f;
           uint32_t h[2][16];
           const uint64_t cs2 = pack2(cs, cs), ad2 = pack2(add, add);
           uint64_t sum2[2] = {0ull, 0ull};
@@ -605,11 +706,13 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             done = true;
           }
         }
-        if (!done) {
-          // ---- the long way, sixteen columns at a time: the largest visible score (and value exponent) first
+        // ---- the long way, sixteen columns at a time. own: each token by its own exponents
+        auto long_way = [&](auto own) {
+          constexpr bool OWN = decltype(own)::value;
           const float cs = fmaxf(crow * exp2i(ek[0]), FLT_MIN);           // (not 0: a masked score is -inf)
+          // the largest visible score, and value exponent
           float mx = -INFINITY;
-          int Et = apart ? -126 : (int)ev[0];
+          int Et = OWN ? -126 : (int)ev[0];
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             uint32_t r[16];
@@ -619,14 +722,15 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const bool see = (v >> e) & 1;
-              const float x = __uint_as_float(r[e]) * (apart ? crow * exp2i(ek[16 * k + e]) : cs);
+              const float x = __uint_as_float(r[e]) * (OWN ? crow * exp2i(ek[16 * k + e]) : cs);
               mx = fmaxf(mx, see ? x : -INFINITY);
-              if (apart && see) Et = max(Et, (int)ev[16 * k + e]);
+              if (OWN && see) Et = max(Et, (int)ev[16 * k + e]);
             }
           }
-          // ---- raise the row's references, and with them what is in O (once the product before has ended)
+          // raise the row's references, and with them what is in O (once the product before has ended). The values' exponent is set with
+          // some room, since scales of later tiles are often a little larger.
           const float m2 = fmaxf(m, mx);
-          const int E2 = first ? Et : max(E, Et);
+          const int E2 = first ? min(Et + ROOM, 127) : Et > E ? min(Et + ROOM, 127) : E;
           l *= m == -INFINITY ? 0.0f : exp2_approx(m - m2);
           if (!first) {
             const float f = m == -INFINITY ? 0.0f : exp2_approx(m - m2 + (float)(E - E2));
@@ -635,13 +739,15 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             fence_after_sync();
             if (__any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
-              for (int k = 0; k < D / 16; ++k) {
-                uint32_t r[16];
-                tmem_ld16(tO + 16 * k, r);
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t r[2][16];
+                tmem_ld16(tO + 32 * k, r[0]);
+                tmem_ld16(tO + 32 * k + 16, r[1]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                tmem_st16(tO + 16 * k, r);
+                for (int e = 0; e < 32; ++e) r[e >> 4][e & 15] = __float_as_uint(__uint_as_float(r[e >> 4][e & 15]) * f);
+                tmem_st16(tO + 32 * k, r[0]);
+                tmem_st16(tO + 32 * k + 16, r[1]);
               }
             }
           }
@@ -649,7 +755,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           E = E2;
           first = false;
           const int dE = max(Et - E, -60);
-          const float mu = m == -INFINITY ? 0.0f : m, off = OFFSET - mu;
+          const float off = OFFSET - (m == -INFINITY ? 0.0f : m), add = off + (OWN ? 0.0f : (float)dE);
           float sum = 0.0f;
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
@@ -660,18 +766,21 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             float x[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const bool see = (v >> e) & 1;
-              x[e] = exp2_approx(fmaf(__uint_as_float(r[e]), apart ? crow * exp2i(ek[16 * k + e]) : cs, off));
-              x[e] = see ? x[e] : 0.0f;
+              x[e] = exp2_approx(fmaf(__uint_as_float(r[e]), OWN ? crow * exp2i(ek[16 * k + e]) : cs, add));
+              x[e] = (v >> e) & 1 ? x[e] : 0.0f;
               sum += x[e];
-              if (see) x[e] *= exp2i(apart ? min(max((int)ev[16 * k + e] - E, -60), 0) : dE);
+              if (OWN && ((v >> e) & 1)) x[e] *= exp2i(min(max((int)ev[16 * k + e] - E, -60), 0));
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[e] = h2pack(x[2 * e], x[2 * e + 1]);
             tmem_st8(tS + 8 * k, h);                      // (columns that were read)
           }
-          l += sum;
+          l = OWN ? l + sum : fmaf(sum, exp2i(-dE), l);
           tmem_wait_st();
+        };
+        if (!done) {
+          if (apart) long_way(std::true_type{});
+          else long_way(std::false_type{});
         }
         fence_before_sync();
         __syncwarp();
@@ -705,34 +814,71 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           E1 = (int)mlp[2];
         }
       }
-      if ((MODE != TC_ALT || w == 0) && good) {
+      if (MODE != TC_ALT || w == 0) {                      // (outputs of a call whose wait gave up are not to be used)
         const float inv = t < nn && Ls > 0.0f ? 1.0f / Ls : 0.0f;
         const float g0 = f0 * exp2i(E0), g1 = f1 * exp2i(E1);
         char *dst = p.o.p + (sg.b * p.o.sb + (long)t * p.o.st + (long)hh * p.o.sh) * 2;
-#pragma unroll 1
-        for (int k = 0; k < D / 16; ++k) {
+        auto columns = [&](int k, float (&y)[16]) {       // columns 16k .. of the row
           uint32_t r[16], r1[16];
           tmem_ld16(tO + 16 * k, r);
           if (MODE == TC_ALT && two) tmem_ld16(tO + D + 16 * k, r1);
           tmem_wait_ld();
-          float y[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             y[e] = __uint_as_float(r[e]) * g0;
             if (MODE == TC_ALT && two) y[e] = fmaf(__uint_as_float(r1[e]), g1, y[e]);
           }
-          if (whole) {
-            if (in) {
+        };
+        if (S::QSMEM) {
+          // through the block's query area, a quarter of the columns at a time, so that rows leave in whole lines: 16-byte piece i of a
+          // row lies at i ^ (row & 7), eight a row
+          char *area = smem + S::OQ + (MODE == TC_SHARE ? w : 0) * S::QB;
+          constexpr int PC = 8;
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            float y[2][16];
+            columns(2 * k, y[0]);
+            columns(2 * k + 1, y[1]);
+            bar_sync(3 + w, 128);                         // the quarter before has left
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                reinterpret_cast<uint4 *>(dst)[2 * k + h] =
-                    make_uint4(pack_bf16x2(y[8 * h] * inv, y[8 * h + 1] * inv), pack_bf16x2(y[8 * h + 2] * inv, y[8 * h + 3] * inv),
-                               pack_bf16x2(y[8 * h + 4] * inv, y[8 * h + 5] * inv), pack_bf16x2(y[8 * h + 6] * inv, y[8 * h + 7] * inv));
+            for (int i = 0; i < PC; ++i)
+              *reinterpret_cast<float4 *>(area + row_lane * 128 + (i ^ (row_lane & 7)) * 16) =
+                  make_float4(y[i >> 2][4 * i & 15], y[i >> 2][(4 * i + 1) & 15], y[i >> 2][(4 * i + 2) & 15], y[i >> 2][(4 * i + 3) & 15]);
+            if (whole && k == 0) reinterpret_cast<float *>(area + 128 * 128)[row_lane] = inv;
+            bar_sync(3 + w, 128);
+#pragma unroll 4
+            for (int x = row_lane; x < 128 * PC; x += 128) {
+              const int r = x / PC, i = x % PC, rr = sg.rb * S::ROWS + (MODE == TC_SHARE ? w * 128 : 0) + r;
+              const float4 v = *reinterpret_cast<const float4 *>(area + r * 128 + (i ^ (r & 7)) * 16);
+              if (!whole) {
+                *reinterpret_cast<float4 *>(part + ((MODE == TC_SHARE ? w * 128 : 0) + r) * D + 32 * k + 4 * i) = v;
+              } else if (rr < T * G) {
+                const int tt = rr / G;
+                const float f = reinterpret_cast<const float *>(area + 128 * 128)[r];
+                *reinterpret_cast<uint2 *>(p.o.p + (sg.b * p.o.sb + (long)tt * p.o.st + (long)(sg.h * G + rr - tt * G) * p.o.sh + 32 * k + 4 * i) * 2) =
+                    make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+              }
             }
-          } else {
+          }
+          bar_sync(3 + w, 128);                           // (the next queries come here)
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < D / 16; ++k) {
+            float y[16];
+            columns(k, y);
+            if (whole) {
+              if (in) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-              *reinterpret_cast<float4 *>(part + prow * D + 16 * k + 4 * h) = make_float4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]);
+                for (int h = 0; h < 2; ++h)
+                  reinterpret_cast<uint4 *>(dst)[2 * k + h] =
+                      make_uint4(pack_bf16x2(y[8 * h] * inv, y[8 * h + 1] * inv), pack_bf16x2(y[8 * h + 2] * inv, y[8 * h + 3] * inv),
+                                 pack_bf16x2(y[8 * h + 4] * inv, y[8 * h + 5] * inv), pack_bf16x2(y[8 * h + 6] * inv, y[8 * h + 7] * inv));
+              }
+            } else {
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                *reinterpret_cast<float4 *>(part + prow * D + 16 * k + 4 * h) = make_float4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]);
+            }
           }
         }
         if (!whole) {
@@ -777,7 +923,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         Segment it;
         int first, last;
         shared(k, it, first, last);
-        join_parts<D, S::ROWS, S::THREADS, false>(p, c.part, TC_PART_FLOATS, first, last, it.b, it.h, it.rb * S::ROWS, seq[it.b].fresh, nullptr);
+        tc_join<D, S::ROWS, S::THREADS>(p, first, last, it.b, it.h, it.rb * S::ROWS, seq[it.b].fresh, reinterpret_cast<float *>(smem));
       }
   }
 }
