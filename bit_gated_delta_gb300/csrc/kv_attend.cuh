@@ -192,21 +192,26 @@ __device__ __forceinline__ Seq sequence(const KvDev &c, int b, bool report) {
   return q;
 }
 // The sequences, and the exclusive prefix sums of their items' tiles of TOK tokens (at least one each), in shared memory:
-// seq[0..batch), cum[0..batch]. (32 bits: the host keeps the line of one launch below 2^31 tiles.)
+// seq[0..batch), cum[0..batch]; returns the most tiles of an item. `warp_sums` holds 64 values. (32 bits: the host keeps the line of one
+// launch below 2^31 tiles.)
 template <int TOK>
-__device__ __forceinline__ void tile_line(const KvDev &c, unsigned per_seq, Seq *seq, unsigned *cum, unsigned *warp_sums) {
+__device__ __forceinline__ unsigned tile_line(const KvDev &c, unsigned per_seq, Seq *seq, unsigned *cum, unsigned *warp_sums) {
   const int n = c.batch, nt = blockDim.x, per = (n + nt - 1) / nt, b0 = threadIdx.x * per;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  unsigned s = 0;
+  unsigned s = 0, most = 0;
   for (int i = 0; i < per && b0 + i < n; ++i) {
     const Seq q = sequence(c, b0 + i, blockIdx.x == 0);
     seq[b0 + i] = q;
-    s += max((q.tokens + TOK - 1) / TOK, 1) * per_seq;
+    const unsigned tiles = max((q.tokens + TOK - 1) / TOK, 1);
+    most = max(most, tiles);
+    s += tiles * per_seq;
     cum[b0 + i + 1] = s;
   }
   if (threadIdx.x == 0) cum[0] = 0;
-  if (n <= 32 && per == 1) {                           // one warp holds them all
+  if (n <= 32) {                                       // one warp holds them all
     if (w == 0) {
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) warp_sums[32] = most;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned y = __shfl_up_sync(0xffffffffu, s, o);
@@ -215,8 +220,10 @@ __device__ __forceinline__ void tile_line(const KvDev &c, unsigned per_seq, Seq 
       if (lane < n) cum[lane + 1] = s;
     }
     __syncthreads();
-    return;
+    return warp_sums[32];
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) warp_sums[32 + w] = most;
   unsigned x = s;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -228,7 +235,10 @@ __device__ __forceinline__ void tile_line(const KvDev &c, unsigned per_seq, Seq 
   unsigned base = x - s;
   for (int i = 0; i < w; ++i) base += warp_sums[i];
   for (int i = 0; i < per && b0 + i < n; ++i) cum[b0 + i + 1] += base;
+  most = 0;
+  for (int i = 0; i < nt >> 5; ++i) most = max(most, warp_sums[32 + i]);
   __syncthreads();
+  return most;
 }
 
 // The item that holds line position p, and its stretch from there up to hi.
@@ -250,49 +260,31 @@ __device__ __forceinline__ Segment segment_at(const Seq *seq, const unsigned *cu
   s.end = (int)min((unsigned)s.tiles, s.tile + (hi - p));
   return s;
 }
-// Where the line is cut: at every `share` tiles, moved to the next item boundary where one lies within `slack` tiles, since an item
-// that two blocks share costs each of them the writing of a part and one of them the joining.
+// Where the line is cut: an item a block, where there are no more items than blocks and the longest is within `extra` tiles of an equal
+// share; else at every `share` tiles, since an item that blocks share costs each of them the writing of a part and one of them the
+// joining.
 struct Cuts {
-  unsigned share, slack, total;
+  unsigned share, total, per_seq;
+  bool each;
 };
 template <int TOK>
 __device__ __forceinline__ unsigned cut_at(const Seq *seq, const unsigned *cum, int batch, const Cuts &c, unsigned i) {
-  const unsigned p = i * c.share;
-  if (p >= c.total) return c.total;
-  if (c.slack == 0) return p;
-  int lo = 0, up = batch;
-  while (up - lo > 1) {
-    const int mid = (lo + up) >> 1;
-    if (cum[mid] <= p) lo = mid;
-    else up = mid;
-  }
-  const unsigned tiles = max((seq[lo].tokens + TOK - 1) / TOK, 1), off = (p - cum[lo]) % tiles, rest = tiles - off;
-  if (off <= rest) return off <= c.slack ? p - off : p;
-  return rest <= c.slack ? p + rest : p;
+  if (!c.each) return i > c.total / c.share ? c.total : min(i * c.share, c.total);
+  const unsigned b = i / c.per_seq;
+  return b >= (unsigned)batch ? c.total : cum[b] + (i - b * c.per_seq) * max((seq[b].tokens + TOK - 1) / TOK, 1);
 }
-// The block whose stretch holds line position pos.
+// This block's stretch [lo, hi). No share is less than `least` tiles, and items of up to `whole` tiles on average are not cut finer.
 template <int TOK>
-__device__ __forceinline__ unsigned block_of(const Seq *seq, const unsigned *cum, int batch, const Cuts &c, unsigned pos) {
-  unsigned i = pos / c.share;
-  const unsigned off = pos - i * c.share;
-  if (off >= c.slack && c.share - off > c.slack) return i;             // no cut this near
-  while (cut_at<TOK>(seq, cum, batch, c, i + 1) <= pos) ++i;
-  while (cut_at<TOK>(seq, cum, batch, c, i) > pos) --i;
-  return i;
-}
-// The cuts of a launch and this block's two, by one warp's first lanes; every warp may call it.
-template <int TOK>
-__device__ __forceinline__ Cuts make_cuts(const Seq *seq, const unsigned *cum, int batch, unsigned items, unsigned least, unsigned whole,
-                                          unsigned slack, unsigned &lo, unsigned &hi) {
+__device__ __forceinline__ Cuts make_cuts(const Seq *seq, const unsigned *cum, int batch, unsigned per_seq, unsigned most, unsigned least,
+                                          unsigned whole, unsigned extra, unsigned &lo, unsigned &hi) {
   Cuts c;
   c.total = cum[batch];
-  c.slack = slack;
-  const unsigned mean = c.total / items;
-  c.share = max((c.total + gridDim.x - 1) / gridDim.x, mean <= whole ? mean : least);
-  const unsigned i = blockIdx.x + (threadIdx.x & 31 ? 1 : 0);
-  const unsigned at = i > c.total / c.share ? c.total : cut_at<TOK>(seq, cum, batch, c, i);
-  lo = __shfl_sync(0xffffffffu, at, 0);
-  hi = __shfl_sync(0xffffffffu, at, 1);
+  c.per_seq = per_seq;
+  const unsigned items = per_seq * batch, mean = c.total / items, even = (c.total + gridDim.x - 1) / gridDim.x;
+  c.each = items <= gridDim.x && most <= even + extra;
+  c.share = max(even, mean <= whole ? mean : least);
+  lo = cut_at<TOK>(seq, cum, batch, c, blockIdx.x);
+  hi = cut_at<TOK>(seq, cum, batch, c, blockIdx.x + 1);
   return c;
 }
 
@@ -471,7 +463,7 @@ struct AttendShape {
   static constexpr size_t ML = (size_t)NW * ROWS * 2 * 4;
   static constexpr size_t OQRAW = RING, OQF = OQRAW + QRAW, OSCR = OQF + QF, OML = OSCR + SCRATCH, OROWS = OML + ML,
                           OBAR = OROWS + ROWS * 4, OSEG = OBAR + (NW * STAGES * 8 + 15) / 16 * 16,
-                          OSUM = OSEG + (SEGS + 1) * sizeof(Segment), OCUM = OSUM + 32 * 4 + 16;
+                          OSUM = OSEG + (SEGS + 1) * sizeof(Segment), OCUM = OSUM + 64 * 4 + 16;
   // prefix sums of up to this many sequences: few capacities, so that the occupancy of each is asked for once
   __host__ __device__ static constexpr int capacity(int batch) { return batch <= 64 ? 64 : batch <= 256 ? 256 : PACE_KV_MAX_BATCH; }
   static constexpr size_t smem(int batch) { return OCUM + (size_t)(capacity(batch) + 1) * 4 + (size_t)capacity(batch) * sizeof(Seq); }
@@ -495,7 +487,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   float *rowmul = reinterpret_cast<float *>(smem + S::OROWS);     // what a row's scores are multiplied by
   Segment *segs = reinterpret_cast<Segment *>(smem + S::OSEG);
   unsigned *wsum = reinterpret_cast<unsigned *>(smem + S::OSUM);
-  int *flag = reinterpret_cast<int *>(wsum + 32);
+  int *flag = reinterpret_cast<int *>(wsum + 64);
   unsigned *cum = reinterpret_cast<unsigned *>(smem + S::OCUM);
   Seq *seq = reinterpret_cast<Seq *>(cum + S::capacity(p.c.batch) + 1);
 
@@ -507,12 +499,12 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   if (lane < STAGES) umma::mbar_init(&bars[lane], 1);
   umma::mbar_fence_init();
   pdl_enter();
-  tile_line<TILE>(c, (unsigned)p.row_blocks * c.Hkv, seq, cum, wsum);
+  const unsigned most = tile_line<TILE>(c, (unsigned)p.row_blocks * c.Hkv, seq, cum, wsum);
 
-  // equal shares, but none finer than a tile for every warp, or than a whole average item of up to three: joining one costs about as
-  // much as three rounds of tiles
+  // no share is less than a tile for every warp, or a whole average item of up to three: joining one costs about as much as three
+  // rounds of tiles
   unsigned lo, hi;
-  const Cuts cuts = make_cuts<TILE>(seq, cum, c.batch, (unsigned)c.batch * c.Hkv * p.row_blocks, NW, 3 * NW, 0, lo, hi);
+  const Cuts cuts = make_cuts<TILE>(seq, cum, c.batch, (unsigned)p.row_blocks * c.Hkv, most, NW, 3 * NW, 4 * NW, lo, hi);
   if (lo >= hi) return;
   auto segment = [&](unsigned at) { return segment_at<TILE>(seq, cum, c.batch, p.row_blocks, at, hi); };
 
@@ -1042,8 +1034,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
     auto shared = [&](int k, Segment &it, int &first, int &last) {
       const unsigned at = k ? hi - 1 : lo;
       it = segment(at);
-      first = (int)block_of<TILE>(seq, cum, c.batch, cuts, at - it.tile);
-      last = (int)block_of<TILE>(seq, cum, c.batch, cuts, at - it.tile + it.tiles - 1);
+      first = (int)((at - it.tile) / cuts.share);
+      last = (int)((at - it.tile + it.tiles - 1) / cuts.share);
     };
     if (tid < 2) {
       bool joins = false;

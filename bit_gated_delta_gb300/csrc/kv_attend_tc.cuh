@@ -9,7 +9,7 @@
 // tiles with new tokens, where rows may see different tokens, each token by its own), weights are 2^8 at the row's
 // running maximum. The powers return with the scores, and in O as a running exponent per row raised like the maximum.
 //
-// Roles (warps): softmax (four a group; thread = row = TMEM lane), four that dequantize, two that copy tiles in and prepare their scales,
+// Roles (warps): softmax (four a group; thread = row = TMEM lane), four that dequantize, two that copy tiles in and prepare their scales (keys', values'),
 // one a softmax group that issues its products (issued by the softmax warps themselves, a prompt chunk took 206 us, not 172). Two softmax groups take turns, so that the tensor cores work on one group's products while the other group forms
 // its weights: the groups are two row blocks (SHARE), or even and odd tiles of one block (ALT, joined at the end through TMEM).
 //   bound: per 64 tokens and row block of 128 at D = 128, 512 cycles of tensor work; 64 scores a thread (4.5 instructions each, two
@@ -27,9 +27,10 @@ namespace kv {
 enum { TC_SHARE = 0, TC_ALT = 1, TC_ONE = 2 };
 constexpr int KVT = 64;               // cached tokens a tile
 constexpr int TC_BLOCKS = 160;        // most blocks of a launch (one an SM)
-// Tiles: the fewest a block takes; items of up to so many on average are not cut; cuts move to an item boundary this near. (A shared
-// item costs about 20 us, its parts written and joined; a tile 0.7 to 1.3 us.)
-constexpr int TC_LEAST = 4, TC_WHOLE = 12, TC_SLACK = 8;
+// Tiles: the fewest a block takes; items of up to so many on average are not cut; an item a block while the longest is so many above an
+// equal share (sharing items cost a launch about 25 us, a tile 0.9 to 1.0 us).
+constexpr int TC_LEAST = 4, TC_WHOLE = 12, TC_EXTRA = 24;
+
 
 template <int D, int BITS, int MODE>
 struct TcShape {
@@ -55,14 +56,14 @@ struct TcShape {
   static constexpr int PB = BITS == 4 ? 16 : 4;                         // scale (and zero points) of one token and group
   static constexpr int PAR = 2 * L::NG * KVT * PB;                      // of a tile
   static constexpr int OEXP = OPAR + 2 * PAR;                           // exponents [8 tiles][k, v][64] int8
-  static constexpr int OOWN = OEXP + 8 * 2 * KVT;                       // whether a tile's tokens have their own [8]
+  static constexpr int OOWN = OEXP + 8 * 2 * KVT;                       // whether a tile's tokens have their own [8][k, v]
   static constexpr int OML = OOWN + 16;                                 // m, l, exponent of group 1 (ALT)
   static constexpr int OBAR = OML + 128 * 12;
   static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 7 * NWG + 5;
-  static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flags, red[16]
-  static constexpr int OCUM = (OMISC + 96 + 15) / 16 * 16;
-  static constexpr size_t smem(int batch) { return OCUM + 32 * 4 + (size_t)(batch + 1) * 4 + (size_t)batch * sizeof(Seq); }
-  static_assert(OCUM + 128 + 4 + 1024 * 16 <= 227 * 1024, "shared memory");
+  static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flags
+  static constexpr int OCUM = (OMISC + 32 + 15) / 16 * 16;
+  static constexpr size_t smem(int batch) { return OCUM + 64 * 4 + (size_t)(batch + 1) * 4 + (size_t)batch * sizeof(Seq); }
+  static_assert(OCUM + 256 + 4 + 1024 * 16 <= 227 * 1024, "shared memory");
 };
 constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 128 + 2 (128 of 256 + 2 are fewer)
 
@@ -219,9 +220,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   int *raw_flags = reinterpret_cast<int *>(smem + S::OMISC);            // [RS]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_flags + 4);
   int *join_flag = raw_flags + 5;
-  float *red = reinterpret_cast<float *>(raw_flags + 8);                // [16]
   unsigned *wsum = reinterpret_cast<unsigned *>(smem + S::OCUM);
-  unsigned *cum = wsum + 32;
+  unsigned *cum = wsum + 64;
   Seq *seq = reinterpret_cast<Seq *>(cum + c.batch + 1);
   int8_t *exps = reinterpret_cast<int8_t *>(smem + S::OEXP);
   volatile uint8_t *own_exps = reinterpret_cast<uint8_t *>(smem + S::OOWN);
@@ -245,12 +245,12 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   }
   pdl_enter();
   fence_before_sync();
-  tile_line<KVT>(c, (unsigned)p.row_blocks * c.Hkv, seq, cum, wsum);      // (its barriers also publish the set-up above)
+  const unsigned most = tile_line<KVT>(c, (unsigned)p.row_blocks * c.Hkv, seq, cum, wsum);      // (its barriers also publish the set-up above)
   fence_after_sync();
   constexpr uint32_t tmem = 0;          // the whole of TMEM is this block's: its first column (a constant keeps addresses uniform)
 
   unsigned lo, hi;
-  const Cuts cuts = make_cuts<KVT>(seq, cum, c.batch, (unsigned)c.batch * c.Hkv * p.row_blocks, TC_LEAST, TC_WHOLE, TC_SLACK, lo, hi);
+  const Cuts cuts = make_cuts<KVT>(seq, cum, c.batch, (unsigned)p.row_blocks * c.Hkv, most, TC_LEAST, TC_WHOLE, TC_EXTRA, lo, hi);
   auto at = [&](unsigned pos) { return segment_at<KVT>(seq, cum, c.batch, p.row_blocks, pos, hi); };
   // A role whose wait gives up goes on without waiting or touching the tensor cores, but keeps the barriers it shares, so that no
   // other warp is left at one; the others' waits then run out too.
@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     if (!good && lane == 0) gave_up();
   } else if (warp >= S::W_PAR && warp < S::W_MMA) {
     // ---------------------------------------------------------------- copies of tiles; their scales and exponents: lane = token
-    const int pw = warp - S::W_PAR, t = pw * 32 + lane, ps = L::pos(lane), vp = L::vpos(lane);
+    // (one warp the keys', one the values')
+    const int pw = warp - S::W_PAR, ps = L::pos(lane), vp = L::vpos(lane);
     int n = 0;
     bool good = true;
     // the copying side, RS - 1 tiles ahead (first of the two warps): segment, storage tiles [at, end) of it, and the pool index of the
@@ -426,47 +427,47 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         good = good && bar_wait(&raw_full[rs], (n / RS) & 1);
         if (n >= 2) good = good && bar_wait(&par_free[n & 1], ((n >> 1) - 1) & 1);
         good = __all_sync(0xffffffffu, good);
-        const char *st = smem + S::ORAW + rs * S::RAW + pw * L::BYTES;
-        char *par = smem + S::OPAR + (n & 1) * S::PAR;
-        const bool live = tile * KVT + t < tokens && ((raw_flags[rs] >> pw) & 1);
-        const bool edge = (tile + 1) * KVT > len;                       // new tokens in the tile, which not every row sees
-        float s[2][NG], top[2];
+        const char *raw = smem + S::ORAW + rs * S::RAW;
+        char *par = smem + S::OPAR + (n & 1) * S::PAR + pw * NG * KVT * S::PB;
+        float s[2][NG], top[2];                           // the lane's tokens: one of each storage tile
         uint32_t z[2][NG];
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          top[part] = 0.0f;
+        for (int half = 0; half < 2; ++half) {
+          const char *st = raw + half * L::BYTES;
+          const bool live = tile * KVT + half * TILE + lane < tokens && ((raw_flags[rs] >> half) & 1);
+          top[half] = 0.0f;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            s[part][g] = live ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(st + (part ? L::VS : L::KS))[g * TILE + ps]) : 0.0f;
-            if (BITS == 4) z[part][g] = reinterpret_cast<const uint8_t *>(st + (part ? L::VZ : L::KZ))[g * TILE + (part ? vp : ps)];
-            top[part] = fmaxf(top[part], s[part][g]);
-          }
-          // (scales are not negative: their bits order as integers)
-          const uint32_t bits = __float_as_uint(top[part]);
-          const uint32_t all = __reduce_max_sync(0xffffffffu, bits), least = __reduce_min_sync(0xffffffffu, bits ? bits : 0x7F7FFFFFu);
-          if (lane == 0) {
-            red[(n & 1) * 8 + part * 2 + pw] = __uint_as_float(all);
-            red[(n & 1) * 8 + 4 + part * 2 + pw] = __uint_as_float(least);
+            const __nv_bfloat16 x = reinterpret_cast<const __nv_bfloat16 *>(st + (pw ? L::VS : L::KS))[g * TILE + ps];
+            s[half][g] = live ? __bfloat162float(x) : 0.0f;
+            if (BITS == 4) z[half][g] = reinterpret_cast<const uint8_t *>(st + (pw ? L::VZ : L::KZ))[g * TILE + (pw ? vp : ps)];
+            top[half] = fmaxf(top[half], s[half][g]);
           }
         }
-        bar_sync(1, 64);
+        // (scales are not negative: their bits order as integers)
+        const uint32_t b0 = __float_as_uint(top[0]), b1 = __float_as_uint(top[1]);
+        const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, max(b0, b1)));
         // one exponent for the tile keeps ten bits of every token whose scale is within 2^12 of the largest; where a new token (that some
         // rows may not see) makes them spread further, each token gets its own
-        const float *rr = red + (n & 1) * 8;
-        const bool own = edge && (fmaxf(rr[0], rr[1]) > 4096.0f * fminf(rr[4], rr[5]) || fmaxf(rr[2], rr[3]) > 4096.0f * fminf(rr[6], rr[7]));
-        if (pw == 0 && lane == 0) own_exps[n & 7] = own;
+        bool own = false;
+        if ((tile + 1) * KVT > len) {
+          const uint32_t least = __reduce_min_sync(0xffffffffu, min(b0 ? b0 : 0x7F7FFFFFu, b1 ? b1 : 0x7F7FFFFFu));
+          own = all > 4096.0f * __uint_as_float(least);
+        }
+        if (lane == 0) own_exps[(n & 7) * 2 + pw] = own;
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const float ref = own ? top[part] : fmaxf(rr[part * 2], rr[part * 2 + 1]);
+        for (int half = 0; half < 2; ++half) {
+          const int t = half * TILE + lane;
+          const float ref = own ? top[half] : all;
           const int e = ref > 0.0f ? (int)(__float_as_uint(ref) >> 23) - 127 : 0;
-          exps[((n & 7) * 2 + part) * KVT + t] = (int8_t)e;
+          exps[((n & 7) * 2 + pw) * KVT + t] = (int8_t)e;
           const float down = exp2i(-e < 127 ? -e : 127);                // (e >= -126)
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            const float sc = s[part][g] * down;
-            char *dst = par + ((part * NG + g) * KVT + t) * S::PB;
+            const float sc = s[half][g] * down;
+            char *dst = par + (g * KVT + t) * S::PB;
             if (BITS == 4)                                // with -(1024 + z) and -(64 + z) as fp16 pairs
-              *reinterpret_cast<uint4 *>(dst) = make_uint4(h2pack(sc, sc), (0xE400u | z[part][g]) * 0x10001u, (0xD400u | (z[part][g] << 4)) * 0x10001u, 0);
+              *reinterpret_cast<uint4 *>(dst) = make_uint4(h2pack(sc, sc), (0xE400u | z[half][g]) * 0x10001u, (0xD400u | (z[half][g] << 4)) * 0x10001u, 0);
             else
               *reinterpret_cast<uint32_t *>(dst) = h2pack(sc, sc);
           }
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         good = __all_sync(0xffffffffu, good && bar_wait(&s_full[buf], (task >> 1) & 1));
         fence_after_sync();
         const int8_t *ek = exps + ((tl & 7) * 2) * KVT, *ev = ek + KVT;
-        const bool apart = edge && own_exps[tl & 7];      // each token by its own exponent
+        const bool apart = edge && (own_exps[(tl & 7) * 2] || own_exps[(tl & 7) * 2 + 1]);   // each token by its own exponents
         bool done = !good;
         // ---- weights by the references at hand: if their sum fits fp16 each of them does, and no maximum is needed
         if (good && !__any_sync(0xffffffffu, first || apart || ev[0] > E)) {
@@ -903,8 +904,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     auto shared = [&](int k, Segment &it, int &first, int &last) {        // the item of the block's first tile, or of its last
       const unsigned pos = k ? hi - 1 : lo;
       it = at(pos);
-      first = (int)block_of<KVT>(seq, cum, c.batch, cuts, pos - it.tile);
-      last = (int)block_of<KVT>(seq, cum, c.batch, cuts, pos - it.tile + it.tiles - 1);
+      first = (int)((pos - it.tile) / cuts.share);
+      last = (int)((pos - it.tile + it.tiles - 1) / cuts.share);
     };
     if (tid < 2) {
       bool joins = false;
