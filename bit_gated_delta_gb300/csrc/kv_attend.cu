@@ -24,7 +24,7 @@ bool use_tc(int io, int rows) { return io == PACE_IO_BF16 && rows >= TC_ROWS; }
 void pace_kv_attend_work(const pace_kv_config &cfg, size_t *count_bytes, size_t *part_bytes) {
   *count_bytes = MAX_BLOCKS * sizeof(int32_t);
   size_t n = (size_t)2 * MAX_BLOCKS * (MAX_ROWS_FLOATS + 64);
-  if (use_tc(cfg.io_dtype, cfg.max_new * (cfg.q_heads / cfg.kv_heads))) n = std::max(n, (size_t)2 * TC_BLOCKS * TC_PART_FLOATS);
+  if (use_tc(cfg.io_dtype, cfg.max_new * (cfg.q_heads / cfg.kv_heads))) n = std::max(n, (size_t)2 * TC_BLOCKS * TC_PART_FLOATS + TC_BLOCKS * 4);
   *part_bytes = n * sizeof(float);
 }
 

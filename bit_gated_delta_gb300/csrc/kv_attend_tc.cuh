@@ -60,11 +60,12 @@ struct TcShape {
   static constexpr int OML = OOWN + 16;                                 // m, l, exponent of group 1 (ALT)
   static constexpr int OBAR = OML + 128 * 12;
   static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 7 * NWG + 5;
-  static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base, join flags
+  static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base
   static constexpr int OCUM = (OMISC + 32 + 15) / 16 * 16;
   static constexpr size_t smem(int batch) { return OCUM + 64 * 4 + (size_t)(batch + 1) * 4 + (size_t)batch * sizeof(Seq); }
   static_assert(OCUM + 256 + 4 + 1024 * 16 <= 227 * 1024, "shared memory");
 };
+constexpr int JOIN_THREADS = 256;
 constexpr int TC_PART_FLOATS = 256 * 130;   // one partial result: 256 rows of 128 + 2 (128 of 256 + 2 are fewer)
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
@@ -132,73 +133,71 @@ __device__ __forceinline__ uint64_t visible(const AttendArgs &p, int b, int t, i
   return ctx | (bits << c0);
 }
 
-// Join the parts of an item, as join_parts, for many rows: the rows' factors go to shared memory first, then each thread takes eight
-// 16-byte pieces of two parts at a time.
-template <int D, int ROWS, int THREADS>
-__device__ void tc_join(const AttendArgs &p, int first, int last, int b, int h, int row0, int fresh, float *factor) {
-  const int G = p.c.group, rows = min(ROWS, p.c.n_tokens * G - row0);
-  const float *parts = p.c.part;
-  auto part = [&](int i) { return parts + (2 * i + (i == first)) * (long)TC_PART_FLOATS; };
-  constexpr int BATCH = 16;                            // parts whose factors are held at a time
-  float *top = factor + ROWS * BATCH, *inv = top + ROWS;
-  for (int r = threadIdx.x; r < rows; r += THREADS) {
+// The item that begins in a block and goes on in later ones, as that block leaves it for the join: sequence (-1: none), head and row
+// block, last block, new tokens.
+__device__ __forceinline__ int4 *tc_shared(const KvDev &c) { return reinterpret_cast<int4 *>(c.part + (size_t)2 * TC_BLOCKS * TC_PART_FLOATS); }
+
+// Joins the parts of shared items in block order, in a launch of its own behind the attention's: one SM draws about 100 GB/s from
+// L2, and parts of 64 to 128 KB that the last of an item's blocks joined by itself took it up to 100 us. A block takes four to
+// sixteen rows of an item at a time, a thread one 16-byte piece of a row, eight parts under way.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(JOIN_THREADS, 4) tc_join_kernel(AttendArgs p, int blocks) {
+  const KvDev &c = p.c;
+  const int G = c.group, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  static_assert(TC_BLOCKS <= JOIN_THREADS, "a thread looks at a block");
+  constexpr int CH = D / 4, SLICE = JOIN_THREADS / CH, SLICES = ROWS / SLICE, U = 8;
+  __shared__ int list[TC_BLOCKS], count[JOIN_THREADS / 32];
+  pdl_enter();
+  const bool mine = tid < blocks && __ldcg(&tc_shared(c)[tid]).x >= 0;
+  const unsigned vote = __ballot_sync(0xffffffffu, mine);
+  if (lane == 0) count[warp] = __popc(vote);
+  __syncthreads();
+  int n = 0, before = 0;
+  for (int i = 0; i < JOIN_THREADS / 32; ++i) {
+    before += i < warp ? count[i] : 0;
+    n += count[i];
+  }
+  if (mine) list[before + __popc(vote & ((1u << lane) - 1))] = tid;
+  __syncthreads();
+  for (int unit = blockIdx.x; unit < n * SLICES; unit += gridDim.x) {
+    const int first = list[unit / SLICES], r = (unit % SLICES) * SLICE + tid / CH, ch = tid % CH;
+    const int4 it = __ldcg(&tc_shared(c)[first]);
+    const int h = it.y / p.row_blocks, row = (it.y - h * p.row_blocks) * ROWS + r, t = row / G;
+    if (row >= c.n_tokens * G) continue;
     float M = -INFINITY, L = 0.0f;
-    for (int i = first; i <= last; ++i) {
-      const float2 e = __ldcg(reinterpret_cast<const float2 *>(part(i) + ROWS * D + 2 * r));
-      const float m = fmaxf(M, e.x);
-      L = (M == -INFINITY ? 0.0f : L * exp2_approx(M - m)) + (e.x == -INFINITY ? 0.0f : e.y * exp2_approx(e.x - m));
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = first; i0 <= it.z; i0 += U) {
+      float2 e[U];                                         // maximum and sum of the row
+      float4 v[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k;
+        const float *part = c.part + (long)(2 * i + (i == first)) * TC_PART_FLOATS;
+        e[k] = make_float2(-INFINITY, 0.0f);
+        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i <= it.z) {
+          e[k] = __ldcg(reinterpret_cast<const float2 *>(part + ROWS * D + 2 * r));
+          v[k] = __ldcg(reinterpret_cast<const float4 *>(part + r * D) + ch);
+        }
+      }
+      float m = M;
+#pragma unroll
+      for (int k = 0; k < U; ++k) m = fmaxf(m, e[k].x);
+      const float f = M == -INFINITY ? 0.0f : exp2_approx(M - m);
+      y.x *= f, y.y *= f, y.z *= f, y.w *= f;
+      L *= f;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const float w = e[k].x == -INFINITY ? 0.0f : exp2_approx(e[k].x - m);
+        L = fmaf(w, e[k].y, L);
+        y.x = fmaf(w, v[k].x, y.x), y.y = fmaf(w, v[k].y, y.y), y.z = fmaf(w, v[k].z, y.z), y.w = fmaf(w, v[k].w, y.w);
+      }
       M = m;
     }
-    top[r] = M;
-    inv[r] = (row0 + r) / G < fresh && L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = t < it.w && L > 0.0f ? 1.0f / L : 0.0f;
+    *reinterpret_cast<uint2 *>(p.o.p + (it.x * p.o.sb + (long)t * p.o.st + (long)(h * G + row - t * G) * p.o.sh + ch * 4) * 2) =
+        make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
   }
-  constexpr int CH = D / 4, U = 8;                     // 16-byte pieces of a row; pieces a thread has under way
-  static_assert(ROWS * CH % (THREADS * U) == 0 || (ROWS * CH >= THREADS && ROWS * CH <= THREADS * U), "every thread takes the same rounds");
-  __syncthreads();
-  for (int x0 = threadIdx.x; x0 < ROWS * CH; x0 += THREADS * U) {
-    float4 y[U];
-#pragma unroll
-    for (int q = 0; q < U; ++q) y[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = first; i0 <= last; i0 += BATCH) {
-      const int n = min(BATCH, last - i0 + 1);
-      __syncthreads();
-      for (int x = threadIdx.x; x < rows * n; x += THREADS) {
-        const int r = x % rows, i = x / rows;
-        const float m = __ldcg(part(i0 + i) + ROWS * D + 2 * r);
-        factor[i * ROWS + r] = m == -INFINITY ? 0.0f : exp2_approx(m - top[r]);
-      }
-      __syncthreads();
-      for (int i = 0; i < n; i += 2) {
-        float4 v[2][U];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int q = 0; q < U; ++q) {
-            const int x = x0 + q * THREADS;
-            v[k][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i + k < n && x < rows * CH) v[k][q] = __ldcg(reinterpret_cast<const float4 *>(part(i0 + i + k)) + x);
-          }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int q = 0; q < U; ++q) {
-            const int r = (x0 + q * THREADS) / CH;
-            const float f = i + k < n && r < rows ? factor[(i + k) * ROWS + r] : 0.0f;
-            y[q].x = fmaf(f, v[k][q].x, y[q].x), y[q].y = fmaf(f, v[k][q].y, y[q].y);
-            y[q].z = fmaf(f, v[k][q].z, y[q].z), y[q].w = fmaf(f, v[k][q].w, y[q].w);
-          }
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const int x = x0 + q * THREADS, r = x / CH, rr = row0 + r, t = rr / G;
-      if (r >= rows) continue;
-      const float f = inv[r];
-      *reinterpret_cast<uint2 *>(p.o.p + (b * p.o.sb + (long)t * p.o.st + (long)(h * G + rr - t * G) * p.o.sh + (x % CH) * 4) * 2) =
-          make_uint2(pack_bf16x2(y[q].x * f, y[q].y * f), pack_bf16x2(y[q].z * f, y[q].w * f));
-    }
-  }
-  __syncthreads();
 }
 
 template <int D, int BITS, int MODE>
@@ -219,7 +218,6 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
            *q_ready = pv_done + 2 * NWG, *par_full = q_ready + NWG, *par_free = par_full + 2, *drain = par_free + 2;
   int *raw_flags = reinterpret_cast<int *>(smem + S::OMISC);            // [RS]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_flags + 4);
-  int *join_flag = raw_flags + 5;
   unsigned *wsum = reinterpret_cast<unsigned *>(smem + S::OCUM);
   unsigned *cum = wsum + 64;
   Seq *seq = reinterpret_cast<Seq *>(cum + c.batch + 1);
@@ -234,7 +232,6 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], S::NDEQ), mbar_init(&v_free[i], S::NRB);
     for (int i = 0; i < 2 * NWG; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 4), mbar_init(&pv_done[i], 1);
     for (int i = 0; i < NWG; ++i) mbar_init(&q_ready[i], 4);
-    join_flag[0] = 0;
     for (int i = 0; i < 2; ++i) mbar_init(&par_full[i], 2), mbar_init(&par_free[i], S::NDEQ);
     mbar_init(drain, NWG);
     mbar_fence_init();
@@ -252,6 +249,12 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   unsigned lo, hi;
   const Cuts cuts = make_cuts<KVT>(seq, cum, c.batch, (unsigned)p.row_blocks * c.Hkv, most, TC_LEAST, TC_WHOLE, TC_EXTRA, lo, hi);
   auto at = [&](unsigned pos) { return segment_at<KVT>(seq, cum, c.batch, p.row_blocks, pos, hi); };
+  if (tid == 0) {
+    const Segment end = lo < hi ? at(hi - 1) : Segment{};
+    const bool on = lo < hi && hi - 1 - end.tile >= lo && end.end < end.tiles;
+    tc_shared(c)[blockIdx.x] = on ? make_int4(end.b, end.h * p.row_blocks + end.rb, (int)((hi - 1 - end.tile + end.tiles - 1) / cuts.share), seq[end.b].fresh)
+                                  : make_int4(-1, 0, 0, 0);
+  }
   // A role whose wait gives up goes on without waiting or touching the tensor cores, but keeps the barriers it shares, so that no
   // other warp is left at one; the others' waits then run out too.
   auto gave_up = [&]() { atomicOr(c.status, PACE_KV_TIMEOUT); };
@@ -887,7 +890,6 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           part[S::ROWS * D + 2 * prow + 1] = Ls;
         }
       }
-      if (!whole && tid == 0) join_flag[0] |= sg.tile ? 1 : 2;          // began in an earlier block, or goes on in a later one
       fence_before_sync();
       if (NWG == 2) bar_sync(2, 256);                     // both groups have read what the next segment overwrites
       ntile += tiles;
@@ -898,35 +900,6 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   __syncthreads();
   fence_after_sync();
   if (warp == S::W_MMA) tmem_dealloc(*tmem_slot, 512);
-  // ---- items that several blocks share: the last to arrive joins the parts in block order
-  const int pseg = join_flag[0];
-  if (pseg) {
-    auto shared = [&](int k, Segment &it, int &first, int &last) {        // the item of the block's first tile, or of its last
-      const unsigned pos = k ? hi - 1 : lo;
-      it = at(pos);
-      first = (int)((pos - it.tile) / cuts.share);
-      last = (int)((pos - it.tile + it.tiles - 1) / cuts.share);
-    };
-    if (tid < 2) {
-      bool joins = false;
-      if ((pseg >> tid) & 1) {
-        Segment it;
-        int first, last;
-        shared(tid, it, first, last);
-        joins = last_part(&c.count[first], last - first + 1);
-      }
-      join_flag[1 + tid] = joins;
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k)
-      if (join_flag[1 + k]) {
-        Segment it;
-        int first, last;
-        shared(k, it, first, last);
-        tc_join<D, S::ROWS, S::THREADS>(p, first, last, it.b, it.h, it.rb * S::ROWS, seq[it.b].fresh, reinterpret_cast<float *>(smem));
-      }
-  }
 }
 
 template <int D, int BITS, int MODE>
@@ -943,7 +916,10 @@ cudaError_t launch_attend_tc(AttendArgs a, cudaStream_t s) {
     grid = std::min(grid, line);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)grid), dim3(S::THREADS), smem, s, attr);
-    return cudaLaunchKernelEx(&cfg, K, part);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, K, part);
+    if (e != cudaSuccess) return e;
+    const cudaLaunchConfig_t join = pdl_config(dim3((unsigned)device_sm_count() * 4), dim3(JOIN_THREADS), 0, s, attr);
+    return cudaLaunchKernelEx(&join, tc_join_kernel<D, S::ROWS>, part, (int)grid);
   });
 }
 
