@@ -57,8 +57,8 @@ struct TcShape {
   static constexpr int PAR = 2 * L::NG * KVT * PB;                      // of a tile
   static constexpr int OEXP = OPAR + 2 * PAR;                           // exponents [8 tiles][k, v][64] int8
   static constexpr int OOWN = OEXP + 8 * 2 * KVT;                       // whether a tile's tokens have their own [8][k, v]
-  static constexpr int OML = OOWN + 16;                                 // m, l, exponent of group 1 (ALT)
-  static constexpr int OBAR = OML + 128 * 12;
+  static constexpr int OML = OOWN + 16;                                 // m, l, exponent of each group's rows (ALT); each row's factor
+  static constexpr int OBAR = OML + 128 * 32;
   static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 7 * NWG + 5;
   static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base
   static constexpr int OCUM = (OMISC + 32 + 15) / 16 * 16;
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) tc_join_kernel(AttendArgs p, 
   for (int unit = blockIdx.x; unit < n * SLICES; unit += gridDim.x) {
     const int first = list[unit / SLICES], r = (unit % SLICES) * SLICE + tid / CH, ch = tid % CH;
     const int4 it = __ldcg(&tc_shared(c)[first]);
-    const int h = it.y / p.row_blocks, row = (it.y - h * p.row_blocks) * ROWS + r, t = row / G;
+    const int h = it.y / p.row_blocks, row = (it.y - h * p.row_blocks) * ROWS + r, t = row_token(p, row);
     if (row >= c.n_tokens * G) continue;
     float M = -INFINITY, L = 0.0f;
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       const int tiles = sg.end - sg.tile;
       const int len = seq[sg.b].len, nn = seq[sg.b].fresh;
       const int row = sg.rb * S::ROWS + (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
-      const int t = row / G, hh = sg.h * G + row - t * G;
+      const int t = row_token(p, row), hh = sg.h * G + row - t * G;
       const bool in = row < T * G;
       // ---- the row's query as fp16 over a power of two, for the products (ALT: group 0 writes, group 1 only needs the power)
       float crow = 0.0f;
@@ -588,8 +588,9 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           char *block = smem + S::OQ + blk * S::QB;
           constexpr int CH = D / 8, STRIDE = MODE == TC_ALT ? 256 : 128;
           const int r0 = sg.rb * S::ROWS + blk * 128;
+#pragma unroll 4
           for (int x = MODE == TC_ALT ? tid : row_lane; x < 128 * CH; x += STRIDE) {
-            const int r = x / CH, ch = x % CH, rr = r0 + r, tt = rr / G;
+            const int r = x / CH, ch = x % CH, rr = r0 + r, tt = row_token(p, rr);
             const bool ok = rr < T * G;
             const char *src = ok ? p.q.p + (sg.b * p.q.sb + (long)tt * p.q.st + (long)(sg.h * G + rr - tt * G) * p.q.sh + ch * 8) * 2 : p.q.p;
             cp_async16(block + (r >> 3) * CH * 128 + ch * 128 + (r & 7) * 16, src, ok);
@@ -803,29 +804,29 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       int E0 = E, E1 = 0;
       bool two = false;
       if (MODE == TC_ALT) {
-        float *mlp = reinterpret_cast<float *>(smem + S::OML) + row_lane * 3;
-        if (w == 1) mlp[0] = m, mlp[1] = l, mlp[2] = (float)E;
+        float *mlp = reinterpret_cast<float *>(smem + S::OML) + row_lane * 6;
+        mlp[3 * w] = m, mlp[3 * w + 1] = l, mlp[3 * w + 2] = (float)E;
         fence_before_sync();
         bar_sync(2, 256);
         fence_after_sync();
-        if (w == 0) {
-          const float m1 = mlp[0];
-          two = tiles > 1;
-          M = fmaxf(m, m1);
-          f0 = m == -INFINITY ? 0.0f : exp2_approx(m - M);
-          f1 = m1 == -INFINITY ? 0.0f : exp2_approx(m1 - M);
-          Ls = f0 * l + f1 * mlp[1];
-          E1 = (int)mlp[2];
-        }
+        two = tiles > 1;
+        M = fmaxf(mlp[0], mlp[3]);
+        f0 = mlp[0] == -INFINITY ? 0.0f : exp2_approx(mlp[0] - M);
+        f1 = mlp[3] == -INFINITY ? 0.0f : exp2_approx(mlp[3] - M);
+        Ls = f0 * mlp[1] + f1 * mlp[4];
+        E0 = (int)mlp[2];
+        E1 = (int)mlp[5];
       }
-      if (MODE != TC_ALT || w == 0) {                      // (outputs of a call whose wait gave up are not to be used)
+      {                                                    // (outputs of a call whose wait gave up are not to be used)
+        const int K0 = MODE == TC_ALT ? w * (D / 32) : 0, K1 = MODE == TC_ALT ? K0 + D / 32 : D / 16;     // (ALT: each group half of the columns)
+        const uint32_t tO0 = tmem + lanes + S::CO + (MODE == TC_ALT ? 0 : w * D);
         const float inv = t < nn && Ls > 0.0f ? 1.0f / Ls : 0.0f;
         const float g0 = f0 * exp2i(E0), g1 = f1 * exp2i(E1);
         char *dst = p.o.p + (sg.b * p.o.sb + (long)t * p.o.st + (long)hh * p.o.sh) * 2;
         auto columns = [&](int k, float (&y)[16]) {       // columns 16k .. of the row
           uint32_t r[16], r1[16];
-          tmem_ld16(tO + 16 * k, r);
-          if (MODE == TC_ALT && two) tmem_ld16(tO + D + 16 * k, r1);
+          tmem_ld16(tO0 + 16 * k, r);
+          if (MODE == TC_ALT && two) tmem_ld16(tO0 + D + 16 * k, r1);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -836,10 +837,12 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         if (S::QSMEM) {
           // through the block's query area, a quarter of the columns at a time, so that rows leave in whole lines: 16-byte piece i of a
           // row lies at i ^ (row & 7), eight a row
-          char *area = smem + S::OQ + (MODE == TC_SHARE ? w : 0) * S::QB;
+          char *area = smem + S::OQ + w * (MODE == TC_SHARE ? S::QB : S::QB / 2);
+          float *factor = reinterpret_cast<float *>(smem + S::OML) + 128 * 6 + w * 128;
           constexpr int PC = 8;
+          factor[row_lane] = inv;
 #pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
+          for (int k = K0 / 2; k < K1 / 2; ++k) {
             float y[2][16];
             columns(2 * k, y[0]);
             columns(2 * k + 1, y[1]);
@@ -848,7 +851,6 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             for (int i = 0; i < PC; ++i)
               *reinterpret_cast<float4 *>(area + row_lane * 128 + (i ^ (row_lane & 7)) * 16) =
                   make_float4(y[i >> 2][4 * i & 15], y[i >> 2][(4 * i + 1) & 15], y[i >> 2][(4 * i + 2) & 15], y[i >> 2][(4 * i + 3) & 15]);
-            if (whole && k == 0) reinterpret_cast<float *>(area + 128 * 128)[row_lane] = inv;
             bar_sync(3 + w, 128);
 #pragma unroll 4
             for (int x = row_lane; x < 128 * PC; x += 128) {
@@ -857,8 +859,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
               if (!whole) {
                 *reinterpret_cast<float4 *>(part + ((MODE == TC_SHARE ? w * 128 : 0) + r) * D + 32 * k + 4 * i) = v;
               } else if (rr < T * G) {
-                const int tt = rr / G;
-                const float f = reinterpret_cast<const float *>(area + 128 * 128)[r];
+                const int tt = row_token(p, rr);
+                const float f = factor[r];
                 *reinterpret_cast<uint2 *>(p.o.p + (sg.b * p.o.sb + (long)tt * p.o.st + (long)(sg.h * G + rr - tt * G) * p.o.sh + 32 * k + 4 * i) * 2) =
                     make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
               }
@@ -867,7 +869,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           bar_sync(3 + w, 128);                           // (the next queries come here)
         } else {
 #pragma unroll 1
-          for (int k = 0; k < D / 16; ++k) {
+          for (int k = K0; k < K1; ++k) {
             float y[16];
             columns(k, y);
             if (whole) {
@@ -885,7 +887,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             }
           }
         }
-        if (!whole) {
+        if (!whole && (MODE != TC_ALT || w == 0)) {
           part[S::ROWS * D + 2 * prow] = M;
           part[S::ROWS * D + 2 * prow + 1] = Ls;
         }
