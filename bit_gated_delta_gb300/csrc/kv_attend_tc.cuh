@@ -57,8 +57,8 @@ struct TcShape {
   static constexpr int PAR = 2 * L::NG * KVT * PB;                      // of a tile
   static constexpr int OEXP = OPAR + 2 * PAR;                           // exponents [8 tiles][k, v][64] int8
   static constexpr int OOWN = OEXP + 8 * 2 * KVT;                       // whether a tile's tokens have their own [8][k, v]
-  static constexpr int OML = OOWN + 16;                                 // m, l, exponent of each group's rows (ALT); each row's factor
-  static constexpr int OBAR = OML + 128 * 32;
+  static constexpr int OML = OOWN + 16;                                 // m, l, exponent of each group's rows (ALT)
+  static constexpr int OBAR = OML + 128 * 24;
   static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 7 * NWG + 5;
   static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base
   static constexpr int OCUM = (OMISC + 32 + 15) / 16 * 16;
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       const int row = sg.rb * S::ROWS + (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
       const int t = row_token(p, row), hh = sg.h * G + row - t * G;
       const bool in = row < T * G;
-      // ---- the row's query as fp16 over a power of two, for the products (ALT: group 0 writes, group 1 only needs the power)
+      // ---- the row's query as fp16 over a power of two, for the products (ALT: both groups read the row, each converts half of it)
       float crow = 0.0f;
       if (good) {
         const int blk = MODE == TC_SHARE ? w : 0;
@@ -590,7 +590,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           const int r0 = sg.rb * S::ROWS + blk * 128;
 #pragma unroll 4
           for (int x = MODE == TC_ALT ? tid : row_lane; x < 128 * CH; x += STRIDE) {
-            const int r = x / CH, ch = x % CH, rr = r0 + r, tt = row_token(p, rr);
+            // (four pieces of eight rows a warp: its writes to shared memory meet no bank twice)
+            const int r = (x >> 5) / (CH / 4) * 8 + (x & 7), ch = (x >> 5) % (CH / 4) * 4 + ((x >> 3) & 3), rr = r0 + r, tt = row_token(p, rr);
             const bool ok = rr < T * G;
             const char *src = ok ? p.q.p + (sg.b * p.q.sb + (long)tt * p.q.st + (long)(sg.h * G + rr - tt * G) * p.q.sh + ch * 8) * 2 : p.q.p;
             cp_async16(block + (r >> 3) * CH * 128 + ch * 128 + (r & 7) * 16, src, ok);
@@ -607,43 +608,55 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           }
           power();
           if (MODE == TC_ALT) bar_sync(2, 256);           // (both groups have read)
-          if (MODE != TC_ALT || w == 0) {
+          auto put = [&](auto from, auto to) {
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
+            for (int i = decltype(from)::value; i < decltype(to)::value; ++i)
               *reinterpret_cast<uint4 *>(mine + i * 128) = make_uint4(conv(x[i].x ^ flip), conv(x[i].y ^ flip), conv(x[i].z ^ flip), conv(x[i].w ^ flip));
-            fence_smem_to_async();
-          }
+          };
+          using std::integral_constant;
+          if (MODE != TC_ALT) put(integral_constant<int, 0>{}, integral_constant<int, CH>{});
+          else if (w == 0) put(integral_constant<int, 0>{}, integral_constant<int, CH / 2>{});         // (each group half of the row)
+          else put(integral_constant<int, CH / 2>{}, integral_constant<int, CH>{});
+          fence_smem_to_async();
         } else {
           const char *src = p.q.p + (sg.b * p.q.sb + (long)t * p.q.st + (long)hh * p.q.sh) * 2;
-          constexpr int HALF = D > 128 ? 2 : 1;           // (at D = 256 in two passes over the row: registers)
+          constexpr int HALF = D > 128 ? 2 : 1;           // (at D = 256 the row waits in TMEM where the converted one will be: registers)
           uint4 x[D / 8 / HALF];
           auto load = [&](int h) {
 #pragma unroll
             for (int i = 0; i < D / 8 / HALF; ++i)
               x[i] = in ? reinterpret_cast<const uint4 *>(src)[h * (D / 8 / HALF) + i] : make_uint4(0, 0, 0, 0);
           };
+          const uint32_t tQ = tmem + lanes + S::CQ + blk * (D / 2);
           for (int h = 0; h < HALF; ++h) {
             load(h);
 #pragma unroll
             for (int i = 0; i < D / 8 / HALF; ++i) widen(x[i]);
-          }
-          power();
-          if (MODE != TC_ALT || w == 0) {
-            for (int h = 0; h < HALF; ++h) {
-              if (HALF > 1) load(h);
+            if (HALF > 1) {
 #pragma unroll
               for (int i = 0; i < D / 32 / HALF; ++i) {
                 uint32_t r[16];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint4 y = x[4 * i + k];
-                  r[4 * k] = conv(y.x ^ flip), r[4 * k + 1] = conv(y.y ^ flip), r[4 * k + 2] = conv(y.z ^ flip), r[4 * k + 3] = conv(y.w ^ flip);
-                }
-                tmem_st16(tmem + lanes + S::CQ + blk * (D / 2) + 16 * (h * (D / 32 / HALF) + i), r);
+                for (int k = 0; k < 16; ++k) r[k] = (&x[4 * i + (k >> 2)].x)[k & 3];
+                tmem_st16(tQ + 16 * (h * (D / 32 / HALF) + i), r);
               }
             }
-            tmem_wait_st();
           }
+          if (HALF > 1) tmem_wait_st();
+          power();
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            if (MODE == TC_ALT && (i & 1) != w) continue;                 // (each group half of the row)
+            uint32_t r[16];
+            if (HALF > 1) {
+              tmem_ld16(tQ + 16 * i, r);
+              tmem_wait_ld();
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) r[k] = conv((HALF > 1 ? r[k] : (&x[4 * (HALF > 1 ? 0 : i) + (k >> 2)].x)[k & 3]) ^ flip);
+            tmem_st16(tQ + 16 * i, r);
+          }
+          tmem_wait_st();
         }
       } else if (S::QSMEM) {                              // (the barriers of the other side)
         if (MODE == TC_ALT) bar_sync(2, 256), bar_sync(2, 256);
@@ -652,7 +665,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       constexpr int STEP = MODE == TC_ALT ? 2 : 1;
       const int i0 = MODE == TC_ALT ? w : 0;
       fence_before_sync();
-      if (MODE == TC_ALT) bar_sync(2, 256);               // (group 1 uses what group 0 wrote)
+      if (MODE == TC_ALT) bar_sync(2, 256);               // (each group uses what both wrote)
       __syncwarp();
       if (lane == 0 && good && i0 < tiles) mbar_arrive(&q_ready[w]);
       float m = -INFINITY, l = 0.0f;
@@ -835,35 +848,54 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           }
         };
         if (S::QSMEM) {
-          // through the block's query area, a quarter of the columns at a time, so that rows leave in whole lines: 16-byte piece i of a
-          // row lies at i ^ (row & 7), eight a row
+          // through the block's query area, 128 bytes of each row at a time, so that rows leave in whole lines: 16-byte piece i of a row
+          // lies at i ^ (row & 7)
           char *area = smem + S::OQ + w * (MODE == TC_SHARE ? S::QB : S::QB / 2);
-          float *factor = reinterpret_cast<float *>(smem + S::OML) + 128 * 6 + w * 128;
           constexpr int PC = 8;
-          factor[row_lane] = inv;
-#pragma unroll 1
-          for (int k = K0 / 2; k < K1 / 2; ++k) {
-            float y[2][16];
-            columns(2 * k, y[0]);
-            columns(2 * k + 1, y[1]);
-            bar_sync(3 + w, 128);                         // the quarter before has left
+          auto exchange = [&](const uint4 (&z)[PC], auto &&store) {
+            bar_sync(3 + w, 128);                         // the columns before have left
 #pragma unroll
-            for (int i = 0; i < PC; ++i)
-              *reinterpret_cast<float4 *>(area + row_lane * 128 + (i ^ (row_lane & 7)) * 16) =
-                  make_float4(y[i >> 2][4 * i & 15], y[i >> 2][(4 * i + 1) & 15], y[i >> 2][(4 * i + 2) & 15], y[i >> 2][(4 * i + 3) & 15]);
+            for (int i = 0; i < PC; ++i) *reinterpret_cast<uint4 *>(area + row_lane * 128 + (i ^ (row_lane & 7)) * 16) = z[i];
             bar_sync(3 + w, 128);
 #pragma unroll 4
             for (int x = row_lane; x < 128 * PC; x += 128) {
-              const int r = x / PC, i = x % PC, rr = sg.rb * S::ROWS + (MODE == TC_SHARE ? w * 128 : 0) + r;
-              const float4 v = *reinterpret_cast<const float4 *>(area + r * 128 + (i ^ (r & 7)) * 16);
-              if (!whole) {
-                *reinterpret_cast<float4 *>(part + ((MODE == TC_SHARE ? w * 128 : 0) + r) * D + 32 * k + 4 * i) = v;
-              } else if (rr < T * G) {
-                const int tt = row_token(p, rr);
-                const float f = factor[r];
-                *reinterpret_cast<uint2 *>(p.o.p + (sg.b * p.o.sb + (long)tt * p.o.st + (long)(sg.h * G + rr - tt * G) * p.o.sh + 32 * k + 4 * i) * 2) =
-                    make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+              const int r = x / PC, i = x % PC;
+              store(r, i, *reinterpret_cast<const uint4 *>(area + r * 128 + (i ^ (r & 7)) * 16));
+            }
+          };
+          const int r0 = MODE == TC_SHARE ? w * 128 : 0;
+          if (whole) {
+#pragma unroll 1
+            for (int k = K0; k < K1; k += 4) {
+              uint4 z[PC];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float y[16];
+                columns(k + j, y);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  z[2 * j + h] = make_uint4(pack_bf16x2(y[8 * h] * inv, y[8 * h + 1] * inv), pack_bf16x2(y[8 * h + 2] * inv, y[8 * h + 3] * inv),
+                                            pack_bf16x2(y[8 * h + 4] * inv, y[8 * h + 5] * inv), pack_bf16x2(y[8 * h + 6] * inv, y[8 * h + 7] * inv));
               }
+              exchange(z, [&](int r, int i, const uint4 &v) {
+                const int rr = sg.rb * S::ROWS + r0 + r, tt = row_token(p, rr);
+                if (rr < T * G)
+                  *reinterpret_cast<uint4 *>(p.o.p + (sg.b * p.o.sb + (long)tt * p.o.st + (long)(sg.h * G + rr - tt * G) * p.o.sh + 16 * k + 8 * i) * 2) = v;
+              });
+            }
+          } else {
+#pragma unroll 1
+            for (int k = K0; k < K1; k += 2) {
+              uint4 z[PC];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float y[16];
+                columns(k + j, y);
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                  z[4 * j + h] = make_uint4(__float_as_uint(y[4 * h]), __float_as_uint(y[4 * h + 1]), __float_as_uint(y[4 * h + 2]), __float_as_uint(y[4 * h + 3]));
+              }
+              exchange(z, [&](int r, int i, const uint4 &v) { *reinterpret_cast<uint4 *>(part + (r0 + r) * D + 16 * k + 4 * i) = v; });
             }
           }
           bar_sync(3 + w, 128);                           // (the next queries come here)
