@@ -43,7 +43,7 @@ struct TcShape {
   static constexpr int RS = BITS == 4 ? (D == 256 ? 3 : 4) : (D == 256 || (MODE == TC_ALT && D == 128) ? 2 : 4);
   static constexpr int NDEQ = MODE == TC_SHARE ? 4 : 8;                 // dequantizing warps (SHARE: a tile serves two row blocks)
   static constexpr int W_DEQ = 4 * NWG, W_PAR = W_DEQ + NDEQ, W_MMA = W_PAR + 2;
-  static constexpr int WARPS = (W_MMA + NWG + 3) / 4 * 4, THREADS = WARPS * 32;
+  static constexpr int WARPS = W_MMA + NWG, THREADS = WARPS * 32;
   // TMEM columns: O, two score tiles a group (each later its weights), and Q where it fits beside them; else Q is in shared memory
   static constexpr bool QSMEM = D == 128;
   static constexpr int CO = 0, CS = NWG * D, CQ = CS + NWG * 2 * KVT;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         const int rs = n % RS;
         const char *raw = smem + S::ORAW + rs * S::RAW;
         char *par = smem + S::OPAR + (n & 1) * S::PAR;
-        good = good && bar_wait(&raw_full[rs], (n / RS) & 1) && bar_wait(&par_full[n & 1], (n >> 1) & 1);
+        good = good && bar_wait(&par_full[n & 1], (n >> 1) & 1);          // (the warps that prepare scales have waited for the tile)
         good = __all_sync(0xffffffffu, good);
         if (!good) continue;
         // codes: warp = 8 or 16 tokens; eight lanes write eight tokens' pieces of one 128-byte core
@@ -383,44 +383,49 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     const int pw = warp - S::W_PAR, ps = L::pos(lane), vp = L::vpos(lane);
     int n = 0;
     bool good = true;
-    // the copying side, RS - 1 tiles ahead (first of the two warps): segment, storage tiles [at, end) of it, and the pool index of the
-    // 32 from `base` on, one a lane
+    // the copying side, RS - 1 tiles ahead, the two warps in turn: segment, storage tiles [at, end) of it, and pool indexes, one a lane:
+    // of the 32 from `base` on, and of the 32 after those (their look-up is under way meanwhile)
     const int tpp = c.page / TILE;
     unsigned lpos = lo;
     Segment ls{0, 0, 0, 0, 0, 0};
-    int lat = 0, lend = 0, lbase = 0, mytile = -2, copied = 0;
+    int lat = 0, lend = 0, lbase = 0, mytile = -2, later = -2, copied = 0;
+    auto look_up = [&](int t) { return t < lend && t * TILE < seq[ls.b].tokens ? tile_index(c, ls.b, ls.h, t, tpp) : -2; };
     auto copy_next = [&]() {
       if (lat >= lend) {
         if (lpos >= hi) return;
         ls = at(lpos);
         lpos += ls.end - ls.tile;
-        lat = 2 * ls.tile;
+        lat = lbase = 2 * ls.tile;
         lend = 2 * ls.end;
-        lbase = lat - 32;
+        mytile = look_up(lat + lane);
+        later = look_up(lat + 32 + lane);
+        if (mytile == -1) atomicOr(c.status, PACE_KV_BAD_PAGE);
       }
       if (lat - lbase >= 32) {
         lbase = lat;
-        mytile = lat + lane < lend && (lat + lane) * TILE < seq[ls.b].tokens ? tile_index(c, ls.b, ls.h, lat + lane, tpp) : -2;
+        mytile = later;
+        later = look_up(lat + 32 + lane);
         if (mytile == -1) atomicOr(c.status, PACE_KV_BAD_PAGE);
       }
-      const int pa = __shfl_sync(0xffffffffu, mytile, lat - lbase), pb = __shfl_sync(0xffffffffu, mytile, lat - lbase + 1);
-      const int stage = copied % RS;
-      if (copied >= RS) good = __all_sync(0xffffffffu, good && bar_wait(&raw_free[stage], (copied / RS - 1) & 1));
-      if (!good) return;
-      if (lane == 0) {
-        raw_flags[stage] = (pa >= 0 ? 1 : 0) | (pb >= 0 ? 2 : 0);
-        const uint32_t bytes = ((pa >= 0) + (pb >= 0)) * L::BYTES;
-        if (bytes) mbar_arrive_expect_tx(&raw_full[stage], bytes);
-        else mbar_arrive(&raw_full[stage]);
-        char *dst = smem + S::ORAW + stage * S::RAW;
-        if (pa >= 0) bulk_g2s(dst, c.pool + (long)pa * L::BYTES, L::BYTES, &raw_full[stage]);
-        if (pb >= 0) bulk_g2s(dst + L::BYTES, c.pool + (long)pb * L::BYTES, L::BYTES, &raw_full[stage]);
+      if ((copied & 1) == pw) {
+        const int pa = __shfl_sync(0xffffffffu, mytile, lat - lbase), pb = __shfl_sync(0xffffffffu, mytile, lat - lbase + 1);
+        const int stage = copied % RS;
+        if (copied >= RS) good = __all_sync(0xffffffffu, good && bar_wait(&raw_free[stage], (copied / RS - 1) & 1));
+        if (!good) return;
+        if (lane == 0) {
+          raw_flags[stage] = (pa >= 0 ? 1 : 0) | (pb >= 0 ? 2 : 0);
+          const uint32_t bytes = ((pa >= 0) + (pb >= 0)) * L::BYTES;
+          if (bytes) mbar_arrive_expect_tx(&raw_full[stage], bytes);
+          else mbar_arrive(&raw_full[stage]);
+          char *dst = smem + S::ORAW + stage * S::RAW;
+          if (pa >= 0) bulk_g2s(dst, c.pool + (long)pa * L::BYTES, L::BYTES, &raw_full[stage]);
+          if (pb >= 0) bulk_g2s(dst + L::BYTES, c.pool + (long)pb * L::BYTES, L::BYTES, &raw_full[stage]);
+        }
       }
       ++copied;
       lat += 2;
     };
-    if (pw == 0)
-      for (int i = 0; i < RS - 1; ++i) copy_next();
+    for (int i = 0; i < RS - 1; ++i) copy_next();
     for (unsigned pos = lo; pos < hi;) {
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
@@ -477,12 +482,12 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         }
         __syncwarp();
         if (lane == 0 && good) mbar_arrive(&par_full[n & 1]);
-        if (pw == 0) copy_next();
+        copy_next();
       }
     }
     if (!good && lane == 0) gave_up();
-    if (pw == 0)                                          // copies still in flight land before the block leaves
-      for (int i = max(0, copied - RS); i < copied; ++i) bar_wait(&raw_full[i % RS], (i / RS) & 1);
+    for (int i = max(0, copied - RS); i < copied; ++i)    // the warp's copies still in flight land before the block leaves
+      if ((i & 1) == pw) bar_wait(&raw_full[i % RS], (i / RS) & 1);
   } else if (warp >= S::W_MMA && warp < S::W_MMA + NWG) {
     // ---------------------------------------------------------------- a group's products. The warp runs as one, so that descriptors and
     // addresses stay in uniform registers; one lane issues. Products run in the order of issue: a score tile may overwrite weights
