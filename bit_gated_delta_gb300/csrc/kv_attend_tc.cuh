@@ -58,7 +58,11 @@ struct TcShape {
   static constexpr int OEXP = OPAR + 2 * PAR;                           // exponents [8 tiles][k, v][64] int8
   static constexpr int OOWN = OEXP + 8 * 2 * KVT;                       // whether a tile's tokens have their own [8][k, v]
   static constexpr int OML = OOWN + 16;                                 // m, l, exponent of each group's rows (ALT)
-  static constexpr int OBAR = OML + 128 * 24;
+  // where each softmax warp turns its rows' outputs, ROWB bytes of a row at a time: the queries' area where there is one
+  static constexpr int ROWB = QSMEM ? 128 : 64;
+  static constexpr int OOUT = QSMEM ? OQ : OML + (MODE == TC_ALT ? 128 * 24 : 0);
+  static constexpr int OBAR = QSMEM ? OML + (MODE == TC_ALT ? 128 * 24 : 0) : OOUT + 4 * NWG * 32 * ROWB;
+  static_assert(!QSMEM || NRB * QB >= 4 * NWG * 32 * ROWB, "outputs");
   static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 7 * NWG + 5;
   static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base
   static constexpr int OCUM = (OMISC + 32 + 15) / 16 * 16;
@@ -840,7 +844,6 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         const uint32_t tO0 = tmem + lanes + S::CO + (MODE == TC_ALT ? 0 : w * D);
         const float inv = t < nn && Ls > 0.0f ? 1.0f / Ls : 0.0f;
         const float g0 = f0 * exp2i(E0), g1 = f1 * exp2i(E1);
-        char *dst = p.o.p + (sg.b * p.o.sb + (long)t * p.o.st + (long)hh * p.o.sh) * 2;
         auto columns = [&](int k, float (&y)[16]) {       // columns 16k .. of the row
           uint32_t r[16], r1[16];
           tmem_ld16(tO0 + 16 * k, r);
@@ -852,76 +855,51 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             if (MODE == TC_ALT && two) y[e] = fmaf(__uint_as_float(r1[e]), g1, y[e]);
           }
         };
-        if (S::QSMEM) {
-          // through the block's query area, 128 bytes of each row at a time, so that rows leave in whole lines: 16-byte piece i of a row
-          // lies at i ^ (row & 7)
-          char *area = smem + S::OQ + w * (MODE == TC_SHARE ? S::QB : S::QB / 2);
-          constexpr int PC = 8;
-          auto exchange = [&](const uint4 (&z)[PC], auto &&store) {
-            bar_sync(3 + w, 128);                         // the columns before have left
+        // through shared memory, so that rows leave in whole lines (or half lines): 16-byte piece i of a row lies at i ^ swizzle
+        constexpr int PC = S::ROWB / 16;
+        char *area = smem + S::OOUT + warp * 32 * S::ROWB;
+        auto slot = [&](int r, int i) { return area + r * S::ROWB + (i ^ (PC == 8 ? r & 7 : (r >> 1) & 3)) * 16; };
+        const int r0 = (MODE == TC_SHARE ? w * 128 : 0) + (warp & 3) * 32;
+        auto exchange = [&](const uint4 *z, auto &&store) {
+          __syncwarp();                                   // the columns before have left
 #pragma unroll
-            for (int i = 0; i < PC; ++i) *reinterpret_cast<uint4 *>(area + row_lane * 128 + (i ^ (row_lane & 7)) * 16) = z[i];
-            bar_sync(3 + w, 128);
+          for (int i = 0; i < PC; ++i) *reinterpret_cast<uint4 *>(slot(lane, i)) = z[i];
+          __syncwarp();
 #pragma unroll 4
-            for (int x = row_lane; x < 128 * PC; x += 128) {
-              const int r = x / PC, i = x % PC;
-              store(r, i, *reinterpret_cast<const uint4 *>(area + r * 128 + (i ^ (r & 7)) * 16));
-            }
-          };
-          const int r0 = MODE == TC_SHARE ? w * 128 : 0;
-          if (whole) {
+          for (int x = lane; x < 32 * PC; x += 32) store(r0 + x / PC, x % PC, *reinterpret_cast<const uint4 *>(slot(x / PC, x % PC)));
+        };
+        if (whole) {
 #pragma unroll 1
-            for (int k = K0; k < K1; k += 4) {
-              uint4 z[PC];
+          for (int k = K0; k < K1; k += PC / 2) {
+            uint4 z[PC];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float y[16];
-                columns(k + j, y);
+            for (int j = 0; j < PC / 2; ++j) {
+              float y[16];
+              columns(k + j, y);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  z[2 * j + h] = make_uint4(pack_bf16x2(y[8 * h] * inv, y[8 * h + 1] * inv), pack_bf16x2(y[8 * h + 2] * inv, y[8 * h + 3] * inv),
-                                            pack_bf16x2(y[8 * h + 4] * inv, y[8 * h + 5] * inv), pack_bf16x2(y[8 * h + 6] * inv, y[8 * h + 7] * inv));
-              }
-              exchange(z, [&](int r, int i, const uint4 &v) {
-                const int rr = sg.rb * S::ROWS + r0 + r, tt = row_token(p, rr);
-                if (rr < T * G)
-                  *reinterpret_cast<uint4 *>(p.o.p + (sg.b * p.o.sb + (long)tt * p.o.st + (long)(sg.h * G + rr - tt * G) * p.o.sh + 16 * k + 8 * i) * 2) = v;
-              });
+              for (int h = 0; h < 2; ++h)
+                z[2 * j + h] = make_uint4(pack_bf16x2(y[8 * h] * inv, y[8 * h + 1] * inv), pack_bf16x2(y[8 * h + 2] * inv, y[8 * h + 3] * inv),
+                                          pack_bf16x2(y[8 * h + 4] * inv, y[8 * h + 5] * inv), pack_bf16x2(y[8 * h + 6] * inv, y[8 * h + 7] * inv));
             }
-          } else {
-#pragma unroll 1
-            for (int k = K0; k < K1; k += 2) {
-              uint4 z[PC];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                float y[16];
-                columns(k + j, y);
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-                  z[4 * j + h] = make_uint4(__float_as_uint(y[4 * h]), __float_as_uint(y[4 * h + 1]), __float_as_uint(y[4 * h + 2]), __float_as_uint(y[4 * h + 3]));
-              }
-              exchange(z, [&](int r, int i, const uint4 &v) { *reinterpret_cast<uint4 *>(part + (r0 + r) * D + 16 * k + 4 * i) = v; });
-            }
+            exchange(z, [&](int r, int i, const uint4 &v) {
+              const int rr = sg.rb * S::ROWS + r, tt = row_token(p, rr);
+              if (rr < T * G)
+                *reinterpret_cast<uint4 *>(p.o.p + (sg.b * p.o.sb + (long)tt * p.o.st + (long)(sg.h * G + rr - tt * G) * p.o.sh + 16 * k + 8 * i) * 2) = v;
+            });
           }
-          bar_sync(3 + w, 128);                           // (the next queries come here)
         } else {
 #pragma unroll 1
-          for (int k = K0; k < K1; ++k) {
-            float y[16];
-            columns(k, y);
-            if (whole) {
-              if (in) {
+          for (int k = K0; k < K1; k += PC / 4) {
+            uint4 z[PC];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  reinterpret_cast<uint4 *>(dst)[2 * k + h] =
-                      make_uint4(pack_bf16x2(y[8 * h] * inv, y[8 * h + 1] * inv), pack_bf16x2(y[8 * h + 2] * inv, y[8 * h + 3] * inv),
-                                 pack_bf16x2(y[8 * h + 4] * inv, y[8 * h + 5] * inv), pack_bf16x2(y[8 * h + 6] * inv, y[8 * h + 7] * inv));
-              }
-            } else {
+            for (int j = 0; j < PC / 4; ++j) {
+              float y[16];
+              columns(k + j, y);
 #pragma unroll
               for (int h = 0; h < 4; ++h)
-                *reinterpret_cast<float4 *>(part + prow * D + 16 * k + 4 * h) = make_float4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]);
+                z[4 * j + h] = make_uint4(__float_as_uint(y[4 * h]), __float_as_uint(y[4 * h + 1]), __float_as_uint(y[4 * h + 2]), __float_as_uint(y[4 * h + 3]));
             }
+            exchange(z, [&](int r, int i, const uint4 &v) { *reinterpret_cast<uint4 *>(part + r * D + 16 * k + 4 * i) = v; });
           }
         }
         if (!whole && (MODE != TC_ALT || w == 0)) {
