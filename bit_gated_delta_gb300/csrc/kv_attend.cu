@@ -15,9 +15,12 @@ cudaError_t attend_tc_8(const AttendArgs &a, int rows, cudaStream_t s);
 using namespace pace::kv;
 
 namespace {
-// Rows of one KV head from which the tensor-memory kernel takes over (bf16 I/O).
+// Rows of one KV head from which the tensor-memory kernel takes over (bf16 I/O). It works on 128 rows whatever their number, and the
+// other on 8 to 32 at a time. Heads of 128, 16 sequences of 8000 tokens: 112 and 98 us at 32 rows, 112 and 141 us at 40; one sequence of
+// 2000 tokens: 17 and 15 us, 18 and 16 us. Heads of 256: 56 and 67 us, 56 and 81 us.
 constexpr int TC_ROWS = 33;
-constexpr int FEW_ITEMS = 64;
+// Rows of an item of the other kernel (fp32 I/O takes three products a tile, and eight rows).
+int block_rows(const KvDev &c) { return c.io == PACE_IO_F32 ? 8 : 2048 / c.d; }
 bool use_tc(int io, int rows) { return io == PACE_IO_BF16 && rows >= TC_ROWS; }
 }  // namespace
 
@@ -33,6 +36,10 @@ cudaError_t pace_launch_kv_attend(const KvDev &c, const KvTensor &q, const uint3
   AttendArgs a{c, q, o, mask, scale * 1.44269504088896340736f, 0, (0x80000000u + c.group - 1) / c.group};
   const int rows = c.n_tokens * c.group;
   if (use_tc(c.io, rows)) return c.bits == 4 ? attend_tc_4(a, rows, s) : attend_tc_8(a, rows, s);
-  const bool few = (long)c.batch * c.Hkv <= FEW_ITEMS;
+  // Blocks of 8 or 16 warps, one an SM, while there are no more items than SMs: an item then stays with one block, or few blocks join its
+  // results. Heads of 128, 4-bit, one token: 144 items of 700 tokens 12 us (smaller blocks 13), of 3000 tokens 22 (28); 160 items 20 (14)
+  // and 34 (29). Under 32 rows, two items a head: 64 heads of 3000 tokens 25 (29), 96 heads 40 (35).
+  const long items = (long)c.batch * c.Hkv * ((rows + block_rows(c) - 1) / block_rows(c));
+  const bool few = items <= pace::device_sm_count();
   return c.bits == 4 ? attend_4(a, rows, few, s) : attend_8(a, rows, few, s);
 }

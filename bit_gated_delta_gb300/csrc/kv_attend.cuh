@@ -171,7 +171,9 @@ struct AttendArgs {
   int row_blocks;       // items of one (sequence, KV head)
   uint32_t group_inv;   // ceil(2^31 / group)
 };
-// Token of a row, row / group: exact for rows below 2^31 / group (a division took ten times as long, and stood before every address).
+// Token of a row, row / group: exact for rows below 2^31 / group. The kernel of many rows uses it (a division before every
+// address took trees from 64 to 68 us); in the kernel of few rows, where a division is rare, it only moved the compiler's choices: 64
+// sequences of 8192 tokens 136 us, not 129.
 __device__ __forceinline__ int row_token(const AttendArgs &p, int row) { return (int)(((uint64_t)(uint32_t)row * p.group_inv) >> 31); }
 
 // One stretch of an item on the line of tiles.
@@ -417,7 +419,7 @@ __device__ void join_parts(const AttendArgs &p, const float *parts, long stride,
     }
   };
   auto write = [&](int x, JoinSum &s) {
-    const int rr = row0 + x / CH, t = row_token(p, rr);
+    const int rr = row0 + x / CH, t = rr / G;
     if (x >= J::PIECES || rr >= rows) return;
     char *dst = p.o.p + (b * p.o.sb + (long)t * p.o.st + (long)(h * G + rr - t * G) * p.o.sh + (x % CH) * 8) * (F32 ? 4 : 2);
     store_out<F32>(dst, s.y, t < fresh && s.L > 0.0f ? 1.0f / s.L : 0.0f);
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   auto copy_queries = [&](const Segment &s) {
     constexpr int CH = S::QROW / 16;
     for (int x = tid; x < ROWS * CH; x += S::THREADS) {
-      const int row = x / CH, ch = x % CH, rr = s.rb * ROWS + row, t = row_token(p, rr);
+      const int row = x / CH, ch = x % CH, rr = s.rb * ROWS + row, t = rr / G;
       const bool in = rr < T * G;
       const char *src = in ? p.q.p + (s.b * p.q.sb + (long)t * p.q.st + (long)(s.h * G + rr - t * G) * p.q.sh) * ES + ch * 16 : p.q.p;
       cp_async16(qraw + row * S::QROW + ch * 16, src, in);
@@ -774,7 +776,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
               for (int r = 0; r < 2; ++r) {
                 bool see = jd < 0;
                 if (!see && jd < nn && tk < tokens) {
-                  const int t = row_token(p, row0 + 8 * n + 2 * cc + r);
+                  const int t = (row0 + 8 * n + 2 * cc + r) / G;
                   if (t < T) see = p.mask ? (p.mask[((long)sg.b * T + t) * words + (jd >> 5)] >> (jd & 31)) & 1u : jd <= t;
                 }
                 if (!see || lost) s[blk][n][2 * half + r] = -INFINITY;
@@ -1013,7 +1015,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = 8 * n + 2 * cc + r, rr = row0 + row, t = row_token(p, rr);
+          const int row = 8 * n + 2 * cc + r, rr = row0 + row, t = rr / G;
           if (rr >= T * G) continue;
           const float inv = !whole ? 1.0f : t < nn && l[n][r] > 0.0f ? 1.0f / l[n][r] : 0.0f;
 #pragma unroll

@@ -3,7 +3,7 @@
 
 namespace pace {
 namespace kv {
-// `few`: fewer items than the blocks of four warps could share out without long joins (see pace_launch_kv_attend).
+// `few`: no more items than SMs (see pace_launch_kv_attend).
 cudaError_t attend_4(const AttendArgs &a, int rows, bool few, cudaStream_t s) {
   const bool f32 = a.c.io == PACE_IO_F32;
   if (a.c.d == 64) {

@@ -27,9 +27,12 @@ namespace kv {
 enum { TC_SHARE = 0, TC_ALT = 1, TC_ONE = 2 };
 constexpr int KVT = 64;               // cached tokens a tile
 constexpr int TC_BLOCKS = 160;        // most blocks of a launch (one an SM)
-// Tiles: the fewest a block takes; items of up to so many on average are not cut; an item a block while the longest is so many above an
-// equal share (sharing items cost a launch about 25 us, a tile 0.9 to 1.0 us).
-constexpr int TC_LEAST = 4, TC_WHOLE = 12, TC_EXTRA = 24;
+// Tiles: the fewest a block takes; items of up to so many on average are not cut.
+constexpr int TC_LEAST = 4, TC_WHOLE = 12;
+// An item a block while the longest is so many tiles above an equal share: sharing costs a block the queries, the first tile and the
+// outputs of another item, about as many tiles' time as this (eight sequences of up to 2048 tokens under trees, heads of 64: 22 us
+// shared, 28 an item a block; sixteen with heads of 128: 71 and 66 us).
+__host__ __device__ constexpr unsigned tc_extra(int D) { return D == 64 ? 10 : 24; }
 
 
 template <int D, int BITS, int MODE>
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   constexpr uint32_t tmem = 0;          // the whole of TMEM is this block's: its first column (a constant keeps addresses uniform)
 
   unsigned lo, hi;
-  const Cuts cuts = make_cuts<KVT>(seq, cum, c.batch, (unsigned)p.row_blocks * c.Hkv, most, TC_LEAST, TC_WHOLE, TC_EXTRA, lo, hi);
+  const Cuts cuts = make_cuts<KVT>(seq, cum, c.batch, (unsigned)p.row_blocks * c.Hkv, most, TC_LEAST, TC_WHOLE, tc_extra(D), lo, hi);
   auto at = [&](unsigned pos) { return segment_at<KVT>(seq, cum, c.batch, p.row_blocks, pos, hi); };
   if (tid == 0) {
     const Segment end = lo < hi ? at(hi - 1) : Segment{};
