@@ -64,8 +64,9 @@ struct TcShape {
   // where each softmax warp turns its rows' outputs, ROWB bytes of a row at a time: the queries' area where there is one
   static constexpr int ROWB = QSMEM ? 128 : 64;
   static constexpr int OOUT = QSMEM ? OQ : OML + (MODE == TC_ALT ? 128 * 24 : 0);
-  static constexpr int OBAR = QSMEM ? OML + (MODE == TC_ALT ? 128 * 24 : 0) : OOUT + 4 * NWG * 32 * ROWB;
-  static_assert(!QSMEM || NRB * QB >= 4 * NWG * 32 * ROWB, "outputs");
+  static constexpr int OUT_GROUP = QSMEM ? NRB * QB / NWG : 4 * 32 * ROWB;   // (ALT: both groups are done when either writes)
+  static constexpr int OBAR = QSMEM ? OML + (MODE == TC_ALT ? 128 * 24 : 0) : OOUT + NWG * OUT_GROUP;
+  static_assert(OUT_GROUP >= 4 * 32 * ROWB, "outputs");
   static constexpr int NBAR = 2 * RS + 2 * KS + 2 * VS + 7 * NWG + 5;
   static constexpr int OMISC = OBAR + NBAR * 8;                         // raw flags [RS], tmem base
   static constexpr int OCUM = (OMISC + 32 + 15) / 16 * 16;
@@ -694,7 +695,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         const bool apart = edge && (own_exps[(tl & 7) * 2] || own_exps[(tl & 7) * 2 + 1]);   // each token by its own exponents
         bool done = !good;
         // ---- weights by the references at hand: if their sum fits fp16 each of them does, and no maximum is needed
-        if (good && !__any_sync(0xffffffffu, first || apart || ev[0] > E)) {
+        const bool unset = in && m == -INFINITY && (!edge || vis);        // sees its first token here: the long way finds its reference
+        if (good && !__any_sync(0xffffffffu, first || apart || unset || ev[0] > E)) {
           const int dE = max((int)ev[0] - E, -60);
           const float cs = crow * exp2i(ek[0]), add = in ? OFFSET + (float)dE - (m == -INFINITY ? 0.0f : m) : -126.0f;
           uint32_t h[2][16];
@@ -860,7 +862,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         };
         // through shared memory, so that rows leave in whole lines (or half lines): 16-byte piece i of a row lies at i ^ swizzle
         constexpr int PC = S::ROWB / 16;
-        char *area = smem + S::OOUT + warp * 32 * S::ROWB;
+        // (where queries lie, each group within its own: the other's products may still read theirs)
+        char *area = smem + S::OOUT + w * S::OUT_GROUP + (warp & 3) * 32 * S::ROWB;
         auto slot = [&](int r, int i) { return area + r * S::ROWB + (i ^ (PC == 8 ? r & 7 : (r >> 1) & 3)) * 16; };
         const int r0 = (MODE == TC_SHARE ? w * 128 : 0) + (warp & 3) * 32;
         auto exchange = [&](const uint4 *z, auto &&store) {
