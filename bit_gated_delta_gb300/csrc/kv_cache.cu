@@ -327,8 +327,8 @@ __global__ void __launch_bounds__(THREADS) read_kernel(KvDev c, const int32_t *_
   constexpr int LPV = D / 8, ROWS = THREADS / LPV, ES = IO32 ? 4 : 2;
   const int a = threadIdx.x % LPV, row = threadIdx.x / LPV;
   pdl_enter();
-  const long item = blockIdx.x;
-  const int head = (int)(item % c.Hkv), ti = (int)((item / c.Hkv) % tiles), b = (int)(item / ((long)c.Hkv * tiles));
+  const unsigned hi = blockIdx.x / (unsigned)c.Hkv;
+  const int head = blockIdx.x - hi * c.Hkv, b = hi / (unsigned)tiles, ti = hi - b * tiles;
   const long f = first ? first[b] : 0;
   const long e = end ? end[b] : (1L << 62);
   const long base = (f >= 0 ? f / TILE : -((-f + TILE - 1) / TILE)) * TILE + (long)ti * TILE;

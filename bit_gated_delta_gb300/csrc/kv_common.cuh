@@ -121,19 +121,19 @@ __device__ __forceinline__ void unpack8(uint2 w, int (&u)[8]) {
   }
 }
 
-// Page of slot `slot` of sequence b, or -1 when the slot is outside the table or the page outside the pool.
+// Page of slot `slot` of sequence b, or -1 when the slot is outside the table or the page outside the pool. (A table holds 2^30 tokens
+// at most, so that slots inside it divide in 32 bits.)
 __device__ __forceinline__ int page_of(const KvDev &c, int b, long slot) {
-  if (slot < 0) return -1;
-  const long col = slot / c.page;
-  if (col >= c.table_cols) return -1;
+  if (slot < 0 || slot >= (long)c.table_cols * c.page) return -1;
+  const unsigned col = (unsigned)slot / (unsigned)c.page;
   const int pg = c.table[(long)b * c.table_cols + col];
   return pg >= 0 && pg < c.n_pages ? pg : -1;
 }
 // Tile holding `slot` (page already checked): pages and heads are 64-bit offsets.
 template <int TB>
 __device__ __forceinline__ char *tile_at(const KvDev &c, int page, int head, long slot) {
-  const long tiles = c.page / TILE;
-  return c.pool + (((long)page * c.Hkv + head) * tiles + (slot % c.page) / TILE) * (long)TB;
+  const unsigned tiles = (unsigned)c.page / TILE;
+  return c.pool + (((long)page * c.Hkv + head) * tiles + ((unsigned)slot / TILE) % tiles) * (long)TB;
 }
 // Index in the pool of tile t (tokens 32t ..) of sequence b and KV head h, or -1; tpp = tiles a page.
 __device__ __forceinline__ int tile_index(const KvDev &c, int b, int h, int t, int tpp) {
