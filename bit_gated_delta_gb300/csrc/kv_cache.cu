@@ -244,11 +244,12 @@ __device__ __forceinline__ void quant8(const float (&xin)[8], uint32_t (&u)[8], 
   }
 }
 
-// The new tokens of a call. The first q_blocks blocks rotate queries (HC heads a lane); the others take key and value vectors, 256/D
-// a warp and KC steps of them: keys are rotated, both quantized and written to their tile.
+// The new tokens of a call. Some blocks rotate queries (HC heads a lane), which is bound by bytes; the others take key and value
+// vectors, 256/D a warp and KC steps of them: keys are rotated, both quantized and written to their tile, which is bound by the
+// arithmetic and its latency. The two kinds are spread evenly over the launch, kv_rate / 2^32 of the blocks being of the second.
 template <int D, int BITS, int IO32, int HC, int KC>
 __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, KvTensor k, KvTensor v, KvTensor qo, KvRope r,
-                                                         const int32_t *__restrict__ positions, int q_blocks) {
+                                                         const int32_t *__restrict__ positions, uint64_t kv_rate) {
   using L = Tile<D, BITS>;
   constexpr int LPV = D / 8, VPW = 32 / LPV, ES = IO32 ? 4 : 2;
   const int lane = threadIdx.x & 31, sub = lane / LPV, a = lane % LPV;
@@ -260,9 +261,10 @@ __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, Kv
     if (report && t < new_tokens(c, b)) atomicOr(c.status, PACE_KV_BAD_POSITION);
     return pos < 0 ? 0 : r.max_pos - 1;
   };
-  if ((int)blockIdx.x < q_blocks) {
+  const unsigned kv_block = (unsigned)((blockIdx.x * kv_rate) >> 32);  // blocks of the second kind before this one
+  if ((unsigned)(((blockIdx.x + 1) * kv_rate) >> 32) == kv_block) {
     const unsigned chunks = (c.Hq + HC - 1) / HC;
-    const unsigned item = (blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5)) * VPW + sub;
+    const unsigned item = ((blockIdx.x - kv_block) * (THREADS / 32) + (threadIdx.x >> 5)) * VPW + sub;
     if (item >= tokens * chunks) return;
     const unsigned tok = item / chunks, h0 = (item - tok * chunks) * HC;
     const int b = tok / c.n_tokens, t = tok - b * c.n_tokens;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, Kv
     return;
   }
   const unsigned nvec = 2 * c.Hkv, chunks = (nvec + KC * VPW - 1) / (KC * VPW);
-  const unsigned item = (blockIdx.x - q_blocks) * (THREADS / 32) + (threadIdx.x >> 5);
+  const unsigned item = kv_block * (THREADS / 32) + (threadIdx.x >> 5);
   if (item >= tokens * chunks) return;                 // whole warps
   const unsigned tok = item / chunks;
   const int v0 = (item - tok * chunks) * KC * VPW;
@@ -460,7 +462,10 @@ cudaError_t launch_append(const KvDev &c, const KvTensor &q, const KvTensor &k, 
   const long tokens = (long)c.batch * c.n_tokens;
   const long q_items = q.p ? tokens * ((c.Hq + HC - 1) / HC) : 0, q_blocks = (q_items + W * VPW - 1) / (W * VPW);
   const long kv_warps = tokens * ((2 * c.Hkv + KC * VPW - 1) / (KC * VPW));
-  return pdl_launch(append_kernel<D, BITS, IO32, HC, KC>, q_blocks + (kv_warps + W - 1) / W, s, c, q, k, v, qo, r, pos, (int)q_blocks);
+  const long kv_blocks = (kv_warps + W - 1) / W, blocks = q_blocks + kv_blocks;
+  // (rounded up: the last block's count comes to kv_blocks, and no count to more)
+  const uint64_t kv_rate = (((uint64_t)kv_blocks << 32) + blocks - 1) / blocks;
+  return pdl_launch(append_kernel<D, BITS, IO32, HC, KC>, blocks, s, c, q, k, v, qo, r, pos, kv_rate);
 }
 
 }  // namespace kv
