@@ -205,20 +205,23 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(KvRope r, int n, int head
 }
 
 // Quantize the lane's eight elements within their group of 64 (eight lanes): codes, scale, zero point. quant_group's
-// arithmetic with the maxima taken by shuffle.
+// arithmetic with the maxima taken by shuffle. Elements are cleaned (NaN to 0, sizes to 2^120) only where one of them needs it.
 template <int BITS>
 __device__ __forceinline__ void quant8(const float (&xin)[8], uint32_t (&u)[8], float &s, int &z) {
-  float x[8];
+  float x[8], A = 0.0f, nan = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[i] = fminf(fmaxf(xin[i], -0x1p120f), 0x1p120f);   // fmaxf drops a NaN
-    if (xin[i] != xin[i]) x[i] = 0.0f;
+    x[i] = xin[i];
+    A = fmaxf(A, fabsf(x[i]));
+    nan = fmaf(x[i], 0.0f, nan);                         // NaN where an element is NaN or infinite
+  }
+  if (A > 0x1p120f || nan != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = xin[i] != xin[i] ? 0.0f : fminf(fmaxf(xin[i], -0x1p120f), 0x1p120f);
+    A = fminf(A, 0x1p120f);
   }
   constexpr int qmax = BITS == 8 ? 127 : 15;
   if (BITS == 8) {
-    float A = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) A = fmaxf(A, fabsf(x[i]));
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) A = fmaxf(A, __shfl_xor_sync(0xffffffffu, A, o));
     s = bf16_round(__fdiv_rn(A, (float)qmax));
@@ -233,23 +236,41 @@ __device__ __forceinline__ void quant8(const float (&xin)[8], uint32_t (&u)[8], 
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
     s = bf16_round(__fdiv_rn(__fsub_rn(hi, lo), (float)qmax));
-    z = s >= FLT_MIN ? min(max(__float2int_rn(__fmul_rn(-lo, __fdiv_rn(1.0f, s))), 0), qmax) : 0;
+    z = s >= FLT_MIN ? min(max(__float2int_rn(__fmul_rn(-lo, __frcp_rn(s))), 0), qmax) : 0;
   }
   if (!(s >= FLT_MIN)) s = 0.0f;
-  const float r = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+  const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+  // Rounded to integers by adding 1.5 * 2^23: the sum's low bits hold the integer, plus `mid`. With 8 bits no code needs a limit: A / 127
+  // exceeds s by 2^-8 of s at most, so that |x r| < 127.497.
+  const float mid = 12582912.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int c = __float2int_rn(__fmul_rn(x[i], r));
-    u[i] = (uint32_t)(BITS == 8 ? min(max(c, -qmax), qmax) + 128 : min(max(c + z, 0), qmax));
+    const int c = __float_as_int(__fadd_rn(__fmul_rn(x[i], r), mid)) - __float_as_int(mid);
+    u[i] = (uint32_t)(BITS == 8 ? c + 128 : min(max(c + z, 0), qmax));
   }
 }
+
+// n / d as n m >> s, exact for n < 2^31 (m = ceil(2^s / d), s = 31 + ceil(log2 d): m d - 2^s < 2^(s - 31)).
+struct Div {
+  uint32_t m;
+  int s;
+};
+inline Div make_div(uint32_t d) {
+  int l = 0;
+  while ((1ull << l) < d) ++l;
+  return Div{(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+__device__ __forceinline__ unsigned divide(unsigned n, const Div &d) { return (unsigned)(((uint64_t)n * d.m) >> d.s); }
+struct AppendDivs {
+  Div q_chunks, kv_chunks, n_tokens, page;
+};
 
 // The new tokens of a call. Some blocks rotate queries (HC heads a lane), which is bound by bytes; the others take key and value
 // vectors, 256/D a warp and KC steps of them: keys are rotated, both quantized and written to their tile, which is bound by the
 // arithmetic and its latency. The two kinds are spread evenly over the launch, kv_rate / 2^32 of the blocks being of the second.
 template <int D, int BITS, int IO32, int HC, int KC>
 __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, KvTensor k, KvTensor v, KvTensor qo, KvRope r,
-                                                         const int32_t *__restrict__ positions, uint64_t kv_rate) {
+                                                         const int32_t *__restrict__ positions, uint64_t kv_rate, AppendDivs by) {
   using L = Tile<D, BITS>;
   constexpr int LPV = D / 8, VPW = 32 / LPV, ES = IO32 ? 4 : 2;
   const int lane = threadIdx.x & 31, sub = lane / LPV, a = lane % LPV;
@@ -266,8 +287,8 @@ __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, Kv
     const unsigned chunks = (c.Hq + HC - 1) / HC;
     const unsigned item = ((blockIdx.x - kv_block) * (THREADS / 32) + (threadIdx.x >> 5)) * VPW + sub;
     if (item >= tokens * chunks) return;
-    const unsigned tok = item / chunks, h0 = (item - tok * chunks) * HC;
-    const int b = tok / c.n_tokens, t = tok - b * c.n_tokens;
+    const unsigned tok = divide(item, by.q_chunks), h0 = (item - tok * chunks) * HC;
+    const int b = divide(tok, by.n_tokens), t = tok - b * c.n_tokens;
     rotate_heads<IO32, HC>(r, q.p + (b * q.sb + t * q.st + h0 * q.sh) * ES, q.sh, qo.p + (b * qo.sb + t * qo.st + h0 * qo.sh) * ES,
                            qo.sh, min(HC, (int)(c.Hq - h0)), a, position(tok, b, t, a == 0), 1.0f);
     return;
@@ -275,9 +296,9 @@ __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, Kv
   const unsigned nvec = 2 * c.Hkv, chunks = (nvec + KC * VPW - 1) / (KC * VPW);
   const unsigned item = kv_block * (THREADS / 32) + (threadIdx.x >> 5);
   if (item >= tokens * chunks) return;                 // whole warps
-  const unsigned tok = item / chunks;
+  const unsigned tok = divide(item, by.kv_chunks);
   const int v0 = (item - tok * chunks) * KC * VPW;
-  const int b = tok / c.n_tokens, t = tok - b * c.n_tokens;
+  const int b = divide(tok, by.n_tokens), t = tok - b * c.n_tokens;
   float x[KC][8];
 #pragma unroll
   for (int i = 0; i < KC; ++i) {
@@ -292,7 +313,15 @@ __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, Kv
   const int len = c.lens[b];
   const long slot = (long)len + t;
   const bool fresh = t < new_tokens(c, b);
-  const int page = fresh ? page_of(c, b, len < 0 ? -1 : slot) : -1;
+  int page = -1;
+  char *tiles = nullptr;                               // the slot's tile of head 0; heads are `head_bytes` apart
+  const int head_bytes = c.page / TILE * L::BYTES;
+  if (fresh && len >= 0 && slot < (long)c.table_cols * c.page) {         // (at most 2^30)
+    const unsigned col = divide((unsigned)slot, by.page);
+    page = c.table[(long)b * c.table_cols + col];
+    if (page >= c.n_pages) page = -1;
+    tiles = c.pool + ((long)page * c.Hkv * (c.page / TILE) + ((unsigned)slot - col * c.page) / TILE) * (long)L::BYTES;
+  }
   if (fresh && page < 0 && lane == 0) atomicOr(c.status, PACE_KV_BAD_PAGE);
   Angles g;
   if (r.table && v0 < c.Hkv) load_angles(r, position(tok, b, t, lane == 0), a, g);
@@ -306,7 +335,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, Kv
     int z;
     quant8<BITS>(x[i], u, s, z);
     if (vec >= (int)nvec || page < 0) continue;
-    char *tile = tile_at<L::BYTES>(c, page, key ? vec : vec - c.Hkv, slot);
+    char *tile = tiles + (long)(key ? vec : vec - c.Hkv) * head_bytes;
     const int tt = (int)(slot % TILE);
     const uint2 w = pack8<BITS>(u);
     char *at = tile + (key ? L::k8(tt, a) : L::v8(tt, a));
@@ -465,7 +494,8 @@ cudaError_t launch_append(const KvDev &c, const KvTensor &q, const KvTensor &k, 
   const long kv_blocks = (kv_warps + W - 1) / W, blocks = q_blocks + kv_blocks;
   // (rounded up: the last block's count comes to kv_blocks, and no count to more)
   const uint64_t kv_rate = (((uint64_t)kv_blocks << 32) + blocks - 1) / blocks;
-  return pdl_launch(append_kernel<D, BITS, IO32, HC, KC>, blocks, s, c, q, k, v, qo, r, pos, kv_rate);
+  const AppendDivs by{make_div((c.Hq + HC - 1) / HC), make_div((2 * c.Hkv + KC * VPW - 1) / (KC * VPW)), make_div(c.n_tokens), make_div(c.page)};
+  return pdl_launch(append_kernel<D, BITS, IO32, HC, KC>, blocks, s, c, q, k, v, qo, r, pos, kv_rate, by);
 }
 
 }  // namespace kv
