@@ -732,12 +732,13 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
                 }
               }
             }
-            float d[NT][4];
+            // (fp32: the tensor cores cut off where they add, so that the small parts have a sum of their own)
+            float d[NT][4], small[NT][4];
             if (F32) {
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) d[n][e] = small[n][e] = 0.0f;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -747,8 +748,14 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
                 for (int e = 0; e < PARTS; ++e) {
                   if (!F32 && k == 0) mma_f16_first(d[n], fr[0][0], fr[1][0], fr[0][1], fr[1][1], q[n][e][0], q[n][e][1]);
                   else if (!F32) mma_f16(d[n], fr[0][2 * k], fr[1][2 * k], fr[0][2 * k + 1], fr[1][2 * k + 1], q[n][e][2 * k], q[n][e][2 * k + 1]);
-                  else mma_bf16(d[n], fr[0][2 * k], fr[1][2 * k], fr[0][2 * k + 1], fr[1][2 * k + 1], q[n][e][2 * k], q[n][e][2 * k + 1]);
+                  else mma_bf16(e ? small[n] : d[n], fr[0][2 * k], fr[1][2 * k], fr[0][2 * k + 1], fr[1][2 * k + 1], q[n][e][2 * k], q[n][e][2 * k + 1]);
                 }
+            if (F32) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[n][e] += small[n][e];
+            }
             const uint32_t sw = blk ? ksw.y : ksw.x;
             const float s0 = __uint_as_float(sw << 16), s1 = __uint_as_float(sw & 0xFFFF0000u);
 #pragma unroll
@@ -934,11 +941,19 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < PARTS; ++e) {
-                  if (!F32) mma_f16(acc[g][i][n], a01[2 * i], a01[2 * i + 1], a23[2 * i], a23[2 * i + 1], bf[n][e][0], bf[n][e][1]);
-                  else mma_bf16(acc[g][i][n], a01[2 * i], a01[2 * i + 1], a23[2 * i], a23[2 * i + 1], bf[n][e][0], bf[n][e][1]);
+              {
+                if (!F32) {
+                  mma_f16(acc[g][i][n], a01[2 * i], a01[2 * i + 1], a23[2 * i], a23[2 * i + 1], bf[n][0][0], bf[n][0][1]);
+                  continue;
                 }
+                // the smallest parts first, and added to the output outside the tensor cores: over thousands of tiles what they cut off
+                // would always lean the same way
+                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int e = PARTS; e-- > 0;) mma_bf16(y, a01[2 * i], a01[2 * i + 1], a23[2 * i], a23[2 * i + 1], bf[n][e][0], bf[n][e][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[g][i][n][e] += y[e];
+              }
           }
         }
       }

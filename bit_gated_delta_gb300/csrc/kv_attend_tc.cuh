@@ -1,19 +1,29 @@
 // Attention of many query rows over the quantized KV cache on the 5th-generation tensor cores (bf16 I/O).
 //
 // A work item is 128 query rows of one KV head (row r = token r/G, head r%G), or two such blocks that share the keys and values.
-// Per 64 cached tokens:  S = Q K^T  and  O += P V,  both tcgen05 with the left operand in TMEM (Q and P, a row per lane) and the
-// dequantized keys and values in shared memory as fp16; S and O accumulate in TMEM in fp32.
+// Per 64 cached tokens:  S = Q K^T  and  O += P V,  both tcgen05: keys and values dequantized to fp16 in shared memory, Q there too
+// (D = 128) or in TMEM, P in TMEM (over the scores it came from); S and O accumulate in TMEM in fp32.
 //
-// fp16 carries 11 bits, against 8 of bf16, so that held values, queries and weights are rounded to 2^-12; its range is kept by
-// exact powers of two: a row of Q is scaled by its largest element, K and V of a tile by its largest group scale (E_k, E_v; in
-// tiles with new tokens, where rows may see different tokens, each token by its own), weights are 2^8 at the row's
-// running maximum. The powers return with the scores, and in O as a running exponent per row raised like the maximum.
+// fp16 carries 11 bits, against 8 of bf16, so that held values, queries and weights are rounded to 2^-11 of themselves; its range is
+// kept by exact powers of two: a row of Q is scaled by its largest element, K and V of a tile by its largest group scale (E_k, E_v; in
+// tiles with new tokens of very different size, where rows may see different ones, each token by its own). The powers return with the
+// scores, and in O as a running exponent per row raised like the maximum. Scores, maxima, sums and outputs are held in fp32. A tile's
+// weights are taken relative to the maximum so far, without a pass for a new one, while their sum stays below 60,000 (so each fits
+// fp16); else the maximum is found and O rescaled.
 //
-// Roles (warps): softmax (four a group; thread = row = TMEM lane), four that dequantize, two that copy tiles in and prepare their scales (keys', values'),
-// one a softmax group that issues its products (issued by the softmax warps themselves, a prompt chunk took 206 us, not 172). Two softmax groups take turns, so that the tensor cores work on one group's products while the other group forms
-// its weights: the groups are two row blocks (SHARE), or even and odd tiles of one block (ALT, joined at the end through TMEM).
-//   bound: per 64 tokens and row block of 128 at D = 128, 512 cycles of tensor work; 64 scores a thread (4.5 instructions each, two
-//   groups a scheduler) and a quarter of 16,384 codes a scheduler (about two instructions each) come to about the same.
+// Roles (warps): softmax (four a group; thread = row = TMEM lane), four or eight that dequantize, two that copy tiles in and prepare
+// their scales in turn, and one a softmax group that issues its products (issued by the softmax warps themselves, a prompt chunk took
+// 206 us, not 172). Two softmax groups take turns, so that the tensor cores work on one group's products while the other forms its
+// weights: the groups are two row blocks (SHARE, above 128 rows), or even and odd tiles of one block (ALT, joined through TMEM). With
+// heads of 256 one group's O fills half of TMEM, and there is one group (ONE). Scores are formed two tiles ahead of the weights.
+//
+// Bound: at D = 128 a tile of 64 tokens takes 650 cycles of tensor work a block of 128 rows (measured: 49 cycles a product of N = 64
+// with both operands in shared memory, 65 one of N = 128), 8192 exponentials (260 cycles a scheduler and group) and 16,384 codes to
+// dequantize. SHARE runs at 2150 cycles a tile for two row blocks, of which the tensor cores work 1300; the dequantizing warps, four of
+// which serve both blocks, are what it waits for (eight cost the softmax warps more issue slots and registers than they gain). ALT runs
+// at 1800: the chain of scale preparation, dequantization and products through shared memory. Fixed per call about 10 us (first look-ups,
+// queries, first tile, outputs), per further item of a block about 8 us.
+//   MEASURED
 // Every wait is bounded; one that gives up sets the status word, and the block leaves after its copies and products have ended.
 #pragma once
 
@@ -33,7 +43,6 @@ constexpr int TC_LEAST = 4, TC_WHOLE = 12;
 // outputs of another item, about as many tiles' time as this (eight sequences of up to 2048 tokens under trees, heads of 64: 22 us
 // shared, 28 an item a block; sixteen with heads of 128: 71 and 66 us).
 __host__ __device__ constexpr unsigned tc_extra(int D) { return D == 64 ? 10 : 24; }
-
 
 template <int D, int BITS, int MODE>
 struct TcShape {

@@ -131,7 +131,9 @@ pace_status pace_kv_read(const pace_kv *kv, const pace_kv_step *step, const int3
  * Every slot below lens[b] is visible; of the new tokens, t sees j where bit j%32 of mask[b][t][j/32] is set (uint32,
  * (n_tokens + 31)/32 words a row; a tree's ancestor bits, itself included), or j <= t where mask is NULL. A row
  * that sees nothing, and rows t >= n_new[b], get zeros. q, o [batch][n_tokens][q_heads][d]. Scores, maxima, sums and
- * the output accumulate in fp32; cached codes enter the products as exact integers. */
+ * the output accumulate in fp32. With fp32 I/O, and where a KV head has up to 32 rows (new tokens times query heads of
+ * it), codes enter the products as exact integers; with bf16 I/O queries and weights are rounded to 11 bits, and above 32
+ * rows held keys and values too. The same call gives the same bits. One launch, or two above 32 rows. */
 pace_status pace_kv_attend(pace_kv *kv, const pace_kv_step *step, const pace_tensor *q, const uint32_t *mask, float scale,
                            const pace_tensor *o, void *stream);
 

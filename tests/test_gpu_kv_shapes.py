@@ -160,3 +160,34 @@ def test_attend_random_shapes(P, seed):
     L.append(lens, T)
     n_new = None if seed % 3 else r.integers(0, T + 1, B).tolist()
     check_attend(L, T, lens, n_new=n_new, mask=["causal", "tree", "empty"][seed % 3] if T > 1 else "causal", view=bool(seed % 2))
+
+
+@pytest.mark.parametrize("d,bits", [(64, 8), (128, 4)])
+def test_fp32_over_long_stretches_of_tiles(P, d, bits):
+    """So many tokens that each warp adds up over a hundred tiles: rounding errors may grow like a random walk but not all lean one way.
+    Scores of up to about 16 bits are off by a few 2^-21 of one, a weight by as much of itself and by ex2's 2^-22; averaged over the
+    rows' many tokens that stays below 1.5e-6 of the outputs."""
+    import torch
+    B, Hq, Hkv, n = 16, 16, 8, 16000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    cols = n // 128 + 1
+    kv = P.PaceKV(P.make_kv_config(Hq, Hkv, d, B * cols, B, bits=bits, page_tokens=128, max_new=4096, io_dtype=P.PACE_IO_F32))
+    table = torch.randperm(B * cols, generator=g, device="cuda").int().view(B, cols)
+    for at in range(0, n, 4000):
+        kv.append(None, rand(B, 4000, Hkv, d), rand(B, 4000, Hkv, d), torch.full((B,), at, dtype=torch.int32, device="cuda"), table)
+    lens = torch.full((B,), n - 2, dtype=torch.int32, device="cuda")
+    q = 2 * rand(B, 2, Hq, d)
+    o = torch.empty_like(q)
+    kv.attend(q, o, lens, table)
+    k, v = torch.empty(2, B, n, Hkv, d, device="cuda")
+    kv.read(k, v, table)
+    num = den = 0.0
+    for b in range(B):
+        for h in range(Hq):
+            s = (q[b, :, h].double() @ k[b, :, h // 2].double().t()) * d ** -0.5
+            s[0, n - 1] = -torch.inf
+            want = torch.softmax(s, -1) @ v[b, :, h // 2].double()
+            num += float(((o[b, :, h].double() - want) ** 2).sum())
+            den += float((want ** 2).sum())
+    assert (num / den) ** 0.5 <= 1.5e-6
