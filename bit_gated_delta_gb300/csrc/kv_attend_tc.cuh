@@ -23,7 +23,9 @@
 // which serve both blocks, are what it waits for (eight cost the softmax warps more issue slots and registers than they gain). ALT runs
 // at 1800: the chain of scale preparation, dequantization and products through shared memory. Fixed per call about 10 us (first look-ups,
 // queries, first tile, outputs), per further item of a block about 8 us.
-//   MEASURED
+// Measured (4-bit cache, cold): prompt chunks of 256 tokens, 4 sequences, 32 and 8 heads of 128, over 8192 tokens 144 us, 970 TFLOP/s
+// of the measured 1880; trees of 25 drafts, 16 sequences, over 2049 to 4096 tokens 62 us, over 8192 116 us; 7 drafts, 32 sequences of
+// 1000 to 6000 tokens, 16 and 2 heads of 256, 66 us.
 // Every wait is bounded; one that gives up sets the status word, and the block leaves after its copies and products have ended.
 #pragma once
 
@@ -37,8 +39,8 @@ namespace kv {
 enum { TC_SHARE = 0, TC_ALT = 1, TC_ONE = 2 };
 constexpr int KVT = 64;               // cached tokens a tile
 constexpr int TC_BLOCKS = 160;        // most blocks of a launch (one an SM)
-// Tiles: the fewest a block takes; items of up to so many on average are not cut.
-constexpr int TC_LEAST = 4, TC_WHOLE = 12;
+// The fewest tiles a block takes (heads of 128, one sequence of 2000 tokens under a tree: 22 us with 4, 23 with 2, 24 with 8).
+constexpr int TC_LEAST = 4;
 // An item a block while the longest is so many tiles above an equal share: sharing costs a block the queries, the first tile and the
 // outputs of another item, about as many tiles' time as this (eight sequences of up to 2048 tokens under trees, heads of 64: 22 us
 // shared, 28 an item a block; sixteen with heads of 128: 71 and 66 us).
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   constexpr uint32_t tmem = 0;          // the whole of TMEM is this block's: its first column (a constant keeps addresses uniform)
 
   unsigned lo, hi;
-  const Cuts cuts = make_cuts<KVT>(seq, cum, c.batch, (unsigned)p.row_blocks * c.Hkv, most, TC_LEAST, TC_WHOLE, tc_extra(D), lo, hi);
+  const Cuts cuts = make_cuts<KVT>(seq, cum, c.batch, (unsigned)p.row_blocks * c.Hkv, most, TC_LEAST, 0, tc_extra(D), lo, hi);
   auto at = [&](unsigned pos) { return segment_at<KVT>(seq, cum, c.batch, p.row_blocks, pos, hi); };
   if (tid == 0) {
     const Segment end = lo < hi ? at(hi - 1) : Segment{};

@@ -2,8 +2,13 @@
 // quantization fused), read-back and the move of an accepted path.
 //
 // All of these move bytes: a lane owns eight consecutive elements (one 16-byte bf16 vector, two fp32 ones), D/8 lanes a head
-// vector, 256/D vectors a warp. The arithmetic per element (a rotation, a group maximum over eight lanes, one rounding) is
-// small beside the memory time, so the floor of every call is its bytes at the copy bandwidth.
+// vector, 256/D vectors a warp; the floor of every call is its bytes at the copy bandwidth (6.8 TB/s; what only writes, 4.0).
+// Measured, with cold caches:
+//   rotation of 16,384 tokens, 32 heads of 128, bf16 (268 MB)                   40 us, 6.7 TB/s
+//   append of 16 x 256 tokens, 48 and 8 heads of 128, 8 bits, 32 of 128 rotated  31 us (126 MB: 19 us); key and value blocks are bound
+//                                                                               by issue (about 300 instructions a warp and vector)
+//   read-back of 4 x 20,000 to 32,768 tokens, 8 heads of 128, 4 bits            113 us; writing as many zeros takes 108
+//   append of 64 single tokens 4 us, keep of 8 paths 4 us: a chain of three dependent loads
 #include "kv_common.cuh"
 
 namespace pace {
@@ -350,7 +355,8 @@ __global__ void __launch_bounds__(THREADS) append_kernel(KvDev c, KvTensor q, Kv
 }
 
 // Held values of a range of slots. A block takes one 32-token tile of one head: it reads the tile's bytes once, each lane the
-// codes of eight elements, and writes rows of the outputs.
+// codes of eight elements, and writes rows of the outputs. Bound by writing; blocks of neighbouring heads run together, so that whole
+// rows are under way (tiles first instead of heads: 115 us, not 113).
 template <int D, int BITS, int IO32>
 __global__ void __launch_bounds__(THREADS) read_kernel(KvDev c, const int32_t *__restrict__ first,
                                                        const int32_t *__restrict__ end, KvTensor k, KvTensor v, int tiles) {
@@ -537,7 +543,10 @@ template <int D, int BITS, int IO32>
 cudaError_t append_go(const KvDev &c, const KvTensor &q, const KvTensor &k, const KvTensor &v, const KvTensor &qo,
                       const KvRope &r, const int32_t *pos, cudaStream_t s) {
   const long vecs = (long)c.batch * c.n_tokens * ((q.p ? c.Hq : 0) + 2 * c.Hkv);
-  if (vecs * (D / 8) > 4L * 2048 * device_sm_count())
+  // Two key or value vectors a lane, and four query heads, once there are lanes for a few waves: the angles, lengths and pages are read
+  // once for them. 32 and 8 heads of 128, 4 bits, rotated: 2,600 lanes an SM 7.1 us either way, 10,000 17.5 and 15.5, 41,000 59 and 49;
+  // with 320 (64 single tokens) one a lane takes 3.9 us and two 5.0.
+  if (vecs * (D / 8) > 4096L * device_sm_count())
     return launch_append<D, BITS, IO32, 4, 2>(c, q, k, v, qo, r, pos, s);
   return launch_append<D, BITS, IO32, 1, 1>(c, q, k, v, qo, r, pos, s);
 }
@@ -556,7 +565,9 @@ cudaError_t keep_go(const KvDev &c, int max_new, const int32_t *idx, const int32
 
 cudaError_t pace_launch_rope(const KvRope &r, int n, int heads, int d, int io, const KvTensor &x, const int32_t *pos,
                              const KvTensor &out, int inverse, cudaStream_t s) {
-  const bool many = (long)n * heads * (d / 8) > 4L * 2048 * device_sm_count();
+  // Four heads a lane share its angles: 32 heads of 128, 860 lanes an SM 3.4 us with one and 3.2 with four, 28,000 35 and 23 us (134 MB,
+  // 5.9 TB/s); with 215 lanes 2.7 and 2.8 us.
+  const bool many = (long)n * heads * (d / 8) > 512L * device_sm_count();
   if (io == PACE_IO_F32)
     return many ? rope_go<1, 4>(r, n, heads, d, x, pos, out, inverse, s) : rope_go<1, 1>(r, n, heads, d, x, pos, out, inverse, s);
   return many ? rope_go<0, 4>(r, n, heads, d, x, pos, out, inverse, s) : rope_go<0, 1>(r, n, heads, d, x, pos, out, inverse, s);
