@@ -19,7 +19,7 @@
 //
 // Bound: at D = 128 a tile of 64 tokens takes 650 cycles of tensor work a block of 128 rows (measured: 49 cycles a product of N = 64
 // with both operands in shared memory, 65 one of N = 128), 8192 exponentials (260 cycles a scheduler and group) and 16,384 codes to
-// dequantize. SHARE runs at 2150 cycles a tile for two row blocks, of which the tensor cores work 1300; the dequantizing warps, four of
+// dequantize. SHARE runs at 2150 cycles (1.05 us) a tile for two row blocks, of which the tensor cores work 1300; the dequantizing warps, four of
 // which serve both blocks, are what it waits for (eight cost the softmax warps more issue slots and registers than they gain). ALT runs
 // at 1800: the chain of scale preparation, dequantization and products through shared memory. Fixed per call about 10 us (first look-ups,
 // queries, first tile, outputs), per further item of a block about 8 us.

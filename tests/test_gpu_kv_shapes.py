@@ -191,3 +191,35 @@ def test_fp32_over_long_stretches_of_tiles(P, d, bits):
             num += float(((o[b, :, h].double() - want) ** 2).sum())
             den += float((want ** 2).sum())
     assert (num / den) ** 0.5 <= 1.5e-6
+
+
+@pytest.mark.parametrize("d,T", [(128, 40), (64, 200), (256, 20)])
+def test_many_rows_on_another_stream_and_from_a_graph(P, d, T):
+    import torch
+    L = Layer(P, 3, 8, 2, d, 4, "bf16", 64, 700, seed=21)
+    L.append([0] * 3, 256)
+    L.append([256] * 3, 200)
+    lens = dev(np.array([456, 100, 333], np.int32))
+    q, k, v = (dev(L.rand(3, T, h, d), L.dt) for h in (8, 2, 2))
+    qo, o = torch.empty_like(q), torch.empty_like(q)
+    rope = P.PaceRope(64, 1000)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def step():
+        L.kv.append(q, k, v, lens, L.table, rope=rope, q_out=qo)
+        L.kv.attend(qo, o, lens, L.table)
+
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    want = host(o)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step()
+    for _ in range(3):
+        o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(host(o), want)
+    assert np.isfinite(want).all() and L.kv.status() == 0
