@@ -11,18 +11,18 @@
 // weights are taken relative to the maximum so far, without a pass for a new one, while their sum stays below 60,000 (so each fits
 // fp16); else the maximum is found and O rescaled.
 //
-// Roles (warps): softmax (four a group; thread = row = TMEM lane), four or eight that dequantize, two that copy tiles in and prepare
-// their scales in turn, and one a softmax group that issues its products (issued by the softmax warps themselves, a prompt chunk took
-// 206 us, not 172). Two softmax groups take turns, so that the tensor cores work on one group's products while the other forms its
+// Roles (warps): softmax (four a group; thread = row = TMEM lane), four or eight that dequantize, two that copy tiles in (in turn) and
+// prepare their scales (one the keys', one the values'), and one a softmax group that issues its products (issued by the softmax warps
+// themselves, a prompt chunk took 206 us, not 172). Two softmax groups take turns, so that the tensor cores work on one group's products while the other forms its
 // weights: the groups are two row blocks (SHARE, above 128 rows), or even and odd tiles of one block (ALT, joined through TMEM). With
 // heads of 256 one group's O fills half of TMEM, and there is one group (ONE). Scores are formed two tiles ahead of the weights.
 //
 // Bound: at D = 128 a tile of 64 tokens takes 650 cycles of tensor work a block of 128 rows (measured: 49 cycles a product of N = 64
 // with both operands in shared memory, 65 one of N = 128), 8192 exponentials (260 cycles a scheduler and group) and 16,384 codes to
-// dequantize. SHARE runs at 2150 cycles (1.05 us) a tile for two row blocks, of which the tensor cores work 1300; the dequantizing warps, four of
-// which serve both blocks, are what it waits for (eight cost the softmax warps more issue slots and registers than they gain). ALT runs
-// at 1800: the chain of scale preparation, dequantization and products through shared memory. Fixed per call about 10 us (first look-ups,
-// queries, first tile, outputs), per further item of a block about 8 us.
+// dequantize. SHARE runs at 2150 cycles (1.05 us) a tile for two row blocks, of which the tensor cores work 1300; the dequantizing
+// warps, four of which serve both blocks, are what it waits for (eight cost the softmax warps more issue slots and registers than they
+// gain). ALT runs at 1800: the chain of scale preparation, dequantization and products through shared memory. Fixed per call about 10 us
+// (first look-ups, queries, first tile, outputs), per further item of a block about 8 us.
 // Measured (4-bit cache, cold): prompt chunks of 256 tokens, 4 sequences, 32 and 8 heads of 128, over 8192 tokens 144 us, 970 TFLOP/s
 // of the measured 1880; trees of 25 drafts, 16 sequences, over 2049 to 4096 tokens 62 us, over 8192 116 us; 7 drafts, 32 sequences of
 // 1000 to 6000 tokens, 16 and 2 heads of 256, 66 us.
