@@ -516,12 +516,13 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   if (lo >= hi) return;
   auto segment = [&](unsigned at) { return segment_at<TILE>(seq, cum, c.batch, p.row_blocks, at, hi); };
 
-  // ---- queries of a segment, copied one segment ahead
+  // ---- queries of a segment, copied one segment ahead; rows past the new tokens are not read (they may hold anything) but zeros
   auto copy_queries = [&](const Segment &s) {
     constexpr int CH = S::QROW / 16;
+    const int fresh = seq[s.b].fresh;                 // (T at most)
     for (int x = tid; x < ROWS * CH; x += S::THREADS) {
       const int row = x / CH, ch = x % CH, rr = s.rb * ROWS + row, t = rr / G;
-      const bool in = rr < T * G;
+      const bool in = t < fresh;
       const char *src = in ? p.q.p + (s.b * p.q.sb + (long)t * p.q.st + (long)(s.h * G + rr - t * G) * p.q.sh) * ES + ch * 16 : p.q.p;
       cp_async16(qraw + row * S::QROW + ch * 16, src, in);
     }

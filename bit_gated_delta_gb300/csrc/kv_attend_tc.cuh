@@ -128,10 +128,9 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, uint32_t s) 
                     h2mul(h2add(__byte_perm(w1, 0x64646464u, 0x4240), off), s), h2mul(h2add(__byte_perm(w1, 0x64646464u, 0x4341), off), s));
 }
 
-// 64 visibility bits of the columns of a tile for row t: columns jd0 + c of the new tokens (negative: context).
+// 64 visibility bits of the columns of a tile for row t < nn: columns jd0 + c of the new tokens (negative: context).
 __device__ __forceinline__ uint64_t visible(const AttendArgs &p, int b, int t, int jd0, int nn) {
   const int T = p.c.n_tokens;
-  if (t >= nn) return 0;
   const int c0 = jd0 < 0 ? min(-jd0, 64) : 0;
   const uint64_t ctx = c0 >= 64 ? ~0ull : (1ull << c0) - 1;
   if (c0 >= 64) return ctx;
@@ -589,7 +588,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       const int len = seq[sg.b].len, nn = seq[sg.b].fresh;
       const int row = sg.rb * S::ROWS + (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
       const int t = row_token(p, row), hh = sg.h * G + row - t * G;
-      const bool in = row < T * G;
+      const bool in = t < nn;                             // (rows past the new tokens are not read, as they may hold anything, but zeros)
       // ---- the row's query as fp16 over a power of two, for the products (ALT: both groups read the row, each converts half of it)
       float crow = 0.0f;
       if (good) {
@@ -616,7 +615,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           for (int x = MODE == TC_ALT ? tid : row_lane; x < 128 * CH; x += STRIDE) {
             // (four pieces of eight rows a warp: its writes to shared memory meet no bank twice)
             const int r = (x >> 5) / (CH / 4) * 8 + (x & 7), ch = (x >> 5) % (CH / 4) * 4 + ((x >> 3) & 3), rr = r0 + r, tt = row_token(p, rr);
-            const bool ok = rr < T * G;
+            const bool ok = tt < nn;
             const char *src = ok ? p.q.p + (sg.b * p.q.sb + (long)tt * p.q.st + (long)(sg.h * G + rr - tt * G) * p.q.sh + ch * 8) * 2 : p.q.p;
             cp_async16(block + (r >> 3) * CH * 128 + ch * 128 + (r & 7) * 16, src, ok);
           }

@@ -1,0 +1,71 @@
+"""Attention-layer operators at the edges of what they accept: padding rows that hold anything, values hidden, lost, empty, infinite or of
+very different size."""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+
+import kv_testlib as K
+from test_gpu_kv import P, Layer, dev, host  # noqa: F401  (P is a fixture)
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def words_of(see):
+    """Mask words [B, T, words] (int32) of see [B, T, T]."""
+    B, T, _ = see.shape
+    words = np.zeros((B, T, (T + 31) // 32), np.uint32)
+    for j in range(T):
+        words[:, :, j // 32] |= see[:, :, j].astype(np.uint32) << np.uint32(j % 32)
+    return words.view(np.int32)
+
+
+def attend(L, q, lens, see=None, n_new=None, table=None):
+    import torch
+    o = torch.full(q.shape, 7.0, dtype=L.dt, device="cuda")
+    L.kv.attend(dev(q, L.dt), o, dev(np.asarray(lens, np.int32)), L.table if table is None else table,
+                mask=None if see is None else dev(words_of(see)), n_new=None if n_new is None else dev(np.asarray(n_new, np.int32)))
+    return host(o)
+
+
+def relative(got, want):
+    return float(np.sqrt(((got.astype(np.float64) - want) ** 2).sum() / (want ** 2).sum()))
+
+
+def expected(L, b, q, len_, T, see=None, hidden=()):
+    """The attention of sequence b's T new tokens in 64 bits; `hidden` slots are seen by no row."""
+    vis = np.concatenate([np.ones((T, len_), bool), np.tril(np.ones((T, T), bool)) if see is None else see], 1)
+    vis[:, list(hidden)] = False
+    return K.attend(q[b].astype(np.float64), L.k[b, :len_ + T], L.v[b, :len_ + T], vis, L.d ** -0.5)
+
+
+# Root mean square errors. bf16: rounding an output to 8 bits is 2^-9.2 of it; queries, weights and held values of 11 bits an eighth of that
+# each, and twice as much by way of the scores (of a few units): all together below 1.2 times 2^-9. fp32: as in check_attend.
+LIMIT = {"bf16": 1.2 * 2.0 ** -9, "f32": 1e-5}
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -3e38])
+@pytest.mark.parametrize("d,bits,T,G,io,n", [(128, 4, 3, 4, "bf16", 100), (64, 8, 6, 4, "f32", 100), (64, 8, 30, 1, "bf16", 100), (128, 8, 40, 2, "bf16", 150),
+                                             (64, 4, 100, 4, "bf16", 150), (256, 4, 60, 1, "bf16", 150), (128, 4, 5, 1, "bf16", 6000),
+                                             (64, 4, 5, 1, "f32", 6000), (128, 4, 100, 2, "bf16", 6000)])
+def test_padding_rows_may_hold_anything(P, d, bits, T, G, io, n, fill):
+    """Queries of rows at and past n_new are not looked at: those rows are zeros, and the others as if the padding were zeros."""
+    L = Layer(P, 3, 2 * G, 2, d, bits, io, 64, n + T, seed=T)
+    for at in range(0, n, 256):
+        L.append([at] * 3, min(256, n - at))
+    lens, n_new = [n, n // 2, 0], [T - 1, T // 2, 0]
+    L.append(lens, T)
+    q = L.rand(3, T, 2 * G, d)
+    for b in range(3):
+        q[b, n_new[b]:] = 0
+    want = attend(L, q, lens, n_new=n_new)
+    for b in range(3):
+        q[b, n_new[b]:] = fill
+    got = attend(L, q, lens, n_new=n_new)
+    for b in range(3):
+        assert (got[b, n_new[b]:] == 0).all()
+        assert np.array_equal(got[b, :n_new[b]], want[b, :n_new[b]])
+    assert np.isfinite(want).all() and L.kv.status() == 0
