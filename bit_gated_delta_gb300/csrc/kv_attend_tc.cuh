@@ -705,9 +705,10 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         const bool apart = edge && (own_exps[(tl & 7) * 2] || own_exps[(tl & 7) * 2 + 1]);   // each token by its own exponents
         bool done = !good;
         // ---- weights by the references at hand: if their sum fits fp16 each of them does, and no maximum is needed
-        const bool unset = in && m == -INFINITY && (!edge || vis);        // sees its first token here: the long way finds its reference
-        if (good && !__any_sync(0xffffffffu, first || apart || unset || ev[0] > E)) {
-          const int dE = max((int)ev[0] - E, -60);
+        // (a tile of which the row sees nothing says nothing about its references)
+        const bool sees = in && (!edge || vis), unset = sees && m == -INFINITY;   // unset: the long way finds its first reference
+        if (good && !__any_sync(0xffffffffu, first || apart || unset || (sees && ev[0] > E))) {
+          const int dE = sees ? max((int)ev[0] - E, -60) : 0;
           const float cs = crow * exp2i(ek[0]), add = in ? OFFSET + (float)dE - (m == -INFINITY ? 0.0f : m) : -126.0f;
           uint32_t h[2][16];
           const uint64_t cs2 = pack2(cs, cs), ad2 = pack2(add, add);
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           const float cs = fmaxf(crow * exp2i(ek[0]), FLT_MIN);           // (not 0: a masked score is -inf)
           // the largest visible score, and value exponent
           float mx = -INFINITY;
-          int Et = OWN ? -126 : (int)ev[0];
+          int Et = OWN || !sees ? -126 : (int)ev[0];
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             uint32_t r[16];

@@ -69,3 +69,26 @@ def test_padding_rows_may_hold_anything(P, d, bits, T, G, io, n, fill):
         assert (got[b, n_new[b]:] == 0).all()
         assert np.array_equal(got[b, :n_new[b]], want[b, :n_new[b]])
     assert np.isfinite(want).all() and L.kv.status() == 0
+
+
+@pytest.mark.parametrize("size", [np.inf, 2.0 ** 40])
+@pytest.mark.parametrize("d,bits,G", [(128, 4, 2), (64, 8, 1), (256, 4, 1), (256, 8, 1)])
+def test_whole_tiles_that_the_mask_hides(P, d, bits, G, size):
+    """Drafts 64..127, hidden from the rows behind them, hold huge keys and values; those rows see what they see without them."""
+    T, ctx = 192, 64
+    L = Layer(P, 1, 2 * G, 2, d, bits, "bf16", 64, ctx + T, seed=d)
+    L.append([0], ctx)
+    k, v = L.rand(1, T, 2, d), L.rand(1, T, 2, d)
+    k[:, 64:128], v[:, 64:128] = (np.inf, np.inf) if np.isinf(size) else (k[:, 64:128] * np.float32(size), v[:, 64:128] * np.float32(size))
+    L.append([ctx], T, k=k, v=v)
+    q = L.rand(1, T, 2 * G, d)
+    see = np.tril(np.ones((T, T), bool))
+    see[128:, :128] = False
+    got = attend(L, q, [ctx], see[None])
+    want = expected(L, 0, q, ctx, T, see)
+    assert relative(got[0, 128:], want[128:]) <= LIMIT["bf16"]
+    # rows that see the new tokens behind the hidden ones alone
+    L2 = Layer(P, 1, 2 * G, 2, d, bits, "bf16", 64, T, seed=d)
+    L2.append([0], T, k=k, v=v)
+    got = attend(L2, q, [0], see[None])
+    assert relative(got[0, 128:], expected(L2, 0, q, 0, T, see)[128:]) <= LIMIT["bf16"]
