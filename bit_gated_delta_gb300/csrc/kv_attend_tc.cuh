@@ -485,9 +485,10 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         for (int half = 0; half < 2; ++half) {
           const int t = half * TILE + lane;
           const float ref = own ? top[half] : all;
-          const int e = ref > 0.0f ? (int)(__float_as_uint(ref) >> 23) - 127 : 0;
+          // (zero values have the lowest exponent: they ask for no room beside others)
+          const int e = ref > 0.0f ? (int)(__float_as_uint(ref) >> 23) - 127 : pw ? -126 : 0;
           exps[((n & 7) * 2 + pw) * KVT + t] = (int8_t)e;
-          const float down = exp2i(-e < 127 ? -e : 127);                // (e >= -126)
+          const float down = exp2i(-e);                   // (e >= -126: scales are normal numbers or zero)
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             const float sc = s[half][g] * down;

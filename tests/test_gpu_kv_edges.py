@@ -92,3 +92,35 @@ def test_whole_tiles_that_the_mask_hides(P, d, bits, G, size):
     L2.append([0], T, k=k, v=v)
     got = attend(L2, q, [0], see[None])
     assert relative(got[0, 128:], expected(L2, 0, q, 0, T, see)[128:]) <= LIMIT["bf16"]
+
+
+@pytest.mark.parametrize("d,bits,T,G", [(128, 4, 1, 4), (128, 4, 40, 2), (64, 8, 100, 2), (128, 8, 150, 1), (256, 4, 50, 1), (256, 8, 50, 1)])
+def test_zero_values_beside_tiny_ones(P, d, bits, T, G):
+    """A context whose first tiles hold zero values, and the others 2^-30: the weights of the others keep their bits."""
+    L = Layer(P, 2, 2 * G, 2, d, bits, "bf16", 64, 512 + T, seed=3)
+    lens = [512, 300]
+    for at in (0, 256):
+        v = L.rand(2, 256, 2, d) * np.float32(2.0 ** -30)
+        if at == 0:
+            v[:, :128] = 0
+        L.append([at] * 2, 256, v=K.bf16(v))
+    L.append(lens, T, v=K.bf16(L.rand(2, T, 2, d) * np.float32(2.0 ** -30)))
+    q = L.rand(2, T, 2 * G, d)
+    got = attend(L, q, lens)
+    for b in range(2):
+        assert relative(got[b], expected(L, b, q, lens[b], T)) <= LIMIT["bf16"]
+
+
+@pytest.mark.parametrize("d,bits,T,G", [(128, 4, 40, 2), (64, 8, 100, 2), (256, 4, 50, 1)])
+def test_a_zero_draft_beside_tiny_ones(P, d, bits, T, G):
+    """New tokens of very different size (one of them hidden and large), among them one whose values are zero."""
+    L = Layer(P, 1, 2 * G, 2, d, bits, "bf16", 64, T, seed=4)
+    v = L.rand(1, T, 2, d) * np.float32(2.0 ** -30)
+    v[0, 1], v[0, 2] = 0, 1e3
+    L.append([0], T, v=K.bf16(v))
+    q = L.rand(1, T, 2 * G, d)
+    see = np.tril(np.ones((T, T), bool))
+    see[:, 2] = False
+    got = attend(L, q, [0], see[None])
+    want = expected(L, 0, q, 0, T, see)
+    assert relative(got[0, 3:], want[3:]) <= LIMIT["bf16"]
