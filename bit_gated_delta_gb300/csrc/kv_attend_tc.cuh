@@ -7,9 +7,10 @@
 // fp16 carries 11 bits, against 8 of bf16, so that held values, queries and weights are rounded to 2^-11 of themselves; its range is
 // kept by exact powers of two: a row of Q is scaled by its largest element, K and V of a tile by its largest group scale (E_k, E_v; in
 // tiles with new tokens of very different size, where rows may see different ones, each token by its own). The powers return with the
-// scores, and in O as a running exponent per row raised like the maximum. Scores, maxima, sums and outputs are held in fp32. A tile's
-// weights are taken relative to the maximum so far, without a pass for a new one, while their sum stays below 60,000 (so each fits
-// fp16); else the maximum is found and O rescaled.
+// scores, and in O as a running exponent per row: the maximum and this exponent together follow the largest of score and value exponent,
+// so that large values of no weight take no bits from the others. Scores, maxima, sums and outputs are held in fp32. A tile's weights are
+// taken relative to the references so far, without a pass for new ones, while their sum stays below 60,000 (so each fits fp16); else
+// the references are found and O rescaled.
 //
 // Roles (warps): softmax (four a group; thread = row = TMEM lane), four or eight that dequantize, two that copy tiles in (in turn) and
 // prepare their scales (one the keys', one the values'), and one a softmax group that issues its products (issued by the softmax warps
@@ -224,9 +225,11 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   using L = Tile<D, BITS>;
   using namespace umma;
   constexpr int NG = L::NG, NWG = S::NWG, KS = S::KS, VS = S::VS, RS = S::RS;
-  // Weights are 2^(OFFSET - ROOM) at the row's reference and the largest value exponent met so far: fp16 reaches 2^-32 below that.
-  constexpr int ROOM = 3;
-  constexpr float OFFSET = 10.0f;
+  // A row's weights are 2^(score - m + value exponent - E + OFFSET), its sum l counts 2^(score - m + OFFSET): m is the largest score when
+  // it was last looked for, m + E - ROOM the largest of score + value exponent. So the token that adds most to the output has a weight of
+  // 2^(OFFSET - ROOM), above which fp16 has room for 2^8 more and below which it keeps 11 bits down to 2^-21, whatever the values of tokens
+  // that weigh nothing.
+  constexpr float ROOM = 3.0f, OFFSET = 10.0f;
   extern __shared__ __align__(128) char smem[];
   const KvDev &c = p.c;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + S::OBAR);
@@ -692,8 +695,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       if (MODE == TC_ALT) bar_sync(2, 256);               // (each group uses what both wrote)
       __syncwarp();
       if (lane == 0 && good && i0 < tiles) mbar_arrive(&q_ready[w]);
-      float m = -INFINITY, l = 0.0f;
-      int E = 0;
+      float m = -INFINITY, l = 0.0f, E = -126.0f;
       bool first = true;
       for (int i = i0; i < tiles; i += STEP, ++task) {
         const int tl = ntile + i, tok0 = (sg.tile + i) * KVT, buf = 2 * w + (task & 1);
@@ -706,11 +708,11 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         const bool apart = edge && (own_exps[(tl & 7) * 2] || own_exps[(tl & 7) * 2 + 1]);   // each token by its own exponents
         bool done = !good;
         // ---- weights by the references at hand: if their sum fits fp16 each of them does, and no maximum is needed
-        // (a tile of which the row sees nothing says nothing about its references)
-        const bool sees = in && (!edge || vis), unset = sees && m == -INFINITY;   // unset: the long way finds its first reference
-        if (good && !__any_sync(0xffffffffu, first || apart || unset || (sees && ev[0] > E))) {
-          const int dE = sees ? max((int)ev[0] - E, -60) : 0;
-          const float cs = crow * exp2i(ek[0]), add = in ? OFFSET + (float)dE - (m == -INFINITY ? 0.0f : m) : -126.0f;
+        const bool sees = in && (!edge || vis), unset = sees && m == -INFINITY;   // unset: the long way finds its first references
+        if (good && !__any_sync(0xffffffffu, first || apart || unset)) {
+          // (values 2^60 below the row's, zeros among them: formed 2^-60 lower for the sum's sake, and here only if all of them are 0 in fp16)
+          const float dE = sees ? fmaxf((float)ev[0] - E, -60.0f) : 0.0f, most = dE == -60.0f ? 0x1p-25f : 60000.0f;
+          const float cs = crow * exp2i(ek[0]), add = in ? OFFSET + dE - (m == -INFINITY ? 0.0f : m) : -126.0f;
           uint32_t h[2][16];
           const uint64_t cs2 = pack2(cs, cs), ad2 = pack2(add, add);
           uint64_t sum2[2] = {0ull, 0ull};
@@ -742,8 +744,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           float sum, odd;
           unpack2(add2(sum2[0], sum2[1]), sum, odd);
           sum += odd;
-          if (__all_sync(0xffffffffu, sum <= 60000.0f)) {
-            l = fmaf(sum, exp2i(-dE), l);
+          if (__all_sync(0xffffffffu, sum <= most)) {
+            l = fmaf(sum, exp2_approx(-dE), l);
             tmem_st16(tS, h[0]);
             tmem_st16(tS + 16, h[1]);
             tmem_wait_st();
@@ -754,9 +756,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         auto long_way = [&](auto own) {
           constexpr bool OWN = decltype(own)::value;
           const float cs = fmaxf(crow * exp2i(ek[0]), FLT_MIN);           // (not 0: a masked score is -inf)
-          // the largest visible score, and value exponent
-          float mx = -INFINITY;
-          int Et = OWN || !sees ? -126 : (int)ev[0];
+          // the largest visible score, and score with its value exponent
+          float mx = -INFINITY, rx = -INFINITY;
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             uint32_t r[16];
@@ -768,16 +769,16 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
               const bool see = (v >> e) & 1;
               const float x = __uint_as_float(r[e]) * (OWN ? crow * exp2i(ek[16 * k + e]) : cs);
               mx = fmaxf(mx, see ? x : -INFINITY);
-              if (OWN && see) Et = max(Et, (int)ev[16 * k + e]);
+              if (OWN) rx = fmaxf(rx, see ? x + (float)ev[16 * k + e] : -INFINITY);
             }
           }
-          // raise the row's references, and with them what is in O (once the product before has ended). The values' exponent is set with
-          // some room, since scales of later tiles are often a little larger.
-          const float m2 = fmaxf(m, mx);
-          const int E2 = first ? min(Et + ROOM, 127) : Et > E ? min(Et + ROOM, 127) : E;
+          if (!OWN) rx = mx + (float)ev[0];
+          // set the row's references, and with them what is in O (once the product before has ended)
+          const float m2 = fmaxf(m, mx), before_top = m + E - ROOM;
+          const float E2 = m2 == m && !(rx > before_top) ? E : fminf(fmaxf(fmaxf(before_top, rx) - m2 + ROOM, -126.0f), 127.0f);
           l *= m == -INFINITY ? 0.0f : exp2_approx(m - m2);
           if (!first) {
-            const float f = m == -INFINITY ? 0.0f : exp2_approx(m - m2 + (float)(E - E2));
+            const float f = m == -INFINITY ? 0.0f : exp2_approx((m - m2) + (E - E2));
             const int before = task - 1;
             good = __all_sync(0xffffffffu, bar_wait(&pv_done[2 * w + (before & 1)], (before >> 1) & 1));
             fence_after_sync();
@@ -798,8 +799,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           m = m2;
           E = E2;
           first = false;
-          const int dE = max(Et - E, -60);
-          const float off = OFFSET - (m == -INFINITY ? 0.0f : m), add = off + (OWN ? 0.0f : (float)dE);
+          const float dE = OWN ? 0.0f : fmaxf((float)ev[0] - E, -60.0f);
+          const float off = OFFSET - (m == -INFINITY ? 0.0f : m), add = off + dE;
           float sum = 0.0f;
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
@@ -810,16 +811,17 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
             float x[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              x[e] = exp2_approx(fmaf(__uint_as_float(r[e]), OWN ? crow * exp2i(ek[16 * k + e]) : cs, add));
-              x[e] = (v >> e) & 1 ? x[e] : 0.0f;
+              const bool see = (v >> e) & 1;
+              const float c = OWN ? crow * exp2i(ek[16 * k + e]) : cs;
+              x[e] = see ? exp2_approx(fmaf(__uint_as_float(r[e]), c, add)) : 0.0f;
               sum += x[e];
-              if (OWN && ((v >> e) & 1)) x[e] *= exp2i(min(max((int)ev[16 * k + e] - E, -60), 0));
+              if (OWN) x[e] = see ? exp2_approx(fmaf(__uint_as_float(r[e]), c, add + ((float)ev[16 * k + e] - E))) : 0.0f;
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[e] = h2pack(x[2 * e], x[2 * e + 1]);
             tmem_st8(tS + 8 * k, h);                      // (columns that were read)
           }
-          l = OWN ? l + sum : fmaf(sum, exp2i(-dE), l);
+          l = fmaf(sum, exp2_approx(-dE), l);
           tmem_wait_st();
         };
         if (!done) {
@@ -839,12 +841,11 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       const bool whole = sg.tile == 0 && sg.end == sg.tiles;
       float *part = c.part + (long)(2 * blockIdx.x + (sg.tile == 0 ? 1 : 0)) * TC_PART_FLOATS;   // (a shared item that starts here is the last)
       const int prow = (MODE == TC_SHARE ? w * 128 : 0) + row_lane;
-      float f0 = 1.0f, f1 = 0.0f, M = m, Ls = l;
-      int E0 = E, E1 = 0;
+      float f0 = 1.0f, f1 = 0.0f, M = m, Ls = l, E0 = E, E1 = 0.0f;
       bool two = false;
       if (MODE == TC_ALT) {
         float *mlp = reinterpret_cast<float *>(smem + S::OML) + row_lane * 6;
-        mlp[3 * w] = m, mlp[3 * w + 1] = l, mlp[3 * w + 2] = (float)E;
+        mlp[3 * w] = m, mlp[3 * w + 1] = l, mlp[3 * w + 2] = E;
         fence_before_sync();
         bar_sync(2, 256);
         fence_after_sync();
@@ -853,14 +854,14 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         f0 = mlp[0] == -INFINITY ? 0.0f : exp2_approx(mlp[0] - M);
         f1 = mlp[3] == -INFINITY ? 0.0f : exp2_approx(mlp[3] - M);
         Ls = f0 * mlp[1] + f1 * mlp[4];
-        E0 = (int)mlp[2];
-        E1 = (int)mlp[5];
+        E0 = mlp[2];
+        E1 = mlp[5];
       }
       {                                                    // (outputs of a call whose wait gave up are not to be used)
         const int K0 = MODE == TC_ALT ? w * (D / 32) : 0, K1 = MODE == TC_ALT ? K0 + D / 32 : D / 16;     // (ALT: each group half of the columns)
         const uint32_t tO0 = tmem + lanes + S::CO + (MODE == TC_ALT ? 0 : w * D);
         const float inv = t < nn && Ls > 0.0f ? 1.0f / Ls : 0.0f;
-        const float g0 = f0 * exp2i(E0), g1 = f1 * exp2i(E1);
+        const float g0 = f0 * exp2_approx(E0), g1 = f1 * exp2_approx(E1);
         auto columns = [&](int k, float (&y)[16]) {       // columns 16k .. of the row
           uint32_t r[16], r1[16];
           tmem_ld16(tO0 + 16 * k, r);

@@ -124,3 +124,46 @@ def test_a_zero_draft_beside_tiny_ones(P, d, bits, T, G):
     got = attend(L, q, [0], see[None])
     want = expected(L, 0, q, 0, T, see)
     assert relative(got[0, 3:], want[3:]) <= LIMIT["bf16"]
+
+
+CONTEXTS = [(128, 4, 1, 4), (64, 8, 20, 1), (128, 4, 40, 2), (64, 8, 100, 2), (128, 8, 150, 1), (256, 4, 50, 1), (256, 8, 50, 1)]
+
+
+@pytest.mark.parametrize("d,bits,T,G", CONTEXTS)
+def test_large_context_tiles_of_no_weight(P, d, bits, T, G):
+    """The first 128 context tokens hold values 2^30 times larger than the others' and take no weight worth naming."""
+    L = Layer(P, 1, 2 * G, 2, d, bits, "bf16", 64, 512 + T, seed=7)
+    q = L.rand(1, T, 2 * G, d)
+    q[..., 0] = 8.0
+    for at in (0, 256):
+        k, v = L.rand(1, 256, 2, d), L.rand(1, 256, 2, d)
+        k[..., 0] = 0
+        if at == 0:
+            v[0, :128] *= np.float32(2.0 ** 30)
+            k[0, :128, :, 0] = -12.0 * d ** 0.5
+        L.append([at], 256, k=k, v=v)
+    L.append([512], T, k=L.rand(1, T, 2, d) * 0.1)
+    got = attend(L, q, [512])
+    assert relative(got[0], expected(L, 0, q, 512, T)) <= LIMIT["bf16"]
+
+
+@pytest.mark.parametrize("d,bits,T,G", CONTEXTS)
+def test_tiny_values_of_much_weight_after_others(P, d, bits, T, G):
+    """A context whose later tokens score 60 bits higher but hold values 2^-80 of the first ones': both sides of the product count."""
+    L = Layer(P, 1, 2 * G, 2, d, bits, "bf16", 64, 512 + T, seed=8)
+    q = L.rand(1, T, 2 * G, d, amp=0.1)
+    q[..., 0] = 8.0
+    for at in (0, 256):
+        k, v = L.rand(1, 256, 2, d, amp=0.1), L.rand(1, 256, 2, d)
+        k[..., 0] = 0
+        if at == 256:
+            v *= np.float32(2.0 ** -80)
+            k[..., 0] = 41.6 / 8 * d ** 0.5                 # 41.6 nats
+        L.append([at], 256, k=K.bf16(k), v=K.bf16(v))
+    k = L.rand(1, T, 2, d, amp=0.1)
+    k[..., 0] = 41.6 / 8 * d ** 0.5
+    L.append([512], T, k=K.bf16(k), v=K.bf16(L.rand(1, T, 2, d) * np.float32(2.0 ** -80)))
+    got = attend(L, q, [512])
+    # the first tokens' part is e^-41.6 2^80 times the others': it alone is the output. Its scores differ from the others' by a key element of
+    # up to 84 in products with 8, rounded to 11 bits: 2^-11 of 60 bits, which moves every weight of the first tokens alike
+    assert relative(got[0], expected(L, 0, q, 512, T)) <= LIMIT["bf16"] + 60 * 2.0 ** -11
