@@ -4,9 +4,10 @@
 // Per 64 cached tokens:  S = Q K^T  and  O += P V,  both tcgen05: keys and values dequantized to fp16 in shared memory, Q there too
 // (D = 128) or in TMEM, P in TMEM (over the scores it came from); S and O accumulate in TMEM in fp32.
 //
-// fp16 carries 11 bits, against 8 of bf16, so that held values, queries and weights are rounded to 2^-11 of themselves; its range is
+// fp16 carries 11 bits, against 8 of bf16, so that held values, queries and weights are rounded to 11 bits; its range is
 // kept by exact powers of two: a row of Q is scaled by its largest element, K and V of a tile by its largest group scale (E_k, E_v; in
-// tiles with new tokens of very different size, where rows may see different ones, each token by its own). The powers return with the
+// tiles with tokens of very different size, of which rows may see or weigh different ones, each token by its own; a group far below the
+// largest of its token keeps fewer bits: 11 down to 2^-14 of it, one less for each power of two further). The powers return with the
 // scores, and in O as a running exponent per row: the maximum and this exponent together follow the largest of score and value exponent,
 // so that large values of no weight take no bits from the others. Scores, maxima, sums and outputs are held in fp32. A tile's weights are
 // taken relative to the references so far, without a pass for new ones, while their sum stays below 60,000 (so each fits fp16); else
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
     for (unsigned pos = lo; pos < hi;) {
       const Segment sg = at(pos);
       pos += sg.end - sg.tile;
-      const int tokens = seq[sg.b].tokens, len = seq[sg.b].len;
+      const int tokens = seq[sg.b].tokens;
       for (int tile = sg.tile; tile < sg.end; ++tile, ++n) {
         const int rs = n % RS;
         good = good && bar_wait(&raw_full[rs], (n / RS) & 1);
@@ -476,13 +477,10 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         // (scales are not negative: their bits order as integers)
         const uint32_t b0 = __float_as_uint(top[0]), b1 = __float_as_uint(top[1]);
         const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, max(b0, b1)));
-        // one exponent for the tile keeps ten bits of every token whose scale is within 2^12 of the largest; where a new token (that some
-        // rows may not see) makes them spread further, each token gets its own
-        bool own = false;
-        if ((tile + 1) * KVT > len) {
-          const uint32_t least = __reduce_min_sync(0xffffffffu, min(b0 ? b0 : 0x7F7FFFFFu, b1 ? b1 : 0x7F7FFFFFu));
-          own = all > 4096.0f * __uint_as_float(least);
-        }
+        // one exponent for the tile keeps eleven bits of every group whose scale is within 2^14 of the largest; where tokens spread by more
+        // than 2^12 (the largest may weigh nothing, or be hidden from some rows), each token gets its own
+        const uint32_t least = __reduce_min_sync(0xffffffffu, min(b0 ? b0 : 0x7F7FFFFFu, b1 ? b1 : 0x7F7FFFFFu));
+        const bool own = all > 4096.0f * __uint_as_float(least);
         if (lane == 0) own_exps[(n & 7) * 2 + pw] = own;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -705,7 +703,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         good = __all_sync(0xffffffffu, good && bar_wait(&s_full[buf], (task >> 1) & 1));
         fence_after_sync();
         const int8_t *ek = exps + ((tl & 7) * 2) * KVT, *ev = ek + KVT;
-        const bool apart = edge && (own_exps[(tl & 7) * 2] || own_exps[(tl & 7) * 2 + 1]);   // each token by its own exponents
+        const bool apart = *reinterpret_cast<const volatile uint16_t *>(own_exps + (tl & 7) * 2);   // each token by its own exponents
         bool done = !good;
         // ---- weights by the references at hand: if their sum fits fp16 each of them does, and no maximum is needed
         const bool sees = in && (!edge || vis), unset = sees && m == -INFINITY;   // unset: the long way finds its first references

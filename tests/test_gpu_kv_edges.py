@@ -167,3 +167,23 @@ def test_tiny_values_of_much_weight_after_others(P, d, bits, T, G):
     # the first tokens' part is e^-41.6 2^80 times the others': it alone is the output. Its scores differ from the others' by a key element of
     # up to 84 in products with 8, rounded to 11 bits: 2^-11 of 60 bits, which moves every weight of the first tokens alike
     assert relative(got[0], expected(L, 0, q, 512, T)) <= LIMIT["bf16"] + 60 * 2.0 ** -11
+
+
+@pytest.mark.parametrize("what", ["value", "key"])
+@pytest.mark.parametrize("d,bits,T,G", CONTEXTS)
+def test_a_large_context_token_of_no_weight(P, d, bits, T, G, what):
+    """One context token holds values 2^30 times larger than its neighbours', or an infinite key, and takes no weight worth naming."""
+    L = Layer(P, 1, 2 * G, 2, d, bits, "bf16", 64, 256 + T, seed=6)
+    k, v = L.rand(1, 256, 2, d), L.rand(1, 256, 2, d)
+    q = L.rand(1, T, 2 * G, d)
+    q[..., 0] = 8.0
+    k[..., 0] = 0
+    if what == "value":
+        v[0, 70] *= np.float32(2.0 ** 30)
+        k[0, 70, :, 0] = -12.0 * d ** 0.5                   # a score near -96: e^-96 2^30 is below 2^-108
+    else:
+        k[0, 70, :, 0] = -np.inf
+    L.append([0], 256, k=k, v=v)
+    L.append([256], T, k=L.rand(1, T, 2, d) * 0.1)
+    got = attend(L, q, [256])
+    assert relative(got[0], expected(L, 0, q, 256, T)) <= LIMIT["bf16"]
