@@ -72,8 +72,8 @@ struct TcShape {
   static constexpr int PB = BITS == 4 ? 16 : 4;                         // scale (and zero points) of one token and group
   static constexpr int PAR = 2 * L::NG * KVT * PB;                      // of a tile
   static constexpr int OEXP = OPAR + 2 * PAR;                           // exponents [8 tiles][k, v][64] int8
-  static constexpr int OOWN = OEXP + 8 * 2 * KVT;                       // whether a tile's tokens have their own [8][k, v]
-  static constexpr int OML = OOWN + 16;                                 // m, l, exponent of each group's rows (ALT)
+  static constexpr int OHOW = OEXP + 8 * 2 * KVT;                       // bit 0: a tile's tokens have their own; 1, 2: lost halves [8][k, v]
+  static constexpr int OML = OHOW + 16;                                 // m, l, exponent of each group's rows (ALT)
   // where each softmax warp turns its rows' outputs, ROWB bytes of a row at a time: the queries' area where there is one
   static constexpr int ROWB = QSMEM ? 128 : 64;
   static constexpr int OOUT = QSMEM ? OQ : OML + (MODE == TC_ALT ? 128 * 24 : 0);
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   unsigned *cum = wsum + 64;
   Seq *seq = reinterpret_cast<Seq *>(cum + c.batch + 1);
   int8_t *exps = reinterpret_cast<int8_t *>(smem + S::OEXP);
-  volatile uint8_t *own_exps = reinterpret_cast<uint8_t *>(smem + S::OOWN);
+  volatile uint8_t *how = reinterpret_cast<uint8_t *>(smem + S::OHOW);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be uniform)
   const int G = c.group, T = c.n_tokens;
 
@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
         // than 2^12 (the largest may weigh nothing, or be hidden from some rows), each token gets its own
         const uint32_t least = __reduce_min_sync(0xffffffffu, min(b0 ? b0 : 0x7F7FFFFFu, b1 ? b1 : 0x7F7FFFFFu));
         const bool own = all > 4096.0f * __uint_as_float(least);
-        if (lane == 0) own_exps[(n & 7) * 2 + pw] = own;
+        // (with the storage tiles that were not brought: those without a page, and past the table's end)
+        if (lane == 0) how[(n & 7) * 2 + pw] = (uint8_t)(own | (~raw_flags[rs] & 3) << 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int t = half * TILE + lane;
@@ -698,12 +699,17 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       for (int i = i0; i < tiles; i += STEP, ++task) {
         const int tl = ntile + i, tok0 = (sg.tile + i) * KVT, buf = 2 * w + (task & 1);
         const uint32_t tS = tmem + lanes + S::CS + buf * KVT;
-        const bool edge = tok0 + KVT > len;               // new tokens or the end in the tile
-        const uint64_t vis = edge && in ? visible(p, sg.b, t, tok0 - len, nn) : 0ull;
+        bool edge = tok0 + KVT > len;                     // new tokens or the end in the tile
+        uint64_t vis = edge && in ? visible(p, sg.b, t, tok0 - len, nn) : 0ull;
         good = __all_sync(0xffffffffu, good && bar_wait(&s_full[buf], (task >> 1) & 1));
         fence_after_sync();
         const int8_t *ek = exps + ((tl & 7) * 2) * KVT, *ev = ek + KVT;
-        const bool apart = *reinterpret_cast<const volatile uint16_t *>(own_exps + (tl & 7) * 2);   // each token by its own exponents
+        const uint32_t kind = *reinterpret_cast<const volatile uint16_t *>(how + (tl & 7) * 2);
+        const bool apart = kind & 0x0101u;                // each token by its own exponents
+        if (kind & 6u) {                                  // no row sees a lost half
+          vis = (edge ? vis : in ? ~0ull : 0ull) & ((kind & 2u ? 0ull : 0xFFFFFFFFull) | (kind & 4u ? 0ull : ~0ull << 32));
+          edge = true;
+        }
         bool done = !good;
         // ---- weights by the references at hand: if their sum fits fp16 each of them does, and no maximum is needed
         const bool sees = in && (!edge || vis), unset = sees && m == -INFINITY;   // unset: the long way finds its first references

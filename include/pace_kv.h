@@ -7,7 +7,8 @@
  * `stream`, argument errors returned on the host before anything is launched, pace_last_error() for the message.
  * Calls on one cache must not overlap on the GPU (same stream, or ordered by events): they share its pages and
  * its work area. Indices that only the device sees (page numbers, lengths, positions, kept drafts) are checked
- * there: a bad one touches nothing outside the cache, and sets a bit that pace_kv_get_status reports.
+ * there: a bad one touches nothing outside the cache, and sets a bit that pace_kv_get_status reports. A slot without a
+ * valid page is not written, reads as zeros, and is seen by no query.
  *
  * Cached values. Each head vector is held in groups of PACE_KV_GROUP consecutive elements with the quantizer of
  * the states (every operation rounds once to fp32; elements are first clamped to +-2^120, NaN counts as 0):

@@ -187,3 +187,24 @@ def test_a_large_context_token_of_no_weight(P, d, bits, T, G, what):
     L.append([256], T, k=L.rand(1, T, 2, d) * 0.1)
     got = attend(L, q, [256])
     assert relative(got[0], expected(L, 0, q, 256, T)) <= LIMIT["bf16"]
+
+
+@pytest.mark.parametrize("d,bits,G", [(128, 4, 1), (64, 8, 1), (256, 4, 1)])
+def test_slots_without_a_page_are_not_seen(P, d, bits, G):
+    """The same, whether a KV head has few rows or many: pages outside the pool, and tokens past an odd table's end."""
+    n, page = 160, 32
+    for T in (20, 32, 33, 130):
+        L = Layer(P, 1, 2 * G, 2, d, bits, "bf16", page, n + T, seed=9)
+        L.append([0], n)
+        L.append([n], T)
+        q = L.rand(1, T, 2 * G, d)
+        bad = L.table.clone()
+        bad[0, 1], bad[0, 4] = -1, L.cfg.n_pages
+        got = attend(L, q, [n], table=bad)
+        assert L.kv.status(clear=True) == P.PACE_KV_BAD_PAGE
+        want = expected(L, 0, q, n, T, hidden=[*range(32, 64), *range(128, 160)])
+        assert relative(got[0], want) <= LIMIT["bf16"]
+        short = L.table[:, :5].contiguous()                 # (160 tokens: the new ones have no slots)
+        got = attend(L, q, [150], table=short)
+        assert L.kv.status(clear=True) == P.PACE_KV_BAD_PAGE
+        assert relative(got[0], expected(L, 0, q, 150, T, hidden=range(160, 150 + T))) <= LIMIT["bf16"]
