@@ -796,7 +796,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       }
       // ---- weights. bf16 I/O: the scale of a value group enters the exponent, w = 2^(s + log2 s_v - m + 6) with m the running
       // maximum of s + log2 s_v, so that fp16 weights keep 11 bits whatever the scales; the sum takes 2^(s - m + 6). fp32 I/O: the
-      // scale multiplies the weight. m is raised only when a score passes it by 2^8 (fp16 weights up to 2^14, sums in fp32).
+      // scale multiplies the weight, and m lies 64 above the scores of tokens whose scale passes 2^60, so that no sum of weighted values
+      // leaves fp32 (held values reach 2^120). m is raised only when a score passes it by 2^8 (fp16 weights up to 2^14, sums in fp32).
       float lv[NG][2][2], lm[2][2];                      // log2 of the value scales of the lane's tokens, their largest
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
@@ -814,6 +815,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
             if (edge && (tok0 + 16 * blk + 8 * half + tau(j) >= tokens || lost)) x = 0.0f;   // never written: may hold anything
             lv[g][blk][half] = !F32 ? log2_approx(x) : x;
             if (!F32) lm[blk][half] = fmaxf(lm[blk][half], lv[g][blk][half]);
+            else if (x >= 0x1p60f) lm[blk][half] = 64.0f;
           }
         }
       }

@@ -208,3 +208,25 @@ def test_slots_without_a_page_are_not_seen(P, d, bits, G):
         got = attend(L, q, [150], table=short)
         assert L.kv.status(clear=True) == P.PACE_KV_BAD_PAGE
         assert relative(got[0], expected(L, 0, q, 150, T, hidden=range(160, 150 + T))) <= LIMIT["bf16"]
+
+
+@pytest.mark.parametrize("n", [200, 6000])
+@pytest.mark.parametrize("d,bits,T,G,io", [(128, 4, 1, 4, "bf16"), (64, 8, 5, 2, "f32"), (128, 4, 2, 2, "f32"), (256, 8, 1, 1, "f32"), (64, 8, 16, 2, "bf16")])
+def test_visible_infinite_values_count_as_their_clamp(P, d, bits, T, G, io, n):
+    """Infinite values are held as 2^120 (as near as their scale comes), and a weighted mean of such values is finite."""
+    L = Layer(P, 1, 2 * G, 2, d, bits, io, 64, n + T, seed=10)
+    v0 = None
+    for at in range(0, n, 250):
+        v0 = L.rand(1, min(250, n - at), 2, d)
+        v0[0, 7::20] = np.inf
+        v0[0, 9::40] = -np.inf
+        L.append([at], v0.shape[1], v=v0)
+    v1 = L.rand(1, T, 2, d)
+    v1[0, 0] = np.inf
+    L.append([n], T, v=v1)
+    q = L.rand(1, T, 2 * G, d)
+    got = attend(L, q, [n])
+    assert np.isfinite(got).all()
+    want = expected(L, 0, q, n, T)
+    scale = 2.0 ** -100                                     # (squares of the errors stay within 64 bits)
+    assert relative(got[0] * scale, want * scale) <= LIMIT[io]
