@@ -864,8 +864,10 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
       {                                                    // (outputs of a call whose wait gave up are not to be used)
         const int K0 = MODE == TC_ALT ? w * (D / 32) : 0, K1 = MODE == TC_ALT ? K0 + D / 32 : D / 16;     // (ALT: each group half of the columns)
         const uint32_t tO0 = tmem + lanes + S::CO + (MODE == TC_ALT ? 0 : w * D);
-        const float inv = t < nn && Ls > 0.0f ? 1.0f / Ls : 0.0f;
-        const float g0 = f0 * exp2_approx(E0), g1 = f1 * exp2_approx(E1);
+        // (held values reach 2^120: beyond 2^40 their weighted sums are formed 2^64 smaller, and a part is left so, under a reference 64 higher)
+        const float high = fmaxf(E0, E1) > 40.0f ? 64.0f : 0.0f;
+        const float inv = t < nn && Ls > 0.0f ? exp2_approx(high) / Ls : 0.0f;
+        const float g0 = f0 * exp2_approx(E0 - high), g1 = f1 * exp2_approx(E1 - high);
         auto columns = [&](int k, float (&y)[16]) {       // columns 16k .. of the row
           uint32_t r[16], r1[16];
           tmem_ld16(tO0 + 16 * k, r);
@@ -926,8 +928,8 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
           }
         }
         if (!whole && (MODE != TC_ALT || w == 0)) {
-          part[S::ROWS * D + 2 * prow] = M;
-          part[S::ROWS * D + 2 * prow + 1] = Ls;
+          part[S::ROWS * D + 2 * prow] = M + high;
+          part[S::ROWS * D + 2 * prow + 1] = Ls * exp2_approx(-high);
         }
       }
       fence_before_sync();

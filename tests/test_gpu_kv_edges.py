@@ -211,7 +211,8 @@ def test_slots_without_a_page_are_not_seen(P, d, bits, G):
 
 
 @pytest.mark.parametrize("n", [200, 6000])
-@pytest.mark.parametrize("d,bits,T,G,io", [(128, 4, 1, 4, "bf16"), (64, 8, 5, 2, "f32"), (128, 4, 2, 2, "f32"), (256, 8, 1, 1, "f32"), (64, 8, 16, 2, "bf16")])
+@pytest.mark.parametrize("d,bits,T,G,io", [(128, 4, 1, 4, "bf16"), (64, 8, 5, 2, "f32"), (128, 4, 2, 2, "f32"), (256, 8, 1, 1, "f32"), (64, 8, 16, 2, "bf16"),
+                                           (128, 4, 40, 2, "bf16"), (64, 8, 150, 1, "bf16"), (256, 4, 50, 1, "bf16")])
 def test_visible_infinite_values_count_as_their_clamp(P, d, bits, T, G, io, n):
     """Infinite values are held as 2^120 (as near as their scale comes), and a weighted mean of such values is finite."""
     L = Layer(P, 1, 2 * G, 2, d, bits, io, 64, n + T, seed=10)
