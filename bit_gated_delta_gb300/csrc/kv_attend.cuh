@@ -1114,9 +1114,10 @@ cudaError_t by_batches(const AttendArgs &a, int tok, F launch) {
   return cudaSuccess;
 }
 
-// resident_blocks of the capacity for large batches (its own cache entry)
-template <auto K>
-int resident_blocks_large(int threads, size_t smem) {
+// resident_blocks with a cache entry for each capacity: their shared memory differs, and the grid, and with it the cuts of the line and the
+// bits of the results, must not depend on which batch was called first.
+template <auto K, int CAPACITY>
+int resident_blocks_of(int threads, size_t smem) {
   static std::atomic<int> cache[PACE_MAX_DEVICES];
   const int dev = current_device();
   int v = cache[dev].load(std::memory_order_relaxed);
@@ -1136,8 +1137,10 @@ cudaError_t launch_attend(AttendArgs a, cudaStream_t s) {
   cudaError_t e = smem_opt_in<K>(227 * 1024);
   if (e != cudaSuccess) return e;
   a.row_blocks = (a.c.n_tokens * a.c.group + S::ROWS - 1) / S::ROWS;
-  static int (*const resident[2])(int, size_t) = {resident_blocks<K>, resident_blocks_large<K>};
-  const int per_sm = resident[S::capacity(a.c.batch) > 128](S::THREADS, smem);
+  const int capacity = S::capacity(a.c.batch);
+  const int per_sm = capacity == 64    ? resident_blocks_of<K, 64>(S::THREADS, smem)
+                     : capacity == 256 ? resident_blocks_of<K, 256>(S::THREADS, smem)
+                                       : resident_blocks_of<K, PACE_KV_MAX_BATCH>(S::THREADS, smem);
   return by_batches(a, TILE, [&](const AttendArgs &part, long line) {
     // no more blocks than the longest possible line of tiles
     long grid = (long)per_sm * device_sm_count();

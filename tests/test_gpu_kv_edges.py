@@ -231,3 +231,39 @@ def test_visible_infinite_values_count_as_their_clamp(P, d, bits, T, G, io, n):
     want = expected(L, 0, q, n, T)
     scale = 2.0 ** -100                                     # (squares of the errors stay within 64 bits)
     assert relative(got[0] * scale, want * scale) <= LIMIT[io]
+
+
+SAME_BITS = """
+import sys
+import numpy as np
+import torch
+sys.path[:0] = [%r, %r]
+import bit_gated_delta_gb300 as P
+from test_gpu_kv import Layer, dev, host
+first = int(sys.argv[1])
+def call(B):
+    L = Layer(P, B, 8, 2, 64, 4, "f32" if sys.argv[2] == "f32" else "bf16", 64, 400, seed=B)
+    L.append([0] * B, 256)
+    L.append([256] * B, 144)
+    lens = L.rng.integers(0, 400, B).tolist()
+    q = L.rand(B, 1, 8, 64)
+    o = torch.empty(B, 1, 8, 64, dtype=L.dt, device="cuda")
+    L.kv.attend(dev(q, L.dt), o, dev(np.asarray(lens, np.int32)), L.table)
+    return host(o)
+if first:
+    call(first)
+np.save(sys.argv[3], call(300))
+"""
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_bits_do_not_depend_on_earlier_calls(tmp_path, P, io):
+    """A call of 300 sequences in a process of its own, and after a call of 200 or 20."""
+    outs = []
+    for first in (0, 200, 20):
+        at = str(tmp_path / f"o{first}.npy")
+        code = SAME_BITS % (ROOT, os.path.join(ROOT, "tests"))
+        r = subprocess.run([sys.executable, "-c", code, str(first), io, at], capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0, r.stderr[-2000:]
+        outs.append(np.load(at))
+    assert np.array_equal(outs[0], outs[1]) and np.array_equal(outs[0], outs[2])
