@@ -33,7 +33,7 @@ void pace_kv_attend_work(const pace_kv_config &cfg, size_t *count_bytes, size_t 
 
 cudaError_t pace_launch_kv_attend(const KvDev &c, const KvTensor &q, const uint32_t *mask, float scale, const KvTensor &o,
                                   cudaStream_t s) {
-  AttendArgs a{c, q, o, mask, scale * 1.44269504088896340736f, 0, (0x80000000u + c.group - 1) / c.group};
+  AttendArgs a{c, q, o, mask, scale * 1.44269504088896340736f, 0, 0, 0, (0x80000000u + c.group - 1) / c.group};
   const int rows = c.n_tokens * c.group;
   if (use_tc(c.io, rows)) return c.bits == 4 ? attend_tc_4(a, rows, s) : attend_tc_8(a, rows, s);
   // Blocks of 8 or 16 warps, one an SM, while there are no more items than SMs: an item then stays with one block, or few blocks join its

@@ -172,6 +172,7 @@ struct AttendArgs {
   const uint32_t *mask;
   float scale_log2;     // softmax scale * log2(e)
   int row_blocks;       // items of one (sequence, KV head)
+  unsigned item0, items;   // the items of each sequence in this launch (numbered by head, then row block): all, or a range of one's
   uint32_t group_inv;   // ceil(2^31 / group)
 };
 // Token of a row, row / group: exact for rows below 2^31 / group. The kernel of many rows uses it (a division before every
@@ -251,8 +252,8 @@ __device__ __forceinline__ unsigned tile_line(const KvDev &c, unsigned per_seq, 
 
 // The item that holds line position p, and its stretch from there up to hi.
 template <int TOK>
-__device__ __forceinline__ Segment segment_at(const Seq *seq, const unsigned *cum, int batch, int row_blocks, unsigned p, unsigned hi) {
-  int lo = 0, up = batch;                  // last b with cum[b] <= p
+__device__ __forceinline__ Segment segment_at(const Seq *seq, const unsigned *cum, const AttendArgs &a, unsigned p, unsigned hi) {
+  int lo = 0, up = a.c.batch;                  // last b with cum[b] <= p
   while (up - lo > 1) {
     const int mid = (lo + up) >> 1;
     if (cum[mid] <= p) lo = mid;
@@ -261,10 +262,10 @@ __device__ __forceinline__ Segment segment_at(const Seq *seq, const unsigned *cu
   Segment s;
   s.b = lo;
   s.tiles = max((seq[lo].tokens + TOK - 1) / TOK, 1);
-  const unsigned r = p - cum[lo], item = r / (unsigned)s.tiles;
-  s.tile = (int)(r - item * s.tiles);
-  s.h = item / row_blocks;
-  s.rb = item - s.h * row_blocks;
+  const unsigned r = p - cum[lo], k = r / (unsigned)s.tiles, item = a.item0 + k;
+  s.tile = (int)(r - k * s.tiles);
+  s.h = item / a.row_blocks;
+  s.rb = item - s.h * a.row_blocks;
   s.end = (int)min((unsigned)s.tiles, s.tile + (hi - p));
   return s;
 }
@@ -300,21 +301,20 @@ __device__ __forceinline__ Cuts make_cuts(const Seq *seq, const unsigned *cum, i
 // whole items until hi. Returns how many; segs[n].tile of the one after them is the line position where they end.
 constexpr int SEGS = 32;
 template <int TOK>
-__device__ __forceinline__ int list_segments(const Seq *seq, const unsigned *cum, int batch, int row_blocks, int kv_heads, unsigned lo,
-                                             unsigned hi, Segment *segs) {
-  const int lane = threadIdx.x & 31;
-  const Segment a = segment_at<TOK>(seq, cum, batch, row_blocks, lo, hi);
-  const unsigned per_b = (unsigned)row_blocks * kv_heads;
-  const unsigned item = (unsigned)a.h * row_blocks + a.rb + lane, db = item / per_b;
+__device__ __forceinline__ int list_segments(const Seq *seq, const unsigned *cum, const AttendArgs &p, unsigned lo, unsigned hi,
+                                             Segment *segs) {
+  const int lane = threadIdx.x & 31, row_blocks = p.row_blocks;
+  const Segment a = segment_at<TOK>(seq, cum, p, lo, hi);
+  const unsigned item = (unsigned)a.h * row_blocks + a.rb - p.item0 + lane, db = item / p.items;
   Segment s = a;
   unsigned at = lo;
   bool in = lane == 0;
-  if (lane > 0 && a.b + (int)db < batch) {
+  if (lane > 0 && a.b + (int)db < p.c.batch) {
     s.b = a.b + db;
     s.tiles = max((seq[s.b].tokens + TOK - 1) / TOK, 1);
-    const unsigned k = item - db * per_b;
-    s.h = k / row_blocks;
-    s.rb = k - s.h * row_blocks;
+    const unsigned k = item - db * p.items, own = p.item0 + k;
+    s.h = own / row_blocks;
+    s.rb = own - s.h * row_blocks;
     s.tile = 0;
     at = cum[s.b] + k * s.tiles;
     in = at < hi;
@@ -507,14 +507,14 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
   if (lane < STAGES) umma::mbar_init(&bars[lane], 1);
   umma::mbar_fence_init();
   pdl_enter();
-  const unsigned most = tile_line<TILE>(c, (unsigned)p.row_blocks * c.Hkv, seq, cum, wsum);
+  const unsigned most = tile_line<TILE>(c, p.items, seq, cum, wsum);
 
   // no share is less than a tile for every warp, or a whole average item of up to three: joining one costs about as much as three
   // rounds of tiles
   unsigned lo, hi;
-  const Cuts cuts = make_cuts<TILE>(seq, cum, c.batch, (unsigned)p.row_blocks * c.Hkv, most, NW, 3 * NW, 4 * NW, lo, hi);
+  const Cuts cuts = make_cuts<TILE>(seq, cum, c.batch, p.items, most, NW, 3 * NW, 4 * NW, lo, hi);
   if (lo >= hi) return;
-  auto segment = [&](unsigned at) { return segment_at<TILE>(seq, cum, c.batch, p.row_blocks, at, hi); };
+  auto segment = [&](unsigned at) { return segment_at<TILE>(seq, cum, p, at, hi); };
 
   // ---- queries of a segment, copied one segment ahead; rows past the new tokens are not read (they may hold anything) but zeros
   auto copy_queries = [&](const Segment &s) {
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 #pragma unroll 1
   for (unsigned round = lo; round < hi;) {            // SEGS segments a round
    if (w == 0) {
-     const int n = list_segments<TILE>(seq, cum, c.batch, p.row_blocks, c.Hkv, round, hi, segs);
+     const int n = list_segments<TILE>(seq, cum, p, round, hi, segs);
      if (lane == 0) segs[SEGS].end = n;
    }
    __syncthreads();
@@ -1093,24 +1093,28 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
 }
 
 // Calls launch(args, tiles) for as many sequences at a time as keep the line of tiles of `tok` tokens, which is counted in 32 bits,
-// below 2^31 whatever their lengths (all of them, but for the largest products of batch, heads, new tokens and table).
+// below 2^31 whatever their lengths (all of them, but for the largest products of batch, heads, new tokens and table); where one sequence
+// passes that, for ranges of its items (a table holds 2^25 tiles at most).
 template <typename F>
 cudaError_t by_batches(const AttendArgs &a, int tok, F launch) {
-  const long per_seq = (long)a.c.Hkv * a.row_blocks * (((long)a.c.table_cols * a.c.page + tok - 1) / tok);
-  const long most = std::max(1L, ((1L << 31) - 1) / per_seq);
+  const long tiles = ((long)a.c.table_cols * a.c.page + tok - 1) / tok, all = (long)a.c.Hkv * a.row_blocks;
+  const long most = ((1L << 31) - 1) / tiles, step = std::min(all, most), seqs = std::max(1L, most / all);
   const int words = (a.c.n_tokens + 31) / 32, es = a.c.io == PACE_IO_F32 ? 4 : 2;
-  for (int b = 0; b < a.c.batch; b += (int)most) {
-    AttendArgs part = a;
-    part.c.batch = (int)std::min(most, (long)a.c.batch - b);
-    part.c.lens += b;
-    if (part.c.n_new) part.c.n_new += b;
-    part.c.table += (long)b * a.c.table_cols;
-    if (part.mask) part.mask += (long)b * a.c.n_tokens * words;
-    part.q.p += b * a.q.sb * es;
-    part.o.p += b * a.o.sb * es;
-    const cudaError_t e = launch(part, per_seq * part.c.batch);
-    if (e != cudaSuccess) return e;
-  }
+  for (long b = 0; b < a.c.batch; b += seqs)
+    for (long item = 0; item < all; item += step) {
+      AttendArgs part = a;
+      part.item0 = (unsigned)item;
+      part.items = (unsigned)std::min(step, all - item);
+      part.c.batch = (int)std::min(seqs, a.c.batch - b);
+      part.c.lens += b;
+      if (part.c.n_new) part.c.n_new += b;
+      part.c.table += b * a.c.table_cols;
+      if (part.mask) part.mask += b * a.c.n_tokens * words;
+      part.q.p += b * a.q.sb * es;
+      part.o.p += b * a.o.sb * es;
+      const cudaError_t e = launch(part, tiles * part.items * part.c.batch);
+      if (e != cudaSuccess) return e;
+    }
   return cudaSuccess;
 }
 

@@ -264,13 +264,13 @@ __global__ void __launch_bounds__(TcShape<D, BITS, MODE>::THREADS, 1) attend_tc_
   }
   pdl_enter();
   fence_before_sync();
-  const unsigned most = tile_line<KVT>(c, (unsigned)p.row_blocks * c.Hkv, seq, cum, wsum);      // (its barriers also publish the set-up above)
+  const unsigned most = tile_line<KVT>(c, p.items, seq, cum, wsum);      // (its barriers also publish the set-up above)
   fence_after_sync();
   constexpr uint32_t tmem = 0;          // the whole of TMEM is this block's: its first column (a constant keeps addresses uniform)
 
   unsigned lo, hi;
-  const Cuts cuts = make_cuts<KVT>(seq, cum, c.batch, (unsigned)p.row_blocks * c.Hkv, most, TC_LEAST, 0, tc_extra(D), lo, hi);
-  auto at = [&](unsigned pos) { return segment_at<KVT>(seq, cum, c.batch, p.row_blocks, pos, hi); };
+  const Cuts cuts = make_cuts<KVT>(seq, cum, c.batch, p.items, most, TC_LEAST, 0, tc_extra(D), lo, hi);
+  auto at = [&](unsigned pos) { return segment_at<KVT>(seq, cum, p, pos, hi); };
   if (tid == 0) {
     const Segment end = lo < hi ? at(hi - 1) : Segment{};
     const bool on = lo < hi && hi - 1 - end.tile >= lo && end.end < end.tiles;

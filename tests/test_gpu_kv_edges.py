@@ -267,3 +267,20 @@ def test_bits_do_not_depend_on_earlier_calls(tmp_path, P, io):
         assert r.returncode == 0, r.stderr[-2000:]
         outs.append(np.load(at))
     assert np.array_equal(outs[0], outs[1]) and np.array_equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("Hkv,G,T,io", [(1, 8, 600, "f32"), (8, 8, 600, "bf16")])
+def test_one_sequence_in_several_launches(P, Hkv, G, T, io):
+    """Where a table could hold 2^30 tokens, the items of one sequence pass what a launch counts, and go out in ranges."""
+    import torch
+    L = Layer(P, 2, Hkv * G, Hkv, 64, 4, io, 4096, 100 + T, seed=12, max_new=600)
+    L.append([0, 0], 100)
+    lens = [100, 33]
+    L.append(lens, T)
+    table = torch.full((2, 1 << 18), -1, dtype=torch.int32, device="cuda")
+    table[:, :L.table.shape[1]] = L.table
+    q = L.rand(2, T, Hkv * G, 64)
+    got = attend(L, q, lens, table=table)
+    assert L.kv.status() == 0
+    for b in range(2):
+        assert relative(got[b], expected(L, b, q, lens[b], T)) <= LIMIT[io]
