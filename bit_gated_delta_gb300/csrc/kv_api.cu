@@ -298,7 +298,7 @@ pace_status pace_kv_get_status(const pace_kv *kv, int clear, int *status_out, vo
   if (word)
     return fail(PACE_ERR_STATE, "cache calls met%s%s%s", word & PACE_KV_BAD_PAGE ? " a slot outside the pages" : "",
                 word & PACE_KV_BAD_POSITION ? " a position outside the rotary table" : "",
-                word & PACE_KV_BAD_KEEP ? " a kept path that does not rise" : "");
+                word & PACE_KV_BAD_KEEP ? " a kept path that does not rise, or its count" : "");
   return ok();
 }
 

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(KvDev c, int max_new, con
   __shared__ uint8_t zero[TILE][2][L::NG];
   const int b = blockIdx.x / c.Hkv, head = blockIdx.x % c.Hkv;
   pdl_enter();
-  const int n = min(max(n_keep[b], 0), c.n_tokens);
+  const int asked = n_keep[b], n = min(max(asked, 0), c.n_tokens);
   const long len = c.lens[b];
   const int32_t *row = idx + (long)b * c.n_tokens;
   int good = n;                                        // the first index that does not rise ends the path
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(KvDev c, int max_new, con
   atomicMin(&sgood, good);
   __syncthreads();
   good = sgood;
-  if (good < n && threadIdx.x == 0) atomicOr(c.status, PACE_KV_BAD_KEEP);
+  if ((good < n || asked != n) && threadIdx.x == 0) atomicOr(c.status, PACE_KV_BAD_KEEP);
   for (int i0 = 0; i0 < good; i0 += TILE) {
     const int m = min(TILE, good - i0);
     for (int w = threadIdx.x; w < m * 2 * PER; w += THREADS) {

@@ -39,7 +39,8 @@ extern "C" {
 enum {
   PACE_KV_BAD_PAGE = 1,      /* a slot outside the page table or a page number outside the pool */
   PACE_KV_BAD_POSITION = 2,  /* a rotary position outside the table (the nearest row was used) */
-  PACE_KV_BAD_KEEP = 4,      /* a kept index outside the drafts or not increasing (it and later ones were left) */
+  PACE_KV_BAD_KEEP = 4,      /* a kept index outside the drafts or not increasing (it and later ones were left), or a kept
+                                count outside 0..n_tokens (taken as the nearest) */
   PACE_KV_TIMEOUT = 8        /* a bounded device wait gave up (the call's outputs are not to be used) */
 };
 

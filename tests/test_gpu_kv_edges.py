@@ -284,3 +284,16 @@ def test_one_sequence_in_several_launches(P, Hkv, G, T, io):
     assert L.kv.status() == 0
     for b in range(2):
         assert relative(got[b], expected(L, b, q, lens[b], T)) <= LIMIT[io]
+
+
+def test_kept_counts_outside_the_path_are_reported(P):
+    L = Layer(P, 3, 2, 2, 64, 8, "f32", 32, 64, seed=6)
+    L.append([0] * 3, 40)
+    before = L.pool.clone()
+    idx = dev(np.tile(np.arange(4, dtype=np.int32), (3, 1)))
+    L.kv.keep(dev(np.array([20] * 3, np.int32)), L.table, idx, dev(np.array([0, 4, 3], np.int32)))
+    assert L.kv.status() == 0
+    for n in ([5, 0, 0], [0, -1, 0], [0, 0, 2 ** 31 - 1]):
+        L.kv.keep(dev(np.array([20] * 3, np.int32)), L.table, idx, dev(np.array(n, np.int32)))
+        assert L.kv.status(clear=True) == P.PACE_KV_BAD_KEEP
+    assert bool((before == L.pool).all())                   # (the paths keep every row where it is)
