@@ -297,3 +297,29 @@ def test_kept_counts_outside_the_path_are_reported(P):
         L.kv.keep(dev(np.array([20] * 3, np.int32)), L.table, idx, dev(np.array(n, np.int32)))
         assert L.kv.status(clear=True) == P.PACE_KV_BAD_KEEP
     assert bool((before == L.pool).all())                   # (the paths keep every row where it is)
+
+
+@pytest.mark.parametrize("rot,scaling", [(256, "ntk"), (64, "parts")])
+def test_an_angle_table_is_built_as_fast_as_by_tensor_operations(P, rot, scaling):
+    """The table's 64-bit powers are formed once a pair, not once an entry (which took four to six times as long)."""
+    import torch
+    n = 32768 * 128 // (rot // 2)
+    rope = P.PaceRope(rot, n, scaling=scaling, factor=4.0, orig_pos=4096)
+    theta = torch.from_numpy(K.thetas(rot, scaling=scaling, factor=4.0, orig_pos=4096)[0]).cuda()
+
+    def plain():
+        angle = torch.arange(n, dtype=torch.float64, device="cuda")[:, None] * theta
+        return torch.cos(angle).float(), torch.sin(angle).float()
+
+    def best(call):
+        times = []
+        for _ in range(8):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            call()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    assert best(lambda: P.pace_rope_table(rope.cfg, rope.ptr, rope.nbytes)) <= best(plain)
