@@ -35,6 +35,27 @@ def _stream(s):
     return s if isinstance(s, int) else s.cuda_stream
 
 
+class _Memory:
+    """Device memory that calls on several streams use: its allocator learns of each stream, so that what is dropped while one of
+    them still works on it is not given out again before that work has ended."""
+
+    def __init__(self, shape, dtype, device, stream):
+        self.tensor = torch.empty(shape, dtype=dtype, device=device)
+        own = torch.cuda.current_stream(self.tensor.device)
+        self.streams = {own.cuda_stream}
+        s = self.on(stream)
+        if s != own.cuda_stream:         # (it may be memory that `own` has not done with)
+            torch.cuda.ExternalStream(s, self.tensor.device).wait_stream(own)
+
+    def on(self, stream):
+        """The raw handle of `stream` (None: the current one), which the memory is now known to be used on."""
+        s = _stream(stream)
+        if s not in self.streams:
+            self.tensor.record_stream(torch.cuda.ExternalStream(s, self.tensor.device))
+            self.streams.add(s)
+        return s
+
+
 @functools.lru_cache(maxsize=None)
 def _fn(name):
     return getattr(lib(), name)
@@ -96,9 +117,10 @@ class PaceRope:
     def __init__(self, rot: int, max_pos: int, device="cuda", stream=None, **kw):
         self.cfg = make_rope_config(rot, max_pos, **kw)
         self.nbytes = pace_rope_bytes(self.cfg)
-        self.table = torch.empty(max_pos, rot // 2, 2, dtype=torch.float32, device=device)
+        self._memory = _Memory((max_pos, rot // 2, 2), torch.float32, device, stream)
+        self.table, self._on = self._memory.tensor, self._memory.on
         self.ptr = self.table.data_ptr()
-        pace_rope_table(self.cfg, self.ptr, self.nbytes, stream)
+        pace_rope_table(self.cfg, self.ptr, self.nbytes, self._on(stream))
 
 
 def pace_rope_apply(rope: PaceRope, x, positions, out, inverse: bool = False, stream=None) -> None:
@@ -108,7 +130,7 @@ def pace_rope_apply(rope: PaceRope, x, positions, out, inverse: bool = False, st
     io = PACE_IO_F32 if x.dtype is torch.float32 else PACE_IO_BF16
     shape = n, h, d = x.shape
     check(_fn("pace_rope_apply")(rope.cfg, rope.ptr, n, h, d, io, _tensor(x, io, shape, "x"), _ints(positions, (n,), "positions"),
-                                 _tensor(out, io, shape, "out"), inverse, _stream(stream)))
+                                 _tensor(out, io, shape, "out"), inverse, rope._on(stream)))
 
 
 # ---- the cache ----------------------------------------------------------------------------------------------------------------
@@ -152,7 +174,8 @@ def pace_kv_append(handle, cfg, q, k, v, lens, table, rope=None, positions=None,
     kv, qs = (B, T, cfg.kv_heads, cfg.d), (B, T, cfg.q_heads, cfg.d)
     check(_fn("pace_kv_append")(handle, _step(B, T, lens, table, n_new), _tensor(q, io, qs, "q"), _tensor(k, io, kv, "k"),
                                 _tensor(v, io, kv, "v"), _tensor(q_out, io, qs, "q_out"), rope.cfg if rope else None,
-                                rope.ptr if rope else None, _ints(positions, (B, T), "positions", True), _stream(stream)))
+                                rope.ptr if rope else None, _ints(positions, (B, T), "positions", True),
+                                rope._on(stream) if rope else _stream(stream)))
 
 
 def pace_kv_read(handle, cfg, k_out, v_out, table, first=None, end=None, stream=None) -> None:
@@ -191,30 +214,32 @@ class PaceKV:
     """Owns a device region (a torch uint8 tensor) bound to a KV-cache handle.
 
     One cache serves one attention layer; lens [B] and table [B, columns] are the caller's and may serve all layers. A step is
-    append (k rotated and quantized, q rotated), attend, and, for drafted trees, keep; the caller then advances lens.
+    append (k rotated and quantized, q rotated), attend, and, for drafted trees, keep; the caller then advances lens. The cache's
+    memory waits for the streams of its calls; tensors passed in are the caller's to keep until a call's stream has done with them.
     """
 
     def __init__(self, cfg: pace_kv_config, device="cuda", stream=None):
         self.cfg = cfg
         self.nbytes = pace_kv_bytes(cfg)
-        self.mem = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
+        self._memory = _Memory(self.nbytes + 256, torch.uint8, device, stream)
+        self.mem, self._on = self._memory.tensor, self._memory.on
         base = (self.mem.data_ptr() + 255) // 256 * 256
-        self.handle = pace_kv_alloc(cfg, base, self.nbytes, stream)
+        self.handle = pace_kv_alloc(cfg, base, self.nbytes, self._on(stream))
 
     def append(self, q, k, v, lens, table, rope=None, positions=None, n_new=None, q_out=None, stream=None):
-        pace_kv_append(self.handle, self.cfg, q, k, v, lens, table, rope, positions, n_new, q_out, stream)
+        pace_kv_append(self.handle, self.cfg, q, k, v, lens, table, rope, positions, n_new, q_out, self._on(stream))
 
     def read(self, k_out, v_out, table, first=None, end=None, stream=None):
-        pace_kv_read(self.handle, self.cfg, k_out, v_out, table, first, end, stream)
+        pace_kv_read(self.handle, self.cfg, k_out, v_out, table, first, end, self._on(stream))
 
     def attend(self, q, o, lens, table, mask=None, n_new=None, scale=None, stream=None):
-        pace_kv_attend(self.handle, self.cfg, q, o, lens, table, mask, n_new, scale, stream)
+        pace_kv_attend(self.handle, self.cfg, q, o, lens, table, mask, n_new, scale, self._on(stream))
 
     def keep(self, lens, table, idx, n_keep, stream=None):
-        pace_kv_keep(self.handle, lens, table, idx, n_keep, stream)
+        pace_kv_keep(self.handle, lens, table, idx, n_keep, self._on(stream))
 
     def status(self, clear: bool = False, stream=None) -> int:
-        return pace_kv_get_status(self.handle, clear, stream)
+        return pace_kv_get_status(self.handle, clear, self._on(stream))
 
     def close(self):
         if getattr(self, "handle", None):

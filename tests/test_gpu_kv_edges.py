@@ -323,3 +323,23 @@ def test_an_angle_table_is_built_as_fast_as_by_tensor_operations(P, rot, scaling
         return min(times)
 
     assert best(lambda: P.pace_rope_table(rope.cfg, rope.ptr, rope.nbytes)) <= best(plain)
+
+
+def test_memory_of_a_cache_waits_for_the_streams_that_use_it(P):
+    """A cache and a table that are dropped while another stream still works on them keep their memory until it is done."""
+    import torch
+    cfg = P.make_kv_config(2, 2, 64, 64, 1, bits=8, page_tokens=64)
+    kv, rope = P.PaceKV(cfg), P.PaceRope(64, 5000)
+    lens, table = dev(np.zeros(1, np.int32)), dev(np.arange(64, dtype=np.int32)[None])
+    q, k, v, qo = (torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)                      # (about 0.2 s)
+        kv.append(q, k, v, lens, table, rope=rope, q_out=qo)
+    sizes = {x.data_ptr(): x.numel() * x.element_size() for x in (kv.mem, rope.table)}
+    del kv, rope
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for size in sizes.values()]
+    busy = not s.query()
+    assert busy and not {o.data_ptr() for o in others} & set(sizes)
+    s.synchronize()
