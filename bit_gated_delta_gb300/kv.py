@@ -2,7 +2,7 @@
 
 Binding of include/pace_kv.h: the pace_* functions marshal tensors (shape, type, device and stride checks happen here, value
 ranges in the library), PaceRope and PaceKV own the table and the cache region. Tensors are [batch, tokens, heads, d] views
-with d contiguous; lengths, page tables, masks and paths are contiguous int32 tensors.
+with d contiguous; lengths, page tables, masks and paths are contiguous int32 tensors; all of a call is on the current device.
 """
 from __future__ import annotations
 
@@ -29,9 +29,12 @@ __all__ = ["make_rope_config", "pace_rope_bytes", "pace_rope_table", "pace_rope_
 
 # The calls below are made for every layer and token, so their marshalling is kept short: raw stream handles, one stride() per
 # tensor, library functions looked up once.
+_device = getattr(torch._C, "_cuda_getDevice", None)     # the current device's index
+
+
 def _stream(s):
     if s is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_device())
     return s if isinstance(s, int) else s.cuda_stream
 
 
@@ -49,6 +52,8 @@ class _Memory:
 
     def on(self, stream):
         """The raw handle of `stream` (None: the current one), which the memory is now known to be used on."""
+        if self.tensor.get_device() != _device():
+            raise ValueError(f"memory on {self.tensor.device}, but the current device is {_device()}")
         s = _stream(stream)
         if s not in self.streams:
             self.tensor.record_stream(torch.cuda.ExternalStream(s, self.tensor.device))
@@ -71,9 +76,9 @@ def _tensor(t, io, shape, name):
     if t is None:
         return None
     st = t.stride()
-    if t.dtype is not _dtype(io) or not t.is_cuda or t.shape != shape or (st[-1] != 1 and shape[-1] > 1 and t.numel()):
-        raise ValueError(f"{name}: expected a {_dtype(io)} CUDA tensor of shape {tuple(shape)} with its last dimension contiguous, "
-                         f"got {t.dtype} on {t.device}, shape {tuple(t.shape)}, strides {st}")
+    if t.dtype is not _dtype(io) or t.get_device() != _device() or t.shape != shape or (st[-1] != 1 and shape[-1] > 1 and t.numel()):
+        raise ValueError(f"{name}: expected a {_dtype(io)} tensor on the current CUDA device, of shape {tuple(shape)} with its last "
+                         f"dimension contiguous, got {t.dtype} on {t.device}, shape {tuple(t.shape)}, strides {st}")
     if 1 in shape:                       # the stride of a single element is anything
         st = [0 if n == 1 else x for n, x in zip(shape, st)]
     return pace_tensor(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
@@ -85,9 +90,9 @@ def _ints(t, shape, name, optional=False):
         if optional:
             return None
         raise ValueError(f"{name} is missing")
-    if t.dtype not in _INTS or not t.is_cuda or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor of shape {tuple(shape)}, got {t.dtype} on {t.device}, "
-                         f"shape {tuple(t.shape)}, strides {t.stride()}")
+    if t.dtype not in _INTS or t.get_device() != _device() or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 tensor on the current CUDA device, of shape {tuple(shape)}, got {t.dtype} on "
+                         f"{t.device}, shape {tuple(t.shape)}, strides {t.stride()}")
     return t.data_ptr()
 
 

@@ -134,3 +134,47 @@ def test_attention_statement_by_hand():
     see = np.array([[True, False, True]])
     assert np.allclose(K.attend(q, k, v, see, 1.0), (1 + 2 * 4) / 3)
     assert (K.attend(q, k, v, np.zeros((1, 3), bool), 1.0) == 0).all()
+
+
+class OnDevice:
+    """What the binding looks at of a tensor, on a device that need not exist."""
+
+    def __init__(self, shape, dtype, device):
+        import torch
+        self.shape, self.dtype, self.device, self.is_cuda = torch.Size(shape), dtype, torch.device("cuda", device), True
+
+    def get_device(self):
+        return self.device.index
+
+    def stride(self):
+        return tuple(int(np.prod(self.shape[i + 1:])) for i in range(len(self.shape)))
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+
+def test_tensors_of_another_device_are_refused(P, monkeypatch):
+    """A call runs on the current device's stream: tensors, caches and tables of another one are refused before any launch."""
+    import torch
+
+    from bit_gated_delta_gb300 import kv
+    monkeypatch.setattr(kv, "_device", lambda: 0, raising=False)
+    shape = (1, 2, 2, 64)
+    assert kv._tensor(OnDevice(shape, torch.bfloat16, 0), P.PACE_IO_BF16, shape, "q").data == 4096
+    assert kv._ints(OnDevice((2,), torch.int32, 0), (2,), "lens") == 4096
+    with pytest.raises(ValueError, match="current CUDA device"):
+        kv._tensor(OnDevice(shape, torch.bfloat16, 1), P.PACE_IO_BF16, shape, "q")
+    with pytest.raises(ValueError, match="current CUDA device"):
+        kv._ints(OnDevice((2,), torch.int32, 1), (2,), "lens")
+    memory = object.__new__(kv._Memory)
+    memory.tensor, memory.streams = OnDevice((64,), torch.uint8, 1), {7}
+    with pytest.raises(ValueError, match="current device"):
+        memory.on(7)
+    memory.tensor = OnDevice((64,), torch.uint8, 0)
+    assert memory.on(7) == 7
