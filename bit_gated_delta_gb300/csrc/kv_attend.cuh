@@ -796,8 +796,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
       }
       // ---- weights. bf16 I/O: the scale of a value group enters the exponent, w = 2^(s + log2 s_v - m + 6) with m the running
       // maximum of s + log2 s_v, so that fp16 weights keep 11 bits whatever the scales; the sum takes 2^(s - m + 6). fp32 I/O: the
-      // scale multiplies the weight, and m lies 64 above the scores of tokens whose scale passes 2^60, so that no sum of weighted values
-      // leaves fp32 (held values reach 2^120). m is raised only when a score passes it by 2^8 (fp16 weights up to 2^14, sums in fp32).
+      // scale multiplies the weight, and m is raised to 64 above the scores of tokens whose scale reaches 2^65, so that no sum of weighted
+      // values leaves fp32 (held values reach 2^120). m is raised only when a score passes it by 2^8 (fp16 weights up to 2^14, sums in fp32).
+      constexpr uint32_t BIG = 0x60000000u;              // 2^65
+      uint32_t top = 0;
       float lv[NG][2][2], lm[2][2];                      // log2 of the value scales of the lane's tokens, their largest
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
@@ -815,12 +817,12 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
             if (edge && (tok0 + 16 * blk + 8 * half + tau(j) >= tokens || lost)) x = 0.0f;   // never written: may hold anything
             lv[g][blk][half] = !F32 ? log2_approx(x) : x;
             if (!F32) lm[blk][half] = fmaxf(lm[blk][half], lv[g][blk][half]);
-            else if (x >= 0x1p60f) lm[blk][half] = 64.0f;
+            else top = max(top, __float_as_uint(x));     // (scales are not negative: their bits order as integers)
           }
         }
       }
       float mx[NT][2];
-      bool grow = false;
+      bool grow = F32 && top >= BIG;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -830,6 +832,20 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
           grow |= mx[n][r] > m[n][r] + 8.0f;
         }
       if (__any_sync(0xffffffffu, grow)) {
+        if (F32 && top >= BIG) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float most = 0.0f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) most = fmaxf(most, lv[g][i >> 1][i & 1]);
+            if (most >= __uint_as_float(BIG)) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) mx[n][r] = fmaxf(mx[n][r], fmaf(s[i >> 1][n][2 * (i & 1) + r], crow[n][r], 64.0f));
+            }
+          }
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
