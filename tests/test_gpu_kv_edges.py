@@ -343,3 +343,44 @@ def test_memory_of_a_cache_waits_for_the_streams_that_use_it(P):
     busy = not s.query()
     assert busy and not {o.data_ptr() for o in others} & set(sizes)
     s.synchronize()
+
+
+# What is left beside the rounding of the output, as a root mean square of the difference from the output type's rounding of the exact
+# value. A rounding to p bits is 0.42 2^-p of a value, so 2e-4 for weights of 11 bits (few rows); with held values of 11 bits and scores that move
+# by twice that, 4e-4 (many rows; held 4-bit values have few bits to lose). An error e moves a bf16 output to its neighbour, 5.6e-3 away, once
+# in 5.6e-3 / 0.8 e: 1e-3 of the output (few rows) and 1.4e-3 (many). Weights of 8 bits would give 2.4e-3 or more. fp32: sums of exact
+# products and the exponential, each a few 2^-23; a lost third part of a query or weight would give 6e-6.
+@pytest.mark.parametrize("d,bits,T,G,io,limit", [
+    (64, 4, 1, 8, "bf16", 1.3e-3), (128, 8, 1, 6, "bf16", 1.3e-3), (128, 4, 4, 4, "bf16", 1.3e-3), (256, 8, 7, 1, "bf16", 1.3e-3), (64, 8, 32, 1, "bf16", 1.3e-3),
+    (128, 4, 25, 4, "bf16", 1.5e-3), (64, 4, 100, 4, "bf16", 1.5e-3), (256, 4, 40, 2, "bf16", 1.5e-3), (128, 8, 60, 4, "bf16", 2e-3), (256, 8, 40, 2, "bf16", 2e-3),
+    (64, 8, 1, 4, "f32", 2e-6), (128, 4, 5, 2, "f32", 2e-6), (256, 8, 20, 1, "f32", 2e-6), (128, 8, 40, 2, "f32", 2e-6)])
+def test_bits_that_queries_weights_and_values_keep(P, d, bits, T, G, io, limit):
+    L = Layer(P, 2, 2 * G, 2, d, bits, io, 64, 750 + T, seed=14)
+    for at in (0, 250, 500):
+        L.append([at] * 2, 250)
+    lens = [750, 611]
+    L.append(lens, T)
+    q = L.rand(2, T, 2 * G, d)
+    got = attend(L, q, lens)
+    for b in range(2):
+        want = expected(L, b, q, lens[b], T)
+        to = K.bf16(want.astype(np.float32)) if io == "bf16" else want
+        assert relative(got[b], to.astype(np.float64)) <= limit
+
+
+@pytest.mark.parametrize("d,bits,T,G", [(128, 4, 1, 4), (128, 8, 20, 1), (256, 8, 1, 4), (128, 4, 40, 2), (128, 8, 150, 1), (256, 4, 50, 1), (256, 8, 50, 1)])
+def test_groups_of_very_different_size(P, d, bits, T, G):
+    """A group 2^-12 of its head vector's largest keeps its bits; one of 2^-30 is within 2^-22 of the vector's largest element."""
+    for ratio in (2.0 ** -12, 2.0 ** -30):
+        L = Layer(P, 1, 2 * G, 2, d, bits, "bf16", 64, 256 + T, seed=15)
+        k, v = L.rand(1, 256 + T, 2, d), L.rand(1, 256 + T, 2, d)
+        v[..., d - 64:] *= np.float32(ratio)
+        L.append([0], 256, k=k[:, :256], v=v[:, :256])
+        L.append([256], T, k=k[:, 256:], v=v[:, 256:])
+        q = L.rand(1, T, 2 * G, d)
+        got, want = attend(L, q, [256])[0], expected(L, 0, q, 256, T)
+        assert relative(got[..., :d - 64], want[..., :d - 64]) <= LIMIT["bf16"]
+        if ratio == 2.0 ** -12:
+            assert relative(got[..., d - 64:], want[..., d - 64:]) <= LIMIT["bf16"]
+        else:
+            assert np.abs(got[..., d - 64:] - want[..., d - 64:]).max() <= 2.0 ** -22 * np.abs(L.v).max()
