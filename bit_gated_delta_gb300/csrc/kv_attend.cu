@@ -16,8 +16,11 @@ using namespace pace::kv;
 
 namespace {
 // Rows of one KV head from which the tensor-memory kernel takes over (bf16 I/O). It works on 128 rows whatever their number, and the
-// other on 8 to 32 at a time. Heads of 128, 16 sequences of 8000 tokens: 112 and 98 us at 32 rows, 112 and 141 us at 40; one sequence of
-// 2000 tokens: 17 and 15 us, 18 and 16 us. Heads of 256: 56 and 67 us, 56 and 81 us.
+// other on 8 (heads of 256), 16 (128) or 32 (64) at a time. One bound for all head sizes, since up to it codes enter the products exactly.
+// 16 sequences of 8000 tokens, 8 KV heads, 4 bits, this kernel's and the other's us at 16, 32, 40 and 64 rows: heads of 64 93 and 44, 95 and
+// 62, 95 and 93, 95 and 93; of 128 118 and 60, 120 and 97, 120 and 140, 120 and 179; of 256 148 and 126, 148 and 226, 149 and 279, 150 and
+// 434 (for speed alone this kernel would take heads of 256 from 17 rows on). One sequence of 2000 tokens, heads of 128: 21 and 21, 21 and 15,
+// 21 and 21, 29 and 21.
 constexpr int TC_ROWS = 33;
 // Rows of an item of the other kernel (fp32 I/O takes three products a tile, and eight rows).
 int block_rows(const KvDev &c) { return c.io == PACE_IO_F32 ? 8 : 2048 / c.d; }

@@ -9,16 +9,21 @@
 //
 // The cache is bound by bytes only if its codes reach the tensor cores in about three instructions each (46 4-bit elements a
 // clock and SM at the measured 6.8 TB/s against 128 lanes, half of that for bit operations), so codes become fp16 under the
-// exponent of 1024 by one bit operation a pair and one exact subtraction on the other pipe, and enter the products as integers.
+// exponent of 1024 by one bit operation a pair and one exact subtraction on the other pipe (the conversion is described by Kim et al.,
+// "Who Says Elephants Can't Run", 2022), and enter the products as integers.
 // The scales of a key group multiply the fp32 accumulators, those of a value group enter the exponent of the weights. Queries and
 // weights are fp16 relative to a power of two (11 bits); with fp32 I/O both are three bf16 parts, so nothing is rounded below 2^-24.
 //
 // Work: the tiles of all (sequence, KV head, row block) items form one line, cut into equal shares, one a block; a block's warps
 // take its tiles in turn, each through its own ring of tiles filled by bulk copies (one copy a tile). Items cut by a share
 // boundary leave partial results; the last block to finish an item joins them, in block order, so results do not depend on timing.
-// Measured, one token, cold: 16 sequences of 30,000 to 32,767 tokens, 48 and 8 heads of 128, 8 bits 160 us (6.6 TB/s; 180 us after
-// other writes have filled the L2); 64 sequences of 512 to 4096 tokens, 32 and 8 heads of 128, 4 bits 51 us (floor 24: the issue of
-// dequantization, 46 elements a clock and SM, and a chain of about 8 us that every call has); one sequence of 300 tokens 8 us.
+// Measured, one token, cold: 16 sequences of 30,000 to 32,767 tokens, 48 and 8 heads of 128, 8 bits 159 us (6.7 TB/s; 180 us after
+// other writes have filled the L2); 64 sequences of 512 to 4096 tokens, 32 and 8 heads of 128, 4 bits 51 us (bytes 24; its instructions,
+// three an element, would issue in 24 too: the rest are waits, of which the counters name fixed latency and barriers first. Most items
+// are cut in two, each cut has its block-wide barriers and a join by one warp, and every call a chain of about 8 us); one sequence of
+// 300 tokens 8 us. fp32 I/O: 16 sequences of 30,000 to 32,000 tokens, 32 and 8 heads of 64, 8 bits 162 us (bytes 77), of 128, 4 bits 219
+// (82); trees of 25 tokens, 8 sequences of 2000 to 4000, heads of 128 152 us; chunks of 256, 2 sequences, 378 us: three products a tile, and
+// eight rows an item, so that each pass over a head's tiles serves eight rows.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -795,7 +800,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) attend_kernel(AttendArgs p) {
           }
       }
       // ---- weights. bf16 I/O: the scale of a value group enters the exponent, w = 2^(s + log2 s_v - m + 6) with m the running
-      // maximum of s + log2 s_v, so that fp16 weights keep 11 bits whatever the scales; the sum takes 2^(s - m + 6). fp32 I/O: the
+      // maximum of s + log2 s_v, so that fp16 weights keep 11 bits down to 2^-20 of a row's largest; the sum takes 2^(s - m + 6). fp32 I/O: the
       // scale multiplies the weight, and m is raised to 64 above the scores of tokens whose scale reaches 2^65, so that no sum of weighted
       // values leaves fp32 (held values reach 2^120). m is raised only when a score passes it by 2^8 (fp16 weights up to 2^14, sums in fp32).
       constexpr uint32_t BIG = 0x60000000u;              // 2^65

@@ -25,9 +25,9 @@
 // warps, four of which serve both blocks, are what it waits for (eight cost the softmax warps more issue slots and registers than they
 // gain). ALT runs at 1800: the chain of scale preparation, dequantization and products through shared memory. Fixed per call about 10 us
 // (first look-ups, queries, first tile, outputs), per further item of a block about 8 us.
-// Measured (4-bit cache, cold): prompt chunks of 256 tokens, 4 sequences, 32 and 8 heads of 128, over 8192 tokens 144 us, 970 TFLOP/s
-// of the measured 1880; trees of 25 drafts, 16 sequences, over 2049 to 4096 tokens 62 us, over 8192 116 us; 7 drafts, 32 sequences of
-// 1000 to 6000 tokens, 16 and 2 heads of 256, 66 us.
+// Measured (4-bit cache, cold): prompt chunks of 256 tokens, 4 sequences, 32 and 8 heads of 128, over 6000 to 8000 tokens 136 us, 860 TFLOP/s
+// of the measured 1880; trees of 25 drafts, 16 sequences, over 2049 to 4096 tokens 63 us (62 before lost halves and the size of context
+// tokens were looked at), 64 rows over 8000 tokens 120 us; 7 drafts, 32 sequences of 1000 to 6000 tokens, 16 and 2 heads of 256, 66 us.
 // Every wait is bounded; one that gives up sets the status word, and the block leaves after its copies and products have ended.
 #pragma once
 
@@ -45,7 +45,8 @@ constexpr int TC_BLOCKS = 160;        // most blocks of a launch (one an SM)
 constexpr int TC_LEAST = 4;
 // An item a block while the longest is so many tiles above an equal share: sharing costs a block the queries, the first tile and the
 // outputs of another item, about as many tiles' time as this (eight sequences of up to 2048 tokens under trees, heads of 64: 22 us
-// shared, 28 an item a block; sixteen with heads of 128: 71 and 66 us).
+// shared, 28 an item a block; sixteen with heads of 128: 71 and 66 us). Heads of 256, with 24 and with 8: 16 sequences of 2000 to 4000
+// tokens, 8 KV heads, 40 rows 83 and 93 us; 64 of 300 to 1200, 2 heads 38 and 58; 8 of 500 to 2000, 8 heads, 100 rows 52 and 44.
 __host__ __device__ constexpr unsigned tc_extra(int D) { return D == 64 ? 10 : 24; }
 
 template <int D, int BITS, int MODE>

@@ -5,8 +5,9 @@
 // vector, 256/D vectors a warp; the floor of every call is its bytes at the copy bandwidth (6.8 TB/s; what only writes, 4.0).
 // Measured, with cold caches:
 //   rotation of 16,384 tokens, 32 heads of 128, bf16 (268 MB)                   40 us, 6.7 TB/s
-//   append of 16 x 256 tokens, 48 and 8 heads of 128, 8 bits, 32 of 128 rotated  31 us (126 MB: 19 us); key and value blocks are bound
-//                                                                               by issue (about 300 instructions a warp and vector)
+//   append of 16 x 256 tokens, 48 and 8 heads of 128, 8 bits, 32 of 128 rotated  30 us (126 MB: 19 us); 20.0 M warp instructions would
+//                                                                               issue in 16 us (slots 63% busy, DRAM 35%): the longest
+//                                                                               stall is on the loads that each warp begins with
 //   read-back of 4 x 20,000 to 32,768 tokens, 8 heads of 128, 4 bits            113 us; writing as many zeros takes 108
 //   append of 64 single tokens 4 us, keep of 8 paths 4 us: a chain of three dependent loads
 #include "kv_common.cuh"

@@ -54,7 +54,9 @@ enum {
  *           fastest is unchanged)
  *   PARTS   per pair by its turns over the trained context r_i = orig_pos theta_i / (2 pi):
  *           g = clamp((r_i - beta_slow) / (beta_fast - beta_slow), 0, 1), theta_i (g + (1 - g) / factor),
- *           with m = 0.1 ln(factor) + 1 (m = 1 for the other kinds) */
+ *           with m = 0.1 ln(factor) + 1 (m = 1 for the other kinds). The ramp is linear in the turns, as published; checkpoints
+ *           whose code ramps linearly over the pair index i, between the pairs that turn beta_fast and beta_slow times, have
+ *           other angles between those pairs */
 enum { PACE_ROPE_HALF = 0, PACE_ROPE_INTERLEAVED = 1 };    /* pairs (i, i + rot/2) or (2i, 2i + 1) */
 enum { PACE_ROPE_PLAIN = 0, PACE_ROPE_LINEAR = 1, PACE_ROPE_NTK = 2, PACE_ROPE_PARTS = 3 };
 
@@ -135,7 +137,11 @@ pace_status pace_kv_read(const pace_kv *kv, const pace_kv_step *step, const int3
  * that sees nothing, and rows t >= n_new[b], get zeros. q, o [batch][n_tokens][q_heads][d]. Scores, maxima, sums and
  * the output accumulate in fp32. With fp32 I/O, and where a KV head has up to 32 rows (new tokens times query heads of
  * it), codes enter the products as exact integers; with bf16 I/O queries and weights are rounded to 11 bits, and above 32
- * rows held keys and values too. The same call gives the same bits. One launch, or two above 32 rows. */
+ * rows held keys and values too. Tokens keep these bits whatever the size of others that weigh less. Within one head
+ * vector a group of values (above 32 rows of keys too) keeps them down to 2^-12 of the largest group and loses them gradually
+ * below; what is lost is below 2^-22 of the vector's largest element. With bf16 I/O and up to 32 rows, values whose scale is
+ * below 2^-80 lose bits, and below 2^-90 count as zero. The same call gives the same bits. One launch, or two above 32 rows (more only where a batch or a sequence
+ * could hold 2^31 tiles of work). */
 pace_status pace_kv_attend(pace_kv *kv, const pace_kv_step *step, const pace_tensor *q, const uint32_t *mask, float scale,
                            const pace_tensor *o, void *stream);
 

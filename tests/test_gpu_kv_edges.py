@@ -384,3 +384,15 @@ def test_groups_of_very_different_size(P, d, bits, T, G):
             assert relative(got[..., d - 64:], want[..., d - 64:]) <= LIMIT["bf16"]
         else:
             assert np.abs(got[..., d - 64:] - want[..., d - 64:]).max() <= 2.0 ** -22 * np.abs(L.v).max()
+
+
+@pytest.mark.parametrize("d,bits,T,G,size", [(128, 4, 1, 4, 2.0 ** -70), (64, 8, 16, 1, 2.0 ** -70), (128, 8, 40, 2, 2.0 ** -110), (64, 4, 100, 2, 2.0 ** -110),
+                                             (256, 4, 50, 1, 2.0 ** -110)])
+def test_tiny_values_alone(P, d, bits, T, G, size):
+    L = Layer(P, 1, 2 * G, 2, d, bits, "bf16", 64, 256 + T, seed=16)
+    v = K.bf16(L.rand(1, 256 + T, 2, d) * np.float32(size))
+    L.append([0], 256, v=v[:, :256])
+    L.append([256], T, v=v[:, 256:])
+    q = L.rand(1, T, 2 * G, d)
+    got, want = attend(L, q, [256])[0].astype(np.float64) / size, expected(L, 0, q, 256, T) / size
+    assert relative(got, want) <= LIMIT["bf16"]
