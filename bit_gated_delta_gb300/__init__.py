@@ -174,7 +174,7 @@ def pace_resident_bits(cfg: pace_config, head_is_int8=None, literal_formula: boo
 
 
 class PaceState:
-    """Owns a device region (a torch uint8 tensor) bound to a libpace state handle."""
+    """Owns a device region (a torch uint8 tensor) bound to a libpace state handle. Its memory waits for the streams of its methods' calls."""
 
     def __init__(self, cfg: pace_config, batch: int, head_is_int8=None, device="cuda", stream=None):
         import torch
@@ -182,9 +182,10 @@ class PaceState:
         self.batch = batch
         self.head_is_int8 = None if head_is_int8 is None else np.asarray(head_is_int8, np.uint8).copy()
         self.nbytes = pace_state_bytes(cfg, head_is_int8)
-        self.mem = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
+        self._memory = _kv._Memory(self.nbytes + 256, torch.uint8, device, stream)
+        self.mem, self._on = self._memory.tensor, self._memory.on
         self.base = (self.mem.data_ptr() + 255) // 256 * 256
-        self.handle = pace_state_alloc(cfg, head_is_int8, self.base, self.nbytes, batch, stream)
+        self.handle = pace_state_alloc(cfg, head_is_int8, self.base, self.nbytes, batch, self._on(stream))
         self.layout = pace_state_get_layout(self.handle)
 
     def region(self):
@@ -193,16 +194,16 @@ class PaceState:
         return self.mem[off:off + self.layout.total_bytes]
 
     def decode_step(self, q, k, v, a, beta, o, stream=None):
-        pace_decode_step(self.handle, q, k, v, a, beta, o, stream)
+        pace_decode_step(self.handle, q, k, v, a, beta, o, self._on(stream))
 
     def prefill_chunk(self, q, k, v, a, beta, o, stream=None):
-        pace_prefill_chunk(self.handle, int(a.shape[-1]), q, k, v, a, beta, o, stream)
+        pace_prefill_chunk(self.handle, int(a.shape[-1]), q, k, v, a, beta, o, self._on(stream))
 
     def flush(self, stream=None):
-        pace_flush(self.handle, stream)
+        pace_flush(self.handle, self._on(stream))
 
     def validate(self, stream=None) -> dict:
-        return pace_validate_state(self.handle, stream)
+        return pace_validate_state(self.handle, self._on(stream))
 
     def close(self):
         if getattr(self, "handle", None):
