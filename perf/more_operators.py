@@ -479,7 +479,7 @@ def _plain_take(table, lens, refs, n_new, page):
     want |= copy[:, None] & (col == c0[:, None])
     need = want.sum(1)
     free = torch.nonzero(refs == 0)[:, 0].int()
-    fits = need.cumsum(0) <= free.numel()
+    fits = (need.cumsum(0) <= free.numel()) | (need == 0)
     want &= fits[:, None]
     copy &= fits
     rank = (want.flatten().cumsum(0) - 1).view(B, C)
