@@ -55,6 +55,22 @@ class pace_kv_step(C.Structure):
                 ("table_cols", C.c_int)]
 
 
+class pace_delta_config(C.Structure):
+    _fields_ = [("heads", C.c_int), ("key_heads", C.c_int), ("d", C.c_int), ("n_slots", C.c_int), ("io_dtype", C.c_int)]
+
+
+class pace_delta_step(C.Structure):
+    _fields_ = [("batch", C.c_int), ("n_tokens", C.c_int), ("slots", C.c_void_p), ("lens", C.c_void_p), ("n_new", C.c_void_p)]
+
+
+class pace_pages_config(C.Structure):
+    _fields_ = [("n_pages", C.c_int), ("page_tokens", C.c_int), ("max_batch", C.c_int)]
+
+
+class pace_pages_layout(C.Structure):
+    _fields_ = [("refs", C.c_size_t), ("src", C.c_size_t), ("dst", C.c_size_t), ("n_moves", C.c_size_t), ("total_bytes", C.c_size_t)]
+
+
 class PaceError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{_STATUS_NAMES.get(status, status)}: {msg}")
@@ -105,6 +121,27 @@ _KV_SIGS = {   # include/pace_kv.h
     "pace_kv_get_status": (_I, [_VP, _I, C.POINTER(C.c_int), _VP]),
 }
 
+_PD, _PP, _PDC, _PPC = C.POINTER(pace_delta_step), C.POINTER(pace_pages_layout), C.POINTER(pace_delta_config), C.POINTER(pace_pages_config)
+_SERVE_SIGS = {   # include/pace_serve.h
+    "pace_delta_bytes": (_I, [_PDC, C.POINTER(_SZ)]),
+    "pace_delta_alloc": (_I, [_PDC, _VP, _SZ, _VP, C.POINTER(_VP)]),
+    "pace_delta_free": (None, [_VP]),
+    "pace_delta_chunk": (_I, [_VP, _PD, _PT, _PT, _PT, _PT, _PT, _PT, _VP]),
+    "pace_delta_draft": (_I, [_VP, _PD, _PT, _PT, _PT, _PT, _PT, _VP, _PT, _VP]),
+    "pace_delta_keep": (_I, [_VP, _PD, _PT, _PT, _PT, _PT, _VP, _I, _VP, _VP]),
+    "pace_delta_get_status": (_I, [_VP, _I, C.POINTER(C.c_int), _VP]),
+    "pace_verify": (_I, [_I, _I, _I, _I, _VP, _PT, _PT, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "pace_pages_get_layout": (_I, [_PPC, _PP]),
+    "pace_pages_alloc": (_I, [_PPC, _VP, _SZ, _VP, C.POINTER(_VP)]),
+    "pace_pages_free": (None, [_VP]),
+    "pace_pages_select": (_I, [_VP, _I, _VP, _I, _VP, _VP, _VP]),
+    "pace_pages_take": (_I, [_VP, _I, _VP, _I, _VP, _VP, _VP, _VP]),
+    "pace_pages_compact": (_I, [_VP, _I, _VP, _I, _VP]),
+    "pace_pages_get_status": (_I, [_VP, _I, C.POINTER(C.c_int), _VP]),
+    "pace_kv_copy_pages": (_I, [_VP, _VP, _VP, _VP, _I, _VP]),
+    "pace_kv_pool": (_I, [_VP, C.POINTER(_VP), C.POINTER(_SZ)]),
+}
+
 
 def lib() -> C.CDLL:
     """The loaded library. Raises if libpace.so has not been built (no fallback exists)."""
@@ -114,7 +151,7 @@ def lib() -> C.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m bit_gated_delta_gb300.build` "
                                "or __graft_entry__.build(); there is no fallback implementation")
         L = C.CDLL(LIB_PATH)
-        for name, (res, args) in {**_SIGS, **_KV_SIGS}.items():
+        for name, (res, args) in {**_SIGS, **_KV_SIGS, **_SERVE_SIGS}.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -130,6 +167,11 @@ def exported_symbols() -> list[str]:
 def exported_kv_symbols() -> list[str]:
     """Names declared in include/pace_kv.h."""
     return list(_KV_SIGS)
+
+
+def exported_serve_symbols() -> list[str]:
+    """Names declared in include/pace_serve.h."""
+    return list(_SERVE_SIGS)
 
 
 def check(status: int) -> None:

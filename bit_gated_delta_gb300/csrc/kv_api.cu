@@ -6,6 +6,7 @@
 #include <new>
 
 #include "kv_common.cuh"
+#include "serve_internal.h"
 
 struct pace_kv {
   pace_kv_config cfg;
@@ -122,6 +123,11 @@ pace_status check_step(const pace_kv *kv, const pace_kv_step *s, const char *cal
 bool empty(const pace_kv_step *s) { return s->batch == 0 || s->n_tokens == 0; }
 
 }  // namespace
+
+const KvDev &pace_kv_view(const pace_kv *kv) { return kv->dev; }
+size_t pace_kv_page_bytes(const pace_kv *kv) {
+  return (size_t)kv->cfg.kv_heads * (kv->cfg.page_tokens / PACE_KV_TILE) * tile_bytes(&kv->cfg);
+}
 
 extern "C" {
 

@@ -1,0 +1,312 @@
+// Verification of drafted tokens against the target's probabilities (pace_serve.h).
+//
+// A cluster of blocks takes a sequence, each block a stretch of the vocabulary, each warp a stretch of that. The walk over the nodes needs p and q
+// at the drafts only, which are fetched for all nodes at once; every block walks by itself. The rows are read where the walk needs a sum:
+// after a refused draft (R = max(R - q Z, 0), whose sum is the next Z) and for the next token. So a chain reads one row of p and q
+// a sequence, whatever its length. The next token is found by the prefix of the blocks' sums, of the warps', and in one warp of the tokens.
+//
+// Sums in fixed point. A value r in 0..1 enters as two integers: the upper from the bits of r + 1 (units of 2^-23, exact), the rest
+// from the bits of rest + 1.5 * 2^-23 (units of 2^-46). Differences p - q carry their rounding error along (it is exact in fp32), so
+// that sums have the accuracy of 64-bit floating point at the fp32 rate (the fp64 pipe is a 64th of it), and no order changes them.
+#include <cooperative_groups.h>
+
+#include "serve_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace pace {
+namespace verify {
+
+constexpr int NODES = PACE_VERIFY_MAX_NODES;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int MAX_BLOCKS = 8;                            // of a cluster
+constexpr int UNROLL = 8;                                // tokens a lane has under way
+
+template <bool F32>
+__device__ __forceinline__ float prob(const char *row, long v) {
+  // clamped to 0..1, NaN is 0
+  return __saturatef(F32 ? __ldg(reinterpret_cast<const float *>(row) + v)
+                         : __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16 *>(row) + v)));
+}
+
+// What refused drafts left of one token: R = p, then R = max(R - q Z_i, 0) for the Z of each refusal, as a sum of two floats.
+struct Rest {
+  float r, e;
+};
+struct Factor {
+  float hi, lo;                                          // Z of a refusal
+};
+__device__ __forceinline__ Rest first_rest(float p, float q) {       // Z = 1
+  const float r = p - q;
+  if (!(r > 0.0f)) return Rest{0.0f, 0.0f};
+  return Rest{r, (p - r) - q};                           // (p >= q: the error of the difference)
+}
+__device__ __forceinline__ Rest next_rest(Rest x, float q, Factor z) {
+  const float m = __fmul_rn(q, z.hi), em = fmaf(q, z.lo, fmaf(q, z.hi, -m));
+  const float s = __fadd_rn(x.r, -m), b = __fadd_rn(s, -x.r);
+  const float err = __fadd_rn(__fadd_rn(x.r, -__fadd_rn(s, -b)), -__fadd_rn(m, b));
+  const float e = __fadd_rn(err, __fadd_rn(x.e, -em)), r = __fadd_rn(s, e);
+  if (!(r > 0.0f)) return Rest{0.0f, 0.0f};
+  return Rest{r, __fadd_rn(e, -__fadd_rn(r, -s))};
+}
+
+// The value in units of 2^-46, as upper (2^-23) and lower part.
+__device__ __forceinline__ void units(Rest x, uint32_t &hi, int &lo) {
+  const float t = __fadd_rn(x.r, 1.0f);
+  hi = __float_as_uint(t) - 0x3F800000u;
+  const float rest = __fadd_rn(__fadd_rn(x.r, -__fadd_rn(t, -1.0f)), x.e);
+  constexpr float M = 1.5f / 8388608.0f;                 // 1.5 * 2^-23: neighbours are 2^-46 apart
+  lo = (int)(__float_as_uint(__fadd_rn(rest, M)) - __float_as_uint(M));
+}
+__device__ __forceinline__ int64_t to_units(Rest x) {
+  uint32_t hi;
+  int lo;
+  units(x, hi, lo);
+  return ((int64_t)hi << 23) + lo;
+}
+
+struct Walk {               // shared by the block
+  int tok[NODES], par[NODES], path[NODES];
+  float p[NODES], q[NODES], u[NODES];                    // at each draft, in its parent's rows
+  Factor z[NODES];                                       // of the refusals at the node so far
+  int refused[NODES];                                    // those drafts
+  int64_t warp_sum[WARPS];
+  int64_t block_sum[2][MAX_BLOCKS];
+  int node, kept, refusals, more;                        // where the walk is; whether it goes on after the sum
+  double Z;
+};
+
+// R of token v at the walk's node.
+template <bool F32, bool Q>
+__device__ __forceinline__ Rest rest_of(const Walk &w, const char *prow, const char *qrow, long v, int refusals) {
+  const float p = prob<F32>(prow, v);
+  if (!Q || refusals == 0) return Rest{p, 0.0f};
+  const float q = prob<F32>(qrow, v);
+  Rest x = first_rest(p, q);
+  for (int i = 1; i < refusals; ++i) x = next_rest(x, q, w.z[i]);
+  return x;
+}
+
+template <bool F32, bool Q>
+__global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int blocks) {
+  __shared__ Walk w;
+  cg::cluster_group cluster = cg::this_cluster();
+  pdl_enter();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / blocks, part = blockIdx.x - b * blocks;
+  const int n = a.n_new ? min(max(a.n_new[b], 0), a.nodes) : a.nodes;
+  const int es = F32 ? 4 : 2;
+  const char *pb = a.p.p + b * a.p.sb * es, *qb = Q ? a.q.p + b * a.q.sb * es : nullptr;
+  auto prow = [&](int i) { return pb + i * a.p.st * es; };
+  auto qrow = [&](int i) { return qb + i * a.q.st * es; };
+
+  // the drafts
+  const int words = (a.nodes + 31) >> 5;
+  for (int i = tid; i < n; i += THREADS) {
+    const int y = a.tokens[(long)b * a.nodes + i];
+    const bool known = y >= 0 && y < a.vocab;
+    int par = i - 1;
+    if (a.mask && i > 0) {
+      const uint32_t *row = a.mask + ((long)b * a.nodes + i) * words;
+      par = -1;
+      for (int k = i >> 5; k >= 0 && par < 0; --k) {
+        uint32_t m = row[k];
+        if (k == i >> 5) m &= (1u << (i & 31)) - 1;
+        if (m) par = k * 32 + 31 - __clz(m);
+      }
+    }
+    w.tok[i] = known ? y : -1;
+    w.par[i] = par;
+    w.u[i] = a.u[(long)b * a.nodes + i];
+    w.p[i] = i > 0 && par >= 0 && known ? prob<F32>(prow(par), y) : 0.0f;
+    w.q[i] = !Q ? 1.0f : i > 0 && par >= 0 && known ? prob<F32>(qrow(par), y) : 0.0f;
+  }
+  if (tid == 0) w.node = 0, w.kept = 1, w.refusals = 0, w.Z = 1.0, w.path[0] = 0;
+  __syncthreads();
+
+  // this block's and warp's tokens
+  const int per_block = (a.vocab + blocks - 1) / blocks, v0 = min(part * per_block, a.vocab), v1 = min(v0 + per_block, a.vocab);
+  const int per_warp = ((v1 - v0 + WARPS - 1) / WARPS + 31) / 32 * 32, lo = min(v0 + warp * per_warp, v1), hi = min(lo + per_warp, v1);
+  int turn = 0;
+  int64_t total = 0;
+  bool whole = false;                                    // nothing was left: the node's own row counts
+  int tried = 0;                                         // drafts up to this one are settled (warp 0)
+  while (n > 0) {
+    // ---- walk until a sum is wanted: that of a refused draft with others behind it (more), or the next token's
+    if (warp == 0 && !whole) {
+      int node = w.node, refusals = w.refusals, kept = w.kept;
+      double Z = w.Z;
+      auto next_draft = [&]() {                          // of the node; n where there is none
+        for (int k = tried / 32 * 32; k < n; k += 32) {
+          const int j = k + lane;
+          const unsigned m = __ballot_sync(0xffffffffu, j > tried && j < n && w.par[j] == node);
+          if (m) return k + __ffs(m) - 1;
+        }
+        return n;
+      };
+      int i = next_draft();
+      bool more = false;
+      while (i < n && !more) {
+        tried = i;
+        const int y = w.tok[i];
+        const double q = w.q[i];
+        double R = w.p[i];                               // what the refusals before left of y
+        if (Q) {
+          for (int k = 0; k < refusals; ++k) R = fmax(R - q * ((double)w.z[k].hi + (double)w.z[k].lo), 0.0);
+        } else {
+          for (int k = 0; k < refusals; ++k)
+            if (w.refused[k] == y) R = 0.0;
+        }
+        const bool keep = y >= 0 && (double)w.u[i] * q * Z < R, refuse = y >= 0 && !keep;
+        __syncwarp();
+        if (lane == 0) {
+          if (keep) w.path[kept] = i;
+          if (refuse) {
+            w.refused[refusals] = y;
+            w.z[refusals] = Factor{(float)Z, (float)(Z - (double)(float)Z)};
+          }
+        }
+        __syncwarp();
+        if (keep) node = i, refusals = 0, Z = 1.0, ++kept;
+        i = next_draft();
+        if (refuse) {
+          ++refusals;
+          if (Q) more = i < n;
+          else Z = fmax(Z - R, 0.0);
+        }
+      }
+      if (lane == 0) w.node = node, w.refusals = refusals, w.kept = kept, w.Z = Z, w.more = more;
+    }
+    __syncthreads();
+    // ---- the sum of R over the vocabulary
+    const int node = w.node, refusals = whole ? 0 : w.refusals;
+    const bool more = !whole && w.more;
+    const char *pr = prow(node), *qr = Q ? qrow(node) : nullptr;
+    int64_t sum = 0;
+    for (int v = lo + lane; v < hi; v += 32 * UNROLL) {
+      float p[UNROLL], q[UNROLL];
+#pragma unroll
+      for (int k = 0; k < UNROLL; ++k) {
+        p[k] = v + 32 * k < hi ? prob<F32>(pr, v + 32 * k) : 0.0f;
+        q[k] = Q && refusals > 0 && v + 32 * k < hi ? prob<F32>(qr, v + 32 * k) : 0.0f;
+      }
+      uint32_t up = 0;
+      int down = 0;
+#pragma unroll
+      for (int k = 0; k < UNROLL; ++k) {
+        Rest x{p[k], 0.0f};
+        if (Q && refusals > 0) {
+          x = first_rest(p[k], q[k]);
+          for (int i = 1; i < refusals; ++i) x = next_rest(x, q[k], w.z[i]);
+        }
+        uint32_t h;
+        int l;
+        units(x, h, l);
+        up += h, down += l;
+      }
+      sum += ((int64_t)up << 23) + down;
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (!Q && lane == 0)                                 // refused tokens count as zero (once each)
+      for (int i = 0; i < refusals; ++i) {
+        const int y = w.refused[i];
+        bool again = y < lo || y >= hi;
+        for (int k = 0; k < i && !again; ++k) again = w.refused[k] == y;
+        if (!again) sum -= to_units(Rest{prob<F32>(pr, y), 0.0f});
+      }
+    if (lane == 0) w.warp_sum[warp] = sum;
+    __syncthreads();
+    if (tid < blocks) {
+      int64_t s = 0;
+      for (int i = 0; i < WARPS; ++i) s += w.warp_sum[i];
+      *cluster.map_shared_rank(&w.block_sum[turn][part], tid) = s;
+    }
+    if (blocks > 1) cluster.sync();
+    else __syncthreads();
+    total = 0;
+    for (int i = 0; i < blocks; ++i) total += w.block_sum[turn][i];
+    turn ^= 1;
+    if (!more) {
+      if (total > 0 || refusals == 0) break;
+      whole = true;
+    } else if (tid == 0) {
+      w.Z = (double)total * (1.0 / 70368744177664.0);    // 2^-46
+    }
+    __syncthreads();
+  }
+
+  // ---- the token that the prefix passes u_0 of the sum at
+  if (n > 0 && total > 0) {
+    const int node = w.node, refusals = whole ? 0 : w.refusals;
+    const char *pr = prow(node), *qr = Q ? qrow(node) : nullptr;
+    const double x = fmin(fmax((double)w.u[0], 0.0) * (double)total, (double)(total - 1));
+    int64_t at = (int64_t)x;                             // the first prefix above it
+    const int64_t *sums = w.block_sum[turn ^ 1];
+    for (int i = 0; i < part; ++i) at -= sums[i];
+    if (at >= 0 && at < sums[part]) {
+      int64_t s = 0;
+      for (int i = 0; i < warp; ++i) s += w.warp_sum[i];
+      at -= s;
+      if (at >= 0 && at < w.warp_sum[warp]) {
+        const int per = (hi - lo + 31) / 32, l0 = min(lo + lane * per, hi), l1 = min(l0 + per, hi);
+        auto value = [&](int v) {
+          if (!Q)
+            for (int i = 0; i < refusals; ++i)
+              if (w.refused[i] == v) return (int64_t)0;
+          return to_units(rest_of<F32, Q>(w, pr, qr, v, refusals));
+        };
+        int64_t mine = 0;
+#pragma unroll 4
+        for (int v = l0; v < l1; ++v) mine += value(v);
+        int64_t before = mine;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, before, m);
+          if (lane >= m) before += y;
+        }
+        before -= mine;
+        if (at >= before && at < before + mine) {
+          int64_t c = before;
+          int v = l0;
+          while (true) {
+            c += value(v);
+            if (c > at) break;
+            ++v;
+          }
+          a.next[b] = v;
+        }
+      }
+    }
+  }
+  if (part == 0) {
+    for (int i = tid; i < a.nodes; i += THREADS) a.idx[(long)b * a.nodes + i] = n > 0 ? w.path[min(i, w.kept - 1)] : 0;
+    if (tid == 0) {
+      a.n_keep[b] = n > 0 ? w.kept : 0;
+      if (n == 0 || total <= 0) a.next[b] = -1;
+    }
+  }
+}
+
+template <bool F32, bool Q>
+cudaError_t launch(const VerifyArgs &a, int blocks, cudaStream_t s) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)(a.batch * blocks)), dim3(THREADS), 0, s, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)blocks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<F32, Q>, a, blocks);
+}
+
+}  // namespace verify
+}  // namespace pace
+
+cudaError_t pace_launch_verify(const VerifyArgs &a, cudaStream_t s) {
+  using namespace pace::verify;
+  // blocks a sequence: as many as two a multiprocessor hold, but no shorter stretches than 2048 tokens
+  int blocks = 1;
+  while (blocks < MAX_BLOCKS && a.batch * blocks * 2 <= 2 * pace::device_sm_count() && a.vocab / (blocks * 2) >= 2048) blocks *= 2;
+  if (a.io == PACE_IO_F32) return a.q.p ? launch<true, true>(a, blocks, s) : launch<true, false>(a, blocks, s);
+  return a.q.p ? launch<false, true>(a, blocks, s) : launch<false, false>(a, blocks, s);
+}

@@ -1,6 +1,6 @@
 """Attention layers of a hybrid model: rotary positions, the quantized paged KV cache and attention over it.
 
-Binding of include/pace_kv.h: the pace_* functions marshal tensors (shape, type, device and stride checks happen here, value
+Binding of include/pace_kv.h (and of pace_serve.h as far as it works on a cache): the pace_* functions marshal tensors (shape, type, device and stride checks happen here, value
 ranges in the library), PaceRope and PaceKV own the table and the cache region. Tensors are [batch, tokens, heads, d] views
 with d contiguous; lengths, page tables, masks and paths are contiguous int32 tensors; all of a call is on the current device.
 """
@@ -23,7 +23,7 @@ _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 __all__ = ["make_rope_config", "pace_rope_bytes", "pace_rope_table", "pace_rope_apply", "PaceRope", "make_kv_config",
            "pace_kv_bytes", "pace_kv_tile_bytes", "pace_kv_alloc", "pace_kv_free", "pace_kv_append", "pace_kv_read",
            "pace_kv_attend", "pace_kv_keep", "pace_kv_get_status", "PaceKV", "pace_kv_config", "pace_rope_config",
-           "PACE_KV_BAD_PAGE", "PACE_KV_BAD_POSITION", "PACE_KV_BAD_KEEP", "PACE_KV_TIMEOUT", "PACE_KV_MAX_BATCH",
+           "pace_kv_copy_pages", "pace_kv_pool", "PACE_KV_BAD_PAGE", "PACE_KV_BAD_POSITION", "PACE_KV_BAD_KEEP", "PACE_KV_TIMEOUT", "PACE_KV_MAX_BATCH",
            "PACE_KV_MAX_NEW"]
 
 
@@ -215,6 +215,20 @@ def pace_kv_get_status(handle, clear: bool = False, stream=None) -> int:
     return out.value
 
 
+def pace_kv_copy_pages(handle, src, dst, n=None, max_n=None, stream=None) -> None:
+    """Copies pages src[i] to dst[i] of a cache, i below the device count n [1] (None: all)."""
+    N = src.shape[0]
+    check(_fn("pace_kv_copy_pages")(handle, _ints(src, (N,), "src"), _ints(dst, (N,), "dst"), _ints(n, (1,), "n", True),
+                                    N if max_n is None else min(max_n, N), _stream(stream)))
+
+
+def pace_kv_pool(handle):
+    """Address of a cache's pages, and the bytes of one."""
+    at, size = C.c_void_p(), C.c_size_t()
+    check(lib().pace_kv_pool(handle, C.byref(at), C.byref(size)))
+    return at.value, size.value
+
+
 class PaceKV:
     """Owns a device region (a torch uint8 tensor) bound to a KV-cache handle.
 
@@ -242,6 +256,17 @@ class PaceKV:
 
     def keep(self, lens, table, idx, n_keep, stream=None):
         pace_kv_keep(self.handle, lens, table, idx, n_keep, self._on(stream))
+
+    def copy_pages(self, pages, stream=None):
+        """Carries out the moves of the last take or compact of `pages` (a PacePages)."""
+        pages._on(stream)
+        pace_kv_copy_pages(self.handle, pages.src, pages.dst, pages.n_moves, stream=self._on(stream))
+
+    def pages(self):
+        """The cache's pages as a uint8 view [n_pages, bytes of a page]."""
+        at, size = pace_kv_pool(self.handle)
+        off = at - self.mem.data_ptr()
+        return self.mem[off:off + self.cfg.n_pages * size].view(self.cfg.n_pages, size)
 
     def status(self, clear: bool = False, stream=None) -> int:
         return pace_kv_get_status(self.handle, clear, self._on(stream))
