@@ -19,7 +19,7 @@ SOURCES = ["pace_api.cu", "decode.cu", "decode_mma_s8.cu", "decode_mma_sm.cu", "
            "decode_bf16.cu", "prefill.cu", "prefill_tc.cu", "state_ops.cu",
            "kv_api.cu", "kv_cache.cu", "kv_attend.cu", "kv_attend_4.cu", "kv_attend_8.cu",
            "kv_attend_tc_4.cu", "kv_attend_tc_8.cu",
-           "serve_api.cu", "delta_step.cu", "verify.cu", "pages.cu"]
+           "serve_api.cu", "delta_step.cu", "delta_chunk_bf16.cu", "delta_chunk_f32.cu", "verify.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

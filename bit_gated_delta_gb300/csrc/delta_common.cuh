@@ -75,5 +75,7 @@ __device__ __forceinline__ int row_of(const DeltaArgs &p, int b, int t) { return
 }  // namespace delta
 }  // namespace pace
 
-// One call's launch (delta_step.cu chooses the kernel).
+// One call's launch (delta_step.cu chooses the kernel); the chunk kernels.
 cudaError_t pace_launch_delta(const DeltaArgs &p, cudaStream_t s);
+cudaError_t pace_launch_delta_chunk_bf16(const DeltaArgs &p, cudaStream_t s);
+cudaError_t pace_launch_delta_chunk_f32(const DeltaArgs &p, cudaStream_t s);

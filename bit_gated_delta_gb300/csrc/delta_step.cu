@@ -11,6 +11,7 @@ namespace delta {
 
 constexpr int STEP_THREADS = 256, STEP_WARPS = STEP_THREADS / 32;
 constexpr int STEP_STAGE = 8;            // tokens staged at a time
+constexpr int STEP_MOST = 8;             // longer calls, and trees, go by chunks (delta_chunk.cuh)
 
 __device__ __forceinline__ uint64_t pk(float a, float b) {
   uint64_t r;
@@ -79,16 +80,13 @@ __global__ void __launch_bounds__(STEP_THREADS) delta_step_kernel(const DeltaArg
 
   uint64_t S[R][2];
   float *state = p.S + ((long)s.slot * p.H + h) * D * D + (long)row0 * D + col;
-  auto load_state = [&]() {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (s.n > 0 && !s.fresh) x = *reinterpret_cast<const float4 *>(state + r * D);
-      S[r][0] = pk(x.x, x.y);
-      S[r][1] = pk(x.z, x.w);
-    }
-  };
-  load_state();
+  for (int r = 0; r < R; ++r) {
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (s.n > 0 && !s.fresh) x = *reinterpret_cast<const float4 *>(state + r * D);
+    S[r][0] = pk(x.x, x.y);
+    S[r][1] = pk(x.z, x.w);
+  }
 
   int turn = 0;
   // one token of the staged ones; `emit`: row of o that its output goes to (-1: none)
@@ -162,28 +160,12 @@ __global__ void __launch_bounds__(STEP_THREADS) delta_step_kernel(const DeltaArg
     if (tid == 160) sh.beta[i] = reinterpret_cast<const float *>(p.beta.p)[b * p.beta.sb + (long)row * p.beta.st + h * p.beta.sh];
   };
 
-  if (!p.mask) {
-    for (int t0 = 0; t0 < s.n; t0 += STEP_STAGE) {
-      const int m = min(STEP_STAGE, s.n - t0);
-      __syncthreads();
-      for (int i = 0; i < m; ++i) stage(i, t0 + i);
-      __syncthreads();
-      for (int i = 0; i < m; ++i) token(i, out ? t0 + i : -1);
-    }
-  } else {
-    // a tree: each token after its ancestors, from the slot's state
-    const int words = (p.n_tokens + 31) >> 5;
-    for (int t = 0; t < s.n; ++t) {
-      const uint32_t *row = p.mask + ((long)b * p.n_tokens + t) * words;
-      load_state();
-      for (int a = 0; a <= t; ++a) {
-        if (a < t && !((row[a >> 5] >> (a & 31)) & 1)) continue;
-        __syncthreads();
-        stage(0, a);
-        __syncthreads();
-        token(0, a == t ? t : -1);
-      }
-    }
+  for (int t0 = 0; t0 < s.n; t0 += STEP_STAGE) {
+    const int m = min(STEP_STAGE, s.n - t0);
+    __syncthreads();
+    for (int i = 0; i < m; ++i) stage(i, t0 + i);
+    __syncthreads();
+    for (int i = 0; i < m; ++i) token(i, out ? t0 + i : -1);
   }
   if (p.write && s.n > 0) {
 #pragma unroll
@@ -214,5 +196,7 @@ cudaError_t launch_step_t(const DeltaArgs &p, cudaStream_t s) {
 
 cudaError_t pace_launch_delta(const DeltaArgs &p, cudaStream_t s) {
   using namespace pace::delta;
+  const int most = p.idx ? (p.n_idx < p.n_tokens ? p.n_idx : p.n_tokens) : p.n_tokens;
+  if (p.mask || most > STEP_MOST) return p.io == PACE_IO_F32 ? pace_launch_delta_chunk_f32(p, s) : pace_launch_delta_chunk_bf16(p, s);
   return p.io == PACE_IO_F32 ? launch_step_t<true>(p, s) : launch_step_t<false>(p, s);
 }
