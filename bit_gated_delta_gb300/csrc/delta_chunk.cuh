@@ -17,9 +17,8 @@
 // of bf16 I/O enter as they are. bf16 I/O forms outputs from two parts (16 bits; o is rounded to 8). The state itself stays in fp32 registers
 // and takes D3 by an ordinary addition: the tensor cores' additions cut off, which would add up over a long prompt.
 //
-// Roles: eight warps own the columns (two a quarter of TMEM's lanes: token blocks of 16 in turn, halves of the state's rows), four copy a
-// chunk's rows in, form R, M, P and T one chunk ahead, one issues the products. T by halves: two 32 x 32 inverses (a thread a
-// column, right-looking, so that a token's chain is one multiply-add), then -T22 M21 T11.
+// Roles: eight warps own the columns (two a quarter of TMEM's lanes: token blocks of 16 in turn, halves of the state's rows), four form R, M, P
+// and T one chunk ahead, three copy rows in, one issues the products.
 // Every wait is bounded; one that gives up sets the status word, after which the block goes on without waiting or products and leaves the state.
 #pragma once
 
@@ -36,7 +35,7 @@ constexpr int C = 64;                                    // tokens a chunk
 
 template <int D, bool F32>
 struct Shape {
-  static constexpr int MAIN = 8, AUX = 4, W_MMA = MAIN + AUX, THREADS = (W_MMA + 1) * 32;
+  static constexpr int MAIN = 8, AUX = 4, W_MMA = MAIN + AUX, W_LOAD = W_MMA + 1, LOAD = 3, THREADS = (W_LOAD + LOAD) * 32;
   static constexpr int NX = F32 ? 3 : 1;                 // parts of q and k
   static constexpr int NO = F32 ? 3 : 2;                 // parts of u and P in the outputs
   static constexpr int NB = F32 ? 1 : 3;                 // chunks of rows in shared memory
@@ -44,10 +43,10 @@ struct Shape {
   static constexpr int XPART = 2 * ROWS, XBUF = NX * XPART;
   static constexpr int VBUF = C * D * (F32 ? 4 : 2);
   static constexpr int TPART = C * C * 2;
-  static constexpr int LD = C + 4;                       // row of the fp32 tables
+  static constexpr int LD = C + 4, LY = 36;              // rows of the fp32 tables
   static constexpr int OX = 0, OV = OX + NB * XBUF, OT = OV + NB * VBUF, OP = OT + 3 * TPART, OM = OP + NO * TPART,
-                       OTF = OM + C * LD * 4, OY = OTF + C * LD * 4, OG = OY + 32 * 36 * 4, OBAR = OG + 3 * 4 * C * 4,
-                       NBAR = 3 * NB + 3 + 14, OMISC = OBAR + NBAR * 8, SMEM = OMISC + 16;
+                       OTF = OM + C * LD * 4, OY = OTF + C * LD * 4, OG = OY + 32 * LY * 4, OBAR = OG + 3 * 4 * C * 4,
+                       NBAR = 2 * NB + 3 + 14, OMISC = OBAR + NBAR * 8, SMEM = OMISC + 16;
   static_assert(SMEM <= 227 * 1024 && OBAR % 8 == 0, "shared memory");
   // TMEM columns: parts of S, later of R_C u; rhs and u beside and over the parts whose products are done; w | p, later the state's
   // increment; u, later P u; dot products of the next chunk
@@ -63,16 +62,24 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
 }
-// Three bf16 parts of two values.
-__device__ __forceinline__ void split3(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-  hi = pack2(x, y);
-  x -= __uint_as_float(hi << 16), y -= __uint_as_float(hi & 0xFFFF0000u);
-  mid = pack2(x, y);
-  x -= __uint_as_float(mid << 16), y -= __uint_as_float(mid & 0xFFFF0000u);
-  lo = pack2(x, y);
+__device__ __forceinline__ void less(float &x, float &y, uint32_t part) {        // (both differences in one instruction)
+  uint64_t d;
+  asm("{\n\t.reg .b64 a, b, m;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tmov.b64 m, {%5, %5};\n\tfma.rn.f32x2 %0, b, m, a;\n\t}"
+      : "=l"(d)
+      : "f"(x), "f"(y), "r"(part << 16), "r"(part & 0xFFFF0000u), "f"(-1.0f));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d));
 }
-__device__ __forceinline__ void cp16(void *dst, const void *src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+// NP bf16 parts of two values.
+template <int NP>
+__device__ __forceinline__ void split(float x, float y, uint32_t *part, int stride) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    part[i * stride] = pack2(x, y);
+    if (i + 1 < NP) less(x, y, part[i * stride]);
+  }
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes) {      // (0: writes zeros)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void aux_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __host__ __device__ constexpr uint32_t idesc(int N, int mn_major) {   // M = 128, bf16, fp32 sums
@@ -82,10 +89,20 @@ __device__ __forceinline__ uint32_t idesc_n(int N) { return idesc(0, 0) | ((uint
 
 constexpr uint64_t WAIT_NS = 1000000000ull;
 
+// y += m x for a pair of rows.
+__device__ __forceinline__ void fma_pair(uint64_t &y, uint64_t m, float x) {
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%2, %2};\n\tfma.rn.f32x2 %0, %1, v, %0;\n\t}" : "+l"(y) : "l"(m), "f"(x));
+}
+__device__ __forceinline__ float2 pair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+
 template <int D, bool F32>
 __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(const DeltaArgs p) {
   using Z = Shape<D, F32>;
-  constexpr int NX = Z::NX, NO = Z::NO, NB = Z::NB, LD = Z::LD, ES = F32 ? 4 : 2;
+  constexpr int NX = Z::NX, NO = Z::NO, NB = Z::NB, LD = Z::LD, LY = Z::LY, ES = F32 ? 4 : 2;
   extern __shared__ __align__(128) char smem[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + Z::OBAR);
   uint64_t *x_full = bar, *x_free = x_full + NB, *gates = x_free + NB, *a1 = gates + 3, *a2 = a1 + 1, *a3 = a2 + 1, *a4 = a3 + 1, *w_done = a4 + 1,
@@ -103,7 +120,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < NB; ++i) mbar_init(&x_full[i], Z::AUX), mbar_init(&x_free[i], 1);
+    for (int i = 0; i < NB; ++i) mbar_init(&x_full[i], Z::LOAD), mbar_init(&x_free[i], 1);
     for (int i = 0; i < 3; ++i) mbar_init(&gates[i], Z::AUX);
     for (uint64_t *x : {a1, a2, a3, a4}) mbar_init(x, Z::MAIN);
     for (uint64_t *x : {w_done, p_done, u_done, s_done, o_done, g_done, drain}) mbar_init(x, 1);
@@ -120,7 +137,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
   fence_after_sync();
   const Seq s = *seq_slot;
   const int n = s.n, chunks = (n + C - 1) / C;
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;          // the whole of TMEM is this block's: its first column (a constant keeps addresses uniform)
   float *state = p.S + ((long)s.slot * p.H + h) * D * D;
   // tokens of a chunk, and as the products count them
   auto tokens = [&](int c) { return min(C, n - c * C); };
@@ -128,8 +145,9 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
 
   bool good = true;
   auto wait = [&](uint64_t *x, int phase) {              // (the whole warp)
-    if (good && !mbar_wait(x, phase & 1, WAIT_NS)) good = false;
-    good = __all_sync(0xffffffffu, good);
+    if (!good) return;
+    if (__all_sync(0xffffffffu, mbar_try_wait(x, phase & 1))) return;
+    good = __all_sync(0xffffffffu, mbar_wait(x, phase & 1, WAIT_NS));
   };
   auto arrive = [&](uint64_t *x) {
     __syncwarp();
@@ -151,7 +169,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         for (int i = 0; i < HALF; i += 16) {
           uint32_t x[3][8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) split3(S[i + 2 * e], S[i + 2 * e + 1], x[0][e], x[1][e], x[2][e]);
+          for (int e = 0; e < 8; ++e) split<3>(S[i + 2 * e], S[i + 2 * e + 1], &x[0][e], 8);
 #pragma unroll
           for (int k = 0; k < 3; ++k) tmem_st8(tl + Z::A1 + k * (D / 2) + grp * (HALF / 2) + i / 2, x[k]);
         }
@@ -163,7 +181,9 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     if (chunks) publish();
     for (int c = 0; c < chunks; ++c) {
       const int nt = tokens(c), np = padded(c), buf = c % NB;
-      const float *ga = reinterpret_cast<const float *>(smem + Z::OG) + (c % 3) * 4 * C, *beta = ga + C, *G = ga + 2 * C, *rho = ga + 3 * C;
+      const float *ga = reinterpret_cast<const float *>(smem + Z::OG) + (c % 3) * 4 * C;
+      const float4 *beta = reinterpret_cast<const float4 *>(ga + C), *G = reinterpret_cast<const float4 *>(ga + 2 * C),
+                   *rho = reinterpret_cast<const float4 *>(ga + 3 * C);
       const char *vrow = smem + Z::OV + buf * Z::VBUF + j * ES;
       // ---- rhs = beta (v - G w)
       wait(&gates[c % 3], c / 3);
@@ -178,16 +198,21 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
           if (t0 < np) {
             uint32_t w[16], x[3][8];
             tmem_ld16(tl + Z::D1 + t0, w);
+            float v[16];
+            const char *at = vrow + t0 * D * ES;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              v[e] = F32 ? *reinterpret_cast<const float *>(at + e * D * ES)
+                         : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at + e * D * ES) << 16);
             tmem_wait_ld();
-            float y[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const char *at = vrow + (t0 + e) * D * ES;
-              const float v = F32 ? *reinterpret_cast<const float *>(at) : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at) << 16);
-              y[e] = beta[t0 + e] * fmaf(-G[t0 + e], __uint_as_float(w[e]), v);
+            for (int e = 0; e < 16; e += 4) {
+              const float4 g = G[(t0 + e) / 4], be = beta[(t0 + e) / 4];
+              const float y0 = be.x * fmaf(-g.x, __uint_as_float(w[e]), v[e]), y1 = be.y * fmaf(-g.y, __uint_as_float(w[e + 1]), v[e + 1]);
+              const float y2 = be.z * fmaf(-g.z, __uint_as_float(w[e + 2]), v[e + 2]), y3 = be.w * fmaf(-g.w, __uint_as_float(w[e + 3]), v[e + 3]);
+              split<3>(y0, y1, &x[0][e / 2], 8);
+              split<3>(y2, y3, &x[0][e / 2 + 1], 8);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) split3(y[2 * e], y[2 * e + 1], x[0][e], x[1][e], x[2][e]);
 #pragma unroll
             for (int k = 0; k < 3; ++k) tmem_st8(tl + Z::A2 + k * (C / 2) + t0 / 2, x[k]);
           }
@@ -210,15 +235,19 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
               tmem_ld16(tl + Z::D1 + C + t0, x);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) y[r][e] = G[t0 + e] * __uint_as_float(x[e]);
+              for (int e = 0; e < 16; e += 4) {
+                const float4 g = G[(t0 + e) / 4];
+                y[r][e] = g.x * __uint_as_float(x[e]), y[r][e + 1] = g.y * __uint_as_float(x[e + 1]);
+                y[r][e + 2] = g.z * __uint_as_float(x[e + 2]), y[r][e + 3] = g.w * __uint_as_float(x[e + 3]);
+              }
             }
           }
         }
       }
+      const float gC = G[C / 4 - 1].w;
       // ---- u, decayed to the chunk's end, and as it is
       wait(u_done, c);
       fence_after_sync();
-      const float gC = G[C - 1];
       if (p.write) {
         if (on) {
 #pragma unroll
@@ -229,8 +258,11 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
               tmem_ld16(tl + Z::D2 + t0, u);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                split3(rho[t0 + 2 * e] * __uint_as_float(u[2 * e]), rho[t0 + 2 * e + 1] * __uint_as_float(u[2 * e + 1]), x[0][e], x[1][e], x[2][e]);
+              for (int e = 0; e < 16; e += 4) {
+                const float4 g = rho[(t0 + e) / 4];
+                split<3>(g.x * __uint_as_float(u[e]), g.y * __uint_as_float(u[e + 1]), &x[0][e / 2], 8);
+                split<3>(g.z * __uint_as_float(u[e + 2]), g.w * __uint_as_float(u[e + 3]), &x[0][e / 2 + 1], 8);
+              }
 #pragma unroll
               for (int k = 0; k < 3; ++k) tmem_st8(tl + Z::A3 + k * (C / 2) + t0 / 2, x[k]);
             }
@@ -246,11 +278,11 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
           for (int r = 0; r < 2; ++r) {
             const int t0 = 16 * (grp + 2 * r);
             if (t0 < np) {
-              uint32_t u[16], x[3][8];
+              uint32_t u[16], x[NO][8];
               tmem_ld16(tl + Z::D2 + t0, u);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) split3(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]), x[0][e], x[1][e], x[2][e]);
+              for (int e = 0; e < 8; ++e) split<NO>(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]), &x[0][e], 8);
 #pragma unroll
               for (int k = 0; k < NO; ++k) tmem_st8(tl + Z::A4 + k * (C / 2) + t0 / 2, x[k]);
             }
@@ -284,6 +316,8 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         wait(o_done, c);
         fence_after_sync();
         if (on) {
+          const long st = p.o.st * ES;
+          char *row = p.o.p + (b * p.o.sb + (long)(c * C) * p.o.st + h * p.o.sh + j) * ES;
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const int t0 = 16 * (grp + 2 * r);
@@ -291,14 +325,20 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
               uint32_t x[16];
               tmem_ld16(tl + Z::D4 + t0, x);
               tmem_wait_ld();
-              char *at = p.o.p + (b * p.o.sb + (long)(c * C + t0) * p.o.st + h * p.o.sh + j) * ES;
-#pragma unroll
-              for (int e = 0; e < 16; ++e, at += p.o.st * ES) {
+              char *at = row + t0 * st;
+              auto put = [&](int e) {
                 const float o = y[r][e] + __uint_as_float(x[e]);
-                if (t0 + e < nt) {
-                  if (F32) *reinterpret_cast<float *>(at) = o;
-                  else *reinterpret_cast<__nv_bfloat16 *>(at) = __float2bfloat16_rn(o);
-                }
+                if (F32) *reinterpret_cast<float *>(at) = o;
+                else *reinterpret_cast<__nv_bfloat16 *>(at) = __float2bfloat16_rn(o);
+                at += st;
+              };
+              if (t0 + 16 <= nt) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) put(e);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (t0 + e < nt) put(e);
               }
             }
           }
@@ -316,169 +356,168 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         *reinterpret_cast<uint4 *>(p.o.p + (b * p.o.sb + (n + i / PIECES) * p.o.st + h * p.o.sh) * ES + i % PIECES * 16) = make_uint4(0, 0, 0, 0);
     }
   } else if (warp < Z::W_MMA) {
-    // ---------------------------------------------------------------- rows and tables of the chunks
+    // ---------------------------------------------------------------- tables of the chunks
     const int at = tid - Z::MAIN * 32, aw = warp - Z::MAIN, t = at & 63;
-    const bool isq = at >= 64;
+    const bool isq = at >= 64;                           // rows of k (M, T), then of q (P)
     float *M = reinterpret_cast<float *>(smem + Z::OM), *Tf = reinterpret_cast<float *>(smem + Z::OTF), *Y = reinterpret_cast<float *>(smem + Z::OY);
     const int words = (p.n_tokens + 31) >> 5;
-    float a_next = 1.0f, b_next = 0.0f;                  // gates of the chunk being loaded (threads 0..63)
-    auto row_at = [&](const KvTensor &x, int row, int head) { return x.p + (b * x.sb + (long)row * x.st + head * x.sh) * ES; };
-    auto load = [&](int c) {
-      const int nt = tokens(c);
-      char *X = smem + Z::OX + (c % NB) * Z::XBUF, *V = smem + Z::OV + (c % NB) * Z::VBUF;
-      // q and k: eight lanes write one core of 8 rows
-#pragma unroll
-      for (int it = 0; it < 2 * (D / 32) * 2; ++it) {
-        const int unit = it * 4 + aw, block = unit / (D / 32), k = (unit % (D / 32)) * 32 + (lane >> 3) * 8;    // blocks 0..7: k, 8..15: q
-        const int r = (block & 7) * 8 + (lane & 7);
-        const bool q = block >= 8, live = r < nt;
-        if (q && !out) continue;
-        const KvTensor &src = q ? p.q : p.k;
-        const char *from = live ? row_at(src, row_of(p, b, c * C + r), hk) + k * ES : src.p;
-        char *to = X + (q ? Z::ROWS : 0) + core_at(r, k, D);
-        if (!F32) {
-          cp16(to, from, live);
-        } else {
-          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
-          if (live) x = reinterpret_cast<const float4 *>(from)[0], y = reinterpret_cast<const float4 *>(from)[1];
-          uint32_t w[3][4];
-          split3(x.x, x.y, w[0][0], w[1][0], w[2][0]);
-          split3(x.z, x.w, w[0][1], w[1][1], w[2][1]);
-          split3(y.x, y.y, w[0][2], w[1][2], w[2][2]);
-          split3(y.z, y.w, w[0][3], w[1][3], w[2][3]);
-#pragma unroll
-          for (int i = 0; i < NX; ++i) *reinterpret_cast<uint4 *>(to + i * Z::XPART) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-        }
-      }
-      constexpr int PIECES = D * ES / 16;
-#pragma unroll
-      for (int it = 0; it < C * PIECES / 128; ++it) {
-        const int i = it * 128 + at, r = i / PIECES, piece = i % PIECES;
-        const bool live = r < nt;
-        cp16(V + r * D * ES + piece * 16, live ? row_at(p.v, row_of(p, b, c * C + r), h) + piece * 16 : p.v.p, live);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+    float a_next = 1.0f, b_next = 0.0f;                  // gates of the next chunk (threads 0..63)
+    auto fetch = [&](int c) {
       a_next = 1.0f, b_next = 0.0f;
-      if (!isq && t < nt) {
+      if (!isq && c < chunks && t < tokens(c)) {
         const long row = row_of(p, b, c * C + t);
         a_next = reinterpret_cast<const float *>(p.a.p)[b * p.a.sb + row * p.a.st + h * p.a.sh];
         b_next = reinterpret_cast<const float *>(p.beta.p)[b * p.beta.sb + row * p.beta.st + h * p.beta.sh];
       }
     };
-    for (int i = at; i < C * LD; i += 128) Tf[i] = 0.0f;
-    if (chunks && NB > 1) load(0);
+    for (int i = at; i < C * LD; i += 128) Tf[i] = 0.0f; // (the upper triangle stays so)
+    fetch(0);
     for (int c = 0; c < chunks; ++c) {
-      const int nt = tokens(c), np = padded(c), buf = c % NB;
-      if (NB == 1) {
-        if (c) wait(&x_free[0], c - 1);
-        load(c);
-      }
-      const float a = a_next, be = b_next;
-      if (NB > 1 && c + 1 < chunks) {
-        if (c + 1 >= NB) wait(&x_free[(c + 1) % NB], (c + 1) / NB - 1);
-        load(c + 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      } else {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-      }
-      fence_smem_to_async();
-      arrive(&x_full[buf]);
-      // ---- decays
+      const int nt = tokens(c), np = padded(c);
+      // ---- decays: a row of R, from its end
       float *ga = reinterpret_cast<float *>(smem + Z::OG) + (c % 3) * 4 * C, *beta = ga + C, *G = ga + 2 * C, *rho = ga + 3 * C;
-      if (!isq) ga[t] = a, beta[t] = be;
-      uint64_t see = ~0ull;                              // ancestors
+      if (!isq) ga[t] = a_next, beta[t] = b_next;
+      fetch(c + 1);
+      uint32_t see[2] = {~0u, ~0u};                      // the token and its ancestors
       if (p.mask) {
-        see = 0;
+        see[0] = see[1] = 0;
         if (t < nt) {
           const uint32_t *row = p.mask + ((long)b * p.n_tokens + t) * words;
-          see = row[0] | (words > 1 ? (uint64_t)row[1] << 32 : 0);
+          see[0] = row[0];
+          if (words > 1) see[1] = row[1];
         }
       }
+      if (t < 32) see[0] = (see[0] | 1u << t) & (2u << t) - 1, see[1] = 0;
+      else see[1] = (see[1] | 1u << (t - 32)) & (2u << (t - 32)) - 1;
       aux_sync();
       float R[C];
-      float r = 1.0f;
+      float r = isq ? 1.0f : beta[t];                    // (rows of M carry beta)
 #pragma unroll
-      for (int i = C - 1; i >= 0; --i) {
-        const bool anc = i == t || (i < t && ((see >> i) & 1));
-        R[i] = anc ? r : 0.0f;
-        if (anc) r *= ga[i];
+      for (int i = C - 4; i >= 0; i -= 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(ga + i);
+        const float as[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+          const bool anc = see[(i + e) >> 5] & (1u << ((i + e) & 31));
+          R[i + e] = anc ? r : 0.0f;
+          r *= anc ? as[e] : 1.0f;
+        }
       }
-      if (!isq) G[t] = r;
-      if (at == C - 1) {
+      if (isq) G[t] = r;
+      if (at == 2 * C - 1) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) rho[i] = R[i];
+        for (int i = 0; i < C; i += 4) *reinterpret_cast<float4 *>(rho + i) = make_float4(R[i], R[i + 1], R[i + 2], R[i + 3]);
       }
       arrive(&gates[c % 3]);
-      // ---- M (kept by columns) and P
+      // ---- M, a column's entries in a row (entries on and above the diagonal are not read, or are zeros), and P
       wait(g_done, c);
       fence_after_sync();
       const uint32_t tl = tmem + ((uint32_t)(aw * 32) << 16) + Z::D0;
-      const float scale = isq ? 1.0f : beta[t];
 #pragma unroll
       for (int i0 = 0; i0 < C; i0 += 16) {
+        uint32_t x[16];
         if (i0 < np) {
-          uint32_t x[16];
           tmem_ld16(tl + i0, x);
           tmem_wait_ld();
+        } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int i = i0 + e;
-            R[i] *= scale * __uint_as_float(x[e]);
-            if (!isq) M[i * LD + t] = i < t ? R[i] : 0.0f;
-          }
+          for (int e = 0; e < 16; ++e) x[e] = 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) R[i0 + e] *= __uint_as_float(x[e]);
+        if (!isq) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) M[(i0 + e) * LD + t] = R[i0 + e];
         }
       }
       fence_before_sync();
       aux_sync();
-      // ---- T = (I + M)^-1
-      if (aw < 2 && aw * 32 < np) {
-        const float *m = M + aw * 32 * LD + aw * 32;
-        float x[32];
+      // ---- T = (I + M)^-1: blocks of 16 on the diagonal (a lane a column, the column's later entries brought up to date as each is known);
+      // then twice the block below two inverses, -T_b M_ba T_a. T_b is read by columns: it takes M's place.
+      {
+        const int o16 = 16 * aw, col = lane & 15;
+        const float *m = M + o16 * LD + o16;
+        float x[16];
+        float4 row[4], next[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = i == lane ? 1.0f : 0.0f;
+        for (int k = 0; k < 4; ++k) next[k] = *reinterpret_cast<const float4 *>(m + 4 * k);
 #pragma unroll
-        for (int i = 0; i < 31; ++i)
+        for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.0f : 0.0f;
 #pragma unroll
-          for (int k = (i + 1) & ~3; k < 32; k += 4) {
-            const float4 y = *reinterpret_cast<const float4 *>(m + i * LD + k);
-            if (k > i) x[k] = fmaf(-y.x, x[i], x[k]);
-            if (k + 1 > i) x[k + 1] = fmaf(-y.y, x[i], x[k + 1]);
-            if (k + 2 > i) x[k + 2] = fmaf(-y.z, x[i], x[k + 2]);
-            if (k + 3 > i) x[k + 3] = fmaf(-y.w, x[i], x[k + 3]);
+        for (int i = 0; i < 15; ++i) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            row[k] = next[k];
+            if (i < 14 && 4 * k + 3 > i + 1) next[k] = *reinterpret_cast<const float4 *>(m + (i + 1) * LD + 4 * k);
           }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) Tf[(aw * 32 + i) * LD + aw * 32 + lane] = x[i];
+          for (int k = 0; k < 4; ++k) {
+            if (4 * k > i) x[4 * k] = fmaf(-row[k].x, x[i], x[4 * k]);
+            if (4 * k + 1 > i) x[4 * k + 1] = fmaf(-row[k].y, x[i], x[4 * k + 1]);
+            if (4 * k + 2 > i) x[4 * k + 2] = fmaf(-row[k].z, x[i], x[4 * k + 2]);
+            if (4 * k + 3 > i) x[4 * k + 3] = fmaf(-row[k].w, x[i], x[4 * k + 3]);
+          }
+        }
+        __syncwarp();
+        if (lane < 16) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) Tf[(o16 + i) * LD + o16 + col] = x[i];
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4 *>(M + (o16 + col) * LD + o16 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        }
       }
       aux_sync();
-      if (np > 32) {
-        float y[8];
+      // rows 4 q .. of a 16 x 16 or 8 q .. of a 32 x 32 block: sum_s first(s, rows) second(s), over pairs of rows
+      if (np > 16) {
+        const int oa = (aw >> 1) * 32, ob = oa + 16, col = lane & 15, q = 4 * ((aw & 1) * 2 + (lane >> 4));
+        float *y = Y + (aw >> 1) * 16 * LY;
+        uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < 32; ++i) {
-          const float x = Tf[i * LD + lane];
-          const float4 m0 = *reinterpret_cast<const float4 *>(M + i * LD + 32 + 8 * aw), m1 = *reinterpret_cast<const float4 *>(M + i * LD + 36 + 8 * aw);
-          y[0] = fmaf(m0.x, x, y[0]), y[1] = fmaf(m0.y, x, y[1]), y[2] = fmaf(m0.z, x, y[2]), y[3] = fmaf(m0.w, x, y[3]);
-          y[4] = fmaf(m1.x, x, y[4]), y[5] = fmaf(m1.y, x, y[5]), y[6] = fmaf(m1.z, x, y[6]), y[7] = fmaf(m1.w, x, y[7]);
+        for (int i = 0; i < 16; ++i) {
+          const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(M + (oa + i) * LD + ob + q);
+          const float x = Tf[(oa + i) * LD + oa + col];
+          fma_pair(s0, m.x, x), fma_pair(s1, m.y, x);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) Y[(8 * aw + i) * 36 + lane] = y[i];
+        float2 v0 = pair(s0), v1 = pair(s1);
+        y[q * LY + col] = -v0.x, y[(q + 1) * LY + col] = -v0.y, y[(q + 2) * LY + col] = -v1.x, y[(q + 3) * LY + col] = -v1.y;
         aux_sync();
+        s0 = s1 = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-#pragma unroll 2
-        for (int k = 0; k < 32; k += 4) {
-          float x[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = Y[(k + e) * 36 + lane];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 m = *reinterpret_cast<const float4 *>(Tf + (32 + 8 * aw + i) * LD + 32 + k);
-            y[i] = fmaf(-m.x, x[0], y[i]), y[i] = fmaf(-m.y, x[1], y[i]), y[i] = fmaf(-m.z, x[2], y[i]), y[i] = fmaf(-m.w, x[3], y[i]);
-          }
+        for (int i = 0; i < 16; ++i) {
+          const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(M + (ob + i) * LD + ob + q);
+          const float x = y[i * LY + col];
+          fma_pair(s0, m.x, x), fma_pair(s1, m.y, x);
         }
+        v0 = pair(s0), v1 = pair(s1);
+        float *to = Tf + (ob + q) * LD + oa + col;
+        to[0] = v0.x, to[LD] = v0.y, to[2 * LD] = v1.x, to[3 * LD] = v1.y;
+        *reinterpret_cast<float4 *>(M + (oa + col) * LD + ob + q) = make_float4(v0.x, v0.y, v1.x, v1.y);
+        aux_sync();
+      }
+      if (np > 32) {
+        const int q = 8 * aw;
+        uint64_t s[4] = {0, 0, 0, 0};
+        auto add = [&](const float *m, float x) {
+          const ulonglong2 m0 = *reinterpret_cast<const ulonglong2 *>(m), m1 = *reinterpret_cast<const ulonglong2 *>(m + 4);
+          fma_pair(s[0], m0.x, x), fma_pair(s[1], m0.y, x), fma_pair(s[2], m1.x, x), fma_pair(s[3], m1.y, x);
+        };
+#pragma unroll 16
+        for (int i = 0; i < 32; ++i) add(M + i * LD + 32 + q, Tf[i * LD + lane]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) Tf[(32 + 8 * aw + i) * LD + lane] = y[i];
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = pair(s[i]);
+          Y[(q + 2 * i) * LY + lane] = -v.x, Y[(q + 2 * i + 1) * LY + lane] = -v.y;
+          s[i] = 0;
+        }
+        aux_sync();
+#pragma unroll 16
+        for (int i = 0; i < 32; ++i) add(M + (32 + i) * LD + 32 + q, Y[i * LY + lane]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = pair(s[i]);
+          Tf[(32 + q + 2 * i) * LD + lane] = v.x, Tf[(33 + q + 2 * i) * LD + lane] = v.y;
+        }
         aux_sync();
       }
       if (c) wait(u_done, c - 1);
@@ -487,10 +526,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         const int i = (at >> 6) * 32 + k;
         const float4 x = *reinterpret_cast<const float4 *>(Tf + t * LD + i), y = *reinterpret_cast<const float4 *>(Tf + t * LD + i + 4);
         uint32_t w[3][4];
-        split3(x.x, x.y, w[0][0], w[1][0], w[2][0]);
-        split3(x.z, x.w, w[0][1], w[1][1], w[2][1]);
-        split3(y.x, y.y, w[0][2], w[1][2], w[2][2]);
-        split3(y.z, y.w, w[0][3], w[1][3], w[2][3]);
+        split<3>(x.x, x.y, &w[0][0], 4), split<3>(x.z, x.w, &w[0][1], 4), split<3>(y.x, y.y, &w[0][2], 4), split<3>(y.z, y.w, &w[0][3], 4);
 #pragma unroll
         for (int e = 0; e < 3; ++e)
           *reinterpret_cast<uint4 *>(smem + Z::OT + e * Z::TPART + core_at(t, i, C)) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
@@ -502,9 +538,9 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         if (isq) {
 #pragma unroll
           for (int i = 0; i < C; i += 8) {
-            uint32_t w[3][4];
+            uint32_t w[NO][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split3(R[i + 2 * e], R[i + 2 * e + 1], w[0][e], w[1][e], w[2][e]);
+            for (int e = 0; e < 4; ++e) split<NO>(R[i + 2 * e], R[i + 2 * e + 1], &w[0][e], 4);
 #pragma unroll
             for (int e = 0; e < NO; ++e)
               *reinterpret_cast<uint4 *>(smem + Z::OP + e * Z::TPART + core_at(t, i, C)) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
@@ -514,42 +550,110 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         arrive(p_ready);
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else if (warp >= Z::W_LOAD) {
+    // ---------------------------------------------------------------- rows of the chunks: one warp k, one q, one v
+    const int what = warp - Z::W_LOAD;
+    const KvTensor &src = what == 0 ? p.k : what == 1 ? p.q : p.v;
+    const char *base = src.p + (b * src.sb + (what == 2 ? h : hk) * src.sh) * ES;
+    const long st = src.st * ES;
+    constexpr int PIECES = D * ES / 16, PER = 32 / PIECES > 0 ? 32 / PIECES : 1;   // of a row of v; rows a warp copies at once
+    auto load = [&](int c) {
+      const int nt = tokens(c);
+      if (what < 2) {
+        // eight lanes write one core of 8 rows
+        const int k = (lane >> 3) * 8;
+        const uint32_t to = smem_u32(smem) + Z::OX + (c % NB) * Z::XBUF + what * Z::ROWS + core_at(lane & 7, k, D);
+        const char *from = base + (long)(c * C + (lane & 7)) * st + k * ES;
+#pragma unroll
+        for (int r0 = 0; r0 < C; r0 += 8, from += 8 * st) {
+          const int r = r0 + (lane & 7);
+          const bool live = r < nt;
+          const char *at = from;
+          if (p.idx) at = base + (live ? row_of(p, b, c * C + r) : 0) * st + k * ES;
+          if (!live) at = src.p;
+#pragma unroll
+          for (int g = 0; g < D / 32; ++g) {
+            const uint32_t dst = to + core_at(r0, g * 32, D);
+            if (!F32) {
+              cp16(dst, at + (live ? g * 32 * ES : 0), live ? 16 : 0);
+            } else {
+              float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
+              if (live) x = reinterpret_cast<const float4 *>(at + g * 32 * ES)[0], y = reinterpret_cast<const float4 *>(at + g * 32 * ES)[1];
+              uint32_t w[3][4];
+              split<3>(x.x, x.y, &w[0][0], 4), split<3>(x.z, x.w, &w[0][1], 4), split<3>(y.x, y.y, &w[0][2], 4), split<3>(y.z, y.w, &w[0][3], 4);
+#pragma unroll
+              for (int i = 0; i < NX; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + i * Z::XPART), "r"(w[i][0]), "r"(w[i][1]), "r"(w[i][2]), "r"(w[i][3])
+                             : "memory");
+            }
+          }
+        }
+      } else {
+        const int piece = lane % PIECES, first = lane / PIECES;
+        const uint32_t to = smem_u32(smem) + Z::OV + (c % NB) * Z::VBUF + first * D * ES + piece * 16;
+        const char *from = base + (long)(c * C + first) * st + piece * 16;
+#pragma unroll 8
+        for (int r0 = 0; r0 < C; r0 += PER, from += PER * st) {
+          const int r = r0 + first;
+          const bool live = r < nt;
+          const char *at = from;
+          if (p.idx) at = base + (live ? row_of(p, b, c * C + r) : 0) * st + piece * 16;
+          cp16(to + r0 * D * ES, live ? at : src.p, live ? 16 : 0);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    static_assert(PIECES <= 32 && C % PER == 0, "v rows");
+    const bool any = what != 1 || out;
+    // a chunk's rows are announced behind the next one's copies
+    for (int c = 0; c < chunks + (NB > 1); ++c) {
+      if (c < chunks) {
+        if (c >= NB) wait(&x_free[c % NB], c / NB - 1);  // (also without rows to copy: an early arrival would count for the chunk before)
+        if (any) load(c);
+      }
+      if (NB > 1 && c < chunks) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fence_smem_to_async();
+      if (NB == 1) arrive(&x_full[0]);
+      else if (c > 0) arrive(&x_full[(c - 1) % NB]);
+    }
   } else {
-    // ---------------------------------------------------------------- products
+    // ---------------------------------------------------------------- products. The warp runs as one, so that descriptors stay in uniform
+    // registers; one lane issues.
     uint32_t leader;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(leader));
     const uint32_t base = smem_u32(smem);
     constexpr uint32_t SBO = (D / 8) * 128;
-    auto x_desc = [&](int c, int part, int q) { return smem_desc(base + Z::OX + (c % NB) * Z::XBUF + part * Z::XPART + q * Z::ROWS, 128, SBO); };
     // D (+)= A B^T summed over part pairs i + j <= MOST, smallest first; `one` issues a pair (the first of all clears D)
     auto pairs = [&](auto na, auto nb, auto most, auto one) {
-      bool first = true;
 #pragma unroll
       for (int sum = decltype(most)::value; sum >= 0; --sum)
 #pragma unroll
         for (int i = 0; i < decltype(na)::value; ++i) {
           const int k = sum - i;
           if (k < 0 || k >= decltype(nb)::value) continue;
-          one(i, k, first);
-          first = false;
+          const int top = decltype(most)::value, last = decltype(nb)::value - 1;
+          one(i, k, sum == (top < last + decltype(na)::value - 1 ? top : last + decltype(na)::value - 1) && (i == 0 || k == last));
         }
     };
-    using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
     using I3 = std::integral_constant<int, 3>;
     using INX = std::integral_constant<int, NX>;
     using INO = std::integral_constant<int, NO>;
+    using IMX = std::integral_constant<int, F32 ? 2 : 0>;
     using IMO = std::integral_constant<int, NO - 1>;
+    const uint64_t x_row = smem_desc(base + Z::OX, 128, SBO), x_col = smem_desc(base + Z::OX, SBO, 128);   // rows, and along their other dimension
+    const uint64_t t_row = smem_desc(base + Z::OT, 128, 1024), p_row = smem_desc(base + Z::OP, 128, 1024);
+    constexpr uint32_t XB = Z::XBUF >> 4, XP = Z::XPART >> 4, TP = Z::TPART >> 4;
     auto dots = [&](int c) {                             // [k | q] k^T
       wait(&x_full[c % NB], c / NB);
       fence_after_sync();
       if (leader && good) {
         const uint32_t id = idesc_n(padded(c));
-        pairs(INX{}, INX{}, I2{}, [&](int i, int k, bool first) {
+        const uint64_t x = x_row + (c % NB) * XB;
+        pairs(INX{}, INX{}, IMX{}, [&](int i, int k, bool first) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + Z::D0, x_desc(c, i, 0) + kk * 16, x_desc(c, k, 0) + kk * 16, id, first && kk == 0 ? 0u : 1u);
+          for (int kk = 0; kk < D / 16; ++kk) mma_ss(tmem + Z::D0, x + i * XP + kk * 16, x + k * XP + kk * 16, id, first && kk == 0 ? 0u : 1u);
         });
         commit(g_done);
       }
@@ -558,20 +662,20 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     for (int c = 0; c < chunks; ++c) {
       const int np = padded(c), steps = np / 16;
       const uint32_t id = idesc_n(np);
+      const uint64_t x = x_row + (c % NB) * XB;
       wait(a1, c);
       fence_after_sync();
       if (leader && good) {
         pairs(I3{}, INX{}, I2{}, [&](int i, int k, bool first) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ts(tmem + Z::D1, tmem + Z::A1 + i * (D / 2) + 8 * kk, x_desc(c, k, 0) + kk * 16, id, first && kk == 0 ? 0u : 1u);
+          for (int kk = 0; kk < D / 16; ++kk) mma_ts(tmem + Z::D1, tmem + Z::A1 + i * (D / 2) + 8 * kk, x + k * XP + kk * 16, id, first && kk == 0 ? 0u : 1u);
         });
         commit(w_done);
         if (out) {
           pairs(I3{}, INX{}, IMO{}, [&](int i, int k, bool first) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_ts(tmem + Z::D1 + C, tmem + Z::A1 + i * (D / 2) + 8 * kk, x_desc(c, k, 1) + kk * 16, id, first && kk == 0 ? 0u : 1u);
+              mma_ts(tmem + Z::D1 + C, tmem + Z::A1 + i * (D / 2) + 8 * kk, x + k * XP + (Z::ROWS >> 4) + kk * 16, id, first && kk == 0 ? 0u : 1u);
           });
           commit(p_done);
         }
@@ -582,9 +686,11 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       // (columns t of step kk's tokens s >= 16 kk begin at t = 16 kk)
       if (leader && good) {
         pairs(I3{}, I3{}, I2{}, [&](int i, int k, bool first) {
-          for (int kk = 0; kk < steps; ++kk)
-            mma_ts(tmem + Z::D2 + 16 * kk, tmem + Z::A2 + i * (C / 2) + 8 * kk,
-                   smem_desc(base + Z::OT + k * Z::TPART + kk * (2 * 1024 + 256), 128, 1024), idesc_n(np - 16 * kk), first && kk == 0 ? 0u : 1u);
+#pragma unroll
+          for (int kk = 0; kk < C / 16; ++kk)
+            if (kk < steps)
+              mma_ts(tmem + Z::D2 + 16 * kk, tmem + Z::A2 + i * (C / 2) + 8 * kk, t_row + k * TP + kk * ((2 * 1024 + 256) >> 4), id - kk * (2u << 17),
+                     first && kk == 0 ? 0u : 1u);
         });
         commit(u_done);
       }
@@ -593,10 +699,12 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         wait(a3, c);
         fence_after_sync();
         if (leader && good) {
+          const uint64_t xc = x_col + (c % NB) * XB;
           pairs(I3{}, INX{}, I2{}, [&](int i, int k, bool first) {
-            for (int kk = 0; kk < steps; ++kk)
-              mma_ts(tmem + Z::D3, tmem + Z::A3 + i * (C / 2) + 8 * kk,
-                     smem_desc(base + Z::OX + (c % NB) * Z::XBUF + k * Z::XPART + kk * 2 * SBO, SBO, 128), idesc(D, 1), first && kk == 0 ? 0u : 1u);
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk)
+              if (kk < steps)
+                mma_ts(tmem + Z::D3, tmem + Z::A3 + i * (C / 2) + 8 * kk, xc + k * XP + kk * (2 * SBO >> 4), idesc(D, 1), first && kk == 0 ? 0u : 1u);
           });
           commit(s_done);
           commit(&x_free[c % NB]);
@@ -608,9 +716,11 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         fence_after_sync();
         if (leader && good) {
           pairs(INO{}, INO{}, IMO{}, [&](int i, int k, bool first) {
-            for (int kk = 0; kk < steps; ++kk)
-              mma_ts(tmem + Z::D4 + 16 * kk, tmem + Z::A4 + i * (C / 2) + 8 * kk,
-                     smem_desc(base + Z::OP + k * Z::TPART + kk * (2 * 1024 + 256), 128, 1024), idesc_n(np - 16 * kk), first && kk == 0 ? 0u : 1u);
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk)
+              if (kk < steps)
+                mma_ts(tmem + Z::D4 + 16 * kk, tmem + Z::A4 + i * (C / 2) + 8 * kk, p_row + k * TP + kk * ((2 * 1024 + 256) >> 4), id - kk * (2u << 17),
+                       first && kk == 0 ? 0u : 1u);
           });
           commit(o_done);
         }
@@ -624,7 +734,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
   if (!good && lane == 0) atomicOr(p.status, PACE_DELTA_TIMEOUT);
   fence_before_sync();
   __syncthreads();
-  if (warp == Z::W_MMA) tmem_dealloc(tmem, 512);
+  if (warp == Z::W_MMA) tmem_dealloc(*tmem_slot, 512);
 }
 
 template <int D, bool F32>
