@@ -18,7 +18,7 @@
 // and takes D3 by an ordinary addition: the tensor cores' additions cut off, which would add up over a long prompt.
 //
 // Roles: sixteen warps own the columns (four a quarter of TMEM's lanes: a block of 16 tokens and a quarter of the state's rows each), four form
-// R, M, P and T one chunk ahead, three copy rows, one issues the products.
+// R, M and P, four T, one chunk ahead, three copy rows, one issues the products.
 // Every wait is bounded; one that gives up sets the status word, after which the block goes on without waiting or products and leaves the state.
 #pragma once
 
@@ -35,25 +35,27 @@ constexpr int C = 64;                                    // tokens a chunk
 
 template <int D, bool F32>
 struct Shape {
-  static constexpr int MAIN = 16, AUX = 4, W_MMA = MAIN + AUX, W_LOAD = W_MMA + 1, THREADS = (W_LOAD + 3) * 32;
+  static constexpr int MAIN = 16, AUX = 4, W_TAB = MAIN, W_INV = W_TAB + AUX, W_MMA = W_INV + AUX, W_LOAD = W_MMA + 1, THREADS = (W_LOAD + 3) * 32;
   static constexpr int NX = F32 ? 3 : 1;                 // parts of q and k
   static constexpr int NO = F32 ? 3 : 2;                 // parts of u and P in the outputs
-  static constexpr int NB = F32 ? 1 : 3;                 // chunks of rows in shared memory
+  static constexpr int NB = F32 ? 1 : 3, NV = F32 ? 1 : 2;   // chunks of rows of q and k, and of v, in shared memory
+  static constexpr int NM = F32 ? 1 : 2;                 // chunks of M
+  static constexpr int NS = F32 ? 3 : 2;                 // parts of the state in w and p
   static constexpr int HELD = D / 4;                     // rows of the state that a thread holds
   static constexpr int ROWS = C * D * 2;                 // one part of 64 rows
   static constexpr int XPART = 2 * ROWS, XBUF = NX * XPART;
   static constexpr int VBUF = C * D * (F32 ? 4 : 2);     // rows of v, later those of o
   static constexpr int TPART = C * C * 2;
   static constexpr int LD = C + 4, LY = 36;              // rows of the fp32 tables
-  static constexpr int OX = 0, OV = OX + NB * XBUF, OT = OV + NB * VBUF, OP = OT + 3 * TPART, OM = OP + 2 * NO * TPART, OY = OM + C * LD * 4,
-                       OG = OY + 32 * LY * 4, OBAR = OG + 3 * 4 * C * 4, NBAR = 3 * NB + 3 + 17, OMISC = OBAR + NBAR * 8, SMEM = OMISC + 16;
+  static constexpr int OX = 0, OV = OX + NB * XBUF, OT = OV + NV * VBUF, OP = OT + 3 * TPART, OM = OP + 2 * NO * TPART, OY = OM + NM * C * LD * 4,
+                       OG = OY + 32 * LY * 4, OBAR = OG + 3 * 4 * C * 4, NBAR = 2 * NB + NV + 2 * NM + 3 + 18, OMISC = OBAR + NBAR * 8, SMEM = OMISC + 16;
   static_assert(SMEM <= 227 * 1024 && OBAR % 8 == 0, "shared memory");
-  // TMEM columns. What lies over something else is written when the products that read that have ended: rhs over the state's third part, R_C u
-  // over its first part and rhs (whose halves are done as those of u are), the state's increment over its other parts, u over w.
-  static constexpr uint32_t W = 256, P = 320, D2 = 384, D4 = 384, D0 = 448, D3 = 64;
+  // TMEM columns. What lies over something else is written when the products that read that have ended: R_C u over rhs (whose halves are done as
+  // those of u are), the state's increment over its parts, u over w; with fp32 I/O rhs over the state's third part, and so q's products before rhs.
+  static constexpr uint32_t W = 256, P = 320, D2 = 384, D4 = 384, D0 = 448, D3 = F32 ? 64 : 0;
   __host__ __device__ static constexpr uint32_t a1(int part) { return 64 * part; }
   __host__ __device__ static constexpr uint32_t a2(int part) { return 128 + 32 * part; }
-  __host__ __device__ static constexpr uint32_t a3(int part) { return part < 2 ? 32 * part : 192; }
+  __host__ __device__ static constexpr uint32_t a3(int part) { return F32 && part < 2 ? 32 * part : 128 + 32 * part; }
   __host__ __device__ static constexpr uint32_t a4(int part) { return part < 2 ? W + 32 * part : 224; }
 };
 
@@ -85,7 +87,8 @@ __device__ __forceinline__ void split(float x, float y, uint32_t *part, int stri
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes) {      // (0: writes zeros)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void aux_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int ID>
+__device__ __forceinline__ void sync4() { asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory"); }      // four warps (1: tables, 2..5: columns, 6: inverses)
 __host__ __device__ constexpr uint32_t idesc(int N, int mn_major) {   // M = 128, bf16, fp32 sums
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)mn_major << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
@@ -108,13 +111,13 @@ __device__ __forceinline__ float2 pair(uint64_t v) {
 template <int D, bool F32>
 __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(const DeltaArgs p) {
   using Z = Shape<D, F32>;
-  constexpr int NX = Z::NX, NO = Z::NO, NB = Z::NB, LD = Z::LD, LY = Z::LY, ES = F32 ? 4 : 2;
+  constexpr int NX = Z::NX, NO = Z::NO, NB = Z::NB, NV = Z::NV, NM = Z::NM, NS = Z::NS, LD = Z::LD, LY = Z::LY, ES = F32 ? 4 : 2;
   extern __shared__ __align__(128) char smem[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + Z::OBAR);
   // (those of two: for the halves of a chunk's tokens)
-  uint64_t *x_full = bar, *x_free = x_full + NB, *o_free = x_free + NB, *ready = o_free + NB, *a1 = ready + 3, *a2 = a1 + 1, *a3 = a2 + 2, *a4 = a3 + 2,
+  uint64_t *x_full = bar, *x_free = x_full + NB, *o_free = x_free + NB, *m_ready = o_free + NV, *m_free = m_ready + NM, *ready = m_free + NM, *a1 = ready + 3, *a2 = a1 + 1, *a3 = a2 + 2, *a4 = a3 + 2,
            *u_done = a4 + 1, *w_done = u_done + 2, *p_done = w_done + 1, *s_done = p_done + 1, *o_done = s_done + 1, *o_read = o_done + 1,
-           *g_done = o_read + 1, *t_ready = g_done + 1, *drain = t_ready + 1;
+           *o_ready = o_read + 1, *g_done = o_ready + 1, *t_ready = g_done + 1, *drain = t_ready + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::OMISC);
   Seq *seq_slot = reinterpret_cast<Seq *>(tmem_slot + 1);
   static_assert(sizeof(Seq) <= 12, "kept beside the TMEM address");
@@ -127,9 +130,11 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < NB; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_free[i], 1), mbar_init(&o_free[i], 1);
+    for (int i = 0; i < NB; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_free[i], 1);
+    for (int i = 0; i < NV; ++i) mbar_init(&o_free[i], 1);
+    for (int i = 0; i < NM; ++i) mbar_init(&m_ready[i], Z::AUX), mbar_init(&m_free[i], Z::AUX);
     for (int i = 0; i < 3; ++i) mbar_init(&ready[i], Z::AUX + 1);
-    for (uint64_t *x : {a1, a4, o_read}) mbar_init(x, Z::MAIN);
+    for (uint64_t *x : {a1, a4, o_read, o_ready}) mbar_init(x, Z::MAIN);
     for (uint64_t *x : {a2, a2 + 1, a3, a3 + 1}) mbar_init(x, Z::MAIN / 2);
     for (uint64_t *x : {w_done, p_done, u_done, u_done + 1, s_done, o_done, g_done, drain}) mbar_init(x, 1);
     mbar_init(t_ready, Z::AUX);
@@ -152,10 +157,9 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
   auto padded = [&](int c) { return (tokens(c) + 15) & ~15; };
 
   bool good = true;
-  auto wait = [&](uint64_t *x, int phase) {              // (the whole warp)
-    if (!good) return;
-    if (__all_sync(0xffffffffu, mbar_try_wait(x, phase & 1))) return;
-    good = __all_sync(0xffffffffu, wait_long(x, phase & 1));
+  auto wait = [&](uint64_t *x, int phase) {              // (by the whole warp)
+    if (good && !mbar_try_wait(x, phase & 1)) good = wait_long(x, phase & 1);
+    __syncwarp();
   };
   auto arrive = [&](uint64_t *x) {
     __syncwarp();
@@ -173,6 +177,47 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     state += (long)(grp * HELD) * D + j;
 #pragma unroll
     for (int i = 0; i < HELD; ++i) S[i] = on && n > 0 && !s.fresh ? state[i * D] : 0.0f;
+    // outputs of a chunk: read when they are done, stored through its rows of v when u's products have been given their rhs
+    uint32_t held[F32 ? 16 : 8];
+    auto read_outputs = [&](int c) {
+      const float4 *Gb = reinterpret_cast<const float4 *>(smem + Z::OG) + (c % 3) * C + 2 * (C / 4);
+      wait(o_done, c);
+      fence_after_sync();
+      if (on && t0 < padded(c)) {
+#pragma unroll
+        for (int e0 = 0; e0 < 16; e0 += 8) {
+          uint32_t x[8], y[8];
+          tmem_ld8(tl + Z::D4 + t0 + e0, x);
+          tmem_ld8(tl + Z::P + t0 + e0, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            const float4 g = Gb[(t0 + e0 + e) / 4];
+            const float o0 = fmaf(g.x, __uint_as_float(y[e]), __uint_as_float(x[e])), o1 = fmaf(g.y, __uint_as_float(y[e + 1]), __uint_as_float(x[e + 1]));
+            const float o2 = fmaf(g.z, __uint_as_float(y[e + 2]), __uint_as_float(x[e + 2])), o3 = fmaf(g.w, __uint_as_float(y[e + 3]), __uint_as_float(x[e + 3]));
+            if (F32) {
+              held[(e0 + e) % (F32 ? 16 : 8)] = __float_as_uint(o0), held[(e0 + e + 1) % (F32 ? 16 : 8)] = __float_as_uint(o1);
+              held[(e0 + e + 2) % (F32 ? 16 : 8)] = __float_as_uint(o2), held[(e0 + e + 3) % (F32 ? 16 : 8)] = __float_as_uint(o3);
+            } else {
+              held[(e0 + e) / 2] = pack2(o0, o1), held[(e0 + e) / 2 + 1] = pack2(o2, o3);
+            }
+          }
+        }
+      }
+      fence_before_sync();
+      arrive(o_read);
+    };
+    auto store_outputs = [&](int c) {
+      if (on && t0 < padded(c)) {
+        char *to = smem + Z::OV + (c % NV) * Z::VBUF + j * ES + t0 * D * ES;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (F32) *reinterpret_cast<uint32_t *>(to + e * D * ES) = held[e % (F32 ? 16 : 8)];
+          else *reinterpret_cast<uint16_t *>(to + e * D * ES) = (uint16_t)(held[e / 2] >> (e & 1) * 16);
+        }
+      }
+      arrive(o_ready);
+    };
     float gC = 1.0f;
     // (the end of a chunk is worked off in the next one's turn, between what that chunk's products wait for)
 #pragma unroll 1
@@ -199,83 +244,58 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         if (on) {
 #pragma unroll
           for (int i = 0; i < HELD; i += 16) {
-            uint32_t x[3][8];
+            uint32_t x[NS][8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) split<3>(S[i + 2 * e], S[i + 2 * e + 1], &x[0][e], 8);
+            for (int e = 0; e < 8; ++e) split<NS>(S[i + 2 * e], S[i + 2 * e + 1], &x[0][e], 8);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) tmem_st8(tl + Z::a1(k) + (grp * HELD + i) / 2, x[k]);
+            for (int k = 0; k < NS; ++k) tmem_st8(tl + Z::a1(k) + (grp * HELD + i) / 2, x[k]);
           }
           tmem_wait_st();
         }
         fence_before_sync();
         arrive(a1);
       }
-      // ---- outputs of the chunk before, through its rows of v
-      if (c > 0 && out) {
-        const float4 *Gb = reinterpret_cast<const float4 *>(smem + Z::OG) + ((c - 1) % 3) * C + 2 * (C / 4);
-        wait(o_done, c - 1);
+      if (out && c > 0) {
+        read_outputs(c - 1);
+        if (NV == 1) store_outputs(c - 1);                 // (this chunk's rows of v come where they leave)
+      }
+      const bool mine = on && t0 < padded(c);            // (the products read no tokens past these)
+      if (c < chunks) {
+        // ---- rhs = beta (v - G w)
+        wait(&ready[c % 3], c / 3);
+        wait(w_done, c);
+        if (F32 && out) wait(p_done, c);                   // (q's products read the part of S that rhs lies over)
         fence_after_sync();
-        if (on && t0 < padded(c - 1)) {
-          char *to = smem + Z::OV + ((c - 1) % NB) * Z::VBUF + j * ES + t0 * D * ES;
+        if (mine) {
+          const char *at = smem + Z::OV + (c % NV) * Z::VBUF + j * ES + t0 * D * ES;
 #pragma unroll 1
-          for (int e0 = 0; e0 < 16; e0 += 8) {
-            uint32_t x[8], y[8];
-            tmem_ld8(tl + Z::D4 + t0 + e0, x);
-            tmem_ld8(tl + Z::P + t0 + e0, y);
+          for (int e0 = 0; e0 < 16; e0 += 8, at += 8 * D * ES) {
+            uint32_t w[8], x[3][4];
+            tmem_ld8(tl + Z::W + t0 + e0, w);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] = F32 ? *reinterpret_cast<const float *>(at + e * D * ES)
+                         : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at + e * D * ES) << 16);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; e += 4, to += 4 * D * ES) {
-              const float4 g = Gb[(t0 + e0 + e) / 4];
-              const float o0 = fmaf(g.x, __uint_as_float(y[e]), __uint_as_float(x[e])), o1 = fmaf(g.y, __uint_as_float(y[e + 1]), __uint_as_float(x[e + 1]));
-              const float o2 = fmaf(g.z, __uint_as_float(y[e + 2]), __uint_as_float(x[e + 2])), o3 = fmaf(g.w, __uint_as_float(y[e + 3]), __uint_as_float(x[e + 3]));
-              if (F32) {
-                *reinterpret_cast<float *>(to) = o0, *reinterpret_cast<float *>(to + D * ES) = o1;
-                *reinterpret_cast<float *>(to + 2 * D * ES) = o2, *reinterpret_cast<float *>(to + 3 * D * ES) = o3;
-              } else {
-                const uint32_t a = pack2(o0, o1), b2 = pack2(o2, o3);
-                *reinterpret_cast<uint16_t *>(to) = (uint16_t)a, *reinterpret_cast<uint16_t *>(to + D * ES) = (uint16_t)(a >> 16);
-                *reinterpret_cast<uint16_t *>(to + 2 * D * ES) = (uint16_t)b2, *reinterpret_cast<uint16_t *>(to + 3 * D * ES) = (uint16_t)(b2 >> 16);
-              }
+            for (int e = 0; e < 8; e += 4) {
+              const float4 g = G[(t0 + e0 + e) / 4], be = beta[(t0 + e0 + e) / 4];
+              const float y0 = be.x * fmaf(-g.x, __uint_as_float(w[e]), v[e]), y1 = be.y * fmaf(-g.y, __uint_as_float(w[e + 1]), v[e + 1]);
+              const float y2 = be.z * fmaf(-g.z, __uint_as_float(w[e + 2]), v[e + 2]), y3 = be.w * fmaf(-g.w, __uint_as_float(w[e + 3]), v[e + 3]);
+              split<3>(y0, y1, &x[0][e / 2], 4);
+              split<3>(y2, y3, &x[0][e / 2 + 1], 4);
             }
+#pragma unroll
+            for (int k = 0; k < 3; ++k) tmem_st4(tl + Z::a2(k) + (t0 + e0) / 2, x[k]);
           }
+          tmem_wait_st();
         }
         fence_before_sync();
-        arrive(o_read);
+        arrive(a2 + half);
       }
+      if (NV > 1 && out && c > 0) store_outputs(c - 1);
       if (c == chunks) break;
-      const bool mine = on && t0 < padded(c);            // (the products read no tokens past these)
-      // ---- rhs = beta (v - G w)
-      wait(&ready[c % 3], c / 3);
-      wait(w_done, c);
-      if (F32 && out) wait(p_done, c);                   // (q's products read the part of S that rhs lies over)
-      fence_after_sync();
-      if (mine) {
-        const char *at = smem + Z::OV + (c % NB) * Z::VBUF + j * ES + t0 * D * ES;
-#pragma unroll 1
-        for (int e0 = 0; e0 < 16; e0 += 8, at += 8 * D * ES) {
-          uint32_t w[8], x[3][4];
-          tmem_ld8(tl + Z::W + t0 + e0, w);
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            v[e] = F32 ? *reinterpret_cast<const float *>(at + e * D * ES)
-                       : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at + e * D * ES) << 16);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const float4 g = G[(t0 + e0 + e) / 4], be = beta[(t0 + e0 + e) / 4];
-            const float y0 = be.x * fmaf(-g.x, __uint_as_float(w[e]), v[e]), y1 = be.y * fmaf(-g.y, __uint_as_float(w[e + 1]), v[e + 1]);
-            const float y2 = be.z * fmaf(-g.z, __uint_as_float(w[e + 2]), v[e + 2]), y3 = be.w * fmaf(-g.w, __uint_as_float(w[e + 3]), v[e + 3]);
-            split<3>(y0, y1, &x[0][e / 2], 4);
-            split<3>(y2, y3, &x[0][e / 2 + 1], 4);
-          }
-#pragma unroll
-          for (int k = 0; k < 3; ++k) tmem_st4(tl + Z::a2(k) + (t0 + e0) / 2, x[k]);
-        }
-        tmem_wait_st();
-      }
-      fence_before_sync();
-      arrive(a2 + half);
       gC = G[C / 4 - 1].w;
       // ---- u, decayed to the chunk's end
       wait(u_done + half, c);
@@ -332,11 +352,10 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       for (long i = tid; i < (long)(p.n_tokens - n) * PIECES; i += Z::MAIN * 32)
         *reinterpret_cast<uint4 *>(p.o.p + (b * p.o.sb + (n + i / PIECES) * p.o.st + h * p.o.sh) * ES + i % PIECES * 16) = make_uint4(0, 0, 0, 0);
     }
-  } else if (warp < Z::W_MMA) {
+  } else if (warp < Z::W_INV) {
     // ---------------------------------------------------------------- tables of the chunks
-    const int at = tid - Z::MAIN * 32, aw = warp - Z::MAIN, t = at & 63;
+    const int at = tid - Z::W_TAB * 32, aw = warp - Z::W_TAB, t = at & 63;
     const bool isq = at >= 64;                           // rows of k (M, T), then of q (P)
-    float *M = reinterpret_cast<float *>(smem + Z::OM), *Y = reinterpret_cast<float *>(smem + Z::OY);
     const int words = (p.n_tokens + 31) >> 5;
     float a_next, b_next;                                // gates of the next chunk (threads 0..63; others and rows past the end: of a row that exists)
     auto fetch = [&](int c) {
@@ -363,7 +382,9 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       }
       if (t < 32) see[0] = (see[0] | 1u << t) & ((2u << t) - 1), see[1] = 0;
       else see[1] = (see[1] | 1u << (t - 32)) & ((2u << (t - 32)) - 1);
-      aux_sync();
+      float *M = reinterpret_cast<float *>(smem + Z::OM) + (c % NM) * C * LD;
+      sync4<1>();
+      if (c >= NM) wait(&m_free[c % NM], c / NM - 1);
       wait(g_done, c);                                   // (with it the output products of the chunk before the last are done)
       fence_after_sync();
       // ---- a row of R from its end, times the dot products: M (a row's entries in a column; rows of M carry beta) and P
@@ -413,9 +434,20 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         }
       }
       if (isq) G[t] = r;
+      fence_smem_to_async();
       fence_before_sync();
       arrive(&ready[c % 3]);
-      aux_sync();
+      arrive(&m_ready[c % NM]);
+    }
+  } else if (warp < Z::W_MMA) {
+    // ---------------------------------------------------------------- inverses
+    const int at = tid - Z::W_INV * 32, aw = warp - Z::W_INV, t = at & 63;
+    float *Y = reinterpret_cast<float *>(smem + Z::OY);
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const int np = padded(c);
+      float *M = reinterpret_cast<float *>(smem + Z::OM) + (c % NM) * C * LD;
+      wait(&m_ready[c % NM], c / NM);
       // ---- T = (I + M)^-1 in M's place, by columns as M: blocks of 16 on the diagonal (a lane a column, whose later entries are brought up to
       // date as each is known); then twice the block below two inverses, -T_b M_ba T_a
       {
@@ -441,7 +473,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
           for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(m + col * LD + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
         }
       }
-      aux_sync();
+      sync4<6>();
       // sums over i of row pairs m(i, rows) x(i)
       if (np > 16) {
         const int oa = (aw >> 1) * 32, ob = oa + 16, col = lane & 15, q = 4 * ((aw & 1) * 2 + (lane >> 4));
@@ -455,7 +487,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         }
         float2 v0 = pair(s0), v1 = pair(s1);
         y[q * LY + col] = -v0.x, y[(q + 1) * LY + col] = -v0.y, y[(q + 2) * LY + col] = -v1.x, y[(q + 3) * LY + col] = -v1.y;
-        aux_sync();
+        sync4<6>();
         s0 = s1 = 0;
 #pragma unroll 8
         for (int i = 0; i < 16; ++i) {
@@ -465,7 +497,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         }
         v0 = pair(s0), v1 = pair(s1);
         *reinterpret_cast<float4 *>(M + (oa + col) * LD + ob + q) = make_float4(v0.x, v0.y, v1.x, v1.y);
-        aux_sync();
+        sync4<6>();
       }
       if (np > 32) {
         const int q = 8 * aw;
@@ -487,13 +519,13 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
           Y[(q + 2 * i) * LY + lane] = -v.x, Y[(q + 2 * i + 1) * LY + lane] = -v.y;
           s[i] = 0;
         }
-        aux_sync();
+        sync4<6>();
 #pragma unroll 8
         for (int i = 0; i < 32; ++i) add(M + (32 + i) * LD + 32 + q, Y[i * LY + lane]);
         const float2 v0 = pair(s[0]), v1 = pair(s[1]), v2 = pair(s[2]), v3 = pair(s[3]);
         *reinterpret_cast<float4 *>(M + lane * LD + 32 + q) = make_float4(v0.x, v0.y, v1.x, v1.y);
         *reinterpret_cast<float4 *>(M + lane * LD + 36 + q) = make_float4(v2.x, v2.y, v3.x, v3.y);
-        aux_sync();
+        sync4<6>();
       }
       if (c) wait(u_done + 1, c - 1);
 #pragma unroll 1
@@ -511,6 +543,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       }
       fence_smem_to_async();
       arrive(t_ready);
+      arrive(&m_free[c % NM]);
     }
   } else if (warp >= Z::W_LOAD) {
     // ---------------------------------------------------------------- rows of the chunks: one warp copies k and q, one v, one o
@@ -521,12 +554,18 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       const int nt = tokens(c);
       const long step = x.st * ES;
       const char *base = x.p + (b * x.sb + head * x.sh) * ES + piece, *at = base + (c * C + first) * step;
-#pragma unroll 4
-      for (int r = 0; r < C; r += per, at += per * step) {
-        const bool live = r + first < nt;
-        const char *from = live ? at : x.p;
-        if (p.idx && live) from = base + row_of(p, b, c * C + r + first) * step;
-        one(r, from, live);
+      const long next = per * step;
+      if (nt == C && !p.idx) {
+#pragma unroll 8
+        for (int r = 0; r < C; r += per, at += next) one(r, at, true);
+      } else {
+#pragma unroll 1
+        for (int r = 0; r < C; r += per, at += next) {
+          const bool live = r + first < nt;
+          const char *from = live ? at : x.p;
+          if (p.idx && live) from = base + row_of(p, b, c * C + r + first) * step;
+          one(r, from, live);
+        }
       }
     };
     auto load = [&](int c) {
@@ -558,7 +597,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       } else {
         constexpr int PIECES = D * ES / 16, PER = 32 / PIECES;             // of a row; rows at once
         static_assert(PIECES <= 32 && C % PER == 0, "rows of v");
-        const uint32_t to = base + Z::OV + (c % NB) * Z::VBUF + lane * 16;
+        const uint32_t to = base + Z::OV + (c % NV) * Z::VBUF + lane * 16;
         rows(p.v, h, c, lane / PIECES, PER, lane % PIECES * 16, [&](int r, const char *from, bool live) { cp16(to + r * D * ES, from, live ? 16 : 0); });
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -567,7 +606,12 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       // v's buffer is free when the outputs written over it have left
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
-        if (c >= NB) wait(what == 1 && out ? &o_free[c % NB] : &x_free[c % NB], c / NB - 1);
+        if (what == 0) {
+          if (c >= NB) wait(&x_free[c % NB], c / NB - 1);
+        } else if (c >= NV) {
+          if (out) wait(&o_free[c % NV], c / NV - 1);
+          else wait(&x_free[(c - NV) % NB], (c - NV) / NB);   // (v has been read before u is formed)
+        }
         load(c);
         fence_smem_to_async();
         arrive(what == 0 ? &x_full[c % NB] : &ready[c % 3]);
@@ -577,14 +621,20 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       constexpr int PIECES = D * ES / 16, PER = 32 / PIECES;
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
-        wait(o_read, c);
+        wait(o_ready, c);
         const int nt = tokens(c), first = lane / PIECES, piece = lane % PIECES;
-        const char *from = smem + Z::OV + (c % NB) * Z::VBUF + first * D * ES + piece * 16;
+        const char *from = smem + Z::OV + (c % NV) * Z::VBUF + first * D * ES + piece * 16;
         char *to = p.o.p + (b * p.o.sb + (long)(c * C + first) * p.o.st + h * p.o.sh) * ES + piece * 16;
+        const long next = PER * p.o.st * ES;
+        if (nt == C) {
 #pragma unroll 8
-        for (int r = 0; r < C; r += PER)
-          if (r + first < nt) *reinterpret_cast<uint4 *>(to + r * p.o.st * ES) = *reinterpret_cast<const uint4 *>(from + r * D * ES);
-        arrive(&o_free[c % NB]);
+          for (int r = 0; r < C; r += PER, to += next) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from + r * D * ES);
+        } else {
+#pragma unroll 1
+          for (int r = 0; r < C; r += PER, to += next)
+            if (r + first < nt) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from + r * D * ES);
+        }
+        arrive(&o_free[c % NV]);
       }
     }
   } else {
@@ -593,6 +643,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     uint32_t leader;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(leader));
     const uint32_t base = smem_u32(smem);
+    auto all_good = [&]() { return good = __all_sync(0xffffffffu, good); };
     constexpr uint32_t SBO = (D / 8) * 128;
     // Part pairs i < NA, k < NK with i + k <= MOST, smallest first; `one` gets `add` for the first of all (0: its product clears D).
     auto pairs = [&](auto na, auto nk, auto most, uint32_t add, auto one) {
@@ -608,12 +659,14 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     using INX = std::integral_constant<int, NX>;
     using INO = std::integral_constant<int, NO>;
     using IMO = std::integral_constant<int, NO - 1>;
+    using INS = std::integral_constant<int, NS>;
+    using IMS = std::integral_constant<int, NS - 1>;
     const uint64_t x_row = smem_desc(base + Z::OX, 128, SBO), x_col = smem_desc(base + Z::OX, SBO, 128);   // rows, and along their other dimension
     const uint64_t t_row = smem_desc(base + Z::OT, 128, 1024), p_row = smem_desc(base + Z::OP, 128, 1024);
     constexpr uint32_t XB = Z::XBUF >> 4, XP = Z::XPART >> 4, TP = Z::TPART >> 4;
     auto dots = [&](int c) {                             // [k | q] k^T
       wait(&x_full[c % NB], c / NB);
-      if (!good) return;
+      if (!all_good()) return;
       fence_after_sync();
       if (leader) {
         const uint32_t id = idesc_n(padded(c));
@@ -632,27 +685,28 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       const uint32_t id = idesc_n(np);
       const uint64_t x = x_row + (c % NB) * XB;
       wait(a1, c);
-      if (!good) break;
+      if (!all_good()) break;
       fence_after_sync();
       if (leader)
-        pairs(I3{}, INX{}, I2{}, 0, [&](int i, int k, uint32_t add) {
+        pairs(INS{}, INX{}, IMS{}, 0, [&](int i, int k, uint32_t add) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) mma_ts(tmem + Z::W, tmem + Z::a1(i) + 8 * kk, x + k * XP + kk * 16, id, kk ? 1u : add);
         });
       if (leader) commit(w_done);
-      if (out) {
+      auto of_q = [&]() {                                // p (the last one has been read)
         if (c) wait(o_read, c - 1);
-        if (!good) break;
+        if (!all_good()) return;
         fence_after_sync();
         if (leader) {
-          pairs(I3{}, INX{}, IMO{}, 0, [&](int i, int k, uint32_t add) {
+          pairs(INS{}, INX{}, IMS{}, 0, [&](int i, int k, uint32_t add) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_ts(tmem + Z::P, tmem + Z::a1(i) + 8 * kk, x + k * XP + (Z::ROWS >> 4) + kk * 16, id, kk ? 1u : add);
           });
-          commit(p_done);
+          if (F32) commit(p_done);
         }
-      }
+      };
+      if (F32 && out) of_q();
       if (NB > 1 && c + 1 < chunks) {
         wait(&ready[c % 3], c / 3);                      // (the last dot products have been read)
         dots(c + 1);
@@ -662,7 +716,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
 #pragma unroll 1
       for (int r = 0; r < 2; ++r) {
         wait(a2 + r, c);
-        if (!good) break;
+        if (!all_good()) break;
         fence_after_sync();
         if (leader) {
           pairs(I3{}, I3{}, I2{}, r, [&](int i, int k, uint32_t add) {
@@ -676,12 +730,13 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
           commit(u_done + r);
         }
       }
+      if (!F32 && out) of_q();
       if (p.write) {
         const uint64_t xc = x_col + (c % NB) * XB;
 #pragma unroll 1
         for (int r = 0; r < 2; ++r) {
           wait(a3 + r, c);
-          if (!good) break;
+          if (!all_good()) break;
           fence_after_sync();
           if (leader)
             pairs(I3{}, INX{}, I2{}, r, [&](int i, int k, uint32_t add) {
@@ -699,7 +754,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       }
       if (out) {
         wait(a4, c);
-        if (!good) break;
+        if (!all_good()) break;
         fence_after_sync();
         if (leader) {
           pairs(INO{}, INO{}, IMO{}, 0, [&](int i, int k, uint32_t add) {
@@ -718,7 +773,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     wait_long(drain, 0);
     __syncwarp();
   }
-  if (!good && lane == 0) atomicOr(p.status, PACE_DELTA_TIMEOUT);
+  if (!good) atomicOr(p.status, PACE_DELTA_TIMEOUT);
   fence_before_sync();
   __syncthreads();
   if (warp == Z::W_MMA) tmem_dealloc(*tmem_slot, 512);
