@@ -33,6 +33,17 @@ using namespace umma;
 
 constexpr int C = 64;                                    // tokens a chunk
 
+// A sequence and head of the call, as a block keeps it: b, h; tokens (0: none, or left out); slot; whether it begins with a zero state.
+struct Unit {
+  uint32_t bh;
+  int n;
+  uint32_t slot;
+};
+constexpr int UNITS = 64;                                // most of a block
+// Most chunks of a call whose blocks go from one sequence and head to the next (512 of equal length, heads of 128: of 64 tokens 39 us, a block for
+// each 46; of 256 110 and 111; of 512 198 and 189; of 1024 367 and 337. 2048 of 64 tokens 134 and 181).
+constexpr int CHUNKS_LASTING = 4;
+
 template <int D, bool F32>
 struct Shape {
   static constexpr int MAIN = 16, AUX = 4, W_TAB = MAIN, W_INV = W_TAB + AUX, W_MMA = W_INV + AUX, W_LOAD = W_MMA + 1, THREADS = (W_LOAD + 3) * 32;
@@ -48,7 +59,7 @@ struct Shape {
   static constexpr int TPART = C * C * 2;
   static constexpr int LD = C + 4, LY = 36;              // rows of the fp32 tables
   static constexpr int OX = 0, OV = OX + NB * XBUF, OT = OV + NV * VBUF, OP = OT + 3 * TPART, OM = OP + 2 * NO * TPART, OY = OM + NM * C * LD * 4,
-                       OG = OY + 32 * LY * 4, OBAR = OG + 3 * 4 * C * 4, NBAR = 2 * NB + NV + 2 * NM + 3 + 18, OMISC = OBAR + NBAR * 8, SMEM = OMISC + 16;
+                       OG = OY + 32 * LY * 4, OBAR = OG + 3 * 4 * C * 4, NBAR = 2 * NB + NV + 2 * NM + 3 + 18, OMISC = OBAR + NBAR * 8, OUNIT = OMISC + 16, SMEM = OUNIT + UNITS * (int)sizeof(Unit);
   static_assert(SMEM <= 227 * 1024 && OBAR % 8 == 0, "shared memory");
   // TMEM columns. What lies over something else is written when the products that read that have ended: R_C u over rhs (whose halves are done as
   // those of u are), the state's increment over its parts, u over w; with fp32 I/O rhs over the state's third part, and so q's products before rhs.
@@ -108,7 +119,8 @@ __device__ __forceinline__ float2 pair(uint64_t v) {
   return r;
 }
 
-template <int D, bool F32>
+// ONE: a block for each sequence and head; else blocks go on from one to the next, whose rows and tables are then under way.
+template <int D, bool F32, bool ONE>
 __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(const DeltaArgs p) {
   using Z = Shape<D, F32>;
   constexpr int NX = Z::NX, NO = Z::NO, NB = Z::NB, NV = Z::NV, NM = Z::NM, NS = Z::NS, LD = Z::LD, LY = Z::LY, ES = F32 ? 4 : 2;
@@ -119,10 +131,8 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
            *u_done = a4 + 1, *w_done = u_done + 2, *p_done = w_done + 1, *s_done = p_done + 1, *o_done = s_done + 1, *o_read = o_done + 1,
            *o_ready = o_read + 1, *g_done = o_ready + 1, *t_ready = g_done + 1, *drain = t_ready + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::OMISC);
-  Seq *seq_slot = reinterpret_cast<Seq *>(tmem_slot + 1);
-  static_assert(sizeof(Seq) <= 12, "kept beside the TMEM address");
+  Unit *unit = reinterpret_cast<Unit *>(smem + Z::OUNIT);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H, hk = h / p.group;
   const bool out = p.o.p != nullptr;
 
   if (warp == Z::W_MMA) {
@@ -141,20 +151,68 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     mbar_fence_init();
   }
   pdl_enter();
-  if (warp == 0) {
-    const Seq s = sequence(p, b, h == 0);
-    if (lane == 0) *seq_slot = s;
+  // ---- this block's sequences and heads. The longest sequences go out first; to lasting blocks in turn there and back
+  const int total = p.batch * p.H, turns = ONE ? 1 : (total + gridDim.x - 1) / gridDim.x;
+  uint16_t *order = reinterpret_cast<uint16_t *>(smem + Z::OX);
+  const bool sorted = total > p.sms && (p.n_new || p.n_keep) && p.batch <= 256;
+  if (sorted) {
+    int *count = reinterpret_cast<int *>(smem + Z::OM);
+    if (tid < p.batch) count[tid] = count_of(p, tid);
+    __syncthreads();
+    if (tid < p.batch) {
+      int rank = 0;
+      for (int i = 0; i < p.batch; ++i) rank += count[i] > count[tid] || (count[i] == count[tid] && i < tid);
+      order[rank] = (uint16_t)tid;
+    }
+    __syncthreads();
+  }
+  for (int k = warp; k < turns; k += Z::THREADS / 32) {
+    const int u = ONE ? blockIdx.x : k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (u >= total) {
+      if (lane == 0) unit[k].n = 0;
+      continue;
+    }
+    const int h = u % p.H, b = sorted ? order[u / p.H] : u / p.H;
+    int bad = 0;
+    Seq s = sequence(p, b, bad);
+    if (s.n > 0 && taken(p, b, s.slot)) {
+      bad |= PACE_DELTA_BAD_SLOT;
+      s.n = 0;
+    }
+    if (bad && h == 0 && lane == 0) atomicOr(p.status, bad);
+    if (lane == 0) unit[k] = Unit{(uint32_t)(b * PACE_MAX_HEADS + h), s.n, (uint32_t)s.slot | (uint32_t)s.fresh << 31};
+    if (out) {                                           // rows past the sequence's tokens
+      constexpr int PIECES = D * ES / 16;
+      char *o = p.o.p + (b * p.o.sb + h * p.o.sh) * ES;
+      for (long i = (long)s.n * PIECES + lane; i < (long)p.n_tokens * PIECES; i += 32)
+        *reinterpret_cast<uint4 *>(o + i / PIECES * p.o.st * ES + i % PIECES * 16) = make_uint4(0, 0, 0, 0);
+    }
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const Seq s = *seq_slot;
-  const int n = s.n, chunks = (n + C - 1) / C;
   constexpr uint32_t tmem = 0;          // the whole of TMEM is this block's: its first column (a constant keeps addresses uniform)
-  float *state = p.S + ((long)s.slot * p.H + h) * D * D;
+  // The unit that a role works on, and the place of the chunk among all chunks of the block (buffers and barriers go by that): its number g, and
+  // what is left of it and how often it went around in a ring of three.
+  int b = 0, h = 0, hk = 0, n = 0, chunks = 0, g = 0, ring = 0, rounds = 0;
+  auto step = [&]() {
+    ++g;
+    if (!ONE && ++ring == 3) ring = 0, ++rounds;
+  };
+  auto g3 = [&]() { return ONE ? g % 3 : ring; };        // (counted where there are many short ones, divided where registers are dearer)
+  auto r3 = [&]() { return ONE ? g / 3 : rounds; };
+  auto take = [&](int k) {
+    const Unit u = unit[k];
+    b = u.bh / PACE_MAX_HEADS, h = u.bh % PACE_MAX_HEADS, hk = h / p.group, n = u.n;
+    chunks = (n + C - 1) / C;
+    return n > 0;
+  };
   // tokens of a chunk, and as the products count them
   auto tokens = [&](int c) { return min(C, n - c * C); };
   auto padded = [&](int c) { return (tokens(c) + 15) & ~15; };
+  static_assert(NB == 3 || NB == 1, "rings");
+  auto at_x = [&]() { return NB == 3 ? g3() : 0; };
+  auto round_x = [&]() { return NB == 3 ? r3() : g; };
 
   bool good = true;
   auto wait = [&](uint64_t *x, int phase) {              // (by the whole warp)
@@ -174,14 +232,11 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     const bool on = (warp & 3) * 32 < D;                 // (heads of 64 leave half of the lanes alone)
     constexpr int HELD = Z::HELD;
     float S[HELD];                                       // rows HELD grp .. of the state's column j
-    state += (long)(grp * HELD) * D + j;
-#pragma unroll
-    for (int i = 0; i < HELD; ++i) S[i] = on && n > 0 && !s.fresh ? state[i * D] : 0.0f;
     // outputs of a chunk: read when they are done, stored through its rows of v when u's products have been given their rhs
     uint32_t held[F32 ? 16 : 8];
-    auto read_outputs = [&](int c) {
-      const float4 *Gb = reinterpret_cast<const float4 *>(smem + Z::OG) + (c % 3) * C + 2 * (C / 4);
-      wait(o_done, c);
+    auto read_outputs = [&](int c) {                     // (the chunk before g)
+      const float4 *Gb = reinterpret_cast<const float4 *>(smem + Z::OG) + (g3() ? g3() - 1 : 2) * C + 2 * (C / 4);
+      wait(o_done, g - 1);
       fence_after_sync();
       if (on && t0 < padded(c)) {
 #pragma unroll
@@ -209,7 +264,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     };
     auto store_outputs = [&](int c) {
       if (on && t0 < padded(c)) {
-        char *to = smem + Z::OV + (c % NV) * Z::VBUF + j * ES + t0 * D * ES;
+        char *to = smem + Z::OV + ((g - 1) % NV) * Z::VBUF + j * ES + t0 * D * ES;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           if (F32) *reinterpret_cast<uint32_t *>(to + e * D * ES) = held[e % (F32 ? 16 : 8)];
@@ -219,13 +274,26 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       arrive(o_ready);
     };
     float gC = 1.0f;
+#pragma unroll 1
+    for (int k = 0; k < turns; ++k) {
+    if (!take(k)) continue;
+    auto state = [&]() {
+      const Unit u = unit[k];
+      return p.S + ((long)(u.slot & 0x7FFFFFFFu) * p.H + u.bh % PACE_MAX_HEADS) * D * D + (long)(grp * HELD) * D + j;
+    };
+    {
+      const float *from = state();
+      const bool held_before = on && !(unit[k].slot >> 31);
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) S[i] = held_before ? from[i * D] : 0.0f;
+    }
     // (the end of a chunk is worked off in the next one's turn, between what that chunk's products wait for)
 #pragma unroll 1
     for (int c = 0; c <= chunks; ++c) {
-      const float4 *ga = reinterpret_cast<const float4 *>(smem + Z::OG) + (c % 3) * C, *beta = ga + C / 4, *G = ga + 2 * (C / 4), *rho = ga + 3 * (C / 4);
+      const float4 *ga = reinterpret_cast<const float4 *>(smem + Z::OG) + g3() * C, *beta = ga + C / 4, *G = ga + 2 * (C / 4), *rho = ga + 3 * (C / 4);
       // ---- the state at the end of the chunk before (its increment lies over parts: all four warps read theirs before any writes)
       if (c > 0 && p.write) {
-        wait(s_done, c - 1);
+        wait(s_done, g - 1);
         fence_after_sync();
         if (on) {
 #pragma unroll
@@ -262,12 +330,12 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       const bool mine = on && t0 < padded(c);            // (the products read no tokens past these)
       if (c < chunks) {
         // ---- rhs = beta (v - G w)
-        wait(&ready[c % 3], c / 3);
-        wait(w_done, c);
-        if (F32 && out) wait(p_done, c);                   // (q's products read the part of S that rhs lies over)
+        wait(&ready[g3()], r3());
+        wait(w_done, g);
+        if (F32 && out) wait(p_done, g);                   // (q's products read the part of S that rhs lies over)
         fence_after_sync();
         if (mine) {
-          const char *at = smem + Z::OV + (c % NV) * Z::VBUF + j * ES + t0 * D * ES;
+          const char *at = smem + Z::OV + (g % NV) * Z::VBUF + j * ES + t0 * D * ES;
 #pragma unroll 1
           for (int e0 = 0; e0 < 16; e0 += 8, at += 8 * D * ES) {
             uint32_t w[8], x[3][4];
@@ -295,10 +363,10 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         arrive(a2 + half);
       }
       if (NV > 1 && out && c > 0) store_outputs(c - 1);
-      if (c == chunks) break;
+      if (c == chunks) break;                            // (its place is the next unit's first chunk's)
       gC = G[C / 4 - 1].w;
       // ---- u, decayed to the chunk's end
-      wait(u_done + half, c);
+      wait(u_done + half, g);
       fence_after_sync();
       if (p.write) {
         if (mine) {
@@ -323,7 +391,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       // ---- u as it is (over w, which the other half's warps have read when their u is done)
       if (out) {
         if (half == 0) {
-          wait(u_done + 1, c);
+          wait(u_done + 1, g);
           fence_after_sync();
         }
         if (mine) {
@@ -342,15 +410,13 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         fence_before_sync();
         arrive(a4);
       }
+          step();
     }
-    if (p.write && n > 0 && on && good) {
+    if (p.write && on && good) {
+      float *to = state();
 #pragma unroll
-      for (int i = 0; i < HELD; ++i) state[i * D] = S[i];
+      for (int i = 0; i < HELD; ++i) to[i * D] = S[i];
     }
-    if (out) {                                           // rows past the sequence's tokens
-      constexpr int PIECES = D * ES / 16;
-      for (long i = tid; i < (long)(p.n_tokens - n) * PIECES; i += Z::MAIN * 32)
-        *reinterpret_cast<uint4 *>(p.o.p + (b * p.o.sb + (n + i / PIECES) * p.o.st + h * p.o.sh) * ES + i % PIECES * 16) = make_uint4(0, 0, 0, 0);
     }
   } else if (warp < Z::W_INV) {
     // ---------------------------------------------------------------- tables of the chunks
@@ -364,11 +430,14 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       a_next = reinterpret_cast<const float *>(p.a.p)[b * p.a.sb + row * p.a.st + h * p.a.sh];
       b_next = reinterpret_cast<const float *>(p.beta.p)[b * p.beta.sb + row * p.beta.st + h * p.beta.sh];
     };
-    if (chunks) fetch(0);
+#pragma unroll 1
+    for (int k = 0; k < turns; ++k) {
+    if (!take(k)) continue;
+    fetch(0);
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       const int nt = tokens(c), np = padded(c);
-      float *ga = reinterpret_cast<float *>(smem + Z::OG) + (c % 3) * 4 * C, *beta = ga + C, *G = ga + 2 * C, *rho = ga + 3 * C;
+      float *ga = reinterpret_cast<float *>(smem + Z::OG) + g3() * 4 * C, *beta = ga + C, *G = ga + 2 * C, *rho = ga + 3 * C;
       if (!isq) ga[t] = t < nt ? a_next : 1.0f, beta[t] = t < nt ? b_next : 0.0f;
       fetch(c + 1);
       uint32_t see[2] = {~0u, ~0u};                      // the token and its ancestors
@@ -382,10 +451,10 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       }
       if (t < 32) see[0] = (see[0] | 1u << t) & ((2u << t) - 1), see[1] = 0;
       else see[1] = (see[1] | 1u << (t - 32)) & ((2u << (t - 32)) - 1);
-      float *M = reinterpret_cast<float *>(smem + Z::OM) + (c % NM) * C * LD;
+      float *M = reinterpret_cast<float *>(smem + Z::OM) + (g % NM) * C * LD;
       sync4<1>();
-      if (c >= NM) wait(&m_free[c % NM], c / NM - 1);
-      wait(g_done, c);                                   // (with it the output products of the chunk before the last are done)
+      if (g >= NM) wait(&m_free[g % NM], g / NM - 1);
+      wait(g_done, g);                                   // (with it the output products of the chunk before the last are done)
       fence_after_sync();
       // ---- a row of R from its end, times the dot products: M (a row's entries in a column; rows of M carry beta) and P
       float r = isq ? 1.0f : beta[t];
@@ -422,7 +491,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
 #pragma unroll
           for (int e = 0; e < 16; ++e) M[(i0 + e) * LD + t] = R[e];
         } else if (out) {
-          char *to = smem + Z::OP + (c & 1) * NO * Z::TPART + core_at(t, 0, C) + i0 * 16;
+          char *to = smem + Z::OP + (g & 1) * NO * Z::TPART + core_at(t, 0, C) + i0 * 16;
 #pragma unroll
           for (int e0 = 0; e0 < 16; e0 += 8) {
             uint32_t w[NO][4];
@@ -436,18 +505,23 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       if (isq) G[t] = r;
       fence_smem_to_async();
       fence_before_sync();
-      arrive(&ready[c % 3]);
-      arrive(&m_ready[c % NM]);
+      arrive(&ready[g3()]);
+      arrive(&m_ready[g % NM]);
+      step();
+    }
     }
   } else if (warp < Z::W_MMA) {
     // ---------------------------------------------------------------- inverses
     const int at = tid - Z::W_INV * 32, aw = warp - Z::W_INV, t = at & 63;
     float *Y = reinterpret_cast<float *>(smem + Z::OY);
 #pragma unroll 1
+    for (int k = 0; k < turns; ++k) {
+    if (!take(k)) continue;
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       const int np = padded(c);
-      float *M = reinterpret_cast<float *>(smem + Z::OM) + (c % NM) * C * LD;
-      wait(&m_ready[c % NM], c / NM);
+      float *M = reinterpret_cast<float *>(smem + Z::OM) + (g % NM) * C * LD;
+      wait(&m_ready[g % NM], g / NM);
       // ---- T = (I + M)^-1 in M's place, by columns as M: blocks of 16 on the diagonal (a lane a column, whose later entries are brought up to
       // date as each is known); then twice the block below two inverses, -T_b M_ba T_a
       {
@@ -527,7 +601,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         *reinterpret_cast<float4 *>(M + lane * LD + 36 + q) = make_float4(v2.x, v2.y, v3.x, v3.y);
         sync4<6>();
       }
-      if (c) wait(u_done + 1, c - 1);
+      if (g) wait(u_done + 1, g - 1);
 #pragma unroll 1
       for (int k = 0; k < 32; k += 8) {
         const int i = (at >> 6) * 32 + k;
@@ -543,7 +617,9 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       }
       fence_smem_to_async();
       arrive(t_ready);
-      arrive(&m_free[c % NM]);
+      arrive(&m_free[g % NM]);
+      step();
+    }
     }
   } else if (warp >= Z::W_LOAD) {
     // ---------------------------------------------------------------- rows of the chunks: one warp copies k and q, one v, one o
@@ -574,7 +650,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         const int k = (lane >> 3) * 8;
 #pragma unroll 1
         for (int q = 0; q < (out ? 2 : 1); ++q) {
-          const uint32_t to = base + Z::OX + (c % NB) * Z::XBUF + q * Z::ROWS + core_at(lane & 7, k, D);
+          const uint32_t to = base + Z::OX + at_x() * Z::XBUF + q * Z::ROWS + core_at(lane & 7, k, D);
           rows(q ? p.q : p.k, hk, c, lane & 7, 8, k * ES, [&](int r, const char *from, bool live) {
 #pragma unroll
             for (int g = 0; g < D / 32; ++g) {
@@ -597,33 +673,37 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       } else {
         constexpr int PIECES = D * ES / 16, PER = 32 / PIECES;             // of a row; rows at once
         static_assert(PIECES <= 32 && C % PER == 0, "rows of v");
-        const uint32_t to = base + Z::OV + (c % NV) * Z::VBUF + lane * 16;
+        const uint32_t to = base + Z::OV + (g % NV) * Z::VBUF + lane * 16;
         rows(p.v, h, c, lane / PIECES, PER, lane % PIECES * 16, [&](int r, const char *from, bool live) { cp16(to + r * D * ES, from, live ? 16 : 0); });
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     };
-    if (what < 2) {
-      // v's buffer is free when the outputs written over it have left
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
+    for (int k = 0; k < turns; ++k) {
+    if (!take(k)) continue;
+    if (what == 1 && !(unit[k].slot >> 31)) {            // the state, for the warps that will hold it
+      const char *from = reinterpret_cast<const char *>(p.S + ((long)unit[k].slot * p.H + h) * D * D);
+      for (int i = lane * 128; i < D * D * 4; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+    }
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      if (what < 2) {
+        // v's buffer is free when the outputs written over it have left
         if (what == 0) {
-          if (c >= NB) wait(&x_free[c % NB], c / NB - 1);
-        } else if (c >= NV) {
-          if (out) wait(&o_free[c % NV], c / NV - 1);
-          else wait(&x_free[(c - NV) % NB], (c - NV) / NB);   // (v has been read before u is formed)
+          if (g >= NB) wait(&x_free[at_x()], round_x() - 1);
+        } else if (g >= NV) {
+          if (out) wait(&o_free[g % NV], g / NV - 1);
+          else wait(&x_free[(g - NV) % NB], (g - NV) / NB);   // (v has been read before u is formed)
         }
         load(c);
         fence_smem_to_async();
-        arrive(what == 0 ? &x_full[c % NB] : &ready[c % 3]);
-      }
-    } else if (out) {
-      // (as many row copies by the bulk-copy unit, 256 bytes each, took 5300 cycles a chunk)
-      constexpr int PIECES = D * ES / 16, PER = 32 / PIECES;
-#pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        wait(o_ready, c);
+        arrive(what == 0 ? &x_full[at_x()] : &ready[g3()]);
+      } else if (out) {
+        // (as many row copies by the bulk-copy unit, 256 bytes each, took 5300 cycles a chunk)
+        constexpr int PIECES = D * ES / 16, PER = 32 / PIECES;
+        wait(o_ready, g);
         const int nt = tokens(c), first = lane / PIECES, piece = lane % PIECES;
-        const char *from = smem + Z::OV + (c % NV) * Z::VBUF + first * D * ES + piece * 16;
+        const char *from = smem + Z::OV + (g % NV) * Z::VBUF + first * D * ES + piece * 16;
         char *to = p.o.p + (b * p.o.sb + (long)(c * C + first) * p.o.st + h * p.o.sh) * ES + piece * 16;
         const long next = PER * p.o.st * ES;
         if (nt == C) {
@@ -634,8 +714,10 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
           for (int r = 0; r < C; r += PER, to += next)
             if (r + first < nt) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from + r * D * ES);
         }
-        arrive(&o_free[c % NV]);
+        arrive(&o_free[g % NV]);
       }
+      step();
+    }
     }
   } else {
     // ---------------------------------------------------------------- products. The warp runs as one, so that descriptors stay in uniform
@@ -664,13 +746,13 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     const uint64_t x_row = smem_desc(base + Z::OX, 128, SBO), x_col = smem_desc(base + Z::OX, SBO, 128);   // rows, and along their other dimension
     const uint64_t t_row = smem_desc(base + Z::OT, 128, 1024), p_row = smem_desc(base + Z::OP, 128, 1024);
     constexpr uint32_t XB = Z::XBUF >> 4, XP = Z::XPART >> 4, TP = Z::TPART >> 4;
-    auto dots = [&](int c) {                             // [k | q] k^T
-      wait(&x_full[c % NB], c / NB);
+    auto dots = [&](int np) {                            // [k | q] k^T of the chunk at this place
+      wait(&x_full[at_x()], round_x());
       if (!all_good()) return;
       fence_after_sync();
       if (leader) {
-        const uint32_t id = idesc_n(padded(c));
-        const uint64_t x = x_row + (c % NB) * XB;
+        const uint32_t id = idesc_n(np);
+        const uint64_t x = x_row + at_x() * XB;
         pairs(INX{}, INX{}, I2{}, 0, [&](int i, int k, uint32_t add) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) mma_ss(tmem + Z::D0, x + i * XP + kk * 16, x + k * XP + kk * 16, id, kk ? 1u : add);
@@ -678,13 +760,26 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         commit(g_done);
       }
     };
-    if (chunks) dots(0);
+    // tokens, padded, of the chunk after chunk c of unit k (c = chunks - 1: of the next unit that has any); 0: none
+    auto after = [&](int k, int c) {
+      if (c + 1 < chunks) return padded(c + 1);
+      for (++k; k < turns; ++k)
+        if (unit[k].n > 0) return (min(C, unit[k].n) + 15) & ~15;
+      return 0;
+    };
+    int np_next = after(-1, 0);
+    if (np_next) dots(np_next);
 #pragma unroll 1
-    for (int c = 0; c < chunks && good; ++c) {           // (without products from a wait on that gave up)
-      const int np = padded(c), steps = np / 16;
+    for (int k = 0; k < turns && good; ++k) {            // (without products from a wait on that gave up)
+    if (!take(k)) continue;
+#pragma unroll 1
+    for (int c = 0; c < chunks && good; ++c) {
+      const int now = g, np = np_next, steps = np / 16;
+      np_next = after(k, c);
       const uint32_t id = idesc_n(np);
-      const uint64_t x = x_row + (c % NB) * XB;
-      wait(a1, c);
+      const uint32_t buf = at_x();
+      const uint64_t x = x_row + buf * XB;
+      wait(a1, now);
       if (!all_good()) break;
       fence_after_sync();
       if (leader)
@@ -694,7 +789,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         });
       if (leader) commit(w_done);
       auto of_q = [&]() {                                // p (the last one has been read)
-        if (c) wait(o_read, c - 1);
+        if (now) wait(o_read, now - 1);
         if (!all_good()) return;
         fence_after_sync();
         if (leader) {
@@ -707,15 +802,16 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         }
       };
       if (F32 && out) of_q();
-      if (NB > 1 && c + 1 < chunks) {
-        wait(&ready[c % 3], c / 3);                      // (the last dot products have been read)
-        dots(c + 1);
+      if (NB > 1 && np_next) {
+        wait(&ready[g3()], r3());                      // (the last dot products have been read)
+        step();
+        dots(np_next);
       }
-      wait(t_ready, c);
+      wait(t_ready, now);
       // (columns t of step kk's tokens s >= 16 kk begin at t = 16 kk; the first two blocks of u need the first two of rhs)
 #pragma unroll 1
       for (int r = 0; r < 2; ++r) {
-        wait(a2 + r, c);
+        wait(a2 + r, now);
         if (!all_good()) break;
         fence_after_sync();
         if (leader) {
@@ -732,10 +828,10 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       }
       if (!F32 && out) of_q();
       if (p.write) {
-        const uint64_t xc = x_col + (c % NB) * XB;
+        const uint64_t xc = x_col + buf * XB;
 #pragma unroll 1
         for (int r = 0; r < 2; ++r) {
-          wait(a3 + r, c);
+          wait(a3 + r, now);
           if (!all_good()) break;
           fence_after_sync();
           if (leader)
@@ -747,13 +843,11 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
               }
             });
         }
-        if (leader) {
-          commit(s_done);
-          commit(&x_free[c % NB]);
-        }
+        if (leader) commit(s_done);
       }
+      if (leader) commit(&x_free[buf]);
       if (out) {
-        wait(a4, c);
+        wait(a4, now);
         if (!all_good()) break;
         fence_after_sync();
         if (leader) {
@@ -761,13 +855,15 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
 #pragma unroll
             for (int kk = 0; kk < C / 16; ++kk)
               if (kk < steps)
-                mma_ts(tmem + Z::D4 + 16 * kk, tmem + Z::a4(i) + 8 * kk, p_row + (c & 1) * NO * TP + k * TP + kk * ((2 * 1024 + 256) >> 4),
+                mma_ts(tmem + Z::D4 + 16 * kk, tmem + Z::a4(i) + 8 * kk, p_row + (now & 1) * NO * TP + k * TP + kk * ((2 * 1024 + 256) >> 4),
                        id - kk * (2u << 17), kk ? 1u : add);
           });
           commit(o_done);
         }
       }
-      if (NB == 1 && c + 1 < chunks) dots(c + 1);
+      if (NB == 1 || !np_next) step();
+      if (NB == 1 && np_next) dots(np_next);
+    }
     }
     if (leader) commit(drain);                           // every product has ended before the block frees its TMEM
     wait_long(drain, 0);
@@ -779,14 +875,22 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
   if (warp == Z::W_MMA) tmem_dealloc(*tmem_slot, 512);
 }
 
-template <int D, bool F32>
-cudaError_t launch_chunk(const DeltaArgs &p, cudaStream_t s) {
+template <int D, bool F32, bool ONE>
+cudaError_t launch_chunk(const DeltaArgs &p, long blocks, cudaStream_t s) {
   using Z = Shape<D, F32>;
-  const cudaError_t e = smem_opt_in<delta_chunk_kernel<D, F32>>(Z::SMEM);
+  const cudaError_t e = smem_opt_in<delta_chunk_kernel<D, F32, ONE>>(Z::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)(p.batch * p.H)), dim3(Z::THREADS), Z::SMEM, s, attr);
-  return cudaLaunchKernelEx(&cfg, delta_chunk_kernel<D, F32>, p);
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)blocks), dim3(Z::THREADS), Z::SMEM, s, attr);
+  return cudaLaunchKernelEx(&cfg, delta_chunk_kernel<D, F32, ONE>, p);
+}
+
+template <int D, bool F32>
+cudaError_t launch_chunk(DeltaArgs p, cudaStream_t s) {
+  const long units = (long)p.batch * p.H, most = p.n_keep && p.n_idx < p.n_tokens ? p.n_idx : p.n_tokens;
+  p.sms = device_sm_count();
+  if (units <= p.sms || most > CHUNKS_LASTING * C) return launch_chunk<D, F32, true>(p, units, s);
+  return launch_chunk<D, F32, false>(p, units > (long)p.sms * UNITS ? (units + UNITS - 1) / UNITS : p.sms, s);
 }
 
 }  // namespace delta

@@ -16,6 +16,7 @@ struct DeltaArgs {
   const int32_t *idx, *n_keep;   // kept paths
   int n_idx;
   int write;                // the states advance
+  int sms;                  // multiprocessors of the device
 };
 
 namespace pace {
@@ -34,14 +35,13 @@ __device__ __forceinline__ int count_of(const DeltaArgs &p, int i) {
   return p.n_keep ? min(max(p.n_keep[i], 0), min(p.n_idx, rows)) : rows;
 }
 
-// `first`: this block reports what is wrong with the sequence (one block of it does).
-__device__ __forceinline__ Seq sequence(const DeltaArgs &p, int b, bool first) {
+// The sequence by its own entries; bits of the status word that are wrong with it are added to `bad`.
+__device__ __forceinline__ Seq sequence(const DeltaArgs &p, int b, int &bad) {
   const int lane = threadIdx.x & 31;
   Seq s;
   s.slot = p.slots ? p.slots[b] : b;
   s.fresh = p.lens && p.lens[b] == 0;
   s.n = count_of(p, b);
-  int bad = 0;
   if (p.n_keep) {           // the path ends before an index that does not rise inside the drafts
     const int rows = p.n_new ? min(max(p.n_new[b], 0), p.n_tokens) : p.n_tokens;
     if (p.n_keep[b] != s.n) bad |= PACE_DELTA_BAD_KEEP;
@@ -56,17 +56,18 @@ __device__ __forceinline__ Seq sequence(const DeltaArgs &p, int b, bool first) {
       }
     }
   }
-  if (s.n > 0) {
-    bool wrong = s.slot < 0 || s.slot >= p.n_slots;
-    if (p.slots && p.write && !wrong)                    // the first of several sequences that would write a slot does
-      for (int i = lane; i < b; i += 32) wrong |= p.slots[i] == s.slot && count_of(p, i) > 0;
-    if (__any_sync(0xffffffffu, wrong)) {
-      bad |= PACE_DELTA_BAD_SLOT;
-      s.n = 0;
-    }
+  if (s.n > 0 && (s.slot < 0 || s.slot >= p.n_slots)) {
+    bad |= PACE_DELTA_BAD_SLOT;
+    s.n = 0;
   }
-  if (bad && first && lane == 0) atomicOr(p.status, bad);
   return s;
+}
+// Whether an earlier sequence of the call writes the same slot (the first of several does).
+__device__ __forceinline__ bool taken(const DeltaArgs &p, int b, int slot) {
+  if (!p.slots || !p.write) return false;
+  bool found = false;
+  for (int i = threadIdx.x & 31; i < b; i += 32) found |= p.slots[i] == slot && count_of(p, i) > 0;
+  return __any_sync(0xffffffffu, found);
 }
 
 // Row of the call's tensors that holds token t of sequence b.

@@ -58,7 +58,7 @@ __device__ __forceinline__ void store4(const KvTensor &x, long at, float4 y) {
 }
 
 template <int D, int COLS, bool F32>
-__global__ void __launch_bounds__(STEP_THREADS) delta_step_kernel(const DeltaArgs p) {
+__global__ void __launch_bounds__(STEP_THREADS, D * COLS == 128 * 128 ? 2 : 4) delta_step_kernel(const DeltaArgs p) {
   constexpr int CG = COLS / 4, RG = STEP_THREADS / CG, R = D / RG, WG = 32 / CG;   // column quads, row groups, rows a thread, row groups a warp
   constexpr int PARTS = D / COLS;
   static_assert(R >= 1 && R % 2 == 0 && WG >= 1, "rows come in pairs");
@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(STEP_THREADS) delta_step_kernel(const DeltaArg
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int part = blockIdx.x % PARTS, unit = blockIdx.x / PARTS, b = unit / p.H, h = unit - b * p.H;
-  const Seq s = sequence(p, b, part == 0 && h == 0 && warp == 0);
+  int bad = 0;
+  Seq s = sequence(p, b, bad);
   const int c = tid % CG, row0 = tid / CG * R, col = part * COLS + 4 * c;
   const bool out = p.o.p != nullptr;
   const int hk = h / p.group;
@@ -87,6 +88,12 @@ __global__ void __launch_bounds__(STEP_THREADS) delta_step_kernel(const DeltaArg
     S[r][0] = pk(x.x, x.y);
     S[r][1] = pk(x.z, x.w);
   }
+
+  if (s.n > 0 && taken(p, b, s.slot)) {                  // (looked at while the state is on its way)
+    bad |= PACE_DELTA_BAD_SLOT;
+    s.n = 0;
+  }
+  if (bad && part == 0 && h == 0 && tid == 0) atomicOr(p.status, bad);
 
   int turn = 0;
   // one token of the staged ones; `emit`: row of o that its output goes to (-1: none)
@@ -188,7 +195,10 @@ cudaError_t launch_step(const DeltaArgs &p, cudaStream_t s) {
 
 template <bool F32>
 cudaError_t launch_step_t(const DeltaArgs &p, cudaStream_t s) {
-  return p.d == 128 ? launch_step<128, 128, F32>(p, s) : launch_step<64, 64, F32>(p, s);
+  if (p.d == 64) return launch_step<64, 64, F32>(p, s);
+  // (a quarter of the columns a block while all of them fit the multiprocessors: 16 heads of one sequence 3.3 us, whole states 4.3; 128 heads 5.8 and 5.7)
+  if (p.batch * p.H * 4 <= device_sm_count()) return launch_step<128, 32, F32>(p, s);
+  return launch_step<128, 128, F32>(p, s);
 }
 
 }  // namespace delta

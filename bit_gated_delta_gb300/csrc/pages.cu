@@ -281,34 +281,44 @@ __global__ void __launch_bounds__(256) renumber_kernel(const PagesDev p, int32_t
 }
 
 // ---- copying ------------------------------------------------------------------------------------------------------------------
-constexpr int COPY_THREADS = 256, COPY_DEPTH = 8, COPY_PIECE = COPY_THREADS * COPY_DEPTH * 16;   // 32 KB a block and turn
+// A block copies a piece of a page a turn, eight 16-byte loads a thread under way, with the next piece's page numbers on their way
+// beside them. Pieces are equal parts of a page.
+constexpr int COPY_THREADS = 256, COPY_DEPTH = 8, COPY_ROW = COPY_THREADS * 16;
+
+__host__ __device__ inline int copy_pieces(long page_bytes) { return (int)((page_bytes + COPY_ROW * COPY_DEPTH - 1) / (COPY_ROW * COPY_DEPTH)); }
 
 __global__ void __launch_bounds__(COPY_THREADS) copy_kernel(char *pool, long page_bytes, int n_pages, int32_t *status,
                                                             const int32_t *src, const int32_t *dst, const int32_t *count, int max_n) {
   pdl_enter();
+  const int pieces = copy_pieces(page_bytes);
+  const long piece = (page_bytes + (long)pieces * COPY_ROW - 1) / ((long)pieces * COPY_ROW) * COPY_ROW;
   const int n = count ? min(max(*count, 0), max_n) : max_n;
-  const int pieces = (int)((page_bytes + COPY_PIECE - 1) / COPY_PIECE);
-  for (long w = blockIdx.x; w < (long)n * pieces; w += gridDim.x) {
-    const int i = (int)(w / pieces);
-    const long at = (w - (long)i * pieces) * COPY_PIECE + threadIdx.x * 16;
-    const int s = src[i], d = dst[i];
+  const long end = (long)n * pieces;
+  int s = 0, d = 0;
+  if (blockIdx.x < end) s = src[blockIdx.x / pieces], d = dst[blockIdx.x / pieces];
+  for (long w = blockIdx.x; w < end; w += gridDim.x) {
+    const long next = w + gridDim.x, first = (w % pieces) * piece;
+    int s1 = 0, d1 = 0;
+    if (next < end) s1 = src[next / pieces], d1 = dst[next / pieces];
     if (s < 0 || s >= n_pages || d < 0 || d >= n_pages) {
-      if (at == 0) atomicOr(status, PACE_KV_BAD_PAGE);
-      continue;
-    }
-    const char *from = pool + s * page_bytes;
-    char *to = pool + d * page_bytes;
-    uint4 v[COPY_DEPTH];
+      if (first == 0 && threadIdx.x == 0) atomicOr(status, PACE_KV_BAD_PAGE);
+    } else {
+      const long last = min(first + piece, page_bytes);
+      const char *from = pool + s * page_bytes;
+      char *to = pool + d * page_bytes;
+      uint4 v[COPY_DEPTH];
 #pragma unroll
-    for (int k = 0; k < COPY_DEPTH; ++k) {
-      const long x = at + (long)k * COPY_THREADS * 16;
-      if (x < page_bytes) v[k] = __ldcs(reinterpret_cast<const uint4 *>(from + x));
-    }
+      for (int k = 0; k < COPY_DEPTH; ++k) {
+        const long x = first + k * COPY_ROW + threadIdx.x * 16;
+        if (x < last) v[k] = __ldcs(reinterpret_cast<const uint4 *>(from + x));
+      }
 #pragma unroll
-    for (int k = 0; k < COPY_DEPTH; ++k) {
-      const long x = at + (long)k * COPY_THREADS * 16;
-      if (x < page_bytes) *reinterpret_cast<uint4 *>(to + x) = v[k];
+      for (int k = 0; k < COPY_DEPTH; ++k) {
+        const long x = first + k * COPY_ROW + threadIdx.x * 16;
+        if (x < last) __stcs(reinterpret_cast<uint4 *>(to + x), v[k]);
+      }
     }
+    s = s1, d = d1;
   }
 }
 
@@ -343,7 +353,7 @@ cudaError_t pace_launch_pages_compact(const PagesDev &p, int batch, int32_t *tab
 cudaError_t pace_launch_kv_copy_pages(char *pool, size_t page_bytes, int n_pages, int32_t *status, const int32_t *src,
                                       const int32_t *dst, const int32_t *n, int max_n, cudaStream_t s) {
   using namespace pace::pages;
-  const long pieces = (long)max_n * (long)((page_bytes + COPY_PIECE - 1) / COPY_PIECE);
+  const long pieces = (long)max_n * copy_pieces((long)page_bytes);
   const long most = 6L * pace::device_sm_count();
   return launch(copy_kernel, pieces < most ? pieces : most, COPY_THREADS, s, pool, (long)page_bytes, n_pages, status, src, dst, n, max_n);
 }

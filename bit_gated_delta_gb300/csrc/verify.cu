@@ -21,6 +21,7 @@ constexpr int NODES = PACE_VERIFY_MAX_NODES;
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int MAX_BLOCKS = 8;                            // of a cluster
 constexpr int UNROLL = 8;                                // tokens a lane has under way
+constexpr int SPAN = 32 * UNROLL, MARKS = 32;            // tokens of a step of a warp; prefixes that a warp keeps
 
 template <bool F32>
 __device__ __forceinline__ float prob(const char *row, long v) {
@@ -71,20 +72,31 @@ struct Walk {               // shared by the block
   Factor z[NODES];                                       // of the refusals at the node so far
   int refused[NODES];                                    // those drafts
   int64_t warp_sum[WARPS];
+  int64_t mark[WARPS][MARKS];                            // sums of a warp's groups of steps
   int64_t block_sum[2][MAX_BLOCKS];
   int node, kept, refusals, more;                        // where the walk is; whether it goes on after the sum
   double Z;
 };
 
-// R of token v at the walk's node.
+// R of the tokens v, v + 32, .. below hi at the walk's node, in units.
 template <bool F32, bool Q>
-__device__ __forceinline__ Rest rest_of(const Walk &w, const char *prow, const char *qrow, long v, int refusals) {
-  const float p = prob<F32>(prow, v);
-  if (!Q || refusals == 0) return Rest{p, 0.0f};
-  const float q = prob<F32>(qrow, v);
-  Rest x = first_rest(p, q);
-  for (int i = 1; i < refusals; ++i) x = next_rest(x, q, w.z[i]);
-  return x;
+__device__ __forceinline__ void step(const Walk &w, const char *prow, const char *qrow, int v, int hi, int refusals, uint32_t (&up)[UNROLL],
+                                     int (&down)[UNROLL]) {
+  float p[UNROLL], q[UNROLL];
+#pragma unroll
+  for (int k = 0; k < UNROLL; ++k) {
+    p[k] = v + 32 * k < hi ? prob<F32>(prow, v + 32 * k) : 0.0f;
+    q[k] = Q && refusals > 0 && v + 32 * k < hi ? prob<F32>(qrow, v + 32 * k) : 0.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < UNROLL; ++k) {
+    Rest x{p[k], 0.0f};
+    if (Q && refusals > 0) {
+      x = first_rest(p[k], q[k]);
+      for (int i = 1; i < refusals; ++i) x = next_rest(x, q[k], w.z[i]);
+    }
+    units(x, up[k], down[k]);
+  }
 }
 
 template <bool F32, bool Q>
@@ -127,6 +139,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int
   // this block's and warp's tokens
   const int per_block = (a.vocab + blocks - 1) / blocks, v0 = min(part * per_block, a.vocab), v1 = min(v0 + per_block, a.vocab);
   const int per_warp = ((v1 - v0 + WARPS - 1) / WARPS + 31) / 32 * 32, lo = min(v0 + warp * per_warp, v1), hi = min(lo + per_warp, v1);
+  const int group = max(1, (per_warp + MARKS * SPAN - 1) / (MARKS * SPAN));       // steps a mark covers
   int turn = 0;
   int64_t total = 0;
   bool whole = false;                                    // nothing was left: the node's own row counts
@@ -149,15 +162,23 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int
       while (i < n && !more) {
         tried = i;
         const int y = w.tok[i];
-        const double q = w.q[i];
         double R = w.p[i];                               // what the refusals before left of y
-        if (Q) {
-          for (int k = 0; k < refusals; ++k) R = fmax(R - q * ((double)w.z[k].hi + (double)w.z[k].lo), 0.0);
+        bool less;
+        if (Q && refusals == 0) {                        // (64 bits only where 32 leave it open: that pipe is slow)
+          const float x = w.u[i] * w.q[i], y32 = w.p[i];
+          less = x < y32;
+          if (!(fabsf(x - y32) > 1e-6f * y32)) less = (double)w.u[i] * (double)w.q[i] < R;
         } else {
-          for (int k = 0; k < refusals; ++k)
-            if (w.refused[k] == y) R = 0.0;
+          const double q = w.q[i];
+          if (Q) {
+            for (int k = 0; k < refusals; ++k) R = fmax(R - q * ((double)w.z[k].hi + (double)w.z[k].lo), 0.0);
+          } else {
+            for (int k = 0; k < refusals; ++k)
+              if (w.refused[k] == y) R = 0.0;
+          }
+          less = (double)w.u[i] * q * Z < R;
         }
-        const bool keep = y >= 0 && (double)w.u[i] * q * Z < R, refuse = y >= 0 && !keep;
+        const bool keep = y >= 0 && less, refuse = y >= 0 && !keep;
         __syncwarp();
         if (lane == 0) {
           if (keep) w.path[kept] = i;
@@ -182,38 +203,37 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int
     const int node = w.node, refusals = whole ? 0 : w.refusals;
     const bool more = !whole && w.more;
     const char *pr = prow(node), *qr = Q ? qrow(node) : nullptr;
+    // values of a step of SPAN tokens from v0 on, lane by lane within rows of 32
     int64_t sum = 0;
-    for (int v = lo + lane; v < hi; v += 32 * UNROLL) {
-      float p[UNROLL], q[UNROLL];
+    for (int g = 0; g < MARKS; ++g) {
+      const int g0 = lo + g * group * SPAN, g1 = min(g0 + group * SPAN, hi);
+      if (g0 >= hi) break;
+      int64_t part_sum = 0;
+      for (int v = g0; v < g1; v += SPAN) {
+        uint32_t h[UNROLL];
+        int l[UNROLL];
+        step<F32, Q>(w, pr, qr, v + lane, hi, refusals, h, l);
+        uint32_t up = 0;
+        int down = 0;
 #pragma unroll
-      for (int k = 0; k < UNROLL; ++k) {
-        p[k] = v + 32 * k < hi ? prob<F32>(pr, v + 32 * k) : 0.0f;
-        q[k] = Q && refusals > 0 && v + 32 * k < hi ? prob<F32>(qr, v + 32 * k) : 0.0f;
+        for (int k = 0; k < UNROLL; ++k) up += h[k], down += l[k];
+        part_sum += ((int64_t)up << 23) + down;
       }
-      uint32_t up = 0;
-      int down = 0;
 #pragma unroll
-      for (int k = 0; k < UNROLL; ++k) {
-        Rest x{p[k], 0.0f};
-        if (Q && refusals > 0) {
-          x = first_rest(p[k], q[k]);
-          for (int i = 1; i < refusals; ++i) x = next_rest(x, q[k], w.z[i]);
-        }
-        uint32_t h;
-        int l;
-        units(x, h, l);
-        up += h, down += l;
-      }
-      sum += ((int64_t)up << 23) + down;
+      for (int m = 16; m > 0; m >>= 1) part_sum += __shfl_xor_sync(0xffffffffu, part_sum, m);
+      sum += part_sum;
+      if (lane == 0) w.mark[warp][g] = part_sum;
     }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
     if (!Q && lane == 0)                                 // refused tokens count as zero (once each)
       for (int i = 0; i < refusals; ++i) {
         const int y = w.refused[i];
         bool again = y < lo || y >= hi;
         for (int k = 0; k < i && !again; ++k) again = w.refused[k] == y;
-        if (!again) sum -= to_units(Rest{prob<F32>(pr, y), 0.0f});
+        if (!again) {
+          const int64_t x = to_units(Rest{prob<F32>(pr, y), 0.0f});
+          sum -= x;
+          w.mark[warp][(y - lo) / (group * SPAN)] -= x;
+        }
       }
     if (lane == 0) w.warp_sum[warp] = sum;
     __syncthreads();
@@ -249,33 +269,35 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int
       for (int i = 0; i < warp; ++i) s += w.warp_sum[i];
       at -= s;
       if (at >= 0 && at < w.warp_sum[warp]) {
-        const int per = (hi - lo + 31) / 32, l0 = min(lo + lane * per, hi), l1 = min(l0 + per, hi);
-        auto value = [&](int v) {
-          if (!Q)
-            for (int i = 0; i < refusals; ++i)
-              if (w.refused[i] == v) return (int64_t)0;
-          return to_units(rest_of<F32, Q>(w, pr, qr, v, refusals));
-        };
-        int64_t mine = 0;
-#pragma unroll 4
-        for (int v = l0; v < l1; ++v) mine += value(v);
-        int64_t before = mine;
+        // the group of steps, the step, the row of 32, the lane
+        // (bounded for rows that change under the call, whose sums do not agree)
+        int g = 0;
+        while (g < MARKS - 1 && at >= w.mark[warp][g]) at -= w.mark[warp][g++];
+        int v = -1;
+        for (int v0 = lo + g * group * SPAN; v < 0 && v0 < hi; v0 += SPAN) {
+          uint32_t h[UNROLL];
+          int l[UNROLL];
+          step<F32, Q>(w, pr, qr, v0 + lane, hi, refusals, h, l);
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, before, m);
-          if (lane >= m) before += y;
-        }
-        before -= mine;
-        if (at >= before && at < before + mine) {
-          int64_t c = before;
-          int v = l0;
-          while (true) {
-            c += value(v);
-            if (c > at) break;
-            ++v;
+          for (int k = 0; k < UNROLL; ++k) {
+            int64_t mine = ((int64_t)h[k] << 23) + l[k];
+            if (!Q)
+              for (int i = 0; i < refusals; ++i)
+                if (w.refused[i] == v0 + 32 * k + lane) mine = 0;
+            int64_t upto = mine;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+              const int64_t y = __shfl_up_sync(0xffffffffu, upto, m);
+              if (lane >= m) upto += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, upto > at);
+            if (v < 0) {
+              if (past) v = v0 + 32 * k + __ffs(past) - 1;
+              else at -= __shfl_sync(0xffffffffu, upto, 31);
+            }
           }
-          a.next[b] = v;
         }
+        if (lane == 0) a.next[b] = v < 0 ? hi - 1 : v;
       }
     }
   }
