@@ -166,6 +166,12 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     }
     __syncthreads();
   }
+  auto zeros = [&](int b, int h, int n, int i, int step) {   // outputs past the sequence's tokens, by `step` threads
+    constexpr int PIECES = D * ES / 16;
+    char *o = p.o.p + (b * p.o.sb + h * p.o.sh) * ES;
+    for (long x = (long)n * PIECES + i; x < (long)p.n_tokens * PIECES; x += step)
+      *reinterpret_cast<uint4 *>(o + x / PIECES * p.o.st * ES + x % PIECES * 16) = make_uint4(0, 0, 0, 0);
+  };
   for (int k = warp; k < turns; k += Z::THREADS / 32) {
     const int u = ONE ? blockIdx.x : k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     if (u >= total) {
@@ -181,12 +187,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     }
     if (bad && h == 0 && lane == 0) atomicOr(p.status, bad);
     if (lane == 0) unit[k] = Unit{(uint32_t)(b * PACE_MAX_HEADS + h), s.n, (uint32_t)s.slot | (uint32_t)s.fresh << 31};
-    if (out) {                                           // rows past the sequence's tokens
-      constexpr int PIECES = D * ES / 16;
-      char *o = p.o.p + (b * p.o.sb + h * p.o.sh) * ES;
-      for (long i = (long)s.n * PIECES + lane; i < (long)p.n_tokens * PIECES; i += 32)
-        *reinterpret_cast<uint4 *>(o + i / PIECES * p.o.st * ES + i % PIECES * 16) = make_uint4(0, 0, 0, 0);
-    }
+    if (out && !ONE) zeros(b, h, s.n, lane, 32);
   }
   fence_before_sync();
   __syncthreads();
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         fence_after_sync();
         if (mine) {
           const char *at = smem + Z::OV + (g % NV) * Z::VBUF + j * ES + t0 * D * ES;
-#pragma unroll 1
+#pragma unroll (ONE ? 2 : 1)
           for (int e0 = 0; e0 < 16; e0 += 8, at += 8 * D * ES) {
             uint32_t w[8], x[3][4];
             tmem_ld8(tl + Z::W + t0 + e0, w);
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       fence_after_sync();
       if (p.write) {
         if (mine) {
-#pragma unroll 1
+#pragma unroll (ONE ? 2 : 1)
           for (int e0 = 0; e0 < 16; e0 += 8) {
             uint32_t u[8], x[3][4];
             tmem_ld8(tl + Z::D2 + t0 + e0, u);
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       for (int i = 0; i < HELD; ++i) to[i * D] = S[i];
     }
     }
+    if (ONE && out) zeros(unit[0].bh / PACE_MAX_HEADS, unit[0].bh % PACE_MAX_HEADS, unit[0].n, tid, Z::MAIN * 32);
   } else if (warp < Z::W_INV) {
     // ---------------------------------------------------------------- tables of the chunks
     const int at = tid - Z::W_TAB * 32, aw = warp - Z::W_TAB, t = at & 63;

@@ -11,7 +11,9 @@ namespace delta {
 
 constexpr int STEP_THREADS = 256, STEP_WARPS = STEP_THREADS / 32;
 constexpr int STEP_STAGE = 8;            // tokens staged at a time
-constexpr int STEP_MOST = 8;             // longer calls, and trees, go by chunks (delta_chunk.cuh)
+// The most tokens of a call that go one by one; longer ones, and trees, go by chunks (delta_chunk.cuh). Measured, heads of 128, us, bf16: 64
+// sequences and heads, 8 tokens 12 (by chunks 12), 1024: 8 tokens 57, 12 tokens 82 (56); fp32: 64 of 12 tokens 16 (18), 1024 of 12 90 (112).
+constexpr int step_most(int io) { return io == PACE_IO_F32 ? 14 : 8; }
 
 __device__ __forceinline__ uint64_t pk(float a, float b) {
   uint64_t r;
@@ -206,7 +208,8 @@ cudaError_t launch_step_t(const DeltaArgs &p, cudaStream_t s) {
 
 cudaError_t pace_launch_delta(const DeltaArgs &p, cudaStream_t s) {
   using namespace pace::delta;
-  const int most = p.idx ? (p.n_idx < p.n_tokens ? p.n_idx : p.n_tokens) : p.n_tokens;
-  if (p.mask || most > STEP_MOST) return p.io == PACE_IO_F32 ? pace_launch_delta_chunk_f32(p, s) : pace_launch_delta_chunk_bf16(p, s);
+  const int most = p.idx && p.n_idx < p.n_tokens ? p.n_idx : p.n_tokens;
+  if ((p.mask && p.n_tokens > 1) || most > step_most(p.io))
+    return p.io == PACE_IO_F32 ? pace_launch_delta_chunk_f32(p, s) : pace_launch_delta_chunk_bf16(p, s);
   return p.io == PACE_IO_F32 ? launch_step_t<true>(p, s) : launch_step_t<false>(p, s);
 }

@@ -66,9 +66,11 @@ def _fn(name):
     return getattr(lib(), name)
 
 
-@functools.lru_cache(maxsize=None)
+_DTYPES = {PACE_IO_BF16: torch.bfloat16, PACE_IO_F32: torch.float32}
+
+
 def _dtype(io):
-    return torch.float32 if io == PACE_IO_F32 else torch.bfloat16
+    return _DTYPES.get(io, torch.bfloat16)
 
 
 def _tensor(t, io, shape, name):
@@ -76,12 +78,19 @@ def _tensor(t, io, shape, name):
     if t is None:
         return None
     st = t.stride()
-    if t.dtype is not _dtype(io) or t.get_device() != _device() or t.shape != shape or (st[-1] != 1 and shape[-1] > 1 and t.numel()):
+    if t.dtype is not _DTYPES.get(io, torch.bfloat16) or t.get_device() != _device() or t.shape != shape or (
+            st[-1] != 1 and shape[-1] > 1 and t.numel()):
         raise ValueError(f"{name}: expected a {_dtype(io)} tensor on the current CUDA device, of shape {tuple(shape)} with its last "
                          f"dimension contiguous, got {t.dtype} on {t.device}, shape {tuple(t.shape)}, strides {st}")
-    if 1 in shape:                       # the stride of a single element is anything
-        st = [0 if n == 1 else x for n, x in zip(shape, st)]
-    return pace_tensor(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+    if len(st) == 4:
+        b, s, h, _ = st
+        if (b | s | h) & 7 and 1 in shape:   # the stride of a single element is anything
+            b, s, h = (0 if n == 1 else x for n, x in zip(shape, (b, s, h)))
+        return pace_tensor(t.data_ptr(), b, s, h)
+    s, h, _ = st
+    if (s | h) & 7 and 1 in shape:
+        s, h = (0 if n == 1 else x for n, x in zip(shape, (s, h)))
+    return pace_tensor(t.data_ptr(), 0, s, h)
 
 
 def _ints(t, shape, name, optional=False):
@@ -244,6 +253,7 @@ class PaceKV:
         self.mem, self._on = self._memory.tensor, self._memory.on
         base = (self.mem.data_ptr() + 255) // 256 * 256
         self.handle = pace_kv_alloc(cfg, base, self.nbytes, self._on(stream))
+        self._pages = None
 
     def append(self, q, k, v, lens, table, rope=None, positions=None, n_new=None, q_out=None, stream=None):
         pace_kv_append(self.handle, self.cfg, q, k, v, lens, table, rope, positions, n_new, q_out, self._on(stream))
@@ -264,9 +274,11 @@ class PaceKV:
 
     def pages(self):
         """The cache's pages as a uint8 view [n_pages, bytes of a page]."""
-        at, size = pace_kv_pool(self.handle)
-        off = at - self.mem.data_ptr()
-        return self.mem[off:off + self.cfg.n_pages * size].view(self.cfg.n_pages, size)
+        if self._pages is None:
+            at, size = pace_kv_pool(self.handle)
+            off = at - self.mem.data_ptr()
+            self._pages = self.mem[off:off + self.cfg.n_pages * size].view(self.cfg.n_pages, size)
+        return self._pages
 
     def status(self, clear: bool = False, stream=None) -> int:
         return pace_kv_get_status(self.handle, clear, self._on(stream))
