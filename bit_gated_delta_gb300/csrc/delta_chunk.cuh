@@ -49,7 +49,7 @@ struct Shape {
   static constexpr int MAIN = 16, AUX = 4, W_TAB = MAIN, W_INV = W_TAB + AUX, W_MMA = W_INV + AUX, W_LOAD = W_MMA + 1, THREADS = (W_LOAD + 3) * 32;
   static constexpr int NX = F32 ? 3 : 1;                 // parts of q and k
   static constexpr int NO = F32 ? 3 : 2;                 // parts of u and P in the outputs
-  static constexpr int NB = F32 ? 1 : 3, NV = F32 ? 1 : 2;   // chunks of rows of q and k, and of v, in shared memory
+  static constexpr int NB = !F32 ? 3 : D == 64 ? 2 : 1, NV = F32 && D == 128 ? 1 : 2;   // chunks of rows of q and k, and of v, in shared memory
   static constexpr int NM = F32 ? 1 : 2;                 // chunks of M
   static constexpr int NS = F32 ? 3 : 2;                 // parts of the state in w and p
   static constexpr int HELD = D / 4;                     // rows of the state that a thread holds
@@ -211,9 +211,8 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
   // tokens of a chunk, and as the products count them
   auto tokens = [&](int c) { return min(C, n - c * C); };
   auto padded = [&](int c) { return (tokens(c) + 15) & ~15; };
-  static_assert(NB == 3 || NB == 1, "rings");
-  auto at_x = [&]() { return NB == 3 ? g3() : 0; };
-  auto round_x = [&]() { return NB == 3 ? r3() : g; };
+  auto at_x = [&]() { return NB == 3 ? g3() : g % NB; };
+  auto round_x = [&]() { return NB == 3 ? r3() : g / NB; };
 
   bool good = true;
   auto wait = [&](uint64_t *x, int phase) {              // (by the whole warp)
