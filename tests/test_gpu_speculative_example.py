@@ -1,0 +1,46 @@
+"""The speculative example runs, keeps its books, and samples as the target does when its drafts are as good as none."""
+import os
+import sys
+
+import pytest
+
+from pace_testlib import ensure_built
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def E():
+    ensure_built()
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import speculative_sampling
+    return speculative_sampling
+
+
+def test_example_runs(E):
+    server, out, mean, held = E.main(steps=10)
+    assert server.status() == [0, 0, 0, 0]
+    assert all(len(o) >= 10 and all(0 <= t < server.vocab for t in o) for o in out)
+    assert 1 <= mean <= 5                                    # (a path of four drafts and the next token)
+    lens = server.lens.tolist()
+    assert [n > 0 for n in lens] == [True, False, False, False, True, False, False, False]
+    assert held == sum(-(-n // E.PAGE) for n in lens) == int((server.table >= 0).sum())
+
+
+def test_samples_that_share_pages_do_not_touch_one_another(E):
+    """Two rows forked from one prompt go on with different tokens: each holds what a row of its own would."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(2)
+    prompt = torch.randint(0, 512, (90,), generator=g, device="cuda").tolist()
+    forked, alone = E.Server(["delta", "attend"], 2, 512), E.Server(["delta", "attend"], 2, 512)
+    forked.prompt([prompt, []])
+    forked.fork([0, 0])
+    alone.prompt([prompt, prompt])
+    more = torch.randint(0, 512, (2, 12), generator=g, device="cuda", dtype=torch.int32)
+    n = torch.full((2,), 12, dtype=torch.int32, device="cuda")
+    for s in (forked, alone):
+        s.take(n)
+    a, b = forked.forward(more, n), alone.forward(more, n)
+    assert torch.equal(a, b)
+    assert torch.equal(forked.layers[0][1].states, alone.layers[0][1].states)
