@@ -341,3 +341,124 @@ def test_refusals(P):
     with pytest.raises(P.PaceError, match="16-byte"):
         D.chunk(q, k, odd, a, beta, o)
     assert D.status() == 0
+
+
+@pytest.mark.parametrize("n", [3, 40, 130])
+def test_outputs_into_part_of_a_tensor(P, n):
+    """o is a view with gaps: what lies between its rows stays as it was."""
+    import torch
+    B, H, d = 3, 2, 64
+    for io in (0, 1):
+        x = inputs(torch, B, n, H, H, d, io, 6)
+        D, E = make(P, torch, H, H, d, io, B), make(P, torch, H, H, d, io, B)
+        want = torch.empty_like(x[2])
+        counts = ints(torch, [n, n // 2, 0])
+        D.chunk(*x, want, n_new=counts)
+        wide = torch.full((B + 1, n + 2, H + 1, d + 16), 9.0, dtype=x[2].dtype, device="cuda")
+        o = wide[1:, 1:1 + n, :H, 8:8 + d]
+        E.chunk(*x, o, n_new=counts)
+        assert torch.equal(o, want) and torch.equal(D.states, E.states)
+        o.fill_(9.0)
+        assert (wide == 9.0).all()
+
+
+@pytest.mark.parametrize("n", [2, 30, 100])
+def test_what_is_not_finite_stays_with_its_sequence_and_head(P, n):
+    """More sequences and heads than multiprocessors, so that blocks go on from a spoiled one to the next."""
+    import torch
+    B, H, d = 40, 8, 64
+    x = inputs(torch, B, n, H, H, d, 0, 7)
+    good, bad = make(P, torch, H, H, d, 0, B), make(P, torch, H, H, d, 0, B)
+    want, got = torch.empty_like(x[2]), torch.empty_like(x[2])
+    good.chunk(*x, want)
+    x = [y.clone() for y in x]
+    spoiled = torch.zeros(B, H, dtype=torch.bool, device="cuda")
+    for b in range(0, B, 3):
+        spoiled[b, b % H] = True
+        x[b % 3][b, n - 1, b % H] = float("nan") if b % 2 else float("inf")
+        x[2][b, 0, b % H] = float("inf")
+    bad.chunk(*x, got)
+    keep = ~spoiled[:, None, :, None].expand(want.shape)
+    assert torch.equal(got[keep], want[keep]) and torch.equal(good.states[~spoiled], bad.states[~spoiled])
+    assert bad.status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 20, 70])
+def test_many_sequences_of_all_lengths(P, n):
+    """Sequences and heads of every length below n, more than the multiprocessors hold at once: the same bits as each sequence alone."""
+    import torch
+    B, H, d = 70, 6, 64
+    x = inputs(torch, B, n, H, 3, d, 0, 9)
+    count = np.random.default_rng(n).integers(0, n + 1, B)
+    D, E = make(P, torch, H, 3, d, 0, B), make(P, torch, H, 3, d, 0, B)
+    o = torch.empty_like(x[2])
+    D.chunk(*x, o, n_new=ints(torch, count))
+    for b in range(0, B, 7):
+        one = torch.empty_like(o[b:b + 1])
+        E.chunk(*(y[b:b + 1] for y in x), one, slots=ints(torch, [b]), n_new=ints(torch, count[b:b + 1]))
+        assert torch.equal(one, o[b:b + 1]) and torch.equal(E.states[b], D.states[b])
+    assert D.status() == E.status() == 0
+
+
+def test_slow_decays_over_a_long_prompt(P):
+    """Decays of 0.999 and more keep errors of hundreds of tokens. bf16 I/O by chunks forms w = S^T k from two parts of S: off by at most 2^-18 |S_j|
+    |k| = 2^-18 sqrt(d) rms, a token's share of which, beta k_i of it, enters the state; n random shares of k_i = 1 / sqrt(d) each come to
+    sqrt(n) 2^-18 rms, 2^-13.4 at n = 600 if none were undone by later tokens."""
+    import torch
+    n, d = 600, 128
+    x = inputs(torch, 1, n, 2, 1, d, 0, 3, a_lo=0.999)
+    D = make(P, torch, 2, 1, d, 0, 1)
+    S = f64(D.states)[0]
+    o = torch.empty_like(x[2])
+    D.chunk(*x, o)
+    q, k, v, a, beta = map(f64, x)
+    for h in range(2):
+        want, end = T.chunk(S[h], q[0, :, 0], k[0, :, 0], v[0, :, h], a[0, :, h], beta[0, :, h])
+        close(o[0, :, h], want, 2.0 ** -8, "outputs")
+        off = np.abs(f64(D.states)[0, h] - end).max() / np.sqrt((end ** 2).mean())
+        assert off < 2.0 ** -13, off
+
+
+def test_memory_waits_for_the_streams_that_use_it(P):
+    import torch
+    side = torch.cuda.Stream()
+    for make_one in (lambda: P.PaceDelta(P.make_delta_config(8, 64, 4)), lambda: P.PacePages(200000, 64, 8)):
+        one = make_one()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000_000)                  # (about 0.2 s)
+            if isinstance(one, P.PaceDelta):
+                x = torch.zeros(4, 1, 8, 64, dtype=torch.bfloat16, device="cuda")
+                gate = torch.ones(4, 1, 8, device="cuda")
+                one.chunk(x, x, x, gate, gate, torch.empty_like(x))
+            else:
+                one.compact(torch.full((8, 4), -1, dtype=torch.int32, device="cuda"))
+        at, size = one.mem.data_ptr(), one.mem.numel()
+        del one
+        other = torch.empty(size, dtype=torch.uint8, device="cuda")
+        busy = not side.query()
+        assert busy and other.data_ptr() != at
+        side.synchronize()
+
+
+def test_longest_offsets(P):
+    """A tensor whose last sequence lies past 2^32 bytes, and states past 2^32 bytes."""
+    import torch
+    H, d = 4, 128
+    D = P.PaceDelta(P.make_delta_config(H, d, 17000))                     # 4.5 GB
+    x = inputs(torch, 1, 70, H, H, d, 0, 5)
+    o, ref = torch.empty_like(x[2]), torch.empty_like(x[2])
+    wide = torch.empty(2, 1 << 31, dtype=torch.bfloat16, device="cuda")   # 8 GB: the second row begins 4 GB in
+    views = [wide[:, i * 40000:i * 40000 + 70 * H * d].view(2, 70, H, d) for i in range(3)]
+    for view, y in zip(views, x):
+        view.zero_()
+        view[1] = y[0]
+    out = wide[:, 200000:200000 + 70 * H * d].view(2, 70, H, d)
+    gates = [g.expand(2, -1, -1) for g in x[3:]]
+    D.chunk(*views, *gates, out, slots=ints(torch, [0, 16999]))
+    D.chunk(*x, ref, slots=ints(torch, [5]))
+    assert torch.equal(out[1], ref[0]) and torch.equal(D.states[16999], D.states[5])
+    D.states.zero_()
+    D.chunk(*(v[:, :1] for v in views), *(g[:, :1] for g in gates), out[:, :1], slots=ints(torch, [0, 16999]))
+    D.chunk(*(y[:, :1] for y in x), ref[:, :1], slots=ints(torch, [5]))
+    assert torch.equal(out[1, :1], ref[0, :1]) and torch.equal(D.states[16999], D.states[5])
