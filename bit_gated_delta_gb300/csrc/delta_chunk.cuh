@@ -14,7 +14,8 @@
 //   D3 = (R_C u) k^T      A = R_C u                                   B = the rows k again, read along the other dimension
 //   D4 = u P^T            A = u                                       B = P
 // fp32 operands are split into bf16 parts (x = hi + mid + lo, 24 bits), of whose products those above 2^-24 are formed, smallest first; q and k
-// of bf16 I/O enter as they are. bf16 I/O forms outputs from two parts (16 bits; o is rounded to 8). The state itself stays in fp32 registers
+// of bf16 I/O enter as they are. bf16 I/O forms D1 from two parts of the state (16 bits; states then differ from 64-bit ones by 3e-7 of their norm,
+// the plain fp32 form by 1.2e-7) and outputs from two of u and P (o is rounded to 8). The state itself stays in fp32 registers
 // and takes D3 by an ordinary addition: the tensor cores' additions cut off, which would add up over a long prompt.
 //
 // Roles: sixteen warps own the columns (four a quarter of TMEM's lanes: a block of 16 tokens and a quarter of the state's rows each), four form
@@ -105,8 +106,8 @@ __host__ __device__ constexpr uint32_t idesc(int N, int mn_major) {   // M = 128
 }
 __device__ __forceinline__ uint32_t idesc_n(int N) { return idesc(0, 0) | ((uint32_t)(N >> 3) << 17); }
 
-// (A wait that is not over at the first look, out of line: the roles' loops together should stay in the instruction cache. With everything
-// unrolled and in line, 92 KB of code, warps waited for instructions four cycles of each five.)
+// (A wait that is not over at the first look, out of line: the roles' loops together should stay in the instruction cache. Unrolled and
+// in line, with eight column warps, 3.9 of the 10.5 warps a scheduler counts an issued instruction waited for theirs; so 0.3 do.)
 static __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, 1000000000ull); }
 
 // y += m x for a pair of rows.
