@@ -423,22 +423,28 @@ def test_memory_waits_for_the_streams_that_use_it(P):
     import torch
     side = torch.cuda.Stream()
     for make_one in (lambda: P.PaceDelta(P.make_delta_config(8, 64, 4)), lambda: P.PacePages(200000, 64, 8)):
-        one = make_one()
-        torch.cuda.synchronize()
-        with torch.cuda.stream(side):
-            torch.cuda._sleep(400_000_000)                  # (about 0.2 s)
-            if isinstance(one, P.PaceDelta):
-                x = torch.zeros(4, 1, 8, 64, dtype=torch.bfloat16, device="cuda")
-                gate = torch.ones(4, 1, 8, device="cuda")
-                one.chunk(x, x, x, gate, gate, torch.empty_like(x))
-            else:
-                one.compact(torch.full((8, 4), -1, dtype=torch.int32, device="cuda"))
-        at, size = one.mem.data_ptr(), one.mem.numel()
-        del one
-        other = torch.empty(size, dtype=torch.uint8, device="cuda")
-        busy = not side.query()
-        assert busy and other.data_ptr() != at
-        side.synchronize()
+        for first in (True, False):                             # (a kernel's first launch loads it, which may wait for the stream)
+            one = make_one()
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                if not first:
+                    torch.cuda._sleep(400_000_000)              # (about 0.2 s)
+                if isinstance(one, P.PaceDelta):
+                    x = torch.zeros(4, 1, 8, 64, dtype=torch.bfloat16, device="cuda")
+                    gate = torch.ones(4, 1, 8, device="cuda")
+                    one.chunk(x, x, x, gate, gate, torch.empty_like(x))
+                else:
+                    one.compact(torch.full((8, 4), -1, dtype=torch.int32, device="cuda"))
+            if first:
+                torch.cuda._sleep(1000)
+                side.synchronize()
+                continue
+            at, size = one.mem.data_ptr(), one.mem.numel()
+            del one
+            other = torch.empty(size, dtype=torch.uint8, device="cuda")
+            busy = not side.query()
+            assert busy and other.data_ptr() != at
+            side.synchronize()
 
 
 def test_longest_offsets(P):
