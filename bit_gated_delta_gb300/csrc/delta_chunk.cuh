@@ -19,7 +19,7 @@
 // and takes D3 by an ordinary addition: the tensor cores' additions cut off, which would add up over a long prompt.
 //
 // Roles: sixteen warps own the columns (four a quarter of TMEM's lanes: a block of 16 tokens and a quarter of the state's rows each), four form
-// R, M and P, four T, one chunk ahead, three copy rows, one issues the products.
+// R, M and P (fp32 I/O: and split the rows of k and q), four T, one chunk ahead, three (two) copy rows, one issues the products.
 // Every wait is bounded; one that gives up sets the status word, after which the block goes on without waiting or products and leaves the state.
 #pragma once
 
@@ -47,7 +47,7 @@ constexpr int CHUNKS_LASTING = 4;
 
 template <int D, bool F32>
 struct Shape {
-  static constexpr int MAIN = 16, AUX = 4, W_TAB = MAIN, W_INV = W_TAB + AUX, W_MMA = W_INV + AUX, W_LOAD = W_MMA + 1, THREADS = (W_LOAD + 3) * 32;
+  static constexpr int MAIN = 16, AUX = 4, W_TAB = MAIN, W_INV = W_TAB + AUX, W_MMA = W_INV + AUX, W_LOAD = W_MMA + 1, LOAD = F32 ? 2 : 3, THREADS = (W_LOAD + LOAD) * 32;
   static constexpr int NX = F32 ? 3 : 1;                 // parts of q and k
   static constexpr int NO = F32 ? 3 : 2;                 // parts of u and P in the outputs
   static constexpr int NB = !F32 ? 3 : D == 64 ? 2 : 1, NV = F32 && D == 128 ? 1 : 2;   // chunks of rows of q and k, and of v, in shared memory
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < NB; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_free[i], 1);
+    for (int i = 0; i < NB; ++i) mbar_init(&x_full[i], F32 ? Z::AUX : 1), mbar_init(&x_free[i], 1);
     for (int i = 0; i < NV; ++i) mbar_init(&o_free[i], 1);
     for (int i = 0; i < NM; ++i) mbar_init(&m_ready[i], Z::AUX), mbar_init(&m_free[i], Z::AUX);
     for (int i = 0; i < 3; ++i) mbar_init(&ready[i], Z::AUX + 1);
@@ -223,6 +223,53 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
   auto arrive = [&](uint64_t *x) {
     __syncwarp();
     if (lane == 0) mbar_arrive(x);
+  };
+
+  // Copies `per` rows at a time: lane's row `first` and piece of it; `one` gets its address and whether the row exists.
+  auto rows = [&](const KvTensor &x, int head, int c, int first, int per, int piece, auto one) {
+    const int nt = tokens(c);
+    const long step = x.st * ES;
+    const char *base = x.p + (b * x.sb + head * x.sh) * ES + piece, *at = base + (c * C + first) * step;
+    const long next = per * step;
+    if (nt == C && !p.idx) {
+#pragma unroll 8
+      for (int r = 0; r < C; r += per, at += next) one(r, at, true);
+    } else {
+#pragma unroll 1
+      for (int r = 0; r < C; r += per, at += next) {
+        const bool live = r + first < nt;
+        const char *from = live ? at : x.p;
+        if (p.idx && live) from = base + row_of(p, b, c * C + r + first) * step;
+        one(r, from, live);
+      }
+    }
+  };
+  // k and q of a chunk into their buffer, by warp `part` of `PARTS`: eight lanes write one core of 8 rows
+  auto load_x = [&](int c, auto parts, int part) {
+    constexpr int PARTS = decltype(parts)::value;
+    const int k = (lane >> 3) * 8, first = part * 8;
+#pragma unroll 1
+    for (int q = 0; q < (out ? 2 : 1); ++q) {
+      const uint32_t to = smem_u32(smem) + Z::OX + at_x() * Z::XBUF + q * Z::ROWS + core_at(first + (lane & 7), k, D);
+      rows(q ? p.q : p.k, hk, c, first + (lane & 7), 8 * PARTS, k * ES, [&](int r, const char *from, bool live) {
+#pragma unroll
+        for (int g = 0; g < D / 32; ++g) {
+          const uint32_t dst = to + core_at(r, g * 32, D);
+          if (!F32) {
+            cp16(dst, from + g * 32 * ES, live ? 16 : 0);          // (a row that does not exist is not read)
+          } else {
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
+            if (live) x = reinterpret_cast<const float4 *>(from + g * 32 * ES)[0], y = reinterpret_cast<const float4 *>(from + g * 32 * ES)[1];
+            uint32_t w[3][4];
+            split<3>(x.x, x.y, &w[0][0], 4), split<3>(x.z, x.w, &w[0][1], 4), split<3>(y.x, y.y, &w[0][2], 4), split<3>(y.z, y.w, &w[0][3], 4);
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + i * Z::XPART), "r"(w[i][0]), "r"(w[i][1]), "r"(w[i][2]), "r"(w[i][3])
+                           : "memory");
+          }
+        }
+      });
+    }
   };
 
   if (warp < Z::MAIN) {
@@ -438,6 +485,18 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     fetch(0);
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
+      if (F32) {
+        // (rows of k and q in parts; 512 chains of 512 tokens, heads of 128: 383 us, with one warp for that 672)
+        if (g >= NB) wait(&x_free[at_x()], round_x() - 1);
+        load_x(c, std::integral_constant<int, Z::AUX>{}, aw);
+        fence_smem_to_async();
+        arrive(&x_full[at_x()]);
+        if (c + 1 < chunks && !p.idx && (c + 1) * C + t < n) {     // the next chunk's, on their way
+          const KvTensor &x = isq && out ? p.q : p.k;
+          const char *next = x.p + (b * x.sb + ((c + 1) * C + t) * x.st + hk * x.sh) * ES;
+          for (int i = 0; i < D * ES; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i));
+        }
+      }
       const int nt = tokens(c), np = padded(c);
       float *ga = reinterpret_cast<float *>(smem + Z::OG) + g3() * 4 * C, *beta = ga + C, *G = ga + 2 * C, *rho = ga + 3 * C;
       if (!isq) ga[t] = t < nt ? a_next : 1.0f, beta[t] = t < nt ? b_next : 0.0f;
@@ -624,54 +683,12 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     }
     }
   } else if (warp >= Z::W_LOAD) {
-    // ---------------------------------------------------------------- rows of the chunks: one warp copies k and q, one v, one o
-    const int what = warp - Z::W_LOAD;
+    // ---------------------------------------------------------------- rows of the chunks: one warp copies k and q (fp32: the tables' warps do), one v, one o
+    const int what = warp - Z::W_LOAD + 3 - Z::LOAD;
     const uint32_t base = smem_u32(smem);
-    // Copies `per` rows at a time: lane's row `first` and piece of it; `one` gets its address and whether the row exists.
-    auto rows = [&](const KvTensor &x, int head, int c, int first, int per, int piece, auto one) {
-      const int nt = tokens(c);
-      const long step = x.st * ES;
-      const char *base = x.p + (b * x.sb + head * x.sh) * ES + piece, *at = base + (c * C + first) * step;
-      const long next = per * step;
-      if (nt == C && !p.idx) {
-#pragma unroll 8
-        for (int r = 0; r < C; r += per, at += next) one(r, at, true);
-      } else {
-#pragma unroll 1
-        for (int r = 0; r < C; r += per, at += next) {
-          const bool live = r + first < nt;
-          const char *from = live ? at : x.p;
-          if (p.idx && live) from = base + row_of(p, b, c * C + r + first) * step;
-          one(r, from, live);
-        }
-      }
-    };
     auto load = [&](int c) {
       if (what == 0) {
-        // eight lanes write one core of 8 rows
-        const int k = (lane >> 3) * 8;
-#pragma unroll 1
-        for (int q = 0; q < (out ? 2 : 1); ++q) {
-          const uint32_t to = base + Z::OX + at_x() * Z::XBUF + q * Z::ROWS + core_at(lane & 7, k, D);
-          rows(q ? p.q : p.k, hk, c, lane & 7, 8, k * ES, [&](int r, const char *from, bool live) {
-#pragma unroll
-            for (int g = 0; g < D / 32; ++g) {
-              const uint32_t dst = to + core_at(r, g * 32, D);
-              if (!F32) {
-                cp16(dst, from + g * 32 * ES, live ? 16 : 0);      // (a row that does not exist is not read)
-              } else {
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
-                if (live) x = reinterpret_cast<const float4 *>(from + g * 32 * ES)[0], y = reinterpret_cast<const float4 *>(from + g * 32 * ES)[1];
-                uint32_t w[3][4];
-                split<3>(x.x, x.y, &w[0][0], 4), split<3>(x.z, x.w, &w[0][1], 4), split<3>(y.x, y.y, &w[0][2], 4), split<3>(y.z, y.w, &w[0][3], 4);
-#pragma unroll
-                for (int i = 0; i < NX; ++i)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + i * Z::XPART), "r"(w[i][0]), "r"(w[i][1]), "r"(w[i][2]), "r"(w[i][3])
-                               : "memory");
-              }
-            }
-          });
-        }
+        load_x(c, std::integral_constant<int, 1>{}, 0);
       } else {
         constexpr int PIECES = D * ES / 16, PER = 32 / PIECES;             // of a row; rows at once
         static_assert(PIECES <= 32 && C % PER == 0, "rows of v");
