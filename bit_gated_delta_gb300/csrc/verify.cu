@@ -103,6 +103,7 @@ template <bool F32, bool Q>
 __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int blocks) {
   __shared__ Walk w;
   cg::cluster_group cluster = cg::this_cluster();
+  if (blocks > 1) cluster.barrier_arrive();              // (a block has begun: others may write to its shared memory)
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / blocks, part = blockIdx.x - b * blocks;
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int
   const int group = max(1, (per_warp + MARKS * SPAN - 1) / (MARKS * SPAN));       // steps a mark covers
   int turn = 0;
   int64_t total = 0;
+  if (blocks > 1) cluster.barrier_wait();
   bool whole = false;                                    // nothing was left: the node's own row counts
   int tried = 0;                                         // drafts up to this one are settled (warp 0)
   while (n > 0) {
