@@ -2,6 +2,8 @@
 //
 // The bookkeeping calls move a few integers a row; what they cost is their chain of dependent loads and barriers, so each is one
 // launch (compaction two), with the loads that do not depend on one another issued together.
+#include <limits.h>
+
 #include "serve_internal.h"
 
 namespace pace {
@@ -107,14 +109,15 @@ __device__ __forceinline__ void load_refs(const PagesDev &p, int first, int (&r)
   }
 }
 
-// Thread b is row b. Shared last pages are counted in a hash table of pages (how many rows of the call write in it, and the first).
-constexpr int HASH = 2048;
+// Thread b is row b. Shared last pages are counted in a hash table of pages: how many rows of the call write in it, and the one with the most
+// tokens in it (of several the first). That one may keep it, whichever of the others the pool has no page for: it writes behind their tokens.
+constexpr int HASH = 2048, PAGE_TOKENS_MAX = 4096;
 __global__ void __launch_bounds__(ONE) take_kernel(const PagesDev p, int batch, int32_t *table, int cols, const int32_t *lens,
                                                    const int32_t *n_new, int32_t *fits) {
-  __shared__ int key[HASH], writers[HASH], lowest[HASH], warp_sum[32];
+  __shared__ int key[HASH], writers[HASH], keeper[HASH], warp_sum[32];
   pdl_enter();
   const int b = threadIdx.x;
-  for (int i = b; i < HASH; i += ONE) key[i] = -1, writers[i] = 0, lowest[i] = PACE_KV_MAX_BATCH;
+  for (int i = b; i < HASH; i += ONE) key[i] = -1, writers[i] = 0, keeper[i] = INT_MAX;
   int len = 0, n = 0;
   if (b < batch) {
     n = max(n_new[b], 0);
@@ -151,6 +154,7 @@ __global__ void __launch_bounds__(ONE) take_kernel(const PagesDev p, int batch, 
   __syncthreads();
   // who writes in a shared page
   const bool shared = on && inside && held > 1;
+  const int place = (PAGE_TOKENS_MAX - (inside ? len % p.page : 0)) * PACE_KV_MAX_BATCH + b;      // the keeper's is the lowest
   int at = 0;
   if (shared) {
     at = (int)(((unsigned)last * 2654435761u) >> 21);
@@ -160,10 +164,10 @@ __global__ void __launch_bounds__(ONE) take_kernel(const PagesDev p, int batch, 
       at = (at + 1) & (HASH - 1);
     }
     atomicAdd(&writers[at], 1);
-    atomicMin(&lowest[at], b);
+    atomicMin(&keeper[at], place);
   }
   __syncthreads();
-  const bool copy = shared && !(writers[at] == held && lowest[at] == b);
+  const bool copy = shared && !(writers[at] == held && keeper[at] == place);
   need += copy;
   int wanted;
   const int rank = block_prefix(need, warp_sum, wanted);

@@ -109,8 +109,9 @@ class Pages:
             if x is not None and self.refs[x] > 1:
                 writers.setdefault(int(x), []).append(b)
         for x, rows in writers.items():
+            keeper = max(rows, key=lambda b: (int(self.lens[b]) % self.page, -b))       # (writes behind every other holder's tokens)
             for b in rows:
-                if not (len(rows) == self.refs[x] and b == rows[0]):
+                if not (len(rows) == self.refs[x] and b == keeper):
                     copies[b] = True
                     wants[b].insert(0, self.cover(self.lens[b]) - 1)
         free = [x for x in range(self.n) if self.refs[x] == 0]

@@ -123,6 +123,21 @@ def test_a_full_pool_serves_rows_in_order(P):
     assert not x.want.refs.any()
 
 
+@pytest.mark.parametrize("lens,n_pages,fits", [([37, 41], 2, [0, 1]), ([41, 37], 2, [1, 0]), ([37, 41, 37, 63], 3, [1, 0, 0, 1]),
+                                               ([40, 40, 40], 2, [1, 0, 0]), ([37, 41, 39], 4, [1, 1, 1])])
+def test_the_longest_holder_keeps_a_page(P, lens, n_pages, fits):
+    """Rows that share their first two pages and end at different tokens of the second. However far the pool goes, no row's tokens lie where
+    another one may write."""
+    table = [[0, 1, -1]] * len(lens)
+    x = Both(P, n_pages, 32, table, lens, [len(lens), len(lens)] + [0] * (n_pages - 2))
+    got = x.take([1] * len(lens))
+    assert got.tolist() == fits
+    for b, n in enumerate(lens):
+        for o, m in enumerate(lens):
+            if o != b and got[b] and x.want.table[b][1] == x.want.table[o][1]:
+                assert n >= m, (b, o)
+
+
 def test_taken_pages_stay_until_the_row_is_shortened(P):
     x = filled(P, np.random.default_rng(1), 2, 6, 32, 20, [30, 10])
     x.take([100, 0])
