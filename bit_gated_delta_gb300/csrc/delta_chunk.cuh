@@ -60,7 +60,8 @@ struct Shape {
   static constexpr int TPART = C * C * 2;
   static constexpr int LD = C + 4, LY = 36;              // rows of the fp32 tables
   static constexpr int OX = 0, OV = OX + NB * XBUF, OT = OV + NV * VBUF, OP = OT + 3 * TPART, OM = OP + 2 * NO * TPART, OY = OM + NM * C * LD * 4,
-                       OG = OY + 32 * LY * 4, OBAR = OG + 3 * 4 * C * 4, NBAR = 2 * NB + NV + 2 * NM + 3 + 18, OMISC = OBAR + NBAR * 8, OUNIT = OMISC + 16, SMEM = OUNIT + UNITS * (int)sizeof(Unit);
+                       OG = OY + 32 * LY * 4, OBAR = OG + 3 * 4 * C * 4, NBAR = 2 * NB + NV + 2 * NM + 3 + 18, OMISC = OBAR + NBAR * 8,
+                       OUNIT = OMISC + 16, SMEM = OUNIT + UNITS * (int)sizeof(Unit);
   static_assert(SMEM <= 227 * 1024 && OBAR % 8 == 0, "shared memory");
   // TMEM columns. What lies over something else is written when the products that read that have ended: R_C u over rhs (whose halves are done as
   // those of u are), the state's increment over its parts, u over w; with fp32 I/O rhs over the state's third part, and so q's products before rhs.
@@ -128,9 +129,9 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
   extern __shared__ __align__(128) char smem[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + Z::OBAR);
   // (those of two: for the halves of a chunk's tokens)
-  uint64_t *x_full = bar, *x_free = x_full + NB, *o_free = x_free + NB, *m_ready = o_free + NV, *m_free = m_ready + NM, *ready = m_free + NM, *a1 = ready + 3, *a2 = a1 + 1, *a3 = a2 + 2, *a4 = a3 + 2,
-           *u_done = a4 + 1, *w_done = u_done + 2, *p_done = w_done + 1, *s_done = p_done + 1, *o_done = s_done + 1, *o_read = o_done + 1,
-           *o_ready = o_read + 1, *g_done = o_ready + 1, *t_ready = g_done + 1, *drain = t_ready + 1;
+  uint64_t *x_full = bar, *x_free = x_full + NB, *o_free = x_free + NB, *m_ready = o_free + NV, *m_free = m_ready + NM, *ready = m_free + NM,
+           *a1 = ready + 3, *a2 = a1 + 1, *a3 = a2 + 2, *a4 = a3 + 2, *u_done = a4 + 1, *w_done = u_done + 2, *p_done = w_done + 1,
+           *s_done = p_done + 1, *o_done = s_done + 1, *o_read = o_done + 1, *o_ready = o_read + 1, *g_done = o_ready + 1, *t_ready = g_done + 1, *drain = t_ready + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::OMISC);
   Unit *unit = reinterpret_cast<Unit *>(smem + Z::OUNIT);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -324,147 +325,147 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     float gC = 1.0f;
 #pragma unroll 1
     for (int k = 0; k < turns; ++k) {
-    if (!take(k)) continue;
-    auto state = [&]() {
-      const Unit u = unit[k];
-      return p.S + ((long)(u.slot & 0x7FFFFFFFu) * p.H + u.bh % PACE_MAX_HEADS) * D * D + (long)(grp * HELD) * D + j;
-    };
-    {
-      const float *from = state();
-      const bool held_before = on && !(unit[k].slot >> 31);
+      if (!take(k)) continue;
+      auto state = [&]() {
+        const Unit u = unit[k];
+        return p.S + ((long)(u.slot & 0x7FFFFFFFu) * p.H + u.bh % PACE_MAX_HEADS) * D * D + (long)(grp * HELD) * D + j;
+      };
+      {
+        const float *from = state();
+        const bool held_before = on && !(unit[k].slot >> 31);
 #pragma unroll
-      for (int i = 0; i < HELD; ++i) S[i] = held_before ? from[i * D] : 0.0f;
-    }
-    // (the end of a chunk is worked off in the next one's turn, between what that chunk's products wait for)
+        for (int i = 0; i < HELD; ++i) S[i] = held_before ? from[i * D] : 0.0f;
+      }
+      // (the end of a chunk is worked off in the next one's turn, between what that chunk's products wait for)
 #pragma unroll 1
-    for (int c = 0; c <= chunks; ++c) {
-      const float4 *ga = reinterpret_cast<const float4 *>(smem + Z::OG) + g3() * C, *beta = ga + C / 4, *G = ga + 2 * (C / 4), *rho = ga + 3 * (C / 4);
-      // ---- the state at the end of the chunk before (its increment lies over parts: all four warps read theirs before any writes)
-      if (c > 0 && p.write) {
-        wait(s_done, g - 1);
-        fence_after_sync();
-        if (on) {
-#pragma unroll
-          for (int i = 0; i < HELD; i += 16) {
-            uint32_t x[16];
-            tmem_ld16(tl + Z::D3 + grp * HELD + i, x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) S[i + e] = fmaf(gC, S[i + e], __uint_as_float(x[e]));
-          }
-          asm volatile("bar.sync %0, 128;" ::"r"(2 + (warp & 3)) : "memory");
-        }
-      }
-      if (c < chunks) {
-        // ---- its parts, as the first operand of w and p
-        if (on) {
-#pragma unroll
-          for (int i = 0; i < HELD; i += 16) {
-            uint32_t x[NS][8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) split<NS>(S[i + 2 * e], S[i + 2 * e + 1], &x[0][e], 8);
-#pragma unroll
-            for (int k = 0; k < NS; ++k) tmem_st8(tl + Z::a1(k) + (grp * HELD + i) / 2, x[k]);
-          }
-          tmem_wait_st();
-        }
-        fence_before_sync();
-        arrive(a1);
-      }
-      if (out && c > 0) {
-        read_outputs(c - 1);
-        if (NV == 1) store_outputs(c - 1);                 // (this chunk's rows of v come where they leave)
-      }
-      const bool mine = on && t0 < padded(c);            // (the products read no tokens past these)
-      if (c < chunks) {
-        // ---- rhs = beta (v - G w)
-        wait(&ready[g3()], r3());
-        wait(w_done, g);
-        if (F32 && out) wait(p_done, g);                   // (q's products read the part of S that rhs lies over)
-        fence_after_sync();
-        if (mine) {
-          const char *at = smem + Z::OV + (g % NV) * Z::VBUF + j * ES + t0 * D * ES;
-#pragma unroll (ONE ? 2 : 1)
-          for (int e0 = 0; e0 < 16; e0 += 8, at += 8 * D * ES) {
-            uint32_t w[8], x[3][4];
-            tmem_ld8(tl + Z::W + t0 + e0, w);
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[e] = F32 ? *reinterpret_cast<const float *>(at + e * D * ES)
-                         : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at + e * D * ES) << 16);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              const float4 g = G[(t0 + e0 + e) / 4], be = beta[(t0 + e0 + e) / 4];
-              const float y0 = be.x * fmaf(-g.x, __uint_as_float(w[e]), v[e]), y1 = be.y * fmaf(-g.y, __uint_as_float(w[e + 1]), v[e + 1]);
-              const float y2 = be.z * fmaf(-g.z, __uint_as_float(w[e + 2]), v[e + 2]), y3 = be.w * fmaf(-g.w, __uint_as_float(w[e + 3]), v[e + 3]);
-              split<3>(y0, y1, &x[0][e / 2], 4);
-              split<3>(y2, y3, &x[0][e / 2 + 1], 4);
-            }
-#pragma unroll
-            for (int k = 0; k < 3; ++k) tmem_st4(tl + Z::a2(k) + (t0 + e0) / 2, x[k]);
-          }
-          tmem_wait_st();
-        }
-        fence_before_sync();
-        arrive(a2 + half);
-      }
-      if (NV > 1 && out && c > 0) store_outputs(c - 1);
-      if (c == chunks) break;                            // (its place is the next unit's first chunk's)
-      gC = G[C / 4 - 1].w;
-      // ---- u, decayed to the chunk's end
-      wait(u_done + half, g);
-      fence_after_sync();
-      if (p.write) {
-        if (mine) {
-#pragma unroll (ONE ? 2 : 1)
-          for (int e0 = 0; e0 < 16; e0 += 8) {
-            uint32_t u[8], x[3][4];
-            tmem_ld8(tl + Z::D2 + t0 + e0, u);
-            const float4 g = rho[(t0 + e0) / 4], f = rho[(t0 + e0) / 4 + 1];
-            tmem_wait_ld();
-            split<3>(g.x * __uint_as_float(u[0]), g.y * __uint_as_float(u[1]), &x[0][0], 4);
-            split<3>(g.z * __uint_as_float(u[2]), g.w * __uint_as_float(u[3]), &x[0][1], 4);
-            split<3>(f.x * __uint_as_float(u[4]), f.y * __uint_as_float(u[5]), &x[0][2], 4);
-            split<3>(f.z * __uint_as_float(u[6]), f.w * __uint_as_float(u[7]), &x[0][3], 4);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) tmem_st4(tl + Z::a3(k) + (t0 + e0) / 2, x[k]);
-          }
-          tmem_wait_st();
-        }
-        fence_before_sync();
-        arrive(a3 + half);
-      }
-      // ---- u as it is (over w, which the other half's warps have read when their u is done)
-      if (out) {
-        if (half == 0) {
-          wait(u_done + 1, g);
+      for (int c = 0; c <= chunks; ++c) {
+        const float4 *ga = reinterpret_cast<const float4 *>(smem + Z::OG) + g3() * C, *beta = ga + C / 4, *G = ga + 2 * (C / 4), *rho = ga + 3 * (C / 4);
+        // ---- the state at the end of the chunk before (its increment lies over parts: all four warps read theirs before any writes)
+        if (c > 0 && p.write) {
+          wait(s_done, g - 1);
           fence_after_sync();
-        }
-        if (mine) {
-#pragma unroll 1
-          for (int e0 = 0; e0 < 16; e0 += 8) {
-            uint32_t u[8], x[NO][4];
-            tmem_ld8(tl + Z::D2 + t0 + e0, u);
-            tmem_wait_ld();
+          if (on) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split<NO>(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]), &x[0][e], 4);
+            for (int i = 0; i < HELD; i += 16) {
+              uint32_t x[16];
+              tmem_ld16(tl + Z::D3 + grp * HELD + i, x);
+              tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < NO; ++k) tmem_st4(tl + Z::a4(k) + (t0 + e0) / 2, x[k]);
+              for (int e = 0; e < 16; ++e) S[i + e] = fmaf(gC, S[i + e], __uint_as_float(x[e]));
+            }
+            asm volatile("bar.sync %0, 128;" ::"r"(2 + (warp & 3)) : "memory");
           }
-          tmem_wait_st();
         }
-        fence_before_sync();
-        arrive(a4);
-      }
-          step();
-    }
-    if (p.write && on && good) {
-      float *to = state();
+        if (c < chunks) {
+          // ---- its parts, as the first operand of w and p
+          if (on) {
 #pragma unroll
-      for (int i = 0; i < HELD; ++i) to[i * D] = S[i];
-    }
+            for (int i = 0; i < HELD; i += 16) {
+              uint32_t x[NS][8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) split<NS>(S[i + 2 * e], S[i + 2 * e + 1], &x[0][e], 8);
+#pragma unroll
+              for (int k = 0; k < NS; ++k) tmem_st8(tl + Z::a1(k) + (grp * HELD + i) / 2, x[k]);
+            }
+            tmem_wait_st();
+          }
+          fence_before_sync();
+          arrive(a1);
+        }
+        if (out && c > 0) {
+          read_outputs(c - 1);
+          if (NV == 1) store_outputs(c - 1);                 // (this chunk's rows of v come where they leave)
+        }
+        const bool mine = on && t0 < padded(c);            // (the products read no tokens past these)
+        if (c < chunks) {
+          // ---- rhs = beta (v - G w)
+          wait(&ready[g3()], r3());
+          wait(w_done, g);
+          if (F32 && out) wait(p_done, g);                   // (q's products read the part of S that rhs lies over)
+          fence_after_sync();
+          if (mine) {
+            const char *at = smem + Z::OV + (g % NV) * Z::VBUF + j * ES + t0 * D * ES;
+#pragma unroll (ONE ? 2 : 1)
+            for (int e0 = 0; e0 < 16; e0 += 8, at += 8 * D * ES) {
+              uint32_t w[8], x[3][4];
+              tmem_ld8(tl + Z::W + t0 + e0, w);
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[e] = F32 ? *reinterpret_cast<const float *>(at + e * D * ES)
+                           : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at + e * D * ES) << 16);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; e += 4) {
+                const float4 g = G[(t0 + e0 + e) / 4], be = beta[(t0 + e0 + e) / 4];
+                const float y0 = be.x * fmaf(-g.x, __uint_as_float(w[e]), v[e]), y1 = be.y * fmaf(-g.y, __uint_as_float(w[e + 1]), v[e + 1]);
+                const float y2 = be.z * fmaf(-g.z, __uint_as_float(w[e + 2]), v[e + 2]), y3 = be.w * fmaf(-g.w, __uint_as_float(w[e + 3]), v[e + 3]);
+                split<3>(y0, y1, &x[0][e / 2], 4);
+                split<3>(y2, y3, &x[0][e / 2 + 1], 4);
+              }
+#pragma unroll
+              for (int k = 0; k < 3; ++k) tmem_st4(tl + Z::a2(k) + (t0 + e0) / 2, x[k]);
+            }
+            tmem_wait_st();
+          }
+          fence_before_sync();
+          arrive(a2 + half);
+        }
+        if (NV > 1 && out && c > 0) store_outputs(c - 1);
+        if (c == chunks) break;                            // (its place is the next unit's first chunk's)
+        gC = G[C / 4 - 1].w;
+        // ---- u, decayed to the chunk's end
+        wait(u_done + half, g);
+        fence_after_sync();
+        if (p.write) {
+          if (mine) {
+#pragma unroll (ONE ? 2 : 1)
+            for (int e0 = 0; e0 < 16; e0 += 8) {
+              uint32_t u[8], x[3][4];
+              tmem_ld8(tl + Z::D2 + t0 + e0, u);
+              const float4 g = rho[(t0 + e0) / 4], f = rho[(t0 + e0) / 4 + 1];
+              tmem_wait_ld();
+              split<3>(g.x * __uint_as_float(u[0]), g.y * __uint_as_float(u[1]), &x[0][0], 4);
+              split<3>(g.z * __uint_as_float(u[2]), g.w * __uint_as_float(u[3]), &x[0][1], 4);
+              split<3>(f.x * __uint_as_float(u[4]), f.y * __uint_as_float(u[5]), &x[0][2], 4);
+              split<3>(f.z * __uint_as_float(u[6]), f.w * __uint_as_float(u[7]), &x[0][3], 4);
+#pragma unroll
+              for (int k = 0; k < 3; ++k) tmem_st4(tl + Z::a3(k) + (t0 + e0) / 2, x[k]);
+            }
+            tmem_wait_st();
+          }
+          fence_before_sync();
+          arrive(a3 + half);
+        }
+        // ---- u as it is (over w, which the other half's warps have read when their u is done)
+        if (out) {
+          if (half == 0) {
+            wait(u_done + 1, g);
+            fence_after_sync();
+          }
+          if (mine) {
+#pragma unroll 1
+            for (int e0 = 0; e0 < 16; e0 += 8) {
+              uint32_t u[8], x[NO][4];
+              tmem_ld8(tl + Z::D2 + t0 + e0, u);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 4; ++e) split<NO>(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]), &x[0][e], 4);
+#pragma unroll
+              for (int k = 0; k < NO; ++k) tmem_st4(tl + Z::a4(k) + (t0 + e0) / 2, x[k]);
+            }
+            tmem_wait_st();
+          }
+          fence_before_sync();
+          arrive(a4);
+        }
+        step();
+      }
+      if (p.write && on && good) {
+        float *to = state();
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) to[i * D] = S[i];
+      }
     }
     if (ONE && out) zeros(unit[0].bh / PACE_MAX_HEADS, unit[0].bh % PACE_MAX_HEADS, unit[0].n, tid, Z::MAIN * 32);
   } else if (warp < Z::W_INV) {
@@ -481,95 +482,95 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     };
 #pragma unroll 1
     for (int k = 0; k < turns; ++k) {
-    if (!take(k)) continue;
-    fetch(0);
+      if (!take(k)) continue;
+      fetch(0);
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      if (F32) {
-        // (rows of k and q in parts; 512 chains of 512 tokens, heads of 128: 383 us, with one warp for that 672)
-        if (g >= NB) wait(&x_free[at_x()], round_x() - 1);
-        load_x(c, std::integral_constant<int, Z::AUX>{}, aw);
+      for (int c = 0; c < chunks; ++c) {
+        if (F32) {
+          // (rows of k and q in parts; 512 chains of 512 tokens, heads of 128: 383 us, with one warp for that 672)
+          if (g >= NB) wait(&x_free[at_x()], round_x() - 1);
+          load_x(c, std::integral_constant<int, Z::AUX>{}, aw);
+          fence_smem_to_async();
+          arrive(&x_full[at_x()]);
+          if (c + 1 < chunks && !p.idx && (c + 1) * C + t < n) {     // the next chunk's, on their way
+            const KvTensor &x = isq && out ? p.q : p.k;
+            const char *next = x.p + (b * x.sb + ((c + 1) * C + t) * x.st + hk * x.sh) * ES;
+            for (int i = 0; i < D * ES; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i));
+          }
+        }
+        const int nt = tokens(c), np = padded(c);
+        float *ga = reinterpret_cast<float *>(smem + Z::OG) + g3() * 4 * C, *beta = ga + C, *G = ga + 2 * C, *rho = ga + 3 * C;
+        if (!isq) ga[t] = t < nt ? a_next : 1.0f, beta[t] = t < nt ? b_next : 0.0f;
+        fetch(c + 1);
+        uint32_t see[2] = {~0u, ~0u};                      // the token and its ancestors
+        if (p.mask) {
+          see[0] = see[1] = 0;
+          if (t < nt) {
+            const uint32_t *row = p.mask + ((long)b * p.n_tokens + t) * words;
+            see[0] = row[0];
+            if (words > 1) see[1] = row[1];
+          }
+        }
+        if (t < 32) see[0] = (see[0] | 1u << t) & ((2u << t) - 1), see[1] = 0;
+        else see[1] = (see[1] | 1u << (t - 32)) & ((2u << (t - 32)) - 1);
+        float *M = reinterpret_cast<float *>(smem + Z::OM) + (g % NM) * C * LD;
+        sync4<1>();
+        if (g >= NM) wait(&m_free[g % NM], g / NM - 1);
+        wait(g_done, g);                                   // (with it the output products of the chunk before the last are done)
+        fence_after_sync();
+        // ---- a row of R from its end, times the dot products: M (a row's entries in a column; rows of M carry beta) and P
+        float r = isq ? 1.0f : beta[t];
+#pragma unroll 1
+        for (int i0 = C - 16; i0 >= 0; i0 -= 16) {
+          uint32_t x[16];
+          if (i0 < np) {
+            tmem_ld16(tmem + ((uint32_t)(aw * 32) << 16) + Z::D0 + i0, x);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = 0;
+          }
+          const uint32_t bits = (i0 < 32 ? see[0] : see[1]) >> (i0 & 31);
+          float R[16];
+#pragma unroll
+          for (int e0 = 12; e0 >= 0; e0 -= 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(ga + i0 + e0);
+            const float as[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 3; e >= 0; --e) {
+              const bool anc = bits & (1u << (e0 + e));
+              R[e0 + e] = anc ? r : 0.0f;
+              r *= anc ? as[e] : 1.0f;
+            }
+          }
+          if (at == 2 * C - 1) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(rho + i0 + e) = make_float4(R[e], R[e + 1], R[e + 2], R[e + 3]);
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) R[e] *= __uint_as_float(x[e]);
+          if (!isq) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) M[(i0 + e) * LD + t] = R[e];
+          } else if (out) {
+            char *to = smem + Z::OP + (g & 1) * NO * Z::TPART + core_at(t, 0, C) + i0 * 16;
+#pragma unroll
+            for (int e0 = 0; e0 < 16; e0 += 8) {
+              uint32_t w[NO][4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) split<NO>(R[e0 + 2 * e], R[e0 + 2 * e + 1], &w[0][e], 4);
+#pragma unroll
+              for (int k = 0; k < NO; ++k) *reinterpret_cast<uint4 *>(to + k * Z::TPART + e0 * 16) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+            }
+          }
+        }
+        if (isq) G[t] = r;
         fence_smem_to_async();
-        arrive(&x_full[at_x()]);
-        if (c + 1 < chunks && !p.idx && (c + 1) * C + t < n) {     // the next chunk's, on their way
-          const KvTensor &x = isq && out ? p.q : p.k;
-          const char *next = x.p + (b * x.sb + ((c + 1) * C + t) * x.st + hk * x.sh) * ES;
-          for (int i = 0; i < D * ES; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i));
-        }
+        fence_before_sync();
+        arrive(&ready[g3()]);
+        arrive(&m_ready[g % NM]);
+        step();
       }
-      const int nt = tokens(c), np = padded(c);
-      float *ga = reinterpret_cast<float *>(smem + Z::OG) + g3() * 4 * C, *beta = ga + C, *G = ga + 2 * C, *rho = ga + 3 * C;
-      if (!isq) ga[t] = t < nt ? a_next : 1.0f, beta[t] = t < nt ? b_next : 0.0f;
-      fetch(c + 1);
-      uint32_t see[2] = {~0u, ~0u};                      // the token and its ancestors
-      if (p.mask) {
-        see[0] = see[1] = 0;
-        if (t < nt) {
-          const uint32_t *row = p.mask + ((long)b * p.n_tokens + t) * words;
-          see[0] = row[0];
-          if (words > 1) see[1] = row[1];
-        }
-      }
-      if (t < 32) see[0] = (see[0] | 1u << t) & ((2u << t) - 1), see[1] = 0;
-      else see[1] = (see[1] | 1u << (t - 32)) & ((2u << (t - 32)) - 1);
-      float *M = reinterpret_cast<float *>(smem + Z::OM) + (g % NM) * C * LD;
-      sync4<1>();
-      if (g >= NM) wait(&m_free[g % NM], g / NM - 1);
-      wait(g_done, g);                                   // (with it the output products of the chunk before the last are done)
-      fence_after_sync();
-      // ---- a row of R from its end, times the dot products: M (a row's entries in a column; rows of M carry beta) and P
-      float r = isq ? 1.0f : beta[t];
-#pragma unroll 1
-      for (int i0 = C - 16; i0 >= 0; i0 -= 16) {
-        uint32_t x[16];
-        if (i0 < np) {
-          tmem_ld16(tmem + ((uint32_t)(aw * 32) << 16) + Z::D0 + i0, x);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = 0;
-        }
-        const uint32_t bits = (i0 < 32 ? see[0] : see[1]) >> (i0 & 31);
-        float R[16];
-#pragma unroll
-        for (int e0 = 12; e0 >= 0; e0 -= 4) {
-          const float4 a = *reinterpret_cast<const float4 *>(ga + i0 + e0);
-          const float as[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-          for (int e = 3; e >= 0; --e) {
-            const bool anc = bits & (1u << (e0 + e));
-            R[e0 + e] = anc ? r : 0.0f;
-            r *= anc ? as[e] : 1.0f;
-          }
-        }
-        if (at == 2 * C - 1) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(rho + i0 + e) = make_float4(R[e], R[e + 1], R[e + 2], R[e + 3]);
-        }
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) R[e] *= __uint_as_float(x[e]);
-        if (!isq) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) M[(i0 + e) * LD + t] = R[e];
-        } else if (out) {
-          char *to = smem + Z::OP + (g & 1) * NO * Z::TPART + core_at(t, 0, C) + i0 * 16;
-#pragma unroll
-          for (int e0 = 0; e0 < 16; e0 += 8) {
-            uint32_t w[NO][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split<NO>(R[e0 + 2 * e], R[e0 + 2 * e + 1], &w[0][e], 4);
-#pragma unroll
-            for (int k = 0; k < NO; ++k) *reinterpret_cast<uint4 *>(to + k * Z::TPART + e0 * 16) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
-          }
-        }
-      }
-      if (isq) G[t] = r;
-      fence_smem_to_async();
-      fence_before_sync();
-      arrive(&ready[g3()]);
-      arrive(&m_ready[g % NM]);
-      step();
-    }
     }
   } else if (warp < Z::W_MMA) {
     // ---------------------------------------------------------------- inverses
@@ -577,110 +578,110 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     float *Y = reinterpret_cast<float *>(smem + Z::OY);
 #pragma unroll 1
     for (int k = 0; k < turns; ++k) {
-    if (!take(k)) continue;
+      if (!take(k)) continue;
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      const int np = padded(c);
-      float *M = reinterpret_cast<float *>(smem + Z::OM) + (g % NM) * C * LD;
-      wait(&m_ready[g % NM], g / NM);
-      // ---- T = (I + M)^-1 in M's place, by columns as M: blocks of 16 on the diagonal (a lane a column, whose later entries are brought up to
-      // date as each is known); then twice the block below two inverses, -T_b M_ba T_a
-      {
-        const int o16 = 16 * aw, col = lane & 15;
-        float *m = M + o16 * LD + o16;
-        float x[16];
+      for (int c = 0; c < chunks; ++c) {
+        const int np = padded(c);
+        float *M = reinterpret_cast<float *>(smem + Z::OM) + (g % NM) * C * LD;
+        wait(&m_ready[g % NM], g / NM);
+        // ---- T = (I + M)^-1 in M's place, by columns as M: blocks of 16 on the diagonal (a lane a column, whose later entries are brought up to
+        // date as each is known); then twice the block below two inverses, -T_b M_ba T_a
+        {
+          const int o16 = 16 * aw, col = lane & 15;
+          float *m = M + o16 * LD + o16;
+          float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.0f : 0.0f;
+          for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.0f : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 15; ++i) {
+          for (int i = 0; i < 15; ++i) {
 #pragma unroll
-          for (int k = (i + 1) & ~3; k < 16; k += 4) {
-            const float4 y = *reinterpret_cast<const float4 *>(m + i * LD + k);
-            if (k > i) x[k] = fmaf(-y.x, x[i], x[k]);
-            if (k + 1 > i) x[k + 1] = fmaf(-y.y, x[i], x[k + 1]);
-            if (k + 2 > i) x[k + 2] = fmaf(-y.z, x[i], x[k + 2]);
-            x[k + 3] = fmaf(-y.w, x[i], x[k + 3]);
+            for (int k = (i + 1) & ~3; k < 16; k += 4) {
+              const float4 y = *reinterpret_cast<const float4 *>(m + i * LD + k);
+              if (k > i) x[k] = fmaf(-y.x, x[i], x[k]);
+              if (k + 1 > i) x[k + 1] = fmaf(-y.y, x[i], x[k + 1]);
+              if (k + 2 > i) x[k + 2] = fmaf(-y.z, x[i], x[k + 2]);
+              x[k + 3] = fmaf(-y.w, x[i], x[k + 3]);
+            }
+          }
+          __syncwarp();
+          if (lane < 16) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(m + col * LD + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
           }
         }
-        __syncwarp();
-        if (lane < 16) {
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(m + col * LD + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-        }
-      }
-      sync4<6>();
-      // sums over i of row pairs m(i, rows) x(i)
-      if (np > 16) {
-        const int oa = (aw >> 1) * 32, ob = oa + 16, col = lane & 15, q = 4 * ((aw & 1) * 2 + (lane >> 4));
-        float *y = Y + (aw >> 1) * 16 * LY;
-        uint64_t s0 = 0, s1 = 0;
-#pragma unroll 8
-        for (int i = 0; i < 16; ++i) {
-          const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(M + (oa + i) * LD + ob + q);
-          const float x = M[(oa + col) * LD + oa + i];
-          fma_pair(s0, m.x, x), fma_pair(s1, m.y, x);
-        }
-        float2 v0 = pair(s0), v1 = pair(s1);
-        y[q * LY + col] = -v0.x, y[(q + 1) * LY + col] = -v0.y, y[(q + 2) * LY + col] = -v1.x, y[(q + 3) * LY + col] = -v1.y;
         sync4<6>();
-        s0 = s1 = 0;
+        // sums over i of row pairs m(i, rows) x(i)
+        if (np > 16) {
+          const int oa = (aw >> 1) * 32, ob = oa + 16, col = lane & 15, q = 4 * ((aw & 1) * 2 + (lane >> 4));
+          float *y = Y + (aw >> 1) * 16 * LY;
+          uint64_t s0 = 0, s1 = 0;
 #pragma unroll 8
-        for (int i = 0; i < 16; ++i) {
-          const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(M + (ob + i) * LD + ob + q);
-          const float x = y[i * LY + col];
-          fma_pair(s0, m.x, x), fma_pair(s1, m.y, x);
+          for (int i = 0; i < 16; ++i) {
+            const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(M + (oa + i) * LD + ob + q);
+            const float x = M[(oa + col) * LD + oa + i];
+            fma_pair(s0, m.x, x), fma_pair(s1, m.y, x);
+          }
+          float2 v0 = pair(s0), v1 = pair(s1);
+          y[q * LY + col] = -v0.x, y[(q + 1) * LY + col] = -v0.y, y[(q + 2) * LY + col] = -v1.x, y[(q + 3) * LY + col] = -v1.y;
+          sync4<6>();
+          s0 = s1 = 0;
+#pragma unroll 8
+          for (int i = 0; i < 16; ++i) {
+            const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(M + (ob + i) * LD + ob + q);
+            const float x = y[i * LY + col];
+            fma_pair(s0, m.x, x), fma_pair(s1, m.y, x);
+          }
+          v0 = pair(s0), v1 = pair(s1);
+          *reinterpret_cast<float4 *>(M + (oa + col) * LD + ob + q) = make_float4(v0.x, v0.y, v1.x, v1.y);
+          sync4<6>();
         }
-        v0 = pair(s0), v1 = pair(s1);
-        *reinterpret_cast<float4 *>(M + (oa + col) * LD + ob + q) = make_float4(v0.x, v0.y, v1.x, v1.y);
-        sync4<6>();
-      }
-      if (np > 32) {
-        const int q = 8 * aw;
-        uint64_t s[4] = {0, 0, 0, 0};
-        auto add = [&](const float *m, float x) {
-          const ulonglong2 m0 = *reinterpret_cast<const ulonglong2 *>(m), m1 = *reinterpret_cast<const ulonglong2 *>(m + 4);
-          fma_pair(s[0], m0.x, x), fma_pair(s[1], m0.y, x), fma_pair(s[2], m1.x, x), fma_pair(s[3], m1.y, x);
-        };
+        if (np > 32) {
+          const int q = 8 * aw;
+          uint64_t s[4] = {0, 0, 0, 0};
+          auto add = [&](const float *m, float x) {
+            const ulonglong2 m0 = *reinterpret_cast<const ulonglong2 *>(m), m1 = *reinterpret_cast<const ulonglong2 *>(m + 4);
+            fma_pair(s[0], m0.x, x), fma_pair(s[1], m0.y, x), fma_pair(s[2], m1.x, x), fma_pair(s[3], m1.y, x);
+          };
 #pragma unroll 1
-        for (int i0 = 0; i0 < 32; i0 += 8) {
-          const float4 x0 = *reinterpret_cast<const float4 *>(M + lane * LD + i0), x1 = *reinterpret_cast<const float4 *>(M + lane * LD + i0 + 4);
-          const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+          for (int i0 = 0; i0 < 32; i0 += 8) {
+            const float4 x0 = *reinterpret_cast<const float4 *>(M + lane * LD + i0), x1 = *reinterpret_cast<const float4 *>(M + lane * LD + i0 + 4);
+            const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) add(M + (i0 + i) * LD + 32 + q, x[i]);
-        }
+            for (int i = 0; i < 8; ++i) add(M + (i0 + i) * LD + 32 + q, x[i]);
+          }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = pair(s[i]);
-          Y[(q + 2 * i) * LY + lane] = -v.x, Y[(q + 2 * i + 1) * LY + lane] = -v.y;
-          s[i] = 0;
-        }
-        sync4<6>();
+          for (int i = 0; i < 4; ++i) {
+            const float2 v = pair(s[i]);
+            Y[(q + 2 * i) * LY + lane] = -v.x, Y[(q + 2 * i + 1) * LY + lane] = -v.y;
+            s[i] = 0;
+          }
+          sync4<6>();
 #pragma unroll 8
-        for (int i = 0; i < 32; ++i) add(M + (32 + i) * LD + 32 + q, Y[i * LY + lane]);
-        const float2 v0 = pair(s[0]), v1 = pair(s[1]), v2 = pair(s[2]), v3 = pair(s[3]);
-        *reinterpret_cast<float4 *>(M + lane * LD + 32 + q) = make_float4(v0.x, v0.y, v1.x, v1.y);
-        *reinterpret_cast<float4 *>(M + lane * LD + 36 + q) = make_float4(v2.x, v2.y, v3.x, v3.y);
-        sync4<6>();
-      }
-      if (g) wait(u_done + 1, g - 1);
+          for (int i = 0; i < 32; ++i) add(M + (32 + i) * LD + 32 + q, Y[i * LY + lane]);
+          const float2 v0 = pair(s[0]), v1 = pair(s[1]), v2 = pair(s[2]), v3 = pair(s[3]);
+          *reinterpret_cast<float4 *>(M + lane * LD + 32 + q) = make_float4(v0.x, v0.y, v1.x, v1.y);
+          *reinterpret_cast<float4 *>(M + lane * LD + 36 + q) = make_float4(v2.x, v2.y, v3.x, v3.y);
+          sync4<6>();
+        }
+        if (g) wait(u_done + 1, g - 1);
 #pragma unroll 1
-      for (int k = 0; k < 32; k += 8) {
-        const int i = (at >> 6) * 32 + k;
-        float x[8];
+        for (int k = 0; k < 32; k += 8) {
+          const int i = (at >> 6) * 32 + k;
+          float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = M[(i + e) * LD + t];
-        uint32_t w[3][4];
+          for (int e = 0; e < 8; ++e) x[e] = M[(i + e) * LD + t];
+          uint32_t w[3][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split<3>(x[2 * e], x[2 * e + 1], &w[0][e], 4);
-        char *to = smem + Z::OT + core_at(t, 0, C) + i * 16;
+          for (int e = 0; e < 4; ++e) split<3>(x[2 * e], x[2 * e + 1], &w[0][e], 4);
+          char *to = smem + Z::OT + core_at(t, 0, C) + i * 16;
 #pragma unroll
-        for (int e = 0; e < 3; ++e) *reinterpret_cast<uint4 *>(to + e * Z::TPART) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+          for (int e = 0; e < 3; ++e) *reinterpret_cast<uint4 *>(to + e * Z::TPART) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+        }
+        fence_smem_to_async();
+        arrive(t_ready);
+        arrive(&m_free[g % NM]);
+        step();
       }
-      fence_smem_to_async();
-      arrive(t_ready);
-      arrive(&m_free[g % NM]);
-      step();
-    }
     }
   } else if (warp >= Z::W_LOAD) {
     // ---------------------------------------------------------------- rows of the chunks: one warp copies k and q (fp32: the tables' warps do), one v, one o
@@ -699,44 +700,44 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     };
 #pragma unroll 1
     for (int k = 0; k < turns; ++k) {
-    if (!take(k)) continue;
-    if (what == 1 && !(unit[k].slot >> 31)) {            // the state, for the warps that will hold it
-      const char *from = reinterpret_cast<const char *>(p.S + ((long)unit[k].slot * p.H + h) * D * D);
-      for (int i = lane * 128; i < D * D * 4; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
-    }
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      if (what < 2) {
-        // v's buffer is free when the outputs written over it have left
-        if (what == 0) {
-          if (g >= NB) wait(&x_free[at_x()], round_x() - 1);
-        } else if (g >= NV) {
-          if (out) wait(&o_free[g % NV], g / NV - 1);
-          else wait(&x_free[(g - NV) % NB], (g - NV) / NB);   // (v has been read before u is formed)
-        }
-        load(c);
-        fence_smem_to_async();
-        arrive(what == 0 ? &x_full[at_x()] : &ready[g3()]);
-      } else if (out) {
-        // (as many row copies by the bulk-copy unit, 256 bytes each, took 5300 cycles a chunk)
-        constexpr int PIECES = D * ES / 16, PER = 32 / PIECES;
-        wait(o_ready, g);
-        const int nt = tokens(c), first = lane / PIECES, piece = lane % PIECES;
-        const char *from = smem + Z::OV + (g % NV) * Z::VBUF + first * D * ES + piece * 16;
-        char *to = p.o.p + (b * p.o.sb + (long)(c * C + first) * p.o.st + h * p.o.sh) * ES + piece * 16;
-        const long next = PER * p.o.st * ES;
-        if (nt == C) {
-#pragma unroll 8
-          for (int r = 0; r < C; r += PER, to += next) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from + r * D * ES);
-        } else {
-#pragma unroll 1
-          for (int r = 0; r < C; r += PER, to += next)
-            if (r + first < nt) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from + r * D * ES);
-        }
-        arrive(&o_free[g % NV]);
+      if (!take(k)) continue;
+      if (what == 1 && !(unit[k].slot >> 31)) {            // the state, for the warps that will hold it
+        const char *from = reinterpret_cast<const char *>(p.S + ((long)unit[k].slot * p.H + h) * D * D);
+        for (int i = lane * 128; i < D * D * 4; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
       }
-      step();
-    }
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        if (what < 2) {
+          // v's buffer is free when the outputs written over it have left
+          if (what == 0) {
+            if (g >= NB) wait(&x_free[at_x()], round_x() - 1);
+          } else if (g >= NV) {
+            if (out) wait(&o_free[g % NV], g / NV - 1);
+            else wait(&x_free[(g - NV) % NB], (g - NV) / NB);   // (v has been read before u is formed)
+          }
+          load(c);
+          fence_smem_to_async();
+          arrive(what == 0 ? &x_full[at_x()] : &ready[g3()]);
+        } else if (out) {
+          // (as many row copies by the bulk-copy unit, 256 bytes each, took 5300 cycles a chunk)
+          constexpr int PIECES = D * ES / 16, PER = 32 / PIECES;
+          wait(o_ready, g);
+          const int nt = tokens(c), first = lane / PIECES, piece = lane % PIECES;
+          const char *from = smem + Z::OV + (g % NV) * Z::VBUF + first * D * ES + piece * 16;
+          char *to = p.o.p + (b * p.o.sb + (long)(c * C + first) * p.o.st + h * p.o.sh) * ES + piece * 16;
+          const long next = PER * p.o.st * ES;
+          if (nt == C) {
+#pragma unroll 8
+            for (int r = 0; r < C; r += PER, to += next) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from + r * D * ES);
+          } else {
+#pragma unroll 1
+            for (int r = 0; r < C; r += PER, to += next)
+              if (r + first < nt) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from + r * D * ES);
+          }
+          arrive(&o_free[g % NV]);
+        }
+        step();
+      }
     }
   } else {
     // ---------------------------------------------------------------- products. The warp runs as one, so that descriptors stay in uniform
@@ -790,99 +791,99 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     if (np_next) dots(np_next);
 #pragma unroll 1
     for (int k = 0; k < turns && good; ++k) {            // (without products from a wait on that gave up)
-    if (!take(k)) continue;
+      if (!take(k)) continue;
 #pragma unroll 1
-    for (int c = 0; c < chunks && good; ++c) {
-      const int now = g, np = np_next, steps = np / 16;
-      np_next = after(k, c);
-      const uint32_t id = idesc_n(np);
-      const uint32_t buf = at_x();
-      const uint64_t x = x_row + buf * XB;
-      wait(a1, now);
-      if (!all_good()) break;
-      fence_after_sync();
-      if (leader)
-        pairs(INS{}, INX{}, IMS{}, 0, [&](int i, int k, uint32_t add) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) mma_ts(tmem + Z::W, tmem + Z::a1(i) + 8 * kk, x + k * XP + kk * 16, id, kk ? 1u : add);
-        });
-      if (leader) commit(w_done);
-      auto of_q = [&]() {                                // p (the last one has been read)
-        if (now) wait(o_read, now - 1);
-        if (!all_good()) return;
-        fence_after_sync();
-        if (leader) {
-          pairs(INS{}, INX{}, IMS{}, 0, [&](int i, int k, uint32_t add) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ts(tmem + Z::P, tmem + Z::a1(i) + 8 * kk, x + k * XP + (Z::ROWS >> 4) + kk * 16, id, kk ? 1u : add);
-          });
-          if (F32) commit(p_done);
-        }
-      };
-      if (F32 && out) of_q();
-      if (NB > 1 && np_next) {
-        wait(&ready[g3()], r3());                      // (the last dot products have been read)
-        step();
-        dots(np_next);
-      }
-      wait(t_ready, now);
-      // (columns t of step kk's tokens s >= 16 kk begin at t = 16 kk; the first two blocks of u need the first two of rhs)
-#pragma unroll 1
-      for (int r = 0; r < 2; ++r) {
-        wait(a2 + r, now);
+      for (int c = 0; c < chunks && good; ++c) {
+        const int now = g, np = np_next, steps = np / 16;
+        np_next = after(k, c);
+        const uint32_t id = idesc_n(np);
+        const uint32_t buf = at_x();
+        const uint64_t x = x_row + buf * XB;
+        wait(a1, now);
         if (!all_good()) break;
         fence_after_sync();
-        if (leader) {
-          pairs(I3{}, I3{}, I2{}, r, [&](int i, int k, uint32_t add) {
+        if (leader)
+          pairs(INS{}, INX{}, IMS{}, 0, [&](int i, int k, uint32_t add) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int kk = 2 * r + e;
-              if (kk < steps)
-                mma_ts(tmem + Z::D2 + 16 * kk, tmem + Z::a2(i) + 8 * kk, t_row + k * TP + kk * ((2 * 1024 + 256) >> 4), id - kk * (2u << 17), e ? 1u : add);
-            }
+            for (int kk = 0; kk < D / 16; ++kk) mma_ts(tmem + Z::W, tmem + Z::a1(i) + 8 * kk, x + k * XP + kk * 16, id, kk ? 1u : add);
           });
-          commit(u_done + r);
+        if (leader) commit(w_done);
+        auto of_q = [&]() {                                // p (the last one has been read)
+          if (now) wait(o_read, now - 1);
+          if (!all_good()) return;
+          fence_after_sync();
+          if (leader) {
+            pairs(INS{}, INX{}, IMS{}, 0, [&](int i, int k, uint32_t add) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ts(tmem + Z::P, tmem + Z::a1(i) + 8 * kk, x + k * XP + (Z::ROWS >> 4) + kk * 16, id, kk ? 1u : add);
+            });
+            if (F32) commit(p_done);
+          }
+        };
+        if (F32 && out) of_q();
+        if (NB > 1 && np_next) {
+          wait(&ready[g3()], r3());                      // (the last dot products have been read)
+          step();
+          dots(np_next);
         }
-      }
-      if (!F32 && out) of_q();
-      if (p.write) {
-        const uint64_t xc = x_col + buf * XB;
+        wait(t_ready, now);
+        // (columns t of step kk's tokens s >= 16 kk begin at t = 16 kk; the first two blocks of u need the first two of rhs)
 #pragma unroll 1
         for (int r = 0; r < 2; ++r) {
-          wait(a3 + r, now);
+          wait(a2 + r, now);
           if (!all_good()) break;
           fence_after_sync();
-          if (leader)
-            pairs(I3{}, INX{}, I2{}, r, [&](int i, int k, uint32_t add) {
+          if (leader) {
+            pairs(I3{}, I3{}, I2{}, r, [&](int i, int k, uint32_t add) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int kk = 2 * r + e;
-                if (kk < steps) mma_ts(tmem + Z::D3, tmem + Z::a3(i) + 8 * kk, xc + k * XP + kk * (2 * SBO >> 4), idesc(D, 1), e ? 1u : add);
+                if (kk < steps)
+                  mma_ts(tmem + Z::D2 + 16 * kk, tmem + Z::a2(i) + 8 * kk, t_row + k * TP + kk * ((2 * 1024 + 256) >> 4), id - kk * (2u << 17), e ? 1u : add);
               }
             });
+            commit(u_done + r);
+          }
         }
-        if (leader) commit(s_done);
-      }
-      if (leader) commit(&x_free[buf]);
-      if (out) {
-        wait(a4, now);
-        if (!all_good()) break;
-        fence_after_sync();
-        if (leader) {
-          pairs(INO{}, INO{}, IMO{}, 0, [&](int i, int k, uint32_t add) {
+        if (!F32 && out) of_q();
+        if (p.write) {
+          const uint64_t xc = x_col + buf * XB;
+#pragma unroll 1
+          for (int r = 0; r < 2; ++r) {
+            wait(a3 + r, now);
+            if (!all_good()) break;
+            fence_after_sync();
+            if (leader)
+              pairs(I3{}, INX{}, I2{}, r, [&](int i, int k, uint32_t add) {
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk)
-              if (kk < steps)
-                mma_ts(tmem + Z::D4 + 16 * kk, tmem + Z::a4(i) + 8 * kk, p_row + (now & 1) * NO * TP + k * TP + kk * ((2 * 1024 + 256) >> 4),
-                       id - kk * (2u << 17), kk ? 1u : add);
-          });
-          commit(o_done);
+                for (int e = 0; e < 2; ++e) {
+                  const int kk = 2 * r + e;
+                  if (kk < steps) mma_ts(tmem + Z::D3, tmem + Z::a3(i) + 8 * kk, xc + k * XP + kk * (2 * SBO >> 4), idesc(D, 1), e ? 1u : add);
+                }
+              });
+          }
+          if (leader) commit(s_done);
         }
+        if (leader) commit(&x_free[buf]);
+        if (out) {
+          wait(a4, now);
+          if (!all_good()) break;
+          fence_after_sync();
+          if (leader) {
+            pairs(INO{}, INO{}, IMO{}, 0, [&](int i, int k, uint32_t add) {
+#pragma unroll
+              for (int kk = 0; kk < C / 16; ++kk)
+                if (kk < steps)
+                  mma_ts(tmem + Z::D4 + 16 * kk, tmem + Z::a4(i) + 8 * kk, p_row + (now & 1) * NO * TP + k * TP + kk * ((2 * 1024 + 256) >> 4),
+                         id - kk * (2u << 17), kk ? 1u : add);
+            });
+            commit(o_done);
+          }
+        }
+        if (NB == 1 || !np_next) step();
+        if (NB == 1 && np_next) dots(np_next);
       }
-      if (NB == 1 || !np_next) step();
-      if (NB == 1 && np_next) dots(np_next);
-    }
     }
     if (leader) commit(drain);                           // every product has ended before the block frees its TMEM
     wait_long(drain, 0);
