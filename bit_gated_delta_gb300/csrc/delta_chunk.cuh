@@ -67,7 +67,8 @@ struct Shape {
                        OG = OY + 32 * LY * 4, OBAR = OG + 3 * 4 * C * 4, NBAR = 2 * NB + NV + 2 * NM + 3 + 18, OMISC = OBAR + NBAR * 8,
                        OUNIT = OMISC + 16, SMEM = OUNIT + UNITS * (int)sizeof(Unit);
   static_assert(SMEM <= 227 * 1024 && OBAR % 8 == 0, "shared memory");
-  // TMEM columns. What lies over something else is written when the products that read that have ended: R_C u over rhs (whose halves are done as
+  // TMEM columns. What lies over something else is written when the products that read that have ended, or by products issued when the warps
+  // that read it have said so (u over the outputs: o_read; tests/test_delta_order_host.py goes through all of them): R_C u over rhs (whose halves are done as
   // those of u are), the state's increment over its parts, u over w; with fp32 I/O rhs over the state's third part, and so q's products before rhs.
   static constexpr uint32_t W = 256, P = 320, D2 = 384, D4 = 384, D0 = 448, D3 = F32 ? 64 : 0;
   __host__ __device__ static constexpr uint32_t a1(int part) { return 64 * part; }
@@ -832,6 +833,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
           dots(np_next);
         }
         wait(t_ready, now);
+        if (!F32 && out && now) wait(o_read, now - 1);     // (u lies where the last outputs did; fp32: q's products have waited for that)
         // (columns t of step kk's tokens s >= 16 kk begin at t = 16 kk; the first two blocks of u need the first two of rhs)
 #pragma unroll 1
         for (int r = 0; r < 2; ++r) {
