@@ -64,7 +64,7 @@ struct Shape {
   static constexpr int TPART = C * C * 2;
   static constexpr int LD = C + 4, LY = 36;              // rows of the fp32 tables
   static constexpr int OX = 0, OV = OX + NB * XBUF, OT = OV + NV * VBUF, OP = OT + 3 * TPART, OM = OP + 2 * NO * TPART, OY = OM + NM * C * LD * 4,
-                       OG = OY + 32 * LY * 4, OBAR = OG + 3 * 4 * C * 4, NBAR = 2 * NB + NV + 2 * NM + 3 + 18, OMISC = OBAR + NBAR * 8,
+                       OG = OY + 32 * LY * 4, OBAR = OG + 3 * 4 * C * 4, NBAR = 2 * NB + 2 * NV + 2 * NM + 3 + 17, OMISC = OBAR + NBAR * 8,
                        OUNIT = OMISC + 16, SMEM = OUNIT + UNITS * (int)sizeof(Unit);
   static_assert(SMEM <= 227 * 1024 && OBAR % 8 == 0, "shared memory");
   // TMEM columns. What lies over something else is written when the products that read that have ended, or by products issued when the warps
@@ -134,9 +134,9 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
   extern __shared__ __align__(128) char smem[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + Z::OBAR);
   // (those of two: for the halves of a chunk's tokens)
-  uint64_t *x_full = bar, *x_free = x_full + NB, *o_free = x_free + NB, *m_ready = o_free + NV, *m_free = m_ready + NM, *ready = m_free + NM,
+  uint64_t *x_full = bar, *x_free = x_full + NB, *o_free = x_free + NB, *o_ready = o_free + NV, *m_ready = o_ready + NV, *m_free = m_ready + NM, *ready = m_free + NM,
            *a1 = ready + 3, *a2 = a1 + 1, *a3 = a2 + 2, *a4 = a3 + 2, *u_done = a4 + 1, *w_done = u_done + 2, *p_done = w_done + 1,
-           *s_done = p_done + 1, *o_done = s_done + 1, *o_read = o_done + 1, *o_ready = o_read + 1, *g_done = o_ready + 1, *t_ready = g_done + 1, *drain = t_ready + 1;
+           *s_done = p_done + 1, *o_done = s_done + 1, *o_read = o_done + 1, *g_done = o_read + 1, *t_ready = g_done + 1, *drain = t_ready + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::OMISC);
   Unit *unit = reinterpret_cast<Unit *>(smem + Z::OUNIT);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -148,10 +148,10 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
   }
   if (tid == 0) {
     for (int i = 0; i < NB; ++i) mbar_init(&x_full[i], F32 ? Z::AUX : 1), mbar_init(&x_free[i], 1);
-    for (int i = 0; i < NV; ++i) mbar_init(&o_free[i], 1);
+    for (int i = 0; i < NV; ++i) mbar_init(&o_free[i], 1), mbar_init(&o_ready[i], Z::MAIN);
     for (int i = 0; i < NM; ++i) mbar_init(&m_ready[i], Z::AUX), mbar_init(&m_free[i], Z::AUX);
     for (int i = 0; i < 3; ++i) mbar_init(&ready[i], Z::AUX + 1);
-    for (uint64_t *x : {a1, a4, o_read, o_ready}) mbar_init(x, Z::MAIN);
+    for (uint64_t *x : {a1, a4, o_read}) mbar_init(x, Z::MAIN);
     for (uint64_t *x : {a2, a2 + 1, a3, a3 + 1}) mbar_init(x, Z::MAIN / 2);
     for (uint64_t *x : {w_done, p_done, u_done, u_done + 1, s_done, o_done, g_done, drain}) mbar_init(x, 1);
     mbar_init(t_ready, Z::AUX);
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
           else *reinterpret_cast<uint16_t *>(to + e * D * ES) = (uint16_t)(held[e / 2] >> (e & 1) * 16);
         }
       }
-      arrive(o_ready);
+      arrive(&o_ready[(g - 1) % NV]);                    // (of this buffer: the next one's outputs may be there before these are looked for)
     };
     float gC = 1.0f;
 #pragma unroll 1
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         } else if (out) {
           // (as many row copies by the bulk-copy unit, 256 bytes each, took 5300 cycles a chunk)
           constexpr int PIECES = D * ES / 16, PER = 32 / PIECES;
-          wait(o_ready, g);
+          wait(&o_ready[g % NV], g / NV);
           const int nt = tokens(c), first = lane / PIECES, piece = lane % PIECES;
           const char *from = smem + Z::OV + (g % NV) * Z::VBUF + first * D * ES + piece * 16;
           char *to = p.o.p + (b * p.o.sb + (long)(c * C + first) * p.o.st + h * p.o.sh) * ES + piece * 16;

@@ -2,7 +2,9 @@
 memory and TMEM, its barriers and its products as a graph of what must come before what, for one sequence of several chunks, for blocks that go on
 from one sequence to the next, for each I/O type and head size, with and without outputs and new states.
 
-Two accesses that overlap, one of them a write, have to be joined by a path.
+* Two accesses that overlap, one of them a write, are joined by a path.
+* An arrival on a phase of a barrier comes after the phase before has ended, and a wait for a phase before the next one has ended: the parity that a
+  wait looks at tells two neighbouring phases apart, no more, and a wait that is overtaken runs out.
 
 `test_the_graph_is_that_of_the_source` holds the graph to the source: the waits, arrivals and commits of each role in their order, and where things
 lie in TMEM.
@@ -109,20 +111,30 @@ class Graph:
                 for m, w2, _, f2, l2 in list_[:i]:
                     if (w or w2) and f < l2 and f2 < l and not self.comes_before(n, m) and not self.comes_before(m, n):
                         found.add((where, max(f, f2), min(l, l2)))
+        for bar, own in self.arrivals.items():
+            for actor, at in own.items():
+                for other in own.values():
+                    assert len(other) == len(at), bar
+                    found |= {("arrival", bar) for i in range(1, len(at)) if not self.comes_before(other[i - 1], at[i])}
+        for n, bar, phase in self.waits:
+            own = self.arrivals[bar]
+            if len(next(iter(own.values()))) > phase + 1 and not any(self.comes_before(n, at[phase + 1]) for at in own.values()):
+                found.add(("overtaken", bar))
         return found
 
 
-def kernel(d, f32, out, write, units, waits_for_reads=True):
+def kernel(d, f32, out, write, units, waits_for_reads=True, ready_by_buffer=True):
     """The graph of a block that goes through units of so many chunks of 64 tokens each."""
     z, g_ = Shape(d, f32), Graph()
     tm = "tmem"
+    o_ready = (lambda g: (f"o_ready{g % z.NV}", g // z.NV)) if ready_by_buffer else (lambda g: ("o_ready", g))
 
     def columns(j):
         me, half, t0, held, g = f"columns{j}", j >> 1, 16 * j, z.d // 4, 0
 
         def store():
             g_.touch(me, "w", f"v{(g - 1) % z.NV}", t0, t0 + 16)
-            g_.arrive(me, "o_ready")
+            g_.arrive(me, o_ready(g - 1)[0])
         for chunks in units:
             for c in range(chunks + 1):
                 if c > 0 and write:
@@ -229,7 +241,7 @@ def kernel(d, f32, out, write, units, waits_for_reads=True):
             g_.touch("v", "w", f"v{g % z.NV}", 0, 64)
             g_.arrive("v", f"ready{g % 3}")
             if out:
-                g_.wait("o", "o_ready", g)
+                g_.wait("o", *o_ready(g))
                 g_.touch("o", "r", f"v{g % z.NV}", 0, 64)
                 g_.arrive("o", f"o_free{g % z.NV}")
 
@@ -302,6 +314,16 @@ def test_outputs_are_read_before_u_is_written_over_them(d):
         assert kernel(d, False, True, True, units, waits_for_reads=False).faults() == {("tmem", D4 + 32, D4 + 48), ("tmem", D4 + 48, D4 + 64)}
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_are_announced_by_buffer(d, f32):
+    """With one barrier for both buffers of outputs the columns' warps may announce chunk g + 1 (into the buffer that g - 1 has left) before the warp
+    that copies outputs has looked for chunk g; it would wait for g + 2, which waits for it."""
+    for units in ([4], [3, 1, 2, 1]):
+        found = kernel(d, f32, True, True, units, ready_by_buffer=False).faults()
+        assert found == (set() if Shape(d, f32).NV == 1 else {("overtaken", "o_ready")})
+
+
 def test_the_graph_is_that_of_the_source():
     text = re.sub(r"//[^\n]*", lambda m: m.group() if "-----" in m.group() else "", open(SOURCE).read())
     assert "W = 256, P = 320, D2 = 384, D4 = 384, D0 = 448, D3 = F32 ? 64 : 0;" in text
@@ -314,13 +336,13 @@ def test_the_graph_is_that_of_the_source():
     assert len(roles) == 5
     calls = re.compile(r"\b(wait|arrive|commit)\(([^;,]*)(?:, ([^;]*))?\);|(bar\.sync) %0|\b(sync4<\d>)\(\)")
     got = [[" ".join(filter(None, m.groups())) for m in calls.finditer(r)] for r in roles]
-    columns = ["wait o_done g - 1", "arrive o_read", "arrive o_ready", "wait s_done g - 1", "bar.sync", "arrive a1", "wait &ready[g3()] r3()", "wait w_done g",
+    columns = ["wait o_done g - 1", "arrive o_read", "arrive &o_ready[(g - 1) % NV]", "wait s_done g - 1", "bar.sync", "arrive a1", "wait &ready[g3()] r3()", "wait w_done g",
                "wait p_done g", "arrive a2 + half", "wait u_done + half g", "arrive a3 + half", "wait u_done + 1 g", "arrive a4"]
     tables = ["wait &x_free[at_x()] round_x() - 1", "arrive &x_full[at_x()]", "sync4<1>", "wait &m_free[g % NM] g / NM - 1", "wait g_done g",
               "arrive &ready[g3()]", "arrive &m_ready[g % NM]"]
     inverses = ["wait &m_ready[g % NM] g / NM"] + ["sync4<6>"] * 5 + ["wait u_done + 1 g - 1", "arrive t_ready", "arrive &m_free[g % NM]"]
     copies = ["wait &x_free[at_x()] round_x() - 1", "wait &o_free[g % NV] g / NV - 1", "wait &x_free[(g - NV) % NB] (g - NV) / NB",
-              "arrive what == 0 ? &x_full[at_x()] : &ready[g3()]", "wait o_ready g", "arrive &o_free[g % NV]"]
+              "arrive what == 0 ? &x_full[at_x()] : &ready[g3()]", "wait &o_ready[g % NV] g / NV", "arrive &o_free[g % NV]"]
     products = ["wait &x_full[at_x()] round_x()", "commit g_done", "wait a1 now", "commit w_done", "wait o_read now - 1", "commit p_done",
                 "wait &ready[g3()] r3()", "wait t_ready now", "wait o_read now - 1", "wait a2 + r now", "commit u_done + r", "wait a3 + r now",
                 "commit s_done", "commit &x_free[buf]", "wait a4 now", "commit o_done", "commit drain"]
