@@ -14,8 +14,8 @@
 //   D3 = (R_C u) k^T      A = R_C u                                   B = the rows k again, read along the other dimension
 //   D4 = u P^T            A = u                                       B = P
 // fp32 operands are split into bf16 parts (x = hi + mid + lo, 24 bits), of whose products those above 2^-24 are formed, smallest first; q and k
-// of bf16 I/O enter as they are. bf16 I/O forms D1 from two parts of the state (16 bits; states then differ from 64-bit ones by 3e-7 of their norm,
-// the plain fp32 form by 1.2e-7) and outputs from two of u and P (o is rounded to 8). The state itself stays in fp32 registers
+// of bf16 I/O enter as they are. bf16 I/O forms S^T q from two parts of the state and outputs from two of u and P (o is rounded to 8 bits); S^T k,
+// which comes back into the state, from three (two left up to 2.4e-6 of the states' norm where decays are slow). The state itself stays in fp32 registers
 // and takes D3 by an ordinary addition: the tensor cores' additions cut off, which would add up over a long prompt.
 //
 // Roles: sixteen warps own the columns (four a quarter of TMEM's lanes: a block of 16 tokens and a quarter of the state's rows each), four form
@@ -56,7 +56,7 @@ struct Shape {
   static constexpr int NO = F32 ? 3 : 2;                 // parts of u and P in the outputs
   static constexpr int NB = !F32 ? 3 : D == 64 ? 2 : 1, NV = F32 && D == 128 ? 1 : 2;   // chunks of rows of q and k, and of v, in shared memory
   static constexpr int NM = F32 ? 1 : 2;                 // chunks of M
-  static constexpr int NS = F32 ? 3 : 2;                 // parts of the state in w and p
+  static constexpr int NS = 3, NQ = F32 ? 3 : 2;         // parts of the state in w, and in p
   static constexpr int HELD = D / 4;                     // rows of the state that a thread holds
   static constexpr int ROWS = C * D * 2;                 // one part of 64 rows
   static constexpr int XPART = 2 * ROWS, XBUF = NX * XPART;
@@ -130,7 +130,7 @@ __device__ __forceinline__ float2 pair(uint64_t v) {
 template <int D, bool F32, bool ONE>
 __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(const DeltaArgs p) {
   using Z = Shape<D, F32>;
-  constexpr int NX = Z::NX, NO = Z::NO, NB = Z::NB, NV = Z::NV, NM = Z::NM, NS = Z::NS, LD = Z::LD, LY = Z::LY, ES = F32 ? 4 : 2;
+  constexpr int NX = Z::NX, NO = Z::NO, NB = Z::NB, NV = Z::NV, NM = Z::NM, NS = Z::NS, NQ = Z::NQ, LD = Z::LD, LY = Z::LY, ES = F32 ? 4 : 2;
   extern __shared__ __align__(128) char smem[];
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + Z::OBAR);
   // (those of two: for the halves of a chunk's tokens)
@@ -768,6 +768,8 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     using IMO = std::integral_constant<int, NO - 1>;
     using INS = std::integral_constant<int, NS>;
     using IMS = std::integral_constant<int, NS - 1>;
+    using INQ = std::integral_constant<int, NQ>;
+    using IMQ = std::integral_constant<int, NQ - 1>;
     const uint64_t x_row = smem_desc(base + Z::OX, 128, SBO), x_col = smem_desc(base + Z::OX, SBO, 128);   // rows, and along their other dimension
     const uint64_t t_row = smem_desc(base + Z::OT, 128, 1024), p_row = smem_desc(base + Z::OP, 128, 1024);
     constexpr uint32_t XB = Z::XBUF >> 4, XP = Z::XPART >> 4, TP = Z::TPART >> 4;
@@ -818,7 +820,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
           if (!all_good()) return;
           fence_after_sync();
           if (leader) {
-            pairs(INS{}, INX{}, IMS{}, 0, [&](int i, int k, uint32_t add) {
+            pairs(INQ{}, INX{}, IMQ{}, 0, [&](int i, int k, uint32_t add) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
                 mma_ts(tmem + Z::P, tmem + Z::a1(i) + 8 * kk, x + k * XP + (Z::ROWS >> 4) + kk * 16, id, kk ? 1u : add);

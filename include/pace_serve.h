@@ -67,8 +67,8 @@ void pace_delta_free(pace_delta *delta);
  * Advance the states by the new tokens (a prompt chunk of any length, or single tokens): o, and S_{n_b} into the slot. Rows of o at and
  * past n_b are zeros; a sequence without tokens keeps its slot as it is. q and o may both be NULL (states only). No two sequences
  * with tokens share a slot. One launch. A few tokens go one by one in fp32; more by chunks of 64 whose products are of fp32 values in
- * parts of 8 bits, three of each, but with bf16 tensors two (16 bits) of the states in S^T k and S^T q and of what forms o. States
- * then differ from those in 64 bits by about 3e-7 of their norm, more (2e-6) where the decays are nearer than 0.001 to 1. */
+ * parts of 8 bits, three of each, but with bf16 tensors two (16 bits) of the states in S^T q and of what forms o. States then differ
+ * from those in 64 bits by less than 1e-6 of their norm, whatever the decays. */
 pace_status pace_delta_chunk(pace_delta *delta, const pace_delta_step *step, const pace_tensor *q, const pace_tensor *k,
                              const pace_tensor *v, const pace_tensor *a, const pace_tensor *beta, const pace_tensor *o,
                              void *stream);

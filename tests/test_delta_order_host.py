@@ -23,7 +23,8 @@ class Shape:
     def __init__(self, d, f32):
         self.d, self.f32 = d, f32
         self.NB, self.NV = (3 if not f32 else 2 if d == 64 else 1), (1 if f32 and d == 128 else 2)
-        self.NM, self.NO, self.NS, self.D3 = (1, 3, 3, 64) if f32 else (2, 2, 2, 0)
+        self.NM, self.NO, self.NQ, self.D3 = (1, 3, 3, 64) if f32 else (2, 2, 2, 0)
+        self.NS = 3
 
     def a1(self, part):
         return 64 * part
@@ -257,7 +258,7 @@ def kernel(d, f32, out, write, units, waits_for_reads=True, ready_by_buffer=True
             def of_q():
                 if g:
                     g_.wait(me, "o_read", g - 1)
-                g_.product(part(z.a1, z.NS, 0, d // 2) + [(f"q{g % z.NB}", 0, 2)], [(tm, P_, P_ + 64)])
+                g_.product(part(z.a1, z.NQ, 0, d // 2) + [(f"q{g % z.NB}", 0, 2)], [(tm, P_, P_ + 64)])
                 if f32:
                     g_.commit("p_done")
             g_.wait(me, "a1", g)
@@ -330,7 +331,7 @@ def test_the_graph_is_that_of_the_source():
     assert "a1(int part) { return 64 * part; }" in text and "a2(int part) { return 128 + 32 * part; }" in text
     assert "a3(int part) { return F32 && part < 2 ? 32 * part : 128 + 32 * part; }" in text
     assert "a4(int part) { return part < 2 ? W + 32 * part : 224; }" in text
-    for x in ("NO = F32 ? 3 : 2;", "NB = !F32 ? 3 : D == 64 ? 2 : 1, NV = F32 && D == 128 ? 1 : 2;", "NM = F32 ? 1 : 2;", "NS = F32 ? 3 : 2;"):
+    for x in ("NO = F32 ? 3 : 2;", "NB = !F32 ? 3 : D == 64 ? 2 : 1, NV = F32 && D == 128 ? 1 : 2;", "NM = F32 ? 1 : 2;", "NS = 3, NQ = F32 ? 3 : 2;"):
         assert x in text
     roles = re.split(r"//\s*-{20,}[^\n]*", text)[1:]
     assert len(roles) == 5

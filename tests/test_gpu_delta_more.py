@@ -44,3 +44,27 @@ def test_long_prompts_repeat_themselves(P, d, io):
             close(want[b, torch.from_numpy(at).cuda(), h], o[at], 2.0 ** -24 if io else 2.0 ** -8, f"outputs of tokens {first}..{first + 31} of the chunks")
         close(end[b, h], last, 0.0, "states")
     assert D.status() == 0
+
+
+@pytest.mark.parametrize("io", [0, 1])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("strong", [False, True])
+def test_states_of_slow_decays_are_held_in_32_bits(P, d, io, strong):
+    """Decays of 0.999 and more, so that hundreds of tokens' errors meet. What fp32 accumulation costs: a sum of the tensor cores takes its largest
+    parts in steps of 16 terms, d / 16 <= 8 for w = S^T k, 4 for u and 4 for the increment, each cut off by half a unit of 2^-23 on average: at most 16 * 2^-24 =
+    2^-20 of the values. A token's error of w enters the state times beta, and takes beta (2 - beta) / d of the error's square along k away: what
+    stays is sqrt(beta / (2 - beta)) <= 1 of it. The three bf16 parts of an operand leave 2^-25, which is small beside that; two would leave 2^-18."""
+    import torch
+    n, H = 900, 4
+    x = inputs(torch, 1, n, H, 2, d, io, 5, a_lo=0.999)
+    if strong:
+        x[4].fill_(1.0)
+    D = make(P, torch, H, 2, d, io, 1)
+    S = f64(D.states)[0]
+    D.chunk(*x, torch.empty_like(x[2]))
+    q, k, v, a, beta = map(f64, x)
+    got = f64(D.states)[0]
+    for h in range(H):
+        _, want = T.chunk(S[h], q[0, :, h // 2], k[0, :, h // 2], v[0, :, h], a[0, :, h], beta[0, :, h])
+        off = np.linalg.norm(got[h] - want) / np.linalg.norm(want)
+        assert off < 2.0 ** -20, off
