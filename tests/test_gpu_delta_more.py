@@ -68,3 +68,94 @@ def test_states_of_slow_decays_are_held_in_32_bits(P, d, io, strong):
         _, want = T.chunk(S[h], q[0, :, h // 2], k[0, :, h // 2], v[0, :, h], a[0, :, h], beta[0, :, h])
         off = np.linalg.norm(got[h] - want) / np.linalg.norm(want)
         assert off < 2.0 ** -20, off
+
+
+def alone(P, torch, kind, D, S, x, o, rows, counts, mask, idx, keep, slots):
+    """Sequences `rows` of a call, each in a call of its own: their outputs and states, from the states S."""
+    E = P.PaceDelta(D.cfg)
+    E.states.copy_(S)
+    for b in rows:
+        one = slice(b, b + 1)
+        y, s = [z[one] for z in x], slots[one]
+        c = None if counts is None else counts[one]
+        got = torch.full_like(o[one], 7.0)
+        if kind == "chunk":
+            E.chunk(*y, got, slots=s, n_new=c)
+        elif kind == "draft":
+            E.draft(*y, got, slots=s, n_new=c, mask=None if mask is None else mask[one].contiguous())
+        else:
+            E.keep(*y[1:], idx[one].contiguous(), keep[one].contiguous(), slots=s, n_new=c)
+        if kind != "keep":
+            assert torch.equal(got, o[one]), f"outputs of sequence {b}"
+        assert torch.equal(E.states[int(s)], D.states[int(s)]), f"state of sequence {b}"
+
+
+def lasting(P, kind, B, n, H, Hk, d, io, seed, every):
+    """A call of many sequences of all lengths and counts, with every few of them against calls of their own and one against the rule."""
+    import torch
+    from test_gpu_delta import tree, words
+    rng = np.random.default_rng(seed)
+    D = make(P, torch, H, Hk, d, io, B + 3, seed)
+    S = D.states.clone()
+    x = inputs(torch, B, n, H, Hk, d, io, seed)
+    counts = rng.integers(0, n + 1, B)
+    counts[0], counts[-1] = n, n
+    slots = rng.permutation(B + 3)[:B]
+    cn, sl = ints(torch, counts), ints(torch, slots)
+    mask = idx = keep = None
+    o = torch.full_like(x[2], 7.0)
+    if kind == "chunk":
+        D.chunk(*x, o, slots=sl, n_new=cn)
+    elif kind == "draft":
+        see = np.stack([tree(rng, n) for _ in range(B)])
+        mask = words(torch, see)
+        D.draft(*x, o, slots=sl, n_new=cn, mask=mask)
+    else:
+        kept = np.minimum(rng.integers(0, n + 1, B), counts)
+        kept[0] = n
+        path = np.zeros((B, n), np.int32)
+        for b in range(B):
+            path[b, :kept[b]] = np.sort(rng.choice(counts[b], kept[b], replace=False)) if kept[b] else []
+        idx, keep = ints(torch, path), ints(torch, kept)
+        D.keep(*x[1:], idx, keep, slots=sl, n_new=cn)
+    assert D.status() == 0
+    alone(P, torch, kind, D, S, x, o, [0, *range(1, B - 1, every), B - 1], cn, mask, idx, keep, sl)
+    q, k, v, a, beta = (f64(y[0]) for y in x)
+    h, hk, before = H - 1, (H - 1) // (H // Hk), f64(S[int(slots[0]), H - 1])
+    t = slice(None) if kind != "keep" else path[0, :kept[0]]
+    if kind == "draft":
+        want, end = T.draft(before, q[:, hk], k[:, hk], v[:, h], a[:, h], beta[:, h], see[0]), before
+    else:
+        want, end = T.chunk(before, q[t, hk], k[t, hk], v[t, h], a[t, h], beta[t, h])
+    if kind != "keep":
+        close(o[0, :, h], want, 2.0 ** -24 if io else 2.0 ** -8, "outputs")
+    close(D.states[int(slots[0]), h], end, 0.0, "states")
+    untouched = [s for s in range(B + 3) if s not in set(slots)] + [int(slots[b]) for b in range(B) if (counts if kind != "keep" else kept)[b] == 0]
+    assert torch.equal(D.states[untouched], S[untouched])
+
+
+@pytest.mark.parametrize("kind", ["chunk", "draft", "keep"])
+@pytest.mark.parametrize("io", [0, 1])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [33, 64])
+def test_blocks_that_go_on(P, n, d, io, kind):
+    lasting(P, kind, 60, n, 6, 3, d, io, n + d, 7)
+
+
+@pytest.mark.parametrize("kind", ["chunk", "keep"])
+@pytest.mark.parametrize("io", [0, 1])
+@pytest.mark.parametrize("d", [64, 128])
+def test_blocks_that_go_on_over_several_chunks(P, d, io, kind):
+    lasting(P, kind, 40, 200, 5, 5, d, io, d, 6)
+
+
+@pytest.mark.parametrize("kind,d,io", [("chunk", 64, 0), ("draft", 128, 0), ("keep", 128, 1)])
+def test_more_than_256_sequences(P, kind, d, io):
+    """Sequences that are not sorted by their length."""
+    lasting(P, kind, 300, 20, 2, 1, d, io, 3, 40)
+
+
+@pytest.mark.parametrize("kind,io", [("chunk", 0), ("draft", 1), ("keep", 0)])
+def test_more_than_64_units_a_multiprocessor(P, kind, io):
+    """16,000 sequences and heads: more blocks than multiprocessors, each with as many units as it can list."""
+    lasting(P, kind, 1000, 17, 16, 4, 64, io, 4, 150)
