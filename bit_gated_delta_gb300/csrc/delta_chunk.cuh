@@ -24,7 +24,8 @@
 // increment 1,200, waits), which bounds the kernel; a block fills TMEM and shared memory, so that nothing overlaps another chain. Heads of 128,
 // bf16: 96 chains of up to 16,384 tokens 1,124 us (1.14 TB/s), 512 of 695 to 2048 tokens 415 us (1.43 TB/s, 171 TFLOP/s by the rule's own
 // count); fp32 512 chains of 512 tokens 383 us (bf16 178). Two warps that issue products, or outputs read later in columns of their own, took longer.
-// Every wait is bounded; one that gives up sets the status word, after which the block goes on without waiting or products and leaves the state.
+// Every wait is bounded; one that gives up sets the status word, after which the block goes on without waiting or products; the warps of the columns
+// agree before they store a state, so that it is whole or as it was.
 #pragma once
 
 #include "delta_common.cuh"
@@ -114,7 +115,12 @@ __device__ __forceinline__ uint32_t idesc_n(int N) { return idesc(0, 0) | ((uint
 
 // (A wait that is not over at the first look, out of line: the roles' loops together should stay in the instruction cache. Unrolled and
 // in line, with eight column warps, 3.9 of the 10.5 warps a scheduler counts an issued instruction waited for theirs; so 0.3 do.)
-static __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, 1000000000ull); }
+static __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, uint32_t *failed, uint32_t limit_ns) {
+  if (mbar_wait(bar, parity, limit_ns)) return true;
+  *reinterpret_cast<volatile uint32_t *>(failed) = 1;
+  return false;
+}
+constexpr uint32_t WAIT_NS = 1000000000;
 
 // y += m x for a pair of rows.
 __device__ __forceinline__ void fma_pair(uint64_t &y, uint64_t m, float x) {
@@ -137,7 +143,8 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
   uint64_t *x_full = bar, *x_free = x_full + NB, *o_free = x_free + NB, *o_ready = o_free + NV, *m_ready = o_ready + NV, *m_free = m_ready + NM, *ready = m_free + NM,
            *a1 = ready + 3, *a2 = a1 + 1, *a3 = a2 + 2, *a4 = a3 + 2, *u_done = a4 + 1, *w_done = u_done + 2, *p_done = w_done + 1,
            *s_done = p_done + 1, *o_done = s_done + 1, *o_read = o_done + 1, *g_done = o_read + 1, *t_ready = g_done + 1, *drain = t_ready + 1;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::OMISC);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Z::OMISC), *failed = tmem_slot + 1;      // failed: a wait of the block gave up
+  const uint32_t limit = p.probe_ns ? p.probe_ns : WAIT_NS;
   Unit *unit = reinterpret_cast<Unit *>(smem + Z::OUNIT);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const bool out = p.o.p != nullptr;
@@ -155,6 +162,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
     for (uint64_t *x : {a2, a2 + 1, a3, a3 + 1}) mbar_init(x, Z::MAIN / 2);
     for (uint64_t *x : {w_done, p_done, u_done, u_done + 1, s_done, o_done, g_done, drain}) mbar_init(x, 1);
     mbar_init(t_ready, Z::AUX);
+    *failed = 0;
     mbar_fence_init();
   }
   pdl_enter();
@@ -223,7 +231,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
 
   bool good = true;
   auto wait = [&](uint64_t *x, int phase) {              // (by the whole warp)
-    if (good && !mbar_try_wait(x, phase & 1)) good = wait_long(x, phase & 1);
+    if (good && !mbar_try_wait(x, phase & 1)) good = wait_long(x, phase & 1, failed, limit);
     __syncwarp();
   };
   auto arrive = [&](uint64_t *x) {
@@ -466,7 +474,12 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         }
         step();
       }
-      if (p.write && on && good) {
+      uint32_t bad = 1;
+      if (p.write) {                                       // (all of them store or none)
+        bad = *reinterpret_cast<volatile uint32_t *>(failed);
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\tbar.red.or.pred q, 7, %1, q;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "+r"(bad) : "n"(Z::MAIN * 32) : "memory");
+      }
+      if (on && !bad) {
         float *to = state();
 #pragma unroll
         for (int i = 0; i < HELD; ++i) to[i * D] = S[i];
@@ -794,10 +807,11 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
         if (unit[k].n > 0) return (min(C, unit[k].n) + 15) & ~15;
       return 0;
     };
+    if (p.probe_ns) wait(drain, 0);                      // (not signalled before the block's last commit)
     int np_next = after(-1, 0);
     if (np_next) dots(np_next);
 #pragma unroll 1
-    for (int k = 0; k < turns && good; ++k) {            // (without products from a wait on that gave up)
+    for (int k = 0; k < turns && all_good(); ++k) {      // (without products from a wait on that gave up)
       if (!take(k)) continue;
 #pragma unroll 1
       for (int c = 0; c < chunks && good; ++c) {
@@ -894,7 +908,7 @@ __global__ void __launch_bounds__(Shape<D, F32>::THREADS, 1) delta_chunk_kernel(
       }
     }
     if (leader) commit(drain);                           // every product has ended before the block frees its TMEM
-    wait_long(drain, 0);
+    wait_long(drain, 0, failed, WAIT_NS);
     __syncwarp();
   }
   if (!good) atomicOr(p.status, PACE_DELTA_TIMEOUT);

@@ -17,6 +17,7 @@ struct DeltaArgs {
   int n_idx;
   int write;                // the states advance
   int sms;                  // multiprocessors of the device
+  uint32_t probe_ns;        // failure-detection test: > 0 makes each block of the chunk kernels wait this long for what nothing signals (serve_internal.h)
 };
 
 namespace pace {

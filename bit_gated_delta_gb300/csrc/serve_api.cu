@@ -225,6 +225,12 @@ pace_status pace_delta_get_status(const pace_delta *delta, int clear, int *statu
   return ok();
 }
 
+pace_status pace_test_delta_wait_probe(pace_delta *delta, uint32_t ns) {
+  if (!delta) return fail(PACE_ERR_INVALID_ARG, "test_delta_wait_probe: handle is NULL");
+  delta->args.probe_ns = ns;
+  return ok();
+}
+
 // ---- verification -----------------------------------------------------------------------------------------------------------------
 pace_status pace_verify(int batch, int n_nodes, int vocab, int io_dtype, const int32_t *tokens, const pace_tensor *p,
                         const pace_tensor *q, const float *u, const uint32_t *mask, const int32_t *n_new, int32_t *idx,

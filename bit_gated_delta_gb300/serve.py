@@ -101,6 +101,14 @@ def pace_delta_get_status(handle, clear: bool = False, stream=None) -> int:
     return _status("pace_delta_get_status", handle, clear, stream)
 
 
+def pace_test_delta_wait_probe(handle, ns: int) -> None:
+    """Failure-detection hook for tests: while ns > 0, calls by chunks of this handle wait that long for what nothing signals, give up and leave the
+    states as they are. 0 turns it off."""
+    fn = lib().pace_test_delta_wait_probe
+    fn.restype, fn.argtypes = C.c_int, [C.c_void_p, C.c_uint32]
+    check(fn(handle, int(ns)))
+
+
 class PaceDelta:
     """The fp32 states of one gated-delta layer, [n_slots, heads, d, d] (`states`, key index first), bound to a handle.
 

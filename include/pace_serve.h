@@ -42,7 +42,7 @@ enum {
                               left out (its outputs are zeros) */
   PACE_DELTA_BAD_KEEP = 2, /* a kept index outside the drafts or not increasing (it and later ones were left), or a kept
                               count outside 0..n_idx (taken as the nearest) */
-  PACE_DELTA_TIMEOUT = 4   /* a bounded device wait gave up (the call's outputs and states are not to be used) */
+  PACE_DELTA_TIMEOUT = 4   /* a bounded device wait gave up: the call's outputs are not to be used, and states are as before or after the call, each whole */
 };
 
 /* The sequences of one call: sequence b has n_b = n_new[b] tokens, clamped to 0..n_tokens (n_new NULL: n_tokens), and the state

@@ -344,7 +344,7 @@ def test_the_graph_is_that_of_the_source():
     inverses = ["wait &m_ready[g % NM] g / NM"] + ["sync4<6>"] * 5 + ["wait u_done + 1 g - 1", "arrive t_ready", "arrive &m_free[g % NM]"]
     copies = ["wait &x_free[at_x()] round_x() - 1", "wait &o_free[g % NV] g / NV - 1", "wait &x_free[(g - NV) % NB] (g - NV) / NB",
               "arrive what == 0 ? &x_full[at_x()] : &ready[g3()]", "wait &o_ready[g % NV] g / NV", "arrive &o_free[g % NV]"]
-    products = ["wait &x_full[at_x()] round_x()", "commit g_done", "wait a1 now", "commit w_done", "wait o_read now - 1", "commit p_done",
+    products = ["wait &x_full[at_x()] round_x()", "commit g_done", "wait drain 0", "wait a1 now", "commit w_done", "wait o_read now - 1", "commit p_done",
                 "wait &ready[g3()] r3()", "wait t_ready now", "wait o_read now - 1", "wait a2 + r now", "commit u_done + r", "wait a3 + r now",
                 "commit s_done", "commit &x_free[buf]", "wait a4 now", "commit o_done", "commit drain"]
     assert got == [columns, tables, inverses, copies, products]

@@ -159,3 +159,33 @@ def test_more_than_256_sequences(P, kind, d, io):
 def test_more_than_64_units_a_multiprocessor(P, kind, io):
     """16,000 sequences and heads: more blocks than multiprocessors, each with as many units as it can list."""
     lasting(P, kind, 1000, 17, 16, 4, 64, io, 4, 150)
+
+
+@pytest.mark.parametrize("io", [0, 1])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind,B,n", [("chunk", 3, 200), ("chunk", 50, 70), ("draft", 50, 20), ("keep", 50, 20), ("keep", 3, 300)])
+def test_waits_that_run_out(P, kind, B, n, d, io):
+    """Each block waits 2 ms for what nothing signals: the call ends, says so, and leaves the states and what lies around the outputs as they were; the next
+    call is like any other. (50 x 4 sequences and heads: blocks that go on from one to the next.)"""
+    import torch
+    H = 4
+    D, E = make(P, torch, H, H, d, io, B), make(P, torch, H, H, d, io, B)
+    S = D.states.clone()
+    x = inputs(torch, B, n, H, H, d, io, 12)
+    idx, keep = ints(torch, np.tile(np.arange(n), (B, 1))), ints(torch, [n] * B)
+    wide = torch.full((B, n + 2, H, d), 7.0, dtype=x[2].dtype, device="cuda")
+    o, want = wide[:, 1:-1], torch.empty_like(x[2])
+
+    def call(to, out):
+        if kind == "keep":
+            to.keep(*x[1:], idx, keep)
+        else:
+            getattr(to, kind)(*x, out)
+    call(E, want)
+    P.serve.pace_test_delta_wait_probe(D.handle, 2_000_000)
+    call(D, o)
+    assert D.status(clear=True) == P.PACE_DELTA_TIMEOUT and D.status() == 0
+    assert torch.equal(D.states, S) and (wide[:, 0] == 7.0).all() and (wide[:, -1] == 7.0).all()
+    P.serve.pace_test_delta_wait_probe(D.handle, 0)
+    call(D, o)
+    assert D.status() == 0 and torch.equal(D.states, E.states) and (kind == "keep" or torch.equal(o, want))
