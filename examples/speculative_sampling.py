@@ -76,7 +76,7 @@ class Server:
                 if mask is None:
                     layer.chunk(q, k, v, a, beta, o, lens=self.lens, n_new=n_new)
                 else:
-                    layer.draft(q, k, v, a, beta, o, n_new=n_new, mask=mask)
+                    layer.draft(q, k, v, a, beta, o, lens=self.lens, n_new=n_new, mask=mask)
                     self.drafts.append((layer, k, v, a, beta))
             x = x + o.flatten(2) @ wo.t()
         return (x @ self.unembed.t()).float() + self.bigrams[tokens.long()]
@@ -136,7 +136,7 @@ class Server:
                 if kind == "attend":
                     layer.keep(self.lens, self.table, idx, n_keep)
             for layer, *x in self.drafts:
-                layer.keep(*x, idx, n_keep)
+                layer.keep(*x, idx, n_keep, lens=self.lens)  # (a row without tokens yet begins with a zero state)
             self.lens += n_keep
             self.pages.select(self.table, self.lens)         # pages of drafts that were not kept go back
             new = torch.cat((tree.gather(1, idx.long()), following[:, None]), 1).tolist()

@@ -44,3 +44,21 @@ def test_samples_that_share_pages_do_not_touch_one_another(E):
     a, b = forked.forward(more, n), alone.forward(more, n)
     assert torch.equal(a, b)
     assert torch.equal(forked.layers[0][1].states, alone.layers[0][1].states)
+
+
+def test_a_row_given_up_begins_anew(E):
+    """A prompt of one token (nothing of it goes through the layers before the first tree) in a row that another sequence has left: the samples and
+    the state of a server in which the row was never used."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(3)
+    old, other = (torch.randint(0, 512, (n,), generator=g, device="cuda").tolist() for n in (80, 50))
+    used, fresh = E.Server(["delta", "attend"], 2, 512), E.Server(["delta", "attend"], 2, 512)
+    used.prompt([old, other])
+    used.fork([-1, 1])
+    fresh.prompt([[], other])
+    got = []
+    for s in (used, fresh):
+        last = s.prompt([[7], []])
+        out, _ = s.sample(last, torch.tensor([True, False], device="cuda"), 6, [0, 0, 0, 1, 2], torch.Generator(device="cuda").manual_seed(4))
+        got.append((out[0], s.layers[0][1].states[0].clone()))
+    assert got[0][0] == got[1][0] and torch.equal(got[0][1], got[1][1])
