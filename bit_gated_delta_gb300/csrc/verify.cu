@@ -6,7 +6,8 @@
 // a sequence, whatever its length. The next token is found by the prefix of the blocks' sums, of the warps', and in one warp of the tokens.
 //
 // Sums in fixed point. A value r in 0..1 enters as two integers: the upper from the bits of r + 1 (units of 2^-23, exact), the rest
-// from the bits of rest + 1.5 * 2^-23 (units of 2^-46). Differences p - q carry their rounding error along (it is exact in fp32), so
+// from the bits of rest + 1.5 * 2^-23 (units of 2^-46; from 2^17 tokens on as much
+// larger that a row of ones stays below 2^63: 2^-45 up to 2^18 - 1 tokens). Differences p - q carry their rounding error along (it is exact in fp32), so
 // that sums have the accuracy of 64-bit floating point at the fp32 rate (the fp64 pipe is a 64th of it), and no order changes them.
 //
 // Bound by the latency of the rows' loads (16 a thread under way): 64 chains of 7 drafts over 131,072 fp32 tokens 28 us, 67 MB, 2.4 TB/s; one over
@@ -54,19 +55,29 @@ __device__ __forceinline__ Rest next_rest(Rest x, float q, Factor z) {
   return Rest{r, __fadd_rn(e, -__fadd_rn(r, -s))};
 }
 
-// The value in units of 2^-46, as upper (2^-23) and lower part.
-__device__ __forceinline__ void units(Rest x, uint32_t &hi, int &lo) {
+// Units of sums over a vocabulary: 2^-(23 + shift).
+struct Units {
+  int shift;
+  float m;                                               // 1.5 * 2^-shift: neighbours are a unit apart
+  double one;                                            // a unit
+  __device__ __forceinline__ explicit Units(int vocab) {
+    shift = 23 - max(0, 32 - __clz(vocab) - 17);
+    m = __uint_as_float((127 - shift) << 23 | 0x400000);
+    one = __hiloint2double((1023 - 23 - shift) << 20, 0);
+  }
+};
+// The value as upper (2^-23) and lower part (units).
+__device__ __forceinline__ void units(Rest x, const Units &z, uint32_t &hi, int &lo) {
   const float t = __fadd_rn(x.r, 1.0f);
   hi = __float_as_uint(t) - 0x3F800000u;
   const float rest = __fadd_rn(__fadd_rn(x.r, -__fadd_rn(t, -1.0f)), x.e);
-  constexpr float M = 1.5f / 8388608.0f;                 // 1.5 * 2^-23: neighbours are 2^-46 apart
-  lo = (int)(__float_as_uint(__fadd_rn(rest, M)) - __float_as_uint(M));
+  lo = (int)(__float_as_uint(__fadd_rn(rest, z.m)) - __float_as_uint(z.m));
 }
-__device__ __forceinline__ int64_t to_units(Rest x) {
+__device__ __forceinline__ int64_t to_units(Rest x, const Units &z) {
   uint32_t hi;
   int lo;
-  units(x, hi, lo);
-  return ((int64_t)hi << 23) + lo;
+  units(x, z, hi, lo);
+  return ((int64_t)hi << z.shift) + lo;
 }
 
 struct Walk {               // shared by the block
@@ -83,7 +94,7 @@ struct Walk {               // shared by the block
 
 // R of the tokens v, v + 32, .. below hi at the walk's node, in units.
 template <bool F32, bool Q>
-__device__ __forceinline__ void step(const Walk &w, const char *prow, const char *qrow, int v, int hi, int refusals, uint32_t (&up)[UNROLL],
+__device__ __forceinline__ void step(const Walk &w, const Units &z, const char *prow, const char *qrow, int v, int hi, int refusals, uint32_t (&up)[UNROLL],
                                      int (&down)[UNROLL]) {
   float p[UNROLL], q[UNROLL];
 #pragma unroll
@@ -98,13 +109,14 @@ __device__ __forceinline__ void step(const Walk &w, const char *prow, const char
       x = first_rest(p[k], q[k]);
       for (int i = 1; i < refusals; ++i) x = next_rest(x, q[k], w.z[i]);
     }
-    units(x, up[k], down[k]);
+    units(x, z, up[k], down[k]);
   }
 }
 
 template <bool F32, bool Q>
 __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int blocks) {
   __shared__ Walk w;
+  const Units z(a.vocab);
   cg::cluster_group cluster = cg::this_cluster();
   if (blocks > 1) cluster.barrier_arrive();              // (a block has begun: others may write to its shared memory)
   pdl_enter();
@@ -217,12 +229,12 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int
       for (int v = g0; v < g1; v += SPAN) {
         uint32_t h[UNROLL];
         int l[UNROLL];
-        step<F32, Q>(w, pr, qr, v + lane, hi, refusals, h, l);
+        step<F32, Q>(w, z, pr, qr, v + lane, hi, refusals, h, l);
         uint32_t up = 0;
         int down = 0;
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) up += h[k], down += l[k];
-        part_sum += ((int64_t)up << 23) + down;
+        part_sum += ((int64_t)up << z.shift) + down;
       }
 #pragma unroll
       for (int m = 16; m > 0; m >>= 1) part_sum += __shfl_xor_sync(0xffffffffu, part_sum, m);
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int
         bool again = y < lo || y >= hi;
         for (int k = 0; k < i && !again; ++k) again = w.refused[k] == y;
         if (!again) {
-          const int64_t x = to_units(Rest{prob<F32>(pr, y), 0.0f});
+          const int64_t x = to_units(Rest{prob<F32>(pr, y), 0.0f}, z);
           sum -= x;
           w.mark[warp][(y - lo) / (group * SPAN)] -= x;
         }
@@ -256,7 +268,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int
       if (total > 0 || refusals == 0) break;
       whole = true;
     } else if (tid == 0) {
-      w.Z = (double)total * (1.0 / 70368744177664.0);    // 2^-46
+      w.Z = (double)total * z.one;
     }
     __syncthreads();
   }
@@ -265,8 +277,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int
   if (n > 0 && total > 0) {
     const int node = w.node, refusals = whole ? 0 : w.refusals;
     const char *pr = prow(node), *qr = Q ? qrow(node) : nullptr;
-    const double x = fmin(fmax((double)w.u[0], 0.0) * (double)total, (double)(total - 1));
-    int64_t at = (int64_t)x;                             // the first prefix above it
+    int64_t at = min((int64_t)(fmax((double)w.u[0], 0.0) * (double)total), total - 1);   // the first prefix above it
     const int64_t *sums = w.block_sum[turn ^ 1];
     for (int i = 0; i < part; ++i) at -= sums[i];
     if (at >= 0 && at < sums[part]) {
@@ -282,10 +293,10 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a, int
         for (int v0 = lo + g * group * SPAN; v < 0 && v0 < hi; v0 += SPAN) {
           uint32_t h[UNROLL];
           int l[UNROLL];
-          step<F32, Q>(w, pr, qr, v0 + lane, hi, refusals, h, l);
+          step<F32, Q>(w, z, pr, qr, v0 + lane, hi, refusals, h, l);
 #pragma unroll
           for (int k = 0; k < UNROLL; ++k) {
-            int64_t mine = ((int64_t)h[k] << 23) + l[k];
+            int64_t mine = ((int64_t)h[k] << z.shift) + l[k];
             if (!Q)
               for (int i = 0; i < refusals; ++i)
                 if (w.refused[i] == v0 + 32 * k + lane) mine = 0;

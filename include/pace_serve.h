@@ -100,10 +100,12 @@ pace_status pace_delta_get_status(const pace_delta *delta, int clear, int *statu
  * From node 0 on, the drafts that hang from the node so far are tried in order. With R = p of the node and Z = 1 at first, draft i with
  * token y is kept if u_i q(y) Z < R(y); the walk then goes on from it. If not, R <- max(R - q Z, 0) and Z <- sum R (q NULL:
  * R(y) <- 0 and Z <- max(Z - R(y), 0)), and the next draft of the node is tried. Where none is left, the next token is the
- * smallest v with R(0) + .. + R(v) > u_0 sum R. So tokens are distributed as the target's own: drafts of one node drawn from q
- * independently of one another, or named by any rule that does not look at u.
+ * smallest v with R(0) + .. + R(v) > u_0 sum R. So tokens are distributed as the target's own, where rows of p sum to 1 and drafts of one
+ * node are drawn from q independently of one another, or named by any rule that does not look at u. Z begins at 1 whatever p sums to:
+ * a row whose sum is off by a factor 1 + e (bf16: up to 2^-9) moves what drafts are kept by as much.
  *
- * Probabilities count as their clamp to 0..1, NaN as 0; sums are taken in fixed point (2^-46), so that the same call gives the same tokens.
+ * Probabilities count as their clamp to 0..1, NaN as 0. Sums are taken in fixed point, so that the same call gives the same tokens: in units of
+ * 2^-46 below 2^17 tokens, twice as large for each doubling from there, so that rows of any sum (all ones, say) are summed right.
  * A draft outside the vocabulary is not kept. Where nothing of R is left, the next token is drawn from p of the node; it is -1 where that is
  * zero too, and for sequences without nodes (n_nodes of sequence b: n_new[b], clamped to 0..n_nodes).
  *
