@@ -62,3 +62,31 @@ def test_a_row_given_up_begins_anew(E):
         out, _ = s.sample(last, torch.tensor([True, False], device="cuda"), 6, [0, 0, 0, 1, 2], torch.Generator(device="cuda").manual_seed(4))
         got.append((out[0], s.layers[0][1].states[0].clone()))
     assert got[0][0] == got[1][0] and torch.equal(got[0][1], got[1][1])
+
+
+def test_tokens_are_distributed_as_the_targets(E):
+    """The token after a prompt, from trees whose drafts come from the bigrams alone: 4,096 samples have the frequencies that the target gives (each off
+    by at most five times sqrt(f (1 - f) / 4096))."""
+    import torch
+    rows, vocab, turns = 256, 8, 16
+    s, alone = E.Server(["delta", "attend"], rows, 128, vocab=vocab), E.Server(["delta", "attend"], rows, 128, vocab=vocab)
+    prompt = torch.randint(0, vocab, (40,), generator=torch.Generator().manual_seed(5)).tolist()
+    for x in (s, alone):
+        x.prompt([prompt] + [[]] * (rows - 1))
+        x.fork([0] * rows)
+    one = torch.ones(rows, dtype=torch.int32, device="cuda")
+    alone.take(one)
+    last = torch.full((rows,), prompt[-1], dtype=torch.int32, device="cuda")
+    p = torch.softmax(alone.forward(last[:, None], one)[0, 0], -1)
+    q = torch.softmax(s.bigrams[prompt[-1]], -1)
+    assert (p - q).abs().max() > 0.05                        # (the drafts' distribution is another)
+    states, lens = s.layers[0][1].states.clone(), s.lens.clone()
+    g, count = torch.Generator(device="cuda").manual_seed(6), torch.zeros(vocab, device="cuda")
+    for _ in range(turns):
+        out, _ = s.sample(last, torch.ones(rows, dtype=torch.bool, device="cuda"), 1, [0, 0, 0, 1], g)
+        count += torch.bincount(torch.tensor([o[0] for o in out], device="cuda"), minlength=vocab)
+        s.layers[0][1].states.copy_(states)
+        s.lens.copy_(lens)
+        s.pages.select(s.table, s.lens)
+    n = rows * turns
+    assert ((count / n - p).abs() <= 5 * (p * (1 - p) / n).sqrt()).all()
