@@ -306,6 +306,8 @@ pace_status pace_pages_take(pace_pages *pages, int batch, int32_t *table, int ta
                             const int32_t *n_new, int32_t *fits, void *stream) {
   pace_status st = check_table(pages, batch, table, table_cols, "pages_take");
   if (st != PACE_OK) return st;
+  if ((int64_t)batch * table_cols > INT32_MAX)             // (what the rows want is summed in 32 bits)
+    return fail(PACE_ERR_UNSUPPORTED, "pages_take: a table of %lld cells, supported 2^31 - 1", (long long)batch * table_cols);
   if (batch > 0 && (!lens || !n_new || !fits || !aligned(lens, 4) || !aligned(n_new, 4) || !aligned(fits, 4)))
     return fail(PACE_ERR_INVALID_ARG, "pages_take: lens, n_new or fits is NULL or not 4-byte aligned");
   return launched(pace_launch_pages_take(pages->dev, batch, table, table_cols, lens, n_new, fits, static_cast<cudaStream_t>(stream)),

@@ -157,7 +157,8 @@ pace_status pace_pages_select(pace_pages *pages, int batch, int32_t *table, int 
 /* Give each row the pages that its next n_new[b] tokens (slots lens[b] ..) need: one for each empty cell of them, and one in the
  * place of a page that they begin in and that other rows hold too, whose tokens are then to be copied (src, dst of the moves).
  * Where all holders of such a page take part, the one with the most tokens in it keeps it (of several the first). Free pages go out from the lowest number, to the rows in
- * order; from the first row on that the pool cannot serve, rows that need pages get none, and fits[b] is 0 (else 1). One launch. */
+ * order; from the first row on that the pool cannot serve, rows that need pages get none, and fits[b] is 0 (else 1). The table has at most
+ * 2^31 - 1 cells. One launch. */
 pace_status pace_pages_take(pace_pages *pages, int batch, int32_t *table, int table_cols, const int32_t *lens,
                             const int32_t *n_new, int32_t *fits, void *stream);
 
