@@ -46,8 +46,9 @@ struct Unit {
   uint32_t slot;
 };
 constexpr int UNITS = 64;                                // most of a block
-// Most chunks of a call whose blocks go from one sequence and head to the next (512 of equal length, heads of 128: of 64 tokens 39 us, a block for
-// each 46; of 256 110 and 111; of 512 198 and 189; of 1024 367 and 337. 2048 of 64 tokens 134 and 181).
+// Most chunks of a call whose blocks go from one sequence and head to the next. 512 of equal length, heads of 128, bf16: of 64 tokens 49 us, a block for
+// each 57; of 128 71 and 76; of 256 117 and 114; of 512 205 and 187; 2048 of 64 tokens 151 and 184. fp32: 2048 of 64 tokens 217 and 258, of 256 697 and 715, of 512 1343
+// and 1330; heads of 64 396 and 436 of 256, 739 and 772 of 512, 1420 and 1443 of 1024.
 constexpr int CHUNKS_LASTING = 4;
 
 template <int D, bool F32>

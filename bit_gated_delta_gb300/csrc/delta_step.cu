@@ -12,9 +12,11 @@ namespace delta {
 
 constexpr int STEP_THREADS = 256, STEP_WARPS = STEP_THREADS / 32;
 constexpr int STEP_STAGE = 8;            // tokens staged at a time
-// The most tokens of a call that go one by one; longer ones, and trees, go by chunks (delta_chunk.cuh). Measured, heads of 128, us, bf16: 64
-// sequences and heads, 8 tokens 12 (by chunks 12), 1024: 8 tokens 57, 12 tokens 82 (56); fp32: 64 of 12 tokens 16 (18), 1024 of 12 90 (112).
-constexpr int step_most(int io) { return io == PACE_IO_F32 ? 14 : 8; }
+// The most tokens of a call that go one by one; longer ones, and trees, go by chunks (delta_chunk.cuh). Measured, us, one by one (by chunks), states not
+// in L2. fp32: 1024 sequences and heads of 128, 10 tokens 89 (94), 12 100 (94), 14 112 (94); 64 of 10 tokens 16 (17), 14 21 (17); 1024 of 64, 12
+// tokens 52 (57). bf16, heads of 128: 1024 of 6 tokens 61 (62), 8 74 (61); 256 of 8 tokens 20 (23), 10 24 (23); heads of 64: 1024 of 8 35 (43), 10 41 (44),
+// 64 of 8 12 (12).
+constexpr int step_most(int io, int d, bool many) { return io == PACE_IO_F32 ? 11 : d == 128 && many ? 6 : 8; }
 
 __device__ __forceinline__ uint64_t pk(float a, float b) {
   uint64_t r;
@@ -204,7 +206,7 @@ cudaError_t launch_step_t(const DeltaArgs &p, cudaStream_t s) {
 cudaError_t pace_launch_delta(const DeltaArgs &p, cudaStream_t s) {
   using namespace pace::delta;
   const int most = p.idx && p.n_idx < p.n_tokens ? p.n_idx : p.n_tokens;
-  if ((p.mask && p.n_tokens > 1) || most > step_most(p.io))
+  if ((p.mask && p.n_tokens > 1) || most > step_most(p.io, p.d, (long)p.batch * p.H > 4 * pace::device_sm_count()))
     return p.io == PACE_IO_F32 ? pace_launch_delta_chunk_f32(p, s) : pace_launch_delta_chunk_bf16(p, s);
   return p.io == PACE_IO_F32 ? launch_step_t<true>(p, s) : launch_step_t<false>(p, s);
 }
