@@ -15,15 +15,18 @@
 //   D4 = u P^T            A = u                                       B = P
 // fp32 operands are split into bf16 parts (x = hi + mid + lo, 24 bits), of whose products those above 2^-24 are formed, smallest first; q and k
 // of bf16 I/O enter as they are. bf16 I/O forms S^T q from two parts of the state and outputs from two of u and P (o is rounded to 8 bits); S^T k,
-// which comes back into the state, from three (two left up to 2.4e-6 of the states' norm where decays are slow). The state itself stays in fp32 registers
-// and takes D3 by an ordinary addition: the tensor cores' additions cut off, which would add up over a long prompt.
+// which comes back into the state, from three (two left up to 2.4e-6 of the states' norm where decays are slow; the third costs 6% of a long
+// prompt). Outputs from three parts as well are as far from those in 64 bits (1.66e-3, the rounding of o) and differ from these in one last bit of
+// some hundreds, for 4 to 7 (u and P) or 15 to 19% (S too) more time. The state itself stays in fp32 registers and takes D3 by an ordinary
+// addition: the tensor cores' additions cut off, which would add up over a long prompt.
 //
 // Roles: sixteen warps own the columns (four a quarter of TMEM's lanes: a block of 16 tokens and a quarter of the state's rows each), four form
 // R, M and P (fp32 I/O: and split the rows of k and q), four T, one chunk ahead, three (two) copy rows, one issues the products.
-// A sequence and head is a chain of chunks, each 4.4 us (9,200 cycles: parts of the state 1,100, w 900, rhs 1,600, u 1,100, its parts 900, the
-// increment 1,200, waits), which bounds the kernel; a block fills TMEM and shared memory, so that nothing overlaps another chain. Heads of 128,
-// bf16: 96 chains of up to 16,384 tokens 1,124 us (1.14 TB/s), 512 of 695 to 2048 tokens 415 us (1.43 TB/s, 171 TFLOP/s by the rule's own
-// count); fp32 512 chains of 512 tokens 383 us (bf16 178). Two warps that issue products, or outputs read later in columns of their own, took longer.
+// A sequence and head is a chain of chunks, each 4.7 us (9,700 cycles: parts of the state and w 2,500, rhs 1,600, u 1,100, its parts 900, the
+// increment 1,200, waits), which bounds this form of the rule (u is formed by two dependent products); a block fills TMEM and shared memory, so that
+// nothing overlaps another chain. Heads of 128, bf16: 96 chains of up to 16,384 tokens 1,200 us (1.07 TB/s), 512 of 695 to 2048 tokens 438 us (1.35 TB/s,
+// 161 TFLOP/s by the rule's own count); fp32 512 chains of 512 tokens 382 us (bf16 185). Two warps that issue products, or outputs read later in columns
+// of their own, took longer.
 // Every wait is bounded; one that gives up sets the status word, after which the block goes on without waiting or products; the warps of the columns
 // agree before they store a state, so that it is whole or as it was.
 #pragma once

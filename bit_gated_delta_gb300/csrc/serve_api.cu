@@ -297,7 +297,8 @@ pace_status pace_pages_select(pace_pages *pages, int batch, int32_t *table, int 
   pace_status st = check_table(pages, batch, table, table_cols, "pages_select");
   if (st != PACE_OK) return st;
   if (batch == 0) return ok();
-  if (!lens || !aligned(lens, 4) || !aligned(src, 4)) return fail(PACE_ERR_INVALID_ARG, "pages_select: lens is NULL, or lens or src not 4-byte aligned");
+  if (!lens || !aligned(lens, 4) || !aligned(src, 4))
+    return fail(PACE_ERR_INVALID_ARG, "pages_select: lens is NULL, or lens or src not 4-byte aligned");
   return launched(pace_launch_pages_select(pages->dev, batch, table, table_cols, lens, src, static_cast<cudaStream_t>(stream)),
                   "pages_select launch");
 }

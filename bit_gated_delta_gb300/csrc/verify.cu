@@ -6,12 +6,13 @@
 // a sequence, whatever its length. The next token is found by the prefix of the blocks' sums, of the warps', and in one warp of the tokens.
 //
 // Sums in fixed point. A value r in 0..1 enters as two integers: the upper from the bits of r + 1 (units of 2^-23, exact), the rest
-// from the bits of rest + 1.5 * 2^-23 (units of 2^-46; from 2^17 tokens on as much
-// larger that a row of ones stays below 2^63: 2^-45 up to 2^18 - 1 tokens). Differences p - q carry their rounding error along (it is exact in fp32), so
-// that sums have the accuracy of 64-bit floating point at the fp32 rate (the fp64 pipe is a 64th of it), and no order changes them.
+// from the bits of rest + 1.5 * 2^-23 (units of 2^-46; from 2^17 tokens on as much larger that a row of ones stays below 2^63: 2^-45 up
+// to 2^18 - 1 tokens). Differences p - q carry their rounding error along (it is exact in fp32), so that sums have the accuracy of
+// 64-bit floating point at the fp32 rate (the fp64 pipe is a 64th of it), and no order changes them.
 //
-// Bound by the latency of the rows' loads (16 a thread under way): 64 chains of 7 drafts over 131,072 fp32 tokens 28 us, 67 MB, 2.4 TB/s; one over
-// 8,192 tokens 8.3 us, dependent loads and a cluster barrier.
+// Bound by the latency of the rows' loads (16 a thread under way): 64 chains of 7 drafts over 131,072 fp32 tokens, 67 MB, 36 us, 1.9 TB/s (rows in L2 28);
+// one over 8,192 tokens 8 us, dependent loads and a cluster barrier. Each refused sibling with others behind it is a pass over the rows: trees of 25 nodes
+// against draft probabilities, 16 over 50,001 tokens 26 us, 64 over 131,072 tokens 73.
 #include <cooperative_groups.h>
 
 #include "serve_internal.h"

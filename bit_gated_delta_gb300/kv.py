@@ -1,7 +1,7 @@
 """Attention layers of a hybrid model: rotary positions, the quantized paged KV cache and attention over it.
 
-Binding of include/pace_kv.h (and of pace_serve.h as far as it works on a cache): the pace_* functions marshal tensors (shape, type, device and stride checks happen here, value
-ranges in the library), PaceRope and PaceKV own the table and the cache region. Tensors are [batch, tokens, heads, d] views
+Binding of include/pace_kv.h (and of pace_serve.h as far as it works on a cache): the pace_* functions marshal tensors
+(shape, type, device and stride checks happen here, value ranges in the library), PaceRope and PaceKV own the table and the cache region. Tensors are [batch, tokens, heads, d] views
 with d contiguous; lengths, page tables, masks and paths are contiguous int32 tensors; all of a call is on the current device.
 """
 from __future__ import annotations
@@ -23,8 +23,8 @@ _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 __all__ = ["make_rope_config", "pace_rope_bytes", "pace_rope_table", "pace_rope_apply", "PaceRope", "make_kv_config",
            "pace_kv_bytes", "pace_kv_tile_bytes", "pace_kv_alloc", "pace_kv_free", "pace_kv_append", "pace_kv_read",
            "pace_kv_attend", "pace_kv_keep", "pace_kv_get_status", "PaceKV", "pace_kv_config", "pace_rope_config",
-           "pace_kv_copy_pages", "pace_kv_pool", "PACE_KV_BAD_PAGE", "PACE_KV_BAD_POSITION", "PACE_KV_BAD_KEEP", "PACE_KV_TIMEOUT", "PACE_KV_MAX_BATCH",
-           "PACE_KV_MAX_NEW"]
+           "pace_kv_copy_pages", "pace_kv_pool", "PACE_KV_BAD_PAGE", "PACE_KV_BAD_POSITION", "PACE_KV_BAD_KEEP",
+           "PACE_KV_TIMEOUT", "PACE_KV_MAX_BATCH", "PACE_KV_MAX_NEW"]
 
 
 # The calls below are made for every layer and token, so their marshalling is kept short: raw stream handles, one stride() per

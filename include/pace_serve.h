@@ -38,16 +38,18 @@ typedef struct pace_delta pace_delta;   /* opaque host handle */
 
 /* Bits of a handle's device status word. */
 enum {
-  PACE_DELTA_BAD_SLOT = 1, /* a slot outside the states, or one that an earlier sequence of the call writes: the sequence was
-                              left out (its outputs are zeros) */
+  PACE_DELTA_BAD_SLOT = 1, /* a slot outside the states, or one that an earlier sequence of the call with tokens has too:
+                              the sequence was left out (its outputs are zeros) */
   PACE_DELTA_BAD_KEEP = 2, /* a kept index outside the drafts or not increasing (it and later ones were left), or a kept
                               count outside 0..n_idx (taken as the nearest) */
-  PACE_DELTA_TIMEOUT = 4   /* a bounded device wait gave up: the call's outputs are not to be used, and states are as before or after the call, each whole */
+  PACE_DELTA_TIMEOUT = 4   /* a bounded device wait gave up: the call's outputs are not to be used; each head's state is whole,
+                              as before the call or as after it */
 };
 
 /* The sequences of one call: sequence b has n_b = n_new[b] tokens, clamped to 0..n_tokens (n_new NULL: n_tokens), and the state
- * of slot slots[b] (slots NULL: slot b). lens, when given, says which sequences begin: where lens[b] == 0 the state before the call counts as
- * zero, whatever the slot holds, so that one vector of lengths serves these calls and those of pace_kv.h. */
+ * of slot slots[b] (slots NULL: slot b). lens, when given, says which sequences begin: where lens[b] == 0 the state before the
+ * call counts as zero, whatever the slot holds, so that one vector of lengths serves these calls and those of pace_kv.h. A
+ * sequence that may begin with drafts (a slot used before, a prompt of one token) needs it in draft and keep too. */
 typedef struct {
   int batch, n_tokens;
   const int32_t *slots;    /* [batch] or NULL */
@@ -64,11 +66,11 @@ void pace_delta_free(pace_delta *delta);
 /* All tensors below are [batch][n_tokens][heads][d] by strides as in pace_kv.h: q, k of key_heads, v, o of heads, 16-byte
  * aligned with strides of 16-byte multiples; a and beta [batch][n_tokens][heads] by strides (4-byte aligned, any strides).
  *
- * Advance the states by the new tokens (a prompt chunk of any length, or single tokens): o, and S_{n_b} into the slot. Rows of o at and
- * past n_b are zeros; a sequence without tokens keeps its slot as it is. q and o may both be NULL (states only). No two sequences
- * with tokens share a slot. One launch. A few tokens go one by one in fp32; more by chunks of 64 whose products are of fp32 values in
- * parts of 8 bits, three of each, but with bf16 tensors two (16 bits) of the states in S^T q and of what forms o. States then differ
- * from those in 64 bits by less than 1e-6 of their norm, whatever the decays. */
+ * Advance the states by the new tokens (a prompt chunk of any length, or single tokens): o, and S_{n_b} into the slot. Rows of
+ * o at and past n_b are zeros; a sequence without tokens keeps its slot as it is. q and o may both be NULL (states only). No two
+ * sequences with tokens share a slot. One launch. A few tokens go one by one in fp32; more by chunks of 64 whose products are of
+ * fp32 values in parts of 8 bits, three of each, but where bf16 outputs are formed two (16 bits) of the states in S^T q, of u and
+ * of q k^T. States then differ from those in 64 bits by 2e-7 of their norm with decays from 0.95 to 1, up to 7e-7 from 0.999. */
 pace_status pace_delta_chunk(pace_delta *delta, const pace_delta_step *step, const pace_tensor *q, const pace_tensor *k,
                              const pace_tensor *v, const pace_tensor *a, const pace_tensor *beta, const pace_tensor *o,
                              void *stream);
@@ -156,9 +158,9 @@ pace_status pace_pages_select(pace_pages *pages, int batch, int32_t *table, int 
 
 /* Give each row the pages that its next n_new[b] tokens (slots lens[b] ..) need: one for each empty cell of them, and one in the
  * place of a page that they begin in and that other rows hold too, whose tokens are then to be copied (src, dst of the moves).
- * Where all holders of such a page take part, the one with the most tokens in it keeps it (of several the first). Free pages go out from the lowest number, to the rows in
- * order; from the first row on that the pool cannot serve, rows that need pages get none, and fits[b] is 0 (else 1). The table has at most
- * 2^31 - 1 cells. One launch. */
+ * Where all holders of such a page take part, the one with the most tokens in it keeps it (of several the first). Free pages go
+ * out from the lowest number, to the rows in order; from the first row on that the pool cannot serve, rows that need pages get
+ * none, and fits[b] is 0 (else 1). The table has at most 2^31 - 1 cells. One launch. */
 pace_status pace_pages_take(pace_pages *pages, int batch, int32_t *table, int table_cols, const int32_t *lens,
                             const int32_t *n_new, int32_t *fits, void *stream);
 
